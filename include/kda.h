@@ -388,6 +388,101 @@ kda_status kda_backward_workspace_size(const kda_backward_args* args, size_t* by
 
 kda_status kda_backward(const kda_backward_args* args, kda_stream_t stream);
 
+/* ========================================================================
+ * The operators around the layer in a hybrid block: the layer norm in front
+ * of the projections, 8-bit storage of the activations that a backward pass
+ * reads, and a second recurrent mixer, the selective state space scan with
+ * its short causal convolution.  They keep the conventions at the top of this
+ * file.  Unlike the entry points above, they put no rule on the alignment of
+ * rows or row strides beyond the element's own size: a layout that allows
+ * 16-byte accesses takes them, any other takes scalar ones.
+ * ======================================================================== */
+
+/* ------------------------------------------------------------------------
+ * kda_layer_norm -- y = (x - mean) / sqrt(var + eps) * weight + bias over the
+ * last axis of x, var the mean of the squared deviations (two passes over the
+ * registers, so a row whose mean is large loses nothing).
+ *
+ *   x, y    [M][row stride] io; y must not overlap x.
+ *   weight, bias  [C] fp32, or NULL (ones, zeros).
+ *   stats   [M][2] fp32 (mean, 1 / sqrt(var + eps)), what kda_layer_norm_backward
+ *           reads, or NULL (not wanted).
+ * C in [1, 32768]; M >= 0.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    int64_t M;
+    int C;
+    kda_dtype io;
+    const void* x;
+    int64_t x_stride;      /* elements between rows; 0 means C */
+    const float* weight;
+    const float* bias;
+    float eps;
+    void* y;
+    int64_t y_stride;      /* 0 means C */
+    float* stats;
+} kda_norm_args;
+
+kda_status kda_layer_norm(const kda_norm_args* args, kda_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * kda_layer_norm_backward -- with xh = (x - mean) rstd and p = dy weight:
+ *   dx = rstd (p - mean(p) - xh mean(p xh)),  dweight = sum_rows dy xh,  dbias = sum_rows dy.
+ *
+ *   x        the forward's input (io), or its 8-bit form (x_scales non-NULL: x is
+ *            then [M][C] codes and x_scales [M][ceil(C/32)], both dense, as
+ *            kda_pack8 writes them; the pass reads them directly).
+ *   stats    what the forward wrote (of the unrounded x).
+ *   dx       [M][dx_stride] io, rounded once; must not overlap an input.
+ *   dweight, dbias  [C] fp32, or NULL (not wanted).  Summed in a fixed order
+ *            (per block over its rows, then over the blocks): two calls give the
+ *            same bits.
+ *   workspace  kda_layer_norm_backward_workspace_size bytes, 256-byte aligned
+ *            (0 when neither dweight nor dbias is wanted); read and written by
+ *            this call alone, nothing in it needs a value before.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    int64_t M;
+    int C;
+    kda_dtype io;
+    const void* dy;
+    int64_t dy_stride;     /* 0 means C */
+    const void* x;
+    int64_t x_stride;      /* 0 means C; ignored for 8-bit x */
+    const uint8_t* x_scales;
+    const float* stats;
+    const float* weight;
+    void* dx;
+    int64_t dx_stride;     /* 0 means C */
+    float* dweight;
+    float* dbias;
+    void* workspace;
+    size_t workspace_bytes;
+} kda_norm_backward_args;
+
+kda_status kda_layer_norm_backward_workspace_size(const kda_norm_backward_args* args, size_t* bytes);
+kda_status kda_layer_norm_backward(const kda_norm_backward_args* args, kda_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * kda_pack8 / kda_unpack8 -- rows stored in 8 bits for a backward pass.
+ *
+ * Every 32 channels of a row share one power of two 2^e, the smallest with
+ * max|x| <= 448 * 2^e (e >= -126; -126 for a block of zeros); codes hold
+ * x 2^-e rounded to e4m3 (nearest, ties to even: at most 2^-4 relative, or
+ * 2^-10 * 2^e absolute below the smallest normal code), scales hold e + 127.
+ * Scaling by powers of two is exact, so the code's rounding is the only one.
+ * NaN and infinities are kept as NaN and leave the block's maximum alone.
+ *
+ *   x       [M][x_stride] dtype (kda_pack8 in, kda_unpack8 out); 0 means C
+ *   codes   [M][C] bytes;  scales [M][ceil(C/32)] bytes; both dense
+ * ------------------------------------------------------------------------ */
+#define KDA_PACK8_BLOCK 32
+
+kda_status kda_pack8(const void* x, int64_t x_stride, kda_dtype dtype, int64_t M, int C, uint8_t* codes,
+                     uint8_t* scales, kda_stream_t stream);
+kda_status kda_unpack8(const uint8_t* codes, const uint8_t* scales, int64_t M, int C, void* x,
+                       int64_t x_stride, kda_dtype dtype, kda_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

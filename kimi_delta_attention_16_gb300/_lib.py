@@ -25,13 +25,16 @@ KDA_FLAG_TEST_DROP_STAGING = 4
 KDA_PATH_SIMT, KDA_PATH_TENSOR_CORE, KDA_PATH_RECURRENT = 0, 1, 2
 KDA_RECURRENT_MAX_LEN = 8
 KDA_MAX_SEGMENTS = 16
+KDA_PACK8_BLOCK = 32
 KDA_EPI_NONE, KDA_EPI_DECAY, KDA_EPI_SIGMOID = 0, 1, 2
-ABI_VERSION = 10401  # kda_backward with chunk records in its workspace
+ABI_VERSION = 10500  # layer norm, 8-bit activations and the selective state space scan
 
 # Every symbol include/kda.h declares.
 EXPORTED = ("kda_status_string", "kda_last_error", "kda_version", "kda_short_conv",
             "kda_prefill_workspace_size", "kda_prefill", "kda_prefill_plan", "kda_prefill_noalloc",
-            "kda_decode_step", "kda_gemm", "kda_backward_workspace_size", "kda_backward")
+            "kda_decode_step", "kda_gemm", "kda_backward_workspace_size", "kda_backward",
+            "kda_layer_norm", "kda_layer_norm_backward_workspace_size", "kda_layer_norm_backward",
+            "kda_pack8", "kda_unpack8")
 NOALLOC_SCRATCH_BYTES = 64 << 20  # KDA_NOALLOC_SCRATCH_BYTES in include/kda.h
 
 _vp = ctypes.c_void_p
@@ -89,6 +92,25 @@ class BackwardArgs(ctypes.Structure):
     ]
 
 
+class NormArgs(ctypes.Structure):
+    """Mirror of kda_norm_args."""
+    _fields_ = [
+        ("M", _i64), ("C", _int), ("io", _int),
+        ("x", _vp), ("x_stride", _i64), ("weight", _vp), ("bias", _vp), ("eps", _f),
+        ("y", _vp), ("y_stride", _i64), ("stats", _vp),
+    ]
+
+
+class NormBackwardArgs(ctypes.Structure):
+    """Mirror of kda_norm_backward_args."""
+    _fields_ = [
+        ("M", _i64), ("C", _int), ("io", _int),
+        ("dy", _vp), ("dy_stride", _i64), ("x", _vp), ("x_stride", _i64), ("x_scales", _vp),
+        ("stats", _vp), ("weight", _vp), ("dx", _vp), ("dx_stride", _i64),
+        ("dweight", _vp), ("dbias", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 def lib_path() -> str:
     return _build.SO
 
@@ -143,5 +165,16 @@ def load(auto_build: bool = True) -> ctypes.CDLL:
                                                     ctypes.POINTER(ctypes.c_size_t)]
         lib.kda_backward.restype = _int
         lib.kda_backward.argtypes = [ctypes.POINTER(BackwardArgs), _vp]
+        for name, args in (("kda_layer_norm", NormArgs), ("kda_layer_norm_backward", NormBackwardArgs)):
+            f = getattr(lib, name)
+            f.restype = _int
+            f.argtypes = [ctypes.POINTER(args), _vp]
+        lib.kda_layer_norm_backward_workspace_size.restype = _int
+        lib.kda_layer_norm_backward_workspace_size.argtypes = [ctypes.POINTER(NormBackwardArgs),
+                                                               ctypes.POINTER(ctypes.c_size_t)]
+        lib.kda_pack8.restype = _int
+        lib.kda_pack8.argtypes = [_vp, _i64, _int, _i64, _int, _vp, _vp, _vp]
+        lib.kda_unpack8.restype = _int
+        lib.kda_unpack8.argtypes = [_vp, _vp, _i64, _int, _vp, _i64, _int, _vp]
         _lib = lib
         return lib

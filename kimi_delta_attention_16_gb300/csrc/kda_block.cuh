@@ -1,0 +1,125 @@
+// kda_block.cuh -- internal launch declarations and device helpers of the operators around the
+// layer (kda_norm.cu, kda_pack8.cu, kda_ssm_*.cu).  Not part of the public ABI.
+#pragma once
+
+#include "kda_internal.cuh"
+
+namespace kda {
+
+// ------------------------------------------------------------------ rows of W elements per access
+// W consecutive elements of a row as they lie in memory: W * sizeof(T) bytes, 16 when the layout
+// allows vectors, one element otherwise.  load() only moves bytes, so several can be in flight
+// before the first conversion.
+template <typename T, int W> struct Raw {
+    static constexpr int kBytes = W * (int)sizeof(T);
+    static_assert(kBytes == 16 || kBytes == 8 || kBytes == 4 || kBytes == 2 || kBytes == 1, "access width");
+    uint32_t w[kBytes >= 4 ? kBytes / 4 : 1];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (kBytes == 16) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+            w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+        } else if constexpr (kBytes == 8) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+            w[0] = u.x; w[1] = u.y;
+        } else if constexpr (kBytes == 4) {
+            w[0] = __ldg(reinterpret_cast<const unsigned int*>(p));
+        } else if constexpr (kBytes == 2) {
+            w[0] = __ldg(reinterpret_cast<const unsigned short*>(p));
+        } else {
+            w[0] = __ldg(reinterpret_cast<const unsigned char*>(p));
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < (kBytes >= 4 ? kBytes / 4 : 1); ++i) w[i] = 0;
+    }
+};
+template <int W> __device__ __forceinline__ void unraw(const Raw<float, W>& r, float (&v)[W]) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = __uint_as_float(r.w[i]);
+}
+template <int W> __device__ __forceinline__ void unraw(const Raw<bf16, W>& r, float (&v)[W]) {
+    if constexpr (W == 1) {
+        v[0] = __uint_as_float(r.w[0] << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+            v[2 * i] = __uint_as_float(r.w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+        }
+    }
+}
+template <int W> __device__ __forceinline__ void store_row(float* p, const float (&v)[W]) {
+    if constexpr (W == 4) {
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+        static_assert(W == 1, "fp32 rows: 4 or 1 elements");
+        *p = v[0];
+    }
+}
+template <int W> __device__ __forceinline__ void store_row(bf16* p, const float (&v)[W]) {
+    if constexpr (W == 8) {
+        store8(p, v);
+    } else {
+        static_assert(W == 1, "bf16 rows: 8 or 1 elements");
+        *p = __float2bfloat16_rn(v[0]);
+    }
+}
+// fp32 parameters (weights, biases) for W consecutive channels; 16-byte accesses when W allows.
+template <int W> __device__ __forceinline__ void load_param(const float* p, float (&v)[W]) {
+    if constexpr (W % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) {
+            const float4 f = __ldg(reinterpret_cast<const float4*>(p) + i);
+            v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = __ldg(p + i);
+    }
+}
+
+// ------------------------------------------------------------------ e4m3 in blocks of 32
+// Byte s stands for 2^(s - 127), s >= 1 (a normal fp32 number).
+__device__ __forceinline__ float scale_of_byte(uint32_t s) { return __uint_as_float(s << 23); }
+// Two codes (low byte first) as fp32 values before the block's scale: by way of fp16, which holds
+// every e4m3 value exactly.
+__device__ __forceinline__ void e4m3x2_to_f(uint32_t two, float& lo, float& hi) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)two));
+    asm("{.reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}"
+        : "=f"(lo), "=f"(hi) : "r"(h));
+}
+template <int W> __device__ __forceinline__ void unraw8(const Raw<uint8_t, W>& r, float scale, float (&v)[W]) {
+    if constexpr (W == 1) {
+        float unused;
+        e4m3x2_to_f(r.w[0] & 0xffu, v[0], unused);
+        v[0] *= scale;
+    } else {
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+            e4m3x2_to_f((r.w[i / 2] >> (16 * (i & 1))) & 0xffffu, v[2 * i], v[2 * i + 1]);
+            v[2 * i] *= scale;
+            v[2 * i + 1] *= scale;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ launchers (arguments validated by the caller)
+cudaError_t launch_layer_norm(const kda_norm_args& a, cudaStream_t s);
+
+// How many row blocks kda_layer_norm_backward runs for M rows of C channels (each leaves one
+// partial sum of the weight's and the bias's gradient in the workspace), and its threads per block.
+struct NormBackwardPlan {
+    int blocks;
+    size_t workspace;  // bytes
+};
+NormBackwardPlan norm_backward_plan(const kda_norm_backward_args& a);
+cudaError_t launch_layer_norm_backward(const kda_norm_backward_args& a, const NormBackwardPlan& p, cudaStream_t s);
+
+cudaError_t launch_pack8(const void* x, int64_t x_stride, kda_dtype dt, int64_t M, int C, uint8_t* codes,
+                         uint8_t* scales, cudaStream_t s);
+cudaError_t launch_unpack8(const uint8_t* codes, const uint8_t* scales, int64_t M, int C, void* x, int64_t x_stride,
+                           kda_dtype dt, cudaStream_t s);
+
+}  // namespace kda

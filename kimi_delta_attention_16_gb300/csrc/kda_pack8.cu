@@ -1,0 +1,180 @@
+// kda_pack8.cu -- rows stored as e4m3 codes with one power of two per 32 channels, and back.
+//
+//   e = the smallest exponent with max|x| <= 448 2^e over the block (448 = the largest e4m3 value)
+//   code = e4m3(x 2^-e), byte = e + 127;  x ~ code 2^e
+//
+// The scaling is exact, so the code's own rounding (half a step: 2^-4 relative) is the only one,
+// and the packed form does not depend on how the maximum is reduced.  Bound by HBM: 2 + 1 bytes
+// per bf16 element, one way.  Four lanes share a block (8 elements each: one 16-byte access of
+// bf16, two of fp32) and join their maxima with two shuffles; a thread takes kRows rows of the
+// same columns at once to keep enough loads in flight.
+#include "kda_block.cuh"
+
+namespace kda {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kElems = 8;  // elements per thread and row
+constexpr int kRows = 4;   // rows per thread
+
+// e of the block's finite maximum (exact: exponent and mantissa bits).
+__device__ __forceinline__ int block_exponent(float amax) {
+    if (!(amax > 0.f)) return -126;
+    int e;
+    const float f = frexpf(amax, &e);  // amax = f 2^e, f in [0.5, 1)
+    e = e - 9 + (f > 0.875f ? 1 : 0);  // 448 = 0.875 * 2^9
+    return e < -126 ? -126 : e;
+}
+
+// Two values (already divided by the block's power of two, at most 448 in magnitude) as codes; NaN and
+// infinities become the NaN code.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+    unsigned short r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads) k_pack8(const T* __restrict__ x, int64_t xs, int64_t M, int C,
+                                                    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+    constexpr int W = VEC ? 16 / (int)sizeof(T) : 1;
+    const int nb = (C + KDA_PACK8_BLOCK - 1) / KDA_PACK8_BLOCK;
+    const int c0 = (blockIdx.x * blockDim.x + threadIdx.x) * kElems;
+    const int n = c0 < C ? (C - c0 < kElems ? C - c0 : kElems) : 0;  // elements of this thread inside the row
+    const int64_t tile = (int64_t)blockDim.y * kRows;
+    for (int64_t base = blockIdx.y * tile; base < M; base += gridDim.y * tile) {  // the same for the whole block
+        const int64_t r0 = base + threadIdx.y * kRows;
+        Raw<T, W> raw[kRows][kElems / W];
+#pragma unroll
+        for (int q = 0; q < kRows; ++q)
+#pragma unroll
+            for (int i = 0; i < kElems / W; ++i)
+                if (r0 + q < M && i * W < n) raw[q][i].load(x + (r0 + q) * xs + c0 + i * W); else raw[q][i].zero();
+#pragma unroll
+        for (int q = 0; q < kRows; ++q) {
+            float v[kElems], amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < kElems / W; ++i) {
+                float t[W];
+                unraw(raw[q][i], t);
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    const float a = fabsf(t[j]);
+                    // infinities turn into NaN here, and a NaN never passes the comparison below
+                    v[i * W + j] = a <= 3.402823466e38f ? t[j] : __int_as_float(0x7fffffff);
+                    if (a <= 3.402823466e38f) amax = fmaxf(amax, a);
+                }
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            const int64_t r = r0 + q;
+            if (r >= M || n == 0) continue;
+            const int e = block_exponent(amax);
+            const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+            uint32_t two[kElems / 2];
+#pragma unroll
+            for (int i = 0; i < kElems / 2; ++i) two[i] = to_e4m3x2(v[2 * i] * inv, v[2 * i + 1] * inv);
+            uint8_t* dst = codes + r * C + c0;
+            if constexpr (VEC) {  // C is a multiple of W, so a row's codes start on a W-byte boundary
+#pragma unroll
+                for (int i = 0; i < kElems / 4; ++i)
+                    if (i * 4 < n) reinterpret_cast<uint32_t*>(dst)[i] = two[2 * i] | (two[2 * i + 1] << 16);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kElems; ++i)
+                    if (i < n) dst[i] = (uint8_t)(two[i / 2] >> (8 * (i & 1)));
+            }
+            if ((threadIdx.x & 3) == 0) scales[r * nb + c0 / KDA_PACK8_BLOCK] = (uint8_t)(e + 127);
+        }
+    }
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads) k_unpack8(const uint8_t* __restrict__ codes,
+                                                      const uint8_t* __restrict__ scales, int64_t M, int C,
+                                                      T* __restrict__ x, int64_t xs) {
+    constexpr int W = VEC ? 16 / (int)sizeof(T) : 1;
+    const int nb = (C + KDA_PACK8_BLOCK - 1) / KDA_PACK8_BLOCK;
+    const int c0 = (blockIdx.x * blockDim.x + threadIdx.x) * kElems;
+    const int n = c0 < C ? (C - c0 < kElems ? C - c0 : kElems) : 0;
+    if (n == 0) return;
+    const int64_t tile = (int64_t)blockDim.y * kRows;
+    for (int64_t base = blockIdx.y * tile; base < M; base += gridDim.y * tile) {  // the same for the whole block
+        const int64_t r0 = base + threadIdx.y * kRows;
+        Raw<uint8_t, W> raw[kRows][kElems / W];
+        uint32_t sc[kRows];
+#pragma unroll
+        for (int q = 0; q < kRows; ++q) {
+            const bool in = r0 + q < M;
+            sc[q] = in ? (uint32_t)__ldg(scales + (r0 + q) * nb + c0 / KDA_PACK8_BLOCK) : 127u;
+#pragma unroll
+            for (int i = 0; i < kElems / W; ++i)
+                if (in && i * W < n) raw[q][i].load(codes + (r0 + q) * C + c0 + i * W); else raw[q][i].zero();
+        }
+#pragma unroll
+        for (int q = 0; q < kRows; ++q) {
+            if (r0 + q >= M) continue;
+#pragma unroll
+            for (int i = 0; i < kElems / W; ++i) {
+                float t[W];
+                unraw8(raw[q][i], scale_of_byte(sc[q]), t);
+                if (i * W < n) store_row(x + (r0 + q) * xs + c0 + i * W, t);
+            }
+        }
+    }
+}
+
+// Rows of `stride` elements at p allow 16-byte accesses of T, and rows of C codes the matching ones.
+template <typename T> bool vec_ok(const void* p, int64_t stride, const uint8_t* codes, int C) {
+    constexpr int W = 16 / (int)sizeof(T);
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % W == 0 && C % W == 0 &&
+           reinterpret_cast<uintptr_t>(codes) % 8 == 0;
+}
+
+// Narrow rows share a block: x = the threads of a row (a power of two, at least the four of one
+// 32-channel block), y = rows.
+dim3 block_of(int C) {
+    int x = 4;
+    while (x < kThreads && x * kElems < C) x *= 2;
+    return dim3(x, kThreads / x);
+}
+dim3 grid_of(int64_t M, int C) {
+    const dim3 b = block_of(C);
+    const int64_t rows = (M + b.y * kRows - 1) / (b.y * kRows);
+    return dim3((unsigned)((C + b.x * kElems - 1) / (b.x * kElems)), (unsigned)(rows < 65535 ? rows : 65535));
+}
+
+}  // namespace
+
+cudaError_t launch_pack8(const void* x, int64_t x_stride, kda_dtype dt, int64_t M, int C, uint8_t* codes,
+                         uint8_t* scales, cudaStream_t s) {
+    const dim3 g = grid_of(M, C), b = block_of(C);
+    if (dt == KDA_BF16) {
+        const bf16* p = static_cast<const bf16*>(x);
+        if (vec_ok<bf16>(x, x_stride, codes, C)) k_pack8<bf16, true><<<g, b, 0, s>>>(p, x_stride, M, C, codes, scales);
+        else k_pack8<bf16, false><<<g, b, 0, s>>>(p, x_stride, M, C, codes, scales);
+    } else {
+        const float* p = static_cast<const float*>(x);
+        if (vec_ok<float>(x, x_stride, codes, C)) k_pack8<float, true><<<g, b, 0, s>>>(p, x_stride, M, C, codes, scales);
+        else k_pack8<float, false><<<g, b, 0, s>>>(p, x_stride, M, C, codes, scales);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_unpack8(const uint8_t* codes, const uint8_t* scales, int64_t M, int C, void* x, int64_t x_stride,
+                           kda_dtype dt, cudaStream_t s) {
+    const dim3 g = grid_of(M, C), b = block_of(C);
+    if (dt == KDA_BF16) {
+        bf16* p = static_cast<bf16*>(x);
+        if (vec_ok<bf16>(x, x_stride, codes, C)) k_unpack8<bf16, true><<<g, b, 0, s>>>(codes, scales, M, C, p, x_stride);
+        else k_unpack8<bf16, false><<<g, b, 0, s>>>(codes, scales, M, C, p, x_stride);
+    } else {
+        float* p = static_cast<float*>(x);
+        if (vec_ok<float>(x, x_stride, codes, C)) k_unpack8<float, true><<<g, b, 0, s>>>(codes, scales, M, C, p, x_stride);
+        else k_unpack8<float, false><<<g, b, 0, s>>>(codes, scales, M, C, p, x_stride);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace kda
