@@ -483,6 +483,176 @@ kda_status kda_pack8(const void* x, int64_t x_stride, kda_dtype dtype, int64_t M
 kda_status kda_unpack8(const uint8_t* codes, const uint8_t* scales, int64_t M, int C, void* x,
                        int64_t x_stride, kda_dtype dtype, kda_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The selective state space mixer: a second recurrent mixer beside the KDA
+ * layer, with a diagonal state of N values per channel and a decay that
+ * depends on the token.  Per channel c and state n:
+ *
+ *   conv   u_t = act(bias + sum_{j=0..3} w[j] x[t-3+j]),  act = SiLU or none
+ *   step   delta_t = softplus(dt_t + dt_bias)       (softplus = 0: delta_t = dt_t + dt_bias)
+ *   scan   h_t[n] = exp(delta_t A[c][n]) h_{t-1}[n] + delta_t u_t B_t[g][n]
+ *   read   y_t = (sum_n C_t[g][n] h_t[n] + D u_t) silu(z_t)
+ *
+ * Channels 0 .. C-1 form G groups of C/G consecutive ones; a group shares its
+ * B and C rows.  Between conv and scan a model projects u to dt, B and C
+ * (kda_gemm), which is why they are two entry points.  Sequences are packed
+ * (cu_seqlens as for kda_prefill; zero lengths allowed, their final state is
+ * their initial state) and never see each other's tokens.  States, decays and
+ * every sum are fp32; only what is stored in io is rounded to it.
+ *
+ * kda_ssm_conv -- the convolution over packed sequences.
+ *   x, y      [T_total][row stride] io, C channels; y must not overlap x.
+ *   w         [C][4] fp32 (tap 3 multiplies x[t]; shorter filters: leading zeros)
+ *   bias      [C] fp32 or NULL (zeros);  silu nonzero: SiLU after the sum
+ *   conv_state_in   [N][C][3] io, oldest first, or NULL (zeros)
+ *   conv_state_out  [N][C][3] io or NULL: the last three raw values of every
+ *             sequence (conv_state_in's where it is shorter); must not overlap
+ *             conv_state_in.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    int N;                 /* sequences */
+    int C;                 /* channels */
+    int64_t T_total;       /* packed tokens */
+    kda_dtype io;
+    int silu;
+    const int32_t* cu_seqlens;       /* device [N+1] */
+    const int32_t* cu_seqlens_host;  /* host [N+1] or NULL (then only device-checked) */
+    const void* x;
+    int64_t x_stride;      /* elements between tokens; 0 means C */
+    const float* w;
+    const float* bias;
+    const void* conv_state_in;
+    void* conv_state_out;
+    void* y;
+    int64_t y_stride;      /* 0 means C */
+    int* d_status;
+} kda_ssm_conv_args;
+
+kda_status kda_ssm_conv(const kda_ssm_conv_args* args, kda_stream_t stream);
+
+/* One token for each of N sequences (T_total is ignored, x and y have N rows, cu_seqlens is
+ * ignored): conv_state_out is read and rolled in place, conv_state_in must be NULL. */
+kda_status kda_ssm_conv_step(const kda_ssm_conv_args* args, kda_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * kda_ssm_conv_backward -- with pre_t the convolution's sum before the activation and
+ * dpre_t = dy_t act'(pre_t):
+ *   dx_t = sum_j w[j] dpre_{t+3-j} (inside the sequence);  dw[j] = sum_t dpre_t x[t-3+j];
+ *   dbias = sum_t dpre_t;  dconv_state_in the same sum at the three places before the start.
+ * fwd: N, C, T_total, io, silu, cu_seqlens (and host copy), x, x_stride, w, bias and
+ * conv_state_in as in the forward call; the rest of it is ignored.  dx is [T_total][dx_stride] io,
+ * rounded once; dw [C][4], dbias [C] (NULL: not wanted) and dconv_state_in [N][C][3] (NULL: not
+ * wanted) are fp32.  dw and dbias are summed in a fixed order.  workspace:
+ * kda_ssm_conv_backward_workspace_size bytes, 256-byte aligned.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    kda_ssm_conv_args fwd;
+    const void* dy;
+    int64_t dy_stride;     /* 0 means C */
+    void* dx;
+    int64_t dx_stride;     /* 0 means C */
+    float* dw;
+    float* dbias;
+    float* dconv_state_in;
+    void* workspace;
+    size_t workspace_bytes;
+} kda_ssm_conv_backward_args;
+
+kda_status kda_ssm_conv_backward_workspace_size(const kda_ssm_conv_backward_args* args, size_t* bytes);
+kda_status kda_ssm_conv_backward(const kda_ssm_conv_backward_args* args, kda_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * kda_ssm_scan -- the scan over packed sequences.
+ *   u, dt, z, y  [T_total][row stride] io, C channels; z NULL: no gate.  y must not overlap an input.
+ *   A         [C][Nst] fp32, expected <= 0 (positive values grow the state without bound)
+ *   B, Cm     [T_total][row stride] io, each row G groups of Nst
+ *   D         [C] fp32 or NULL (zeros);  dt_bias [C] fp32 or NULL (zeros)
+ *   initial_state  [N][C][Nst] fp32 or NULL (zeros)
+ *   final_state    [N][C][Nst] fp32 or NULL; must not overlap initial_state
+ * Nst in {8, 16, 32, 64}; G >= 1 divides C.  A, the states and the workspace 16-byte aligned
+ * (the workspace 256).
+ *
+ * A long stream with few channels is cut into equal pieces of the packed token axis (whatever the
+ * sequences' borders): a first kernel takes every piece but the last from a zero state, a second
+ * joins them (the state at a piece's start is the carried one times exp(A times the sum of delta),
+ * plus what the piece before added), and the main kernel runs all pieces at once.  The workspace
+ * holds one state and one sum of delta per piece; none when one piece suffices.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    int N;                 /* sequences */
+    int C;                 /* channels */
+    int Nst;               /* states per channel */
+    int G;                 /* groups of B and Cm */
+    int64_t T_total;
+    kda_dtype io;
+    int softplus;
+    const int32_t* cu_seqlens;
+    const int32_t* cu_seqlens_host;
+    const void* u;
+    int64_t u_stride;      /* 0 means C */
+    const void* dt;
+    int64_t dt_stride;     /* 0 means C */
+    const float* A;
+    const void* B;
+    int64_t B_stride;      /* 0 means G*Nst */
+    const void* Cm;
+    int64_t C_stride;      /* 0 means G*Nst */
+    const float* D;
+    const void* z;
+    int64_t z_stride;      /* 0 means C */
+    const float* dt_bias;
+    const float* initial_state;
+    float* final_state;
+    void* y;
+    int64_t y_stride;      /* 0 means C */
+    void* workspace;
+    size_t workspace_bytes;
+    int* d_status;
+} kda_ssm_args;
+
+kda_status kda_ssm_scan_workspace_size(const kda_ssm_args* args, size_t* bytes);
+kda_status kda_ssm_scan(const kda_ssm_args* args, kda_stream_t stream);
+
+/* One token for each of N sequences: rows of u, dt, B, Cm, z and y are the sequences, and
+ * final_state is read and updated in place (initial_state must be NULL; T_total, cu_seqlens and
+ * the workspace are ignored). */
+kda_status kda_ssm_step(const kda_ssm_args* args, kda_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * kda_ssm_backward -- the gradients of one kda_ssm_scan call.  With g_t = dy_t silu(z_t) and
+ * lambda_t the gradient of h_t:
+ *   lambda_t = C_t g_t + a_{t+1} lambda_{t+1}   (d_final_state joins at a sequence's last token)
+ *   dC_t = sum_c g_t h_t;  dB_t = sum_c lambda_t delta_t u_t;  dA = sum_t lambda_t a_t h_{t-1} delta_t
+ *   du_t = delta_t sum_n lambda_t B_t + D g_t;  dD = sum_t g_t u_t
+ *   ddelta_t = u_t sum_n lambda_t B_t + sum_n lambda_t a_t h_{t-1} A;  ddt_t = ddelta_t softplus'
+ *   dz_t = dy_t (sum_n C_t h_t + D u_t) silu'(z_t);  dinitial_state = a_1 lambda_1
+ * fwd: the forward call's arguments; its y, final_state and workspace are ignored (the states are
+ * recomputed).  du, ddt, dz, dB and dC are io, dense ([T_total][C], [T_total][G][Nst]), rounded
+ * once; dA [C][Nst], dD [C], ddt_bias [C] and dinitial_state [N][C][Nst] are fp32.  dz, dD,
+ * ddt_bias and dinitial_state may be NULL (not wanted); the others must not.  Sums over channels
+ * and tokens go through the workspace in a fixed order.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    kda_ssm_args fwd;
+    const void* dy;
+    int64_t dy_stride;     /* 0 means C */
+    const float* d_final_state;  /* [N][C][Nst] fp32 or NULL (zeros) */
+    void* du;
+    void* ddt;
+    float* dA;
+    void* dB;
+    void* dC;
+    float* dD;
+    void* dz;
+    float* ddt_bias;
+    float* dinitial_state;
+    void* workspace;
+    size_t workspace_bytes;
+} kda_ssm_backward_args;
+
+kda_status kda_ssm_backward_workspace_size(const kda_ssm_backward_args* args, size_t* bytes);
+kda_status kda_ssm_backward(const kda_ssm_backward_args* args, kda_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -34,7 +34,9 @@ EXPORTED = ("kda_status_string", "kda_last_error", "kda_version", "kda_short_con
             "kda_prefill_workspace_size", "kda_prefill", "kda_prefill_plan", "kda_prefill_noalloc",
             "kda_decode_step", "kda_gemm", "kda_backward_workspace_size", "kda_backward",
             "kda_layer_norm", "kda_layer_norm_backward_workspace_size", "kda_layer_norm_backward",
-            "kda_pack8", "kda_unpack8")
+            "kda_pack8", "kda_unpack8", "kda_ssm_conv", "kda_ssm_conv_step",
+            "kda_ssm_conv_backward_workspace_size", "kda_ssm_conv_backward", "kda_ssm_scan_workspace_size",
+            "kda_ssm_scan", "kda_ssm_step", "kda_ssm_backward_workspace_size", "kda_ssm_backward")
 NOALLOC_SCRATCH_BYTES = 64 << 20  # KDA_NOALLOC_SCRATCH_BYTES in include/kda.h
 
 _vp = ctypes.c_void_p
@@ -111,6 +113,47 @@ class NormBackwardArgs(ctypes.Structure):
     ]
 
 
+class SsmConvArgs(ctypes.Structure):
+    """Mirror of kda_ssm_conv_args."""
+    _fields_ = [
+        ("N", _int), ("C", _int), ("T_total", _i64), ("io", _int), ("silu", _int),
+        ("cu_seqlens", _vp), ("cu_seqlens_host", _vp),
+        ("x", _vp), ("x_stride", _i64), ("w", _vp), ("bias", _vp),
+        ("conv_state_in", _vp), ("conv_state_out", _vp), ("y", _vp), ("y_stride", _i64), ("d_status", _vp),
+    ]
+
+
+class SsmConvBackwardArgs(ctypes.Structure):
+    """Mirror of kda_ssm_conv_backward_args."""
+    _fields_ = [
+        ("fwd", SsmConvArgs), ("dy", _vp), ("dy_stride", _i64), ("dx", _vp), ("dx_stride", _i64),
+        ("dw", _vp), ("dbias", _vp), ("dconv_state_in", _vp), ("workspace", _vp),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class SsmArgs(ctypes.Structure):
+    """Mirror of kda_ssm_args."""
+    _fields_ = [
+        ("N", _int), ("C", _int), ("Nst", _int), ("G", _int), ("T_total", _i64), ("io", _int), ("softplus", _int),
+        ("cu_seqlens", _vp), ("cu_seqlens_host", _vp),
+        ("u", _vp), ("u_stride", _i64), ("dt", _vp), ("dt_stride", _i64), ("A", _vp),
+        ("B", _vp), ("B_stride", _i64), ("Cm", _vp), ("C_stride", _i64), ("D", _vp),
+        ("z", _vp), ("z_stride", _i64), ("dt_bias", _vp), ("initial_state", _vp), ("final_state", _vp),
+        ("y", _vp), ("y_stride", _i64), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+        ("d_status", _vp),
+    ]
+
+
+class SsmBackwardArgs(ctypes.Structure):
+    """Mirror of kda_ssm_backward_args."""
+    _fields_ = [
+        ("fwd", SsmArgs), ("dy", _vp), ("dy_stride", _i64), ("d_final_state", _vp),
+        ("du", _vp), ("ddt", _vp), ("dA", _vp), ("dB", _vp), ("dC", _vp), ("dD", _vp), ("dz", _vp),
+        ("ddt_bias", _vp), ("dinitial_state", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 def lib_path() -> str:
     return _build.SO
 
@@ -165,13 +208,18 @@ def load(auto_build: bool = True) -> ctypes.CDLL:
                                                     ctypes.POINTER(ctypes.c_size_t)]
         lib.kda_backward.restype = _int
         lib.kda_backward.argtypes = [ctypes.POINTER(BackwardArgs), _vp]
-        for name, args in (("kda_layer_norm", NormArgs), ("kda_layer_norm_backward", NormBackwardArgs)):
+        for name, args in (("kda_layer_norm", NormArgs), ("kda_layer_norm_backward", NormBackwardArgs),
+                           ("kda_ssm_conv", SsmConvArgs), ("kda_ssm_conv_step", SsmConvArgs),
+                           ("kda_ssm_conv_backward", SsmConvBackwardArgs), ("kda_ssm_scan", SsmArgs),
+                           ("kda_ssm_step", SsmArgs), ("kda_ssm_backward", SsmBackwardArgs)):
             f = getattr(lib, name)
             f.restype = _int
             f.argtypes = [ctypes.POINTER(args), _vp]
-        lib.kda_layer_norm_backward_workspace_size.restype = _int
-        lib.kda_layer_norm_backward_workspace_size.argtypes = [ctypes.POINTER(NormBackwardArgs),
-                                                               ctypes.POINTER(ctypes.c_size_t)]
+        for name, args in (("kda_layer_norm_backward", NormBackwardArgs), ("kda_ssm_conv_backward", SsmConvBackwardArgs),
+                           ("kda_ssm_scan", SsmArgs), ("kda_ssm_backward", SsmBackwardArgs)):
+            f = getattr(lib, name + "_workspace_size")
+            f.restype = _int
+            f.argtypes = [ctypes.POINTER(args), ctypes.POINTER(ctypes.c_size_t)]
         lib.kda_pack8.restype = _int
         lib.kda_pack8.argtypes = [_vp, _i64, _int, _i64, _int, _vp, _vp, _vp]
         lib.kda_unpack8.restype = _int

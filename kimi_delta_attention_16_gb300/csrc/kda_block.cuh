@@ -105,7 +105,71 @@ template <int W> __device__ __forceinline__ void unraw8(const Raw<uint8_t, W>& r
     }
 }
 
+// ------------------------------------------------------------------ sums in a fixed order
+// Column sums of part [rows][W] fp32: 32 columns per block, the rows dealt to 32 warps and joined in
+// a fixed order, so the result depends on nothing but rows, W and the values.  put(column, sum).
+template <typename Put>
+__global__ void __launch_bounds__(1024) k_column_sum(const float* __restrict__ part, int64_t rows, int64_t W, Put put) {
+    __shared__ float sm[32][33];
+    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
+    float s = 0.f;
+    if (c < W) {
+#pragma unroll 4
+        for (int64_t g = threadIdx.y; g < rows; g += 32) s += part[g * W + c];
+    }
+    sm[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y || c >= W) return;
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) s += sm[k][threadIdx.x];
+    put(c, s);
+}
+template <typename Put>
+cudaError_t launch_column_sum(const float* part, int64_t rows, int64_t W, Put put, cudaStream_t s) {
+    k_column_sum<<<(unsigned)((W + 31) / 32), dim3(32, 32), 0, s>>>(part, rows, W, put);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ packed sequences
+// The sequence that holds token t: the last n in [0, N) with cu[n] <= t (cu[n + 1] > t when cu is
+// consistent, so empty sequences are passed over).  Always in range.
+__device__ __forceinline__ int seq_of(const int32_t* __restrict__ cu, int N, int64_t t) {
+    int lo = 0, hi = N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((int64_t)cu[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
 // ------------------------------------------------------------------ launchers (arguments validated by the caller)
+// dst[n] = src[n] (zeros when src is NULL) for every sequence of no tokens, `per` bytes each (a
+// multiple of 2): what a kernel over tokens never reaches.
+cudaError_t launch_empty_sequences(const int32_t* cu, int N, const void* src, void* dst, int64_t per, cudaStream_t s);
+
+cudaError_t launch_ssm_conv(const kda_ssm_conv_args& a, cudaStream_t s);
+cudaError_t launch_ssm_conv_step(const kda_ssm_conv_args& a, cudaStream_t s);
+struct ConvBackwardPlan {
+    int run;        // tokens per thread
+    int64_t rows;   // partial sums of dw and dbias
+    size_t workspace;
+};
+ConvBackwardPlan conv_backward_plan(const kda_ssm_conv_args& f);
+cudaError_t launch_ssm_conv_backward(const kda_ssm_conv_backward_args& a, const ConvBackwardPlan& p, cudaStream_t s);
+
+// Pieces of the packed token axis that the scan runs side by side, and where the workspace holds
+// their states [pieces][C][Nst] and sums of delta [pieces][C].
+struct ScanPlan {
+    int64_t piece;   // tokens per piece (a multiple of the tile)
+    int pieces;
+    size_t sums;     // byte offset
+    size_t workspace;
+};
+ScanPlan scan_plan(const kda_ssm_args& a);
+cudaError_t launch_ssm_scan(const kda_ssm_args& a, const ScanPlan& p, cudaStream_t s);
+cudaError_t launch_ssm_step(const kda_ssm_args& a, cudaStream_t s);
+
 cudaError_t launch_layer_norm(const kda_norm_args& a, cudaStream_t s);
 
 // How many row blocks kda_layer_norm_backward runs for M rows of C channels (each leaves one

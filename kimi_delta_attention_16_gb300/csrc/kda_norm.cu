@@ -8,7 +8,7 @@
 // registers of one block (VPT accesses of W elements per thread), so the statistics take two
 // passes over registers, none over memory.  The backward is persistent: a thread owns the same
 // columns in every row of its block, keeps their dw and db sums in registers and leaves one
-// partial per block, which k_norm_param_sum adds up in block order (no atomics: the same bits
+// partial per block, which k_column_sum adds up in block order (no atomics: the same bits
 // every time).  The next row's accesses are issued before the current row's sums.
 #include "kda_block.cuh"
 
@@ -188,29 +188,17 @@ k_layer_norm_bwd(const T* __restrict__ dy, int64_t dys, const void* __restrict__
     }
 }
 
-// dw and db: column sums of the blocks' partials [blocks][2][C], 32 columns per block, the rows
-// dealt to 32 warps and joined in a fixed order.
-__global__ void __launch_bounds__(1024) k_norm_param_sum(const float* __restrict__ part, int blocks, int C,
-                                                         float* __restrict__ dw, float* __restrict__ db) {
-    __shared__ float sm[32][33];
-    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x, W = 2 * (int64_t)C;
-    float s = 0.f;
-    if (c < W) {
-#pragma unroll 4
-        for (int g = threadIdx.y; g < blocks; g += 32) s += part[g * W + c];
+struct PutParams {  // column c of [dw | db]
+    float *dw, *db;
+    int C;
+    __device__ void operator()(int64_t c, float s) const {
+        if (c < C) {
+            if (dw) dw[c] = s;
+        } else if (db) {
+            db[c - C] = s;
+        }
     }
-    sm[threadIdx.y][threadIdx.x] = s;
-    __syncthreads();
-    if (threadIdx.y) return;
-    s = 0.f;
-#pragma unroll
-    for (int k = 0; k < 32; ++k) s += sm[k][threadIdx.x];
-    if (c < C) {
-        if (dw) dw[c] = s;
-    } else if (c < W && db) {
-        db[c - C] = s;
-    }
-}
+};
 
 bool vec_ok(const void* p, int64_t stride, int esize, int w) {
     return reinterpret_cast<uintptr_t>(p) % (w * esize) == 0 && stride % w == 0;
@@ -318,9 +306,7 @@ cudaError_t launch_layer_norm_backward(const kda_norm_backward_args& a, const No
 #undef KDA_LNB
     cudaError_t e = cudaGetLastError();
     if (e || !part) return e;
-    k_norm_param_sum<<<(unsigned)((2 * (int64_t)a.C + 31) / 32), dim3(32, 32), 0, s>>>(part, p.blocks, a.C, a.dweight,
-                                                                                       a.dbias);
-    return cudaGetLastError();
+    return launch_column_sum(part, p.blocks, 2 * (int64_t)a.C, PutParams{a.dweight, a.dbias, a.C}, s);
 }
 
 }  // namespace kda

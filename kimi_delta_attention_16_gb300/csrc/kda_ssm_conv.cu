@@ -1,0 +1,380 @@
+// kda_ssm_conv.cu -- the selective scan's causal depthwise convolution of width 4: packed prompts,
+// one token per sequence, and the gradients.
+//
+//   pre_t = bias + sum_j w[j] x[t-3+j],  y_t = silu(pre_t)
+//   dpre_t = dy_t silu'(pre_t),  dx_t = sum_j w[j] dpre_{t+3-j},  dw[j] = sum_t dpre_t x[t-3+j]
+//
+// Bound by HBM (one read of x, one write of y; backward: x and dy read, dx written).  A thread
+// owns W consecutive channels (one 16-byte access, or one element where the layout allows no more)
+// and walks a run of tokens with the last three raw values in registers; the loads of kBatch tokens
+// are issued together.  The backward walks forward too: the contributions to the last three dx wait
+// in registers, and a run reads three tokens past its end to finish its own.  dw and dbias: per
+// thread over its run, per block over its runs through shared memory, then over the blocks.
+#include "kda_block.cuh"
+
+namespace kda {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 4;
+
+__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// Raw value at place `pos` (< 0: before the sequence, from the conv state or zero), W channels from c.
+template <typename T, int W>
+__device__ __forceinline__ void place(const T* __restrict__ x, int64_t xs, const T* __restrict__ cs, int64_t s, int64_t pos,
+                                      int64_t n, int C, int c, float (&v)[W]) {
+    if (pos >= 0) {
+        Raw<T, W> r;
+        r.load(x + (s + pos) * xs + c);
+        unraw(r, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[j] = cs && pos >= -3 ? to_f(cs[(n * C + c + j) * 3 + 3 + pos]) : 0.f;
+    }
+}
+
+template <typename T, int W>
+__global__ void __launch_bounds__(kThreads)
+k_conv(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const float* __restrict__ bias, int silu,
+       const int32_t* __restrict__ cu, int N, int64_t T_total, int C, const T* __restrict__ cs_in, T* __restrict__ cs_out,
+       T* __restrict__ y, int64_t ys, int run) {
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * W;
+    const int64_t t0 = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * run;
+    if (c >= C || t0 >= T_total) return;
+    const int64_t t1 = t0 + run < T_total ? t0 + run : T_total;
+    float wt[4][W], bs[W], win[3][W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        const float4 f = make_float4(w[(int64_t)(c + j) * 4], w[(int64_t)(c + j) * 4 + 1], w[(int64_t)(c + j) * 4 + 2],
+                                     w[(int64_t)(c + j) * 4 + 3]);
+        wt[0][j] = f.x; wt[1][j] = f.y; wt[2][j] = f.z; wt[3][j] = f.w;
+        bs[j] = bias ? bias[c + j] : 0.f;
+    }
+    int n = seq_of(cu, N, t0);
+    int64_t s, e;
+    seq_range(cu, n, T_total, s, e);
+#pragma unroll
+    for (int m = 0; m < 3; ++m) place(x, xs, cs_in, s, t0 - s - 3 + m, n, C, c, win[m]);
+    for (int64_t tb = t0; tb < t1; tb += kBatch) {
+        Raw<T, W> raw[kBatch];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q)
+            if (tb + q < t1) raw[q].load(x + (tb + q) * xs + c); else raw[q].zero();
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const int64_t t = tb + q;
+            if (t >= t1) break;
+            if (t >= e && n < N - 1) {  // crossed into a later sequence
+                while (t >= e && n < N - 1) {
+                    ++n;
+                    seq_range(cu, n, T_total, s, e);
+                }
+#pragma unroll
+                for (int m = 0; m < 3; ++m) place(x, xs, cs_in, s, t - s - 3 + m, n, C, c, win[m]);
+            }
+            float v[W], o[W];
+            unraw(raw[q], v);
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                float a = bs[j];
+                a = fmaf(wt[0][j], win[0][j], a);
+                a = fmaf(wt[1][j], win[1][j], a);
+                a = fmaf(wt[2][j], win[2][j], a);
+                a = fmaf(wt[3][j], v[j], a);
+                o[j] = silu ? a * sigmoid_fast(a) : a;
+                win[0][j] = win[1][j];
+                win[1][j] = win[2][j];
+                win[2][j] = v[j];
+            }
+            store_row(y + t * ys + c, o);
+            if (cs_out && t == e - 1) {
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+#pragma unroll
+                    for (int m = 0; m < 3; ++m) cs_out[((int64_t)n * C + c + j) * 3 + m] = from_f<T>(win[m][j]);
+            }
+        }
+    }
+}
+
+// One token per sequence: the three old values and the new one, the state rolled in place.  Its own
+// thread reads and writes a (sequence, channel)'s state.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+k_conv_step(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const float* __restrict__ bias, int silu,
+            int N, int C, T* __restrict__ cs, T* __restrict__ y, int64_t ys) {
+    const int c = blockIdx.x * kThreads + threadIdx.x;
+    if (c >= C) return;
+    const float w0 = w[(int64_t)c * 4], w1 = w[(int64_t)c * 4 + 1], w2 = w[(int64_t)c * 4 + 2], w3 = w[(int64_t)c * 4 + 3];
+    const float b = bias ? bias[c] : 0.f;
+    for (int64_t n = blockIdx.y; n < N; n += gridDim.y) {
+        T* st = cs + (n * C + c) * 3;
+        const T s1 = st[1], s2 = st[2], xv = x[n * xs + c];
+        float a = fmaf(w0, to_f(st[0]), b);
+        a = fmaf(w1, to_f(s1), a);
+        a = fmaf(w2, to_f(s2), a);
+        a = fmaf(w3, to_f(xv), a);
+        y[n * ys + c] = from_f<T>(silu ? a * sigmoid_fast(a) : a);
+        st[0] = s1;
+        st[1] = s2;
+        st[2] = xv;
+    }
+}
+
+template <typename T, int W>
+__global__ void __launch_bounds__(kThreads)
+k_conv_bwd(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const float* __restrict__ bias, int silu,
+           const int32_t* __restrict__ cu, int N, int64_t T_total, int C, const T* __restrict__ cs_in,
+           const T* __restrict__ dy, int64_t dys, T* __restrict__ dx, int64_t dxs, float* __restrict__ dcs,
+           float* __restrict__ part, int run) {
+    extern __shared__ float sm[];  // [blockDim.y][5][blockDim.x * W]
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * W;
+    const int64_t t0 = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * run;
+    float gw[5][W];  // dw[0..3], dbias
+#pragma unroll
+    for (int k = 0; k < 5; ++k)
+#pragma unroll
+        for (int j = 0; j < W; ++j) gw[k][j] = 0.f;
+    if (c < C && t0 < T_total) {
+        const int64_t t1 = t0 + run < T_total ? t0 + run : T_total;
+        float wt[4][W], bs[W], win[3][W], pend[3][W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) wt[k][j] = w[(int64_t)(c + j) * 4 + k];
+            bs[j] = bias ? bias[c + j] : 0.f;
+            pend[0][j] = pend[1][j] = pend[2][j] = 0.f;
+        }
+        int n = seq_of(cu, N, t0);
+        int64_t s, e;
+        seq_range(cu, n, T_total, s, e);
+#pragma unroll
+        for (int m = 0; m < 3; ++m) place(x, xs, cs_in, s, t0 - s - 3 + m, n, C, c, win[m]);
+        // The finished gradient of the value at place p (absolute): a token of this run, or one of the
+        // three values before a sequence that starts in it.
+        auto put = [&](int64_t p, const float (&v)[W]) {
+            if (p >= s) {
+                if (p >= t0 && p < t1) store_row(dx + p * dxs + c, v);
+            } else if (dcs && s >= t0 && p >= s - 3) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) dcs[((int64_t)n * C + c + j) * 3 + (p - s + 3)] = v[j];
+            }
+        };
+        auto flush = [&](int64_t t) {  // the sequence ends before t: nothing more reaches the pending three
+#pragma unroll
+            for (int m = 0; m < 3; ++m) put(t - 3 + m, pend[m]);
+        };
+        const int64_t last = t1 + 3 < T_total ? t1 + 3 : T_total;
+        bool open = true;  // the pending three still wait for tokens of their own sequence
+        for (int64_t tb = t0; tb < last && open; tb += kBatch) {
+            Raw<T, W> rx[kBatch], rd[kBatch];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                if (tb + q < last) {
+                    rx[q].load(x + (tb + q) * xs + c);
+                    rd[q].load(dy + (tb + q) * dys + c);
+                } else {
+                    rx[q].zero();
+                    rd[q].zero();
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const int64_t t = tb + q;
+                if (t >= last || !open) break;
+                if (t >= e && n < N - 1) {
+                    flush(e);
+                    if (t >= t1) {  // past this run's tokens and its last sequence
+                        open = false;
+                        break;
+                    }
+                    while (t >= e && n < N - 1) {
+                        ++n;
+                        seq_range(cu, n, T_total, s, e);
+                    }
+#pragma unroll
+                    for (int m = 0; m < 3; ++m) place(x, xs, cs_in, s, t - s - 3 + m, n, C, c, win[m]);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) pend[0][j] = pend[1][j] = pend[2][j] = 0.f;
+                }
+                float v[W], d[W];
+                unraw(rx[q], v);
+                unraw(rd[q], d);
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    if (silu) {
+                        float a = bs[j];
+                        a = fmaf(wt[0][j], win[0][j], a);
+                        a = fmaf(wt[1][j], win[1][j], a);
+                        a = fmaf(wt[2][j], win[2][j], a);
+                        a = fmaf(wt[3][j], v[j], a);
+                        const float sg = sigmoid_fast(a);
+                        d[j] *= sg * fmaf(a, 1.f - sg, 1.f);
+                    }
+                    if (t < t1) {
+                        gw[0][j] = fmaf(d[j], win[0][j], gw[0][j]);
+                        gw[1][j] = fmaf(d[j], win[1][j], gw[1][j]);
+                        gw[2][j] = fmaf(d[j], win[2][j], gw[2][j]);
+                        gw[3][j] = fmaf(d[j], v[j], gw[3][j]);
+                        gw[4][j] += d[j];
+                    }
+                    win[0][j] = win[1][j];
+                    win[1][j] = win[2][j];
+                    win[2][j] = v[j];
+                    pend[0][j] = fmaf(wt[0][j], d[j], pend[0][j]);
+                }
+                put(t - 3, pend[0]);
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    pend[0][j] = fmaf(wt[1][j], d[j], pend[1][j]);
+                    pend[1][j] = fmaf(wt[2][j], d[j], pend[2][j]);
+                    pend[2][j] = wt[3][j] * d[j];
+                }
+            }
+        }
+        if (open && last == T_total) flush(T_total);
+    }
+    const int bw = blockDim.x * W;  // channels of the block
+#pragma unroll
+    for (int k = 0; k < 5; ++k)
+#pragma unroll
+        for (int j = 0; j < W; ++j) sm[(threadIdx.y * 5 + k) * bw + threadIdx.x * W + j] = gw[k][j];
+    __syncthreads();
+    for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < 5 * bw; i += blockDim.x * blockDim.y) {
+        float t = 0.f;
+        for (int r = 0; r < blockDim.y; ++r) t += sm[r * 5 * bw + i];
+        const int k = i / bw, ch = blockIdx.y * bw + i - k * bw;
+        if (ch < C) part[((int64_t)blockIdx.x * 5 + k) * C + ch] = t;
+    }
+}
+
+struct PutConv {  // column k * C + c of [dw[0] | dw[1] | dw[2] | dw[3] | dbias]
+    float *dw, *db;
+    int C;
+    __device__ void operator()(int64_t i, float s) const {
+        const int64_t k = i / C, c = i - k * C;
+        if (k < 4) {
+            if (dw) dw[c * 4 + k] = s;
+        } else if (db) {
+            db[c] = s;
+        }
+    }
+};
+
+__global__ void k_empty_sequences(const int32_t* __restrict__ cu, int N, const uint16_t* __restrict__ src,
+                                  uint16_t* __restrict__ dst, int64_t per) {
+    for (int64_t n = blockIdx.y; n < N; n += gridDim.y) {
+        if (cu[n + 1] != cu[n]) continue;
+        for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < per; i += (int64_t)gridDim.x * blockDim.x)
+            dst[n * per + i] = src ? src[n * per + i] : (uint16_t)0;
+    }
+}
+
+bool wide(const void* p, int64_t stride, int es) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % (16 / es) == 0;
+}
+int64_t stride_or(int64_t s, int64_t d) { return s ? s : d; }
+
+// Threads along the channels: a power of two, at most a warp.
+int lanes_of(int accesses) {
+    int x = 1;
+    while (x < 32 && x < accesses) x *= 2;
+    return x;
+}
+
+// Tokens per thread: long runs re-read fewer border tokens, short ones fill the GPU; 64 once
+// there are over 1,024 threads per SM, never below 8.
+int run_of(int64_t T, int64_t accesses) {
+    DeviceInfo di{0, 0, 0};
+    const int64_t want = 1024 * (int64_t)(current_device_info(&di) ? di.sm_count : 1);
+    int run = 64;
+    while (run > 8 && T * accesses / run < want) run /= 2;
+    return run;
+}
+
+}  // namespace
+
+cudaError_t launch_empty_sequences(const int32_t* cu, int N, const void* src, void* dst, int64_t per, cudaStream_t s) {
+    const int64_t units = per / 2;
+    const int64_t bx = (units + 255) / 256;
+    k_empty_sequences<<<dim3((unsigned)(bx < 64 ? bx : 64), (unsigned)(N < 4096 ? N : 4096)), 256, 0, s>>>(
+        cu, N, static_cast<const uint16_t*>(src), static_cast<uint16_t*>(dst), units);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_ssm_conv(const kda_ssm_conv_args& a, cudaStream_t s) {
+    const int es = a.io == KDA_BF16 ? 2 : 4;
+    const int64_t xs = stride_or(a.x_stride, a.C), ys = stride_or(a.y_stride, a.C);
+    const bool vec = a.C % (16 / es) == 0 && wide(a.x, xs, es) && wide(a.y, ys, es);
+    const int W = vec ? 16 / es : 1;
+    const int acc = (a.C + W - 1) / W;
+    const dim3 b(lanes_of(acc), kThreads / lanes_of(acc));
+    const int run = run_of(a.T_total, acc);
+    const dim3 g((unsigned)((a.T_total + (int64_t)run * b.y - 1) / ((int64_t)run * b.y)), (unsigned)((acc + b.x - 1) / b.x));
+#define KDA_CONV(T, W)                                                                                              \
+    k_conv<T, W><<<g, b, 0, s>>>(static_cast<const T*>(a.x), xs, a.w, a.bias, a.silu, a.cu_seqlens, a.N, a.T_total,  \
+                                 a.C, static_cast<const T*>(a.conv_state_in), static_cast<T*>(a.conv_state_out),     \
+                                 static_cast<T*>(a.y), ys, run)
+    if (a.io == KDA_BF16) {
+        if (vec) KDA_CONV(bf16, 8); else KDA_CONV(bf16, 1);
+    } else {
+        if (vec) KDA_CONV(float, 4); else KDA_CONV(float, 1);
+    }
+#undef KDA_CONV
+    return cudaGetLastError();
+}
+
+cudaError_t launch_ssm_conv_step(const kda_ssm_conv_args& a, cudaStream_t s) {
+    const int64_t xs = stride_or(a.x_stride, a.C), ys = stride_or(a.y_stride, a.C);
+    const dim3 g((unsigned)((a.C + kThreads - 1) / kThreads), (unsigned)(a.N < 65535 ? a.N : 65535));
+    if (a.io == KDA_BF16)
+        k_conv_step<<<g, kThreads, 0, s>>>(static_cast<const bf16*>(a.x), xs, a.w, a.bias, a.silu, a.N, a.C,
+                                           static_cast<bf16*>(a.conv_state_out), static_cast<bf16*>(a.y), ys);
+    else
+        k_conv_step<<<g, kThreads, 0, s>>>(static_cast<const float*>(a.x), xs, a.w, a.bias, a.silu, a.N, a.C,
+                                           static_cast<float*>(a.conv_state_out), static_cast<float*>(a.y), ys);
+    return cudaGetLastError();
+}
+
+ConvBackwardPlan conv_backward_plan(const kda_ssm_conv_args& f) {
+    const int es = f.io == KDA_BF16 ? 2 : 4;
+    // The layout of the rows may rule out wide accesses only after the workspace was sized, so the run
+    // and the partial rows follow from sizes alone: those of the wide layout hold for both.
+    const int acc = (f.C + 16 / es - 1) / (16 / es);
+    ConvBackwardPlan p;
+    p.run = run_of(f.T_total, acc);
+    const int64_t by = kThreads / lanes_of(acc);
+    p.rows = (f.T_total + p.run * by - 1) / (p.run * by);
+    p.workspace = (size_t)p.rows * 5 * f.C * sizeof(float);
+    return p;
+}
+
+cudaError_t launch_ssm_conv_backward(const kda_ssm_conv_backward_args& a, const ConvBackwardPlan& p, cudaStream_t s) {
+    const kda_ssm_conv_args& f = a.fwd;
+    const int es = f.io == KDA_BF16 ? 2 : 4;
+    const int64_t xs = stride_or(f.x_stride, f.C), dys = stride_or(a.dy_stride, f.C), dxs = stride_or(a.dx_stride, f.C);
+    const bool vec = f.C % (16 / es) == 0 && wide(f.x, xs, es) && wide(a.dy, dys, es) && wide(a.dx, dxs, es);
+    const int W = vec ? 16 / es : 1;
+    const int lanes = lanes_of((f.C + 16 / es - 1) / (16 / es));
+    const dim3 b(lanes, kThreads / lanes);
+    const dim3 g((unsigned)p.rows, (unsigned)((f.C + (int64_t)lanes * W - 1) / ((int64_t)lanes * W)));
+    const size_t smem = (size_t)kThreads * 5 * W * sizeof(float);  // at most 40 KB
+    float* part = static_cast<float*>(a.workspace);
+#define KDA_CONVB(T, W)                                                                                             \
+    k_conv_bwd<T, W><<<g, b, smem, s>>>(static_cast<const T*>(f.x), xs, f.w, f.bias, f.silu, f.cu_seqlens, f.N,      \
+                                        f.T_total, f.C, static_cast<const T*>(f.conv_state_in),                      \
+                                        static_cast<const T*>(a.dy), dys, static_cast<T*>(a.dx), dxs,                \
+                                        a.dconv_state_in, part, p.run)
+    if (f.io == KDA_BF16) {
+        if (vec) KDA_CONVB(bf16, 8); else KDA_CONVB(bf16, 1);
+    } else {
+        if (vec) KDA_CONVB(float, 4); else KDA_CONVB(float, 1);
+    }
+#undef KDA_CONVB
+    if (cudaError_t e = cudaGetLastError()) return e;
+    return launch_column_sum(part, p.rows, 5 * (int64_t)f.C, PutConv{a.dw, a.dbias, f.C}, s);
+}
+
+}  // namespace kda
