@@ -170,6 +170,21 @@ ScanPlan scan_plan(const kda_ssm_args& a);
 cudaError_t launch_ssm_scan(const kda_ssm_args& a, const ScanPlan& p, cudaStream_t s);
 cudaError_t launch_ssm_step(const kda_ssm_args& a, cudaStream_t s);
 
+// The scan's gradients: pieces of the token axis and the byte offsets of the workspace's parts.
+struct SsmBackwardPlan {
+    int64_t piece;
+    int pieces;
+    size_t fwd, rev;      // [pieces][C][Nst]: states at the pieces' starts; gradients that enter from the right
+    size_t fsum, rsum;    // [pieces][C]: sums of delta
+    size_t ckpt;          // [ceil(T / 4)][C][Nst]: the state in front of every fourth token
+    size_t pa;            // [pieces][C][Nst]: parts of dA
+    size_t pd;            // [pieces * rows][2][C]: parts of dD and ddt_bias
+    size_t pbc;           // [G * blocks][T][2 Nst]: parts of dB and dC
+    size_t workspace;
+};
+SsmBackwardPlan ssm_backward_plan(const kda_ssm_args& f);
+cudaError_t launch_ssm_backward(const kda_ssm_backward_args& a, const SsmBackwardPlan& p, cudaStream_t s);
+
 cudaError_t launch_layer_norm(const kda_norm_args& a, cudaStream_t s);
 
 // How many row blocks kda_layer_norm_backward runs for M rows of C channels (each leaves one

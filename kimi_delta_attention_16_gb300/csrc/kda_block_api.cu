@@ -407,7 +407,62 @@ kda_status kda_ssm_step(const kda_ssm_args* a, kda_stream_t stream) {
     return ok();
 }
 
-kda_status kda_ssm_backward_workspace_size(const kda_ssm_backward_args*, size_t*) { return KDA_ERR_UNSUPPORTED; }
-kda_status kda_ssm_backward(const kda_ssm_backward_args*, kda_stream_t) { return KDA_ERR_UNSUPPORTED; }
+kda_status kda_ssm_backward_workspace_size(const kda_ssm_backward_args* b, size_t* bytes) {
+    if (!bytes) return fail(KDA_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = 0;
+    if (!b) return fail(KDA_ERR_INVALID_ARG, "args is NULL");
+    const kda_ssm_args& f = b->fwd;
+    if (kda_status st = check_ssm_sizes(f)) return st;
+    if (f.T_total < 0 || f.T_total > 0x7fffffffLL || f.C > kMaxChannels) return fail(KDA_ERR_INVALID_ARG, "bad sizes");
+    if (f.T_total > 0) *bytes = ssm_backward_plan(f).workspace;
+    return ok();
+}
+
+kda_status kda_ssm_backward(const kda_ssm_backward_args* b, kda_stream_t stream) {
+    if (!b) return fail(KDA_ERR_INVALID_ARG, "args is NULL");
+    const kda_ssm_args& f = b->fwd;
+    kda_status st;
+    if ((st = check_packed(f.N, f.C, f.T_total, f.io, f.cu_seqlens, f.cu_seqlens_host)) || (st = check_ssm_sizes(f)))
+        return st;
+    const size_t es = dsize(f.io), cb = (size_t)f.C * 4, an = cb * f.Nst, sb = state_bytes(f);
+    if (!b->dA) return fail(KDA_ERR_INVALID_ARG, "dA is NULL");
+    if (!aligned(b->dA, 4) || !aligned(b->dD, 4) || !aligned(b->ddt_bias, 4) || !aligned(b->dinitial_state, 16) ||
+        !aligned(b->d_final_state, 16))
+        return fail(KDA_ERR_INVALID_ARG, "dA, dD and ddt_bias must be 4-byte aligned, the states' gradients 16-byte");
+    const size_t rb = (size_t)f.T_total * f.C * es, gb = (size_t)f.T_total * f.G * f.Nst * es;
+    const int64_t dys = stride_or(b->dy_stride, f.C);
+    SsmBackwardPlan p{};
+    if (f.T_total > 0) {
+        if ((st = check_ssm_rows(f, f.T_total)) || (st = check_plain_rows(b->dy, f.T_total, dys, f.C, es, "dy"))) return st;
+        if (!b->du || !b->ddt || !b->dB || !b->dC)
+            return fail(KDA_ERR_INVALID_ARG, "du, ddt, dB and dC must be non-NULL");
+        if (!aligned(b->du, es) || !aligned(b->ddt, es) || !aligned(b->dB, es) || !aligned(b->dC, es) || !aligned(b->dz, es))
+            return fail(KDA_ERR_INVALID_ARG, "a gradient is not aligned to its element");
+        if (b->dz && !f.z) return fail(KDA_ERR_INVALID_ARG, "dz wanted but z is NULL");
+        p = ssm_backward_plan(f);
+        if ((st = check_workspace(b->workspace, b->workspace_bytes, p.workspace))) return st;
+    }
+    const Span outs[] = {{b->du, rb, "du"}, {b->ddt, rb, "ddt"}, {b->dA, an, "dA"}, {b->dB, gb, "dB"}, {b->dC, gb, "dC"},
+                         {b->dD, cb, "dD"}, {b->dz, rb, "dz"}, {b->ddt_bias, cb, "ddt_bias"},
+                         {b->dinitial_state, sb, "dinitial_state"}, {b->workspace, p.workspace, "workspace"}};
+    if ((st = check_overlaps(outs, ssm_inputs(f, f.T_total).in))) return st;
+    const Span more[] = {{b->dy, rows_bytes(f.T_total, dys, f.C, es), "dy"}, {b->d_final_state, sb, "d_final_state"}};
+    if ((st = check_overlaps(outs, more))) return st;
+    cudaStream_t s = cu_stream(stream);
+    cudaError_t e;
+    if (f.T_total == 0) {  // no tokens: the final states are the initial ones, every other gradient is zero
+        if ((e = cudaMemsetAsync(b->dA, 0, an, s)) || (b->dD && (e = cudaMemsetAsync(b->dD, 0, cb, s))) ||
+            (b->ddt_bias && (e = cudaMemsetAsync(b->ddt_bias, 0, cb, s))))
+            return cuda_fail(e, "ssm backward");
+    }
+    if (f.N == 0) return ok();
+    if (!f.cu_seqlens_host && (e = launch_check_cu(f.cu_seqlens, f.N, f.T_total, f.d_status, s)))
+        return cuda_fail(e, "check cu_seqlens");
+    if (b->dinitial_state && may_have_empty(f.N, f.cu_seqlens_host) &&
+        (e = launch_empty_sequences(f.cu_seqlens, f.N, b->d_final_state, b->dinitial_state, sb / f.N, s)))
+        return cuda_fail(e, "ssm initial state gradient");
+    if (f.T_total > 0 && (e = launch_ssm_backward(*b, p, s))) return cuda_fail(e, "ssm backward");
+    return ok();
+}
 
 }  // extern "C"

@@ -10,20 +10,29 @@ namespace ssm {
 // softplus(x) = max(x, 0) + log(1 + e^-|x|), to a few units of the last place for every x: the
 // logarithm as 2 atanh(s), s = e / (2 + e) <= 1/3, by its odd power series up to s^13 (the next
 // term is below 2^-26 of the sum).  log(1 + e) directly would lose the digits of a small e.
-__device__ __forceinline__ float softplus(float x) {
-    const float e = expf(-fabsf(x));
-    const float s = __fdividef(e, 2.f + e), q = s * s;
-    float p = 1.f / 13.f;
-    p = fmaf(p, q, 1.f / 11.f);
-    p = fmaf(p, q, 1.f / 9.f);
-    p = fmaf(p, q, 1.f / 7.f);
-    p = fmaf(p, q, 1.f / 5.f);
-    p = fmaf(p, q, 1.f / 3.f);
-    p = fmaf(p, q, 1.f);
-    return fmaxf(x, 0.f) + 2.f * s * p;
+// Both halves of a pair at once.
+__device__ __forceinline__ float rcp_hw(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
-__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + expf(-x)); }
+__device__ __forceinline__ f2 softplus2(f2 x) {
+    const f2 t = mul2(f2_of(fabsf(f2_lo(x)), fabsf(f2_hi(x))), f2_dup(-kLog2e));
+    const f2 e = f2_of(exp2_hw(f2_lo(t)), exp2_hw(f2_hi(t)));
+    const f2 d = add2(e, f2_dup(2.f));
+    const f2 s = mul2(e, f2_of(rcp_hw(f2_lo(d)), rcp_hw(f2_hi(d)))), q = mul2(s, s);
+    f2 p = f2_dup(2.f / 13.f);
+    p = fma2(p, q, f2_dup(2.f / 11.f));
+    p = fma2(p, q, f2_dup(2.f / 9.f));
+    p = fma2(p, q, f2_dup(2.f / 7.f));
+    p = fma2(p, q, f2_dup(2.f / 5.f));
+    p = fma2(p, q, f2_dup(2.f / 3.f));
+    p = fma2(p, q, f2_dup(2.f));
+    return fma2(s, p, f2_of(fmaxf(f2_lo(x), 0.f), fmaxf(f2_hi(x), 0.f)));
+}
+__device__ __forceinline__ float softplus(float x) { return f2_lo(softplus2(f2_of(x, 0.f))); }
+__device__ __forceinline__ float sigmoid(float x) { return rcp_hw(1.f + exp2_hw(-kLog2e * x)); }
+__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 
 // 2^x of both halves.
 __device__ __forceinline__ f2 exp2_2(f2 x) { return f2_of(exp2_hw(f2_lo(x)), exp2_hw(f2_hi(x))); }
@@ -44,25 +53,65 @@ struct Params {
     const float *A, *D, *dt_bias, *init;
     float* fin;
     const int32_t* cu;
-    float *ws_state, *ws_sum;
+    float *ws_state, *ws_sum, *ckpt;
     int64_t T, piece;
     int N, C, G, Cg, bpg;  // sequences, channels, groups, channels and blocks per group
     int pieces, softplus;
+    bool vec;  // 16-byte copies of every row
 };
 
-constexpr int kCB = 64;  // channels per block
+Params params_of(const kda_ssm_args& a);  // everything but the pieces and the workspace
+// The state in front of every fourth token to p.ckpt [ceil(T / 4)][C][NS] (pieces start at multiples of 8).
+cudaError_t launch_states(Params& p, const kda_ssm_args& a, cudaStream_t s);
 
-// Block of kCB channels (32 pairs c, c + 32) x NS states: a thread holds 4 states of both channels
-// of a pair.  The lanes of a warp that share states are neighbours, so a token's B and C, four
-// floats per lane, take two shared-memory cycles per warp instead of four.
+// Block of CB channels x NS states: a thread holds up to 16 states of one channel, L threads share a
+// channel.  Lanes that hold the same states are neighbours, so they read a token's B and C at one
+// shared-memory address (broadcast).
 template <int NS> struct Lay {
-    static constexpr int L = NS / 4;          // threads along the states
-    static constexpr int kThreads = 32 * L;
-    static constexpr int KPW = 32 / L;        // channel pairs per warp
-    static constexpr int TT = NS == 64 ? 8 : 16;  // tokens per tile
-    static constexpr int EPT = TT * kCB / kThreads;  // (token, channel) elements per thread and tile
-    static constexpr int BPT = TT * NS / kThreads;   // elements of B (and C) per thread and tile
+    static constexpr int SPT = NS < 16 ? NS : 16;  // states per thread
+    static constexpr int L = NS / SPT;             // threads per channel
+    static constexpr int NT = 64;                  // threads per block
+    static constexpr int CB = NT / L;              // channels per block
+    static constexpr int KPW = 32 / L;             // channels per warp
+    static constexpr int TT = 8;                   // tokens per tile
+    static constexpr int BPT = TT * NS / NT;       // elements of B (and C) per thread and tile
+    static_assert(BPT >= 1, "tile too small");
 };
+
+// ------------------------------------------------------------------ tiles of rows through shared memory
+// kDepth tiles of TT rows x W elements in flight: asynchronous 16-byte copies where base, stride and
+// first column allow them (the last piece of a row may be short: it is filled with zeros), plain
+// element copies otherwise.  `rows_left`: rows of the tile that exist; the others keep old contents.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// One tile: rows [0, rows) of `src` (already at the tile's first row and the block's first column), W
+// columns of which `cols` exist, into dst[TT][W].
+template <typename T, int TT, int W, int NT>
+__device__ __forceinline__ void copy_tile(T* dst, const T* src, int64_t stride, int rows, int cols, bool vec) {
+    if (vec) {
+        constexpr int E = 16 / (int)sizeof(T), PR = W / E;  // elements per piece, pieces per row
+        static_assert(W % E == 0, "rows are whole pieces");
+#pragma unroll
+        for (int k = 0; k < (TT * PR + NT - 1) / NT; ++k) {
+            const int i = k * NT + (int)threadIdx.x, r = i / PR, c = i % PR * E;
+            if ((TT * PR) % NT && i >= TT * PR) break;
+            const int left = cols - c;
+            if (r < rows && left > 0)
+                cp_async16(dst + r * W + c, src + r * stride + c, left >= E ? 16 : left * (int)sizeof(T));
+        }
+    } else {
+#pragma unroll 4
+        for (int i = threadIdx.x; i < TT * W; i += NT) {
+            const int r = i / W, c = i % W;
+            if (r < rows && c < cols) dst[i] = src[r * stride + c];
+        }
+    }
+}
 
 }  // namespace ssm
 }  // namespace kda

@@ -1,0 +1,618 @@
+// kda_ssm_backward.cu -- the gradients of the selective state space scan.
+//
+//   g_t = dy_t silu(z_t);  lambda_t = C_t g_t + a_{t+1} lambda_{t+1};  q_t = a_{t+1} lambda_{t+1}
+//   dC_t = sum_c g h_t;  dB_t = sum_c lambda delta u;  dA += lambda a h_{t-1} delta
+//   s1 = sum_n lambda B;  s2 = sum_n lambda a h_{t-1} A
+//   du = delta s1 + D g;  ddelta = u s1 + s2;  dz = dy (sum_n C h + D u) silu'(z)
+//
+// The states are recomputed.  Forward passes leave the state in front of every fourth token; the
+// main kernel walks a piece of the token axis backwards in tiles of four, runs a tile forward from
+// its checkpoint with a h_{t-1} of all four tokens in registers, and then backward.  Where a stream
+// is cut into pieces, what enters a piece from the right comes from a pass of its own (k_rev), the
+// mirror image of the forward scan's.
+//
+// Two sums cross the threads for every token: over the states (s1, s2, y of a channel) and over the
+// channels (dB, dC of a state).  A thread therefore holds a 4 x 4 tile of (channel, state): both
+// sums run over four values in registers first, which costs nothing (they ride on the products),
+// and the rest goes through shared memory.  Sums over the blocks' channels and over the pieces go
+// through the workspace and are added in a fixed order.
+#include "kda_ssm.cuh"
+
+namespace kda {
+
+namespace {
+
+using namespace ssm;
+
+struct BParams {
+    Params f;
+    const void* dy;
+    int64_t dys;
+    const float* dfin;
+    float *rev, *rsum, *pa, *pd, *pbc, *dinit;
+    void *du, *ddt, *dz;
+    int bpg;  // blocks per group of the main kernel
+    bool vec; // 16-byte copies of every row, dy's too
+};
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+// ------------------------------------------------------------------ what enters a piece from the right
+// Pieces 1 .. pieces - 1, each from zero at its right end (or from d_final_state where a sequence
+// ends): q in front of its first token, and its sum of delta.  Layout and copies as in the forward scan.
+template <typename T, int NS>
+__global__ void __launch_bounds__(Lay<NS>::NT, 8) k_rev(BParams b) {
+    using Y = Lay<NS>;
+    constexpr int TT = Y::TT, NT = Y::NT, BPT = Y::BPT, H = Y::SPT / 2, Q = Y::SPT / 4, CB = Y::CB;
+    constexpr int kDepth = 4;
+    struct Tile {
+        T dt[TT][CB], dy[TT][CB], z[TT][CB], C[TT][NS];
+    };
+    __shared__ __align__(16) Tile ring[kDepth];
+    __shared__ __align__(16) float sC[2][TT][NS];
+    const Params& p = b.f;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int l = lane / Y::KPW, cl = warp * Y::KPW + lane % Y::KPW;
+    const int g = blockIdx.x / p.bpg;
+    const int c_lo = g * p.Cg + (blockIdx.x % p.bpg) * CB, c_hi = (g + 1) * p.Cg, cols = c_hi - c_lo;
+    const bool in = c_lo + cl < c_hi, gate = p.z != nullptr;
+    const int c = in ? c_lo + cl : c_hi - 1;
+    const int piece = blockIdx.y + 1;
+    const int64_t t0 = piece * p.piece, t1 = t0 + p.piece < p.T ? t0 + p.piece : p.T;
+    const int64_t so = (int64_t)c * NS + l * Y::SPT;
+    f2 A2[H], q[H];
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p.A + so) + i);
+        A2[2 * i] = f2_of(a.x * kLog2e, a.y * kLog2e);
+        A2[2 * i + 1] = f2_of(a.z * kLog2e, a.w * kLog2e);
+    }
+    auto load_q = [&](const float* base, int64_t n) {
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (base) s = reinterpret_cast<const float4*>(base + n * p.C * NS + so)[i];
+            q[2 * i] = f2_of(s.x, s.y);
+            q[2 * i + 1] = f2_of(s.z, s.w);
+        }
+    };
+    int n = seq_of(p.cu, p.N, t1 - 1);
+    int64_t s0 = p.cu[n];
+    load_q(p.cu[n + 1] == t1 ? b.dfin : nullptr, n);
+    const float bias = p.dt_bias ? p.dt_bias[c] : 0.f;
+    const int tiles = (int)((t1 - t0 + TT - 1) / TT);
+    auto issue = [&](int j) {  // the j-th tile from the right
+        if (j < tiles) {
+            Tile& r = ring[j % kDepth];
+            const int64_t tb = t0 + (int64_t)(tiles - 1 - j) * TT;
+            const int rows = (int)(t1 - tb < TT ? t1 - tb : TT);
+            copy_tile<T, TT, CB, NT>(&r.dt[0][0], static_cast<const T*>(p.dt) + tb * p.dts + c_lo, p.dts, rows, cols, b.vec);
+            copy_tile<T, TT, CB, NT>(&r.dy[0][0], static_cast<const T*>(b.dy) + tb * b.dys + c_lo, b.dys, rows, cols, b.vec);
+            if (gate)
+                copy_tile<T, TT, CB, NT>(&r.z[0][0], static_cast<const T*>(p.z) + tb * p.zs + c_lo, p.zs, rows, cols, b.vec);
+            copy_tile<T, TT, NS, NT>(&r.C[0][0], static_cast<const T*>(p.Cm) + tb * p.cs + g * NS, p.cs, rows, NS, b.vec);
+        }
+        cp_commit();
+    };
+    auto widen = [&](int j) {
+        const Tile& r = ring[j % kDepth];
+#pragma unroll
+        for (int k = 0; k < BPT; ++k) {
+            const int i = k * NT + tid;
+            sC[j & 1][i / NS][i % NS] = to_f(r.C[i / NS][i % NS]);
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < kDepth - 1; ++j) issue(j);
+    cp_wait<kDepth - 2>();
+    __syncthreads();
+    widen(0);
+    float dsum = 0.f;
+    for (int j = 0; j < tiles; ++j) {
+        const int64_t tb = t0 + (int64_t)(tiles - 1 - j) * TT;
+        const int buf = j & 1;
+        cp_wait<kDepth - 3>();
+        __syncthreads();
+        if (j + 1 < tiles) widen(j + 1);
+        issue(j + kDepth - 1);
+        const Tile& r = ring[j % kDepth];
+        const int nt = (int)(t1 - tb < TT ? t1 - tb : TT);
+        auto token = [&](int t, float d, float gv) {
+            const f2 dd = f2_dup(d), gg = f2_dup(gv);
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                const float4 v = *reinterpret_cast<const float4*>(&sC[buf][t][l * Y::SPT + 4 * i]);
+                q[2 * i] = mul2(exp2_2(mul2(dd, A2[2 * i])), fma2(f2_of(v.x, v.y), gg, q[2 * i]));
+                q[2 * i + 1] = mul2(exp2_2(mul2(dd, A2[2 * i + 1])), fma2(f2_of(v.z, v.w), gg, q[2 * i + 1]));
+            }
+        };
+        auto grad = [&](int t) {
+            const float d = to_f(r.dy[t][cl]);
+            return gate ? d * silu(to_f(r.z[t][cl])) : d;
+        };
+        if (nt == TT && s0 <= tb) {  // no sequence starts behind the tile's first token
+            float d[TT], gv[TT];
+#pragma unroll
+            for (int t = 0; t < TT; t += 2) {
+                const f2 x = add2(f2_of(to_f(r.dt[t][cl]), to_f(r.dt[t + 1][cl])), f2_dup(bias));
+                const f2 v = p.softplus ? softplus2(x) : x;
+                d[t] = f2_lo(v);
+                d[t + 1] = f2_hi(v);
+                gv[t] = grad(t);
+                gv[t + 1] = grad(t + 1);
+            }
+#pragma unroll
+            for (int t = TT - 1; t >= 0; --t) {
+                token(t, d[t], gv[t]);
+                dsum += d[t];
+            }
+        } else {
+#pragma unroll 1
+            for (int t = nt - 1; t >= 0; --t) {
+                if (tb + t < s0) {  // into the sequence before
+                    n = seq_of(p.cu, p.N, tb + t);
+                    s0 = p.cu[n];
+                    load_q(b.dfin, n);
+                }
+                const float x = to_f(r.dt[t][cl]) + bias, d = p.softplus ? softplus(x) : x;
+                token(t, d, grad(t));
+                dsum += d;
+            }
+        }
+    }
+    if (in) {
+#pragma unroll
+        for (int i = 0; i < Q; ++i)
+            reinterpret_cast<float4*>(b.rev + (int64_t)piece * p.C * NS + so)[i] =
+                make_float4(f2_lo(q[2 * i]), f2_hi(q[2 * i]), f2_lo(q[2 * i + 1]), f2_hi(q[2 * i + 1]));
+        if (l == 0) b.rsum[(int64_t)piece * p.C + c] = dsum;
+    }
+}
+
+// Slot k: from what piece k sends to its left by itself to all that it sends (what piece k - 1 starts from).
+template <int NS> __global__ void __launch_bounds__(256) k_rev_join(BParams b) {
+    const Params& p = b.f;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = (int64_t)p.C * NS;
+    if (i >= row) return;
+    const int64_t c = i / NS;
+    const float a2 = p.A[i] * kLog2e;
+    float carry = b.rev[(p.pieces - 1) * row + i];
+#pragma unroll 4
+    for (int k = p.pieces - 2; k >= 1; --k) {
+        const bool started = p.cu[seq_of(p.cu, p.N, (k + 1) * p.piece - 1)] >= k * p.piece;
+        const float own = b.rev[k * row + i];
+        const float f = exp2_hw(a2 * b.rsum[(int64_t)k * p.C + c]);
+        carry = started ? own : fmaf(f, carry, own);
+        b.rev[k * row + i] = carry;
+    }
+}
+
+// ------------------------------------------------------------------ the main kernel
+// Block of CH channels x NS states, 4 x 4 per thread; lanes with the same states are neighbours.
+template <int NS> struct BLay {
+    static constexpr int L = NS / 4;            // threads along the states
+    static constexpr int NT = 128;
+    static constexpr int KK = NT / L;           // threads along the channels
+    static constexpr int KPW = 32 / L;
+    static constexpr int CH = 4 * KK;           // channels per block
+    static constexpr int TT = 4;                // tokens per tile
+    static constexpr int EPT = TT * CH / NT;    // (token, channel) elements per thread and tile
+    static constexpr int CPT = CH > NT ? CH / NT : 1;  // distinct channels among them
+    static constexpr int RPC = NT > CH ? NT / CH : 1;  // threads that share a channel's elements
+    static constexpr int BPT = (TT * NS + NT - 1) / NT;
+    static constexpr int VW = 2 * NS + 4;       // row of the dB | dC parts, padded against bank conflicts
+};
+template <typename T, int NS> struct BShared {
+    using Y = BLay<NS>;
+    struct Tile {
+        T u[Y::TT][Y::CH], dt[Y::TT][Y::CH], z[Y::TT][Y::CH], dy[Y::TT][Y::CH], B[Y::TT][NS], C[Y::TT][NS];
+    };
+    Tile ring[2];
+    float4 ck[2][4][Y::NT];                       // checkpoints, each thread its own
+    float d[Y::TT][Y::CH], du[Y::TT][Y::CH], g[Y::TT][Y::CH];
+    float B[Y::TT][NS], C[Y::TT][NS];
+    float part[3][Y::TT][Y::L][Y::CH];            // s1, s2, y
+    float bc[Y::TT][Y::KK][Y::VW];                // dB | dC
+};
+
+template <typename T, int NS>
+__global__ void __launch_bounds__(128, 2) k_ssm_bwd(BParams b) {
+    using Y = BLay<NS>;
+    constexpr int L = Y::L, NT = Y::NT, CH = Y::CH, TT = Y::TT, EPT = Y::EPT;
+    extern __shared__ __align__(16) unsigned char raw_shared[];
+    BShared<T, NS>& sm = *reinterpret_cast<BShared<T, NS>*>(raw_shared);
+    const Params& p = b.f;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int l = lane / Y::KPW, kk = warp * Y::KPW + lane % Y::KPW;
+    const int g = blockIdx.x / b.bpg;
+    const int c_lo = g * p.Cg + (blockIdx.x % b.bpg) * CH, c_hi = (g + 1) * p.Cg, cols = c_hi - c_lo;
+    const int piece = blockIdx.y;
+    const int64_t t0 = piece * p.piece, t1 = t0 + p.piece < p.T ? t0 + p.piece : p.T;
+    const bool gate = p.z != nullptr;
+
+    // 4 channels x 4 states: pairs run over the channels (0, 1) and (2, 3)
+    auto load_tile = [&](const float* base, int64_t row, f2 (&v)[4][2], float scale) {
+        float m[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int ch = c_lo + 4 * kk + i;
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (base && ch < c_hi) f = *reinterpret_cast<const float4*>(base + (row * p.C + ch) * NS + 4 * l);
+            m[i][0] = f.x; m[i][1] = f.y; m[i][2] = f.z; m[i][3] = f.w;
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) v[s][h] = f2_of(m[2 * h][s] * scale, m[2 * h + 1][s] * scale);
+    };
+    auto store_tile = [&](float* base, int64_t row, const f2 (&v)[4][2]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int ch = c_lo + 4 * kk + i, h = i / 2;
+            float o[4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) o[s] = i & 1 ? f2_hi(v[s][h]) : f2_lo(v[s][h]);
+            if (ch < c_hi)
+                *reinterpret_cast<float4*>(base + (row * p.C + ch) * NS + 4 * l) = make_float4(o[0], o[1], o[2], o[3]);
+        }
+    };
+    f2 A2[4][2], q[4][2], dA[4][2];
+    load_tile(p.A, 0, A2, kLog2e);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) dA[s][0] = dA[s][1] = f2_dup(0.f);
+    int n = seq_of(p.cu, p.N, t1 - 1);
+    int64_t s0 = p.cu[n];  // start of the sequence that the walk is in
+    if (p.cu[n + 1] == t1) load_tile(b.dfin, n, q, 1.f);
+    else load_tile(piece + 1 < p.pieces ? b.rev : nullptr, piece + 1, q, 1.f);
+
+    // this thread's elements: token (i NT + tid) / CH, channel (i NT + tid) % CH
+    float bias[Y::CPT], skip[Y::CPT], accD[Y::CPT], accB[Y::CPT];
+    bool cin[Y::CPT];
+#pragma unroll
+    for (int k = 0; k < Y::CPT; ++k) {
+        const int ch = c_lo + (k * NT + tid) % CH;
+        cin[k] = ch < c_hi;
+        bias[k] = cin[k] && p.dt_bias ? p.dt_bias[ch] : 0.f;
+        skip[k] = cin[k] && p.D ? p.D[ch] : 0.f;
+        accD[k] = accB[k] = 0.f;
+    }
+    const int tiles = (int)((t1 - t0 + TT - 1) / TT);
+    auto issue = [&](int j) {  // the j-th tile from the right
+        if (j < tiles) {
+            typename BShared<T, NS>::Tile& r = sm.ring[j & 1];
+            const int64_t tb = t0 + (int64_t)(tiles - 1 - j) * TT;
+            const int rows = (int)(t1 - tb < TT ? t1 - tb : TT);
+            copy_tile<T, TT, CH, NT>(&r.u[0][0], static_cast<const T*>(p.u) + tb * p.us + c_lo, p.us, rows, cols, b.vec);
+            copy_tile<T, TT, CH, NT>(&r.dt[0][0], static_cast<const T*>(p.dt) + tb * p.dts + c_lo, p.dts, rows, cols, b.vec);
+            copy_tile<T, TT, CH, NT>(&r.dy[0][0], static_cast<const T*>(b.dy) + tb * b.dys + c_lo, b.dys, rows, cols, b.vec);
+            if (gate)
+                copy_tile<T, TT, CH, NT>(&r.z[0][0], static_cast<const T*>(p.z) + tb * p.zs + c_lo, p.zs, rows, cols, b.vec);
+            copy_tile<T, TT, NS, NT>(&r.B[0][0], static_cast<const T*>(p.B) + tb * p.bs + g * NS, p.bs, rows, NS, b.vec);
+            copy_tile<T, TT, NS, NT>(&r.C[0][0], static_cast<const T*>(p.Cm) + tb * p.cs + g * NS, p.cs, rows, NS, b.vec);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // a channel past the group's last: zeros
+                const int ch = c_lo + 4 * kk + i;
+                const float* src = p.ckpt + (tb / 4 * p.C + (ch < c_hi ? ch : c_lo)) * NS + 4 * l;
+                cp_async16(&sm.ck[j & 1][i][tid], src, ch < c_hi ? 16 : 0);
+            }
+        }
+        cp_commit();
+    };
+    issue(0);
+    cp_wait<0>();
+    __syncthreads();
+    for (int j = 0; j < tiles; ++j) {
+        const int64_t tb = t0 + (int64_t)(tiles - 1 - j) * TT;
+        const int nt = (int)(t1 - tb < TT ? t1 - tb : TT);
+        const typename BShared<T, NS>::Tile& r = sm.ring[j & 1];
+        // Step sizes and gradients of the reads; tokens past the end and channels past the group count as
+        // zeros everywhere, which leaves states, gradients and sums as they are.
+        float x[EPT], u[EPT], z[EPT], dy[EPT];
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+            const int e = i * NT + tid, t = e / CH, cc = e % CH, k = i % Y::CPT;
+            const bool on = t < nt && cin[k];
+            x[i] = on ? to_f(r.dt[t][cc]) + bias[k] : 0.f;
+            u[i] = on ? to_f(r.u[t][cc]) : 0.f;
+            dy[i] = on ? to_f(r.dy[t][cc]) : 0.f;
+            z[i] = on && gate ? to_f(r.z[t][cc]) : 0.f;
+            const float d = on ? (p.softplus ? softplus(x[i]) : x[i]) : 0.f;
+            sm.d[t][cc] = d;
+            sm.du[t][cc] = d * u[i];
+            sm.g[t][cc] = gate ? dy[i] * silu(z[i]) : dy[i];
+        }
+#pragma unroll
+        for (int k = 0; k < Y::BPT; ++k) {
+            const int i = k * NT + tid;
+            if ((TT * NS) % NT && i >= TT * NS) break;
+            const bool on = i / NS < nt;
+            sm.B[i / NS][i % NS] = on ? to_f(r.B[i / NS][i % NS]) : 0.f;
+            sm.C[i / NS][i % NS] = on ? to_f(r.C[i / NS][i % NS]) : 0.f;
+        }
+        f2 h[4][2];
+        {
+            float m[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 f = sm.ck[j & 1][i][tid];
+                m[i][0] = f.x; m[i][1] = f.y; m[i][2] = f.z; m[i][3] = f.w;
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) h[s][k] = f2_of(m[2 * k][s], m[2 * k + 1][s]);
+        }
+        __syncthreads();
+        issue(j + 1);
+
+        f2 ha[TT][4][2];  // a_t h_{t-1}
+        auto pair4 = [&](const float* v, f2 (&o)[2]) {  // four channels of a row
+            const float4 f = *reinterpret_cast<const float4*>(v + 4 * kk);
+            o[0] = f2_of(f.x, f.y);
+            o[1] = f2_of(f.z, f.w);
+        };
+        auto dup4 = [&](const float* v, f2 (&o)[4]) {  // four states of a row, each for both channels of a pair
+            const float4 f = *reinterpret_cast<const float4*>(v + 4 * l);
+            o[0] = f2_dup(f.x); o[1] = f2_dup(f.y); o[2] = f2_dup(f.z); o[3] = f2_dup(f.w);
+        };
+        auto forward = [&](int t) {
+            f2 d[2], du[2], B[4];
+            pair4(sm.d[t], d);
+            pair4(sm.du[t], du);
+            dup4(sm.B[t], B);
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    ha[t][s][k] = mul2(exp2_2(mul2(d[k], A2[s][k])), h[s][k]);
+                    h[s][k] = fma2(du[k], B[s], ha[t][s][k]);
+                }
+        };
+        auto backward = [&](int t) {
+            f2 d[2], du[2], gg[2], B[4], C[4], s1[2], s2[2], y[2];
+            pair4(sm.d[t], d);
+            pair4(sm.du[t], du);
+            pair4(sm.g[t], gg);
+            dup4(sm.B[t], B);
+            dup4(sm.C[t], C);
+            float dB[4], dC[4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) s1[k] = s2[k] = y[k] = f2_dup(0.f);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                f2 vb = f2_dup(0.f), vc = f2_dup(0.f);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const f2 hk = fma2(du[k], B[s], ha[t][s][k]);
+                    const f2 lam = fma2(C[s], gg[k], q[s][k]);
+                    vc = fma2(gg[k], hk, vc);
+                    vb = fma2(lam, du[k], vb);
+                    y[k] = fma2(C[s], hk, y[k]);
+                    s1[k] = fma2(lam, B[s], s1[k]);
+                    const f2 w = mul2(lam, ha[t][s][k]);
+                    s2[k] = fma2(w, A2[s][k], s2[k]);
+                    dA[s][k] = fma2(w, d[k], dA[s][k]);
+                    q[s][k] = mul2(exp2_2(mul2(d[k], A2[s][k])), lam);
+                }
+                dB[s] = f2_lo(vb) + f2_hi(vb);
+                dC[s] = f2_lo(vc) + f2_hi(vc);
+            }
+            auto put = [&](float* row, const f2 (&v)[2]) {
+                *reinterpret_cast<float4*>(row + 4 * kk) = make_float4(f2_lo(v[0]), f2_hi(v[0]), f2_lo(v[1]), f2_hi(v[1]));
+            };
+            put(sm.part[0][t][l], s1);
+            put(sm.part[1][t][l], s2);
+            put(sm.part[2][t][l], y);
+            *reinterpret_cast<float4*>(&sm.bc[t][kk][4 * l]) = make_float4(dB[0], dB[1], dB[2], dB[3]);
+            *reinterpret_cast<float4*>(&sm.bc[t][kk][NS + 4 * l]) = make_float4(dC[0], dC[1], dC[2], dC[3]);
+        };
+        if (s0 < tb) {  // no sequence starts in the tile
+#pragma unroll
+            for (int t = 0; t < TT; ++t) forward(t);
+#pragma unroll
+            for (int t = TT - 1; t >= 0; --t) backward(t);
+        } else {
+            auto starts = [&](int64_t t, int& m) {  // whether token t is its sequence's first
+                m = seq_of(p.cu, p.N, t);
+                return (int64_t)p.cu[m] == t;
+            };
+            int m;
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                if (t < nt && starts(tb + t, m)) load_tile(p.init, m, h, 1.f);
+                forward(t);
+            }
+#pragma unroll
+            for (int t = TT - 1; t >= 0; --t) {
+                backward(t);
+                if (t < nt && starts(tb + t, m)) {  // q is the initial state's gradient; on to the sequence before
+                    if (b.dinit) store_tile(b.dinit, m, q);
+                    if (tb + t > 0) {
+                        n = seq_of(p.cu, p.N, tb + t - 1);
+                        s0 = p.cu[n];
+                        load_tile(b.dfin, n, q, 1.f);
+                    }
+                }
+            }
+        }
+        cp_wait<0>();
+        __syncthreads();
+
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+            const int e = i * NT + tid, t = e / CH, cc = e % CH, k = i % Y::CPT;
+            if (t >= nt || !cin[k]) continue;
+            float s1 = 0.f, s2 = 0.f, y = 0.f;
+#pragma unroll
+            for (int v = 0; v < L; ++v) {
+                s1 += sm.part[0][t][v][cc];
+                s2 += sm.part[1][t][v][cc];
+                y += sm.part[2][t][v][cc];
+            }
+            const float d = sm.d[t][cc], gv = sm.g[t][cc];
+            const int64_t o = (tb + t) * p.C + c_lo + cc;
+            static_cast<T*>(b.du)[o] = from_f<T>(fmaf(d, s1, skip[k] * gv));
+            float dd = fmaf(u[i], s1, kLn2 * s2);  // A2 carries log2 e
+            if (p.softplus) dd *= sigmoid(x[i]);
+            static_cast<T*>(b.ddt)[o] = from_f<T>(dd);
+            accB[k] += dd;
+            accD[k] = fmaf(gv, u[i], accD[k]);
+            if (b.dz) {
+                const float sg = sigmoid(z[i]);
+                static_cast<T*>(b.dz)[o] = from_f<T>(dy[i] * fmaf(skip[k], u[i], y) * sg * fmaf(z[i], 1.f - sg, 1.f));
+            }
+        }
+        float* pbc = b.pbc + ((int64_t)blockIdx.x * p.T + tb) * 2 * NS;
+#pragma unroll
+        for (int i = tid; i < TT * 2 * NS; i += NT) {
+            const int t = i / (2 * NS), v = i % (2 * NS);
+            float s = 0.f;
+#pragma unroll 8
+            for (int k = 0; k < Y::KK; ++k) s += sm.bc[t][k][v];
+            if (t < nt) pbc[i] = s;
+        }
+        // d and g of this tile are read above, and written again only by the same thread's next tile
+    }
+    store_tile(b.pa, piece, dA);
+#pragma unroll
+    for (int k = 0; k < Y::CPT; ++k) {
+        const int cc = (k * NT + tid) % CH, row = Y::RPC > 1 ? tid / CH : 0;
+        if (!cin[k]) continue;
+        float* o = b.pd + ((int64_t)piece * Y::RPC + row) * 2 * p.C + c_lo + cc;
+        o[0] = accD[k];
+        o[p.C] = accB[k];
+    }
+}
+
+// dB and dC: the sums over a group's blocks.
+template <typename T>
+__global__ void __launch_bounds__(256) k_bc_sum(const float* __restrict__ part, int64_t T_total, int G, int bpg, int NS,
+                                                T* __restrict__ dB, T* __restrict__ dC) {
+    const int64_t W = T_total * 2 * NS, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= W) return;
+    const int g = blockIdx.y;
+    float s = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < bpg; ++k) s += part[((int64_t)g * bpg + k) * W + i];
+    const int64_t t = i / (2 * NS), v = i % (2 * NS);
+    T* o = v < NS ? dB : dC;
+    o[(t * G + g) * NS + v % NS] = from_f<T>(s);
+}
+
+struct PutRow {
+    float* p;
+    __device__ void operator()(int64_t c, float s) const { p[c] = s; }
+};
+struct PutDB {  // column c of [dD | ddt_bias]
+    float *dd, *db;
+    int C;
+    __device__ void operator()(int64_t c, float s) const {
+        if (c < C) {
+            if (dd) dd[c] = s;
+        } else if (db) {
+            db[c - C] = s;
+        }
+    }
+};
+
+template <int NS> constexpr int rows_per_channel() { return BLay<NS>::RPC; }
+int rpc_of(int ns) { return ns <= 16 ? 1 : ns / 16; }
+int ch_of(int ns) { return 2048 / ns; }
+
+template <typename T, int NS>
+cudaError_t backward_as(BParams& b, const kda_ssm_backward_args& a, cudaStream_t s) {
+    using Y = BLay<NS>;
+    Params& p = b.f;
+    cudaError_t e;
+    if ((e = launch_states(p, a.fwd, s))) return e;  // sets p.bpg for the scan's layout, which k_rev shares
+    if (p.pieces > 1) {
+        k_rev<T, NS><<<dim3((unsigned)(p.bpg * p.G), p.pieces - 1), Lay<NS>::NT, 0, s>>>(b);
+        if ((e = cudaGetLastError())) return e;
+        if (p.pieces > 2) {
+            k_rev_join<NS><<<(unsigned)(((int64_t)p.C * NS + 255) / 256), 256, 0, s>>>(b);
+            if ((e = cudaGetLastError())) return e;
+        }
+    }
+    const int smem = (int)sizeof(BShared<T, NS>);
+    if ((e = cudaFuncSetAttribute(k_ssm_bwd<T, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
+    k_ssm_bwd<T, NS><<<dim3((unsigned)(b.bpg * p.G), p.pieces), Y::NT, smem, s>>>(b);
+    if ((e = cudaGetLastError())) return e;
+    const int64_t W = p.T * 2 * NS;
+    k_bc_sum<T><<<dim3((unsigned)((W + 255) / 256), p.G), 256, 0, s>>>(b.pbc, p.T, p.G, b.bpg, NS, static_cast<T*>(a.dB),
+                                                                       static_cast<T*>(a.dC));
+    if ((e = cudaGetLastError())) return e;
+    if ((e = launch_column_sum(b.pa, p.pieces, (int64_t)p.C * NS, PutRow{a.dA}, s))) return e;
+    if (!a.dD && !a.ddt_bias) return cudaSuccess;
+    return launch_column_sum(b.pd, (int64_t)p.pieces * Y::RPC, 2 * (int64_t)p.C, PutDB{a.dD, a.ddt_bias, p.C}, s);
+}
+
+}  // namespace
+
+SsmBackwardPlan ssm_backward_plan(const kda_ssm_args& f) {
+    DeviceInfo di{0, 0, 0};
+    const int64_t sms = current_device_info(&di) ? di.sm_count : 1;
+    const int64_t cg = f.C / f.G, ch = ch_of(f.Nst), blocks = f.G * ((cg + ch - 1) / ch);
+    SsmBackwardPlan p{};
+    // Six blocks per SM, pieces of at least 64 tokens.
+    int64_t k = (6 * sms + blocks - 1) / blocks;
+    if (k > f.T_total / 64) k = f.T_total / 64;
+    if (k < 1) k = 1;
+    p.piece = ((f.T_total + k - 1) / k + 7) / 8 * 8;
+    p.pieces = (int)((f.T_total + p.piece - 1) / p.piece);
+    const size_t st = (size_t)f.C * f.Nst * sizeof(float), row = (size_t)f.C * sizeof(float);
+    size_t at = 0;
+    auto take = [&at](size_t bytes) {
+        const size_t o = at;
+        at += (bytes + 255) / 256 * 256;
+        return o;
+    };
+    p.fwd = take(p.pieces * st);
+    p.rev = take(p.pieces * st);
+    p.fsum = take(p.pieces * row);
+    p.rsum = take(p.pieces * row);
+    p.ckpt = take((size_t)(f.T_total + 3) / 4 * st);
+    p.pa = take(p.pieces * st);
+    p.pd = take((size_t)p.pieces * rpc_of(f.Nst) * 2 * row);
+    p.pbc = take((size_t)blocks * f.T_total * 2 * f.Nst * sizeof(float));
+    p.workspace = at;
+    return p;
+}
+
+cudaError_t launch_ssm_backward(const kda_ssm_backward_args& a, const SsmBackwardPlan& pl, cudaStream_t s) {
+    BParams b{};
+    b.f = params_of(a.fwd);
+    char* ws = static_cast<char*>(a.workspace);
+    auto at = [ws](size_t o) { return reinterpret_cast<float*>(ws + o); };
+    b.f.piece = pl.piece;
+    b.f.pieces = pl.pieces;
+    b.f.ws_state = at(pl.fwd);
+    b.f.ws_sum = at(pl.fsum);
+    b.f.ckpt = at(pl.ckpt);
+    b.f.fin = nullptr;
+    b.rev = at(pl.rev);
+    b.rsum = at(pl.rsum);
+    b.pa = at(pl.pa);
+    b.pd = at(pl.pd);
+    b.pbc = at(pl.pbc);
+    b.dy = a.dy;
+    b.dys = a.dy_stride ? a.dy_stride : a.fwd.C;
+    b.dfin = a.d_final_state;
+    b.dinit = a.dinitial_state;
+    b.du = a.du;
+    b.ddt = a.ddt;
+    b.dz = a.fwd.z ? a.dz : nullptr;
+    const int es = a.fwd.io == KDA_BF16 ? 2 : 4, ch = ch_of(a.fwd.Nst);
+    b.bpg = (b.f.Cg + ch - 1) / ch;
+    b.vec = b.f.vec && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 && b.dys * es % 16 == 0;
+#define KDA_BWD(T)                                               \
+    switch (a.fwd.Nst) {                                         \
+        case 8: return backward_as<T, 8>(b, a, s);               \
+        case 16: return backward_as<T, 16>(b, a, s);             \
+        case 32: return backward_as<T, 32>(b, a, s);             \
+        default: return backward_as<T, 64>(b, a, s);             \
+    }
+    if (a.fwd.io == KDA_BF16) { KDA_BWD(bf16) } else { KDA_BWD(float) }
+#undef KDA_BWD
+}
+
+}  // namespace kda

@@ -21,181 +21,181 @@ namespace {
 
 using namespace ssm;
 
-// kMain: the outputs.  Otherwise the state that a piece leaves when it starts from zero (or from the
-// initial state of a sequence that starts at its first token or inside it), and its sum of delta.
-template <typename T, int NS, bool kMain>
-__global__ void __launch_bounds__(Lay<NS>::kThreads) k_scan(Params p) {
+// kOut: the outputs, from the carried state.  kPiece: the state that a piece leaves when it starts
+// from zero (or from the initial state of a sequence that starts at its first token or inside it),
+// and its sum of delta.  kStates: from the carried state, the state in front of every fourth token.
+enum { kPiece, kOut, kStates };
+template <typename T, int NS, int kMode>
+__global__ void __launch_bounds__(Lay<NS>::NT, 8) k_scan(Params p) {
     using Y = Lay<NS>;
-    constexpr int L = Y::L, TT = Y::TT, NT = Y::kThreads, EPT = Y::EPT, BPT = Y::BPT;
-    __shared__ float2 sd[TT][kCB];                            // delta, delta u
-    __shared__ __align__(16) float sB[TT][NS], sC[kMain ? TT : 1][NS];
-    __shared__ __align__(16) float sy[kMain ? TT : 1][kCB][L];  // parts of sum_n C h
+    constexpr bool kMain = kMode == kOut;
+    constexpr int L = Y::L, TT = Y::TT, NT = Y::NT, BPT = Y::BPT, H = Y::SPT / 2, Q = Y::SPT / 4, CB = Y::CB;
+    constexpr int kDepth = 4;  // tiles in flight
+    struct Tile {
+        T u[TT][CB], dt[TT][CB], z[kMain ? TT : 1][CB], B[TT][NS], C[kMain ? TT : 1][NS];
+    };
+    __shared__ __align__(16) Tile ring[kDepth];
+    __shared__ __align__(16) float sB[2][TT][NS], sC[kMain ? 2 : 1][TT][NS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int l = lane / Y::KPW;  // which SPT states of the channel
     const int g = blockIdx.x / p.bpg;
-    const int c_lo = g * p.Cg + (blockIdx.x % p.bpg) * kCB, c_hi = (g + 1) * p.Cg;
+    const int ch = g * p.Cg + (blockIdx.x % p.bpg) * Y::CB + warp * Y::KPW + lane % Y::KPW, c_hi = (g + 1) * p.Cg;
+    const bool in = ch < c_hi, gate = kMain && p.z;
+    const int c = in ? ch : c_hi - 1;  // threads past the group shadow its last channel and store nothing
     const int piece = blockIdx.y;
     const int64_t t0 = piece * p.piece, t1 = t0 + p.piece < p.T ? t0 + p.piece : p.T;
+    const int64_t so = (int64_t)c * NS + l * Y::SPT;  // this thread's states in a row of [C][NS]
 
-    // this thread's states: channels cp and cp + 32 of the block, states 4 l .. 4 l + 3
-    const int l = lane / Y::KPW, cp = warp * Y::KPW + lane % Y::KPW;
-    const int ch[2] = {c_lo + cp, c_lo + cp + 32};
-    f2 A2[2][2], h[2][2];
-    float dsum[2] = {0.f, 0.f};
+    f2 A2[H], h[H];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (ch[i] < c_hi) a = *reinterpret_cast<const float4*>(p.A + (int64_t)ch[i] * NS + 4 * l);
-        A2[i][0] = f2_of(a.x * kLog2e, a.y * kLog2e);
-        A2[i][1] = f2_of(a.z * kLog2e, a.w * kLog2e);
+    for (int i = 0; i < Q; ++i) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p.A + so) + i);
+        A2[2 * i] = f2_of(a.x * kLog2e, a.y * kLog2e);
+        A2[2 * i + 1] = f2_of(a.z * kLog2e, a.w * kLog2e);
     }
     auto load_state = [&](const float* base, int64_t n) {  // row n of [..][C][NS], or zeros
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < Q; ++i) {
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (base && ch[i] < c_hi) s = *reinterpret_cast<const float4*>(base + (n * p.C + ch[i]) * NS + 4 * l);
-            h[i][0] = f2_of(s.x, s.y);
-            h[i][1] = f2_of(s.z, s.w);
+            if (base) s = reinterpret_cast<const float4*>(base + n * p.C * NS + so)[i];
+            h[2 * i] = f2_of(s.x, s.y);
+            h[2 * i + 1] = f2_of(s.z, s.w);
         }
     };
     auto store_state = [&](float* base, int64_t n) {
+        if (!in) return;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (ch[i] < c_hi)
-                *reinterpret_cast<float4*>(base + (n * p.C + ch[i]) * NS + 4 * l) =
-                    make_float4(f2_lo(h[i][0]), f2_hi(h[i][0]), f2_lo(h[i][1]), f2_hi(h[i][1]));
+        for (int i = 0; i < Q; ++i)
+            reinterpret_cast<float4*>(base + n * p.C * NS + so)[i] =
+                make_float4(f2_lo(h[2 * i]), f2_hi(h[2 * i]), f2_lo(h[2 * i + 1]), f2_hi(h[2 * i + 1]));
     };
     int n = seq_of(p.cu, p.N, t0);
     int64_t seq_end = p.cu[n + 1];
     if (p.cu[n] == t0) load_state(p.init, n);
-    else if (kMain && piece > 0) load_state(p.ws_state, piece);
+    else if (kMode != kPiece && piece > 0) load_state(p.ws_state, piece);
     else load_state(nullptr, 0);
-    auto cross = [&](int64_t t) {  // sequence n ended before token t
-        if (kMain && p.fin) store_state(p.fin, n);
-        while (n < p.N - 1 && p.cu[n + 1] <= t) ++n;
-        seq_end = p.cu[n + 1];
-        load_state(p.init, n);
-    };
 
-    // this thread's elements of a tile: tokens tid / kCB + k (NT / kCB), one channel
-    const int ec = c_lo + tid % kCB, et = tid / kCB;
-    const bool ein = ec < c_hi;
-    const float bias = ein && p.dt_bias ? p.dt_bias[ec] : 0.f;
-    const float skip = kMain && ein && p.D ? p.D[ec] : 0.f;
-    const T* up = static_cast<const T*>(p.u) + ec;
-    const T* dp = static_cast<const T*>(p.dt) + ec;
-    const T* zp = kMain && p.z ? static_cast<const T*>(p.z) + ec : nullptr;
-    const T* bp = static_cast<const T*>(p.B) + (int64_t)g * NS;
-    const T* cpn = static_cast<const T*>(p.Cm) + (int64_t)g * NS;
-    Raw<T, 1> ru[EPT], rd[EPT], rz[EPT], rb[BPT], rc[BPT];
-    auto fetch = [&](int64_t tb) {
-#pragma unroll
-        for (int k = 0; k < EPT; ++k) {
-            const int64_t t = tb + et + k * (NT / kCB);
-            ru[k].zero(); rd[k].zero(); rz[k].zero();
-            if (t < t1 && ein) {
-                ru[k].load(up + t * p.us);
-                rd[k].load(dp + t * p.dts);
-                if (zp) rz[k].load(zp + t * p.zs);
-            }
+    const float bias = p.dt_bias ? p.dt_bias[c] : 0.f, skip = kMain && p.D ? p.D[c] : 0.f;
+    T* yp = static_cast<T*>(p.y) + c + t0 * p.ys;
+    const int c_lo = ch - (warp * Y::KPW + lane % Y::KPW), cols = c_hi - c_lo, cl = ch - c_lo;
+    const int tiles = (int)((t1 - t0 + TT - 1) / TT);
+    auto issue = [&](int k) {  // copies of tile k (a group of its own, empty past the end)
+        if (k < tiles) {
+            Tile& r = ring[k % kDepth];
+            const int64_t tb = t0 + (int64_t)k * TT;
+            const int rows = (int)(t1 - tb < TT ? t1 - tb : TT);
+            copy_tile<T, TT, CB, NT>(&r.u[0][0], static_cast<const T*>(p.u) + tb * p.us + c_lo, p.us, rows, cols, p.vec);
+            copy_tile<T, TT, CB, NT>(&r.dt[0][0], static_cast<const T*>(p.dt) + tb * p.dts + c_lo, p.dts, rows, cols, p.vec);
+            if (gate)
+                copy_tile<T, TT, CB, NT>(&r.z[0][0], static_cast<const T*>(p.z) + tb * p.zs + c_lo, p.zs, rows, cols, p.vec);
+            copy_tile<T, TT, NS, NT>(&r.B[0][0], static_cast<const T*>(p.B) + tb * p.bs + g * NS, p.bs, rows, NS, p.vec);
+            if (kMain)
+                copy_tile<T, TT, NS, NT>(&r.C[0][0], static_cast<const T*>(p.Cm) + tb * p.cs + g * NS, p.cs, rows, NS, p.vec);
         }
+        cp_commit();
+    };
+    auto widen = [&](int k) {  // B and C of tile k in fp32
+        const Tile& r = ring[k % kDepth];
 #pragma unroll
-        for (int k = 0; k < BPT; ++k) {
-            const int i = k * NT + tid;
-            const int64_t t = tb + i / NS;
-            rb[k].zero(); rc[k].zero();
-            if (t < t1) {
-                rb[k].load(bp + t * p.bs + i % NS);
-                if (kMain) rc[k].load(cpn + t * p.cs + i % NS);
-            }
+        for (int j = 0; j < BPT; ++j) {
+            const int i = j * NT + tid;
+            sB[k & 1][i / NS][i % NS] = to_f(r.B[i / NS][i % NS]);
+            if (kMain) sC[k & 1][i / NS][i % NS] = to_f(r.C[i / NS][i % NS]);
         }
     };
-    fetch(t0);
-    for (int64_t tb = t0; tb < t1; tb += TT) {
-        float u[EPT], z[EPT];
 #pragma unroll
-        for (int k = 0; k < EPT; ++k) {
-            float v[1];
-            unraw(ru[k], v);
-            u[k] = v[0];
-            unraw(rz[k], v);
-            z[k] = v[0];
-            unraw(rd[k], v);
-            const float x = v[0] + bias;
-            float d = p.softplus ? softplus(x) : x;
-            if (tb + et + k * (NT / kCB) >= t1 || !ein) d = 0.f;
-            sd[et + k * (NT / kCB)][tid % kCB] = make_float2(d, d * u[k]);
-        }
+    for (int k = 0; k < kDepth - 1; ++k) issue(k);
+    cp_wait<kDepth - 2>();  // tile 0
+    __syncthreads();
+    widen(0);
+    float dsum = 0.f;
+    for (int k = 0; k < tiles; ++k) {
+        const int64_t tb = t0 + (int64_t)k * TT;
+        const int buf = k & 1;
+        cp_wait<kDepth - 3>();  // tile k + 1
+        __syncthreads();        // its rows are visible, tile k's fp32 rows too, and tile k - 1 is done with
+        if (k + 1 < tiles) widen(k + 1);
+        issue(k + kDepth - 1);
+        const Tile& r = ring[k % kDepth];
+        const int nt = (int)(t1 - tb < TT ? t1 - tb : TT);
+        // One token: the states move on, the return value is this thread's part of sum_n C h.
+        auto token = [&](int t, float d, float u) {
+            const f2 dd = f2_dup(d), du = f2_dup(d * u);
+            f2 y[2] = {f2_dup(0.f), f2_dup(0.f)};
 #pragma unroll
-        for (int k = 0; k < BPT; ++k) {
-            const int i = k * NT + tid;
-            float v[1];
-            unraw(rb[k], v);
-            sB[i / NS][i % NS] = v[0];
-            if (kMain) {
-                unraw(rc[k], v);
-                sC[i / NS][i % NS] = v[0];
-            }
-        }
-        __syncthreads();
-        if (tb + TT < t1) fetch(tb + TT);
-
-        auto token = [&](int t) {
-            const float4 b = *reinterpret_cast<const float4*>(&sB[t][4 * l]);
-            const f2 b0 = f2_of(b.x, b.y), b1 = f2_of(b.z, b.w);
-            f2 c0, c1;
-            if (kMain) {
-                const float4 c = *reinterpret_cast<const float4*>(&sC[t][4 * l]);
-                c0 = f2_of(c.x, c.y);
-                c1 = f2_of(c.z, c.w);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float2 dv = sd[t][cp + 32 * i];
-                const f2 d = f2_dup(dv.x), du = f2_dup(dv.y);
-                h[i][0] = fma2(exp2_2(mul2(d, A2[i][0])), h[i][0], mul2(du, b0));
-                h[i][1] = fma2(exp2_2(mul2(d, A2[i][1])), h[i][1], mul2(du, b1));
+            for (int i = 0; i < Q; ++i) {
+                const float4 b = *reinterpret_cast<const float4*>(&sB[buf][t][l * Y::SPT + 4 * i]);
+                h[2 * i] = fma2(exp2_2(mul2(dd, A2[2 * i])), h[2 * i], mul2(du, f2_of(b.x, b.y)));
+                h[2 * i + 1] = fma2(exp2_2(mul2(dd, A2[2 * i + 1])), h[2 * i + 1], mul2(du, f2_of(b.z, b.w)));
                 if (kMain) {
-                    const f2 y = fma2(h[i][1], c1, mul2(h[i][0], c0));
-                    sy[t][cp + 32 * i][l] = f2_lo(y) + f2_hi(y);
-                } else {
-                    dsum[i] += dv.x;
+                    const float4 v = *reinterpret_cast<const float4*>(&sC[buf][t][l * Y::SPT + 4 * i]);
+                    y[0] = fma2(h[2 * i], f2_of(v.x, v.y), y[0]);
+                    y[1] = fma2(h[2 * i + 1], f2_of(v.z, v.w), y[1]);
                 }
             }
+            if (!kMain) return 0.f;
+            y[0] = add2(y[0], y[1]);
+            return f2_lo(y[0]) + f2_hi(y[0]);
         };
-        if (tb == seq_end) cross(tb);
-        if (tb + TT <= t1 && seq_end >= tb + TT) {
-#pragma unroll 4
-            for (int t = 0; t < TT; ++t) token(t);
+        auto finish = [&](int t, float s, float u) {  // the parts of a channel, the skip, the gate
+#pragma unroll
+            for (int o = Y::KPW; o < 32; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+            s = fmaf(skip, u, s);
+            if (gate) s *= silu(to_f(r.z[t][cl]));
+            return s;
+        };
+        if (nt == TT && seq_end >= tb + TT) {  // no border: eight tokens without a branch between them
+            float d[TT], u[TT], s[TT];
+#pragma unroll
+            for (int t = 0; t < TT; t += 2) {
+                const f2 x = add2(f2_of(to_f(r.dt[t][cl]), to_f(r.dt[t + 1][cl])), f2_dup(bias));
+                const f2 v = p.softplus ? softplus2(x) : x;
+                d[t] = f2_lo(v);
+                d[t + 1] = f2_hi(v);
+                u[t] = to_f(r.u[t][cl]);
+                u[t + 1] = to_f(r.u[t + 1][cl]);
+            }
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                if (kMode == kStates && t % 4 == 0) store_state(p.ckpt, (tb + t) / 4);
+                s[t] = token(t, d[t], u[t]);
+                if (!kMain) dsum += d[t];
+            }
+            if (kMain) {
+#pragma unroll
+                for (int t = 0; t < TT; ++t) s[t] = finish(t, s[t], u[t]);
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    if (in && (L == 1 || l == 0)) *yp = from_f<T>(s[t]);
+                    yp += p.ys;
+                }
+            }
         } else {
-            const int nt = (int)(t1 - tb < TT ? t1 - tb : TT);
 #pragma unroll 1
             for (int t = 0; t < nt; ++t) {
-                if (tb + t == seq_end) cross(tb + t);
-                token(t);
-            }
-        }
-        __syncthreads();
-        if (kMain && ein) {
-            T* yp = static_cast<T*>(p.y) + ec;
-#pragma unroll
-            for (int k = 0; k < EPT; ++k) {
-                const int t = et + k * (NT / kCB);
-                if (tb + t >= t1) continue;
-                float s = skip * u[k];
-#pragma unroll
-                for (int j = 0; j < L; ++j) s += sy[t][tid % kCB][j];
-                yp[(tb + t) * p.ys] = from_f<T>(p.z ? s * silu(z[k]) : s);
+                if (kMode == kStates && t % 4 == 0) store_state(p.ckpt, (tb + t) / 4);
+                if (tb + t == seq_end) {  // sequence n ended before this token
+                    if (kMain && p.fin) store_state(p.fin, n);
+                    while (n < p.N - 1 && p.cu[n + 1] <= tb + t) ++n;
+                    seq_end = p.cu[n + 1];
+                    load_state(p.init, n);
+                }
+                const float x = to_f(r.dt[t][cl]) + bias, d = p.softplus ? softplus(x) : x, u = to_f(r.u[t][cl]);
+                const float s = token(t, d, u);
+                dsum += d;
+                if (kMain) {
+                    const float o = finish(t, s, u);
+                    if (in && (L == 1 || l == 0)) *yp = from_f<T>(o);
+                    yp += p.ys;
+                }
             }
         }
     }
     if (kMain) {
         if (p.fin && seq_end == t1) store_state(p.fin, n);
-    } else {
+    } else if (kMode == kPiece) {
         store_state(p.ws_state, piece + 1);
-        if (l == 0)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (ch[i] < c_hi) p.ws_sum[(int64_t)piece * p.C + ch[i]] = dsum[i];
+        if (in && l == 0) p.ws_sum[(int64_t)piece * p.C + c] = dsum;
     }
 }
 
@@ -273,35 +273,33 @@ template <typename T, int NS> __global__ void __launch_bounds__(kStepThreads) k_
     }
 }
 
-int64_t or_(int64_t s, int64_t d) { return s ? s : d; }
-
-Params params_of(const kda_ssm_args& a) {
-    Params p{};
-    const int64_t gn = (int64_t)a.G * a.Nst;
-    p.u = a.u; p.dt = a.dt; p.z = a.z; p.B = a.B; p.Cm = a.Cm; p.y = a.y;
-    p.us = or_(a.u_stride, a.C); p.dts = or_(a.dt_stride, a.C); p.zs = or_(a.z_stride, a.C);
-    p.bs = or_(a.B_stride, gn); p.cs = or_(a.C_stride, gn); p.ys = or_(a.y_stride, a.C);
-    p.A = a.A; p.D = a.D; p.dt_bias = a.dt_bias; p.init = a.initial_state; p.fin = a.final_state;
-    p.cu = a.cu_seqlens;
-    p.T = a.T_total; p.N = a.N; p.C = a.C; p.G = a.G; p.Cg = a.C / a.G;
-    p.bpg = (p.Cg + kCB - 1) / kCB;
-    p.softplus = a.softplus;
-    return p;
-}
-
-template <typename T, int NS> cudaError_t scan_as(const Params& p, cudaStream_t s) {
-    const int nt = Lay<NS>::kThreads;
+// The states at the pieces' starts, then the pass over all pieces.
+template <typename T, int NS, int kMode> cudaError_t scan_as(Params& p, cudaStream_t s) {
+    using Y = Lay<NS>;
+    p.bpg = (p.Cg + Y::CB - 1) / Y::CB;
     const unsigned gx = (unsigned)(p.bpg * p.G);
     if (p.pieces > 1) {
-        k_scan<T, NS, false><<<dim3(gx, p.pieces - 1), nt, 0, s>>>(p);
+        k_scan<T, NS, kPiece><<<dim3(gx, p.pieces - 1), Y::NT, 0, s>>>(p);
         if (cudaError_t e = cudaGetLastError()) return e;
         if (p.pieces > 2) {
             k_scan_join<NS><<<(unsigned)(((int64_t)p.C * NS + 255) / 256), 256, 0, s>>>(p);
             if (cudaError_t e = cudaGetLastError()) return e;
         }
     }
-    k_scan<T, NS, true><<<dim3(gx, p.pieces), nt, 0, s>>>(p);
+    k_scan<T, NS, kMode><<<dim3(gx, p.pieces), Y::NT, 0, s>>>(p);
     return cudaGetLastError();
+}
+
+template <int kMode> cudaError_t scan_mode(Params& p, const kda_ssm_args& a, cudaStream_t s) {
+#define KDA_SCAN(T)                                              \
+    switch (a.Nst) {                                             \
+        case 8: return scan_as<T, 8, kMode>(p, s);               \
+        case 16: return scan_as<T, 16, kMode>(p, s);             \
+        case 32: return scan_as<T, 32, kMode>(p, s);             \
+        default: return scan_as<T, 64, kMode>(p, s);             \
+    }
+    if (a.io == KDA_BF16) { KDA_SCAN(bf16) } else { KDA_SCAN(float) }
+#undef KDA_SCAN
 }
 
 template <typename T, int NS> cudaError_t step_as(const Params& p, cudaStream_t s) {
@@ -314,14 +312,34 @@ template <typename T, int NS> cudaError_t step_as(const Params& p, cudaStream_t 
 
 }  // namespace
 
+ssm::Params ssm::params_of(const kda_ssm_args& a) {
+    auto or_ = [](int64_t s, int64_t d) { return s ? s : d; };
+    Params p{};
+    const int64_t gn = (int64_t)a.G * a.Nst;
+    p.u = a.u; p.dt = a.dt; p.z = a.z; p.B = a.B; p.Cm = a.Cm; p.y = a.y;
+    p.us = or_(a.u_stride, a.C); p.dts = or_(a.dt_stride, a.C); p.zs = or_(a.z_stride, a.C);
+    p.bs = or_(a.B_stride, gn); p.cs = or_(a.C_stride, gn); p.ys = or_(a.y_stride, a.C);
+    p.A = a.A; p.D = a.D; p.dt_bias = a.dt_bias; p.init = a.initial_state; p.fin = a.final_state;
+    p.cu = a.cu_seqlens;
+    p.T = a.T_total; p.N = a.N; p.C = a.C; p.G = a.G; p.Cg = a.C / a.G;
+    p.softplus = a.softplus;
+    const int es = a.io == KDA_BF16 ? 2 : 4;
+    auto wide = [es](const void* q, int64_t stride) {
+        return reinterpret_cast<uintptr_t>(q) % 16 == 0 && stride * es % 16 == 0;
+    };
+    p.vec = wide(p.u, p.us) && wide(p.dt, p.dts) && (!p.z || wide(p.z, p.zs)) && wide(p.B, p.bs) && wide(p.Cm, p.cs) &&
+            (a.G == 1 || (int64_t)p.Cg * es % 16 == 0);
+    return p;
+}
+
 ScanPlan scan_plan(const kda_ssm_args& a) {
     DeviceInfo di{0, 0, 0};
     const int64_t sms = current_device_info(&di) ? di.sm_count : 1;
-    const int64_t cg = a.C / a.G, blocks = a.G * ((cg + kCB - 1) / kCB);
-    const int64_t warps = blocks * (a.Nst / 4), tt = a.Nst == 64 ? 8 : 16;
+    const int64_t tt = 8, cb = a.Nst <= 16 ? 64 : 1024 / a.Nst;  // Lay<Nst>'s tile and channels per block
     ScanPlan p{};
-    // Enough warps for 16 per SM, pieces of at least 8 tiles.
-    int64_t k = (16 * sms + warps - 1) / warps;
+    const int64_t warps = a.G * ((a.C / a.G + cb - 1) / cb) * 2;
+    // Enough warps for 30 per SM, pieces of at least 8 tiles.
+    int64_t k = (30 * sms + warps - 1) / warps;
     const int64_t most = a.T_total / (8 * tt);
     if (k > most) k = most;
     if (k < 1) k = 1;
@@ -341,16 +359,10 @@ cudaError_t launch_ssm_scan(const kda_ssm_args& a, const ScanPlan& pl, cudaStrea
     p.pieces = pl.pieces;
     p.ws_state = static_cast<float*>(a.workspace);
     p.ws_sum = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + pl.sums);
-#define KDA_SCAN(T)                                              \
-    switch (a.Nst) {                                             \
-        case 8: return scan_as<T, 8>(p, s);                      \
-        case 16: return scan_as<T, 16>(p, s);                    \
-        case 32: return scan_as<T, 32>(p, s);                    \
-        default: return scan_as<T, 64>(p, s);                    \
-    }
-    if (a.io == KDA_BF16) { KDA_SCAN(bf16) } else { KDA_SCAN(float) }
-#undef KDA_SCAN
+    return scan_mode<kOut>(p, a, s);
 }
+
+cudaError_t ssm::launch_states(Params& p, const kda_ssm_args& a, cudaStream_t s) { return scan_mode<kStates>(p, a, s); }
 
 cudaError_t launch_ssm_step(const kda_ssm_args& a, cudaStream_t s) {
     const Params p = params_of(a);

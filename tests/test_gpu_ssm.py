@@ -242,3 +242,160 @@ def test_steps_continue_a_prompt(n, Ch, N, G, io, gate):
         rows = [c2[i] + lens[i] + j for i in range(n)]
         within(outs[j], ry[rows], ey[rows] + U[io] * (ry[rows].abs() + ey[rows]), f"step {j}")
     within(state, rf, ef, "state")
+
+
+# ------------------------------------------------------------------ gradients of the scan
+GRADS = {"u": "du", "dt": "ddt", "A": "dA", "B": "dB", "C": "dC", "D": "dD", "z": "dz", "dt_bias": "ddt_bias",
+         "init": "dinitial_state"}
+
+
+def ref_grads(a, lens, dy, dfin, softplus=True):
+    """The formula's gradients, by autograd over the 64-bit recurrence."""
+    leaves = {k: f64(t).requires_grad_() for k, t in a.items() if t is not None}
+    v = {k: leaves.get(k) for k in a}
+    y, fin = ssm_ref(v["u"], v["dt"], v["A"], v["B"], v["C"], lens, v["D"], v["z"], v["dt_bias"], softplus, v["init"])
+    loss = (y * f64(dy)).sum() + (0 if dfin is None else (fin * f64(dfin)).sum())
+    got = torch.autograd.grad(loss, list(leaves.values()), allow_unused=True)
+    return {GRADS[k]: (torch.zeros_like(leaves[k]) if g is None else g) for k, g in zip(leaves, got)}
+
+
+def run_backward(a, lens, dy, dfin, how="dense", **kw):
+    v = {k: (rows_in(t, how) if k in ("u", "dt", "z") and t is not None else to(t)) for k, t in a.items()}
+    return kda.kda_ssm_backward(v["u"], v["dt"], v["A"], v["B"], v["C"], cu_of(lens), rows_in(dy, how), D=v["D"],
+                                z=v["z"], dt_bias=v["dt_bias"], initial_state=v["init"], d_final_state=to(dfin), **kw)
+
+
+def grad_bounds(a, lens, dy, dfin, softplus=True):
+    """Bounds of every gradient: the gradients of the same scan on magnitudes (all terms positive, nothing cancels) times
+    a relative error.  Every factor of a term carries at most 60 units of the last place (two step sizes, an exponential,
+    the gate and its slope, up to eight products), a state's and its gradient's memory adds 4 units per token of it, and a
+    sum over K terms K units.  The exponent delta A comes with 13 units (10 of delta, 3 of A log2 e and the product), and an
+    error d of an exponent E is a relative error d E of e^E: a term that has passed k decays of exponent x each has 13 k x
+    units, and weighted by the terms' own size e^(-k x) the mean of k x is at most 1 beyond the decay that the term itself
+    carries, for the state and for its gradient: 13 (2 max|delta A| + 2) units."""
+    mag = {k: (None if t is None else f64(t).abs()) for k, t in a.items()}
+    x = f64(a["dt"]) + (0 if a["dt_bias"] is None else f64(a["dt_bias"]))
+    delta = (torch.logaddexp(x, torch.zeros_like(x)) if softplus else x).abs()
+    T, Ch = delta.shape
+    G, N = a["B"].shape[1:]
+    u, B, C = (mag[k] for k in ("u", "B", "C"))
+    A = f64(a["A"])
+    wide = lambda r: r.unsqueeze(1).expand(G, Ch // G, N).reshape(Ch, N)  # noqa: E731
+    sz = dsz = torch.ones(T, Ch, dtype=torch.float64)
+    if a["z"] is not None:
+        z = f64(a["z"])
+        sg = torch.sigmoid(z)
+        sz, dsz = (z * sg).abs(), (sg * (1 + z.abs()))
+    g = f64(dy).abs() * sz
+    skip = torch.zeros(Ch, dtype=torch.float64) if a["D"] is None else f64(a["D"]).abs()
+    k = {n: torch.zeros_like(t) for n, t in (("du", u), ("ddt", u), ("dz", u), ("dB", B), ("dC", C), ("dA", A))}
+    k["dD"], k["ddt_bias"] = torch.zeros(Ch, dtype=torch.float64), torch.zeros(Ch, dtype=torch.float64)
+    k["dinitial_state"] = torch.zeros(len(lens), Ch, N, dtype=torch.float64)
+    # relative error of states and their gradients: per token of memory, at most the memory's length
+    mem = 0.0
+    t0 = 0
+    for i, L in enumerate(lens):
+        h = torch.zeros(Ch, N, dtype=torch.float64) if a["init"] is None else mag["init"][i]
+        hist = []
+        for t in range(t0, t0 + L):
+            hist.append(h)
+            h = torch.exp(delta[t].unsqueeze(1) * A) * h + (delta[t] * u[t]).unsqueeze(1) * wide(B[t])
+        hist.append(h)
+        q = torch.zeros(Ch, N, dtype=torch.float64) if dfin is None else f64(dfin)[i].abs()
+        for t in range(t0 + L - 1, t0 - 1, -1):
+            h, before = hist[t - t0 + 1], hist[t - t0]
+            d = delta[t].unsqueeze(1)
+            dec = torch.exp(d * A)
+            lam = q + g[t].unsqueeze(1) * wide(C[t])
+            k["dC"][t] += (g[t].unsqueeze(1) * h).view(G, Ch // G, N).sum(1)
+            k["dB"][t] += (lam * d * u[t].unsqueeze(1)).view(G, Ch // G, N).sum(1)
+            s1 = (lam * wide(B[t])).sum(1)
+            w = lam * dec * before
+            k["dA"] += w * d
+            k["du"][t] = delta[t] * s1 + skip * g[t]
+            slope = torch.sigmoid(x[t]) if softplus else 1.0
+            k["ddt"][t] = (u[t] * s1 + (w * A.abs()).sum(1)) * slope
+            k["dz"][t] = f64(dy)[t].abs() * ((wide(C[t]) * h).sum(1) + skip * u[t]) * dsz[t]
+            q = dec * lam
+        if L == 0 and dfin is not None:
+            q = f64(dfin)[i].abs()
+        k["dinitial_state"][i] = q
+        t0 += L
+    k["dD"], k["ddt_bias"] = (g * u).sum(0), k["ddt"].sum(0)
+    steps = min(max(lens), 4000)
+    rel = (60 + 2 * x.abs().max().item() * 4) * U32 + 4 * steps * U32 * 0.25 * 2
+    rel += 13 * U32 * (2 * (delta.unsqueeze(2) * A).abs().max().item() + 2)
+    return {n: v * (rel + (Ch if n in ("dB", "dC") else T if n in ("dA", "dD", "ddt_bias") else N) * U32) + 1e-30
+            for n, v in k.items()}
+
+
+BWD_LENS = [[1], [2, 3], [4, 8, 12], [0, 16, 0, 33, 1, 0, 1, 1, 6], [131], [90, 3, 260]]
+
+
+@pytest.mark.parametrize("lens", BWD_LENS)
+@pytest.mark.parametrize("Ch,N,G,how,io", [
+    (64, 16, 1, "dense", BF), (128, 16, 1, "dense", FP), (40, 8, 2, "odd", BF), (1, 16, 1, "dense", FP),
+    (96, 32, 3, "strided", BF), (130, 64, 2, "dense", FP), (300, 8, 1, "odd", FP), (65, 64, 1, "dense", BF)])
+def test_scan_gradients(lens, Ch, N, G, how, io):
+    T, n = sum(lens), len(lens)
+    a = ssm_inputs(T + Ch + N, T, Ch, N, G, io, n, gate=Ch != 40, skip=Ch != 96, state=Ch != 300, bias=Ch != 65)
+    g = gen(T)
+    dy, dfin = randn(g, T, Ch, dtype=io), (randn(g, n, Ch, N) if Ch != 130 else None)
+    got = run_backward(a, lens, dy, dfin, how)
+    ref, tol = ref_grads(a, lens, dy, dfin), grad_bounds(a, lens, dy, dfin)
+    assert set(got) == set(ref)
+    for name, r in ref.items():
+        u = U[io] if name in ("du", "ddt", "dz", "dB", "dC") else 0.0
+        within(got[name], r, tol[name] + u * (r.abs() + tol[name]), name)
+
+
+@pytest.mark.parametrize("lens", [[1500], [700, 0, 1, 900, 64]])
+@pytest.mark.parametrize("N,G", [(16, 1), (32, 2)])
+def test_scan_gradients_over_pieces(lens, N, G):
+    T, n, Ch = sum(lens), len(lens), 48
+    a = ssm_inputs(T + N, T, Ch, N, G, FP, n, slow=True)
+    g = gen(T)
+    dy, dfin = randn(g, T, Ch), randn(g, n, Ch, N)
+    got = run_backward(a, lens, dy, dfin)
+    ref, tol = ref_grads(a, lens, dy, dfin), grad_bounds(a, lens, dy, dfin)
+    for name, r in ref.items():
+        within(got[name], r, tol[name] + U32 * r.abs(), name)
+    again = run_backward(a, lens, dy, dfin, check_cu_on_host=False)
+    assert all(torch.equal(got[k], again[k]) for k in got)  # fixed order of the sums
+
+
+def test_scan_gradients_against_differences():
+    """Central differences of the GPU scan itself, along random directions (fp32: a step of 2^-6 leaves a truncation error
+    of h^2 times the third derivative, and a rounding error of 2^-24 |loss terms| / h)."""
+    lens = [37, 20]
+    a = ssm_inputs(77, 57, 32, 16, 1, FP, 2)
+    g = gen(78)
+    dy, dfin = randn(g, 57, 32), randn(g, 2, 32, 16)
+    got = run_backward(a, lens, dy, dfin)
+    step = 2.0 ** -6
+    for k, name in GRADS.items():
+        v = randn(g, *a[k].shape)
+        v /= v.norm()
+        if k in ("A", "dt"):
+            v *= 0.5
+
+        def loss(sign):
+            b = dict(a)
+            b[k] = a[k] + sign * step * v
+            y, fin = ssm_ref(b["u"], b["dt"], b["A"], b["B"], b["C"], lens, b["D"], b["z"], b["dt_bias"], True, b["init"])
+            yg, fg = run_scan(b, lens)
+            return (yg.cpu().double() * f64(dy)).sum() + (fg.cpu().double() * f64(dfin)).sum(), (y * f64(dy)).abs().sum()
+
+        (hi, mag), (lo, _) = loss(1), loss(-1)
+        want = ((hi - lo) / (2 * step)).item()
+        have = (got[name].cpu().double() * v).sum().item()
+        scale = got[name].cpu().double().norm().item()
+        assert abs(want - have) <= 0.02 * scale + 64 * U32 * float(mag) / step, (name, want, have, scale)
+
+
+def test_scan_gradients_nothing_to_do():
+    a = ssm_inputs(23, 0, 16, 8, 1, FP, 2)
+    dfin = randn(gen(1), 2, 16, 8)
+    got = run_backward(a, [0, 0], torch.empty(0, 16), dfin)
+    assert torch.equal(got["dinitial_state"].cpu(), dfin)
+    assert not got["dA"].any() and not got["dD"].any() and not got["ddt_bias"].any()
