@@ -164,6 +164,8 @@ def load(auto_build: bool = True) -> ctypes.CDLL:
     Raises if the library cannot be produced: there is no fallback path.
     """
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -208,18 +210,14 @@ def load(auto_build: bool = True) -> ctypes.CDLL:
                                                     ctypes.POINTER(ctypes.c_size_t)]
         lib.kda_backward.restype = _int
         lib.kda_backward.argtypes = [ctypes.POINTER(BackwardArgs), _vp]
-        for name, args in (("kda_layer_norm", NormArgs), ("kda_layer_norm_backward", NormBackwardArgs),
-                           ("kda_ssm_conv", SsmConvArgs), ("kda_ssm_conv_step", SsmConvArgs),
-                           ("kda_ssm_conv_backward", SsmConvBackwardArgs), ("kda_ssm_scan", SsmArgs),
-                           ("kda_ssm_step", SsmArgs), ("kda_ssm_backward", SsmBackwardArgs)):
+        # the operators around the layer take their structs as bytes or by reference
+        for name in ("kda_layer_norm", "kda_layer_norm_backward", "kda_ssm_conv", "kda_ssm_conv_step",
+                     "kda_ssm_conv_backward", "kda_ssm_scan", "kda_ssm_step", "kda_ssm_backward"):
             f = getattr(lib, name)
-            f.restype = _int
-            f.argtypes = [ctypes.POINTER(args), _vp]
-        for name, args in (("kda_layer_norm_backward", NormBackwardArgs), ("kda_ssm_conv_backward", SsmConvBackwardArgs),
-                           ("kda_ssm_scan", SsmArgs), ("kda_ssm_backward", SsmBackwardArgs)):
+            f.restype, f.argtypes = _int, [_vp, _vp]
+        for name in ("kda_layer_norm_backward", "kda_ssm_conv_backward", "kda_ssm_scan", "kda_ssm_backward"):
             f = getattr(lib, name + "_workspace_size")
-            f.restype = _int
-            f.argtypes = [ctypes.POINTER(args), ctypes.POINTER(ctypes.c_size_t)]
+            f.restype, f.argtypes = _int, [_vp, _vp]
         lib.kda_pack8.restype = _int
         lib.kda_pack8.argtypes = [_vp, _i64, _int, _i64, _int, _vp, _vp, _vp]
         lib.kda_unpack8.restype = _int

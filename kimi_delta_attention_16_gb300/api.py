@@ -14,7 +14,7 @@ from typing import Optional, Tuple
 import numpy as np
 import torch
 
-from . import _lib
+from . import _autograd, _lib
 
 _DT = {torch.bfloat16: _lib.KDA_BF16, torch.float32: _lib.KDA_FP32}
 _TORCH = {_lib.KDA_BF16: torch.bfloat16, _lib.KDA_FP32: torch.float32}
@@ -441,18 +441,23 @@ class _KDALayer(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, conv_w, g, beta, gate, rms_w, initial_state, conv_state_in, cu_pair,
-                eps_l2, eps_rms, scale):
+                eps_l2, eps_rms, scale, saved):
         out, fin = kda_prefill(q, k, v, conv_w, g, beta, cu_pair, gate=gate, rms_w=rms_w, eps_l2=eps_l2,
                                eps_rms=eps_rms, scale=scale, initial_state=initial_state,
                                conv_state_in=conv_state_in)
-        ctx.save_for_backward(q, k, v, conv_w, g, beta, gate, rms_w, initial_state, conv_state_in)
+        keep = saved == "e4m3" and any(ctx.needs_input_grad)
+        kept = [x for t in (q, k, v, gate) for x in (_pack_heads(t) if keep and t is not None else (t, None))]
+        ctx.save_for_backward(*kept, conv_w, g, beta, rms_w, initial_state, conv_state_in)
+        ctx.dtype = q.dtype
         ctx.cu_pair = cu_pair
         ctx.hp = (eps_l2, eps_rms, scale)
         return out, fin
 
     @staticmethod
     def backward(ctx, dout, dfin):
-        q, k, v, conv_w, g, beta, gate, rms_w, initial_state, conv_state_in = ctx.saved_tensors
+        *kept, conv_w, g, beta, rms_w, initial_state, conv_state_in = ctx.saved_tensors
+        q, k, v, gate = (t if sc is None else _unpack_heads(t, sc, ctx.dtype, g.shape)
+                         for t, sc in zip(kept[::2], kept[1::2]))
         eps_l2, eps_rms, scale = ctx.hp
         if dout is None:
             dout = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
@@ -469,18 +474,34 @@ class _KDALayer(torch.autograd.Function):
         names = ["dq", "dk", "dv", "dconv_w", "dg", "dbeta", "dgate", "drms_w", "dinitial_state",
                  "dconv_state_in"]
         ins = [q, k, v, conv_w, g, beta, gate, rms_w, initial_state, conv_state_in]
-        return (*(cast(n, t) for n, t in zip(names, ins)), None, None, None, None)
+        return (*(cast(n, t) for n, t in zip(names, ins)), None, None, None, None, None)
+
+
+def _pack_heads(t: torch.Tensor):
+    """[T, H, D] rows as kda_pack8 stores them."""
+    from .block import kda_pack8
+    return kda_pack8(t.reshape(t.shape[0], -1))
+
+
+def _unpack_heads(codes: torch.Tensor, scales: torch.Tensor, dtype, shape) -> torch.Tensor:
+    from .block import kda_unpack8
+    return kda_unpack8(codes, scales, dtype=dtype).view(shape)
 
 
 def kda_layer(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, conv_w: torch.Tensor, g: torch.Tensor,
               beta: torch.Tensor, cu_seqlens, *, gate: Optional[torch.Tensor] = None,
               rms_w: Optional[torch.Tensor] = None, eps_l2: float = 1e-6, eps_rms: float = 1e-6,
               scale: float = 1.0, initial_state: Optional[torch.Tensor] = None,
-              conv_state_in: Optional[torch.Tensor] = None):
+              conv_state_in: Optional[torch.Tensor] = None, saved: str = "io"):
     """The KDA layer as a differentiable PyTorch operation: returns (out, final_state) from
     kda_prefill, and on backward runs kda_backward (D = 128) for every input that requires a
     gradient (q, k, v, conv_w, g, beta, gate, rms_w, initial_state, conv_state_in).  The
-    gradients are those of the exact layer in fp32, cast to each input's dtype."""
+    gradients are those of the exact layer in fp32, cast to each input's dtype.
+
+    saved="e4m3" keeps q, k, v and gate in 8 bits for the backward pass (kda_pack8: a little over half of bf16's
+    memory): the gradients are then those at the rounded values.  g, beta and the states stay as they are.  In a
+    captured graph, see kda_ssm_layer's note."""
+    _autograd.check_saved(saved)
     cu_pair = _cu_pair(cu_seqlens, q.device)
-    return _KDALayer.apply(q, k, v, conv_w, g, beta, gate, rms_w, initial_state, conv_state_in, cu_pair,
-                           float(eps_l2), float(eps_rms), float(scale))
+    return _autograd.apply(_KDALayer, "kda_layer", q, k, v, conv_w, g, beta, gate, rms_w, initial_state, conv_state_in,
+                           cu_pair, float(eps_l2), float(eps_rms), float(scale), saved)

@@ -3,69 +3,35 @@ storage of activations, and the selective state space scan with its short causal
 
 Marshalling only, as in ``api``: the arithmetic runs in libkda.so.  Every tensor lives on the
 current CUDA device.  Rows may be strided views (the last axis contiguous); outputs and workspace
-are allocated on the stream that the call runs on.
+are allocated on the stream that the call runs on.  Arguments travel as packed C structs
+(``struct`` formats of the types in include/kda.h), since small calls are bound by this side.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import struct
 from typing import Optional
 
+import numpy as np
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _lib
-from .api import _DT, KDAError, _cu_pair, _same_cuda_device
+from . import _autograd, _lib
+from .api import _DT, KDAError, _cu_pair
 
-SAVED = ("io", "e4m3")  # how a layer keeps its large inputs for its backward pass
+_F32, _U8 = torch.float32, torch.uint8
+_BLOCK = _lib.KDA_PACK8_BLOCK
 
-
-@contextlib.contextmanager
-def _on(stream, *inputs):
-    """The stream of a call as an integer.  With a stream given that is not the current one, what the
-    call allocates belongs to that stream, and the inputs are marked as used on it, so that the
-    allocator gives neither away before the kernels are done."""
-    if stream is None:
-        yield torch.cuda.current_stream().cuda_stream
-        return
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-    if s == torch.cuda.current_stream():
-        yield s.cuda_stream
-        return
-    for t in inputs:
-        if t is not None and t.is_cuda:
-            t.record_stream(s)
-    with torch.cuda.stream(s):
-        yield s.cuda_stream
-
-
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _io(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in _DT:
-        raise ValueError(f"{name} is {t.dtype}; expected bfloat16 or float32")
-    return _DT[t.dtype]
-
-
-def _rows(t: torch.Tensor, shape, dtype, name: str) -> int:
-    """Row stride (elements) of a [M, C] tensor whose rows are dense."""
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"the rows of {name} must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _dense(t: Optional[torch.Tensor], shape, dtype, name: str) -> None:
-    if t is None:
-        return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                         f"got {t.dtype} {tuple(t.shape)}")
+# the argument structs of include/kda.h, member by member ("0P" pads a struct that others follow)
+_NORM = struct.Struct("@qii PqPPf PqP")
+_NORM_BWD = struct.Struct("@qii PqPqP PPPq PPPN")
+_CONV_FMT = "iiqii PP PqPP PPPqP 0P"
+_CONV = struct.Struct("@" + _CONV_FMT)
+_CONV_BWD = struct.Struct("@" + _CONV_FMT + "PqPq PPPPN")
+_SSM_FMT = "iiiiqii PP PqPqP PqPqP PqPPP PqPNP 0P"
+_SSM = struct.Struct("@" + _SSM_FMT)
+_SSM_BWD = struct.Struct("@" + _SSM_FMT + "PqP PPPPPPPPPPN")
 
 
 def _check(st: int, where: str) -> None:
@@ -73,17 +39,101 @@ def _check(st: int, where: str) -> None:
         raise KDAError(st, where)
 
 
-def _workspace(size_fn, args, where: str, workspace, device):
-    """Fills args.workspace: the caller's buffer, or a new one of the size the library asks for."""
+@contextlib.contextmanager
+def _on(stream, *inputs):
+    """Makes `stream` current.  What the call allocates then belongs to it, and the inputs are marked as
+    used on it, so that the allocator gives neither away before the kernels are done."""
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    if s != torch.cuda.current_stream():
+        for t in inputs:
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(s)
+    with torch.cuda.stream(s):
+        yield
+
+
+def _device(first: torch.Tensor, **others) -> int:
+    """Index of the current device, on which every given tensor has to be: the library dereferences these
+    pointers only on the GPU, and a host pointer there would fault."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"tensors are on {dev}; every tensor must be on a CUDA device")
+    for name, t in others.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, other tensors on {dev}")
+    index = torch.cuda.current_device()
+    if dev.index != index:
+        raise ValueError(f"tensors are on {dev} but the current device is cuda:{index}")
+    return index
+
+
+def _stream_of(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _ptr(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _io(t: torch.Tensor, name: str) -> int:
+    io = _DT.get(t.dtype)
+    if io is None:
+        raise ValueError(f"{name} is {t.dtype}; expected bfloat16 or float32")
+    return io
+
+
+def _shape2(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"expected {name} [rows, channels], got {tuple(t.shape)}")
+    return t.shape
+
+
+def _rows(t: torch.Tensor, M: int, C: int, dtype, name: str) -> int:
+    """Row stride (elements) of a [M, C] tensor whose rows are dense."""
+    if t.dim() != 2 or t.shape[0] != M or t.shape[1] != C:
+        raise ValueError(f"{name} must be {(M, C)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
+    s0, s1 = t.stride()
+    if C > 1 and s1 != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return s0 if M > 1 else C
+
+
+def _dense(t: Optional[torch.Tensor], shape, dtype, name: str) -> int:
+    """Pointer of a contiguous tensor of this shape and dtype (0 for None)."""
+    if t is None:
+        return 0
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _workspace(size_fn, packed: bytes, where: str, workspace, device):
+    """(pointer, bytes, tensor): the caller's buffer, or a new one of the size the library asks for."""
     if workspace is None:
         n = ctypes.c_size_t(0)
-        _check(size_fn(ctypes.byref(args), ctypes.byref(n)), where)
+        _check(size_fn(packed, ctypes.byref(n)), where)
         if n.value == 0:
-            return None
-        workspace = torch.empty(n.value, dtype=torch.uint8, device=device)
-    args.workspace = workspace.data_ptr()
-    args.workspace_bytes = workspace.numel() * workspace.element_size()
-    return workspace
+            return 0, 0, None
+        workspace = torch.empty(n.value, dtype=_U8, device=device)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _packed_cu(cu_seqlens, device):
+    """(device int32 tensor, host int32 array, sequences).  A prepared pair is taken as it is."""
+    if isinstance(cu_seqlens, tuple):
+        dev, host = cu_seqlens
+        if not (isinstance(host, np.ndarray) and host.dtype == np.int32 and host.flags.c_contiguous):
+            host = np.ascontiguousarray(host, dtype=np.int32)
+        if not isinstance(dev, torch.Tensor) or dev.dtype != torch.int32 or not dev.is_contiguous():
+            raise ValueError("the device half of cu_seqlens must be a contiguous int32 tensor")
+    else:
+        dev, host = _cu_pair(cu_seqlens, device)
+    if host.ndim != 1 or host.shape[0] < 1 or dev.numel() != host.shape[0]:
+        raise ValueError("cu_seqlens must hold one more entry than there are sequences, on the device as on the host")
+    return dev, host, host.shape[0] - 1
 
 
 # ------------------------------------------------------------------ layer norm
@@ -92,22 +142,20 @@ def kda_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
     """Layer norm over the last axis of x [M, C] (bf16 or fp32, rows may be strided); weight and bias [C] fp32 or
     None.  Returns y (x's dtype), or (y, stats) with return_stats: stats [M, 2] fp32 holds each row's mean and
     1 / sqrt(var + eps), which kda_layer_norm_backward reads.  C is at most 32768."""
+    if stream is not None:
+        with _on(stream, x, weight, bias, y):
+            return kda_layer_norm(x, weight, bias, eps=eps, y=y, return_stats=return_stats)
     lib = _lib.load()
-    if x.dim() != 2:
-        raise ValueError(f"expected x [M, C], got {tuple(x.shape)}")
-    a = _lib.NormArgs()
-    a.M, a.C, a.io = x.shape[0], x.shape[1], _io(x, "x")
-    a.x, a.x_stride = x.data_ptr(), _rows(x, x.shape, x.dtype, "x")
-    _dense(weight, (a.C,), torch.float32, "weight")
-    _dense(bias, (a.C,), torch.float32, "bias")
-    _same_cuda_device(x=x, weight=weight, bias=bias, y=y)
-    with _on(stream, x, weight, bias, y) as s:
-        if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        stats = torch.empty((a.M, 2), dtype=torch.float32, device=x.device) if return_stats else None
-        a.weight, a.bias, a.eps = _ptr(weight), _ptr(bias), float(eps)
-        a.y, a.y_stride, a.stats = y.data_ptr(), _rows(y, x.shape, x.dtype, "y"), _ptr(stats)
-        _check(lib.kda_layer_norm(ctypes.byref(a), s), "kda_layer_norm")
+    M, C = _shape2(x, "x")
+    io, dtype = _io(x, "x"), x.dtype
+    xs, w, b = _rows(x, M, C, dtype, "x"), _dense(weight, (C,), _F32, "weight"), _dense(bias, (C,), _F32, "bias")
+    ys = C if y is None else _rows(y, M, C, dtype, "y")
+    index = _device(x, weight=weight, bias=bias, y=y)
+    if y is None:
+        y = torch.empty((M, C), dtype=dtype, device=x.device)
+    stats = torch.empty((M, 2), dtype=_F32, device=x.device) if return_stats else None
+    a = _NORM.pack(M, C, io, x.data_ptr(), xs, w, b, eps, y.data_ptr(), ys, _ptr(stats))
+    _check(lib.kda_layer_norm(a, _stream_of(index)), "kda_layer_norm")
     return (y, stats) if return_stats else y
 
 
@@ -117,32 +165,34 @@ def kda_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tens
     """Gradients of sum(dy * y) of one kda_layer_norm call: a dict of dx (dy's dtype) and, with param_grads, dweight
     and dbias [C] fp32 (summed in a fixed order).  x is the forward's input, or its 8-bit codes with x_scales given
     (the pair kda_pack8 returns), which the kernel reads directly; stats come from the forward."""
+    if stream is not None:
+        with _on(stream, dy, x, stats, weight, x_scales, workspace):
+            return kda_layer_norm_backward(dy, x, stats, weight, x_scales=x_scales, param_grads=param_grads,
+                                           workspace=workspace)
     lib = _lib.load()
-    if dy.dim() != 2:
-        raise ValueError(f"expected dy [M, C], got {tuple(dy.shape)}")
-    a = _lib.NormBackwardArgs()
-    a.M, a.C, a.io = dy.shape[0], dy.shape[1], _io(dy, "dy")
-    a.dy, a.dy_stride = dy.data_ptr(), _rows(dy, dy.shape, dy.dtype, "dy")
+    M, C = _shape2(dy, "dy")
+    io, dtype, dev = _io(dy, "dy"), dy.dtype, dy.device
+    dys = _rows(dy, M, C, dtype, "dy")
     if x_scales is None:
-        a.x_stride = _rows(x, dy.shape, dy.dtype, "x")
+        xs, xp, sp = _rows(x, M, C, dtype, "x"), x.data_ptr(), 0
     else:
-        _dense(x, dy.shape, torch.uint8, "x (8-bit codes)")
-        _dense(x_scales, (a.M, -(-a.C // _lib.KDA_PACK8_BLOCK)), torch.uint8, "x_scales")
-    a.x, a.x_scales = x.data_ptr(), _ptr(x_scales)
-    _dense(stats, (a.M, 2), torch.float32, "stats")
-    _dense(weight, (a.C,), torch.float32, "weight")
-    _same_cuda_device(dy=dy, x=x, stats=stats, weight=weight, x_scales=x_scales, workspace=workspace)
-    dev = dy.device
-    with _on(stream, dy, x, stats, weight, x_scales, workspace) as s:
-        res = {"dx": torch.empty(dy.shape, dtype=dy.dtype, device=dev)}
-        if param_grads:
-            res["dweight"] = torch.empty((a.C,), dtype=torch.float32, device=dev)
-            res["dbias"] = torch.empty((a.C,), dtype=torch.float32, device=dev)
-        a.stats, a.weight, a.dx = stats.data_ptr(), _ptr(weight), res["dx"].data_ptr()
-        a.dweight, a.dbias = _ptr(res.get("dweight")), _ptr(res.get("dbias"))
-        workspace = _workspace(lib.kda_layer_norm_backward_workspace_size, a, "kda_layer_norm_backward_workspace_size",
-                               workspace, dev)
-        _check(lib.kda_layer_norm_backward(ctypes.byref(a), s), "kda_layer_norm_backward")
+        xs, xp = C, _dense(x, (M, C), _U8, "x (8-bit codes)")
+        sp = _dense(x_scales, (M, -(-C // _BLOCK)), _U8, "x_scales")
+    st, w = _dense(stats, (M, 2), _F32, "stats"), _dense(weight, (C,), _F32, "weight")
+    index = _device(dy, x=x, stats=stats, weight=weight, x_scales=x_scales, workspace=workspace)
+    res = {"dx": torch.empty((M, C), dtype=dtype, device=dev)}
+    dw = db = 0
+    if param_grads:
+        both = torch.empty((2, C), dtype=_F32, device=dev)
+        res["dweight"], res["dbias"] = both.unbind(0)
+        dw = both.data_ptr()
+        db = dw + 4 * C
+    args = (M, C, io, dy.data_ptr(), dys, xp, xs, sp, st, w, res["dx"].data_ptr(), C, dw, db)
+    p, n, keep = 0, 0, None
+    if param_grads:
+        p, n, keep = _workspace(lib.kda_layer_norm_backward_workspace_size, _NORM_BWD.pack(*args, 0, 0),
+                                "kda_layer_norm_backward_workspace_size", workspace, dev)
+    _check(lib.kda_layer_norm_backward(_NORM_BWD.pack(*args, p, n), _stream_of(index)), "kda_layer_norm_backward")
     return res
 
 
@@ -151,16 +201,16 @@ def kda_pack8(x: torch.Tensor, *, stream=None):
     """x [M, C] (bf16 or fp32, rows may be strided) in 8 bits: (codes [M, C] uint8, scales [M, ceil(C / 32)] uint8).
     Each block of 32 channels is stored as e4m3 under the smallest power of two that keeps its largest magnitude
     within 448; scales hold the exponent + 127.  NaN and infinities come back as NaN."""
+    if stream is not None:
+        with _on(stream, x):
+            return kda_pack8(x)
     lib = _lib.load()
-    if x.dim() != 2:
-        raise ValueError(f"expected x [M, C], got {tuple(x.shape)}")
-    M, C = x.shape
-    io, xs = _io(x, "x"), _rows(x, x.shape, x.dtype, "x")
-    _same_cuda_device(x=x)
-    with _on(stream, x) as s:
-        codes = torch.empty((M, C), dtype=torch.uint8, device=x.device)
-        scales = torch.empty((M, -(-C // _lib.KDA_PACK8_BLOCK)), dtype=torch.uint8, device=x.device)
-        _check(lib.kda_pack8(x.data_ptr(), xs, io, M, C, codes.data_ptr(), scales.data_ptr(), s), "kda_pack8")
+    M, C = _shape2(x, "x")
+    io, xs = _io(x, "x"), _rows(x, M, C, x.dtype, "x")
+    index = _device(x)
+    codes = torch.empty((M, C), dtype=_U8, device=x.device)
+    scales = torch.empty((M, -(-C // _BLOCK)), dtype=_U8, device=x.device)
+    _check(lib.kda_pack8(x.data_ptr(), xs, io, M, C, codes.data_ptr(), scales.data_ptr(), _stream_of(index)), "kda_pack8")
     return codes, scales
 
 
@@ -168,24 +218,264 @@ def kda_unpack8(codes: torch.Tensor, scales: torch.Tensor, *, dtype=torch.bfloat
                 stream=None) -> torch.Tensor:
     """The values that kda_pack8's codes and scales stand for, [M, C] in dtype (exact in bf16 and fp32 wherever the
     value itself is a normal number)."""
+    if stream is not None:
+        with _on(stream, codes, scales, out):
+            return kda_unpack8(codes, scales, dtype=dtype, out=out)
     lib = _lib.load()
-    if codes.dim() != 2:
-        raise ValueError(f"expected codes [M, C], got {tuple(codes.shape)}")
-    M, C = codes.shape
-    _dense(codes, (M, C), torch.uint8, "codes")
-    _dense(scales, (M, -(-C // _lib.KDA_PACK8_BLOCK)), torch.uint8, "scales")
-    _same_cuda_device(codes=codes, scales=scales, out=out)
-    with _on(stream, codes, scales, out) as s:
-        if out is None:
-            out = torch.empty((M, C), dtype=dtype, device=codes.device)
-        io, xs = _io(out, "out"), _rows(out, (M, C), out.dtype, "out")
-        _check(lib.kda_unpack8(codes.data_ptr(), scales.data_ptr(), M, C, out.data_ptr(), xs, io, s), "kda_unpack8")
+    M, C = _shape2(codes, "codes")
+    cp, sp = _dense(codes, (M, C), _U8, "codes"), _dense(scales, (M, -(-C // _BLOCK)), _U8, "scales")
+    if out is None and dtype not in _DT:
+        raise ValueError(f"dtype is {dtype}; expected bfloat16 or float32")
+    if out is not None:
+        dtype = out.dtype
+        _io(out, "out")
+    xs = C if out is None else _rows(out, M, C, dtype, "out")
+    index = _device(codes, scales=scales, out=out)
+    if out is None:
+        out = torch.empty((M, C), dtype=dtype, device=codes.device)
+    _check(lib.kda_unpack8(cp, sp, M, C, out.data_ptr(), xs, _DT[dtype], _stream_of(index)), "kda_unpack8")
     return out
 
 
-def _check_saved(saved: str) -> None:
-    if saved not in SAVED:
-        raise ValueError(f"saved must be one of {SAVED}, got {saved!r}")
+# ------------------------------------------------------------------ the selective scan's short convolution
+def _need(t, name: str):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    return t
+
+
+def kda_ssm_conv(x: torch.Tensor, w: torch.Tensor, cu_seqlens, *, bias: Optional[torch.Tensor] = None,
+                 silu: bool = True, conv_state_in: Optional[torch.Tensor] = None,
+                 conv_state_out: Optional[torch.Tensor] = None, output_conv_state: bool = False,
+                 y: Optional[torch.Tensor] = None, d_status=None, check_cu_on_host: bool = True, stream=None):
+    """The selective scan's causal depthwise convolution of width 4 over packed sequences: x [T, C] (bf16 or fp32, rows
+    may be strided), w [C, 4] fp32 (tap 3 multiplies x[t]), bias [C] fp32 or None; silu: SiLU after the sum.
+    conv_state_in [N, C, 3] like x continues earlier tokens.  Returns y, or (y, conv_state_out [N, C, 3]) when
+    output_conv_state is set or a conv_state_out is given."""
+    if stream is not None:
+        with _on(stream, x, w, bias, conv_state_in, conv_state_out, y, d_status):
+            return kda_ssm_conv(x, w, cu_seqlens, bias=bias, silu=silu, conv_state_in=conv_state_in,
+                                conv_state_out=conv_state_out, output_conv_state=output_conv_state, y=y,
+                                d_status=d_status, check_cu_on_host=check_cu_on_host)
+    lib = _lib.load()
+    T, C = _shape2(x, "x")
+    io, dtype, dev = _io(x, "x"), x.dtype, x.device
+    xs, wp, bp = _rows(x, T, C, dtype, "x"), _dense(_need(w, "w"), (C, 4), _F32, "w"), _dense(bias, (C,), _F32, "bias")
+    ys = C if y is None else _rows(y, T, C, dtype, "y")
+    index = _device(x, w=w, bias=bias, conv_state_in=conv_state_in, conv_state_out=conv_state_out, y=y, d_status=d_status)
+    cu, host, N = _packed_cu(cu_seqlens, dev)
+    _device(x, cu_seqlens=cu)
+    if conv_state_out is None and output_conv_state:
+        conv_state_out = torch.empty((N, C, 3), dtype=dtype, device=dev)
+    si = _dense(conv_state_in, (N, C, 3), dtype, "conv_state_in")
+    so = _dense(conv_state_out, (N, C, 3), dtype, "conv_state_out")
+    if y is None:
+        y = torch.empty((T, C), dtype=dtype, device=dev)
+    a = _CONV.pack(N, C, T, io, bool(silu), cu.data_ptr(), host.ctypes.data if check_cu_on_host else 0, x.data_ptr(), xs,
+                   wp, bp, si, so, y.data_ptr(), ys, _ptr(d_status))
+    _check(lib.kda_ssm_conv(a, _stream_of(index)), "kda_ssm_conv")
+    return y if conv_state_out is None else (y, conv_state_out)
+
+
+def kda_ssm_conv_step(x: torch.Tensor, w: torch.Tensor, conv_state: torch.Tensor, *,
+                      bias: Optional[torch.Tensor] = None, silu: bool = True, y: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """One token for each of N sequences: x [N, C]; conv_state [N, C, 3] like x is rolled in place.  Returns y [N, C]."""
+    if stream is not None:
+        with _on(stream, x, w, conv_state, bias, y):
+            return kda_ssm_conv_step(x, w, conv_state, bias=bias, silu=silu, y=y)
+    lib = _lib.load()
+    N, C = _shape2(x, "x")
+    io, dtype = _io(x, "x"), x.dtype
+    xs, wp, bp = _rows(x, N, C, dtype, "x"), _dense(_need(w, "w"), (C, 4), _F32, "w"), _dense(bias, (C,), _F32, "bias")
+    sp = _dense(_need(conv_state, "conv_state"), (N, C, 3), dtype, "conv_state")
+    ys = C if y is None else _rows(y, N, C, dtype, "y")
+    index = _device(x, w=w, conv_state=conv_state, bias=bias, y=y)
+    if y is None:
+        y = torch.empty((N, C), dtype=dtype, device=x.device)
+    a = _CONV.pack(N, C, 0, io, bool(silu), 0, 0, x.data_ptr(), xs, wp, bp, 0, sp, y.data_ptr(), ys, 0)
+    _check(lib.kda_ssm_conv_step(a, _stream_of(index)), "kda_ssm_conv_step")
+    return y
+
+
+def kda_ssm_conv_backward(x: torch.Tensor, w: torch.Tensor, cu_seqlens, dy: torch.Tensor, *,
+                          bias: Optional[torch.Tensor] = None, silu: bool = True,
+                          conv_state_in: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                          d_status=None, check_cu_on_host: bool = True, stream=None) -> dict:
+    """Gradients of sum(dy * y) of one kda_ssm_conv call (same inputs): a dict of dx (x's dtype), dw [C, 4] fp32, dbias
+    [C] fp32 when bias is given, dconv_state_in [N, C, 3] fp32 when conv_state_in is given."""
+    if stream is not None:
+        with _on(stream, x, w, dy, bias, conv_state_in, workspace, d_status):
+            return kda_ssm_conv_backward(x, w, cu_seqlens, dy, bias=bias, silu=silu, conv_state_in=conv_state_in,
+                                         workspace=workspace, d_status=d_status, check_cu_on_host=check_cu_on_host)
+    lib = _lib.load()
+    T, C = _shape2(x, "x")
+    io, dtype, dev = _io(x, "x"), x.dtype, x.device
+    xs, wp, bp = _rows(x, T, C, dtype, "x"), _dense(_need(w, "w"), (C, 4), _F32, "w"), _dense(bias, (C,), _F32, "bias")
+    dys = _rows(dy, T, C, dtype, "dy")
+    index = _device(x, w=w, dy=dy, bias=bias, conv_state_in=conv_state_in, workspace=workspace, d_status=d_status)
+    cu, host, N = _packed_cu(cu_seqlens, dev)
+    _device(x, cu_seqlens=cu)
+    si = _dense(conv_state_in, (N, C, 3), dtype, "conv_state_in")
+    res = {"dx": torch.empty((T, C), dtype=dtype, device=dev), "dw": torch.empty((C, 4), dtype=_F32, device=dev)}
+    if bias is not None:
+        res["dbias"] = torch.empty((C,), dtype=_F32, device=dev)
+    if conv_state_in is not None:
+        res["dconv_state_in"] = torch.empty((N, C, 3), dtype=_F32, device=dev)
+    args = (N, C, T, io, bool(silu), cu.data_ptr(), host.ctypes.data if check_cu_on_host else 0, x.data_ptr(), xs, wp, bp,
+            si, 0, 0, 0, _ptr(d_status), dy.data_ptr(), dys, res["dx"].data_ptr(), C, res["dw"].data_ptr(),
+            _ptr(res.get("dbias")), _ptr(res.get("dconv_state_in")))
+    p, n, keep = _workspace(lib.kda_ssm_conv_backward_workspace_size, _CONV_BWD.pack(*args, 0, 0),
+                            "kda_ssm_conv_backward_workspace_size", workspace, dev)
+    _check(lib.kda_ssm_conv_backward(_CONV_BWD.pack(*args, p, n), _stream_of(index)), "kda_ssm_conv_backward")
+    return res
+
+
+# ------------------------------------------------------------------ the selective scan
+def _grouped(t: torch.Tensor, rows: int, G: int, N: int, dtype, name: str) -> int:
+    """Row stride of a [rows, G, N] tensor whose (G, N) block is dense."""
+    if t.dim() != 3 or t.shape != (rows, G, N) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} of shape {(rows, G, N)}, got {t.dtype} {tuple(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if (N > 1 and s2 != 1) or (G > 1 and s1 != N):
+        raise ValueError(f"the (G, N) block of each row of {name} must be contiguous")
+    return s0 if rows > 1 else G * N
+
+
+def _ssm_inputs(u, dt, A, B, C, D, z, dt_bias):
+    """Checked shapes, dtypes and strides of the inputs that prompt, step and gradients share: the sizes, and the
+    values of kda_ssm_args from u to dt_bias."""
+    if u.dim() != 2 or A.dim() != 2 or B.dim() != 3:
+        raise ValueError(f"expected u [T, C], A [C, N] and B [T, G, N], got {tuple(u.shape)}, {tuple(A.shape)}, "
+                         f"{tuple(B.shape)}")
+    T, Ch = u.shape
+    N, G, dtype = A.shape[1], B.shape[1], u.dtype
+    io = _io(u, "u")
+    vals = (u.data_ptr(), _rows(u, T, Ch, dtype, "u"), dt.data_ptr(), _rows(dt, T, Ch, dtype, "dt"),
+            _dense(A, (Ch, N), _F32, "A"), B.data_ptr(), _grouped(B, T, G, N, dtype, "B"), C.data_ptr(),
+            _grouped(C, T, G, N, dtype, "C"), _dense(D, (Ch,), _F32, "D"), _ptr(z),
+            0 if z is None else _rows(z, T, Ch, dtype, "z"), _dense(dt_bias, (Ch,), _F32, "dt_bias"))
+    return T, Ch, N, G, io, dtype, vals
+
+
+def kda_ssm_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, cu_seqlens, *,
+                 D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                 dt_bias: Optional[torch.Tensor] = None, softplus: bool = True,
+                 initial_state: Optional[torch.Tensor] = None, output_final_state: bool = True,
+                 final_state: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, d_status=None, check_cu_on_host: bool = True, stream=None):
+    """The selective state space scan over packed sequences; returns (y, final_state or None).
+
+    u, dt, z: [T, Ch] (bf16 or fp32, one dtype; rows may be strided); A [Ch, N] fp32 (<= 0; N in 8, 16, 32, 64);
+    B, C: [T, G, N] like u, each group of Ch / G channels reads one; D, dt_bias [Ch] fp32 or None; z None: no gate.
+    softplus: the step size is softplus(dt + dt_bias), else dt + dt_bias.  initial_state / final_state [num_sequences,
+    Ch, N] fp32 (not the same buffer)."""
+    if stream is not None:
+        with _on(stream, u, dt, A, B, C, D, z, dt_bias, initial_state, final_state, y, workspace, d_status):
+            return kda_ssm_scan(u, dt, A, B, C, cu_seqlens, D=D, z=z, dt_bias=dt_bias, softplus=softplus,
+                                initial_state=initial_state, output_final_state=output_final_state,
+                                final_state=final_state, y=y, workspace=workspace, d_status=d_status,
+                                check_cu_on_host=check_cu_on_host)
+    lib = _lib.load()
+    T, Ch, N, G, io, dtype, vals = _ssm_inputs(u, dt, A, B, C, D, z, dt_bias)
+    ys, dev = Ch if y is None else _rows(y, T, Ch, dtype, "y"), u.device
+    index = _device(u, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias, initial_state=initial_state,
+                    final_state=final_state, y=y, workspace=workspace, d_status=d_status)
+    cu, host, n = _packed_cu(cu_seqlens, dev)
+    _device(u, cu_seqlens=cu)
+    ip = _dense(initial_state, (n, Ch, N), _F32, "initial_state")
+    if final_state is None and output_final_state:
+        final_state = torch.empty((n, Ch, N), dtype=_F32, device=dev)
+    fp = _dense(final_state, (n, Ch, N), _F32, "final_state")
+    if y is None:
+        y = torch.empty((T, Ch), dtype=dtype, device=dev)
+    args = (n, Ch, N, G, T, io, bool(softplus), cu.data_ptr(), host.ctypes.data if check_cu_on_host else 0, *vals, ip, fp,
+            y.data_ptr(), ys)
+    status = _ptr(d_status)
+    p, size, keep = _workspace(lib.kda_ssm_scan_workspace_size, _SSM.pack(*args, 0, 0, status),
+                               "kda_ssm_scan_workspace_size", workspace, dev)
+    _check(lib.kda_ssm_scan(_SSM.pack(*args, p, size, status), _stream_of(index)), "kda_ssm_scan")
+    return y, final_state
+
+
+def kda_ssm_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                 state: torch.Tensor, *, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                 dt_bias: Optional[torch.Tensor] = None, softplus: bool = True, y: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """One token for each of n sequences: u, dt, z [n, Ch], B, C [n, G, N]; state [n, Ch, N] fp32 is updated in place.
+    Returns y [n, Ch]."""
+    if stream is not None:
+        with _on(stream, u, dt, A, B, C, state, D, z, dt_bias, y):
+            return kda_ssm_step(u, dt, A, B, C, state, D=D, z=z, dt_bias=dt_bias, softplus=softplus, y=y)
+    lib = _lib.load()
+    n, Ch, N, G, io, dtype, vals = _ssm_inputs(u, dt, A, B, C, D, z, dt_bias)
+    sp = _dense(_need(state, "state"), (n, Ch, N), _F32, "state")
+    ys = Ch if y is None else _rows(y, n, Ch, dtype, "y")
+    index = _device(u, dt=dt, A=A, B=B, C=C, state=state, D=D, z=z, dt_bias=dt_bias, y=y)
+    if y is None:
+        y = torch.empty((n, Ch), dtype=dtype, device=u.device)
+    a = _SSM.pack(n, Ch, N, G, 0, io, bool(softplus), 0, 0, *vals, 0, sp, y.data_ptr(), ys, 0, 0, 0)
+    _check(lib.kda_ssm_step(a, _stream_of(index)), "kda_ssm_step")
+    return y
+
+
+def kda_ssm_backward(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, cu_seqlens,
+                     dy: torch.Tensor, *, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                     dt_bias: Optional[torch.Tensor] = None, softplus: bool = True,
+                     initial_state: Optional[torch.Tensor] = None, d_final_state: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, d_status=None, check_cu_on_host: bool = True,
+                     stream=None) -> dict:
+    """Gradients of sum(dy * y) + sum(d_final_state * final_state) of one kda_ssm_scan call (same inputs): a dict of du,
+    ddt [T, Ch], dB, dC [T, G, N] (u's dtype), dA [Ch, N] fp32 and, where the input is given, dz (u's dtype), dD,
+    ddt_bias [Ch] fp32 and dinitial_state fp32.  The workspace holds the states in front of every fourth token:
+    about T * Ch * N bytes."""
+    if stream is not None:
+        with _on(stream, u, dt, A, B, C, dy, D, z, dt_bias, initial_state, d_final_state, workspace, d_status):
+            return kda_ssm_backward(u, dt, A, B, C, cu_seqlens, dy, D=D, z=z, dt_bias=dt_bias, softplus=softplus,
+                                    initial_state=initial_state, d_final_state=d_final_state, workspace=workspace,
+                                    d_status=d_status, check_cu_on_host=check_cu_on_host)
+    lib = _lib.load()
+    T, Ch, N, G, io, dtype, vals = _ssm_inputs(u, dt, A, B, C, D, z, dt_bias)
+    dys, dev = _rows(dy, T, Ch, dtype, "dy"), u.device
+    index = _device(u, dt=dt, A=A, B=B, C=C, dy=dy, D=D, z=z, dt_bias=dt_bias, initial_state=initial_state,
+                    d_final_state=d_final_state, workspace=workspace, d_status=d_status)
+    cu, host, n = _packed_cu(cu_seqlens, dev)
+    _device(u, cu_seqlens=cu)
+    ip = _dense(initial_state, (n, Ch, N), _F32, "initial_state")
+    dfp = _dense(d_final_state, (n, Ch, N), _F32, "d_final_state")
+
+    def io_rows(*shape):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+    def params(*shape):
+        return torch.empty(shape, dtype=_F32, device=dev)
+
+    res = {"du": io_rows(T, Ch), "ddt": io_rows(T, Ch), "dA": params(Ch, N), "dB": io_rows(T, G, N), "dC": io_rows(T, G, N)}
+    if z is not None:
+        res["dz"] = io_rows(T, Ch)
+    if D is not None:
+        res["dD"] = params(Ch)
+    if dt_bias is not None:
+        res["ddt_bias"] = params(Ch)
+    if initial_state is not None:
+        res["dinitial_state"] = params(n, Ch, N)
+    args = (n, Ch, N, G, T, io, bool(softplus), cu.data_ptr(), host.ctypes.data if check_cu_on_host else 0, *vals, ip, 0,
+            0, 0, 0, 0, _ptr(d_status), dy.data_ptr(), dys, dfp,
+            *(_ptr(res.get(k)) for k in ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dinitial_state")))
+    p, size, keep = _workspace(lib.kda_ssm_backward_workspace_size, _SSM_BWD.pack(*args, 0, 0),
+                               "kda_ssm_backward_workspace_size", workspace, dev)
+    _check(lib.kda_ssm_backward(_SSM_BWD.pack(*args, p, size), _stream_of(index)), "kda_ssm_backward")
+    return res
+
+
+# ------------------------------------------------------------------ differentiable forms
+def _keep(t: Optional[torch.Tensor], saved: str):
+    """(t, None), or t [M, C] as 8-bit codes and scales."""
+    return (t, None) if t is None or saved == "io" else kda_pack8(t)
+
+
+def _restore(t: Optional[torch.Tensor], scales: Optional[torch.Tensor], dtype):
+    return t if scales is None else kda_unpack8(t, scales, dtype=dtype)
 
 
 class _NormLayer(torch.autograd.Function):
@@ -194,9 +484,8 @@ class _NormLayer(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps, saved):
         y, stats = kda_layer_norm(x, weight, bias, eps=eps, return_stats=True)
-        kept = kda_pack8(x) if saved == "e4m3" else (x, None)
-        ctx.save_for_backward(*kept, stats, weight)
-        ctx.has_bias = bias is not None
+        if any(ctx.needs_input_grad):
+            ctx.save_for_backward(*_keep(x, saved), stats, weight)
         return y
 
     @staticmethod
@@ -213,245 +502,80 @@ def kda_norm_layer(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
                    eps: float = 1e-5, saved: str = "io") -> torch.Tensor:
     """Layer norm of x [M, C] as a differentiable PyTorch operation.  saved="e4m3" keeps x in 8 bits for the backward
     pass (a little over half the memory of bf16): the gradients are then those at the rounded x, with the exact
-    mean and deviation."""
-    _check_saved(saved)
-    return _NormLayer.apply(x, weight, bias, float(eps), saved)
+    mean and deviation.  In a captured graph, see kda_ssm_layer's note."""
+    _autograd.check_saved(saved)
+    return _autograd.apply(_NormLayer, "kda_norm_layer", x, weight, bias, float(eps), saved)
 
 
-# ------------------------------------------------------------------ the selective scan's short convolution
-def _param(t: Optional[torch.Tensor], shape, name: str):
-    _dense(t, shape, torch.float32, name)
-    return _ptr(t)
+class _SsmConvLayer(torch.autograd.Function):
+    """kda_ssm_conv forward, kda_ssm_conv_backward backward."""
+
+    @staticmethod
+    def forward(ctx, x, w, bias, conv_state_in, cu_pair, silu, saved):
+        y = kda_ssm_conv(x, w, cu_pair, bias=bias, silu=silu, conv_state_in=conv_state_in)
+        if any(ctx.needs_input_grad):
+            ctx.save_for_backward(*_keep(x, saved), w, bias, conv_state_in)
+            ctx.rest = (cu_pair, silu, x.dtype)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, scales, w, bias, state = ctx.saved_tensors
+        cu_pair, silu, dtype = ctx.rest
+        g = kda_ssm_conv_backward(_restore(x, scales, dtype), w, cu_pair, dy.contiguous(), bias=bias, silu=silu,
+                                  conv_state_in=state)
+        want = ctx.needs_input_grad
+        dstate = g["dconv_state_in"].to(state.dtype) if want[3] else None
+        return (g["dx"] if want[0] else None, g["dw"] if want[1] else None, g["dbias"] if want[2] else None, dstate,
+                None, None, None)
 
 
-def _rows2(t: torch.Tensor, name: str):
-    if t.dim() != 2:
-        raise ValueError(f"expected {name} [T, C], got {tuple(t.shape)}")
-    return t.shape
+def kda_ssm_conv_layer(x: torch.Tensor, w: torch.Tensor, cu_seqlens, *, bias: Optional[torch.Tensor] = None,
+                       silu: bool = True, conv_state_in: Optional[torch.Tensor] = None, saved: str = "io") -> torch.Tensor:
+    """kda_ssm_conv as a differentiable PyTorch operation: y, with gradients for x, w, bias and conv_state_in.
+    saved="e4m3" keeps x in 8 bits for the backward pass.  In a captured graph, see kda_ssm_layer's note."""
+    _autograd.check_saved(saved)
+    return _autograd.apply(_SsmConvLayer, "kda_ssm_conv_layer", x, w, bias, conv_state_in,
+                           _cu_pair(cu_seqlens, x.device), bool(silu), saved)
 
 
-def _conv_args(x, w, bias, silu, T, C):
-    a = _lib.SsmConvArgs()
-    a.C, a.T_total, a.io, a.silu = C, T, _io(x, "x"), int(bool(silu))
-    a.x, a.x_stride = x.data_ptr(), _rows(x, (T, C), x.dtype, "x")
-    if w is None:
-        raise ValueError("w is required")
-    a.w, a.bias = _param(w, (C, 4), "w"), _param(bias, (C,), "bias")
-    return a
+class _SsmLayer(torch.autograd.Function):
+    """kda_ssm_scan forward, kda_ssm_backward backward."""
+
+    @staticmethod
+    def forward(ctx, u, dt, A, B, C, D, z, dt_bias, initial_state, cu_pair, softplus, saved):
+        y, fin = kda_ssm_scan(u, dt, A, B, C, cu_pair, D=D, z=z, dt_bias=dt_bias, softplus=softplus,
+                              initial_state=initial_state)
+        if any(ctx.needs_input_grad):
+            ctx.save_for_backward(*_keep(u, saved), *_keep(z, saved), dt, A, B, C, D, dt_bias, initial_state)
+            ctx.rest = (cu_pair, softplus, u.dtype)
+        ctx.set_materialize_grads(False)
+        return y, fin
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dfin):
+        u, us, z, zs, dt, A, B, C, D, dt_bias, init = ctx.saved_tensors
+        cu_pair, softplus, dtype = ctx.rest
+        dy = torch.zeros(dt.shape, dtype=dtype, device=dt.device) if dy is None else dy.contiguous()
+        g = kda_ssm_backward(_restore(u, us, dtype), dt, A, B, C, cu_pair, dy, D=D, z=_restore(z, zs, dtype),
+                             dt_bias=dt_bias, softplus=softplus, initial_state=init,
+                             d_final_state=None if dfin is None else dfin.contiguous())
+        names = ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dinitial_state")
+        return (*(g[n] if want else None for n, want in zip(names, ctx.needs_input_grad)), None, None, None)
 
 
-def _packed(a, cu_dev, cu_host, check_cu_on_host: bool) -> int:
-    a.N = cu_host.shape[0] - 1
-    a.cu_seqlens = cu_dev.data_ptr()
-    a.cu_seqlens_host = cu_host.ctypes.data if check_cu_on_host else None
-    return a.N
+def kda_ssm_layer(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, cu_seqlens, *,
+                  D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                  dt_bias: Optional[torch.Tensor] = None, softplus: bool = True,
+                  initial_state: Optional[torch.Tensor] = None, saved: str = "io"):
+    """kda_ssm_scan as a differentiable PyTorch operation: (y, final_state), with gradients for u, dt, A, B, C, D, z,
+    dt_bias and initial_state.  saved="e4m3" keeps u and z in 8 bits for the backward pass; dt, B and C stay as they
+    are (a step size enters the decays' exponents, and B and C are small).
 
-
-def kda_ssm_conv(x: torch.Tensor, w: torch.Tensor, cu_seqlens, *, bias: Optional[torch.Tensor] = None,
-                 silu: bool = True, conv_state_in: Optional[torch.Tensor] = None,
-                 conv_state_out: Optional[torch.Tensor] = None, output_conv_state: bool = False,
-                 y: Optional[torch.Tensor] = None, d_status=None, check_cu_on_host: bool = True, stream=None):
-    """The selective scan's causal depthwise convolution of width 4 over packed sequences: x [T, C] (bf16 or fp32, rows
-    may be strided), w [C, 4] fp32 (tap 3 multiplies x[t]), bias [C] fp32 or None; silu: SiLU after the sum.
-    conv_state_in [N, C, 3] like x continues earlier tokens.  Returns y, or (y, conv_state_out [N, C, 3]) when
-    output_conv_state is set or a conv_state_out is given."""
-    lib = _lib.load()
-    T, C = _rows2(x, "x")
-    a = _conv_args(x, w, bias, silu, T, C)
-    with _on(stream, x, w, bias, conv_state_in, conv_state_out, y, d_status) as s:
-        cu_dev, cu_host = _cu_pair(cu_seqlens, x.device)
-        N = _packed(a, cu_dev, cu_host, check_cu_on_host)
-        _dense(conv_state_in, (N, C, 3), x.dtype, "conv_state_in")
-        if y is None:
-            y = torch.empty((T, C), dtype=x.dtype, device=x.device)
-        if conv_state_out is None and output_conv_state:
-            conv_state_out = torch.empty((N, C, 3), dtype=x.dtype, device=x.device)
-        _dense(conv_state_out, (N, C, 3), x.dtype, "conv_state_out")
-        _same_cuda_device(x=x, w=w, bias=bias, cu_seqlens=cu_dev, conv_state_in=conv_state_in,
-                          conv_state_out=conv_state_out, y=y, d_status=d_status)
-        a.conv_state_in, a.conv_state_out, a.d_status = _ptr(conv_state_in), _ptr(conv_state_out), _ptr(d_status)
-        a.y, a.y_stride = y.data_ptr(), _rows(y, (T, C), x.dtype, "y")
-        _check(lib.kda_ssm_conv(ctypes.byref(a), s), "kda_ssm_conv")
-    return y if conv_state_out is None else (y, conv_state_out)
-
-
-def kda_ssm_conv_step(x: torch.Tensor, w: torch.Tensor, conv_state: torch.Tensor, *,
-                      bias: Optional[torch.Tensor] = None, silu: bool = True, y: Optional[torch.Tensor] = None,
-                      stream=None) -> torch.Tensor:
-    """One token for each of N sequences: x [N, C]; conv_state [N, C, 3] like x is rolled in place.  Returns y [N, C]."""
-    lib = _lib.load()
-    N, C = _rows2(x, "x")
-    a = _conv_args(x, w, bias, silu, N, C)
-    a.N = N
-    if conv_state is None:
-        raise ValueError("conv_state is required")
-    _dense(conv_state, (N, C, 3), x.dtype, "conv_state")
-    _same_cuda_device(x=x, w=w, bias=bias, conv_state=conv_state, y=y)
-    with _on(stream, x, w, bias, conv_state, y) as s:
-        if y is None:
-            y = torch.empty((N, C), dtype=x.dtype, device=x.device)
-        a.conv_state_out = conv_state.data_ptr()
-        a.y, a.y_stride = y.data_ptr(), _rows(y, (N, C), x.dtype, "y")
-        _check(lib.kda_ssm_conv_step(ctypes.byref(a), s), "kda_ssm_conv_step")
-    return y
-
-
-def kda_ssm_conv_backward(x: torch.Tensor, w: torch.Tensor, cu_seqlens, dy: torch.Tensor, *,
-                          bias: Optional[torch.Tensor] = None, silu: bool = True,
-                          conv_state_in: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                          d_status=None, check_cu_on_host: bool = True, stream=None) -> dict:
-    """Gradients of sum(dy * y) of one kda_ssm_conv call (same inputs): a dict of dx (x's dtype), dw [C, 4] fp32, dbias
-    [C] fp32 when bias is given, dconv_state_in [N, C, 3] fp32 when conv_state_in is given."""
-    lib = _lib.load()
-    T, C = _rows2(x, "x")
-    b = _lib.SsmConvBackwardArgs()
-    with _on(stream, x, w, bias, dy, conv_state_in, workspace, d_status) as s:
-        cu_dev, cu_host = _cu_pair(cu_seqlens, x.device)
-        b.fwd = _conv_args(x, w, bias, silu, T, C)
-        N = _packed(b.fwd, cu_dev, cu_host, check_cu_on_host)
-        _dense(conv_state_in, (N, C, 3), x.dtype, "conv_state_in")
-        _same_cuda_device(x=x, w=w, bias=bias, dy=dy, cu_seqlens=cu_dev, conv_state_in=conv_state_in,
-                          workspace=workspace, d_status=d_status)
-        f32 = dict(dtype=torch.float32, device=x.device)
-        res = {"dx": torch.empty((T, C), dtype=x.dtype, device=x.device), "dw": torch.empty((C, 4), **f32)}
-        if bias is not None:
-            res["dbias"] = torch.empty((C,), **f32)
-        if conv_state_in is not None:
-            res["dconv_state_in"] = torch.empty((N, C, 3), **f32)
-        b.fwd.conv_state_in, b.fwd.d_status = _ptr(conv_state_in), _ptr(d_status)
-        b.dy, b.dy_stride = dy.data_ptr(), _rows(dy, (T, C), x.dtype, "dy")
-        b.dx, b.dw = res["dx"].data_ptr(), res["dw"].data_ptr()
-        b.dbias, b.dconv_state_in = _ptr(res.get("dbias")), _ptr(res.get("dconv_state_in"))
-        workspace = _workspace(lib.kda_ssm_conv_backward_workspace_size, b, "kda_ssm_conv_backward_workspace_size",
-                               workspace, x.device)
-        _check(lib.kda_ssm_conv_backward(ctypes.byref(b), s), "kda_ssm_conv_backward")
-    return res
-
-
-# ------------------------------------------------------------------ the selective scan
-def _ssm_args(u, dt, A, B, C, *, D, z, dt_bias, softplus, rows, where):
-    """SsmArgs with the inputs that prompt, step and gradients share, checked for shape and dtype."""
-    if u.dim() != 2 or A.dim() != 2 or B.dim() != 3:
-        raise ValueError(f"{where}: expected u [T, C], A [C, N] and B [T, G, N], got {tuple(u.shape)}, "
-                         f"{tuple(A.shape)}, {tuple(B.shape)}")
-    Ch, N, G = u.shape[1], A.shape[1], B.shape[1]
-    a = _lib.SsmArgs()
-    a.C, a.Nst, a.G, a.io, a.softplus = Ch, N, G, _io(u, "u"), int(bool(softplus))
-    a.u, a.u_stride = u.data_ptr(), _rows(u, (rows, Ch), u.dtype, "u")
-    a.dt, a.dt_stride = dt.data_ptr(), _rows(dt, (rows, Ch), u.dtype, "dt")
-    a.A = _param(A, (Ch, N), "A")
-
-    def grouped(t, name):
-        if tuple(t.shape) != (rows, G, N) or t.dtype != u.dtype:
-            raise ValueError(f"{name} must be {u.dtype} of shape {(rows, G, N)}, got {t.dtype} {tuple(t.shape)}")
-        if (N > 1 and t.stride(2) != 1) or (G > 1 and t.stride(1) != N):
-            raise ValueError(f"the (G, N) block of each row of {name} must be contiguous")
-        return t.data_ptr(), (t.stride(0) if rows > 1 else G * N)
-
-    a.B, a.B_stride = grouped(B, "B")
-    a.Cm, a.C_stride = grouped(C, "C")
-    a.D, a.dt_bias = _param(D, (Ch,), "D"), _param(dt_bias, (Ch,), "dt_bias")
-    if z is not None:
-        a.z, a.z_stride = z.data_ptr(), _rows(z, (rows, Ch), u.dtype, "z")
-    return a, Ch, N, G
-
-
-def kda_ssm_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, cu_seqlens, *,
-                 D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
-                 dt_bias: Optional[torch.Tensor] = None, softplus: bool = True,
-                 initial_state: Optional[torch.Tensor] = None, output_final_state: bool = True,
-                 final_state: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
-                 workspace: Optional[torch.Tensor] = None, d_status=None, check_cu_on_host: bool = True, stream=None):
-    """The selective state space scan over packed sequences; returns (y, final_state or None).
-
-    u, dt, z: [T, Ch] (bf16 or fp32, one dtype; rows may be strided); A [Ch, N] fp32 (<= 0; N in 8, 16, 32, 64);
-    B, C: [T, G, N] like u, each group of Ch / G channels reads one; D, dt_bias [Ch] fp32 or None; z None: no gate.
-    softplus: the step size is softplus(dt + dt_bias), else dt + dt_bias.  initial_state / final_state [num_sequences,
-    Ch, N] fp32 (not the same buffer)."""
-    lib = _lib.load()
-    T = u.shape[0]
-    a, Ch, N, G = _ssm_args(u, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, softplus=softplus, rows=T, where="kda_ssm_scan")
-    a.T_total = T
-    with _on(stream, u, dt, A, B, C, D, z, dt_bias, initial_state, final_state, y, workspace, d_status) as s:
-        cu_dev, cu_host = _cu_pair(cu_seqlens, u.device)
-        n = _packed(a, cu_dev, cu_host, check_cu_on_host)
-        if y is None:
-            y = torch.empty((T, Ch), dtype=u.dtype, device=u.device)
-        if final_state is None and output_final_state:
-            final_state = torch.empty((n, Ch, N), dtype=torch.float32, device=u.device)
-        a.initial_state = _param(initial_state, (n, Ch, N), "initial_state")
-        a.final_state = _param(final_state, (n, Ch, N), "final_state")
-        a.y, a.y_stride, a.d_status = y.data_ptr(), _rows(y, (T, Ch), u.dtype, "y"), _ptr(d_status)
-        _same_cuda_device(u=u, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias, cu_seqlens=cu_dev,
-                          initial_state=initial_state, final_state=final_state, y=y, workspace=workspace,
-                          d_status=d_status)
-        workspace = _workspace(lib.kda_ssm_scan_workspace_size, a, "kda_ssm_scan_workspace_size", workspace, u.device)
-        _check(lib.kda_ssm_scan(ctypes.byref(a), s), "kda_ssm_scan")
-    return y, final_state
-
-
-def kda_ssm_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
-                 state: torch.Tensor, *, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
-                 dt_bias: Optional[torch.Tensor] = None, softplus: bool = True, y: Optional[torch.Tensor] = None,
-                 stream=None) -> torch.Tensor:
-    """One token for each of n sequences: u, dt, z [n, Ch], B, C [n, G, N]; state [n, Ch, N] fp32 is updated in place.
-    Returns y [n, Ch]."""
-    lib = _lib.load()
-    n = u.shape[0]
-    a, Ch, N, G = _ssm_args(u, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, softplus=softplus, rows=n, where="kda_ssm_step")
-    a.N = n
-    if state is None:
-        raise ValueError("state is required")
-    a.final_state = _param(state, (n, Ch, N), "state")
-    _same_cuda_device(u=u, dt=dt, A=A, B=B, C=C, state=state, D=D, z=z, dt_bias=dt_bias, y=y)
-    with _on(stream, u, dt, A, B, C, state, D, z, dt_bias, y) as s:
-        if y is None:
-            y = torch.empty((n, Ch), dtype=u.dtype, device=u.device)
-        a.y, a.y_stride = y.data_ptr(), _rows(y, (n, Ch), u.dtype, "y")
-        _check(lib.kda_ssm_step(ctypes.byref(a), s), "kda_ssm_step")
-    return y
-
-
-def kda_ssm_backward(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, cu_seqlens,
-                     dy: torch.Tensor, *, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
-                     dt_bias: Optional[torch.Tensor] = None, softplus: bool = True,
-                     initial_state: Optional[torch.Tensor] = None, d_final_state: Optional[torch.Tensor] = None,
-                     workspace: Optional[torch.Tensor] = None, d_status=None, check_cu_on_host: bool = True,
-                     stream=None) -> dict:
-    """Gradients of sum(dy * y) + sum(d_final_state * final_state) of one kda_ssm_scan call (same inputs): a dict of du,
-    ddt [T, Ch], dB, dC [T, G, N] (u's dtype), dA [Ch, N] fp32 and, where the input is given, dz (u's dtype), dD,
-    ddt_bias [Ch] fp32 and dinitial_state fp32."""
-    lib = _lib.load()
-    T = u.shape[0]
-    b = _lib.SsmBackwardArgs()
-    f, Ch, N, G = _ssm_args(u, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, softplus=softplus, rows=T,
-                            where="kda_ssm_backward")
-    f.T_total = T
-    with _on(stream, u, dt, A, B, C, dy, D, z, dt_bias, initial_state, d_final_state, workspace, d_status) as s:
-        cu_dev, cu_host = _cu_pair(cu_seqlens, u.device)
-        n = _packed(f, cu_dev, cu_host, check_cu_on_host)
-        f.initial_state = _param(initial_state, (n, Ch, N), "initial_state")
-        f.d_status = _ptr(d_status)
-        b.fwd = f
-        b.dy, b.dy_stride = dy.data_ptr(), _rows(dy, (T, Ch), u.dtype, "dy")
-        b.d_final_state = _param(d_final_state, (n, Ch, N), "d_final_state")
-        _same_cuda_device(u=u, dt=dt, A=A, B=B, C=C, dy=dy, D=D, z=z, dt_bias=dt_bias, cu_seqlens=cu_dev,
-                          initial_state=initial_state, d_final_state=d_final_state, workspace=workspace,
-                          d_status=d_status)
-        io, f32 = dict(dtype=u.dtype, device=u.device), dict(dtype=torch.float32, device=u.device)
-        res = {"du": torch.empty((T, Ch), **io), "ddt": torch.empty((T, Ch), **io), "dA": torch.empty((Ch, N), **f32),
-               "dB": torch.empty((T, G, N), **io), "dC": torch.empty((T, G, N), **io)}
-        if z is not None:
-            res["dz"] = torch.empty((T, Ch), **io)
-        if D is not None:
-            res["dD"] = torch.empty((Ch,), **f32)
-        if dt_bias is not None:
-            res["ddt_bias"] = torch.empty((Ch,), **f32)
-        if initial_state is not None:
-            res["dinitial_state"] = torch.empty((n, Ch, N), **f32)
-        for name, t in res.items():
-            setattr(b, name, t.data_ptr())
-        workspace = _workspace(lib.kda_ssm_backward_workspace_size, b, "kda_ssm_backward_workspace_size", workspace,
-                               u.device)
-        _check(lib.kda_ssm_backward(ctypes.byref(b), s), "kda_ssm_backward")
-    return res
+    In a captured graph: pass cu_seqlens as a prepared (device, host) pair, and let no eager graph of the same leaves
+    live; the call raises if one that it knows of does."""
+    _autograd.check_saved(saved)
+    return _autograd.apply(_SsmLayer, "kda_ssm_layer", u, dt, A, B, C, D, z, dt_bias, initial_state,
+                           _cu_pair(cu_seqlens, u.device), bool(softplus), saved)
