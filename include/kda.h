@@ -406,7 +406,7 @@ kda_status kda_backward(const kda_backward_args* args, kda_stream_t stream);
  *   x, y    [M][row stride] io; y must not overlap x.
  *   weight, bias  [C] fp32, or NULL (ones, zeros).
  *   stats   [M][2] fp32 (mean, 1 / sqrt(var + eps)), what kda_layer_norm_backward
- *           reads, or NULL (not wanted).
+ *           reads, or NULL (not wanted); 8-byte aligned.
  * C in [1, 32768]; M >= 0.
  * ------------------------------------------------------------------------ */
 typedef struct {

@@ -52,18 +52,17 @@ def _on(stream, *inputs):
         yield
 
 
-def _device(first: torch.Tensor, **others) -> int:
+def _device(first: torch.Tensor, *others) -> int:
     """Index of the current device, on which every given tensor has to be: the library dereferences these
     pointers only on the GPU, and a host pointer there would fault."""
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError(f"tensors are on {dev}; every tensor must be on a CUDA device")
-    for name, t in others.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, other tensors on {dev}")
-    index = torch.cuda.current_device()
-    if dev.index != index:
-        raise ValueError(f"tensors are on {dev} but the current device is cuda:{index}")
+    index = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors are on {first.device} and on {t.device}; every tensor must be on one CUDA device")
+    if index < 0:
+        raise ValueError(f"tensors are on {first.device}; every tensor must be on a CUDA device")
+    if index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {first.device} but the current device is cuda:{torch.cuda.current_device()}")
     return index
 
 
@@ -90,12 +89,12 @@ def _shape2(t: torch.Tensor, name: str):
 
 def _rows(t: torch.Tensor, M: int, C: int, dtype, name: str) -> int:
     """Row stride (elements) of a [M, C] tensor whose rows are dense."""
-    if t.dim() != 2 or t.shape[0] != M or t.shape[1] != C:
+    if t.shape != (M, C):
         raise ValueError(f"{name} must be {(M, C)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
     s0, s1 = t.stride()
-    if C > 1 and s1 != 1:
+    if s1 != 1 and C > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
     return s0 if M > 1 else C
 
@@ -110,14 +109,25 @@ def _dense(t: Optional[torch.Tensor], shape, dtype, name: str) -> int:
     return t.data_ptr()
 
 
-def _workspace(size_fn, packed: bytes, where: str, workspace, device):
-    """(pointer, bytes, tensor): the caller's buffer, or a new one of the size the library asks for."""
+_sizes: dict = {}  # workspace bytes by entry point, device and sizes: what the library answered
+
+
+def _workspace(name: str, index: int, sizes, fmt, args, tail, workspace, device):
+    """(pointer, bytes, tensor): the caller's buffer, or a new one of the size the library asks for.  The size is a
+    function of the sizes and the device alone, so its answer is kept."""
     if workspace is None:
-        n = ctypes.c_size_t(0)
-        _check(size_fn(packed, ctypes.byref(n)), where)
-        if n.value == 0:
+        key = (name, index, sizes)
+        n = _sizes.get(key)
+        if n is None:
+            c = ctypes.c_size_t(0)
+            _check(getattr(_lib.load(), name)(fmt.pack(*args, 0, 0, *tail), ctypes.byref(c)), name)
+            if len(_sizes) >= 4096:
+                _sizes.clear()
+            n = _sizes[key] = c.value
+        if n == 0:
             return 0, 0, None
-        workspace = torch.empty(n.value, dtype=_U8, device=device)
+        workspace = torch.empty(n, dtype=_U8, device=device)
+        return workspace.data_ptr(), n, workspace
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
@@ -150,7 +160,7 @@ def kda_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
     io, dtype = _io(x, "x"), x.dtype
     xs, w, b = _rows(x, M, C, dtype, "x"), _dense(weight, (C,), _F32, "weight"), _dense(bias, (C,), _F32, "bias")
     ys = C if y is None else _rows(y, M, C, dtype, "y")
-    index = _device(x, weight=weight, bias=bias, y=y)
+    index = _device(x, weight, bias, y)
     if y is None:
         y = torch.empty((M, C), dtype=dtype, device=x.device)
     stats = torch.empty((M, 2), dtype=_F32, device=x.device) if return_stats else None
@@ -179,19 +189,18 @@ def kda_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tens
         xs, xp = C, _dense(x, (M, C), _U8, "x (8-bit codes)")
         sp = _dense(x_scales, (M, -(-C // _BLOCK)), _U8, "x_scales")
     st, w = _dense(stats, (M, 2), _F32, "stats"), _dense(weight, (C,), _F32, "weight")
-    index = _device(dy, x=x, stats=stats, weight=weight, x_scales=x_scales, workspace=workspace)
+    index = _device(dy, x, stats, weight, x_scales, workspace)
     res = {"dx": torch.empty((M, C), dtype=dtype, device=dev)}
     dw = db = 0
     if param_grads:
-        both = torch.empty((2, C), dtype=_F32, device=dev)
-        res["dweight"], res["dbias"] = both.unbind(0)
-        dw = both.data_ptr()
-        db = dw + 4 * C
+        res["dweight"] = gw = torch.empty((C,), dtype=_F32, device=dev)
+        res["dbias"] = gb = torch.empty((C,), dtype=_F32, device=dev)
+        dw, db = gw.data_ptr(), gb.data_ptr()
     args = (M, C, io, dy.data_ptr(), dys, xp, xs, sp, st, w, res["dx"].data_ptr(), C, dw, db)
     p, n, keep = 0, 0, None
     if param_grads:
-        p, n, keep = _workspace(lib.kda_layer_norm_backward_workspace_size, _NORM_BWD.pack(*args, 0, 0),
-                                "kda_layer_norm_backward_workspace_size", workspace, dev)
+        p, n, keep = _workspace("kda_layer_norm_backward_workspace_size", index, (M, C, io), _NORM_BWD, args, (),
+                                workspace, dev)
     _check(lib.kda_layer_norm_backward(_NORM_BWD.pack(*args, p, n), _stream_of(index)), "kda_layer_norm_backward")
     return res
 
@@ -230,7 +239,7 @@ def kda_unpack8(codes: torch.Tensor, scales: torch.Tensor, *, dtype=torch.bfloat
         dtype = out.dtype
         _io(out, "out")
     xs = C if out is None else _rows(out, M, C, dtype, "out")
-    index = _device(codes, scales=scales, out=out)
+    index = _device(codes, scales, out)
     if out is None:
         out = torch.empty((M, C), dtype=dtype, device=codes.device)
     _check(lib.kda_unpack8(cp, sp, M, C, out.data_ptr(), xs, _DT[dtype], _stream_of(index)), "kda_unpack8")
@@ -262,9 +271,9 @@ def kda_ssm_conv(x: torch.Tensor, w: torch.Tensor, cu_seqlens, *, bias: Optional
     io, dtype, dev = _io(x, "x"), x.dtype, x.device
     xs, wp, bp = _rows(x, T, C, dtype, "x"), _dense(_need(w, "w"), (C, 4), _F32, "w"), _dense(bias, (C,), _F32, "bias")
     ys = C if y is None else _rows(y, T, C, dtype, "y")
-    index = _device(x, w=w, bias=bias, conv_state_in=conv_state_in, conv_state_out=conv_state_out, y=y, d_status=d_status)
+    index = _device(x, w, bias, conv_state_in, conv_state_out, y, d_status)
     cu, host, N = _packed_cu(cu_seqlens, dev)
-    _device(x, cu_seqlens=cu)
+    _device(x, cu)
     if conv_state_out is None and output_conv_state:
         conv_state_out = torch.empty((N, C, 3), dtype=dtype, device=dev)
     si = _dense(conv_state_in, (N, C, 3), dtype, "conv_state_in")
@@ -290,7 +299,7 @@ def kda_ssm_conv_step(x: torch.Tensor, w: torch.Tensor, conv_state: torch.Tensor
     xs, wp, bp = _rows(x, N, C, dtype, "x"), _dense(_need(w, "w"), (C, 4), _F32, "w"), _dense(bias, (C,), _F32, "bias")
     sp = _dense(_need(conv_state, "conv_state"), (N, C, 3), dtype, "conv_state")
     ys = C if y is None else _rows(y, N, C, dtype, "y")
-    index = _device(x, w=w, conv_state=conv_state, bias=bias, y=y)
+    index = _device(x, w, conv_state, bias, y)
     if y is None:
         y = torch.empty((N, C), dtype=dtype, device=x.device)
     a = _CONV.pack(N, C, 0, io, bool(silu), 0, 0, x.data_ptr(), xs, wp, bp, 0, sp, y.data_ptr(), ys, 0)
@@ -313,9 +322,9 @@ def kda_ssm_conv_backward(x: torch.Tensor, w: torch.Tensor, cu_seqlens, dy: torc
     io, dtype, dev = _io(x, "x"), x.dtype, x.device
     xs, wp, bp = _rows(x, T, C, dtype, "x"), _dense(_need(w, "w"), (C, 4), _F32, "w"), _dense(bias, (C,), _F32, "bias")
     dys = _rows(dy, T, C, dtype, "dy")
-    index = _device(x, w=w, dy=dy, bias=bias, conv_state_in=conv_state_in, workspace=workspace, d_status=d_status)
+    index = _device(x, w, dy, bias, conv_state_in, workspace, d_status)
     cu, host, N = _packed_cu(cu_seqlens, dev)
-    _device(x, cu_seqlens=cu)
+    _device(x, cu)
     si = _dense(conv_state_in, (N, C, 3), dtype, "conv_state_in")
     res = {"dx": torch.empty((T, C), dtype=dtype, device=dev), "dw": torch.empty((C, 4), dtype=_F32, device=dev)}
     if bias is not None:
@@ -325,8 +334,7 @@ def kda_ssm_conv_backward(x: torch.Tensor, w: torch.Tensor, cu_seqlens, dy: torc
     args = (N, C, T, io, bool(silu), cu.data_ptr(), host.ctypes.data if check_cu_on_host else 0, x.data_ptr(), xs, wp, bp,
             si, 0, 0, 0, _ptr(d_status), dy.data_ptr(), dys, res["dx"].data_ptr(), C, res["dw"].data_ptr(),
             _ptr(res.get("dbias")), _ptr(res.get("dconv_state_in")))
-    p, n, keep = _workspace(lib.kda_ssm_conv_backward_workspace_size, _CONV_BWD.pack(*args, 0, 0),
-                            "kda_ssm_conv_backward_workspace_size", workspace, dev)
+    p, n, keep = _workspace("kda_ssm_conv_backward_workspace_size", index, (T, C, io), _CONV_BWD, args, (), workspace, dev)
     _check(lib.kda_ssm_conv_backward(_CONV_BWD.pack(*args, p, n), _stream_of(index)), "kda_ssm_conv_backward")
     return res
 
@@ -379,10 +387,10 @@ def kda_ssm_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Te
     lib = _lib.load()
     T, Ch, N, G, io, dtype, vals = _ssm_inputs(u, dt, A, B, C, D, z, dt_bias)
     ys, dev = Ch if y is None else _rows(y, T, Ch, dtype, "y"), u.device
-    index = _device(u, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias, initial_state=initial_state,
-                    final_state=final_state, y=y, workspace=workspace, d_status=d_status)
+    index = _device(u, dt, A, B, C, D, z, dt_bias, initial_state,
+                    final_state, y, workspace, d_status)
     cu, host, n = _packed_cu(cu_seqlens, dev)
-    _device(u, cu_seqlens=cu)
+    _device(u, cu)
     ip = _dense(initial_state, (n, Ch, N), _F32, "initial_state")
     if final_state is None and output_final_state:
         final_state = torch.empty((n, Ch, N), dtype=_F32, device=dev)
@@ -392,8 +400,7 @@ def kda_ssm_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Te
     args = (n, Ch, N, G, T, io, bool(softplus), cu.data_ptr(), host.ctypes.data if check_cu_on_host else 0, *vals, ip, fp,
             y.data_ptr(), ys)
     status = _ptr(d_status)
-    p, size, keep = _workspace(lib.kda_ssm_scan_workspace_size, _SSM.pack(*args, 0, 0, status),
-                               "kda_ssm_scan_workspace_size", workspace, dev)
+    p, size, keep = _workspace("kda_ssm_scan_workspace_size", index, (T, Ch, N, G, io), _SSM, args, (status,), workspace, dev)
     _check(lib.kda_ssm_scan(_SSM.pack(*args, p, size, status), _stream_of(index)), "kda_ssm_scan")
     return y, final_state
 
@@ -411,7 +418,7 @@ def kda_ssm_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Te
     n, Ch, N, G, io, dtype, vals = _ssm_inputs(u, dt, A, B, C, D, z, dt_bias)
     sp = _dense(_need(state, "state"), (n, Ch, N), _F32, "state")
     ys = Ch if y is None else _rows(y, n, Ch, dtype, "y")
-    index = _device(u, dt=dt, A=A, B=B, C=C, state=state, D=D, z=z, dt_bias=dt_bias, y=y)
+    index = _device(u, dt, A, B, C, state, D, z, dt_bias, y)
     if y is None:
         y = torch.empty((n, Ch), dtype=dtype, device=u.device)
     a = _SSM.pack(n, Ch, N, G, 0, io, bool(softplus), 0, 0, *vals, 0, sp, y.data_ptr(), ys, 0, 0, 0)
@@ -437,10 +444,10 @@ def kda_ssm_backward(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torc
     lib = _lib.load()
     T, Ch, N, G, io, dtype, vals = _ssm_inputs(u, dt, A, B, C, D, z, dt_bias)
     dys, dev = _rows(dy, T, Ch, dtype, "dy"), u.device
-    index = _device(u, dt=dt, A=A, B=B, C=C, dy=dy, D=D, z=z, dt_bias=dt_bias, initial_state=initial_state,
-                    d_final_state=d_final_state, workspace=workspace, d_status=d_status)
+    index = _device(u, dt, A, B, C, dy, D, z, dt_bias, initial_state,
+                    d_final_state, workspace, d_status)
     cu, host, n = _packed_cu(cu_seqlens, dev)
-    _device(u, cu_seqlens=cu)
+    _device(u, cu)
     ip = _dense(initial_state, (n, Ch, N), _F32, "initial_state")
     dfp = _dense(d_final_state, (n, Ch, N), _F32, "d_final_state")
 
@@ -462,8 +469,7 @@ def kda_ssm_backward(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torc
     args = (n, Ch, N, G, T, io, bool(softplus), cu.data_ptr(), host.ctypes.data if check_cu_on_host else 0, *vals, ip, 0,
             0, 0, 0, 0, _ptr(d_status), dy.data_ptr(), dys, dfp,
             *(_ptr(res.get(k)) for k in ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dinitial_state")))
-    p, size, keep = _workspace(lib.kda_ssm_backward_workspace_size, _SSM_BWD.pack(*args, 0, 0),
-                               "kda_ssm_backward_workspace_size", workspace, dev)
+    p, size, keep = _workspace("kda_ssm_backward_workspace_size", index, (T, Ch, N, G, io), _SSM_BWD, args, (), workspace, dev)
     _check(lib.kda_ssm_backward(_SSM_BWD.pack(*args, p, size), _stream_of(index)), "kda_ssm_backward")
     return res
 

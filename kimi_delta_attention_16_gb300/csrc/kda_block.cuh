@@ -10,7 +10,7 @@ namespace kda {
 // W consecutive elements of a row as they lie in memory: W * sizeof(T) bytes, 16 when the layout
 // allows vectors, one element otherwise.  load() only moves bytes, so several can be in flight
 // before the first conversion.
-template <typename T, int W> struct Raw {
+template <typename T, int W> struct alignas(W * sizeof(T)) Raw {
     static constexpr int kBytes = W * (int)sizeof(T);
     static_assert(kBytes == 16 || kBytes == 8 || kBytes == 4 || kBytes == 2 || kBytes == 1, "access width");
     uint32_t w[kBytes >= 4 ? kBytes / 4 : 1];
@@ -49,6 +49,13 @@ template <int W> __device__ __forceinline__ void unraw(const Raw<bf16, W>& r, fl
         }
     }
 }
+// The same as fp32 pairs (W even).
+template <typename T, int W> __device__ __forceinline__ void unraw2(const Raw<T, W>& r, f2 (&v)[W / 2]) {
+    float t[W];
+    unraw(r, t);
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) v[i] = f2_of(t[2 * i], t[2 * i + 1]);
+}
 template <int W> __device__ __forceinline__ void store_row(float* p, const float (&v)[W]) {
     if constexpr (W == 4) {
         *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
@@ -79,6 +86,24 @@ template <int W> __device__ __forceinline__ void load_param(const float* p, floa
     }
 }
 
+// ------------------------------------------------------------------ asynchronous copies to shared memory
+// 16 bytes, of which the first `bytes` are read and the rest filled with zeros.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// All W elements of an access (4, 8 or 16 bytes).
+template <typename T, int W> __device__ __forceinline__ void cp_async_raw(Raw<T, W>* dst, const T* src) {
+    constexpr int n = Raw<T, W>::kBytes;
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    if constexpr (n == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(n) : "memory");
+}
+
 // ------------------------------------------------------------------ e4m3 in blocks of 32
 // Byte s stands for 2^(s - 127), s >= 1 (a normal fp32 number).
 __device__ __forceinline__ float scale_of_byte(uint32_t s) { return __uint_as_float(s << 23); }
@@ -90,19 +115,20 @@ __device__ __forceinline__ void e4m3x2_to_f(uint32_t two, float& lo, float& hi) 
     asm("{.reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}"
         : "=f"(lo), "=f"(hi) : "r"(h));
 }
-template <int W> __device__ __forceinline__ void unraw8(const Raw<uint8_t, W>& r, float scale, float (&v)[W]) {
+template <int W> __device__ __forceinline__ void unraw(const Raw<uint8_t, W>& r, float (&v)[W]) {  // codes, unscaled
     if constexpr (W == 1) {
         float unused;
         e4m3x2_to_f(r.w[0] & 0xffu, v[0], unused);
-        v[0] *= scale;
     } else {
 #pragma unroll
-        for (int i = 0; i < W / 2; ++i) {
+        for (int i = 0; i < W / 2; ++i)
             e4m3x2_to_f((r.w[i / 2] >> (16 * (i & 1))) & 0xffffu, v[2 * i], v[2 * i + 1]);
-            v[2 * i] *= scale;
-            v[2 * i + 1] *= scale;
-        }
     }
+}
+template <int W> __device__ __forceinline__ void unraw8(const Raw<uint8_t, W>& r, float scale, float (&v)[W]) {
+    unraw(r, v);
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] *= scale;
 }
 
 // ------------------------------------------------------------------ sums in a fixed order

@@ -160,8 +160,9 @@ kda_status kda_layer_norm(const kda_norm_args* a, kda_stream_t stream) {
     const size_t es = dsize(a->io);
     const int64_t xs = a->x_stride ? a->x_stride : a->C, ys = a->y_stride ? a->y_stride : a->C;
     if ((st = check_plain_rows(a->x, a->M, xs, a->C, es, "x")) || (st = check_plain_rows(a->y, a->M, ys, a->C, es, "y")) ||
-        (st = check_f32(a->weight, "weight")) || (st = check_f32(a->bias, "bias")) || (st = check_f32(a->stats, "stats")))
+        (st = check_f32(a->weight, "weight")) || (st = check_f32(a->bias, "bias")))
         return st;
+    if (!aligned(a->stats, 8)) return fail(KDA_ERR_INVALID_ARG, "stats is not 8-byte aligned");
     const size_t cb = (size_t)a->C * 4;
     const Span outs[] = {{a->y, rows_bytes(a->M, ys, a->C, es), "y"}, {a->stats, (size_t)a->M * 8, "stats"}};
     const Span ins[] = {{a->x, rows_bytes(a->M, xs, a->C, es), "x"}, {a->weight, cb, "weight"}, {a->bias, cb, "bias"}};
@@ -201,7 +202,7 @@ kda_status kda_layer_norm_backward(const kda_norm_backward_args* a, kda_stream_t
         (st = check_plain_rows(a->dx, a->M, dxs, a->C, es, "dx")))
         return st;
     if (!a->stats) return fail(KDA_ERR_INVALID_ARG, "stats is NULL");
-    if ((st = check_f32(a->stats, "stats"))) return st;
+    if (!aligned(a->stats, 8)) return fail(KDA_ERR_INVALID_ARG, "stats is not 8-byte aligned");
     const NormBackwardPlan p = norm_backward_plan(*a);
     if ((st = check_workspace(a->workspace, a->workspace_bytes, p.workspace))) return st;
     const Span outs[] = {{a->dx, rows_bytes(a->M, dxs, a->C, es), "dx"}, {a->dweight, cb, "dweight"},

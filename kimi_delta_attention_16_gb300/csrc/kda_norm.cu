@@ -18,25 +18,40 @@ namespace {
 
 constexpr int kMaxWarps = 32;
 
-// Sum over the block; every thread gets it.  `buf` is written and read once: a caller that comes
-// back to the same buffer has passed another barrier in between.
-template <int K> __device__ __forceinline__ void block_sum(float (&v)[K], float (*buf)[K]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+// Sum over the block of one or two values; every thread gets it.  Two values share the shuffles: the
+// first exchange leaves one of them in each half of the warp.  `buf` is written and read once: a caller
+// that comes back to the same buffer has passed another barrier in between.
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ float warp_sum2(float a, float b) {  // a's sum in the lower half, b's in the upper
+    const bool up = threadIdx.x & 16;
+    float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ void block_sum(float (&v)[1], float (*buf)[1]) {
+    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    v[0] = warp_sum(v[0]);
     if (nw == 1) return;
-    if (lane == 0)
-#pragma unroll
-        for (int k = 0; k < K; ++k) buf[warp][k] = v[k];
+    if (lane == 0) buf[threadIdx.x >> 5][0] = v[0];
     __syncthreads();
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        v[k] = lane < nw ? buf[lane][k] : 0.f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    v[0] = warp_sum(lane < nw ? buf[lane][0] : 0.f);
+}
+__device__ __forceinline__ void block_sum(float (&v)[2], float (*buf)[2]) {
+    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    float s = warp_sum2(v[0], v[1]);
+    if (nw > 1) {
+        if ((lane & 15) == 0) buf[threadIdx.x >> 5][lane >> 4] = s;
+        __syncthreads();
+        const float2 t = lane < nw ? *reinterpret_cast<const float2*>(buf[lane]) : make_float2(0.f, 0.f);
+        s = warp_sum2(t.x, t.y);
     }
+    v[0] = __shfl_sync(0xffffffffu, s, 0);
+    v[1] = __shfl_sync(0xffffffffu, s, 16);
 }
 
 // Column of access i of this thread (in elements): consecutive threads take consecutive accesses.
@@ -100,6 +115,145 @@ k_layer_norm(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, c
     }
 }
 
+// ------------------------------------------------------------------ many rows
+// Persistent blocks that take R rows at a time, with kDepth - 1 groups of them on their way to shared
+// memory.  A thread copies and reads its own columns only, so no barrier guards the ring.  R = 2 rows
+// share the shuffles and barriers of their sums, and arithmetic runs on fp32 pairs.
+constexpr int kDepth = 3;
+
+// Sums of four values over a warp: lane 0 gets a's, 16 b's, 8 c's, 24 d's (six shuffles).
+__device__ __forceinline__ float warp_sum4(float a, float b, float c, float d) {
+    const bool hi = threadIdx.x & 16, hi8 = threadIdx.x & 8;
+    const float p = (hi ? b : a) + __shfl_xor_sync(0xffffffffu, hi ? a : b, 16);
+    const float q = (hi ? d : c) + __shfl_xor_sync(0xffffffffu, hi ? c : d, 16);
+    float v = (hi8 ? q : p) + __shfl_xor_sync(0xffffffffu, hi8 ? p : q, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ void block_sum4(float (&v)[4], float (*buf)[4]) {
+    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    float s = warp_sum4(v[0], v[1], v[2], v[3]);
+    if (nw > 1) {
+        if ((lane & 7) == 0) buf[threadIdx.x >> 5][((lane >> 4) & 1) + ((lane >> 2) & 2)] = s;
+        __syncthreads();
+        const float4 t = lane < nw ? *reinterpret_cast<const float4*>(buf[lane]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        s = warp_sum4(t.x, t.y, t.z, t.w);
+    }
+    v[0] = __shfl_sync(0xffffffffu, s, 0);
+    v[1] = __shfl_sync(0xffffffffu, s, 16);
+    v[2] = __shfl_sync(0xffffffffu, s, 8);
+    v[3] = __shfl_sync(0xffffffffu, s, 24);
+}
+__device__ __forceinline__ float f2_sum(f2 v) { return f2_lo(v) + f2_hi(v); }
+
+// Threads that a block of the row kernels may have: what leaves a thread the registers it needs.
+// Threads of a block of the row kernels: 72 registers for each leave two blocks to an SM.
+constexpr int kRowThreads = 448;
+__device__ __forceinline__ float rstd_of(float v) {  // 1 / sqrt(v): the hardware's value and one Newton step
+    const float r = rsqrtf(v);
+    return r * fmaf(-0.5f * v * r, r, 1.5f);
+}
+
+template <typename T, int W, int VPT, int R>
+__global__ void __launch_bounds__(kRowThreads, 2)
+k_layer_norm_rows(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const float* __restrict__ b, float eps,
+                  T* __restrict__ y, int64_t ys, float* __restrict__ stats, int64_t M, int C) {
+    constexpr int P = W / 2;
+    extern __shared__ __align__(16) unsigned char shared[];
+    Raw<T, W>* ring = reinterpret_cast<Raw<T, W>*>(shared) + threadIdx.x;  // [kDepth][R][VPT][blockDim.x]
+    __shared__ __align__(8) float red[2][kMaxWarps][2];
+    const float inv_c = 1.0f / (float)C;
+    f2 wv[VPT][P], bv[VPT][P];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = col_of<W>(i);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            wv[i][j] = w && c < C ? f2_of(w[c + 2 * j], w[c + 2 * j + 1]) : f2_dup(1.f);
+            bv[i][j] = b && c < C ? f2_of(b[c + 2 * j], b[c + 2 * j + 1]) : f2_dup(0.f);
+        }
+    }
+    auto issue = [&](int64_t r0, int slot) {  // rows r0, r0 + gridDim.x, ..
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t r = r0 + (int64_t)k * gridDim.x;
+            if (r < M)
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+                    const int c = col_of<W>(i);
+                    if (c < C) cp_async_raw<T, W>(ring + ((slot * R + k) * VPT + i) * blockDim.x, x + r * xs + c);
+                }
+        }
+        cp_commit();
+    };
+    const int64_t step = (int64_t)R * gridDim.x;
+#pragma unroll
+    for (int d = 0; d < kDepth - 1; ++d) issue(blockIdx.x + d * step, d);
+    int slot = 0;
+    for (int64_t r0 = blockIdx.x; r0 < M; r0 += step) {
+        cp_wait<kDepth - 2>();
+        // Each of the three passes reads the rows from the ring again: registers for them would halve the blocks.
+        float s[2] = {0.f, 0.f}, mean[2];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            f2 t = f2_dup(0.f);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                if (col_of<W>(i) < C) {
+                    f2 v[P];
+                    unraw2(ring[((slot * R + k) * VPT + i) * blockDim.x], v);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) t = add2(t, v[j]);
+                }
+            s[k] = f2_sum(t);
+        }
+        issue(r0 + (kDepth - 1) * step, (slot + kDepth - 1) % kDepth);
+        block_sum(s, red[0]);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            mean[k] = s[k] * inv_c;
+            f2 t = f2_dup(0.f);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                if (col_of<W>(i) < C) {
+                    f2 v[P];
+                    unraw2(ring[((slot * R + k) * VPT + i) * blockDim.x], v);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) {
+                        v[j] = add2(v[j], f2_dup(-mean[k]));
+                        t = fma2(v[j], v[j], t);
+                    }
+                }
+            s[k] = f2_sum(t);
+        }
+        block_sum(s, red[1]);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t r = r0 + (int64_t)k * gridDim.x;
+            if (r >= M) break;
+            const float rstd = rstd_of(fmaf(s[k], inv_c, eps));
+            if (stats && threadIdx.x == 0) *reinterpret_cast<float2*>(stats + 2 * r) = make_float2(mean[k], rstd);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = col_of<W>(i);
+                if (c >= C) continue;
+                f2 v[P];
+                unraw2(ring[((slot * R + k) * VPT + i) * blockDim.x], v);
+                float o[W];
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    const f2 n = fma2(mul2(add2(v[j], f2_dup(-mean[k])), f2_dup(rstd)), wv[i][j], bv[i][j]);
+                    o[2 * j] = f2_lo(n);
+                    o[2 * j + 1] = f2_hi(n);
+                }
+                store_row(y + r * ys + c, o);
+            }
+        }
+        slot = (slot + 1) % kDepth;
+    }
+}
+
 template <typename T, bool X8, int W, int VPT>
 __global__ void __launch_bounds__(1024)
 k_layer_norm_bwd(const T* __restrict__ dy, int64_t dys, const void* __restrict__ xv, int64_t xs,
@@ -108,7 +262,7 @@ k_layer_norm_bwd(const T* __restrict__ dy, int64_t dys, const void* __restrict__
     using XT = typename std::conditional<X8, uint8_t, T>::type;
     const XT* x = static_cast<const XT*>(xv);
     const int nb = (C + KDA_PACK8_BLOCK - 1) / KDA_PACK8_BLOCK;
-    __shared__ float red[2][kMaxWarps][2];
+    __shared__ __align__(8) float red[2][kMaxWarps][2];
     const float inv_c = 1.0f / (float)C;
     float wv[VPT][W], dw[VPT][W], db[VPT][W];
 #pragma unroll
@@ -188,6 +342,159 @@ k_layer_norm_bwd(const T* __restrict__ dy, int64_t dys, const void* __restrict__
     }
 }
 
+// The gradient of many rows in 16-byte layouts, as the forward takes them.
+template <typename T, bool X8, int W, int VPT, int R>
+__global__ void __launch_bounds__(kRowThreads, 2)
+k_layer_norm_bwd_rows(const T* __restrict__ dy, int64_t dys, const void* __restrict__ xv, int64_t xs,
+                      const uint8_t* __restrict__ scales, const float* __restrict__ stats, const float* __restrict__ w,
+                      T* __restrict__ dx, int64_t dxs, float* __restrict__ part, int64_t M, int C) {
+    using XT = typename std::conditional<X8, uint8_t, T>::type;
+    constexpr int P = W / 2;
+    extern __shared__ __align__(16) unsigned char shared[];
+    Raw<T, W>* ring_y = reinterpret_cast<Raw<T, W>*>(shared) + threadIdx.x;  // [kDepth][R][VPT][blockDim.x], both
+    Raw<XT, W>* ring_x =
+        reinterpret_cast<Raw<XT, W>*>(shared + (size_t)kDepth * R * VPT * blockDim.x * sizeof(Raw<T, W>)) + threadIdx.x;
+    __shared__ __align__(16) float red[2][kMaxWarps][4];
+    const XT* x = static_cast<const XT*>(xv);
+    const int nb = (C + KDA_PACK8_BLOCK - 1) / KDA_PACK8_BLOCK;
+    const float inv_c = 1.0f / (float)C;
+    f2 wv[VPT][P], dw[VPT][P], db[VPT][P];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = col_of<W>(i);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            dw[i][j] = db[i][j] = f2_dup(0.f);
+            wv[i][j] = w && c < C ? f2_of(w[c + 2 * j], w[c + 2 * j + 1]) : f2_dup(1.f);
+        }
+    }
+    auto issue = [&](int64_t r0, int slot) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t r = r0 + (int64_t)k * gridDim.x;
+            if (r < M)
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+                    const int c = col_of<W>(i), at = ((slot * R + k) * VPT + i) * blockDim.x;
+                    if (c < C) {
+                        cp_async_raw<XT, W>(ring_x + at, x + r * (X8 ? (int64_t)C : xs) + c);
+                        cp_async_raw<T, W>(ring_y + at, dy + r * dys + c);
+                    }
+                }
+        }
+        cp_commit();
+    };
+    uint32_t sr[R][VPT];
+    float2 st[R];
+    auto small = [&](int64_t r0) {  // what the next rows need besides: their statistics and their blocks' scales
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t r = r0 + (int64_t)k * gridDim.x;
+            st[k] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) sr[k][i] = 127;
+            if (r >= M) continue;
+            st[k] = __ldg(reinterpret_cast<const float2*>(stats + 2 * r));
+            if (X8)
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    if (col_of<W>(i) < C) sr[k][i] = (uint32_t)__ldg(scales + r * nb + col_of<W>(i) / KDA_PACK8_BLOCK);
+        }
+    };
+    const int64_t step = (int64_t)R * gridDim.x;
+#pragma unroll
+    for (int d = 0; d < kDepth - 1; ++d) issue(blockIdx.x + d * step, d);
+    small(blockIdx.x);
+    int slot = 0, buf = 0;
+    for (int64_t r0 = blockIdx.x; r0 < M; r0 += step) {
+        cp_wait<kDepth - 2>();
+        float2 at_st[R];
+        uint32_t at_sr[R][VPT];
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        // xh and dy weight of one access, from the ring: read once for the sums and once for dx, since registers for
+        // them would halve the blocks.
+        auto terms = [&](int k, int i, f2 (&xh)[P], f2 (&d)[P]) {
+            const int at = ((slot * R + k) * VPT + i) * blockDim.x;
+            unraw2(ring_x[at], xh);
+            unraw2(ring_y[at], d);
+            const f2 shift = f2_dup(-at_st[k].x * at_st[k].y);
+            const f2 m = f2_dup(X8 ? scale_of_byte(at_sr[k][i]) * at_st[k].y : at_st[k].y);
+#pragma unroll
+            for (int j = 0; j < P; ++j) xh[j] = fma2(xh[j], m, shift);
+        };
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            at_st[k] = st[k];
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) at_sr[k][i] = sr[k][i];
+            if (r0 + (int64_t)k * gridDim.x >= M) continue;  // its slot holds no row
+            f2 a = f2_dup(0.f), b = f2_dup(0.f);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                if (col_of<W>(i) >= C) continue;
+                f2 xh[P], d[P];
+                terms(k, i, xh, d);
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    dw[i][j] = fma2(d[j], xh[j], dw[i][j]);
+                    db[i][j] = add2(db[i][j], d[j]);
+                    d[j] = mul2(d[j], wv[i][j]);
+                    a = add2(a, d[j]);
+                    b = fma2(d[j], xh[j], b);
+                }
+            }
+            s[2 * k] = f2_sum(a);
+            s[2 * k + 1] = f2_sum(b);
+        }
+        issue(r0 + (kDepth - 1) * step, (slot + kDepth - 1) % kDepth);
+        small(r0 + step);
+        if constexpr (R == 1) {
+            float t[2] = {s[0], s[1]};
+            block_sum(t, reinterpret_cast<float(*)[2]>(red[buf]));
+            s[0] = t[0];
+            s[1] = t[1];
+        } else {
+            block_sum4(s, red[buf]);
+        }
+        buf ^= 1;
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t r = r0 + (int64_t)k * gridDim.x;
+            if (r >= M) break;
+            const float rs = at_st[k].y;
+            const f2 m0 = f2_dup(-s[2 * k] * inv_c * rs), m1 = f2_dup(-s[2 * k + 1] * inv_c * rs), rr = f2_dup(rs);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = col_of<W>(i);
+                if (c >= C) continue;
+                f2 xh[P], d[P];
+                terms(k, i, xh, d);
+                float o[W];
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    const f2 v = fma2(rr, mul2(d[j], wv[i][j]), fma2(xh[j], m1, m0));
+                    o[2 * j] = f2_lo(v);
+                    o[2 * j + 1] = f2_hi(v);
+                }
+                store_row(dx + r * dxs + c, o);
+            }
+        }
+        slot = (slot + 1) % kDepth;
+    }
+    if (!part) return;
+    float* pw = part + (int64_t)blockIdx.x * 2 * C;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = col_of<W>(i);
+        if (c >= C) continue;
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            *reinterpret_cast<float2*>(pw + c + 2 * j) = make_float2(f2_lo(dw[i][j]), f2_hi(dw[i][j]));
+            *reinterpret_cast<float2*>(pw + C + c + 2 * j) = make_float2(f2_lo(db[i][j]), f2_hi(db[i][j]));
+        }
+    }
+}
+
 struct PutParams {  // column c of [dw | db]
     float *dw, *db;
     int C;
@@ -223,6 +530,30 @@ cudaError_t launch_layer_norm(const kda_norm_args& a, cudaStream_t s) {
     const int64_t n = vec ? a.C / vw : a.C;
     const int vpt = accesses(n, 512, vec ? 16 : 32);
     const int nt = warps32((n + vpt - 1) / vpt);
+    // Rows through shared memory once every SM has several of them to take in turn (the ring needs rows to
+    // come): 8,192 x 7,168 bf16.  Fewer rows go one per block.
+    DeviceInfo di{0, 0, 0};
+    const int sms = current_device_info(&di) ? di.sm_count : 1;
+    if (vec && n <= 2 * kRowThreads) {
+        const int row_v = n <= kRowThreads / 2 ? 1 : 2;
+        const int rt = warps32((n + row_v - 1) / row_v);
+        const size_t smem = (size_t)kDepth * 2 * row_v * rt * 16;
+        const int per_sm = 2 * kRowThreads / rt;
+        if (a.M >= 4 * (int64_t)sms * per_sm) {
+            cudaError_t e = cudaSuccess;
+#define KDA_LNR(T, W, V)                                                                                             \
+    if (!(e = cudaFuncSetAttribute(k_layer_norm_rows<T, W, V, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))) \
+        k_layer_norm_rows<T, W, V, 2><<<sms * per_sm, rt, smem, s>>>(static_cast<const T*>(a.x), xs, a.weight, a.bias, \
+                                                                  a.eps, static_cast<T*>(a.y), ys, a.stats, a.M, a.C)
+            if (a.io == KDA_BF16) {
+                if (row_v == 1) { KDA_LNR(bf16, 8, 1); } else { KDA_LNR(bf16, 8, 2); }
+            } else {
+                if (row_v == 1) { KDA_LNR(float, 4, 1); } else { KDA_LNR(float, 4, 2); }
+            }
+#undef KDA_LNR
+            return e ? e : cudaGetLastError();
+        }
+    }
     const unsigned grid = (unsigned)(a.M < 0x7fffffff ? a.M : 0x7fffffff);
 #define KDA_LN(T, W, V)                                                                                       \
     k_layer_norm<T, W, V><<<grid, nt, 0, s>>>(static_cast<const T*>(a.x), xs, a.weight, a.bias, a.eps,         \
@@ -268,8 +599,11 @@ NormBackwardPlan norm_backward_plan(const kda_norm_backward_args& a) {
     NormBackwardPlan p{0, 0};
     DeviceInfo di{0, 0, 0};
     const int sms = current_device_info(&di) ? di.sm_count : 1;
-    const int nt = warps32(a.C < 1024 ? a.C : 1024);  // an upper bound on the threads of any layout
-    int per_sm = 1024 / nt;
+    // Blocks that fill an SM's threads when the layout allows 16-byte accesses (known only once the
+    // pointers are; the sizes alone have to fix the workspace).
+    const int vw = a.io == KDA_BF16 ? 8 : 4, acc = (a.C + vw - 1) / vw;
+    const int nt = warps32(acc <= kRowThreads / 2 ? acc : (acc + 1) / 2);
+    int per_sm = nt <= kRowThreads ? 2 * kRowThreads / nt : 1;
     if (per_sm > 8) per_sm = 8;
     const int64_t most = (int64_t)sms * per_sm;
     p.blocks = (int)(a.M < most ? a.M : most);
@@ -282,6 +616,31 @@ cudaError_t launch_layer_norm_backward(const kda_norm_backward_args& a, const No
     const int64_t dys = a.dy_stride ? a.dy_stride : a.C, dxs = a.dx_stride ? a.dx_stride : a.C;
     const int64_t xs = a.x_stride ? a.x_stride : a.C;
     float* part = p.workspace ? static_cast<float*>(a.workspace) : nullptr;
+    cudaError_t e = cudaSuccess;
+    const int es = a.io == KDA_BF16 ? 2 : 4;
+    const int acc = a.C / (16 / es);  // accesses per row, where the layout is wide
+    if (h.vec && acc <= 2 * kRowThreads) {
+        const int v = acc <= kRowThreads / 2 ? 1 : 2, rows = 3 - v, nt = warps32((acc + v - 1) / v);
+        const size_t smem = (size_t)kDepth * rows * v * nt * (16 + (a.x_scales ? 16 / es : 16));
+#define KDA_LNBR(T, X8, W, V)                                                                                        \
+    if (!(e = cudaFuncSetAttribute(k_layer_norm_bwd_rows<T, X8, W, V, 3 - V>,                                        \
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))                         \
+        k_layer_norm_bwd_rows<T, X8, W, V, 3 - V><<<p.blocks, nt, smem, s>>>(static_cast<const T*>(a.dy), dys, a.x, xs, \
+                                                                      a.x_scales, a.stats, a.weight,                 \
+                                                                      static_cast<T*>(a.dx), dxs, part, a.M, a.C)
+#define KDA_LNBR_X(T, W)                                                                                             \
+    if (a.x_scales) {                                                                                                \
+        if (v == 1) { KDA_LNBR(T, true, W, 1); } else { KDA_LNBR(T, true, W, 2); }                                   \
+    } else {                                                                                                         \
+        if (v == 1) { KDA_LNBR(T, false, W, 1); } else { KDA_LNBR(T, false, W, 2); }                                 \
+    }
+        if (a.io == KDA_BF16) { KDA_LNBR_X(bf16, 8) } else { KDA_LNBR_X(float, 4) }
+#undef KDA_LNBR_X
+#undef KDA_LNBR
+        if (!e) e = cudaGetLastError();
+        if (e || !part) return e;
+        return launch_column_sum(part, p.blocks, 2 * (int64_t)a.C, PutParams{a.dweight, a.dbias, a.C}, s);
+    }
 #define KDA_LNB(T, X8, W, V)                                                                                   \
     k_layer_norm_bwd<T, X8, W, V><<<p.blocks, h.nt, 0, s>>>(static_cast<const T*>(a.dy), dys, a.x, xs,          \
                                                             a.x_scales, a.stats, a.weight,                      \
@@ -304,7 +663,7 @@ cudaError_t launch_layer_norm_backward(const kda_norm_backward_args& a, const No
 #undef KDA_LNB_X
 #undef KDA_LNB_V
 #undef KDA_LNB
-    cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     if (e || !part) return e;
     return launch_column_sum(part, p.blocks, 2 * (int64_t)a.C, PutParams{a.dweight, a.dbias, a.C}, s);
 }

@@ -82,13 +82,6 @@ template <int NS> struct Lay {
 // kDepth tiles of TT rows x W elements in flight: asynchronous 16-byte copies where base, stride and
 // first column allow them (the last piece of a row may be short: it is filled with zeros), plain
 // element copies otherwise.  `rows_left`: rows of the tile that exist; the others keep old contents.
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
-    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // One tile: rows [0, rows) of `src` (already at the tile's first row and the block's first column), W
 // columns of which `cols` exist, into dst[TT][W].
 template <typename T, int TT, int W, int NT>

@@ -43,7 +43,7 @@ def norm(**kw):
     (dict(M=-1), INVALID), (dict(C=0), INVALID), (dict(C=32769), UNSUPPORTED), (dict(io=2), INVALID),
     (dict(x=None), INVALID), (dict(y=None), INVALID), (dict(x=at(0, 1)), INVALID), (dict(x_stride=99), INVALID),
     (dict(y_stride=-100), INVALID), (dict(weight=at(1, 2)), INVALID), (dict(y=at(0)), INVALID),
-    (dict(y=at(0, 700)), INVALID), (dict(stats=at(3, 8)), INVALID), (dict(y=at(1)), INVALID),
+    (dict(y=at(0, 700)), INVALID), (dict(stats=at(3, 8)), INVALID), (dict(stats=at(4, 4)), INVALID), (dict(y=at(1)), INVALID),
     (dict(x_stride=1 << 58, M=4), UNSUPPORTED)])
 def test_layer_norm_refusals(kw, code):
     assert call("kda_layer_norm", norm(**kw)) == code
@@ -59,7 +59,7 @@ def norm_bwd(**kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(M=-1), INVALID), (dict(C=40000), UNSUPPORTED), (dict(dy=None), INVALID), (dict(x=None), INVALID),
-    (dict(stats=None), INVALID), (dict(dx=None), INVALID), (dict(dx=at(0)), INVALID), (dict(dweight=at(6)), INVALID),
+    (dict(stats=None), INVALID), (dict(stats=at(2, 4)), INVALID), (dict(dx=None), INVALID), (dict(dx=at(0)), INVALID), (dict(dweight=at(6)), INVALID),
     (dict(workspace=None), WORKSPACE), (dict(workspace_bytes=16), WORKSPACE), (dict(workspace=at(8, 16)), WORKSPACE),
     (dict(workspace=at(2)), INVALID), (dict(x_scales=at(4)), INVALID), (dict(dy_stride=10), INVALID)])
 def test_layer_norm_backward_refusals(kw, code):
