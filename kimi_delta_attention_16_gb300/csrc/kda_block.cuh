@@ -67,8 +67,10 @@ template <int W> __device__ __forceinline__ void store_row(float* p, const float
 template <int W> __device__ __forceinline__ void store_row(bf16* p, const float (&v)[W]) {
     if constexpr (W == 8) {
         store8(p, v);
+    } else if constexpr (W == 4) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     } else {
-        static_assert(W == 1, "bf16 rows: 8 or 1 elements");
+        static_assert(W == 1, "bf16 rows: 8, 4 or 1 elements");
         *p = __float2bfloat16_rn(v[0]);
     }
 }

@@ -18,13 +18,31 @@ constexpr int kThreads = 256;
 constexpr int kElems = 8;  // elements per thread and row
 constexpr int kRows = 4;   // rows per thread
 
-// e of the block's finite maximum (exact: exponent and mantissa bits).
-__device__ __forceinline__ int block_exponent(float amax) {
-    if (!(amax > 0.f)) return -126;
-    int e;
-    const float f = frexpf(amax, &e);  // amax = f 2^e, f in [0.5, 1)
-    e = e - 9 + (f > 0.875f ? 1 : 0);  // 448 = 0.875 * 2^9
-    return e < -126 ? -126 : e;
+// The scale byte (e + 127) of a block whose largest finite magnitude has these fp32 bits: the exponent, one
+// more where the mantissa is above 1.75 (448 = 1.75 * 2^8), and never below that of 2^-126.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t bits) {
+    const int e = (int)((bits + 0x1fffffu) >> 23) - 8;
+    return e < 1 ? 1u : (uint32_t)e;
+}
+
+// Largest magnitude among a thread's elements, as fp32 bits (magnitudes order as integers), not finite
+// where an element is.
+template <int W, int K> __device__ __forceinline__ uint32_t abs_max(const Raw<float, W> (&r)[K]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+#pragma unroll
+        for (int j = 0; j < W; ++j) m = max(m, r[i].w[j] & 0x7fffffffu);
+    return m;
+}
+template <int W, int K> __device__ __forceinline__ uint32_t abs_max(const Raw<bf16, W> (&r)[K]) {
+    constexpr int kWords = W >= 2 ? W / 2 : 1;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) m = __vmaxu2(m, r[i].w[j] & 0x7fff7fffu);
+    return max(m << 16, m & 0xffff0000u);
 }
 
 // Two values (already divided by the block's power of two, at most 448 in magnitude) as codes; NaN and
@@ -53,39 +71,52 @@ __global__ void __launch_bounds__(kThreads) k_pack8(const T* __restrict__ x, int
                 if (r0 + q < M && i * W < n) raw[q][i].load(x + (r0 + q) * xs + c0 + i * W); else raw[q][i].zero();
 #pragma unroll
         for (int q = 0; q < kRows; ++q) {
-            float v[kElems], amax = 0.f;
+            float v[kElems];
 #pragma unroll
             for (int i = 0; i < kElems / W; ++i) {
                 float t[W];
                 unraw(raw[q][i], t);
 #pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    const float a = fabsf(t[j]);
-                    // infinities turn into NaN here, and a NaN never passes the comparison below
-                    v[i * W + j] = a <= 3.402823466e38f ? t[j] : __int_as_float(0x7fffffff);
-                    if (a <= 3.402823466e38f) amax = fmaxf(amax, a);
+                for (int j = 0; j < W; ++j) v[i * W + j] = t[j];
+            }
+            uint32_t amax = abs_max(raw[q]);
+            if (amax >= 0x7f800000u) {  // rare: infinities turn into NaN, and neither counts
+                amax = 0;
+#pragma unroll
+                for (int j = 0; j < kElems; ++j) {
+                    const uint32_t m = __float_as_uint(v[j]) & 0x7fffffffu;
+                    if (m >= 0x7f800000u) v[j] = __uint_as_float(0x7fffffffu); else amax = max(amax, m);
                 }
             }
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             const int64_t r = r0 + q;
             if (r >= M || n == 0) continue;
-            const int e = block_exponent(amax);
-            const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+            const uint32_t byte = scale_byte(amax);
+            const f2 inv = f2_dup(__uint_as_float((254u - byte) << 23));  // 2^-e
             uint32_t two[kElems / 2];
 #pragma unroll
-            for (int i = 0; i < kElems / 2; ++i) two[i] = to_e4m3x2(v[2 * i] * inv, v[2 * i + 1] * inv);
+            for (int i = 0; i < kElems / 2; ++i) {
+                const f2 s = mul2(f2_of(v[2 * i], v[2 * i + 1]), inv);
+                two[i] = to_e4m3x2(f2_lo(s), f2_hi(s));
+            }
             uint8_t* dst = codes + r * C + c0;
             if constexpr (VEC) {  // C is a multiple of W, so a row's codes start on a W-byte boundary
 #pragma unroll
-                for (int i = 0; i < kElems / 4; ++i)
-                    if (i * 4 < n) reinterpret_cast<uint32_t*>(dst)[i] = two[2 * i] | (two[2 * i + 1] << 16);
+                for (int i = 0; i < kElems / 4; ++i) two[i] = two[2 * i] | (two[2 * i + 1] << 16);
+                if constexpr (W == kElems) {
+                    *reinterpret_cast<uint2*>(dst) = make_uint2(two[0], two[1]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kElems / 4; ++i)
+                        if (i * 4 < n) reinterpret_cast<uint32_t*>(dst)[i] = two[i];
+                }
             } else {
 #pragma unroll
                 for (int i = 0; i < kElems; ++i)
                     if (i < n) dst[i] = (uint8_t)(two[i / 2] >> (8 * (i & 1)));
             }
-            if ((threadIdx.x & 3) == 0) scales[r * nb + c0 / KDA_PACK8_BLOCK] = (uint8_t)(e + 127);
+            if ((threadIdx.x & 3) == 0) scales[r * nb + c0 / KDA_PACK8_BLOCK] = (uint8_t)byte;
         }
     }
 }

@@ -17,7 +17,8 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;
+constexpr int kBatch = 4;  // tokens whose loads are in flight together
+constexpr int kWide = 4;   // channels per thread where the layout allows (8 bytes of bf16, 16 of fp32)
 
 __device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
@@ -35,6 +36,26 @@ __device__ __forceinline__ void place(const T* __restrict__ x, int64_t xs, const
     }
 }
 
+// W consecutive values of a state that the same kernel writes (no read-only cache).
+template <int W> __device__ __forceinline__ void load_state(const float* p, float (&v)[W]) {
+    if constexpr (W == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(p);
+        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+    } else {
+        v[0] = *p;
+    }
+}
+template <int W> __device__ __forceinline__ void load_state(const bf16* p, float (&v)[W]) {
+    Raw<bf16, W> r;
+    if constexpr (W == 4) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        r.w[0] = u.x; r.w[1] = u.y;
+    } else {
+        r.w[0] = *reinterpret_cast<const unsigned short*>(p);
+    }
+    unraw(r, v);
+}
+
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads)
 k_conv(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const float* __restrict__ bias, int silu,
@@ -47,9 +68,8 @@ k_conv(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const f
     float wt[4][W], bs[W], win[3][W];
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-        const float4 f = make_float4(w[(int64_t)(c + j) * 4], w[(int64_t)(c + j) * 4 + 1], w[(int64_t)(c + j) * 4 + 2],
-                                     w[(int64_t)(c + j) * 4 + 3]);
-        wt[0][j] = f.x; wt[1][j] = f.y; wt[2][j] = f.z; wt[3][j] = f.w;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) wt[k][j] = w[(int64_t)(c + j) * 4 + k];
         bs[j] = bias ? bias[c + j] : 0.f;
     }
     int n = seq_of(cu, N, t0);
@@ -57,15 +77,39 @@ k_conv(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const f
     seq_range(cu, n, T_total, s, e);
 #pragma unroll
     for (int m = 0; m < 3; ++m) place(x, xs, cs_in, s, t0 - s - 3 + m, n, C, c, win[m]);
+    const T* xp = x + t0 * xs + c;
+    T* yp = y + t0 * ys + c;
+    auto token = [&](const Raw<T, W>& raw) {
+        float v[W], o[W];
+        unraw(raw, v);
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            float a = fmaf(wt[0][j], win[0][j], bs[j]);
+            a = fmaf(wt[1][j], win[1][j], a);
+            a = fmaf(wt[2][j], win[2][j], a);
+            a = fmaf(wt[3][j], v[j], a);
+            o[j] = silu ? a * sigmoid_fast(a) : a;
+            win[0][j] = win[1][j];
+            win[1][j] = win[2][j];
+            win[2][j] = v[j];
+        }
+        store_row(yp, o);
+        yp += ys;
+    };
     for (int64_t tb = t0; tb < t1; tb += kBatch) {
         Raw<T, W> raw[kBatch];
+        if (tb + kBatch <= t1 && tb + kBatch < e) {  // no sequence ends here: tokens without a branch between them
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q)
-            if (tb + q < t1) raw[q].load(x + (tb + q) * xs + c); else raw[q].zero();
+            for (int q = 0; q < kBatch; ++q) {
+                raw[q].load(xp);
+                xp += xs;
+            }
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-            const int64_t t = tb + q;
-            if (t >= t1) break;
+            for (int q = 0; q < kBatch; ++q) token(raw[q]);
+            continue;
+        }
+#pragma unroll 1
+        for (int64_t t = tb; t < tb + kBatch && t < t1; ++t) {
             if (t >= e && n < N - 1) {  // crossed into a later sequence
                 while (t >= e && n < N - 1) {
                     ++n;
@@ -74,21 +118,9 @@ k_conv(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const f
 #pragma unroll
                 for (int m = 0; m < 3; ++m) place(x, xs, cs_in, s, t - s - 3 + m, n, C, c, win[m]);
             }
-            float v[W], o[W];
-            unraw(raw[q], v);
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                float a = bs[j];
-                a = fmaf(wt[0][j], win[0][j], a);
-                a = fmaf(wt[1][j], win[1][j], a);
-                a = fmaf(wt[2][j], win[2][j], a);
-                a = fmaf(wt[3][j], v[j], a);
-                o[j] = silu ? a * sigmoid_fast(a) : a;
-                win[0][j] = win[1][j];
-                win[1][j] = win[2][j];
-                win[2][j] = v[j];
-            }
-            store_row(y + t * ys + c, o);
+            raw[0].load(xp);
+            xp += xs;
+            token(raw[0]);
             if (cs_out && t == e - 1) {
 #pragma unroll
                 for (int j = 0; j < W; ++j)
@@ -100,26 +132,65 @@ k_conv(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const f
 }
 
 // One token per sequence: the three old values and the new one, the state rolled in place.  Its own
-// thread reads and writes a (sequence, channel)'s state.
-template <typename T>
+// thread reads and writes the state of W channels (3 W consecutive values: three accesses of W) and takes
+// several sequences in turn, kStepRows of them in flight at once.
+constexpr int kStepRows = 4;
+template <typename T, int W>
 __global__ void __launch_bounds__(kThreads)
 k_conv_step(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const float* __restrict__ bias, int silu,
-            int N, int C, T* __restrict__ cs, T* __restrict__ y, int64_t ys) {
-    const int c = blockIdx.x * kThreads + threadIdx.x;
+            int N, int C, T* cs, T* __restrict__ y, int64_t ys) {
+    const int c = (blockIdx.x * kThreads + threadIdx.x) * W;
     if (c >= C) return;
-    const float w0 = w[(int64_t)c * 4], w1 = w[(int64_t)c * 4 + 1], w2 = w[(int64_t)c * 4 + 2], w3 = w[(int64_t)c * 4 + 3];
-    const float b = bias ? bias[c] : 0.f;
-    for (int64_t n = blockIdx.y; n < N; n += gridDim.y) {
-        T* st = cs + (n * C + c) * 3;
-        const T s1 = st[1], s2 = st[2], xv = x[n * xs + c];
-        float a = fmaf(w0, to_f(st[0]), b);
-        a = fmaf(w1, to_f(s1), a);
-        a = fmaf(w2, to_f(s2), a);
-        a = fmaf(w3, to_f(xv), a);
-        y[n * ys + c] = from_f<T>(silu ? a * sigmoid_fast(a) : a);
-        st[0] = s1;
-        st[1] = s2;
-        st[2] = xv;
+    float wt[4][W], bs[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) wt[k][j] = w[(int64_t)(c + j) * 4 + k];
+        bs[j] = bias ? bias[c + j] : 0.f;
+    }
+    for (int64_t n0 = (int64_t)blockIdx.y * kStepRows; n0 < N; n0 += (int64_t)gridDim.y * kStepRows) {
+        float st[kStepRows][3 * W], xv[kStepRows][W];
+#pragma unroll
+        for (int q = 0; q < kStepRows; ++q) {
+            const int64_t n = n0 + q < N ? n0 + q : N - 1;
+            const T* p = cs + (n * C + c) * 3;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                float t[W];
+                load_state(p + k * W, t);
+#pragma unroll
+                for (int j = 0; j < W; ++j) st[q][k * W + j] = t[j];
+            }
+            Raw<T, W> r;
+            r.load(x + n * xs + c);
+            unraw(r, xv[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < kStepRows; ++q) {
+            const int64_t n = n0 + q;
+            if (n >= N) break;
+            float o[W], roll[3 * W];
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                float a = fmaf(wt[0][j], st[q][3 * j], bs[j]);
+                a = fmaf(wt[1][j], st[q][3 * j + 1], a);
+                a = fmaf(wt[2][j], st[q][3 * j + 2], a);
+                a = fmaf(wt[3][j], xv[q][j], a);
+                o[j] = silu ? a * sigmoid_fast(a) : a;
+                roll[3 * j] = st[q][3 * j + 1];
+                roll[3 * j + 1] = st[q][3 * j + 2];
+                roll[3 * j + 2] = xv[q][j];
+            }
+            store_row(y + n * ys + c, o);
+            T* p = cs + (n * C + c) * 3;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                float t[W];
+#pragma unroll
+                for (int j = 0; j < W; ++j) t[j] = roll[k * W + j];
+                store_row(p + k * W, t);
+            }
+        }
     }
 }
 
@@ -139,7 +210,7 @@ k_conv_bwd(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, con
         for (int j = 0; j < W; ++j) gw[k][j] = 0.f;
     if (c < C && t0 < T_total) {
         const int64_t t1 = t0 + run < T_total ? t0 + run : T_total;
-        float wt[4][W], bs[W], win[3][W], pend[3][W];
+        float wt[4][W], bs[W], win[3][W], pend[3][W], out[W];
 #pragma unroll
         for (int j = 0; j < W; ++j) {
 #pragma unroll
@@ -168,22 +239,69 @@ k_conv_bwd(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, con
         };
         const int64_t last = t1 + 3 < T_total ? t1 + 3 : T_total;
         bool open = true;  // the pending three still wait for tokens of their own sequence
-        for (int64_t tb = t0; tb < last && open; tb += kBatch) {
-            Raw<T, W> rx[kBatch], rd[kBatch];
+        auto slope = [&](float (&v)[W], float (&d)[W]) {  // dy of a token to dpre
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-                if (tb + q < last) {
-                    rx[q].load(x + (tb + q) * xs + c);
-                    rd[q].load(dy + (tb + q) * dys + c);
-                } else {
-                    rx[q].zero();
-                    rd[q].zero();
+            for (int j = 0; j < W; ++j) {
+                if (silu) {
+                    float a = fmaf(wt[0][j], win[0][j], bs[j]);
+                    a = fmaf(wt[1][j], win[1][j], a);
+                    a = fmaf(wt[2][j], win[2][j], a);
+                    a = fmaf(wt[3][j], v[j], a);
+                    const float sg = sigmoid_fast(a);
+                    d[j] *= sg * fmaf(a, 1.f - sg, 1.f);
                 }
             }
+        };
+        auto sums = [&](const float (&v)[W], const float (&d)[W]) {
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-                const int64_t t = tb + q;
-                if (t >= last || !open) break;
+            for (int j = 0; j < W; ++j) {
+                gw[0][j] = fmaf(d[j], win[0][j], gw[0][j]);
+                gw[1][j] = fmaf(d[j], win[1][j], gw[1][j]);
+                gw[2][j] = fmaf(d[j], win[2][j], gw[2][j]);
+                gw[3][j] = fmaf(d[j], v[j], gw[3][j]);
+                gw[4][j] += d[j];
+            }
+        };
+        auto move = [&](const float (&v)[W], const float (&d)[W]) {  // leaves the gradient of place t - 3 in `out`
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                win[0][j] = win[1][j];
+                win[1][j] = win[2][j];
+                win[2][j] = v[j];
+                out[j] = fmaf(wt[0][j], d[j], pend[0][j]);
+                pend[0][j] = fmaf(wt[1][j], d[j], pend[1][j]);
+                pend[1][j] = fmaf(wt[2][j], d[j], pend[2][j]);
+                pend[2][j] = wt[3][j] * d[j];
+            }
+        };
+        const T *xp = x + t0 * xs + c, *dp = dy + t0 * dys + c;
+        for (int64_t tb = t0; tb < last && open; tb += kBatch) {
+            Raw<T, W> rx[kBatch], rd[kBatch];
+            if (tb - 3 >= t0 && tb - 3 >= s && tb + kBatch <= t1 && tb + kBatch <= e) {
+                // own tokens only, and every finished place is one of them: no branch between the tokens
+                T* op = dx + (tb - 3) * dxs + c;
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q) {
+                    rx[q].load(xp);
+                    rd[q].load(dp);
+                    xp += xs;
+                    dp += dys;
+                }
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q) {
+                    float v[W], d[W];
+                    unraw(rx[q], v);
+                    unraw(rd[q], d);
+                    slope(v, d);
+                    sums(v, d);
+                    move(v, d);
+                    store_row(op, out);
+                    op += dxs;
+                }
+                continue;
+            }
+#pragma unroll 1
+            for (int64_t t = tb; t < tb + kBatch && t < last; ++t) {
                 if (t >= e && n < N - 1) {
                     flush(e);
                     if (t >= t1) {  // past this run's tokens and its last sequence
@@ -200,38 +318,16 @@ k_conv_bwd(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, con
                     for (int j = 0; j < W; ++j) pend[0][j] = pend[1][j] = pend[2][j] = 0.f;
                 }
                 float v[W], d[W];
-                unraw(rx[q], v);
-                unraw(rd[q], d);
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    if (silu) {
-                        float a = bs[j];
-                        a = fmaf(wt[0][j], win[0][j], a);
-                        a = fmaf(wt[1][j], win[1][j], a);
-                        a = fmaf(wt[2][j], win[2][j], a);
-                        a = fmaf(wt[3][j], v[j], a);
-                        const float sg = sigmoid_fast(a);
-                        d[j] *= sg * fmaf(a, 1.f - sg, 1.f);
-                    }
-                    if (t < t1) {
-                        gw[0][j] = fmaf(d[j], win[0][j], gw[0][j]);
-                        gw[1][j] = fmaf(d[j], win[1][j], gw[1][j]);
-                        gw[2][j] = fmaf(d[j], win[2][j], gw[2][j]);
-                        gw[3][j] = fmaf(d[j], v[j], gw[3][j]);
-                        gw[4][j] += d[j];
-                    }
-                    win[0][j] = win[1][j];
-                    win[1][j] = win[2][j];
-                    win[2][j] = v[j];
-                    pend[0][j] = fmaf(wt[0][j], d[j], pend[0][j]);
-                }
-                put(t - 3, pend[0]);
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    pend[0][j] = fmaf(wt[1][j], d[j], pend[1][j]);
-                    pend[1][j] = fmaf(wt[2][j], d[j], pend[2][j]);
-                    pend[2][j] = wt[3][j] * d[j];
-                }
+                rx[0].load(xp);
+                rd[0].load(dp);
+                xp += xs;
+                dp += dys;
+                unraw(rx[0], v);
+                unraw(rd[0], d);
+                slope(v, d);
+                if (t < t1) sums(v, d);
+                move(v, d);
+                put(t - 3, out);
             }
         }
         if (open && last == T_total) flush(T_total);
@@ -273,7 +369,7 @@ __global__ void k_empty_sequences(const int32_t* __restrict__ cu, int N, const u
 }
 
 bool wide(const void* p, int64_t stride, int es) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % (16 / es) == 0;
+    return reinterpret_cast<uintptr_t>(p) % (kWide * es) == 0 && stride % kWide == 0;
 }
 int64_t stride_or(int64_t s, int64_t d) { return s ? s : d; }
 
@@ -307,8 +403,8 @@ cudaError_t launch_empty_sequences(const int32_t* cu, int N, const void* src, vo
 cudaError_t launch_ssm_conv(const kda_ssm_conv_args& a, cudaStream_t s) {
     const int es = a.io == KDA_BF16 ? 2 : 4;
     const int64_t xs = stride_or(a.x_stride, a.C), ys = stride_or(a.y_stride, a.C);
-    const bool vec = a.C % (16 / es) == 0 && wide(a.x, xs, es) && wide(a.y, ys, es);
-    const int W = vec ? 16 / es : 1;
+    const bool vec = a.C % kWide == 0 && wide(a.x, xs, es) && wide(a.y, ys, es);
+    const int W = vec ? kWide : 1;
     const int acc = (a.C + W - 1) / W;
     const dim3 b(lanes_of(acc), kThreads / lanes_of(acc));
     const int run = run_of(a.T_total, acc);
@@ -318,7 +414,7 @@ cudaError_t launch_ssm_conv(const kda_ssm_conv_args& a, cudaStream_t s) {
                                  a.C, static_cast<const T*>(a.conv_state_in), static_cast<T*>(a.conv_state_out),     \
                                  static_cast<T*>(a.y), ys, run)
     if (a.io == KDA_BF16) {
-        if (vec) KDA_CONV(bf16, 8); else KDA_CONV(bf16, 1);
+        if (vec) KDA_CONV(bf16, 4); else KDA_CONV(bf16, 1);
     } else {
         if (vec) KDA_CONV(float, 4); else KDA_CONV(float, 1);
     }
@@ -328,21 +424,27 @@ cudaError_t launch_ssm_conv(const kda_ssm_conv_args& a, cudaStream_t s) {
 
 cudaError_t launch_ssm_conv_step(const kda_ssm_conv_args& a, cudaStream_t s) {
     const int64_t xs = stride_or(a.x_stride, a.C), ys = stride_or(a.y_stride, a.C);
-    const dim3 g((unsigned)((a.C + kThreads - 1) / kThreads), (unsigned)(a.N < 65535 ? a.N : 65535));
-    if (a.io == KDA_BF16)
-        k_conv_step<<<g, kThreads, 0, s>>>(static_cast<const bf16*>(a.x), xs, a.w, a.bias, a.silu, a.N, a.C,
-                                           static_cast<bf16*>(a.conv_state_out), static_cast<bf16*>(a.y), ys);
-    else
-        k_conv_step<<<g, kThreads, 0, s>>>(static_cast<const float*>(a.x), xs, a.w, a.bias, a.silu, a.N, a.C,
-                                           static_cast<float*>(a.conv_state_out), static_cast<float*>(a.y), ys);
+    const int es = a.io == KDA_BF16 ? 2 : 4;
+    const bool vec = a.C % kWide == 0 && wide(a.x, xs, es) && wide(a.y, ys, es) && wide(a.conv_state_out, 0, es);
+    const int W = vec ? kWide : 1, per = kThreads * W;
+    const int64_t rows = (a.N + kStepRows - 1) / kStepRows;
+    const dim3 g((unsigned)((a.C + per - 1) / per), (unsigned)(rows < 65535 ? rows : 65535));
+#define KDA_CONVS(T, W)                                                                                             \
+    k_conv_step<T, W><<<g, kThreads, 0, s>>>(static_cast<const T*>(a.x), xs, a.w, a.bias, a.silu, a.N, a.C,          \
+                                             static_cast<T*>(a.conv_state_out), static_cast<T*>(a.y), ys)
+    if (a.io == KDA_BF16) {
+        if (vec) KDA_CONVS(bf16, 4); else KDA_CONVS(bf16, 1);
+    } else {
+        if (vec) KDA_CONVS(float, 4); else KDA_CONVS(float, 1);
+    }
+#undef KDA_CONVS
     return cudaGetLastError();
 }
 
 ConvBackwardPlan conv_backward_plan(const kda_ssm_conv_args& f) {
-    const int es = f.io == KDA_BF16 ? 2 : 4;
     // The layout of the rows may rule out wide accesses only after the workspace was sized, so the run
     // and the partial rows follow from sizes alone: those of the wide layout hold for both.
-    const int acc = (f.C + 16 / es - 1) / (16 / es);
+    const int acc = (f.C + kWide - 1) / kWide;
     ConvBackwardPlan p;
     p.run = run_of(f.T_total, acc);
     const int64_t by = kThreads / lanes_of(acc);
@@ -355,12 +457,12 @@ cudaError_t launch_ssm_conv_backward(const kda_ssm_conv_backward_args& a, const 
     const kda_ssm_conv_args& f = a.fwd;
     const int es = f.io == KDA_BF16 ? 2 : 4;
     const int64_t xs = stride_or(f.x_stride, f.C), dys = stride_or(a.dy_stride, f.C), dxs = stride_or(a.dx_stride, f.C);
-    const bool vec = f.C % (16 / es) == 0 && wide(f.x, xs, es) && wide(a.dy, dys, es) && wide(a.dx, dxs, es);
-    const int W = vec ? 16 / es : 1;
-    const int lanes = lanes_of((f.C + 16 / es - 1) / (16 / es));
+    const bool vec = f.C % kWide == 0 && wide(f.x, xs, es) && wide(a.dy, dys, es) && wide(a.dx, dxs, es);
+    const int W = vec ? kWide : 1;
+    const int lanes = lanes_of((f.C + kWide - 1) / kWide);
     const dim3 b(lanes, kThreads / lanes);
     const dim3 g((unsigned)p.rows, (unsigned)((f.C + (int64_t)lanes * W - 1) / ((int64_t)lanes * W)));
-    const size_t smem = (size_t)kThreads * 5 * W * sizeof(float);  // at most 40 KB
+    const size_t smem = (size_t)kThreads * 5 * W * sizeof(float);  // at most 20 KB
     float* part = static_cast<float*>(a.workspace);
 #define KDA_CONVB(T, W)                                                                                             \
     k_conv_bwd<T, W><<<g, b, smem, s>>>(static_cast<const T*>(f.x), xs, f.w, f.bias, f.silu, f.cu_seqlens, f.N,      \
@@ -368,7 +470,7 @@ cudaError_t launch_ssm_conv_backward(const kda_ssm_conv_backward_args& a, const 
                                         static_cast<const T*>(a.dy), dys, static_cast<T*>(a.dx), dxs,                \
                                         a.dconv_state_in, part, p.run)
     if (f.io == KDA_BF16) {
-        if (vec) KDA_CONVB(bf16, 8); else KDA_CONVB(bf16, 1);
+        if (vec) KDA_CONVB(bf16, 4); else KDA_CONVB(bf16, 1);
     } else {
         if (vec) KDA_CONVB(float, 4); else KDA_CONVB(float, 1);
     }

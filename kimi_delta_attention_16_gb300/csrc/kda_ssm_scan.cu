@@ -218,57 +218,80 @@ template <int NS> __global__ void __launch_bounds__(256) k_scan_join(Params p) {
     }
 }
 
-// One token per sequence: a thread holds 4 states of one channel and takes several sequences in
-// turn, kRows states in flight at once.  Bound by HBM: the state read and written.
+// One token per sequence: a thread holds 4 states of one channel and takes several sequences in turn,
+// kRows states in flight at once.  Bound by HBM: the state read and written.  kVec: a thread's four
+// elements of B and C come in one access.
 constexpr int kStepThreads = 256;
 constexpr int kRows = 4;
-template <typename T, int NS> __global__ void __launch_bounds__(kStepThreads) k_step(Params p) {
-    constexpr int L = NS / 4;
+template <typename T, int NS, bool kVec> __global__ void __launch_bounds__(kStepThreads, 3) k_step(Params p) {
+    constexpr int L = NS / 4, W = kVec ? 4 : 1;
     const int64_t i = (int64_t)blockIdx.x * kStepThreads + threadIdx.x;
     const int l = (int)(i % L);
     const bool in = i / L < p.C;
     const int64_t c = in ? i / L : p.C - 1;  // idle threads shadow the last channel and store nothing
     const int64_t g = c / p.Cg;
     const float4 a = *reinterpret_cast<const float4*>(p.A + c * NS + 4 * l);
-    const float a2[4] = {a.x * kLog2e, a.y * kLog2e, a.z * kLog2e, a.w * kLog2e};
+    const f2 a2[2] = {f2_of(a.x * kLog2e, a.y * kLog2e), f2_of(a.z * kLog2e, a.w * kLog2e)};
     const float bias = p.dt_bias ? p.dt_bias[c] : 0.f, skip = p.D ? p.D[c] : 0.f;
     const T *up = static_cast<const T*>(p.u) + c, *dp = static_cast<const T*>(p.dt) + c;
     const T* zp = p.z ? static_cast<const T*>(p.z) + c : nullptr;
     const T *bp = static_cast<const T*>(p.B) + g * NS + 4 * l, *cp = static_cast<const T*>(p.Cm) + g * NS + 4 * l;
     T* yp = static_cast<T*>(p.y) + c;
+    auto val = [](const Raw<T, 1>& r) {
+        float v[1];
+        unraw(r, v);
+        return v[0];
+    };
+    auto four = [](const Raw<T, W> (&r)[4 / W], f2 (&o)[2]) {
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4 / W; ++j) {
+            float t[W];
+            unraw(r[j], t);
+#pragma unroll
+            for (int k = 0; k < W; ++k) v[j * W + k] = t[k];
+        }
+        o[0] = f2_of(v[0], v[1]);
+        o[1] = f2_of(v[2], v[3]);
+    };
     for (int64_t r0 = (int64_t)blockIdx.y * kRows; r0 < p.N; r0 += (int64_t)gridDim.y * kRows) {
         float4 s[kRows];
-        float u[kRows], x[kRows], z[kRows], b[kRows][4], cc[kRows][4];
+        Raw<T, 1> u[kRows], x[kRows], z[kRows];
+        Raw<T, W> b[kRows][4 / W], cc[kRows][4 / W];
 #pragma unroll
         for (int q = 0; q < kRows; ++q) {
             const int64_t r = r0 + q < p.N ? r0 + q : p.N - 1;
             s[q] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (in) s[q] = *reinterpret_cast<const float4*>(p.fin + (r * p.C + c) * NS + 4 * l);
-            u[q] = ldf(up + r * p.us);
-            x[q] = ldf(dp + r * p.dts) + bias;
-            z[q] = zp ? ldf(zp + r * p.zs) : 0.f;
+            u[q].load(up + r * p.us);
+            x[q].load(dp + r * p.dts);
+            z[q].zero();
+            if (zp) z[q].load(zp + r * p.zs);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                b[q][j] = ldf(bp + r * p.bs + j);
-                cc[q][j] = ldf(cp + r * p.cs + j);
+            for (int j = 0; j < 4 / W; ++j) {
+                b[q][j].load(bp + r * p.bs + j * W);
+                cc[q][j].load(cp + r * p.cs + j * W);
             }
         }
 #pragma unroll
         for (int q = 0; q < kRows; ++q) {
-            const float d = p.softplus ? softplus(x[q]) : x[q], du = d * u[q];
-            float h[4] = {s[q].x, s[q].y, s[q].z, s[q].w}, y = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                h[j] = fmaf(exp2_hw(d * a2[j]), h[j], du * b[q][j]);
-                y = fmaf(h[j], cc[q][j], y);
-            }
+            const float uv = val(u[q]), xv = val(x[q]) + bias, d = p.softplus ? softplus(xv) : xv;
+            const f2 dd = f2_dup(d), du = f2_dup(d * uv);
+            f2 bv[2], cv[2];
+            four(b[q], bv);
+            four(cc[q], cv);
+            const f2 h0 = fma2(exp2_2(mul2(dd, a2[0])), f2_of(s[q].x, s[q].y), mul2(du, bv[0]));
+            const f2 h1 = fma2(exp2_2(mul2(dd, a2[1])), f2_of(s[q].z, s[q].w), mul2(du, bv[1]));
+            const f2 y2 = fma2(h1, cv[1], mul2(h0, cv[0]));
+            float y = f2_lo(y2) + f2_hi(y2);
 #pragma unroll
             for (int o = 1; o < L; o *= 2) y += __shfl_xor_sync(0xffffffffu, y, o);
             const int64_t r = r0 + q;
             if (r >= p.N || !in) continue;
-            *reinterpret_cast<float4*>(p.fin + (r * p.C + c) * NS + 4 * l) = make_float4(h[0], h[1], h[2], h[3]);
-            y = fmaf(skip, u[q], y);
-            if (l == 0) yp[r * p.ys] = from_f<T>(zp ? y * silu(z[q]) : y);
+            *reinterpret_cast<float4*>(p.fin + (r * p.C + c) * NS + 4 * l) =
+                make_float4(f2_lo(h0), f2_hi(h0), f2_lo(h1), f2_hi(h1));
+            y = fmaf(skip, uv, y);
+            if (l == 0) yp[r * p.ys] = from_f<T>(zp ? y * silu(val(z[q])) : y);
         }
     }
 }
@@ -305,8 +328,13 @@ template <int kMode> cudaError_t scan_mode(Params& p, const kda_ssm_args& a, cud
 template <typename T, int NS> cudaError_t step_as(const Params& p, cudaStream_t s) {
     const int64_t threads = (int64_t)p.C * (NS / 4);
     const int64_t rows = (p.N + kRows - 1) / kRows;
-    k_step<T, NS><<<dim3((unsigned)((threads + kStepThreads - 1) / kStepThreads), (unsigned)(rows < 65535 ? rows : 65535)),
-                    kStepThreads, 0, s>>>(p);
+    const dim3 g((unsigned)((threads + kStepThreads - 1) / kStepThreads), (unsigned)(rows < 65535 ? rows : 65535));
+    constexpr int bytes = 4 * sizeof(T);
+    auto wide = [](const void* q, int64_t stride) {
+        return reinterpret_cast<uintptr_t>(q) % bytes == 0 && stride * sizeof(T) % bytes == 0;
+    };
+    if (wide(p.B, p.bs) && wide(p.Cm, p.cs)) k_step<T, NS, true><<<g, kStepThreads, 0, s>>>(p);
+    else k_step<T, NS, false><<<g, kStepThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
