@@ -49,12 +49,12 @@ template <int W> __device__ __forceinline__ void unraw(const Raw<bf16, W>& r, fl
         }
     }
 }
-// The same as fp32 pairs (W even).
-template <typename T, int W> __device__ __forceinline__ void unraw2(const Raw<T, W>& r, f2 (&v)[W / 2]) {
+// The same as fp32 pairs; one element makes a pair with zero.
+template <typename T, int W> __device__ __forceinline__ void unraw2(const Raw<T, W>& r, f2 (&v)[(W + 1) / 2]) {
     float t[W];
     unraw(r, t);
 #pragma unroll
-    for (int i = 0; i < W / 2; ++i) v[i] = f2_of(t[2 * i], t[2 * i + 1]);
+    for (int i = 0; i < (W + 1) / 2; ++i) v[i] = f2_of(t[2 * i], 2 * i + 1 < W ? t[2 * i + 1] : 0.f);
 }
 template <int W> __device__ __forceinline__ void store_row(float* p, const float (&v)[W]) {
     if constexpr (W == 4) {
@@ -74,6 +74,12 @@ template <int W> __device__ __forceinline__ void store_row(bf16* p, const float 
         *p = __float2bfloat16_rn(v[0]);
     }
 }
+template <typename T, int W> __device__ __forceinline__ void store_row2(T* p, const f2 (&v)[(W + 1) / 2]) {
+    float t[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) t[i] = i & 1 ? f2_hi(v[i / 2]) : f2_lo(v[i / 2]);
+    store_row(p, t);
+}
 // fp32 parameters (weights, biases) for W consecutive channels; 16-byte accesses when W allows.
 template <int W> __device__ __forceinline__ void load_param(const float* p, float (&v)[W]) {
     if constexpr (W % 4 == 0) {
@@ -86,6 +92,22 @@ template <int W> __device__ __forceinline__ void load_param(const float* p, floa
 #pragma unroll
         for (int i = 0; i < W; ++i) v[i] = __ldg(p + i);
     }
+}
+
+// ------------------------------------------------------------------ activations
+// Sigmoid and SiLU from the hardware's exponential and reciprocal (each within two units of the last
+// place, without the range checks of the library forms: e^-x overflows to a sigmoid of 0, as it should).
+__device__ __forceinline__ float rcp_hw(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float sigmoid(float x) { return rcp_hw(1.f + exp2_hw(-kLog2e * x)); }
+__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
+__device__ __forceinline__ f2 exp2_2(f2 x) { return f2_of(exp2_hw(f2_lo(x)), exp2_hw(f2_hi(x))); }
+__device__ __forceinline__ f2 sigmoid2(f2 x) {
+    const f2 d = add2(exp2_2(mul2(x, f2_dup(-kLog2e))), f2_dup(1.f));
+    return f2_of(rcp_hw(f2_lo(d)), rcp_hw(f2_hi(d)));
 }
 
 // ------------------------------------------------------------------ asynchronous copies to shared memory

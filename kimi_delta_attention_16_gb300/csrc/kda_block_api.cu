@@ -402,6 +402,9 @@ kda_status kda_ssm_step(const kda_ssm_args* a, kda_stream_t stream) {
     const size_t es = dsize(a->io);
     const int64_t ys = stride_or(a->y_stride, a->C);
     if ((st = check_ssm_rows(*a, a->N)) || (st = check_plain_rows(a->y, a->N, ys, a->C, es, "y"))) return st;
+    const int64_t strides[] = {a->u_stride, a->dt_stride, a->z_stride, a->B_stride, a->C_stride, a->y_stride};
+    for (int64_t s : strides)
+        if (s * (int64_t)es > 0xffffffffLL) return fail(KDA_ERR_UNSUPPORTED, "kda_ssm_step takes row strides below 4 GB");
     const Span outs[] = {{a->y, rows_bytes(a->N, ys, a->C, es), "y"}, {a->final_state, state_bytes(*a), "final_state"}};
     if ((st = check_overlaps(outs, ssm_inputs(*a, a->N).in))) return st;
     if (const cudaError_t e = launch_ssm_step(*a, cu_stream(stream))) return cuda_fail(e, "ssm step");

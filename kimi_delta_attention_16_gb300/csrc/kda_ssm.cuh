@@ -11,11 +11,6 @@ namespace ssm {
 // logarithm as 2 atanh(s), s = e / (2 + e) <= 1/3, by its odd power series up to s^13 (the next
 // term is below 2^-26 of the sum).  log(1 + e) directly would lose the digits of a small e.
 // Both halves of a pair at once.
-__device__ __forceinline__ float rcp_hw(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ f2 softplus2(f2 x) {
     const f2 t = mul2(f2_of(fabsf(f2_lo(x)), fabsf(f2_hi(x))), f2_dup(-kLog2e));
     const f2 e = f2_of(exp2_hw(f2_lo(t)), exp2_hw(f2_hi(t)));
@@ -31,12 +26,6 @@ __device__ __forceinline__ f2 softplus2(f2 x) {
     return fma2(s, p, f2_of(fmaxf(f2_lo(x), 0.f), fmaxf(f2_hi(x), 0.f)));
 }
 __device__ __forceinline__ float softplus(float x) { return f2_lo(softplus2(f2_of(x, 0.f))); }
-__device__ __forceinline__ float sigmoid(float x) { return rcp_hw(1.f + exp2_hw(-kLog2e * x)); }
-__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
-
-// 2^x of both halves.
-__device__ __forceinline__ f2 exp2_2(f2 x) { return f2_of(exp2_hw(f2_lo(x)), exp2_hw(f2_hi(x))); }
-
 template <typename T> __device__ __forceinline__ float ldf(const T* p) {
     Raw<T, 1> r;
     r.load(p);

@@ -20,19 +20,33 @@ constexpr int kThreads = 256;
 constexpr int kBatch = 4;  // tokens whose loads are in flight together
 constexpr int kWide = 4;   // channels per thread where the layout allows (8 bytes of bf16, 16 of fp32)
 
-__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-
 // Raw value at place `pos` (< 0: before the sequence, from the conv state or zero), W channels from c.
 template <typename T, int W>
 __device__ __forceinline__ void place(const T* __restrict__ x, int64_t xs, const T* __restrict__ cs, int64_t s, int64_t pos,
-                                      int64_t n, int C, int c, float (&v)[W]) {
+                                      int64_t n, int C, int c, f2 (&v)[(W + 1) / 2]) {
     if (pos >= 0) {
         Raw<T, W> r;
         r.load(x + (s + pos) * xs + c);
-        unraw(r, v);
+        unraw2(r, v);
     } else {
+        float t[W];
 #pragma unroll
-        for (int j = 0; j < W; ++j) v[j] = cs && pos >= -3 ? to_f(cs[(n * C + c + j) * 3 + 3 + pos]) : 0.f;
+        for (int j = 0; j < W; ++j) t[j] = cs && pos >= -3 ? to_f(cs[(n * C + c + j) * 3 + 3 + pos]) : 0.f;
+#pragma unroll
+        for (int j = 0; j < (W + 1) / 2; ++j) v[j] = f2_of(t[2 * j], 2 * j + 1 < W ? t[2 * j + 1] : 0.f);
+    }
+}
+
+// Taps and bias of W channels as pairs.
+template <int W>
+__device__ __forceinline__ void load_taps(const float* __restrict__ w, const float* __restrict__ bias, int64_t c,
+                                          f2 (&wt)[4][(W + 1) / 2], f2 (&bs)[(W + 1) / 2]) {
+#pragma unroll
+    for (int j = 0; j < (W + 1) / 2; ++j) {
+        const bool two = 2 * j + 1 < W;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) wt[k][j] = f2_of(w[(c + 2 * j) * 4 + k], two ? w[(c + 2 * j + 1) * 4 + k] : 0.f);
+        bs[j] = bias ? f2_of(bias[c + 2 * j], two ? bias[c + 2 * j + 1] : 0.f) : f2_dup(0.f);
     }
 }
 
@@ -65,35 +79,28 @@ k_conv(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const f
     const int64_t t0 = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * run;
     if (c >= C || t0 >= T_total) return;
     const int64_t t1 = t0 + run < T_total ? t0 + run : T_total;
-    float wt[4][W], bs[W], win[3][W];
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) wt[k][j] = w[(int64_t)(c + j) * 4 + k];
-        bs[j] = bias ? bias[c + j] : 0.f;
-    }
+    constexpr int P = (W + 1) / 2;
+    f2 wt[4][P], bs[P], win[3][P];
+    load_taps<W>(w, bias, c, wt, bs);
     int n = seq_of(cu, N, t0);
     int64_t s, e;
     seq_range(cu, n, T_total, s, e);
 #pragma unroll
-    for (int m = 0; m < 3; ++m) place(x, xs, cs_in, s, t0 - s - 3 + m, n, C, c, win[m]);
+    for (int m = 0; m < 3; ++m) place<T, W>(x, xs, cs_in, s, t0 - s - 3 + m, n, C, c, win[m]);
     const T* xp = x + t0 * xs + c;
     T* yp = y + t0 * ys + c;
     auto token = [&](const Raw<T, W>& raw) {
-        float v[W], o[W];
-        unraw(raw, v);
+        f2 v[P], o[P];
+        unraw2(raw, v);
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            float a = fmaf(wt[0][j], win[0][j], bs[j]);
-            a = fmaf(wt[1][j], win[1][j], a);
-            a = fmaf(wt[2][j], win[2][j], a);
-            a = fmaf(wt[3][j], v[j], a);
-            o[j] = silu ? a * sigmoid_fast(a) : a;
+        for (int j = 0; j < P; ++j) {
+            o[j] = fma2(wt[3][j], v[j], fma2(wt[2][j], win[2][j], fma2(wt[1][j], win[1][j], fma2(wt[0][j], win[0][j], bs[j]))));
+            if (silu) o[j] = mul2(o[j], sigmoid2(o[j]));
             win[0][j] = win[1][j];
             win[1][j] = win[2][j];
             win[2][j] = v[j];
         }
-        store_row(yp, o);
+        store_row2<T, W>(yp, o);
         yp += ys;
     };
     for (int64_t tb = t0; tb < t1; tb += kBatch) {
@@ -116,7 +123,7 @@ k_conv(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const f
                     seq_range(cu, n, T_total, s, e);
                 }
 #pragma unroll
-                for (int m = 0; m < 3; ++m) place(x, xs, cs_in, s, t - s - 3 + m, n, C, c, win[m]);
+                for (int m = 0; m < 3; ++m) place<T, W>(x, xs, cs_in, s, t - s - 3 + m, n, C, c, win[m]);
             }
             raw[0].load(xp);
             xp += xs;
@@ -125,7 +132,8 @@ k_conv(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const f
 #pragma unroll
                 for (int j = 0; j < W; ++j)
 #pragma unroll
-                    for (int m = 0; m < 3; ++m) cs_out[((int64_t)n * C + c + j) * 3 + m] = from_f<T>(win[m][j]);
+                    for (int m = 0; m < 3; ++m)
+                        cs_out[((int64_t)n * C + c + j) * 3 + m] = from_f<T>(j & 1 ? f2_hi(win[m][j / 2]) : f2_lo(win[m][j / 2]));
             }
         }
     }
@@ -176,7 +184,7 @@ k_conv_step(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, co
                 a = fmaf(wt[1][j], st[q][3 * j + 1], a);
                 a = fmaf(wt[2][j], st[q][3 * j + 2], a);
                 a = fmaf(wt[3][j], xv[q][j], a);
-                o[j] = silu ? a * sigmoid_fast(a) : a;
+                o[j] = silu ? a * sigmoid(a) : a;
                 roll[3 * j] = st[q][3 * j + 1];
                 roll[3 * j + 1] = st[q][3 * j + 2];
                 roll[3 * j + 2] = xv[q][j];
@@ -203,34 +211,32 @@ k_conv_bwd(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, con
     extern __shared__ float sm[];  // [blockDim.y][5][blockDim.x * W]
     const int c = (blockIdx.y * blockDim.x + threadIdx.x) * W;
     const int64_t t0 = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * run;
-    float gw[5][W];  // dw[0..3], dbias
+    constexpr int P = (W + 1) / 2;
+    f2 gw[5][P];  // dw[0..3], dbias
 #pragma unroll
     for (int k = 0; k < 5; ++k)
 #pragma unroll
-        for (int j = 0; j < W; ++j) gw[k][j] = 0.f;
+        for (int j = 0; j < P; ++j) gw[k][j] = f2_dup(0.f);
     if (c < C && t0 < T_total) {
         const int64_t t1 = t0 + run < T_total ? t0 + run : T_total;
-        float wt[4][W], bs[W], win[3][W], pend[3][W], out[W];
+        f2 wt[4][P], bs[P], win[3][P], pend[3][P], out[P];
+        load_taps<W>(w, bias, c, wt, bs);
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) wt[k][j] = w[(int64_t)(c + j) * 4 + k];
-            bs[j] = bias ? bias[c + j] : 0.f;
-            pend[0][j] = pend[1][j] = pend[2][j] = 0.f;
-        }
+        for (int j = 0; j < P; ++j) pend[0][j] = pend[1][j] = pend[2][j] = f2_dup(0.f);
         int n = seq_of(cu, N, t0);
         int64_t s, e;
         seq_range(cu, n, T_total, s, e);
 #pragma unroll
-        for (int m = 0; m < 3; ++m) place(x, xs, cs_in, s, t0 - s - 3 + m, n, C, c, win[m]);
+        for (int m = 0; m < 3; ++m) place<T, W>(x, xs, cs_in, s, t0 - s - 3 + m, n, C, c, win[m]);
         // The finished gradient of the value at place p (absolute): a token of this run, or one of the
         // three values before a sequence that starts in it.
-        auto put = [&](int64_t p, const float (&v)[W]) {
+        auto put = [&](int64_t p, const f2 (&v)[P]) {
             if (p >= s) {
-                if (p >= t0 && p < t1) store_row(dx + p * dxs + c, v);
+                if (p >= t0 && p < t1) store_row2<T, W>(dx + p * dxs + c, v);
             } else if (dcs && s >= t0 && p >= s - 3) {
 #pragma unroll
-                for (int j = 0; j < W; ++j) dcs[((int64_t)n * C + c + j) * 3 + (p - s + 3)] = v[j];
+                for (int j = 0; j < W; ++j)
+                    dcs[((int64_t)n * C + c + j) * 3 + (p - s + 3)] = j & 1 ? f2_hi(v[j / 2]) : f2_lo(v[j / 2]);
             }
         };
         auto flush = [&](int64_t t) {  // the sequence ends before t: nothing more reaches the pending three
@@ -239,39 +245,36 @@ k_conv_bwd(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, con
         };
         const int64_t last = t1 + 3 < T_total ? t1 + 3 : T_total;
         bool open = true;  // the pending three still wait for tokens of their own sequence
-        auto slope = [&](float (&v)[W], float (&d)[W]) {  // dy of a token to dpre
+        auto slope = [&](const f2 (&v)[P], f2 (&d)[P]) {  // dy of a token to dpre
+            if (!silu) return;
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                if (silu) {
-                    float a = fmaf(wt[0][j], win[0][j], bs[j]);
-                    a = fmaf(wt[1][j], win[1][j], a);
-                    a = fmaf(wt[2][j], win[2][j], a);
-                    a = fmaf(wt[3][j], v[j], a);
-                    const float sg = sigmoid_fast(a);
-                    d[j] *= sg * fmaf(a, 1.f - sg, 1.f);
-                }
+            for (int j = 0; j < P; ++j) {
+                const f2 a = fma2(wt[3][j], v[j],
+                                  fma2(wt[2][j], win[2][j], fma2(wt[1][j], win[1][j], fma2(wt[0][j], win[0][j], bs[j]))));
+                const f2 sg = sigmoid2(a), t = fma2(a, sub2(f2_dup(1.f), sg), f2_dup(1.f));
+                d[j] = mul2(d[j], mul2(sg, t));
             }
         };
-        auto sums = [&](const float (&v)[W], const float (&d)[W]) {
+        auto sums = [&](const f2 (&v)[P], const f2 (&d)[P]) {
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                gw[0][j] = fmaf(d[j], win[0][j], gw[0][j]);
-                gw[1][j] = fmaf(d[j], win[1][j], gw[1][j]);
-                gw[2][j] = fmaf(d[j], win[2][j], gw[2][j]);
-                gw[3][j] = fmaf(d[j], v[j], gw[3][j]);
-                gw[4][j] += d[j];
+            for (int j = 0; j < P; ++j) {
+                gw[0][j] = fma2(d[j], win[0][j], gw[0][j]);
+                gw[1][j] = fma2(d[j], win[1][j], gw[1][j]);
+                gw[2][j] = fma2(d[j], win[2][j], gw[2][j]);
+                gw[3][j] = fma2(d[j], v[j], gw[3][j]);
+                gw[4][j] = add2(gw[4][j], d[j]);
             }
         };
-        auto move = [&](const float (&v)[W], const float (&d)[W]) {  // leaves the gradient of place t - 3 in `out`
+        auto move = [&](const f2 (&v)[P], const f2 (&d)[P]) {  // leaves the gradient of place t - 3 in `out`
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
+            for (int j = 0; j < P; ++j) {
                 win[0][j] = win[1][j];
                 win[1][j] = win[2][j];
                 win[2][j] = v[j];
-                out[j] = fmaf(wt[0][j], d[j], pend[0][j]);
-                pend[0][j] = fmaf(wt[1][j], d[j], pend[1][j]);
-                pend[1][j] = fmaf(wt[2][j], d[j], pend[2][j]);
-                pend[2][j] = wt[3][j] * d[j];
+                out[j] = fma2(wt[0][j], d[j], pend[0][j]);
+                pend[0][j] = fma2(wt[1][j], d[j], pend[1][j]);
+                pend[1][j] = fma2(wt[2][j], d[j], pend[2][j]);
+                pend[2][j] = mul2(wt[3][j], d[j]);
             }
         };
         const T *xp = x + t0 * xs + c, *dp = dy + t0 * dys + c;
@@ -289,13 +292,13 @@ k_conv_bwd(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, con
                 }
 #pragma unroll
                 for (int q = 0; q < kBatch; ++q) {
-                    float v[W], d[W];
-                    unraw(rx[q], v);
-                    unraw(rd[q], d);
+                    f2 v[P], d[P];
+                    unraw2(rx[q], v);
+                    unraw2(rd[q], d);
                     slope(v, d);
                     sums(v, d);
                     move(v, d);
-                    store_row(op, out);
+                    store_row2<T, W>(op, out);
                     op += dxs;
                 }
                 continue;
@@ -313,17 +316,17 @@ k_conv_bwd(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, con
                         seq_range(cu, n, T_total, s, e);
                     }
 #pragma unroll
-                    for (int m = 0; m < 3; ++m) place(x, xs, cs_in, s, t - s - 3 + m, n, C, c, win[m]);
+                    for (int m = 0; m < 3; ++m) place<T, W>(x, xs, cs_in, s, t - s - 3 + m, n, C, c, win[m]);
 #pragma unroll
-                    for (int j = 0; j < W; ++j) pend[0][j] = pend[1][j] = pend[2][j] = 0.f;
+                    for (int j = 0; j < P; ++j) pend[0][j] = pend[1][j] = pend[2][j] = f2_dup(0.f);
                 }
-                float v[W], d[W];
+                f2 v[P], d[P];
                 rx[0].load(xp);
                 rd[0].load(dp);
                 xp += xs;
                 dp += dys;
-                unraw(rx[0], v);
-                unraw(rd[0], d);
+                unraw2(rx[0], v);
+                unraw2(rd[0], d);
                 slope(v, d);
                 if (t < t1) sums(v, d);
                 move(v, d);
@@ -336,7 +339,7 @@ k_conv_bwd(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, con
 #pragma unroll
     for (int k = 0; k < 5; ++k)
 #pragma unroll
-        for (int j = 0; j < W; ++j) sm[(threadIdx.y * 5 + k) * bw + threadIdx.x * W + j] = gw[k][j];
+        for (int j = 0; j < W; ++j) sm[(threadIdx.y * 5 + k) * bw + threadIdx.x * W + j] = j & 1 ? f2_hi(gw[k][j / 2]) : f2_lo(gw[k][j / 2]);
     __syncthreads();
     for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < 5 * bw; i += blockDim.x * blockDim.y) {
         float t = 0.f;

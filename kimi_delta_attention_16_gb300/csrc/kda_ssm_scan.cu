@@ -223,7 +223,7 @@ template <int NS> __global__ void __launch_bounds__(256) k_scan_join(Params p) {
 // elements of B and C come in one access.
 constexpr int kStepThreads = 256;
 constexpr int kRows = 4;
-template <typename T, int NS, bool kVec> __global__ void __launch_bounds__(kStepThreads, 3) k_step(Params p) {
+template <typename T, int NS, bool kVec> __global__ void __launch_bounds__(kStepThreads, 3) k_step(Params p, int rows) {
     constexpr int L = NS / 4, W = kVec ? 4 : 1;
     const int64_t i = (int64_t)blockIdx.x * kStepThreads + threadIdx.x;
     const int l = (int)(i % L);
@@ -236,7 +236,15 @@ template <typename T, int NS, bool kVec> __global__ void __launch_bounds__(kStep
     const T *up = static_cast<const T*>(p.u) + c, *dp = static_cast<const T*>(p.dt) + c;
     const T* zp = p.z ? static_cast<const T*>(p.z) + c : nullptr;
     const T *bp = static_cast<const T*>(p.B) + g * NS + 4 * l, *cp = static_cast<const T*>(p.Cm) + g * NS + 4 * l;
-    T* yp = static_cast<T*>(p.y) + c;
+    float* sp = p.fin + c * NS + 4 * l;
+    // Row r of a tensor: 32 x 32 bits to 64 in one instruction (row strides are below 4 GB).
+    auto at = [](auto* base, uint32_t r, uint32_t bytes) {
+        return reinterpret_cast<decltype(base)>(reinterpret_cast<uintptr_t>(base) + (uint64_t)r * bytes);
+    };
+    const uint32_t ub = (uint32_t)p.us * sizeof(T), db = (uint32_t)p.dts * sizeof(T), zb = (uint32_t)p.zs * sizeof(T),
+                   bb = (uint32_t)p.bs * sizeof(T), cb = (uint32_t)p.cs * sizeof(T), yb = (uint32_t)p.ys * sizeof(T),
+                   sb = (uint32_t)p.C * NS * sizeof(float);
+    const int first = blockIdx.y * rows, last = first + rows < p.N ? first + rows : p.N;  // this block's sequences
     auto val = [](const Raw<T, 1>& r) {
         float v[1];
         unraw(r, v);
@@ -254,27 +262,27 @@ template <typename T, int NS, bool kVec> __global__ void __launch_bounds__(kStep
         o[0] = f2_of(v[0], v[1]);
         o[1] = f2_of(v[2], v[3]);
     };
-    for (int64_t r0 = (int64_t)blockIdx.y * kRows; r0 < p.N; r0 += (int64_t)gridDim.y * kRows) {
+    for (int r0 = first; r0 < last; r0 += kRows) {
+        const int n = last - r0;  // sequences left
         float4 s[kRows];
         Raw<T, 1> u[kRows], x[kRows], z[kRows];
         Raw<T, W> b[kRows][4 / W], cc[kRows][4 / W];
 #pragma unroll
         for (int q = 0; q < kRows; ++q) {
-            const int64_t r = r0 + q < p.N ? r0 + q : p.N - 1;
-            s[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (in) s[q] = *reinterpret_cast<const float4*>(p.fin + (r * p.C + c) * NS + 4 * l);
-            u[q].load(up + r * p.us);
-            x[q].load(dp + r * p.dts);
-            z[q].zero();
-            if (zp) z[q].load(zp + r * p.zs);
+            const uint32_t r = r0 + (q < n ? q : 0);
+            s[q] = in ? *at(reinterpret_cast<const float4*>(sp), r, sb) : make_float4(0.f, 0.f, 0.f, 0.f);
+            u[q].load(at(up, r, ub));
+            x[q].load(at(dp, r, db));
+            if (zp) z[q].load(at(zp, r, zb));
 #pragma unroll
             for (int j = 0; j < 4 / W; ++j) {
-                b[q][j].load(bp + r * p.bs + j * W);
-                cc[q][j].load(cp + r * p.cs + j * W);
+                b[q][j].load(at(bp, r, bb) + j * W);
+                cc[q][j].load(at(cp, r, cb) + j * W);
             }
         }
 #pragma unroll
         for (int q = 0; q < kRows; ++q) {
+            if (q >= n) break;  // the same for the whole block
             const float uv = val(u[q]), xv = val(x[q]) + bias, d = p.softplus ? softplus(xv) : xv;
             const f2 dd = f2_dup(d), du = f2_dup(d * uv);
             f2 bv[2], cv[2];
@@ -286,12 +294,11 @@ template <typename T, int NS, bool kVec> __global__ void __launch_bounds__(kStep
             float y = f2_lo(y2) + f2_hi(y2);
 #pragma unroll
             for (int o = 1; o < L; o *= 2) y += __shfl_xor_sync(0xffffffffu, y, o);
-            const int64_t r = r0 + q;
-            if (r >= p.N || !in) continue;
-            *reinterpret_cast<float4*>(p.fin + (r * p.C + c) * NS + 4 * l) =
-                make_float4(f2_lo(h0), f2_hi(h0), f2_lo(h1), f2_hi(h1));
-            y = fmaf(skip, uv, y);
-            if (l == 0) yp[r * p.ys] = from_f<T>(zp ? y * silu(val(z[q])) : y);
+            if (in) {
+                *at(reinterpret_cast<float4*>(sp), r0 + q, sb) = make_float4(f2_lo(h0), f2_hi(h0), f2_lo(h1), f2_hi(h1));
+                y = fmaf(skip, uv, y);
+                if (l == 0) *at(static_cast<T*>(p.y) + c, r0 + q, yb) = from_f<T>(zp ? y * silu(val(z[q])) : y);
+            }
         }
     }
 }
@@ -327,14 +334,19 @@ template <int kMode> cudaError_t scan_mode(Params& p, const kda_ssm_args& a, cud
 
 template <typename T, int NS> cudaError_t step_as(const Params& p, cudaStream_t s) {
     const int64_t threads = (int64_t)p.C * (NS / 4);
-    const int64_t rows = (p.N + kRows - 1) / kRows;
-    const dim3 g((unsigned)((threads + kStepThreads - 1) / kStepThreads), (unsigned)(rows < 65535 ? rows : 65535));
+    // Sequences per thread: four at once, and more rounds (up to four) while three blocks per SM are left.
+    DeviceInfo di{0, 0, 0};
+    const int64_t blocks = (threads + kStepThreads - 1) / kStepThreads, sms = current_device_info(&di) ? di.sm_count : 1;
+    int rows = kRows;
+    while (rows < 4 * kRows && blocks * ((p.N + 2 * rows - 1) / (2 * rows)) >= 3 * sms) rows *= 2;
+    while ((p.N + rows - 1) / rows > 65535) rows *= 2;
+    const dim3 g((unsigned)blocks, (unsigned)((p.N + rows - 1) / rows));
     constexpr int bytes = 4 * sizeof(T);
     auto wide = [](const void* q, int64_t stride) {
         return reinterpret_cast<uintptr_t>(q) % bytes == 0 && stride * sizeof(T) % bytes == 0;
     };
-    if (wide(p.B, p.bs) && wide(p.Cm, p.cs)) k_step<T, NS, true><<<g, kStepThreads, 0, s>>>(p);
-    else k_step<T, NS, false><<<g, kStepThreads, 0, s>>>(p);
+    if (wide(p.B, p.bs) && wide(p.Cm, p.cs)) k_step<T, NS, true><<<g, kStepThreads, 0, s>>>(p, rows);
+    else k_step<T, NS, false><<<g, kStepThreads, 0, s>>>(p, rows);
     return cudaGetLastError();
 }
 
