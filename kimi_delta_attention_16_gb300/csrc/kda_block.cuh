@@ -193,6 +193,17 @@ __device__ __forceinline__ int seq_of(const int32_t* __restrict__ cu, int N, int
     return lo;
 }
 
+// A copy of cu in shared memory where it fits: looking a token up there costs no chain of memory
+// latencies.  Every thread of the block calls it; it ends with a barrier.
+constexpr int kStagedCu = 512;
+__device__ __forceinline__ const int32_t* stage_cu(const int32_t* __restrict__ cu, int N, int32_t (&shared)[kStagedCu]) {
+    const int t = threadIdx.y * blockDim.x + threadIdx.x, nt = blockDim.x * blockDim.y;
+    if (N < kStagedCu)
+        for (int i = t; i <= N; i += nt) shared[i] = cu[i];
+    __syncthreads();
+    return N < kStagedCu ? shared : cu;
+}
+
 // ------------------------------------------------------------------ launchers (arguments validated by the caller)
 // dst[n] = src[n] (zeros when src is NULL) for every sequence of no tokens, `per` bytes each (a
 // multiple of 2): what a kernel over tokens never reaches.

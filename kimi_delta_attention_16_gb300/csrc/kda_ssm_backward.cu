@@ -76,9 +76,6 @@ __global__ void __launch_bounds__(Lay<NS>::NT, 8) k_rev(BParams b) {
             q[2 * i + 1] = f2_of(s.z, s.w);
         }
     };
-    int n = seq_of(p.cu, p.N, t1 - 1);
-    int64_t s0 = p.cu[n];
-    load_q(p.cu[n + 1] == t1 ? b.dfin : nullptr, n);
     const float bias = p.dt_bias ? p.dt_bias[c] : 0.f;
     const int tiles = (int)((t1 - t0 + TT - 1) / TT);
     auto issue = [&](int j) {  // the j-th tile from the right
@@ -104,6 +101,9 @@ __global__ void __launch_bounds__(Lay<NS>::NT, 8) k_rev(BParams b) {
     };
 #pragma unroll
     for (int j = 0; j < kDepth - 1; ++j) issue(j);
+    int n = seq_of(p.cu, p.N, t1 - 1);
+    int64_t s0 = p.cu[n];
+    load_q(p.cu[n + 1] == t1 ? b.dfin : nullptr, n);
     cp_wait<kDepth - 2>();
     __syncthreads();
     widen(0);
@@ -260,11 +260,6 @@ __global__ void __launch_bounds__(128, 2) k_ssm_bwd(BParams b) {
     load_tile(p.A, 0, A2, kLog2e);
 #pragma unroll
     for (int s = 0; s < 4; ++s) dA[s][0] = dA[s][1] = f2_dup(0.f);
-    int n = seq_of(p.cu, p.N, t1 - 1);
-    int64_t s0 = p.cu[n];  // start of the sequence that the walk is in
-    if (p.cu[n + 1] == t1) load_tile(b.dfin, n, q, 1.f);
-    else load_tile(piece + 1 < p.pieces ? b.rev : nullptr, piece + 1, q, 1.f);
-
     // this thread's elements: token (i NT + tid) / CH, channel (i NT + tid) % CH
     float bias[Y::CPT], skip[Y::CPT], accD[Y::CPT], accB[Y::CPT];
     bool cin[Y::CPT];
@@ -299,6 +294,10 @@ __global__ void __launch_bounds__(128, 2) k_ssm_bwd(BParams b) {
         cp_commit();
     };
     issue(0);
+    int n = seq_of(p.cu, p.N, t1 - 1);
+    int64_t s0 = p.cu[n];  // start of the sequence that the walk is in
+    if (p.cu[n + 1] == t1) load_tile(b.dfin, n, q, 1.f);
+    else load_tile(piece + 1 < p.pieces ? b.rev : nullptr, piece + 1, q, 1.f);
     cp_wait<0>();
     __syncthreads();
     for (int j = 0; j < tiles; ++j) {

@@ -17,8 +17,61 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;  // tokens whose loads are in flight together
+constexpr int kBatch = 4;   // tokens taken together
 constexpr int kWide = 4;   // channels per thread where the layout allows (8 bytes of bf16, 16 of fp32)
+
+// A thread's own rows (W channels, consecutive tokens) through shared memory: up to four batches of kBatch
+// tokens are in flight, the thread reads back what it copied itself, so nothing waits for anybody else.
+// Accesses below 4 bytes (bf16 rows that allow no more) cannot be copied this way: those are read when
+// their batch begins.
+template <typename T, int W> struct Rows {
+    static constexpr bool kAsync = Raw<T, W>::kBytes >= 4;
+    static constexpr int kGroups = Raw<T, W>::kBytes == 16 ? 2 : 4;  // batches in flight: 128 bytes per thread
+    static constexpr int kSlots = kAsync ? kGroups * kBatch : 1;
+    Raw<T, W>* ring;  // [kSlots][kThreads], at this thread
+    const T* src;     // the next token to copy
+    int64_t stride;
+    int left;         // tokens that are left to copy
+    int next;         // slot of the next batch to copy
+    Raw<T, W> now[kAsync ? 1 : kBatch];
+    __device__ __forceinline__ void begin(Raw<T, W>* shared, const T* first, int64_t st, int tokens) {
+        ring = shared + threadIdx.y * blockDim.x + threadIdx.x;
+        src = first;
+        stride = st;
+        left = tokens;
+        next = 0;
+    }
+    __device__ __forceinline__ void issue() {  // the caller commits
+        if constexpr (kAsync) {
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                if (q < left) cp_async_raw<T, W>(ring + (next + q) * kThreads, src);
+                src += stride;
+            }
+            left -= kBatch;
+            next = next + kBatch == kSlots ? 0 : next + kBatch;
+        }
+    }
+    __device__ __forceinline__ void take() {  // the batch at the front, where it is read now
+        if constexpr (!kAsync) {
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                if (q < left) now[q].load(src);
+                src += stride;
+            }
+            left -= kBatch;
+        }
+    }
+    // Token q of the batch in slots [slot, slot + kBatch).
+    __device__ __forceinline__ Raw<T, W> get(int slot, int q) const {
+        if constexpr (kAsync) return ring[(slot + q) * kThreads];
+        Raw<T, W> r = now[0];
+#pragma unroll
+        for (int k = 1; k < (kAsync ? 1 : kBatch); ++k)
+            if (q == k) r = now[k];
+        return r;
+    }
+};
 
 // Raw value at place `pos` (< 0: before the sequence, from the conv state or zero), W channels from c.
 template <typename T, int W>
@@ -34,6 +87,18 @@ __device__ __forceinline__ void place(const T* __restrict__ x, int64_t xs, const
         for (int j = 0; j < W; ++j) t[j] = cs && pos >= -3 ? to_f(cs[(n * C + c + j) * 3 + 3 + pos]) : 0.f;
 #pragma unroll
         for (int j = 0; j < (W + 1) / 2; ++j) v[j] = f2_of(t[2 * j], 2 * j + 1 < W ? t[2 * j + 1] : 0.f);
+    }
+}
+
+// The three values before token t of a sequence that starts at s.  `raw` holds the three rows before t as
+// they lie in memory (loaded before s was known); those before s come from the conv state instead.
+template <typename T, int W>
+__device__ __forceinline__ void window(const Raw<T, W> (&raw)[3], const T* __restrict__ x, int64_t xs, const T* __restrict__ cs,
+                                       int64_t s, int64_t t, int64_t n, int C, int c, f2 (&win)[3][(W + 1) / 2]) {
+#pragma unroll
+    for (int m = 0; m < 3; ++m) {
+        if (t - 3 + m >= s) unraw2(raw[m], win[m]);
+        else place<T, W>(x, xs, cs, s, t - s - 3 + m, n, C, c, win[m]);
     }
 }
 
@@ -73,21 +138,37 @@ template <int W> __device__ __forceinline__ void load_state(const bf16* p, float
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads)
 k_conv(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const float* __restrict__ bias, int silu,
-       const int32_t* __restrict__ cu, int N, int64_t T_total, int C, const T* __restrict__ cs_in, T* __restrict__ cs_out,
-       T* __restrict__ y, int64_t ys, int run) {
-    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * W;
-    const int64_t t0 = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * run;
-    if (c >= C || t0 >= T_total) return;
+       const int32_t* cu, int N, int64_t T_total, int C, const T* __restrict__ cs_in, T* __restrict__ cs_out,
+       T* __restrict__ y, int64_t ys, int run, unsigned strips) {
+    __shared__ int32_t staged[kStagedCu];
+    __shared__ Raw<T, W> shared[Rows<T, W>::kSlots * kThreads];
+    const unsigned rows = blockIdx.x / strips, strip = blockIdx.x - rows * strips;
+    const int c = (strip * blockDim.x + threadIdx.x) * W;
+    const int64_t t0 = ((int64_t)rows * blockDim.y + threadIdx.y) * run;
+    const bool on = c < C && t0 < T_total;
     const int64_t t1 = t0 + run < T_total ? t0 + run : T_total;
     constexpr int P = (W + 1) / 2;
+    Raw<T, W> before[3];
     f2 wt[4][P], bs[P], win[3][P];
-    load_taps<W>(w, bias, c, wt, bs);
+    Rows<T, W> in;
+    if (on) {
+        in.begin(shared, x + t0 * xs + c, xs, (int)(t1 - t0));
+#pragma unroll
+        for (int g = 0; g < Rows<T, W>::kGroups - 1; ++g) {
+            in.issue();
+            cp_commit();
+        }
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+            if (t0 - 3 + m >= 0) before[m].load(x + (t0 - 3 + m) * xs + c);
+        load_taps<W>(w, bias, c, wt, bs);
+    }
+    cu = stage_cu(cu, N, staged);
+    if (!on) return;
     int n = seq_of(cu, N, t0);
     int64_t s, e;
     seq_range(cu, n, T_total, s, e);
-#pragma unroll
-    for (int m = 0; m < 3; ++m) place<T, W>(x, xs, cs_in, s, t0 - s - 3 + m, n, C, c, win[m]);
-    const T* xp = x + t0 * xs + c;
+    window<T, W>(before, x, xs, cs_in, s, t0, n, C, c, win);
     T* yp = y + t0 * ys + c;
     auto token = [&](const Raw<T, W>& raw) {
         f2 v[P], o[P];
@@ -103,18 +184,16 @@ k_conv(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const f
         store_row2<T, W>(yp, o);
         yp += ys;
     };
+    int slot = 0;
     for (int64_t tb = t0; tb < t1; tb += kBatch) {
-        Raw<T, W> raw[kBatch];
+        in.issue();
+        cp_commit();
+        cp_wait<Rows<T, W>::kGroups - 1>();
+        in.take();
         if (tb + kBatch <= t1 && tb + kBatch < e) {  // no sequence ends here: tokens without a branch between them
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-                raw[q].load(xp);
-                xp += xs;
-            }
-#pragma unroll
-            for (int q = 0; q < kBatch; ++q) token(raw[q]);
-            continue;
-        }
+            for (int q = 0; q < kBatch; ++q) token(in.get(slot, q));
+        } else
 #pragma unroll 1
         for (int64_t t = tb; t < tb + kBatch && t < t1; ++t) {
             if (t >= e && n < N - 1) {  // crossed into a later sequence
@@ -125,9 +204,7 @@ k_conv(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const f
 #pragma unroll
                 for (int m = 0; m < 3; ++m) place<T, W>(x, xs, cs_in, s, t - s - 3 + m, n, C, c, win[m]);
             }
-            raw[0].load(xp);
-            xp += xs;
-            token(raw[0]);
+            token(in.get(slot, (int)(t - tb)));
             if (cs_out && t == e - 1) {
 #pragma unroll
                 for (int j = 0; j < W; ++j)
@@ -136,6 +213,7 @@ k_conv(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const f
                         cs_out[((int64_t)n * C + c + j) * 3 + m] = from_f<T>(j & 1 ? f2_hi(win[m][j / 2]) : f2_lo(win[m][j / 2]));
             }
         }
+        slot = slot + kBatch >= Rows<T, W>::kSlots ? 0 : slot + kBatch;
     }
 }
 
@@ -203,31 +281,52 @@ k_conv_step(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, co
 }
 
 template <typename T, int W>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 k_conv_bwd(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const float* __restrict__ bias, int silu,
-           const int32_t* __restrict__ cu, int N, int64_t T_total, int C, const T* __restrict__ cs_in,
+           const int32_t* cu, int N, int64_t T_total, int C, const T* __restrict__ cs_in,
            const T* __restrict__ dy, int64_t dys, T* __restrict__ dx, int64_t dxs, float* __restrict__ dcs,
-           float* __restrict__ part, int run) {
-    extern __shared__ float sm[];  // [blockDim.y][5][blockDim.x * W]
-    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * W;
-    const int64_t t0 = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * run;
+           float* __restrict__ part, int run, unsigned strips) {
+    extern __shared__ __align__(16) float sm[];  // [blockDim.y][5][blockDim.x * W]
+    __shared__ int32_t staged[kStagedCu];
+    Raw<T, W>* shared_x = reinterpret_cast<Raw<T, W>*>(sm);  // the rows in flight; the sums of the block at the end
+    Raw<T, W>* shared_d = shared_x + Rows<T, W>::kSlots * kThreads;
+    const unsigned rows = blockIdx.x / strips, strip = blockIdx.x - rows * strips;
+    const int c = (strip * blockDim.x + threadIdx.x) * W;
+    const int64_t t0 = ((int64_t)rows * blockDim.y + threadIdx.y) * run;
+    const int64_t t1 = t0 + run < T_total ? t0 + run : T_total, last = t1 + 3 < T_total ? t1 + 3 : T_total;
     constexpr int P = (W + 1) / 2;
     f2 gw[5][P];  // dw[0..3], dbias
 #pragma unroll
     for (int k = 0; k < 5; ++k)
 #pragma unroll
         for (int j = 0; j < P; ++j) gw[k][j] = f2_dup(0.f);
-    if (c < C && t0 < T_total) {
-        const int64_t t1 = t0 + run < T_total ? t0 + run : T_total;
-        f2 wt[4][P], bs[P], win[3][P], pend[3][P], out[P];
+    Raw<T, W> before[3];
+    f2 wt[4][P], bs[P];
+    const bool on = c < C && t0 < T_total;
+    Rows<T, W> inx, ind;
+    if (on) {
+        inx.begin(shared_x, x + t0 * xs + c, xs, (int)(last - t0));
+        ind.begin(shared_d, dy + t0 * dys + c, dys, (int)(last - t0));
+#pragma unroll
+        for (int g = 0; g < Rows<T, W>::kGroups - 1; ++g) {
+            inx.issue();
+            ind.issue();
+            cp_commit();
+        }
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+            if (t0 - 3 + m >= 0) before[m].load(x + (t0 - 3 + m) * xs + c);
         load_taps<W>(w, bias, c, wt, bs);
+    }
+    cu = stage_cu(cu, N, staged);
+    if (on) {
+        f2 win[3][P], pend[3][P], out[P];
 #pragma unroll
         for (int j = 0; j < P; ++j) pend[0][j] = pend[1][j] = pend[2][j] = f2_dup(0.f);
         int n = seq_of(cu, N, t0);
         int64_t s, e;
         seq_range(cu, n, T_total, s, e);
-#pragma unroll
-        for (int m = 0; m < 3; ++m) place<T, W>(x, xs, cs_in, s, t0 - s - 3 + m, n, C, c, win[m]);
+        window<T, W>(before, x, xs, cs_in, s, t0, n, C, c, win);
         // The finished gradient of the value at place p (absolute): a token of this run, or one of the
         // three values before a sequence that starts in it.
         auto put = [&](int64_t p, const f2 (&v)[P]) {
@@ -243,7 +342,6 @@ k_conv_bwd(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, con
 #pragma unroll
             for (int m = 0; m < 3; ++m) put(t - 3 + m, pend[m]);
         };
-        const int64_t last = t1 + 3 < T_total ? t1 + 3 : T_total;
         bool open = true;  // the pending three still wait for tokens of their own sequence
         auto slope = [&](const f2 (&v)[P], f2 (&d)[P]) {  // dy of a token to dpre
             if (!silu) return;
@@ -277,24 +375,24 @@ k_conv_bwd(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, con
                 pend[2][j] = mul2(wt[3][j], d[j]);
             }
         };
-        const T *xp = x + t0 * xs + c, *dp = dy + t0 * dys + c;
+        int slot = 0;
         for (int64_t tb = t0; tb < last && open; tb += kBatch) {
-            Raw<T, W> rx[kBatch], rd[kBatch];
+            inx.issue();
+            ind.issue();
+            cp_commit();
+            cp_wait<Rows<T, W>::kGroups - 1>();
+            inx.take();
+            ind.take();
+            const int at = slot;
+            slot = slot + kBatch >= Rows<T, W>::kSlots ? 0 : slot + kBatch;
             if (tb - 3 >= t0 && tb - 3 >= s && tb + kBatch <= t1 && tb + kBatch <= e) {
                 // own tokens only, and every finished place is one of them: no branch between the tokens
                 T* op = dx + (tb - 3) * dxs + c;
 #pragma unroll
                 for (int q = 0; q < kBatch; ++q) {
-                    rx[q].load(xp);
-                    rd[q].load(dp);
-                    xp += xs;
-                    dp += dys;
-                }
-#pragma unroll
-                for (int q = 0; q < kBatch; ++q) {
                     f2 v[P], d[P];
-                    unraw2(rx[q], v);
-                    unraw2(rd[q], d);
+                    unraw2(inx.get(at, q), v);
+                    unraw2(ind.get(at, q), d);
                     slope(v, d);
                     sums(v, d);
                     move(v, d);
@@ -321,12 +419,8 @@ k_conv_bwd(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, con
                     for (int j = 0; j < P; ++j) pend[0][j] = pend[1][j] = pend[2][j] = f2_dup(0.f);
                 }
                 f2 v[P], d[P];
-                rx[0].load(xp);
-                rd[0].load(dp);
-                xp += xs;
-                dp += dys;
-                unraw2(rx[0], v);
-                unraw2(rd[0], d);
+                unraw2(inx.get(at, (int)(t - tb)), v);
+                unraw2(ind.get(at, (int)(t - tb)), d);
                 slope(v, d);
                 if (t < t1) sums(v, d);
                 move(v, d);
@@ -336,6 +430,8 @@ k_conv_bwd(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, con
         if (open && last == T_total) flush(T_total);
     }
     const int bw = blockDim.x * W;  // channels of the block
+    cp_wait<0>();
+    __syncthreads();  // every thread is done with the rows that lie where the sums go
 #pragma unroll
     for (int k = 0; k < 5; ++k)
 #pragma unroll
@@ -344,8 +440,8 @@ k_conv_bwd(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, con
     for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < 5 * bw; i += blockDim.x * blockDim.y) {
         float t = 0.f;
         for (int r = 0; r < blockDim.y; ++r) t += sm[r * 5 * bw + i];
-        const int k = i / bw, ch = blockIdx.y * bw + i - k * bw;
-        if (ch < C) part[((int64_t)blockIdx.x * 5 + k) * C + ch] = t;
+        const int k = i / bw, ch = strip * bw + i - k * bw;
+        if (ch < C) part[((int64_t)rows * 5 + k) * C + ch] = t;
     }
 }
 
@@ -411,11 +507,13 @@ cudaError_t launch_ssm_conv(const kda_ssm_conv_args& a, cudaStream_t s) {
     const int acc = (a.C + W - 1) / W;
     const dim3 b(lanes_of(acc), kThreads / lanes_of(acc));
     const int run = run_of(a.T_total, acc);
-    const dim3 g((unsigned)((a.T_total + (int64_t)run * b.y - 1) / ((int64_t)run * b.y)), (unsigned)((acc + b.x - 1) / b.x));
+    // Blocks that run together cover whole rows (strips of channels first), not one strip of many rows.
+    const unsigned strips = (unsigned)((acc + b.x - 1) / b.x);
+    const unsigned g = strips * (unsigned)((a.T_total + (int64_t)run * b.y - 1) / ((int64_t)run * b.y));
 #define KDA_CONV(T, W)                                                                                              \
     k_conv<T, W><<<g, b, 0, s>>>(static_cast<const T*>(a.x), xs, a.w, a.bias, a.silu, a.cu_seqlens, a.N, a.T_total,  \
                                  a.C, static_cast<const T*>(a.conv_state_in), static_cast<T*>(a.conv_state_out),     \
-                                 static_cast<T*>(a.y), ys, run)
+                                 static_cast<T*>(a.y), ys, run, strips)
     if (a.io == KDA_BF16) {
         if (vec) KDA_CONV(bf16, 4); else KDA_CONV(bf16, 1);
     } else {
@@ -464,21 +562,26 @@ cudaError_t launch_ssm_conv_backward(const kda_ssm_conv_backward_args& a, const 
     const int W = vec ? kWide : 1;
     const int lanes = lanes_of((f.C + kWide - 1) / kWide);
     const dim3 b(lanes, kThreads / lanes);
-    const dim3 g((unsigned)p.rows, (unsigned)((f.C + (int64_t)lanes * W - 1) / ((int64_t)lanes * W)));
-    const size_t smem = (size_t)kThreads * 5 * W * sizeof(float);  // at most 20 KB
+    const unsigned strips = (unsigned)((f.C + (int64_t)lanes * W - 1) / ((int64_t)lanes * W));
+    const unsigned g = strips * (unsigned)p.rows;
+    const size_t row = (size_t)2 * kThreads * (es * W == 16 ? 2 : 4) * kBatch * W * es, sum = (size_t)kThreads * 5 * W * sizeof(float);
+    const int smem = (int)(row > sum ? row : sum);  // at most 64 KB
+    cudaError_t e = cudaSuccess;
     float* part = static_cast<float*>(a.workspace);
 #define KDA_CONVB(T, W)                                                                                             \
+    if (!(e = cudaFuncSetAttribute(k_conv_bwd<T, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))            \
     k_conv_bwd<T, W><<<g, b, smem, s>>>(static_cast<const T*>(f.x), xs, f.w, f.bias, f.silu, f.cu_seqlens, f.N,      \
                                         f.T_total, f.C, static_cast<const T*>(f.conv_state_in),                      \
                                         static_cast<const T*>(a.dy), dys, static_cast<T*>(a.dx), dxs,                \
-                                        a.dconv_state_in, part, p.run)
+                                        a.dconv_state_in, part, p.run, strips)
     if (f.io == KDA_BF16) {
-        if (vec) KDA_CONVB(bf16, 4); else KDA_CONVB(bf16, 1);
+        if (vec) { KDA_CONVB(bf16, 4); } else { KDA_CONVB(bf16, 1); }
     } else {
-        if (vec) KDA_CONVB(float, 4); else KDA_CONVB(float, 1);
+        if (vec) { KDA_CONVB(float, 4); } else { KDA_CONVB(float, 1); }
     }
 #undef KDA_CONVB
-    if (cudaError_t e = cudaGetLastError()) return e;
+    if (!e) e = cudaGetLastError();
+    if (e) return e;
     return launch_column_sum(part, p.rows, 5 * (int64_t)f.C, PutConv{a.dw, a.dbias, f.C}, s);
 }
 

@@ -69,12 +69,6 @@ __global__ void __launch_bounds__(Lay<NS>::NT, 8) k_scan(Params p) {
             reinterpret_cast<float4*>(base + n * p.C * NS + so)[i] =
                 make_float4(f2_lo(h[2 * i]), f2_hi(h[2 * i]), f2_lo(h[2 * i + 1]), f2_hi(h[2 * i + 1]));
     };
-    int n = seq_of(p.cu, p.N, t0);
-    int64_t seq_end = p.cu[n + 1];
-    if (p.cu[n] == t0) load_state(p.init, n);
-    else if (kMode != kPiece && piece > 0) load_state(p.ws_state, piece);
-    else load_state(nullptr, 0);
-
     const float bias = p.dt_bias ? p.dt_bias[c] : 0.f, skip = kMain && p.D ? p.D[c] : 0.f;
     T* yp = static_cast<T*>(p.y) + c + t0 * p.ys;
     const int c_lo = ch - (warp * Y::KPW + lane % Y::KPW), cols = c_hi - c_lo, cl = ch - c_lo;
@@ -105,6 +99,11 @@ __global__ void __launch_bounds__(Lay<NS>::NT, 8) k_scan(Params p) {
     };
 #pragma unroll
     for (int k = 0; k < kDepth - 1; ++k) issue(k);
+    int n = seq_of(p.cu, p.N, t0);
+    int64_t seq_end = p.cu[n + 1];
+    if (p.cu[n] == t0) load_state(p.init, n);
+    else if (kMode != kPiece && piece > 0) load_state(p.ws_state, piece);
+    else load_state(nullptr, 0);
     cp_wait<kDepth - 2>();  // tile 0
     __syncthreads();
     widen(0);
