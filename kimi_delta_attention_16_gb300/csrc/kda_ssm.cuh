@@ -67,6 +67,50 @@ template <int NS> struct Lay {
     static_assert(BPT >= 1, "tile too small");
 };
 
+// ------------------------------------------------------------------ joining the pieces
+constexpr int kJoinThreads = 128;
+constexpr int kMaxPieces = 1024;  // of a plan
+constexpr int kJoinBits = kMaxPieces;
+
+// Bit k: a sequence starts in piece k (at its first token or inside), so nothing passes through it.
+__device__ __forceinline__ void mark_started(const Params& p, uint32_t (&bits)[kJoinBits / 32]) {
+    for (int k = threadIdx.x; k < kJoinBits; k += kJoinThreads) {
+        bool s = false;
+        if (k < p.pieces) {
+            const int64_t t1 = (k + 1) * p.piece < p.T ? (k + 1) * p.piece : p.T;
+            s = p.cu[seq_of(p.cu, p.N, t1 - 1)] >= k * p.piece;
+        }
+        const uint32_t w = __ballot_sync(0xffffffffu, s);
+        if ((threadIdx.x & 31) == 0) bits[k / 32] = w;
+    }
+    __syncthreads();
+}
+
+// carry = (carry, unless a sequence started in the piece) 2^(a2 sum of delta) + the piece's own, over
+// `count` pieces from `k` on (kDir: +1 or -1), each result written over the own one.  Eight pieces' values
+// are loaded before the first is used: the chain is one multiply-add per piece, not one latency.
+template <int kDir>
+__device__ __forceinline__ void join(const Params& p, const uint32_t* started, int k, int count, float a2, float carry,
+                                     float* slot, const float* sum, int64_t row) {
+    constexpr int U = 8;
+    for (int c = 0; c < count; c += U) {
+        float o[U], f[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int64_t q = k + (int64_t)kDir * (c + j);
+            o[j] = c + j < count ? slot[q * row] : 0.f;
+            f[j] = c + j < count ? sum[q * p.C] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            if (c + j >= count) break;
+            const int64_t q = k + (int64_t)kDir * (c + j);
+            carry = started[q / 32] >> (q & 31) & 1 ? o[j] : fmaf(exp2_hw(a2 * f[j]), carry, o[j]);
+            slot[q * row] = carry;
+        }
+    }
+}
+
 // ------------------------------------------------------------------ tiles of rows through shared memory
 // kDepth tiles of TT rows x W elements in flight: asynchronous 16-byte copies where base, stride and
 // first column allow them (the last piece of a row may be short: it is filled with zeros), plain

@@ -170,21 +170,16 @@ __global__ void __launch_bounds__(Lay<NS>::NT, 8) k_rev(BParams b) {
 }
 
 // Slot k: from what piece k sends to its left by itself to all that it sends (what piece k - 1 starts from).
-template <int NS> __global__ void __launch_bounds__(256) k_rev_join(BParams b) {
+template <int NS> __global__ void __launch_bounds__(kJoinThreads) k_rev_join(BParams b) {
     const Params& p = b.f;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = (int64_t)p.C * NS;
+    __shared__ uint32_t started[kJoinBits / 32];
+    mark_started(p, started);
+    const int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x, row = (int64_t)p.C * NS;
     if (i >= row) return;
-    const int64_t c = i / NS;
     const float a2 = p.A[i] * kLog2e;
-    float carry = b.rev[(p.pieces - 1) * row + i];
-#pragma unroll 4
-    for (int k = p.pieces - 2; k >= 1; --k) {
-        const bool started = p.cu[seq_of(p.cu, p.N, (k + 1) * p.piece - 1)] >= k * p.piece;
-        const float own = b.rev[k * row + i];
-        const float f = exp2_hw(a2 * b.rsum[(int64_t)k * p.C + c]);
-        carry = started ? own : fmaf(f, carry, own);
-        b.rev[k * row + i] = carry;
-    }
+    float* slot = b.rev + i;
+    const float* sum = b.rsum + i / NS;
+    join<-1>(p, started, p.pieces - 2, p.pieces - 2, a2, slot[(p.pieces - 1) * row], slot, sum, row);
 }
 
 // ------------------------------------------------------------------ the main kernel
@@ -528,7 +523,7 @@ cudaError_t backward_as(BParams& b, const kda_ssm_backward_args& a, cudaStream_t
         k_rev<T, NS><<<dim3((unsigned)(p.bpg * p.G), p.pieces - 1), Lay<NS>::NT, 0, s>>>(b);
         if ((e = cudaGetLastError())) return e;
         if (p.pieces > 2) {
-            k_rev_join<NS><<<(unsigned)(((int64_t)p.C * NS + 255) / 256), 256, 0, s>>>(b);
+            k_rev_join<NS><<<(unsigned)(((int64_t)p.C * NS + kJoinThreads - 1) / kJoinThreads), kJoinThreads, 0, s>>>(b);
             if ((e = cudaGetLastError())) return e;
         }
     }
@@ -552,8 +547,10 @@ SsmBackwardPlan ssm_backward_plan(const kda_ssm_args& f) {
     const int64_t sms = current_device_info(&di) ? di.sm_count : 1;
     const int64_t cg = f.C / f.G, ch = ch_of(f.Nst), blocks = f.G * ((cg + ch - 1) / ch);
     SsmBackwardPlan p{};
-    // Six blocks per SM, pieces of at least 64 tokens.
-    int64_t k = (6 * sms + blocks - 1) / blocks;
+    // Two blocks of the main kernel run on an SM and eight of the passes before it, of which it takes twice as many:
+    // up to four whole rounds of the former are two of the latter.  Pieces of at least 64 tokens.
+    int64_t k = 8 * sms / blocks;
+    if (k > kMaxPieces) k = kMaxPieces;
     if (k > f.T_total / 64) k = f.T_total / 64;
     if (k < 1) k = 1;
     p.piece = ((f.T_total + k - 1) / k + 7) / 8 * 8;

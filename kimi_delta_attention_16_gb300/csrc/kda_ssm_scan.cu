@@ -198,23 +198,16 @@ __global__ void __launch_bounds__(Lay<NS>::NT, 8) k_scan(Params p) {
     }
 }
 
-// The state at each piece's start, in the slots where the pieces left their own: carried state
-// times 2^(A log2 e sum of delta), unless a sequence started in the piece, plus the piece's own.
-template <int NS> __global__ void __launch_bounds__(256) k_scan_join(Params p) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = (int64_t)p.C * NS;
+// The state at each piece's start, in the slots where the pieces left their own: slot k + 1 holds what
+// piece k leaves by itself, and then what piece k + 1 starts from.
+template <int NS> __global__ void __launch_bounds__(kJoinThreads) k_scan_join(Params p) {
+    __shared__ uint32_t started[kJoinBits / 32];
+    mark_started(p, started);
+    const int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x, row = (int64_t)p.C * NS;
     if (i >= row) return;
-    const int64_t c = i / NS;
     const float a2 = p.A[i] * kLog2e;
-    float carry = p.ws_state[row + i];
-#pragma unroll 4
-    for (int k = 1; k < p.pieces - 1; ++k) {
-        const int64_t t1 = (k + 1) * p.piece;
-        const bool started = p.cu[seq_of(p.cu, p.N, t1 - 1)] >= k * p.piece;
-        const float own = p.ws_state[(k + 1) * row + i];
-        const float f = exp2_hw(a2 * p.ws_sum[(int64_t)k * p.C + c]);
-        carry = started ? own : fmaf(f, carry, own);
-        p.ws_state[(k + 1) * row + i] = carry;
-    }
+    float* slot = p.ws_state + row + i;  // of piece 0
+    join<1>(p, started, 1, p.pieces - 2, a2, *slot, slot, p.ws_sum + i / NS, row);
 }
 
 // One token per sequence: a thread holds 4 states of one channel and takes several sequences in turn,
@@ -311,7 +304,7 @@ template <typename T, int NS, int kMode> cudaError_t scan_as(Params& p, cudaStre
         k_scan<T, NS, kPiece><<<dim3(gx, p.pieces - 1), Y::NT, 0, s>>>(p);
         if (cudaError_t e = cudaGetLastError()) return e;
         if (p.pieces > 2) {
-            k_scan_join<NS><<<(unsigned)(((int64_t)p.C * NS + 255) / 256), 256, 0, s>>>(p);
+            k_scan_join<NS><<<(unsigned)(((int64_t)p.C * NS + kJoinThreads - 1) / kJoinThreads), kJoinThreads, 0, s>>>(p);
             if (cudaError_t e = cudaGetLastError()) return e;
         }
     }
@@ -377,8 +370,11 @@ ScanPlan scan_plan(const kda_ssm_args& a) {
     const int64_t tt = 8, cb = a.Nst <= 16 ? 64 : 1024 / a.Nst;  // Lay<Nst>'s tile and channels per block
     ScanPlan p{};
     const int64_t warps = a.G * ((a.C / a.G + cb - 1) / cb) * 2;
-    // Enough warps for 30 per SM, pieces of at least 8 tiles.
-    int64_t k = (30 * sms + warps - 1) / warps;
+    // Two whole rounds of blocks, of which eight run on an SM; pieces of at least 8 tiles.  (One piece of 8,192
+    // tokens x 12,288 channels leaves two thirds of the warp slots empty: 1.5 ms, against 0.8 ms in 12 pieces, the
+    // pass over their own states included.)
+    int64_t k = 16 * sms / (warps / 2);
+    if (k > kMaxPieces) k = kMaxPieces;
     const int64_t most = a.T_total / (8 * tt);
     if (k > most) k = most;
     if (k < 1) k = 1;
