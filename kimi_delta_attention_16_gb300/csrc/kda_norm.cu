@@ -33,16 +33,16 @@ __device__ __forceinline__ float warp_sum2(float a, float b) {  // a's sum in th
     for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-__device__ __forceinline__ void block_sum(float (&v)[1], float (*buf)[1]) {
-    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+template <int NT = 0> __device__ __forceinline__ void block_sum(float (&v)[1], float (*buf)[1]) {
+    const int lane = threadIdx.x & 31, nw = (NT ? NT : blockDim.x) >> 5;
     v[0] = warp_sum(v[0]);
     if (nw == 1) return;
     if (lane == 0) buf[threadIdx.x >> 5][0] = v[0];
     __syncthreads();
     v[0] = warp_sum(lane < nw ? buf[lane][0] : 0.f);
 }
-__device__ __forceinline__ void block_sum(float (&v)[2], float (*buf)[2]) {
-    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+template <int NT = 0> __device__ __forceinline__ void block_sum(float (&v)[2], float (*buf)[2]) {
+    const int lane = threadIdx.x & 31, nw = (NT ? NT : blockDim.x) >> 5;
     float s = warp_sum2(v[0], v[1]);
     if (nw > 1) {
         if ((lane & 15) == 0) buf[threadIdx.x >> 5][lane >> 4] = s;
@@ -55,8 +55,8 @@ __device__ __forceinline__ void block_sum(float (&v)[2], float (*buf)[2]) {
 }
 
 // Column of access i of this thread (in elements): consecutive threads take consecutive accesses.
-template <int W> __device__ __forceinline__ int col_of(int i) {
-    return (i * (int)blockDim.x + (int)threadIdx.x) * W;
+template <int W, int NT = 0> __device__ __forceinline__ int col_of(int i) {  // NT: threads of the block, 0 when it varies
+    return (i * (NT ? NT : (int)blockDim.x) + (int)threadIdx.x) * W;
 }
 
 template <typename T, int W, int VPT>
@@ -131,8 +131,8 @@ __device__ __forceinline__ float warp_sum4(float a, float b, float c, float d) {
     for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-__device__ __forceinline__ void block_sum4(float (&v)[4], float (*buf)[4]) {
-    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+template <int NT> __device__ __forceinline__ void block_sum4(float (&v)[4], float (*buf)[4]) {
+    const int lane = threadIdx.x & 31, nw = NT >> 5;
     float s = warp_sum4(v[0], v[1], v[2], v[3]);
     if (nw > 1) {
         if ((lane & 7) == 0) buf[threadIdx.x >> 5][((lane >> 4) & 1) + ((lane >> 2) & 2)] = s;
@@ -148,49 +148,74 @@ __device__ __forceinline__ void block_sum4(float (&v)[4], float (*buf)[4]) {
 __device__ __forceinline__ float f2_sum(f2 v) { return f2_lo(v) + f2_hi(v); }
 
 // Threads that a block of the row kernels may have: what leaves a thread the registers it needs.
-// Threads of a block of the row kernels: 72 registers for each leave two blocks to an SM.
+// Threads of a block of the row kernels: fixed, so that every offset in the ring is a constant; 448 with 72
+// registers each leave two blocks to an SM.
 constexpr int kRowThreads = 448;
+constexpr int row_blocks(int nt) { return 2 * kRowThreads / nt > 8 ? 8 : 2 * kRowThreads / nt; }
+struct RowShape {
+    int vpt, nt;  // accesses per thread, threads
+};
+RowShape row_shape(int64_t n) {  // for n accesses per row, at most 2 kRowThreads
+    if (n > kRowThreads) return {2, kRowThreads};
+    for (int nt : {64, 128, 256})
+        if (n <= nt) return {1, nt};
+    return {1, kRowThreads};
+}
+#define KDA_ROW_SHAPES(h, X)             \
+    if (h.vpt == 2) { X(2, kRowThreads); } \
+    else if (h.nt == 64) { X(1, 64); }     \
+    else if (h.nt == 128) { X(1, 128); }   \
+    else if (h.nt == 256) { X(1, 256); }   \
+    else { X(1, kRowThreads); }
 __device__ __forceinline__ float rstd_of(float v) {  // 1 / sqrt(v): the hardware's value and one Newton step
     const float r = rsqrtf(v);
     return r * fmaf(-0.5f * v * r, r, 1.5f);
 }
 
-template <typename T, int W, int VPT, int R>
-__global__ void __launch_bounds__(kRowThreads, 2)
+template <typename T, int W, int VPT, int R, int NT>
+__global__ void __launch_bounds__(NT, row_blocks(NT))
 k_layer_norm_rows(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const float* __restrict__ b, float eps,
                   T* __restrict__ y, int64_t ys, float* __restrict__ stats, int64_t M, int C) {
     constexpr int P = W / 2;
     extern __shared__ __align__(16) unsigned char shared[];
-    Raw<T, W>* ring = reinterpret_cast<Raw<T, W>*>(shared) + threadIdx.x;  // [kDepth][R][VPT][blockDim.x]
     __shared__ __align__(8) float red[2][kMaxWarps][2];
     const float inv_c = 1.0f / (float)C;
+    bool in[VPT];  // whether this thread's access i lies inside a row
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) in[i] = col_of<W, NT>(i) < C;
     f2 wv[VPT][P], bv[VPT][P];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = col_of<W>(i);
+        const int c = col_of<W, NT>(i);
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-            wv[i][j] = w && c < C ? f2_of(w[c + 2 * j], w[c + 2 * j + 1]) : f2_dup(1.f);
-            bv[i][j] = b && c < C ? f2_of(b[c + 2 * j], b[c + 2 * j + 1]) : f2_dup(0.f);
+            wv[i][j] = w && in[i] ? f2_of(w[c + 2 * j], w[c + 2 * j + 1]) : f2_dup(1.f);
+            bv[i][j] = b && in[i] ? f2_of(b[c + 2 * j], b[c + 2 * j + 1]) : f2_dup(0.f);
         }
     }
-    auto issue = [&](int64_t r0, int slot) {  // rows r0, r0 + gridDim.x, ..
+    // The ring: kDepth slots of R rows; a thread's access i of row k lies at slot + (k VPT + i) NT.
+    constexpr int kSlot = R * VPT * NT;
+    Raw<T, W>* const ring = reinterpret_cast<Raw<T, W>*>(shared) + threadIdx.x;
+    const int64_t row_step = (int64_t)gridDim.x, step = R * row_step;
+    const T* src = x + blockIdx.x * xs + threadIdx.x * W;  // the row that is copied next
+    int64_t src_row = blockIdx.x;
+    int put = 0, get = 0;  // slots
+    auto issue = [&]() {
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const int64_t r = r0 + (int64_t)k * gridDim.x;
-            if (r < M)
+            if (src_row < M)
 #pragma unroll
-                for (int i = 0; i < VPT; ++i) {
-                    const int c = col_of<W>(i);
-                    if (c < C) cp_async_raw<T, W>(ring + ((slot * R + k) * VPT + i) * blockDim.x, x + r * xs + c);
-                }
+                for (int i = 0; i < VPT; ++i)
+                    if (in[i]) cp_async_raw<T, W>(ring + put + (k * VPT + i) * NT, src + i * NT * W);
+            src += row_step * xs;
+            src_row += row_step;
         }
         cp_commit();
+        put = put + kSlot == kDepth * kSlot ? 0 : put + kSlot;
     };
-    const int64_t step = (int64_t)R * gridDim.x;
 #pragma unroll
-    for (int d = 0; d < kDepth - 1; ++d) issue(blockIdx.x + d * step, d);
-    int slot = 0;
+    for (int d = 0; d < kDepth - 1; ++d) issue();
+    T* dst = y + blockIdx.x * ys + threadIdx.x * W;
     for (int64_t r0 = blockIdx.x; r0 < M; r0 += step) {
         cp_wait<kDepth - 2>();
         // Each of the three passes reads the rows from the ring again: registers for them would halve the blocks.
@@ -200,25 +225,25 @@ k_layer_norm_rows(const T* __restrict__ x, int64_t xs, const float* __restrict__
             f2 t = f2_dup(0.f);
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
-                if (col_of<W>(i) < C) {
+                if (in[i]) {
                     f2 v[P];
-                    unraw2(ring[((slot * R + k) * VPT + i) * blockDim.x], v);
+                    unraw2(ring[get + (k * VPT + i) * NT], v);
 #pragma unroll
                     for (int j = 0; j < P; ++j) t = add2(t, v[j]);
                 }
             s[k] = f2_sum(t);
         }
-        issue(r0 + (kDepth - 1) * step, (slot + kDepth - 1) % kDepth);
-        block_sum(s, red[0]);
+        issue();
+        block_sum<NT>(s, red[0]);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             mean[k] = s[k] * inv_c;
             f2 t = f2_dup(0.f);
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
-                if (col_of<W>(i) < C) {
+                if (in[i]) {
                     f2 v[P];
-                    unraw2(ring[((slot * R + k) * VPT + i) * blockDim.x], v);
+                    unraw2(ring[get + (k * VPT + i) * NT], v);
 #pragma unroll
                     for (int j = 0; j < P; ++j) {
                         v[j] = add2(v[j], f2_dup(-mean[k]));
@@ -227,19 +252,18 @@ k_layer_norm_rows(const T* __restrict__ x, int64_t xs, const float* __restrict__
                 }
             s[k] = f2_sum(t);
         }
-        block_sum(s, red[1]);
+        block_sum<NT>(s, red[1]);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const int64_t r = r0 + (int64_t)k * gridDim.x;
+            const int64_t r = r0 + k * row_step;
             if (r >= M) break;
             const float rstd = rstd_of(fmaf(s[k], inv_c, eps));
             if (stats && threadIdx.x == 0) *reinterpret_cast<float2*>(stats + 2 * r) = make_float2(mean[k], rstd);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int c = col_of<W>(i);
-                if (c >= C) continue;
+                if (!in[i]) continue;
                 f2 v[P];
-                unraw2(ring[((slot * R + k) * VPT + i) * blockDim.x], v);
+                unraw2(ring[get + (k * VPT + i) * NT], v);
                 float o[W];
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
@@ -247,10 +271,11 @@ k_layer_norm_rows(const T* __restrict__ x, int64_t xs, const float* __restrict__
                     o[2 * j] = f2_lo(n);
                     o[2 * j + 1] = f2_hi(n);
                 }
-                store_row(y + r * ys + c, o);
+                store_row(dst + i * NT * W, o);
             }
+            dst += row_step * ys;
         }
-        slot = (slot + 1) % kDepth;
+        get = get + kSlot == kDepth * kSlot ? 0 : get + kSlot;
     }
 }
 
@@ -343,95 +368,106 @@ k_layer_norm_bwd(const T* __restrict__ dy, int64_t dys, const void* __restrict__
 }
 
 // The gradient of many rows in 16-byte layouts, as the forward takes them.
-template <typename T, bool X8, int W, int VPT, int R>
-__global__ void __launch_bounds__(kRowThreads, 2)
+template <typename T, bool X8, int W, int VPT, int R, int NT>
+__global__ void __launch_bounds__(NT, row_blocks(NT))
 k_layer_norm_bwd_rows(const T* __restrict__ dy, int64_t dys, const void* __restrict__ xv, int64_t xs,
                       const uint8_t* __restrict__ scales, const float* __restrict__ stats, const float* __restrict__ w,
                       T* __restrict__ dx, int64_t dxs, float* __restrict__ part, int64_t M, int C) {
     using XT = typename std::conditional<X8, uint8_t, T>::type;
     constexpr int P = W / 2;
     extern __shared__ __align__(16) unsigned char shared[];
-    Raw<T, W>* ring_y = reinterpret_cast<Raw<T, W>*>(shared) + threadIdx.x;  // [kDepth][R][VPT][blockDim.x], both
-    Raw<XT, W>* ring_x =
-        reinterpret_cast<Raw<XT, W>*>(shared + (size_t)kDepth * R * VPT * blockDim.x * sizeof(Raw<T, W>)) + threadIdx.x;
     __shared__ __align__(16) float red[2][kMaxWarps][4];
     const XT* x = static_cast<const XT*>(xv);
     const int nb = (C + KDA_PACK8_BLOCK - 1) / KDA_PACK8_BLOCK;
     const float inv_c = 1.0f / (float)C;
+    bool in[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) in[i] = col_of<W, NT>(i) < C;
     f2 wv[VPT][P], dw[VPT][P], db[VPT][P];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = col_of<W>(i);
+        const int c = col_of<W, NT>(i);
 #pragma unroll
         for (int j = 0; j < P; ++j) {
             dw[i][j] = db[i][j] = f2_dup(0.f);
-            wv[i][j] = w && c < C ? f2_of(w[c + 2 * j], w[c + 2 * j + 1]) : f2_dup(1.f);
+            wv[i][j] = w && in[i] ? f2_of(w[c + 2 * j], w[c + 2 * j + 1]) : f2_dup(1.f);
         }
     }
-    auto issue = [&](int64_t r0, int slot) {
+    // Two rings, of dy and x, laid out as the forward's.
+    constexpr int kSlot = R * VPT * NT;
+    Raw<T, W>* const ring_y = reinterpret_cast<Raw<T, W>*>(shared) + threadIdx.x;
+    Raw<XT, W>* const ring_x = reinterpret_cast<Raw<XT, W>*>(shared + kDepth * kSlot * sizeof(Raw<T, W>)) + threadIdx.x;
+    const int64_t row_step = (int64_t)gridDim.x, step = R * row_step, x_step = X8 ? (int64_t)C : xs;
+    const XT* src_x = x + blockIdx.x * x_step + threadIdx.x * W;
+    const T* src_y = dy + blockIdx.x * dys + threadIdx.x * W;
+    int put = 0, get = 0;  // slots
+    auto issue = [&](int64_t r) {  // rows r, r + gridDim.x, ..
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const int64_t r = r0 + (int64_t)k * gridDim.x;
-            if (r < M)
+            if (r + k * row_step < M)
 #pragma unroll
-                for (int i = 0; i < VPT; ++i) {
-                    const int c = col_of<W>(i), at = ((slot * R + k) * VPT + i) * blockDim.x;
-                    if (c < C) {
-                        cp_async_raw<XT, W>(ring_x + at, x + r * (X8 ? (int64_t)C : xs) + c);
-                        cp_async_raw<T, W>(ring_y + at, dy + r * dys + c);
+                for (int i = 0; i < VPT; ++i)
+                    if (in[i]) {
+                        cp_async_raw<XT, W>(ring_x + put + (k * VPT + i) * NT, src_x + i * NT * W);
+                        cp_async_raw<T, W>(ring_y + put + (k * VPT + i) * NT, src_y + i * NT * W);
                     }
-                }
+            src_x += row_step * x_step;
+            src_y += row_step * dys;
         }
         cp_commit();
+        put = put + kSlot == kDepth * kSlot ? 0 : put + kSlot;
     };
     uint32_t sr[R][VPT];
     float2 st[R];
-    auto small = [&](int64_t r0) {  // what the next rows need besides: their statistics and their blocks' scales
+    const float2* src_st = reinterpret_cast<const float2*>(stats) + blockIdx.x;
+    const uint8_t* src_sc = scales + blockIdx.x * (int64_t)nb;
+    auto small = [&](int64_t r) {  // what the next rows need besides: their statistics and their blocks' scales
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const int64_t r = r0 + (int64_t)k * gridDim.x;
             st[k] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) sr[k][i] = 127;
-            if (r >= M) continue;
-            st[k] = __ldg(reinterpret_cast<const float2*>(stats + 2 * r));
-            if (X8)
+            if (r + k * row_step < M) {
+                st[k] = __ldg(src_st);
+                if (X8)
 #pragma unroll
-                for (int i = 0; i < VPT; ++i)
-                    if (col_of<W>(i) < C) sr[k][i] = (uint32_t)__ldg(scales + r * nb + col_of<W>(i) / KDA_PACK8_BLOCK);
+                    for (int i = 0; i < VPT; ++i)
+                        if (in[i]) sr[k][i] = (uint32_t)__ldg(src_sc + col_of<W, NT>(i) / KDA_PACK8_BLOCK);
+            }
+            src_st += row_step;
+            if (X8) src_sc += row_step * nb;
         }
     };
-    const int64_t step = (int64_t)R * gridDim.x;
 #pragma unroll
-    for (int d = 0; d < kDepth - 1; ++d) issue(blockIdx.x + d * step, d);
+    for (int d = 0; d < kDepth - 1; ++d) issue(blockIdx.x + d * step);
     small(blockIdx.x);
-    int slot = 0, buf = 0;
+    int buf = 0;
+    T* dst = dx + blockIdx.x * dxs + threadIdx.x * W;
     for (int64_t r0 = blockIdx.x; r0 < M; r0 += step) {
         cp_wait<kDepth - 2>();
-        float2 at_st[R];
-        uint32_t at_sr[R][VPT];
+        float rs[R], sh[R];  // 1 / deviation and -mean / deviation
+        uint32_t sc[R][VPT];
         float s[4] = {0.f, 0.f, 0.f, 0.f};
-        // xh and dy weight of one access, from the ring: read once for the sums and once for dx, since registers for
+        // xh and dy of one access, from the ring: read once for the sums and once for dx, since registers for
         // them would halve the blocks.
         auto terms = [&](int k, int i, f2 (&xh)[P], f2 (&d)[P]) {
-            const int at = ((slot * R + k) * VPT + i) * blockDim.x;
-            unraw2(ring_x[at], xh);
-            unraw2(ring_y[at], d);
-            const f2 shift = f2_dup(-at_st[k].x * at_st[k].y);
-            const f2 m = f2_dup(X8 ? scale_of_byte(at_sr[k][i]) * at_st[k].y : at_st[k].y);
+            unraw2(ring_x[get + (k * VPT + i) * NT], xh);
+            unraw2(ring_y[get + (k * VPT + i) * NT], d);
+            const f2 m = f2_dup(X8 ? scale_of_byte(sc[k][i]) * rs[k] : rs[k]), shift = f2_dup(sh[k]);
 #pragma unroll
             for (int j = 0; j < P; ++j) xh[j] = fma2(xh[j], m, shift);
         };
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            at_st[k] = st[k];
+            rs[k] = st[k].y;
+            sh[k] = -st[k].x * st[k].y;
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) at_sr[k][i] = sr[k][i];
-            if (r0 + (int64_t)k * gridDim.x >= M) continue;  // its slot holds no row
+            for (int i = 0; i < VPT; ++i) sc[k][i] = sr[k][i];
+            if (R > 1 && r0 + k * row_step >= M) continue;  // its slot holds no row
             f2 a = f2_dup(0.f), b = f2_dup(0.f);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                if (col_of<W>(i) >= C) continue;
+                if (!in[i]) continue;
                 f2 xh[P], d[P];
                 terms(k, i, xh, d);
 #pragma unroll
@@ -446,27 +482,24 @@ k_layer_norm_bwd_rows(const T* __restrict__ dy, int64_t dys, const void* __restr
             s[2 * k] = f2_sum(a);
             s[2 * k + 1] = f2_sum(b);
         }
-        issue(r0 + (kDepth - 1) * step, (slot + kDepth - 1) % kDepth);
+        issue(r0 + (kDepth - 1) * step);
         small(r0 + step);
         if constexpr (R == 1) {
             float t[2] = {s[0], s[1]};
-            block_sum(t, reinterpret_cast<float(*)[2]>(red[buf]));
+            block_sum<NT>(t, reinterpret_cast<float(*)[2]>(red[buf]));
             s[0] = t[0];
             s[1] = t[1];
         } else {
-            block_sum4(s, red[buf]);
+            block_sum4<NT>(s, red[buf]);
         }
         buf ^= 1;
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const int64_t r = r0 + (int64_t)k * gridDim.x;
-            if (r >= M) break;
-            const float rs = at_st[k].y;
-            const f2 m0 = f2_dup(-s[2 * k] * inv_c * rs), m1 = f2_dup(-s[2 * k + 1] * inv_c * rs), rr = f2_dup(rs);
+            if (R > 1 && r0 + k * row_step >= M) break;
+            const f2 m0 = f2_dup(-s[2 * k] * inv_c * rs[k]), m1 = f2_dup(-s[2 * k + 1] * inv_c * rs[k]), rr = f2_dup(rs[k]);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int c = col_of<W>(i);
-                if (c >= C) continue;
+                if (!in[i]) continue;
                 f2 xh[P], d[P];
                 terms(k, i, xh, d);
                 float o[W];
@@ -476,16 +509,17 @@ k_layer_norm_bwd_rows(const T* __restrict__ dy, int64_t dys, const void* __restr
                     o[2 * j] = f2_lo(v);
                     o[2 * j + 1] = f2_hi(v);
                 }
-                store_row(dx + r * dxs + c, o);
+                store_row(dst + i * NT * W, o);
             }
+            dst += row_step * dxs;
         }
-        slot = (slot + 1) % kDepth;
+        get = get + kSlot == kDepth * kSlot ? 0 : get + kSlot;
     }
     if (!part) return;
     float* pw = part + (int64_t)blockIdx.x * 2 * C;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = col_of<W>(i);
+        const int c = col_of<W, NT>(i);
         if (c >= C) continue;
 #pragma unroll
         for (int j = 0; j < P; ++j) {
@@ -535,21 +569,19 @@ cudaError_t launch_layer_norm(const kda_norm_args& a, cudaStream_t s) {
     DeviceInfo di{0, 0, 0};
     const int sms = current_device_info(&di) ? di.sm_count : 1;
     if (vec && n <= 2 * kRowThreads) {
-        const int row_v = n <= kRowThreads / 2 ? 1 : 2;
-        const int rt = warps32((n + row_v - 1) / row_v);
-        const size_t smem = (size_t)kDepth * 2 * row_v * rt * 16;
-        const int per_sm = 2 * kRowThreads / rt;
+        const RowShape h = row_shape(n);
+        const int smem = kDepth * 2 * h.vpt * h.nt * 16, per_sm = row_blocks(h.nt);
         if (a.M >= 4 * (int64_t)sms * per_sm) {
             cudaError_t e = cudaSuccess;
-#define KDA_LNR(T, W, V)                                                                                             \
-    if (!(e = cudaFuncSetAttribute(k_layer_norm_rows<T, W, V, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))) \
-        k_layer_norm_rows<T, W, V, 2><<<sms * per_sm, rt, smem, s>>>(static_cast<const T*>(a.x), xs, a.weight, a.bias, \
-                                                                  a.eps, static_cast<T*>(a.y), ys, a.stats, a.M, a.C)
-            if (a.io == KDA_BF16) {
-                if (row_v == 1) { KDA_LNR(bf16, 8, 1); } else { KDA_LNR(bf16, 8, 2); }
-            } else {
-                if (row_v == 1) { KDA_LNR(float, 4, 1); } else { KDA_LNR(float, 4, 2); }
-            }
+#define KDA_LNR(T, W, V, NT)                                                                                         \
+    if (!(e = cudaFuncSetAttribute(k_layer_norm_rows<T, W, V, 2, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) \
+        k_layer_norm_rows<T, W, V, 2, NT><<<sms * per_sm, NT, smem, s>>>(                                            \
+            static_cast<const T*>(a.x), xs, a.weight, a.bias, a.eps, static_cast<T*>(a.y), ys, a.stats, a.M, a.C)
+#define KDA_LNR_B(V, NT) KDA_LNR(bf16, 8, V, NT)
+#define KDA_LNR_F(V, NT) KDA_LNR(float, 4, V, NT)
+            if (a.io == KDA_BF16) { KDA_ROW_SHAPES(h, KDA_LNR_B) } else { KDA_ROW_SHAPES(h, KDA_LNR_F) }
+#undef KDA_LNR_F
+#undef KDA_LNR_B
 #undef KDA_LNR
             return e ? e : cudaGetLastError();
         }
@@ -602,9 +634,7 @@ NormBackwardPlan norm_backward_plan(const kda_norm_backward_args& a) {
     // Blocks that fill an SM's threads when the layout allows 16-byte accesses (known only once the
     // pointers are; the sizes alone have to fix the workspace).
     const int vw = a.io == KDA_BF16 ? 8 : 4, acc = (a.C + vw - 1) / vw;
-    const int nt = warps32(acc <= kRowThreads / 2 ? acc : (acc + 1) / 2);
-    int per_sm = nt <= kRowThreads ? 2 * kRowThreads / nt : 1;
-    if (per_sm > 8) per_sm = 8;
+    const int per_sm = acc <= 2 * kRowThreads ? row_blocks(row_shape(acc).nt) : 1;
     const int64_t most = (int64_t)sms * per_sm;
     p.blocks = (int)(a.M < most ? a.M : most);
     p.workspace = (a.dweight || a.dbias) ? (size_t)p.blocks * 2 * a.C * sizeof(float) : 0;
@@ -620,22 +650,27 @@ cudaError_t launch_layer_norm_backward(const kda_norm_backward_args& a, const No
     const int es = a.io == KDA_BF16 ? 2 : 4;
     const int acc = a.C / (16 / es);  // accesses per row, where the layout is wide
     if (h.vec && acc <= 2 * kRowThreads) {
-        const int v = acc <= kRowThreads / 2 ? 1 : 2, rows = 3 - v, nt = warps32((acc + v - 1) / v);
-        const size_t smem = (size_t)kDepth * rows * v * nt * (16 + (a.x_scales ? 16 / es : 16));
-#define KDA_LNBR(T, X8, W, V)                                                                                        \
-    if (!(e = cudaFuncSetAttribute(k_layer_norm_bwd_rows<T, X8, W, V, 3 - V>,                                        \
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))                         \
-        k_layer_norm_bwd_rows<T, X8, W, V, 3 - V><<<p.blocks, nt, smem, s>>>(static_cast<const T*>(a.dy), dys, a.x, xs, \
-                                                                      a.x_scales, a.stats, a.weight,                 \
-                                                                      static_cast<T*>(a.dx), dxs, part, a.M, a.C)
-#define KDA_LNBR_X(T, W)                                                                                             \
-    if (a.x_scales) {                                                                                                \
-        if (v == 1) { KDA_LNBR(T, true, W, 1); } else { KDA_LNBR(T, true, W, 2); }                                   \
-    } else {                                                                                                         \
-        if (v == 1) { KDA_LNBR(T, false, W, 1); } else { KDA_LNBR(T, false, W, 2); }                                 \
-    }
-        if (a.io == KDA_BF16) { KDA_LNBR_X(bf16, 8) } else { KDA_LNBR_X(float, 4) }
-#undef KDA_LNBR_X
+        const RowShape r = row_shape(acc);
+        const int smem = kDepth * (3 - r.vpt) * r.vpt * r.nt * (16 + (a.x_scales ? 16 / es : 16));
+#define KDA_LNBR(T, X8, W, V, NT)                                                                                    \
+    if (!(e = cudaFuncSetAttribute(k_layer_norm_bwd_rows<T, X8, W, V, 3 - V, NT>,                                    \
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))                              \
+        k_layer_norm_bwd_rows<T, X8, W, V, 3 - V, NT><<<p.blocks, NT, smem, s>>>(                                    \
+            static_cast<const T*>(a.dy), dys, a.x, xs, a.x_scales, a.stats, a.weight, static_cast<T*>(a.dx), dxs, part, \
+            a.M, a.C)
+#define KDA_LNBR_B8(V, NT) KDA_LNBR(bf16, true, 8, V, NT)
+#define KDA_LNBR_B(V, NT) KDA_LNBR(bf16, false, 8, V, NT)
+#define KDA_LNBR_F8(V, NT) KDA_LNBR(float, true, 4, V, NT)
+#define KDA_LNBR_F(V, NT) KDA_LNBR(float, false, 4, V, NT)
+        if (a.io == KDA_BF16) {
+            if (a.x_scales) { KDA_ROW_SHAPES(r, KDA_LNBR_B8) } else { KDA_ROW_SHAPES(r, KDA_LNBR_B) }
+        } else {
+            if (a.x_scales) { KDA_ROW_SHAPES(r, KDA_LNBR_F8) } else { KDA_ROW_SHAPES(r, KDA_LNBR_F) }
+        }
+#undef KDA_LNBR_F
+#undef KDA_LNBR_F8
+#undef KDA_LNBR_B
+#undef KDA_LNBR_B8
 #undef KDA_LNBR
         if (!e) e = cudaGetLastError();
         if (e || !part) return e;

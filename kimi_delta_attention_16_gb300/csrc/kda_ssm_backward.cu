@@ -547,9 +547,10 @@ SsmBackwardPlan ssm_backward_plan(const kda_ssm_args& f) {
     const int64_t sms = current_device_info(&di) ? di.sm_count : 1;
     const int64_t cg = f.C / f.G, ch = ch_of(f.Nst), blocks = f.G * ((cg + ch - 1) / ch);
     SsmBackwardPlan p{};
-    // Two blocks of the main kernel run on an SM and eight of the passes before it, of which it takes twice as many:
-    // up to four whole rounds of the former are two of the latter.  Pieces of at least 64 tokens.
-    int64_t k = 8 * sms / blocks;
+    // Two blocks of the main kernel run on an SM and eight of the passes before it, of which there are twice as many:
+    // two whole rounds of the former are one of the latter (4,096 tokens x 4,096 channels x 16: 0.71 ms for forward
+    // and gradients, 0.74 to 0.77 with one, three, four or six rounds).  Pieces of at least 64 tokens.
+    int64_t k = 4 * sms / blocks;
     if (k > kMaxPieces) k = kMaxPieces;
     if (k > f.T_total / 64) k = f.T_total / 64;
     if (k < 1) k = 1;
