@@ -148,24 +148,35 @@ template <int NT> __device__ __forceinline__ void block_sum4(float (&v)[4], floa
 __device__ __forceinline__ float f2_sum(f2 v) { return f2_lo(v) + f2_hi(v); }
 
 // Threads that a block of the row kernels may have: what leaves a thread the registers it needs.
-// Threads of a block of the row kernels: fixed, so that every offset in the ring is a constant; 448 with 72
-// registers each leave two blocks to an SM.
+// Shapes of the row kernels: accesses per thread and threads, fixed so that every offset in the ring is a
+// constant.  448 threads of 72 registers leave two blocks to an SM (7,168 bf16 channels: 2 x 448 accesses); up
+// to 1,792 accesses take four per thread.  Wider rows go through the kernels above, one at a time.
 constexpr int kRowThreads = 448;
-constexpr int row_blocks(int nt) { return 2 * kRowThreads / nt > 8 ? 8 : 2 * kRowThreads / nt; }
+constexpr int kRowAccesses = 4 * kRowThreads;
+constexpr int row_blocks(int nt, int vpt) {
+    const int b = vpt == 4 ? 512 / nt : 2 * kRowThreads / nt;
+    return b < 1 ? 1 : b > 8 ? 8 : b;
+}
 struct RowShape {
-    int vpt, nt;  // accesses per thread, threads
+    int vpt, nt;
 };
-RowShape row_shape(int64_t n) {  // for n accesses per row, at most 2 kRowThreads
-    if (n > kRowThreads) return {2, kRowThreads};
+RowShape row_shape(int64_t n) {  // for n accesses per row, at most kRowAccesses
+    if (n > 4 * 256) return {4, kRowThreads};
+    if (n > 2 * kRowThreads) return {4, 256};
+    if (n > 2 * 256) return {2, kRowThreads};
+    if (n > kRowThreads) return {2, 256};
     for (int nt : {64, 128, 256})
         if (n <= nt) return {1, nt};
     return {1, kRowThreads};
 }
-#define KDA_ROW_SHAPES(h, X)             \
-    if (h.vpt == 2) { X(2, kRowThreads); } \
-    else if (h.nt == 64) { X(1, 64); }     \
-    else if (h.nt == 128) { X(1, 128); }   \
-    else if (h.nt == 256) { X(1, 256); }   \
+#define KDA_ROW_SHAPES(h, X)                             \
+    if (h.vpt == 4 && h.nt == 256) { X(4, 256); }        \
+    else if (h.vpt == 4) { X(4, kRowThreads); }          \
+    else if (h.vpt == 2 && h.nt == 256) { X(2, 256); }   \
+    else if (h.vpt == 2) { X(2, kRowThreads); }          \
+    else if (h.nt == 64) { X(1, 64); }                   \
+    else if (h.nt == 128) { X(1, 128); }                 \
+    else if (h.nt == 256) { X(1, 256); }                 \
     else { X(1, kRowThreads); }
 __device__ __forceinline__ float rstd_of(float v) {  // 1 / sqrt(v): the hardware's value and one Newton step
     const float r = rsqrtf(v);
@@ -173,7 +184,7 @@ __device__ __forceinline__ float rstd_of(float v) {  // 1 / sqrt(v): the hardwar
 }
 
 template <typename T, int W, int VPT, int R, int NT>
-__global__ void __launch_bounds__(NT, row_blocks(NT))
+__global__ void __launch_bounds__(NT, row_blocks(NT, VPT))
 k_layer_norm_rows(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const float* __restrict__ b, float eps,
                   T* __restrict__ y, int64_t ys, float* __restrict__ stats, int64_t M, int C) {
     constexpr int P = W / 2;
@@ -199,6 +210,15 @@ k_layer_norm_rows(const T* __restrict__ x, int64_t xs, const float* __restrict__
     const int64_t row_step = (int64_t)gridDim.x, step = R * row_step;
     const T* src = x + blockIdx.x * xs + threadIdx.x * W;  // the row that is copied next
     int64_t src_row = blockIdx.x;
+    auto row_sum = [&](float (&v)[2], int b) {
+        if constexpr (R == 2) {
+            block_sum<NT>(v, red[b]);
+        } else {
+            float one[1] = {v[0]};
+            block_sum<NT>(one, reinterpret_cast<float(*)[1]>(red[b]));
+            v[0] = one[0];
+        }
+    };
     int put = 0, get = 0;  // slots
     auto issue = [&]() {
 #pragma unroll
@@ -234,7 +254,7 @@ k_layer_norm_rows(const T* __restrict__ x, int64_t xs, const float* __restrict__
             s[k] = f2_sum(t);
         }
         issue();
-        block_sum<NT>(s, red[0]);
+        row_sum(s, 0);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             mean[k] = s[k] * inv_c;
@@ -252,7 +272,7 @@ k_layer_norm_rows(const T* __restrict__ x, int64_t xs, const float* __restrict__
                 }
             s[k] = f2_sum(t);
         }
-        block_sum<NT>(s, red[1]);
+        row_sum(s, 1);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             const int64_t r = r0 + k * row_step;
@@ -369,10 +389,10 @@ k_layer_norm_bwd(const T* __restrict__ dy, int64_t dys, const void* __restrict__
 
 // The gradient of many rows in 16-byte layouts, as the forward takes them.
 template <typename T, bool X8, int W, int VPT, int R, int NT>
-__global__ void __launch_bounds__(NT, row_blocks(NT))
-k_layer_norm_bwd_rows(const T* __restrict__ dy, int64_t dys, const void* __restrict__ xv, int64_t xs,
+__global__ void __launch_bounds__(NT, row_blocks(NT, VPT))
+k_layer_norm_bwd_rows(const T* __restrict__ dy, uint32_t dys, const void* __restrict__ xv, uint32_t xs,
                       const uint8_t* __restrict__ scales, const float* __restrict__ stats, const float* __restrict__ w,
-                      T* __restrict__ dx, int64_t dxs, float* __restrict__ part, int64_t M, int C) {
+                      T* __restrict__ dx, uint32_t dxs, float* __restrict__ part, int M, int C) {
     using XT = typename std::conditional<X8, uint8_t, T>::type;
     constexpr int P = W / 2;
     extern __shared__ __align__(16) unsigned char shared[];
@@ -397,53 +417,57 @@ k_layer_norm_bwd_rows(const T* __restrict__ dy, int64_t dys, const void* __restr
     constexpr int kSlot = R * VPT * NT;
     Raw<T, W>* const ring_y = reinterpret_cast<Raw<T, W>*>(shared) + threadIdx.x;
     Raw<XT, W>* const ring_x = reinterpret_cast<Raw<XT, W>*>(shared + kDepth * kSlot * sizeof(Raw<T, W>)) + threadIdx.x;
-    const int64_t row_step = (int64_t)gridDim.x, step = R * row_step, x_step = X8 ? (int64_t)C : xs;
-    const XT* src_x = x + blockIdx.x * x_step + threadIdx.x * W;
-    const T* src_y = dy + blockIdx.x * dys + threadIdx.x * W;
+    // Rows are counted in 32 bits and strides in bytes below 4 GB: a row's address is one instruction, and no
+    // running pointer holds registers.
+    const int row_step = gridDim.x, step = R * row_step;
+    const XT* tx = x + threadIdx.x * W;
+    const T* ty = dy + threadIdx.x * W;
+    T* tdx = dx + threadIdx.x * W;
+    auto at = [](auto* base, int r, uint32_t bytes) {
+        return reinterpret_cast<decltype(base)>(reinterpret_cast<uintptr_t>(base) + (uint64_t)(uint32_t)r * bytes);
+    };
     int put = 0, get = 0;  // slots
-    auto issue = [&](int64_t r) {  // rows r, r + gridDim.x, ..
+    auto issue = [&](int r0) {  // rows r0, r0 + gridDim.x, ..
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            if (r + k * row_step < M)
+            const int r = r0 + k * row_step;
+            if (r < M) {
+                const XT* sx = at(tx, r, xs);
+                const T* sy = at(ty, r, dys);
 #pragma unroll
                 for (int i = 0; i < VPT; ++i)
                     if (in[i]) {
-                        cp_async_raw<XT, W>(ring_x + put + (k * VPT + i) * NT, src_x + i * NT * W);
-                        cp_async_raw<T, W>(ring_y + put + (k * VPT + i) * NT, src_y + i * NT * W);
+                        cp_async_raw<XT, W>(ring_x + put + (k * VPT + i) * NT, sx + i * NT * W);
+                        cp_async_raw<T, W>(ring_y + put + (k * VPT + i) * NT, sy + i * NT * W);
                     }
-            src_x += row_step * x_step;
-            src_y += row_step * dys;
+            }
         }
         cp_commit();
         put = put + kSlot == kDepth * kSlot ? 0 : put + kSlot;
     };
     uint32_t sr[R][VPT];
     float2 st[R];
-    const float2* src_st = reinterpret_cast<const float2*>(stats) + blockIdx.x;
-    const uint8_t* src_sc = scales + blockIdx.x * (int64_t)nb;
-    auto small = [&](int64_t r) {  // what the next rows need besides: their statistics and their blocks' scales
+    auto small = [&](int r0) {  // what the next rows need besides: their statistics and their blocks' scales
 #pragma unroll
         for (int k = 0; k < R; ++k) {
+            const int r = r0 + k * row_step;
             st[k] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) sr[k][i] = 127;
-            if (r + k * row_step < M) {
-                st[k] = __ldg(src_st);
+            if (r < M) {
+                st[k] = __ldg(at(reinterpret_cast<const float2*>(stats), r, 8));
                 if (X8)
 #pragma unroll
                     for (int i = 0; i < VPT; ++i)
-                        if (in[i]) sr[k][i] = (uint32_t)__ldg(src_sc + col_of<W, NT>(i) / KDA_PACK8_BLOCK);
+                        if (in[i]) sr[k][i] = (uint32_t)__ldg(at(scales, r, nb) + col_of<W, NT>(i) / KDA_PACK8_BLOCK);
             }
-            src_st += row_step;
-            if (X8) src_sc += row_step * nb;
         }
     };
 #pragma unroll
     for (int d = 0; d < kDepth - 1; ++d) issue(blockIdx.x + d * step);
     small(blockIdx.x);
     int buf = 0;
-    T* dst = dx + blockIdx.x * dxs + threadIdx.x * W;
-    for (int64_t r0 = blockIdx.x; r0 < M; r0 += step) {
+    for (int r0 = blockIdx.x; r0 < M; r0 += step) {
         cp_wait<kDepth - 2>();
         float rs[R], sh[R];  // 1 / deviation and -mean / deviation
         uint32_t sc[R][VPT];
@@ -509,9 +533,8 @@ k_layer_norm_bwd_rows(const T* __restrict__ dy, int64_t dys, const void* __restr
                     o[2 * j] = f2_lo(v);
                     o[2 * j + 1] = f2_hi(v);
                 }
-                store_row(dst + i * NT * W, o);
+                store_row(at(tdx, r0 + k * row_step, dxs) + i * NT * W, o);
             }
-            dst += row_step * dxs;
         }
         get = get + kSlot == kDepth * kSlot ? 0 : get + kSlot;
     }
@@ -568,14 +591,14 @@ cudaError_t launch_layer_norm(const kda_norm_args& a, cudaStream_t s) {
     // come): 8,192 x 7,168 bf16.  Fewer rows go one per block.
     DeviceInfo di{0, 0, 0};
     const int sms = current_device_info(&di) ? di.sm_count : 1;
-    if (vec && n <= 2 * kRowThreads) {
+    if (vec && n <= kRowAccesses) {
         const RowShape h = row_shape(n);
-        const int smem = kDepth * 2 * h.vpt * h.nt * 16, per_sm = row_blocks(h.nt);
+        const int smem = kDepth * (h.vpt == 4 ? 1 : 2) * h.vpt * h.nt * 16, per_sm = row_blocks(h.nt, h.vpt);
         if (a.M >= 4 * (int64_t)sms * per_sm) {
             cudaError_t e = cudaSuccess;
 #define KDA_LNR(T, W, V, NT)                                                                                         \
-    if (!(e = cudaFuncSetAttribute(k_layer_norm_rows<T, W, V, 2, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) \
-        k_layer_norm_rows<T, W, V, 2, NT><<<sms * per_sm, NT, smem, s>>>(                                            \
+    if (!(e = cudaFuncSetAttribute(k_layer_norm_rows<T, W, V, V == 4 ? 1 : 2, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) \
+        k_layer_norm_rows<T, W, V, V == 4 ? 1 : 2, NT><<<sms * per_sm, NT, smem, s>>>(                                            \
             static_cast<const T*>(a.x), xs, a.weight, a.bias, a.eps, static_cast<T*>(a.y), ys, a.stats, a.M, a.C)
 #define KDA_LNR_B(V, NT) KDA_LNR(bf16, 8, V, NT)
 #define KDA_LNR_F(V, NT) KDA_LNR(float, 4, V, NT)
@@ -634,7 +657,8 @@ NormBackwardPlan norm_backward_plan(const kda_norm_backward_args& a) {
     // Blocks that fill an SM's threads when the layout allows 16-byte accesses (known only once the
     // pointers are; the sizes alone have to fix the workspace).
     const int vw = a.io == KDA_BF16 ? 8 : 4, acc = (a.C + vw - 1) / vw;
-    const int per_sm = acc <= 2 * kRowThreads ? row_blocks(row_shape(acc).nt) : 1;
+    const RowShape h = acc <= kRowAccesses ? row_shape(acc) : RowShape{4, kRowThreads};
+    const int per_sm = row_blocks(h.nt, h.vpt);
     const int64_t most = (int64_t)sms * per_sm;
     p.blocks = (int)(a.M < most ? a.M : most);
     p.workspace = (a.dweight || a.dbias) ? (size_t)p.blocks * 2 * a.C * sizeof(float) : 0;
@@ -649,15 +673,16 @@ cudaError_t launch_layer_norm_backward(const kda_norm_backward_args& a, const No
     cudaError_t e = cudaSuccess;
     const int es = a.io == KDA_BF16 ? 2 : 4;
     const int acc = a.C / (16 / es);  // accesses per row, where the layout is wide
-    if (h.vec && acc <= 2 * kRowThreads) {
+    const int64_t most = (int64_t)0xffffffff / es;  // elements of a row stride below 4 GB
+    if (h.vec && acc <= kRowAccesses && a.M < (1 << 30) && dys <= most && dxs <= most && xs <= most) {
         const RowShape r = row_shape(acc);
-        const int smem = kDepth * (3 - r.vpt) * r.vpt * r.nt * (16 + (a.x_scales ? 16 / es : 16));
+        const int smem = kDepth * (r.vpt == 1 ? 2 : 1) * r.vpt * r.nt * (16 + (a.x_scales ? 16 / es : 16));
 #define KDA_LNBR(T, X8, W, V, NT)                                                                                    \
-    if (!(e = cudaFuncSetAttribute(k_layer_norm_bwd_rows<T, X8, W, V, 3 - V, NT>,                                    \
+    if (!(e = cudaFuncSetAttribute(k_layer_norm_bwd_rows<T, X8, W, V, V == 1 ? 2 : 1, NT>,                                    \
                                    cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))                              \
-        k_layer_norm_bwd_rows<T, X8, W, V, 3 - V, NT><<<p.blocks, NT, smem, s>>>(                                    \
-            static_cast<const T*>(a.dy), dys, a.x, xs, a.x_scales, a.stats, a.weight, static_cast<T*>(a.dx), dxs, part, \
-            a.M, a.C)
+        k_layer_norm_bwd_rows<T, X8, W, V, V == 1 ? 2 : 1, NT><<<p.blocks, NT, smem, s>>>(                                    \
+            static_cast<const T*>(a.dy), (uint32_t)(dys * es), a.x, (uint32_t)(a.x_scales ? a.C : xs * es), a.x_scales, \
+            a.stats, a.weight, static_cast<T*>(a.dx), (uint32_t)(dxs * es), part, (int)a.M, a.C)
 #define KDA_LNBR_B8(V, NT) KDA_LNBR(bf16, true, 8, V, NT)
 #define KDA_LNBR_B(V, NT) KDA_LNBR(bf16, false, 8, V, NT)
 #define KDA_LNBR_F8(V, NT) KDA_LNBR(float, true, 4, V, NT)

@@ -76,6 +76,29 @@ def test_layer_norm_and_gradient(M, C, how, io, saved):
     assert all(torch.equal(got[k], again[k]) for k in got)  # fixed order of the sums
 
 
+@pytest.mark.parametrize("io", [BF, FP])
+@pytest.mark.parametrize("M,C", [(5000, 96), (4900, 520), (2600, 1800), (1500, 2048), (1300, 4096), (1300, 7168), (700, 8192),
+                                 (650, 14336)])
+def test_layer_norm_many_rows(M, C, io):
+    """Enough rows for every SM to take several in turn, at each width class, without a weight in the odd ones."""
+    g = gen(M + C)
+    x, dy = (randn(g, M, C) * 3 + randn(g, M, 1) * 5).to(io), randn(g, M, C, dtype=io)
+    w, b = (randn(g, C, std=0.3, mean=1.0), randn(g, C, std=0.3)) if C % 1000 else (None, None)
+    put = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    y, stats = kda.kda_layer_norm(x.to(DEV), put(w), put(b), return_stats=True)
+    got = kda.kda_layer_norm_backward(dy.to(DEV), x.to(DEV), stats, put(w))
+    ref = norm_ref(x, w, b, 1e-5, dy)
+    tol, u = norm_bounds(x, ref, w, b, dy), U[io]
+    within(y, ref["y"], tol["y"] + u * (ref["y"].abs() + tol["y"]), "y")
+    within(got["dx"], ref["dx"], tol["dx"] + u * (ref["dx"].abs() + tol["dx"]), "dx")
+    within(got["dweight"], ref["dweight"], tol["dweight"], "dweight")
+    within(got["dbias"], ref["dbias"], tol["dbias"], "dbias")
+    again = kda.kda_layer_norm(x.to(DEV), put(w), put(b))
+    few = kda.kda_layer_norm(x[:5].to(DEV), put(w), put(b))
+    assert torch.equal(again, y)
+    within(few, ref["y"][:5], (tol["y"] + u * (ref["y"].abs() + tol["y"]))[:5], "five rows")
+
+
 def test_layer_norm_without_parameters_and_large_mean():
     g = gen(3)
     x = randn(g, 9, 512) + 1000.0  # a two-pass variance keeps its digits: one pass of squares would lose six
