@@ -480,7 +480,7 @@ class _KDALayer(torch.autograd.Function):
 def _pack_heads(t: torch.Tensor):
     """[T, H, D] rows as kda_pack8 stores them."""
     from .block import kda_pack8
-    return kda_pack8(t.reshape(t.shape[0], -1))
+    return kda_pack8(t.reshape(t.shape[0], t.shape[1] * t.shape[2]))
 
 
 def _unpack_heads(codes: torch.Tensor, scales: torch.Tensor, dtype, shape) -> torch.Tensor:

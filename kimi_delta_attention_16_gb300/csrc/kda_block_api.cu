@@ -219,6 +219,7 @@ kda_status kda_layer_norm_backward(const kda_norm_backward_args* a, kda_stream_t
 static kda_status check_pack8(const void* x, int64_t xs, int dtype, int64_t M, int C, const uint8_t* codes,
                               const uint8_t* scales) {
     if (M < 0 || C < 1) return fail(KDA_ERR_INVALID_ARG, "bad sizes M=%lld C=%d", (long long)M, C);
+    if (C > 1 << 30) return fail(KDA_ERR_UNSUPPORTED, "C=%d above 2^30", C);
     if (!valid_dtype(dtype)) return fail(KDA_ERR_INVALID_ARG, "unknown dtype %d", dtype);
     if (M == 0) return KDA_OK;
     const size_t es = dsize((kda_dtype)dtype);

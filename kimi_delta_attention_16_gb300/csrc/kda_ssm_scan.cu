@@ -124,8 +124,10 @@ __global__ void __launch_bounds__(Lay<NS>::NT, 8) k_scan(Params p) {
 #pragma unroll
             for (int i = 0; i < Q; ++i) {
                 const float4 b = *reinterpret_cast<const float4*>(&sB[buf][t][l * Y::SPT + 4 * i]);
-                h[2 * i] = fma2(exp2_2(mul2(dd, A2[2 * i])), h[2 * i], mul2(du, f2_of(b.x, b.y)));
-                h[2 * i + 1] = fma2(exp2_2(mul2(dd, A2[2 * i + 1])), h[2 * i + 1], mul2(du, f2_of(b.z, b.w)));
+                // the product first, then the multiply-add that shares du: three different register pairs in one
+                // instruction cost a third cycle
+                h[2 * i] = fma2(du, f2_of(b.x, b.y), mul2(exp2_2(mul2(dd, A2[2 * i])), h[2 * i]));
+                h[2 * i + 1] = fma2(du, f2_of(b.z, b.w), mul2(exp2_2(mul2(dd, A2[2 * i + 1])), h[2 * i + 1]));
                 if (kMain) {
                     const float4 v = *reinterpret_cast<const float4*>(&sC[buf][t][l * Y::SPT + 4 * i]);
                     y[0] = fma2(h[2 * i], f2_of(v.x, v.y), y[0]);

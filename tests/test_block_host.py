@@ -71,7 +71,7 @@ def test_layer_norm_backward_refusals(kw, code):
     (4, 8, 3, at(0), 0, at(1), at(2), INVALID), (4, 8, 0, None, 0, at(1), at(2), INVALID),
     (4, 8, 0, at(0), 0, None, at(2), INVALID), (4, 8, 0, at(0), 7, at(1), at(2), INVALID),
     (4, 8, 1, at(0, 2), 0, at(1), at(2), INVALID), (4, 8, 0, at(0), 0, at(0, 8), at(2), INVALID),
-    (4, 8, 0, at(0), 0, at(1), at(1, 31), INVALID)])
+    (4, 8, 0, at(0), 0, at(1), at(1, 31), INVALID), (1, (1 << 30) + 1, 0, at(0), 0, at(40), at(80), UNSUPPORTED)])
 def test_pack8_refusals(M, C, dtype, x, stride, codes, scales, code):
     lib = _lib.load()
     assert lib.kda_pack8(x, stride, dtype, M, C, codes, scales, None) == code
@@ -152,7 +152,8 @@ def test_ssm_scan_refusals(kw, code):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(initial_state=at(9)), INVALID), (dict(final_state=None), INVALID), (dict(Nst=4), UNSUPPORTED), (dict(G=7), INVALID),
-    (dict(u=None), INVALID), (dict(y=at(10)), INVALID), (dict(N=-1), INVALID), (dict(io=2), INVALID), (dict(A=None), INVALID)])
+    (dict(u=None), INVALID), (dict(y=at(10)), INVALID), (dict(N=-1), INVALID), (dict(io=2), INVALID), (dict(A=None), INVALID),
+    (dict(u_stride=1 << 31), UNSUPPORTED), (dict(B_stride=1 << 32), UNSUPPORTED)])
 def test_ssm_step_refusals(kw, code):
     assert call("kda_ssm_step", ssm(**{"initial_state": None, **kw})) == code
 

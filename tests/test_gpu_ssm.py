@@ -399,3 +399,63 @@ def test_scan_gradients_nothing_to_do():
     got = run_backward(a, [0, 0], torch.empty(0, 16), dfin)
     assert torch.equal(got["dinitial_state"].cpu(), dfin)
     assert not got["dA"].any() and not got["dD"].any() and not got["ddt_bias"].any()
+
+
+@pytest.mark.parametrize("bad", [[0, 50, 20, 64], [3, 10, 30, 64], [0, 10, 90, 64], [0, 10, 30, 60], [0, -5, 30, 64]])
+def test_inconsistent_device_cu_seqlens_is_reported(bad):
+    """A device-only cu_seqlens that does not partition the tokens is flagged through d_status; every index stays in
+    range (sequence numbers and ranges are clamped), so the call ends and the next one is right."""
+    import numpy as np
+    from kimi_delta_attention_16_gb300 import _lib
+    a = ssm_inputs(61, 64, 64, 16, 1, FP, 3)
+    v = {k: to(t) for k, t in a.items()}
+    cu = (torch.tensor(bad, dtype=torch.int32, device=DEV), np.asarray([0, 10, 30, 64], np.int32))
+    kw = dict(check_cu_on_host=False)
+    x, w, dy = v["u"], randn(gen(62), 64, 4).to(DEV), randn(gen(63), 64, 64).to(DEV)
+    ins, more = (v["u"], v["dt"], v["A"], v["B"], v["C"]), dict(D=v["D"], z=v["z"], dt_bias=v["dt_bias"], initial_state=v["init"])
+    calls = [lambda s: kda.kda_ssm_conv(x, w, cu, output_conv_state=True, d_status=s, **kw),
+             lambda s: kda.kda_ssm_conv_backward(x, w, cu, dy, d_status=s, **kw),
+             lambda s: kda.kda_ssm_scan(*ins, cu, d_status=s, **more, **kw),
+             lambda s: kda.kda_ssm_backward(*ins, cu, dy, d_status=s, **more, **kw)]
+    for f in calls:
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        f(status)
+        assert status.item() == _lib.KDA_ERR_DEVICE_ARG
+    y, _ = run_scan(a, [10, 20, 34])
+    ry, _ = ssm_ref(a["u"], a["dt"], a["A"], a["B"], a["C"], [10, 20, 34], a["D"], a["z"], a["dt_bias"], True, a["init"])
+    ey, _ = scan_bounds(a, [10, 20, 34])
+    within(y, ry, ey + U32 * ry.abs(), "y")
+
+
+def test_large_offsets():
+    """Rows whose offsets pass 32 bits: strided views with a row stride of 2^26 + 8 elements (bf16, 40 rows: 5 GB)."""
+    stride, T, C = (1 << 26) + 8, 40, 64
+    buf = torch.empty(stride * T, dtype=BF, device=DEV)
+    a = ssm_inputs(71, T, C, 16, 1, BF, 2)
+
+    def far(t, off):
+        view = torch.as_strided(buf, (T, C), (stride, 1), off)
+        view.copy_(t.to(DEV))
+        return view
+    u, dt, z, x = far(a["u"], 0), far(a["dt"], 64), far(a["z"], 128), far(a["u"] * 2, 192)
+    lens = [30, 10]
+    rest = (to(a["A"]), to(a["B"]), to(a["C"]))
+    more = dict(D=to(a["D"]), dt_bias=to(a["dt_bias"]), initial_state=to(a["init"]))
+    y, fin = kda.kda_ssm_scan(u, dt, *rest, cu_of(lens), z=z, **more)
+    y0, fin0 = kda.kda_ssm_scan(to(a["u"]), to(a["dt"]), *rest, cu_of(lens), z=to(a["z"]), **more)
+    assert torch.equal(y, y0) and torch.equal(fin, fin0)
+    st, st0 = fin.repeat(20, 1, 1).contiguous(), fin.repeat(20, 1, 1).contiguous()
+    y = kda.kda_ssm_step(u, dt, *rest, st, z=z, D=more["D"], dt_bias=more["dt_bias"])
+    y0 = kda.kda_ssm_step(to(a["u"]), to(a["dt"]), *rest, st0, z=to(a["z"]), D=more["D"], dt_bias=more["dt_bias"])
+    assert torch.equal(y, y0) and torch.equal(st, st0)
+    w = randn(gen(72), C, 4).to(DEV)
+    assert torch.equal(kda.kda_ssm_conv(x, w, cu_of(lens)), kda.kda_ssm_conv(to(a["u"] * 2), w, cu_of(lens)))
+    n, ns = kda.kda_layer_norm(x, return_stats=True)
+    m, ms = kda.kda_layer_norm(to(a["u"] * 2), return_stats=True)
+    assert torch.equal(n, m) and torch.equal(ns, ms)
+    g, g0 = kda.kda_layer_norm_backward(u, x, ns), kda.kda_layer_norm_backward(to(a["u"]), to(a["u"] * 2), ms)
+    assert all(torch.equal(g[k], g0[k]) for k in g)
+    c, c0 = kda.kda_pack8(x), kda.kda_pack8(to(a["u"] * 2))
+    assert torch.equal(c[0], c0[0]) and torch.equal(c[1], c0[1])
+    out = torch.as_strided(buf, (T, C), (stride, 1), 256)
+    assert torch.equal(kda.kda_unpack8(*c, out=out), kda.kda_unpack8(*c))
