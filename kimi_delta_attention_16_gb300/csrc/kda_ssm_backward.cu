@@ -32,7 +32,8 @@ struct BParams {
     float *rev, *rsum, *pa, *pd, *pbc, *dinit;
     void *du, *ddt, *dz;
     int bpg;  // blocks per group of the main kernel
-    bool vec; // 16-byte copies of every row, dy's too
+    bool vec;   // 16-byte copies of every row, dy's too
+    bool wide;  // two channels per access to du, ddt and dz
 };
 
 constexpr float kLn2 = 0.6931471805599453f;
@@ -191,9 +192,9 @@ template <int NS> struct BLay {
     static constexpr int KPW = 32 / L;
     static constexpr int CH = 4 * KK;           // channels per block
     static constexpr int TT = 4;                // tokens per tile
-    static constexpr int EPT = TT * CH / NT;    // (token, channel) elements per thread and tile
-    static constexpr int CPT = CH > NT ? CH / NT : 1;  // distinct channels among them
-    static constexpr int RPC = NT > CH ? NT / CH : 1;  // threads that share a channel's elements
+    // Elementwise work: a thread has the same two channels of every RPT-th token of the tile.
+    static constexpr int PR = CH / 2, RPT = NT / PR, PPT = RPT < TT ? TT / RPT : 1;
+    static constexpr int RPC = RPT < TT ? RPT : TT;  // threads that share a channel (NS = 64: half of them idle)
     static constexpr int BPT = (TT * NS + NT - 1) / NT;
     static constexpr int VW = 2 * NS + 4;       // row of the dB | dC parts, padded against bank conflicts
 };
@@ -210,10 +211,24 @@ template <typename T, int NS> struct BShared {
     float bc[Y::TT][Y::KK][Y::VW];                // dB | dC
 };
 
+// Two neighbouring elements (aligned to both).
+__device__ __forceinline__ f2 pair_of(const float* v) {
+    const float2 f = *reinterpret_cast<const float2*>(v);
+    return f2_of(f.x, f.y);
+}
+__device__ __forceinline__ f2 pair_of(const bf16* v) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(v);
+    return f2_of(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ void put2(float* o, f2 v) { *reinterpret_cast<float2*>(o) = make_float2(f2_lo(v), f2_hi(v)); }
+__device__ __forceinline__ void put2(bf16* o, f2 v) {
+    *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(f2_lo(v), f2_hi(v));
+}
+
 template <typename T, int NS>
 __global__ void __launch_bounds__(128, 2) k_ssm_bwd(BParams b) {
     using Y = BLay<NS>;
-    constexpr int L = Y::L, NT = Y::NT, CH = Y::CH, TT = Y::TT, EPT = Y::EPT;
+    constexpr int L = Y::L, NT = Y::NT, CH = Y::CH, TT = Y::TT, PPT = Y::PPT;
     extern __shared__ __align__(16) unsigned char raw_shared[];
     BShared<T, NS>& sm = *reinterpret_cast<BShared<T, NS>*>(raw_shared);
     const Params& p = b.f;
@@ -224,6 +239,17 @@ __global__ void __launch_bounds__(128, 2) k_ssm_bwd(BParams b) {
     const int piece = blockIdx.y;
     const int64_t t0 = piece * p.piece, t1 = t0 + p.piece < p.T ? t0 + p.piece : p.T;
     const bool gate = p.z != nullptr;
+    const int cc = 2 * (tid % Y::PR), row = tid / Y::PR, c0 = c_lo + cc;  // this thread's two channels, its first token
+    const bool in0 = c0 < c_hi, in1 = c0 + 1 < c_hi;
+    auto store = [&](void* base, int64_t o, f2 v) {  // this thread's two channels of a row
+        T* q = static_cast<T*>(base) + o;
+        if (b.wide) {
+            put2(q, v);
+        } else {
+            q[0] = from_f<T>(f2_lo(v));
+            if (in1) q[1] = from_f<T>(f2_hi(v));
+        }
+    };
 
     // 4 channels x 4 states: pairs run over the channels (0, 1) and (2, 3)
     auto load_tile = [&](const float* base, int64_t row, f2 (&v)[4][2], float scale) {
@@ -255,17 +281,9 @@ __global__ void __launch_bounds__(128, 2) k_ssm_bwd(BParams b) {
     load_tile(p.A, 0, A2, kLog2e);
 #pragma unroll
     for (int s = 0; s < 4; ++s) dA[s][0] = dA[s][1] = f2_dup(0.f);
-    // this thread's elements: token (i NT + tid) / CH, channel (i NT + tid) % CH
-    float bias[Y::CPT], skip[Y::CPT], accD[Y::CPT], accB[Y::CPT];
-    bool cin[Y::CPT];
-#pragma unroll
-    for (int k = 0; k < Y::CPT; ++k) {
-        const int ch = c_lo + (k * NT + tid) % CH;
-        cin[k] = ch < c_hi;
-        bias[k] = cin[k] && p.dt_bias ? p.dt_bias[ch] : 0.f;
-        skip[k] = cin[k] && p.D ? p.D[ch] : 0.f;
-        accD[k] = accB[k] = 0.f;
-    }
+    auto both = [&](const float* v) { return f2_of(v && in0 ? v[c0] : 0.f, v && in1 ? v[c0 + 1] : 0.f); };
+    const f2 bias = both(p.dt_bias), skip = both(p.D);
+    f2 accD = f2_dup(0.f), accB = accD;
     const int tiles = (int)((t1 - t0 + TT - 1) / TT);
     auto issue = [&](int j) {  // the j-th tile from the right
         if (j < tiles) {
@@ -301,19 +319,25 @@ __global__ void __launch_bounds__(128, 2) k_ssm_bwd(BParams b) {
         const typename BShared<T, NS>::Tile& r = sm.ring[j & 1];
         // Step sizes and gradients of the reads; tokens past the end and channels past the group count as
         // zeros everywhere, which leaves states, gradients and sums as they are.
-        float x[EPT], u[EPT], z[EPT], dy[EPT];
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-            const int e = i * NT + tid, t = e / CH, cc = e % CH, k = i % Y::CPT;
-            const bool on = t < nt && cin[k];
-            x[i] = on ? to_f(r.dt[t][cc]) + bias[k] : 0.f;
-            u[i] = on ? to_f(r.u[t][cc]) : 0.f;
-            dy[i] = on ? to_f(r.dy[t][cc]) : 0.f;
-            z[i] = on && gate ? to_f(r.z[t][cc]) : 0.f;
-            const float d = on ? (p.softplus ? softplus(x[i]) : x[i]) : 0.f;
-            sm.d[t][cc] = d;
-            sm.du[t][cc] = d * u[i];
-            sm.g[t][cc] = gate ? dy[i] * silu(z[i]) : dy[i];
+        for (int i = 0; i < PPT; ++i) {
+            const int t = i * Y::RPT + row;
+            if (Y::RPT > TT && t >= TT) break;
+            const bool on0 = t < nt && in0, on1 = t < nt && in1;
+            auto get = [&](const T* v) {
+                const f2 w = pair_of(v);
+                return f2_of(on0 ? f2_lo(w) : 0.f, on1 ? f2_hi(w) : 0.f);
+            };
+            const f2 x = add2(get(&r.dt[t][cc]), bias);
+            f2 d = p.softplus ? softplus2(x) : x, gv = get(&r.dy[t][cc]);
+            d = f2_of(on0 ? f2_lo(d) : 0.f, on1 ? f2_hi(d) : 0.f);
+            if (gate) {
+                const f2 z = get(&r.z[t][cc]);
+                gv = mul2(gv, mul2(z, sigmoid2(z)));
+            }
+            put2(&sm.d[t][cc], d);
+            put2(&sm.du[t][cc], mul2(d, get(&r.u[t][cc])));
+            put2(&sm.g[t][cc], gv);
         }
 #pragma unroll
         for (int k = 0; k < Y::BPT; ++k) {
@@ -323,23 +347,19 @@ __global__ void __launch_bounds__(128, 2) k_ssm_bwd(BParams b) {
             sm.B[i / NS][i % NS] = on ? to_f(r.B[i / NS][i % NS]) : 0.f;
             sm.C[i / NS][i % NS] = on ? to_f(r.C[i / NS][i % NS]) : 0.f;
         }
-        f2 h[4][2];
-        {
-            float m[4][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 f = sm.ck[j & 1][i][tid];
-                m[i][0] = f.x; m[i][1] = f.y; m[i][2] = f.z; m[i][3] = f.w;
-            }
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) h[s][k] = f2_of(m[2 * k][s], m[2 * k + 1][s]);
-        }
         __syncthreads();
         issue(j + 1);
 
-        f2 ha[TT][4][2];  // a_t h_{t-1}
+        // The state in front of each token: the tile's first stays in shared memory, the others in registers.
+        f2 hs[TT - 1][4][2];
+        auto before = [&](int t, f2 (&h)[4][2]) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    h[s][k] = t ? hs[t - 1][s][k]
+                                : f2_of((&sm.ck[j & 1][2 * k][tid].x)[s], (&sm.ck[j & 1][2 * k + 1][tid].x)[s]);
+        };
         auto pair4 = [&](const float* v, f2 (&o)[2]) {  // four channels of a row
             const float4 f = *reinterpret_cast<const float4*>(v + 4 * kk);
             o[0] = f2_of(f.x, f.y);
@@ -349,21 +369,22 @@ __global__ void __launch_bounds__(128, 2) k_ssm_bwd(BParams b) {
             const float4 f = *reinterpret_cast<const float4*>(v + 4 * l);
             o[0] = f2_dup(f.x); o[1] = f2_dup(f.y); o[2] = f2_dup(f.z); o[3] = f2_dup(f.w);
         };
-        auto forward = [&](int t) {
-            f2 d[2], du[2], B[4];
+        auto forward = [&](int t) {  // the state behind token t
+            f2 d[2], du[2], B[4], h[4][2];
             pair4(sm.d[t], d);
             pair4(sm.du[t], du);
             dup4(sm.B[t], B);
+            before(t, h);
 #pragma unroll
             for (int s = 0; s < 4; ++s)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    ha[t][s][k] = mul2(exp2_2(mul2(d[k], A2[s][k])), h[s][k]);
-                    h[s][k] = fma2(du[k], B[s], ha[t][s][k]);
-                }
+                for (int k = 0; k < 2; ++k)
+                    hs[t][s][k] = fma2(du[k], B[s], mul2(exp2_2(mul2(d[k], A2[s][k])), h[s][k]));
         };
-        auto backward = [&](int t) {
-            f2 d[2], du[2], gg[2], B[4], C[4], s1[2], s2[2], y[2];
+        // kKept: the state behind token t is what stands in front of the next one.
+        auto backward = [&](int t, auto kept) {
+            f2 d[2], du[2], gg[2], B[4], C[4], s1[2], s2[2], y[2], h[4][2];
+            before(t, h);
             pair4(sm.d[t], d);
             pair4(sm.du[t], du);
             pair4(sm.g[t], gg);
@@ -377,16 +398,18 @@ __global__ void __launch_bounds__(128, 2) k_ssm_bwd(BParams b) {
                 f2 vb = f2_dup(0.f), vc = f2_dup(0.f);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const f2 hk = fma2(du[k], B[s], ha[t][s][k]);
-                    const f2 lam = fma2(C[s], gg[k], q[s][k]);
+                    const f2 a = exp2_2(mul2(d[k], A2[s][k])), lam = fma2(C[s], gg[k], q[s][k]);
+                    f2 hk;
+                    if constexpr (kept) hk = hs[t < TT - 1 ? t : 0][s][k];
+                    else hk = fma2(du[k], B[s], mul2(a, h[s][k]));
+                    q[s][k] = mul2(a, lam);
                     vc = fma2(gg[k], hk, vc);
                     vb = fma2(lam, du[k], vb);
                     y[k] = fma2(C[s], hk, y[k]);
                     s1[k] = fma2(lam, B[s], s1[k]);
-                    const f2 w = mul2(lam, ha[t][s][k]);
+                    const f2 w = mul2(q[s][k], h[s][k]);
                     s2[k] = fma2(w, A2[s][k], s2[k]);
                     dA[s][k] = fma2(w, d[k], dA[s][k]);
-                    q[s][k] = mul2(exp2_2(mul2(d[k], A2[s][k])), lam);
                 }
                 dB[s] = f2_lo(vb) + f2_hi(vb);
                 dC[s] = f2_lo(vc) + f2_hi(vc);
@@ -402,9 +425,10 @@ __global__ void __launch_bounds__(128, 2) k_ssm_bwd(BParams b) {
         };
         if (s0 < tb) {  // no sequence starts in the tile
 #pragma unroll
-            for (int t = 0; t < TT; ++t) forward(t);
+            for (int t = 0; t < TT - 1; ++t) forward(t);
+            backward(TT - 1, std::false_type{});
 #pragma unroll
-            for (int t = TT - 1; t >= 0; --t) backward(t);
+            for (int t = TT - 2; t >= 0; --t) backward(t, std::true_type{});
         } else {
             auto starts = [&](int64_t t, int& m) {  // whether token t is its sequence's first
                 m = seq_of(p.cu, p.N, t);
@@ -413,12 +437,23 @@ __global__ void __launch_bounds__(128, 2) k_ssm_bwd(BParams b) {
             int m;
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
-                if (t < nt && starts(tb + t, m)) load_tile(p.init, m, h, 1.f);
-                forward(t);
+                if (t < nt && starts(tb + t, m)) {
+                    if (t) load_tile(p.init, m, hs[t ? t - 1 : 0], 1.f);
+                    else
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int ch = c_lo + 4 * kk + i;
+                            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (p.init && ch < c_hi)
+                                f = *reinterpret_cast<const float4*>(p.init + ((int64_t)m * p.C + ch) * NS + 4 * l);
+                            sm.ck[j & 1][i][tid] = f;
+                        }
+                }
+                if (t < TT - 1) forward(t);
             }
 #pragma unroll
             for (int t = TT - 1; t >= 0; --t) {
-                backward(t);
+                backward(t, std::false_type{});
                 if (t < nt && starts(tb + t, m)) {  // q is the initial state's gradient; on to the sequence before
                     if (b.dinit) store_tile(b.dinit, m, q);
                     if (tb + t > 0) {
@@ -433,48 +468,50 @@ __global__ void __launch_bounds__(128, 2) k_ssm_bwd(BParams b) {
         __syncthreads();
 
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-            const int e = i * NT + tid, t = e / CH, cc = e % CH, k = i % Y::CPT;
-            if (t >= nt || !cin[k]) continue;
-            float s1 = 0.f, s2 = 0.f, y = 0.f;
+        for (int i = 0; i < PPT; ++i) {
+            const int t = i * Y::RPT + row;
+            if (t >= nt || !in0) continue;
+            f2 s1 = f2_dup(0.f), s2 = s1, y = s1;
 #pragma unroll
             for (int v = 0; v < L; ++v) {
-                s1 += sm.part[0][t][v][cc];
-                s2 += sm.part[1][t][v][cc];
-                y += sm.part[2][t][v][cc];
+                s1 = add2(s1, pair_of(&sm.part[0][t][v][cc]));
+                s2 = add2(s2, pair_of(&sm.part[1][t][v][cc]));
+                y = add2(y, pair_of(&sm.part[2][t][v][cc]));
             }
-            const float d = sm.d[t][cc], gv = sm.g[t][cc];
-            const int64_t o = (tb + t) * p.C + c_lo + cc;
-            static_cast<T*>(b.du)[o] = from_f<T>(fmaf(d, s1, skip[k] * gv));
-            float dd = fmaf(u[i], s1, kLn2 * s2);  // A2 carries log2 e
-            if (p.softplus) dd *= sigmoid(x[i]);
-            static_cast<T*>(b.ddt)[o] = from_f<T>(dd);
-            accB[k] += dd;
-            accD[k] = fmaf(gv, u[i], accD[k]);
+            // The elements come from shared memory once more: held since the step sizes they cost 16 registers (339 us
+            // against 329 at 4,096 tokens x 4,096 channels x 16).
+            const f2 d = pair_of(&sm.d[t][cc]), gv = pair_of(&sm.g[t][cc]), u = pair_of(&r.u[t][cc]);
+            const int64_t o = (tb + t) * p.C + c0;
+            store(b.du, o, fma2(d, s1, mul2(skip, gv)));
+            f2 dd = fma2(u, s1, mul2(f2_dup(kLn2), s2));  // A2 carries log2 e
+            if (p.softplus) dd = mul2(dd, sigmoid2(add2(pair_of(&r.dt[t][cc]), bias)));
+            store(b.ddt, o, dd);
+            accB = add2(accB, dd);
+            accD = fma2(gv, u, accD);
             if (b.dz) {
-                const float sg = sigmoid(z[i]);
-                static_cast<T*>(b.dz)[o] = from_f<T>(dy[i] * fmaf(skip[k], u[i], y) * sg * fmaf(z[i], 1.f - sg, 1.f));
+                const f2 z = pair_of(&r.z[t][cc]), sg = sigmoid2(z), one = f2_dup(1.f);
+                const f2 slope = mul2(sg, fma2(z, fma2(sg, f2_dup(-1.f), one), one));
+                store(b.dz, o, mul2(mul2(pair_of(&r.dy[t][cc]), fma2(skip, u, y)), slope));
             }
         }
+        // Two values of a token's row per thread, half of the parts in each half of a warp.
         float* pbc = b.pbc + ((int64_t)blockIdx.x * p.T + tb) * 2 * NS;
 #pragma unroll
-        for (int i = tid; i < TT * 2 * NS; i += NT) {
-            const int t = i / (2 * NS), v = i % (2 * NS);
-            float s = 0.f;
-#pragma unroll 8
-            for (int k = 0; k < Y::KK; ++k) s += sm.bc[t][k][v];
-            if (t < nt) pbc[i] = s;
+        for (int i = warp * 16 + lane % 16; i < TT * NS; i += NT / 2) {
+            const int t = i / NS, v = 2 * (i % NS);
+            f2 s = f2_dup(0.f);
+#pragma unroll
+            for (int k = 0; k < Y::KK; k += 2) s = add2(s, pair_of(&sm.bc[t][k + lane / 16][v]));
+            s = add2(s, f2_of(__shfl_xor_sync(0xffffffffu, f2_lo(s), 16), __shfl_xor_sync(0xffffffffu, f2_hi(s), 16)));
+            if (t < nt && lane < 16) put2(pbc + 2 * i, s);
         }
         // d and g of this tile are read above, and written again only by the same thread's next tile
     }
     store_tile(b.pa, piece, dA);
-#pragma unroll
-    for (int k = 0; k < Y::CPT; ++k) {
-        const int cc = (k * NT + tid) % CH, row = Y::RPC > 1 ? tid / CH : 0;
-        if (!cin[k]) continue;
-        float* o = b.pd + ((int64_t)piece * Y::RPC + row) * 2 * p.C + c_lo + cc;
-        o[0] = accD[k];
-        o[p.C] = accB[k];
+    if (row < Y::RPC) {
+        float* o = b.pd + ((int64_t)piece * Y::RPC + row) * 2 * p.C + c0;
+        if (in0) o[0] = f2_lo(accD), o[p.C] = f2_lo(accB);
+        if (in1) o[1] = f2_hi(accD), o[p.C + 1] = f2_hi(accB);
     }
 }
 
@@ -509,8 +546,7 @@ struct PutDB {  // column c of [dD | ddt_bias]
     }
 };
 
-template <int NS> constexpr int rows_per_channel() { return BLay<NS>::RPC; }
-int rpc_of(int ns) { return ns <= 16 ? 1 : ns / 16; }
+int rpc_of(int ns) { return ns <= 32 ? ns / 8 : 4; }
 int ch_of(int ns) { return 2048 / ns; }
 
 template <typename T, int NS>
@@ -600,6 +636,8 @@ cudaError_t launch_ssm_backward(const kda_ssm_backward_args& a, const SsmBackwar
     b.dz = a.fwd.z ? a.dz : nullptr;
     const int es = a.fwd.io == KDA_BF16 ? 2 : 4, ch = ch_of(a.fwd.Nst);
     b.bpg = (b.f.Cg + ch - 1) / ch;
+    auto pairs = [es](const void* q) { return reinterpret_cast<uintptr_t>(q) % (2 * es) == 0; };
+    b.wide = b.f.Cg % 2 == 0 && pairs(b.du) && pairs(b.ddt) && pairs(b.dz);
     b.vec = b.f.vec && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 && b.dys * es % 16 == 0;
 #define KDA_BWD(T)                                               \
     switch (a.fwd.Nst) {                                         \
