@@ -111,10 +111,9 @@ __device__ __forceinline__ f2 sigmoid2(f2 x) {
 }
 
 // ------------------------------------------------------------------ asynchronous copies to shared memory
-// 16 bytes, of which the first `bytes` are read and the rest filled with zeros.
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
     const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }

@@ -84,11 +84,12 @@ __global__ void __launch_bounds__(Lay<NS>::NT, 8) k_rev(BParams b) {
             Tile& r = ring[j % kDepth];
             const int64_t tb = t0 + (int64_t)(tiles - 1 - j) * TT;
             const int rows = (int)(t1 - tb < TT ? t1 - tb : TT);
-            copy_tile<T, TT, CB, NT>(&r.dt[0][0], static_cast<const T*>(p.dt) + tb * p.dts + c_lo, p.dts, rows, cols, b.vec);
-            copy_tile<T, TT, CB, NT>(&r.dy[0][0], static_cast<const T*>(b.dy) + tb * b.dys + c_lo, b.dys, rows, cols, b.vec);
+            const uint32_t row = (uint32_t)tb;
+            copy_tile<T, TT, CB, NT>(&r.dt[0][0], static_cast<const T*>(p.dt) + c_lo, p.dts, row, rows, cols, b.vec);
+            copy_tile<T, TT, CB, NT>(&r.dy[0][0], static_cast<const T*>(b.dy) + c_lo, b.dys, row, rows, cols, b.vec);
             if (gate)
-                copy_tile<T, TT, CB, NT>(&r.z[0][0], static_cast<const T*>(p.z) + tb * p.zs + c_lo, p.zs, rows, cols, b.vec);
-            copy_tile<T, TT, NS, NT>(&r.C[0][0], static_cast<const T*>(p.Cm) + tb * p.cs + g * NS, p.cs, rows, NS, b.vec);
+                copy_tile<T, TT, CB, NT>(&r.z[0][0], static_cast<const T*>(p.z) + c_lo, p.zs, row, rows, cols, b.vec);
+            copy_tile<T, TT, NS, NT>(&r.C[0][0], static_cast<const T*>(p.Cm) + g * NS, p.cs, row, rows, NS, b.vec);
         }
         cp_commit();
     };
@@ -290,19 +291,19 @@ __global__ void __launch_bounds__(128, 2) k_ssm_bwd(BParams b) {
             typename BShared<T, NS>::Tile& r = sm.ring[j & 1];
             const int64_t tb = t0 + (int64_t)(tiles - 1 - j) * TT;
             const int rows = (int)(t1 - tb < TT ? t1 - tb : TT);
-            copy_tile<T, TT, CH, NT>(&r.u[0][0], static_cast<const T*>(p.u) + tb * p.us + c_lo, p.us, rows, cols, b.vec);
-            copy_tile<T, TT, CH, NT>(&r.dt[0][0], static_cast<const T*>(p.dt) + tb * p.dts + c_lo, p.dts, rows, cols, b.vec);
-            copy_tile<T, TT, CH, NT>(&r.dy[0][0], static_cast<const T*>(b.dy) + tb * b.dys + c_lo, b.dys, rows, cols, b.vec);
+            const uint32_t row = (uint32_t)tb;
+            copy_tile<T, TT, CH, NT>(&r.u[0][0], static_cast<const T*>(p.u) + c_lo, p.us, row, rows, cols, b.vec);
+            copy_tile<T, TT, CH, NT>(&r.dt[0][0], static_cast<const T*>(p.dt) + c_lo, p.dts, row, rows, cols, b.vec);
+            copy_tile<T, TT, CH, NT>(&r.dy[0][0], static_cast<const T*>(b.dy) + c_lo, b.dys, row, rows, cols, b.vec);
             if (gate)
-                copy_tile<T, TT, CH, NT>(&r.z[0][0], static_cast<const T*>(p.z) + tb * p.zs + c_lo, p.zs, rows, cols, b.vec);
-            copy_tile<T, TT, NS, NT>(&r.B[0][0], static_cast<const T*>(p.B) + tb * p.bs + g * NS, p.bs, rows, NS, b.vec);
-            copy_tile<T, TT, NS, NT>(&r.C[0][0], static_cast<const T*>(p.Cm) + tb * p.cs + g * NS, p.cs, rows, NS, b.vec);
+                copy_tile<T, TT, CH, NT>(&r.z[0][0], static_cast<const T*>(p.z) + c_lo, p.zs, row, rows, cols, b.vec);
+            copy_tile<T, TT, NS, NT>(&r.B[0][0], static_cast<const T*>(p.B) + g * NS, p.bs, row, rows, NS, b.vec);
+            copy_tile<T, TT, NS, NT>(&r.C[0][0], static_cast<const T*>(p.Cm) + g * NS, p.cs, row, rows, NS, b.vec);
+            const float* ck = p.ckpt + (int64_t)(row / 4) * (uint32_t)(p.C * NS) + (c_lo + 4 * kk) * NS + 4 * l;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {  // a channel past the group's last: zeros
-                const int ch = c_lo + 4 * kk + i;
-                const float* src = p.ckpt + (tb / 4 * p.C + (ch < c_hi ? ch : c_lo)) * NS + 4 * l;
-                cp_async16(&sm.ck[j & 1][i][tid], src, ch < c_hi ? 16 : 0);
-            }
+            for (int i = 0; i < 4; ++i)
+                if (c_lo + 4 * kk + i < c_hi) cp_async16(&sm.ck[j & 1][i][tid], ck + i * NS);
+                else sm.ck[j & 1][i][tid] = make_float4(0.f, 0.f, 0.f, 0.f);  // past the group's last channel
         }
         cp_commit();
     };
@@ -638,7 +639,8 @@ cudaError_t launch_ssm_backward(const kda_ssm_backward_args& a, const SsmBackwar
     b.bpg = (b.f.Cg + ch - 1) / ch;
     auto pairs = [es](const void* q) { return reinterpret_cast<uintptr_t>(q) % (2 * es) == 0; };
     b.wide = b.f.Cg % 2 == 0 && pairs(b.du) && pairs(b.ddt) && pairs(b.dz);
-    b.vec = b.f.vec && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 && b.dys * es % 16 == 0;
+    b.vec = b.f.vec && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 && b.dys * es % 16 == 0 &&
+            b.dys * es < (int64_t)1 << 32;
 #define KDA_BWD(T)                                               \
     switch (a.fwd.Nst) {                                         \
         case 8: return backward_as<T, 8>(b, a, s);               \

@@ -78,13 +78,14 @@ __global__ void __launch_bounds__(Lay<NS>::NT, 8) k_scan(Params p) {
             Tile& r = ring[k % kDepth];
             const int64_t tb = t0 + (int64_t)k * TT;
             const int rows = (int)(t1 - tb < TT ? t1 - tb : TT);
-            copy_tile<T, TT, CB, NT>(&r.u[0][0], static_cast<const T*>(p.u) + tb * p.us + c_lo, p.us, rows, cols, p.vec);
-            copy_tile<T, TT, CB, NT>(&r.dt[0][0], static_cast<const T*>(p.dt) + tb * p.dts + c_lo, p.dts, rows, cols, p.vec);
+            const uint32_t row = (uint32_t)tb;
+            copy_tile<T, TT, CB, NT>(&r.u[0][0], static_cast<const T*>(p.u) + c_lo, p.us, row, rows, cols, p.vec);
+            copy_tile<T, TT, CB, NT>(&r.dt[0][0], static_cast<const T*>(p.dt) + c_lo, p.dts, row, rows, cols, p.vec);
             if (gate)
-                copy_tile<T, TT, CB, NT>(&r.z[0][0], static_cast<const T*>(p.z) + tb * p.zs + c_lo, p.zs, rows, cols, p.vec);
-            copy_tile<T, TT, NS, NT>(&r.B[0][0], static_cast<const T*>(p.B) + tb * p.bs + g * NS, p.bs, rows, NS, p.vec);
+                copy_tile<T, TT, CB, NT>(&r.z[0][0], static_cast<const T*>(p.z) + c_lo, p.zs, row, rows, cols, p.vec);
+            copy_tile<T, TT, NS, NT>(&r.B[0][0], static_cast<const T*>(p.B) + g * NS, p.bs, row, rows, NS, p.vec);
             if (kMain)
-                copy_tile<T, TT, NS, NT>(&r.C[0][0], static_cast<const T*>(p.Cm) + tb * p.cs + g * NS, p.cs, rows, NS, p.vec);
+                copy_tile<T, TT, NS, NT>(&r.C[0][0], static_cast<const T*>(p.Cm) + g * NS, p.cs, row, rows, NS, p.vec);
         }
         cp_commit();
     };
@@ -359,10 +360,10 @@ ssm::Params ssm::params_of(const kda_ssm_args& a) {
     p.softplus = a.softplus;
     const int es = a.io == KDA_BF16 ? 2 : 4;
     auto wide = [es](const void* q, int64_t stride) {
-        return reinterpret_cast<uintptr_t>(q) % 16 == 0 && stride * es % 16 == 0;
+        return reinterpret_cast<uintptr_t>(q) % 16 == 0 && stride * es % 16 == 0 && stride * es < (int64_t)1 << 32;
     };
     p.vec = wide(p.u, p.us) && wide(p.dt, p.dts) && (!p.z || wide(p.z, p.zs)) && wide(p.B, p.bs) && wide(p.Cm, p.cs) &&
-            (a.G == 1 || (int64_t)p.Cg * es % 16 == 0);
+            (int64_t)p.Cg * es % 16 == 0;
     return p;
 }
 
