@@ -44,24 +44,40 @@ struct Params {
     const int32_t* cu;
     float *ws_state, *ws_sum, *ckpt;
     int64_t T, piece;
-    int N, C, G, Cg, bpg;  // sequences, channels, groups, channels and blocks per group
+    int N, C, G, Cg;  // sequences, channels, groups, channels per group
     int pieces, softplus;
-    bool vec;  // 16-byte copies of every row, strides below 4 GB
+    bool vec;   // 16-byte copies of every row, strides below 4 GB
+    bool wide;  // two channels per access to y
 };
 
 Params params_of(const kda_ssm_args& a);  // everything but the pieces and the workspace
 // The state in front of every fourth token to p.ckpt [ceil(T / 4)][C][NS] (pieces start at multiples of 8).
-cudaError_t launch_states(Params& p, const kda_ssm_args& a, cudaStream_t s);
+cudaError_t launch_states(const Params& p, const kda_ssm_args& a, cudaStream_t s);
 
-// Block of CB channels x NS states: a thread holds up to 16 states of one channel, L threads share a
-// channel.  Lanes that hold the same states are neighbours, so they read a token's B and C at one
+// Two neighbouring elements (aligned to both).
+__device__ __forceinline__ f2 pair_of(const float* v) {
+    const float2 f = *reinterpret_cast<const float2*>(v);
+    return f2_of(f.x, f.y);
+}
+__device__ __forceinline__ f2 pair_of(const bf16* v) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(v);
+    return f2_of(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ void put2(float* o, f2 v) { *reinterpret_cast<float2*>(o) = make_float2(f2_lo(v), f2_hi(v)); }
+__device__ __forceinline__ void put2(bf16* o, f2 v) {
+    *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(f2_lo(v), f2_hi(v));
+}
+
+// Block of CB channels x NS states: a thread holds up to 16 states of CPT neighbouring channels, L threads
+// share them.  Lanes that hold the same states are neighbours, so they read a token's B and C at one
 // shared-memory address (broadcast).
-template <int NS> struct Lay {
-    static constexpr int SPT = NS < 16 ? NS : 16;  // states per thread
+template <int NS, int kChannels> struct Lay {
+    static constexpr int CPT = kChannels;
+    static constexpr int SPT = NS < 16 ? NS : 16;  // states per thread and channel
     static constexpr int L = NS / SPT;             // threads per channel
     static constexpr int NT = 64;                  // threads per block
-    static constexpr int CB = NT / L;              // channels per block
-    static constexpr int KPW = 32 / L;             // channels per warp
+    static constexpr int CB = CPT * NT / L;        // channels per block
+    static constexpr int KPW = 32 / L;             // threads along the channels per warp
     static constexpr int TT = 8;                   // tokens per tile
     static constexpr int BPT = TT * NS / NT;       // elements of B (and C) per thread and tile
     static_assert(BPT >= 1, "tile too small");

@@ -42,8 +42,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Pieces 1 .. pieces - 1, each from zero at its right end (or from d_final_state where a sequence
 // ends): q in front of its first token, and its sum of delta.  Layout and copies as in the forward scan.
 template <typename T, int NS>
-__global__ void __launch_bounds__(Lay<NS>::NT, 8) k_rev(BParams b) {
-    using Y = Lay<NS>;
+__global__ void __launch_bounds__(Lay<NS, 1>::NT, 8) k_rev(BParams b) {
+    using Y = Lay<NS, 1>;
     constexpr int TT = Y::TT, NT = Y::NT, BPT = Y::BPT, H = Y::SPT / 2, Q = Y::SPT / 4, CB = Y::CB;
     constexpr int kDepth = 4;
     struct Tile {
@@ -54,8 +54,8 @@ __global__ void __launch_bounds__(Lay<NS>::NT, 8) k_rev(BParams b) {
     const Params& p = b.f;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int l = lane / Y::KPW, cl = warp * Y::KPW + lane % Y::KPW;
-    const int g = blockIdx.x / p.bpg;
-    const int c_lo = g * p.Cg + (blockIdx.x % p.bpg) * CB, c_hi = (g + 1) * p.Cg, cols = c_hi - c_lo;
+    const int bpg = (p.Cg + CB - 1) / CB, g = blockIdx.x / bpg;  // blocks per group
+    const int c_lo = g * p.Cg + (blockIdx.x % bpg) * CB, c_hi = (g + 1) * p.Cg, cols = c_hi - c_lo;
     const bool in = c_lo + cl < c_hi, gate = p.z != nullptr;
     const int c = in ? c_lo + cl : c_hi - 1;
     const int piece = blockIdx.y + 1;
@@ -211,20 +211,6 @@ template <typename T, int NS> struct BShared {
     float part[3][Y::TT][Y::L][Y::CH];            // s1, s2, y
     float bc[Y::TT][Y::KK][Y::VW];                // dB | dC
 };
-
-// Two neighbouring elements (aligned to both).
-__device__ __forceinline__ f2 pair_of(const float* v) {
-    const float2 f = *reinterpret_cast<const float2*>(v);
-    return f2_of(f.x, f.y);
-}
-__device__ __forceinline__ f2 pair_of(const bf16* v) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(v);
-    return f2_of(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-__device__ __forceinline__ void put2(float* o, f2 v) { *reinterpret_cast<float2*>(o) = make_float2(f2_lo(v), f2_hi(v)); }
-__device__ __forceinline__ void put2(bf16* o, f2 v) {
-    *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(f2_lo(v), f2_hi(v));
-}
 
 template <typename T, int NS>
 __global__ void __launch_bounds__(128, 2) k_ssm_bwd(BParams b) {
@@ -555,9 +541,10 @@ cudaError_t backward_as(BParams& b, const kda_ssm_backward_args& a, cudaStream_t
     using Y = BLay<NS>;
     Params& p = b.f;
     cudaError_t e;
-    if ((e = launch_states(p, a.fwd, s))) return e;  // sets p.bpg for the scan's layout, which k_rev shares
+    if ((e = launch_states(p, a.fwd, s))) return e;
     if (p.pieces > 1) {
-        k_rev<T, NS><<<dim3((unsigned)(p.bpg * p.G), p.pieces - 1), Lay<NS>::NT, 0, s>>>(b);
+        constexpr int CB = Lay<NS, 1>::CB;
+        k_rev<T, NS><<<dim3((unsigned)((p.Cg + CB - 1) / CB * p.G), p.pieces - 1), Lay<NS, 1>::NT, 0, s>>>(b);
         if ((e = cudaGetLastError())) return e;
         if (p.pieces > 2) {
             k_rev_join<NS><<<(unsigned)(((int64_t)p.C * NS + kJoinThreads - 1) / kJoinThreads), kJoinThreads, 0, s>>>(b);

@@ -3,13 +3,20 @@
 //   delta = softplus(dt + b),  h_t[n] = 2^(delta A[n] log2 e) h_{t-1}[n] + delta u B_t[n],
 //   y_t = (sum_n C_t[n] h_t[n] + D u) silu(z)
 //
-// Per (token, channel, state) one exponential and four multiply-add-pipe operations, against 8 / N
-// bytes of HBM traffic per state: at N = 16 the arithmetic weighs more than the bytes (8,192 tokens
-// of 12,288 channels: 0.17 ms of either pipe, 0.12 ms of HBM).  So the inner loop keeps states and
-// decay rates in registers as pairs (fp32x2 instructions), reads a token's B and C once for two
-// channels, and leaves each thread's part of y in shared memory, where the epilogue adds the parts
-// of a channel, the skip and the gate.  Tokens come in tiles: the next tile's loads are in flight
-// while the current one is scanned.
+// Per (token, channel, state) one exponential and four multiply-add-pipe operations (one of them 2^x's
+// argument), against 8 / N bytes of HBM traffic: at N = 16 the arithmetic weighs more than the bytes (8,192
+// tokens of 12,288 channels: 0.17 ms of either pipe, 0.12 ms of HBM).  So a thread keeps all (up to 16)
+// states and decay rates of its channels in registers as pairs (fp32x2 instructions), and nothing but the
+// token's B and C (fp32 in shared memory, one broadcast read for all lanes) and its step size comes from
+// outside.  Rows come in tiles of eight tokens by asynchronous copies, three tiles in flight.
+//
+// One channel's tokens are a chain, and channels alone do not fill the GPU: the token axis is cut into
+// pieces.  kPiece runs every piece from a zero state, k_scan_join carries the states through (a piece's
+// effect on what enters it is 2^(A log2 e sum of delta)), kOut runs the pieces again from the right states.
+//
+// Measured, 8,192 x 12,288 x 16 bf16 with the gate: 691 us = 404 (kOut, 2.0 TB/s) + 278 (kPiece) + 9.
+// Bound by instruction issue and the register file: taken out one at a time in a copy, the exponentials
+// are worth 35 us, reading B and C 56, softplus 50, the gate 40, the copies 67, the stores 0.
 //
 // Sequences are walked, not mapped: a piece of the packed stream starts in the middle of whatever
 // sequence holds its first token, and at a border the state is stored and the next one's loaded.
@@ -25,12 +32,35 @@ using namespace ssm;
 // from zero (or from the initial state of a sequence that starts at its first token or inside it),
 // and its sum of delta.  kStates: from the carried state, the state in front of every fourth token.
 enum { kPiece, kOut, kStates };
+
+// Channels per thread: two, so that a token's B and C are read from shared memory once for both (8,192 tokens x
+// 12,288 channels x 16: outputs 455 -> 403 us, six blocks of 168 registers per SM against eight of 128); one for the
+// checkpoints, whose stores of two rows per thread cost more than that (4,096 x 4,096 x 16: 73 against 93 us).
+template <int NS, int kMode> using ScanLay = Lay<NS, kMode == kStates ? 1 : 2>;
+// A value per channel of a thread: a pair, or one.
+template <int CPT> struct Chans {
+    using V = f2;
+};
+template <> struct Chans<1> {
+    using V = float;
+};
+__device__ __forceinline__ float chan(f2 v, int k) { return k ? f2_hi(v) : f2_lo(v); }
+__device__ __forceinline__ float chan(float v, int) { return v; }
+__device__ __forceinline__ f2 times(f2 a, f2 b) { return mul2(a, b); }
+__device__ __forceinline__ float times(float a, float b) { return a * b; }
+__device__ __forceinline__ f2 plus(f2 a, f2 b) { return add2(a, b); }
+__device__ __forceinline__ float plus(float a, float b) { return a + b; }
+__device__ __forceinline__ void join_chans(f2& v, float a, float b) { v = f2_of(a, b); }
+__device__ __forceinline__ void join_chans(float& v, float a, float) { v = a; }
+
 template <typename T, int NS, int kMode>
-__global__ void __launch_bounds__(Lay<NS>::NT, 8) k_scan(Params p) {
-    using Y = Lay<NS>;
+__global__ void __launch_bounds__(ScanLay<NS, kMode>::NT, kMode == kOut ? 6 : 8) k_scan(Params p) {
+    using Y = ScanLay<NS, kMode>;
     constexpr bool kMain = kMode == kOut;
+    constexpr int CPT = Y::CPT;
+    using V = typename Chans<CPT>::V;
     constexpr int L = Y::L, TT = Y::TT, NT = Y::NT, BPT = Y::BPT, H = Y::SPT / 2, Q = Y::SPT / 4, CB = Y::CB;
-    constexpr int kDepth = 4;  // tiles in flight
+    constexpr int kDepth = 3;  // tiles in flight (four: no gain)
     struct Tile {
         T u[TT][CB], dt[TT][CB], z[kMain ? TT : 1][CB], B[TT][NS], C[kMain ? TT : 1][NS];
     };
@@ -38,40 +68,56 @@ __global__ void __launch_bounds__(Lay<NS>::NT, 8) k_scan(Params p) {
     __shared__ __align__(16) float sB[2][TT][NS], sC[kMain ? 2 : 1][TT][NS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int l = lane / Y::KPW;  // which SPT states of the channel
-    const int g = blockIdx.x / p.bpg;
-    const int ch = g * p.Cg + (blockIdx.x % p.bpg) * Y::CB + warp * Y::KPW + lane % Y::KPW, c_hi = (g + 1) * p.Cg;
-    const bool in = ch < c_hi, gate = kMain && p.z;
-    const int c = in ? ch : c_hi - 1;  // threads past the group shadow its last channel and store nothing
+    const int bpg = (p.Cg + CB - 1) / CB, g = blockIdx.x / bpg;  // blocks per group
+    const int c_lo = g * p.Cg + (blockIdx.x % bpg) * CB, c_hi = (g + 1) * p.Cg, cols = c_hi - c_lo;
+    const int cl = CPT * (warp * Y::KPW + lane % Y::KPW), ch = c_lo + cl;  // this thread's (first) channel
+    const bool gate = kMain && p.z;
+    auto in = [&](int k) { return ch + k < c_hi; };  // threads past the group shadow its last channel, store nothing
     const int piece = blockIdx.y;
     const int64_t t0 = piece * p.piece, t1 = t0 + p.piece < p.T ? t0 + p.piece : p.T;
-    const int64_t so = (int64_t)c * NS + l * Y::SPT;  // this thread's states in a row of [C][NS]
-
-    f2 A2[H], h[H];
+    uint32_t so[CPT];  // this thread's states in a row of [C][NS]
+    f2 A2[CPT][H], h[CPT][H];
+    V bias, skip, dsum;
 #pragma unroll
-    for (int i = 0; i < Q; ++i) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p.A + so) + i);
-        A2[2 * i] = f2_of(a.x * kLog2e, a.y * kLog2e);
-        A2[2 * i + 1] = f2_of(a.z * kLog2e, a.w * kLog2e);
-    }
-    auto load_state = [&](const float* base, int64_t n) {  // row n of [..][C][NS], or zeros
+    for (int k = 0; k < CPT; ++k) {
+        const int c = in(k) ? ch + k : c_hi - 1;
+        so[k] = (uint32_t)(c * NS + l * Y::SPT);
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (base) s = reinterpret_cast<const float4*>(base + n * p.C * NS + so)[i];
-            h[2 * i] = f2_of(s.x, s.y);
-            h[2 * i + 1] = f2_of(s.z, s.w);
+            const float4 a = __ldg(reinterpret_cast<const float4*>(p.A + so[k]) + i);
+            A2[k][2 * i] = f2_of(a.x * kLog2e, a.y * kLog2e);
+            A2[k][2 * i + 1] = f2_of(a.z * kLog2e, a.w * kLog2e);
         }
+    }
+    auto both = [&](const float* v) {  // a parameter of this thread's channels
+        V o;
+        join_chans(o, v && in(0) ? v[ch] : 0.f, CPT == 2 && v && in(1) ? v[ch + 1] : 0.f);
+        return o;
+    };
+    bias = both(p.dt_bias);
+    skip = both(kMain ? p.D : nullptr);
+    dsum = both(nullptr);
+    auto load_state = [&](const float* base, int64_t n) {  // row n of [..][C][NS], or zeros
+#pragma unroll
+        for (int k = 0; k < CPT; ++k)
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (base) s = reinterpret_cast<const float4*>(base + n * p.C * NS + so[k])[i];
+                h[k][2 * i] = f2_of(s.x, s.y);
+                h[k][2 * i + 1] = f2_of(s.z, s.w);
+            }
     };
     auto store_state = [&](float* base, int64_t n) {
-        if (!in) return;
 #pragma unroll
-        for (int i = 0; i < Q; ++i)
-            reinterpret_cast<float4*>(base + n * p.C * NS + so)[i] =
-                make_float4(f2_lo(h[2 * i]), f2_hi(h[2 * i]), f2_lo(h[2 * i + 1]), f2_hi(h[2 * i + 1]));
+        for (int k = 0; k < CPT; ++k)
+            if (in(k))
+#pragma unroll
+                for (int i = 0; i < Q; ++i)
+                    reinterpret_cast<float4*>(base + n * p.C * NS + so[k])[i] =
+                        make_float4(f2_lo(h[k][2 * i]), f2_hi(h[k][2 * i]), f2_lo(h[k][2 * i + 1]), f2_hi(h[k][2 * i + 1]));
     };
-    const float bias = p.dt_bias ? p.dt_bias[c] : 0.f, skip = kMain && p.D ? p.D[c] : 0.f;
-    T* yp = static_cast<T*>(p.y) + c + t0 * p.ys;
-    const int c_lo = ch - (warp * Y::KPW + lane % Y::KPW), cols = c_hi - c_lo, cl = ch - c_lo;
+    T* yp = static_cast<T*>(p.y) + ch + t0 * p.ys;
     const int tiles = (int)((t1 - t0 + TT - 1) / TT);
     auto issue = [&](int k) {  // copies of tile k (a group of its own, empty past the end)
         if (k < tiles) {
@@ -108,7 +154,6 @@ __global__ void __launch_bounds__(Lay<NS>::NT, 8) k_scan(Params p) {
     cp_wait<kDepth - 2>();  // tile 0
     __syncthreads();
     widen(0);
-    float dsum = 0.f;
     for (int k = 0; k < tiles; ++k) {
         const int64_t tb = t0 + (int64_t)k * TT;
         const int buf = k & 1;
@@ -118,60 +163,91 @@ __global__ void __launch_bounds__(Lay<NS>::NT, 8) k_scan(Params p) {
         issue(k + kDepth - 1);
         const Tile& r = ring[k % kDepth];
         const int nt = (int)(t1 - tb < TT ? t1 - tb : TT);
-        // One token: the states move on, the return value is this thread's part of sum_n C h.
-        auto token = [&](int t, float d, float u) {
-            const f2 dd = f2_dup(d), du = f2_dup(d * u);
-            f2 y[2] = {f2_dup(0.f), f2_dup(0.f)};
+        // One token: the states move on; the return value is this thread's part of sum_n C h.
+        auto token = [&](int t, V d, V u) {
+            const V x = times(d, u);
+            f2 y[CPT];
+#pragma unroll
+            for (int k = 0; k < CPT; ++k) y[k] = f2_dup(0.f);
 #pragma unroll
             for (int i = 0; i < Q; ++i) {
                 const float4 b = *reinterpret_cast<const float4*>(&sB[buf][t][l * Y::SPT + 4 * i]);
                 // the product first, then the multiply-add that shares du: three different register pairs in one
                 // instruction cost a third cycle
-                h[2 * i] = fma2(du, f2_of(b.x, b.y), mul2(exp2_2(mul2(dd, A2[2 * i])), h[2 * i]));
-                h[2 * i + 1] = fma2(du, f2_of(b.z, b.w), mul2(exp2_2(mul2(dd, A2[2 * i + 1])), h[2 * i + 1]));
+#pragma unroll
+                for (int k = 0; k < CPT; ++k) {
+                    const f2 dd = f2_dup(chan(d, k)), du = f2_dup(chan(x, k));
+                    h[k][2 * i] = fma2(du, f2_of(b.x, b.y), mul2(exp2_2(mul2(dd, A2[k][2 * i])), h[k][2 * i]));
+                    h[k][2 * i + 1] = fma2(du, f2_of(b.z, b.w), mul2(exp2_2(mul2(dd, A2[k][2 * i + 1])), h[k][2 * i + 1]));
+                }
                 if (kMain) {
                     const float4 v = *reinterpret_cast<const float4*>(&sC[buf][t][l * Y::SPT + 4 * i]);
-                    y[0] = fma2(h[2 * i], f2_of(v.x, v.y), y[0]);
-                    y[1] = fma2(h[2 * i + 1], f2_of(v.z, v.w), y[1]);
+#pragma unroll
+                    for (int k = 0; k < CPT; ++k) {
+                        y[k] = fma2(h[k][2 * i], f2_of(v.x, v.y), y[k]);
+                        y[k] = fma2(h[k][2 * i + 1], f2_of(v.z, v.w), y[k]);
+                    }
                 }
             }
-            if (!kMain) return 0.f;
-            y[0] = add2(y[0], y[1]);
-            return f2_lo(y[0]) + f2_hi(y[0]);
+            if (!kMain) dsum = plus(dsum, d);
+            V out;
+            join_chans(out, f2_lo(y[0]) + f2_hi(y[0]), f2_lo(y[CPT - 1]) + f2_hi(y[CPT - 1]));
+            return out;
         };
-        auto finish = [&](int t, float s, float u) {  // the parts of a channel, the skip, the gate
+        auto soft = [&](f2 x) { return p.softplus ? softplus2(x) : x; };
+        auto finish = [&](int t, V y, V u) {  // the parts of a channel, the skip, the gate
+            if constexpr (kMain) {
 #pragma unroll
-            for (int o = Y::KPW; o < 32; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-            s = fmaf(skip, u, s);
-            if (gate) s *= silu(to_f(r.z[t][cl]));
-            return s;
+                for (int o = Y::KPW; o < 32; o *= 2)
+                    y = add2(y, f2_of(__shfl_xor_sync(0xffffffffu, f2_lo(y), o), __shfl_xor_sync(0xffffffffu, f2_hi(y), o)));
+                y = fma2(skip, u, y);
+                if (gate) {
+                    const f2 z = pair_of(&r.z[t][cl]);
+                    y = mul2(y, mul2(z, sigmoid2(z)));
+                }
+            }
+            return y;
+        };
+        auto put = [&](V y) {  // a row's outputs, and on to the next row
+            if constexpr (kMain) {
+                if (in(0) && (L == 1 || l == 0)) {
+                    if (p.wide) {
+                        put2(yp, y);
+                    } else {
+                        yp[0] = from_f<T>(f2_lo(y));
+                        if (in(1)) yp[1] = from_f<T>(f2_hi(y));
+                    }
+                }
+                yp += p.ys;
+            }
         };
         if (nt == TT && seq_end >= tb + TT) {  // no border: eight tokens without a branch between them
-            float d[TT], u[TT], s[TT];
+            V d[TT], u[TT], y[TT];
+            if constexpr (CPT == 2) {
 #pragma unroll
-            for (int t = 0; t < TT; t += 2) {
-                const f2 x = add2(f2_of(to_f(r.dt[t][cl]), to_f(r.dt[t + 1][cl])), f2_dup(bias));
-                const f2 v = p.softplus ? softplus2(x) : x;
-                d[t] = f2_lo(v);
-                d[t + 1] = f2_hi(v);
-                u[t] = to_f(r.u[t][cl]);
-                u[t + 1] = to_f(r.u[t + 1][cl]);
+                for (int t = 0; t < TT; ++t) {
+                    d[t] = soft(add2(pair_of(&r.dt[t][cl]), bias));
+                    u[t] = pair_of(&r.u[t][cl]);
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < TT; t += 2) {
+                    const f2 v = soft(add2(f2_of(to_f(r.dt[t][cl]), to_f(r.dt[t + 1][cl])), f2_dup(bias)));
+                    d[t] = f2_lo(v);
+                    d[t + 1] = f2_hi(v);
+                    u[t] = to_f(r.u[t][cl]);
+                    u[t + 1] = to_f(r.u[t + 1][cl]);
+                }
             }
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
                 if (kMode == kStates && t % 4 == 0) store_state(p.ckpt, (tb + t) / 4);
-                s[t] = token(t, d[t], u[t]);
-                if (!kMain) dsum += d[t];
+                y[t] = token(t, d[t], u[t]);
             }
-            if (kMain) {
 #pragma unroll
-                for (int t = 0; t < TT; ++t) s[t] = finish(t, s[t], u[t]);
+            for (int t = 0; t < TT; ++t) y[t] = finish(t, y[t], u[t]);
 #pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    if (in && (L == 1 || l == 0)) *yp = from_f<T>(s[t]);
-                    yp += p.ys;
-                }
-            }
+            for (int t = 0; t < TT; ++t) put(y[t]);
         } else {
 #pragma unroll 1
             for (int t = 0; t < nt; ++t) {
@@ -182,14 +258,15 @@ __global__ void __launch_bounds__(Lay<NS>::NT, 8) k_scan(Params p) {
                     seq_end = p.cu[n + 1];
                     load_state(p.init, n);
                 }
-                const float x = to_f(r.dt[t][cl]) + bias, d = p.softplus ? softplus(x) : x, u = to_f(r.u[t][cl]);
-                const float s = token(t, d, u);
-                dsum += d;
-                if (kMain) {
-                    const float o = finish(t, s, u);
-                    if (in && (L == 1 || l == 0)) *yp = from_f<T>(o);
-                    yp += p.ys;
+                V d, u;
+                if constexpr (CPT == 2) {
+                    d = soft(add2(pair_of(&r.dt[t][cl]), bias));
+                    u = pair_of(&r.u[t][cl]);
+                } else {
+                    d = f2_lo(soft(f2_dup(to_f(r.dt[t][cl]) + bias)));
+                    u = to_f(r.u[t][cl]);
                 }
+                put(finish(t, token(t, d, u), u));
             }
         }
     }
@@ -197,7 +274,10 @@ __global__ void __launch_bounds__(Lay<NS>::NT, 8) k_scan(Params p) {
         if (p.fin && seq_end == t1) store_state(p.fin, n);
     } else if (kMode == kPiece) {
         store_state(p.ws_state, piece + 1);
-        if (in && l == 0) p.ws_sum[(int64_t)piece * p.C + c] = dsum;
+        if (l == 0)
+#pragma unroll
+            for (int k = 0; k < CPT; ++k)
+                if (in(k)) p.ws_sum[(int64_t)piece * p.C + ch + k] = chan(dsum, k);
     }
 }
 
@@ -299,23 +379,22 @@ template <typename T, int NS, bool kVec> __global__ void __launch_bounds__(kStep
 }
 
 // The states at the pieces' starts, then the pass over all pieces.
-template <typename T, int NS, int kMode> cudaError_t scan_as(Params& p, cudaStream_t s) {
-    using Y = Lay<NS>;
-    p.bpg = (p.Cg + Y::CB - 1) / Y::CB;
-    const unsigned gx = (unsigned)(p.bpg * p.G);
+template <typename T, int NS, int kMode> cudaError_t scan_as(const Params& p, cudaStream_t s) {
+    // Blocks of a pass: those of the channels times `pieces`.
+    auto grid = [&p](int cb, int pieces) { return dim3((unsigned)((p.Cg + cb - 1) / cb * p.G), (unsigned)pieces); };
     if (p.pieces > 1) {
-        k_scan<T, NS, kPiece><<<dim3(gx, p.pieces - 1), Y::NT, 0, s>>>(p);
+        k_scan<T, NS, kPiece><<<grid(ScanLay<NS, kPiece>::CB, p.pieces - 1), ScanLay<NS, kPiece>::NT, 0, s>>>(p);
         if (cudaError_t e = cudaGetLastError()) return e;
         if (p.pieces > 2) {
             k_scan_join<NS><<<(unsigned)(((int64_t)p.C * NS + kJoinThreads - 1) / kJoinThreads), kJoinThreads, 0, s>>>(p);
             if (cudaError_t e = cudaGetLastError()) return e;
         }
     }
-    k_scan<T, NS, kMode><<<dim3(gx, p.pieces), Y::NT, 0, s>>>(p);
+    k_scan<T, NS, kMode><<<grid(ScanLay<NS, kMode>::CB, p.pieces), ScanLay<NS, kMode>::NT, 0, s>>>(p);
     return cudaGetLastError();
 }
 
-template <int kMode> cudaError_t scan_mode(Params& p, const kda_ssm_args& a, cudaStream_t s) {
+template <int kMode> cudaError_t scan_mode(const Params& p, const kda_ssm_args& a, cudaStream_t s) {
 #define KDA_SCAN(T)                                              \
     switch (a.Nst) {                                             \
         case 8: return scan_as<T, 8, kMode>(p, s);               \
@@ -364,19 +443,20 @@ ssm::Params ssm::params_of(const kda_ssm_args& a) {
     };
     p.vec = wide(p.u, p.us) && wide(p.dt, p.dts) && (!p.z || wide(p.z, p.zs)) && wide(p.B, p.bs) && wide(p.Cm, p.cs) &&
             (int64_t)p.Cg * es % 16 == 0;
+    p.wide = p.Cg % 2 == 0 && p.ys % 2 == 0 && reinterpret_cast<uintptr_t>(p.y) % (2 * es) == 0;
     return p;
 }
 
 ScanPlan scan_plan(const kda_ssm_args& a) {
     DeviceInfo di{0, 0, 0};
     const int64_t sms = current_device_info(&di) ? di.sm_count : 1;
-    const int64_t tt = 8, cb = a.Nst <= 16 ? 64 : 1024 / a.Nst;  // Lay<Nst>'s tile and channels per block
+    const int64_t tt = 8, cb = a.Nst <= 16 ? 128 : 2048 / a.Nst;  // ScanLay<Nst, kOut>'s tile and channels per block
     ScanPlan p{};
-    const int64_t warps = a.G * ((a.C / a.G + cb - 1) / cb) * 2;
-    // Two whole rounds of blocks, of which eight run on an SM; pieces of at least 8 tiles.  (One piece of 8,192
-    // tokens x 12,288 channels leaves two thirds of the warp slots empty: 1.5 ms, against 0.8 ms in 12 pieces, the
-    // pass over their own states included.)
-    int64_t k = 16 * sms / (warps / 2);
+    const int64_t blocks = a.G * ((a.C / a.G + cb - 1) / cb);
+    // Two whole rounds of blocks, of which six run on an SM; pieces of at least 8 tiles.  (One piece of 8,192
+    // tokens x 12,288 channels leaves most warp slots empty: 1.5 ms, against 0.69 ms in 19 pieces, the pass over
+    // their own states included; one round: 0.76 ms, three: 0.71, four: 0.69.)
+    int64_t k = 12 * sms / blocks;
     if (k > kMaxPieces) k = kMaxPieces;
     const int64_t most = a.T_total / (8 * tt);
     if (k > most) k = most;
@@ -400,7 +480,7 @@ cudaError_t launch_ssm_scan(const kda_ssm_args& a, const ScanPlan& pl, cudaStrea
     return scan_mode<kOut>(p, a, s);
 }
 
-cudaError_t ssm::launch_states(Params& p, const kda_ssm_args& a, cudaStream_t s) { return scan_mode<kStates>(p, a, s); }
+cudaError_t ssm::launch_states(const Params& p, const kda_ssm_args& a, cudaStream_t s) { return scan_mode<kStates>(p, a, s); }
 
 cudaError_t launch_ssm_step(const kda_ssm_args& a, cudaStream_t s) {
     const Params p = params_of(a);
