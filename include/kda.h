@@ -474,7 +474,7 @@ kda_status kda_layer_norm_backward(const kda_norm_backward_args* args, kda_strea
  * NaN and infinities are kept as NaN and leave the block's maximum alone.
  *
  *   x       [M][x_stride] dtype (kda_pack8 in, kda_unpack8 out); 0 means C
- *   codes   [M][C] bytes;  scales [M][ceil(C/32)] bytes; both dense
+ *   codes   [M][C] bytes;  scales [M][ceil(C/32)] bytes; both dense; C <= 2^30
  * ------------------------------------------------------------------------ */
 #define KDA_PACK8_BLOCK 32
 
@@ -502,6 +502,7 @@ kda_status kda_unpack8(const uint8_t* codes, const uint8_t* scales, int64_t M, i
  *
  * kda_ssm_conv -- the convolution over packed sequences.
  *   x, y      [T_total][row stride] io, C channels; y must not overlap x.
+ *   C         up to 2^20
  *   w         [C][4] fp32 (tap 3 multiplies x[t]; shorter filters: leading zeros)
  *   bias      [C] fp32 or NULL (zeros);  silu nonzero: SiLU after the sum
  *   conv_state_in   [N][C][3] io, oldest first, or NULL (zeros)
@@ -569,7 +570,7 @@ kda_status kda_ssm_conv_backward(const kda_ssm_conv_backward_args* args, kda_str
  *   D         [C] fp32 or NULL (zeros);  dt_bias [C] fp32 or NULL (zeros)
  *   initial_state  [N][C][Nst] fp32 or NULL (zeros)
  *   final_state    [N][C][Nst] fp32 or NULL; must not overlap initial_state
- * Nst in {8, 16, 32, 64}; G >= 1 divides C.  A, the states and the workspace 16-byte aligned
+ * C up to 2^20; Nst in {8, 16, 32, 64}; G >= 1 divides C.  A, the states and the workspace 16-byte aligned
  * (the workspace 256).
  *
  * A long stream with few channels is cut into equal pieces of the packed token axis (whatever the
@@ -615,7 +616,7 @@ kda_status kda_ssm_scan(const kda_ssm_args* args, kda_stream_t stream);
 
 /* One token for each of N sequences: rows of u, dt, B, Cm, z and y are the sequences, and
  * final_state is read and updated in place (initial_state must be NULL; T_total, cu_seqlens and
- * the workspace are ignored). */
+ * the workspace are ignored).  Row strides are below 4 GB. */
 kda_status kda_ssm_step(const kda_ssm_args* args, kda_stream_t stream);
 
 /* ------------------------------------------------------------------------

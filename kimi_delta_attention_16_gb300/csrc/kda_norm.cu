@@ -6,10 +6,16 @@
 //
 // Both are bound by HBM: one read of x (and dy), one write of y (dx).  A row lives in the
 // registers of one block (VPT accesses of W elements per thread), so the statistics take two
-// passes over registers, none over memory.  The backward is persistent: a thread owns the same
+// passes over registers, none over memory: k_layer_norm, k_layer_norm_bwd.  Many rows in 16-byte layouts
+// (k_layer_norm_rows, k_layer_norm_bwd_rows) are taken two at a time by persistent blocks, with
+// the next ones on their way to a ring in shared memory: registers alone cannot hold enough
+// loads in flight (8,192 x 7,168 bf16: forward 64 -> 40 us).  The backward is persistent: a thread owns the same
 // columns in every row of its block, keeps their dw and db sums in registers and leaves one
 // partial per block, which k_column_sum adds up in block order (no atomics: the same bits
-// every time).  The next row's accesses are issued before the current row's sums.
+// every time).
+//
+// Measured, 8,192 x 7,168 bf16: forward 40 us (5.8 TB/s), backward 69 us (5.1 TB/s; 74 from 8-bit x) and 6 us
+// for the column sums.  The backward is bound by instruction issue (two rows' sums, dw and db per element).
 #include "kda_block.cuh"
 
 namespace kda {

@@ -8,6 +8,9 @@
 // per bf16 element, one way.  Four lanes share a block (8 elements each: one 16-byte access of
 // bf16, two of fp32) and join their maxima with two shuffles; a thread takes kRows rows of the
 // same columns at once to keep enough loads in flight.
+//
+// Measured, 8,192 x 12,288 bf16: packing 59 us (5.1 TB/s, bound by instruction issue: the maximum, the scaling and the
+// conversion of every element), unpacking 47 us (6.4 TB/s).
 #include "kda_block.cuh"
 
 namespace kda {

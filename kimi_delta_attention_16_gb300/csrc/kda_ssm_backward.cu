@@ -7,15 +7,23 @@
 //
 // The states are recomputed.  Forward passes leave the state in front of every fourth token; the
 // main kernel walks a piece of the token axis backwards in tiles of four, runs a tile forward from
-// its checkpoint with a h_{t-1} of all four tokens in registers, and then backward.  Where a stream
-// is cut into pieces, what enters a piece from the right comes from a pass of its own (k_rev), the
-// mirror image of the forward scan's.
+// its checkpoint with the state in front of each token in registers (so that q_t h_{t-1} needs no decayed
+// state), and then backward.  Where a stream is cut into pieces, what enters a piece from the right
+// comes from a pass of its own (k_rev), the mirror image of the forward scan's.
 //
 // Two sums cross the threads for every token: over the states (s1, s2, y of a channel) and over the
 // channels (dB, dC of a state).  A thread therefore holds a 4 x 4 tile of (channel, state): both
 // sums run over four values in registers first, which costs nothing (they ride on the products),
 // and the rest goes through shared memory.  Sums over the blocks' channels and over the pieces go
 // through the workspace and are added in a fixed order.
+//
+// Measured, 4,096 x 4,096 x 16 bf16 with the gate: 600 us = pieces' own states 54, checkpoints 72,
+// k_rev 65, the main kernel 321, joins and sums 35, launch gaps.  The main kernel issues an instruction in 44 %
+// of the cycles: two blocks of 255-register threads per SM leave two warps per scheduler, whose dependent
+// instructions wait for one another.  Three blocks (168 registers) spill: 640 us; 2 channels x 4 states
+// per thread (four blocks of 128 registers) 356, its cross-thread sums cost what the warps gain.
+// In a copy without them: the border path 18 us, dB and dC across threads 42, the elementwise end
+// of a tile 68, the copies 60.
 #include "kda_ssm.cuh"
 
 namespace kda {

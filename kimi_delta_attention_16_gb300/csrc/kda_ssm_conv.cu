@@ -5,11 +5,16 @@
 //   dpre_t = dy_t silu'(pre_t),  dx_t = sum_j w[j] dpre_{t+3-j},  dw[j] = sum_t dpre_t x[t-3+j]
 //
 // Bound by HBM (one read of x, one write of y; backward: x and dy read, dx written).  A thread
-// owns W consecutive channels (one 16-byte access, or one element where the layout allows no more)
-// and walks a run of tokens with the last three raw values in registers; the loads of kBatch tokens
-// are issued together.  The backward walks forward too: the contributions to the last three dx wait
-// in registers, and a run reads three tokens past its end to finish its own.  dw and dbias: per
-// thread over its run, per block over its runs through shared memory, then over the blocks.
+// owns kWide = 4 consecutive channels (one element where the layout allows no more) and walks a run of
+// tokens with the last three raw values in registers; its rows come by asynchronous copies into a ring of
+// its own in shared memory, up to four batches of kBatch tokens ahead (batches loaded to registers kept
+// too few bytes in flight: forward 60 -> 48 us, backward 128 -> 97).
+// The backward walks forward too: the contributions to the last three dx wait in registers, and a run
+// reads three tokens past its end to finish its own.  dw and dbias: per thread over its run, per block over
+// its runs through shared memory, then over the blocks, in a fixed order.
+//
+// Measured, 8,192 x 8,192 bf16 in 7 sequences: forward 48 us (5.6 TB/s), backward 97 us (4.2 TB/s: two blocks
+// of 128-register threads per SM); one token for 256 sequences of 12,288 channels 12 us.
 #include "kda_block.cuh"
 
 namespace kda {
