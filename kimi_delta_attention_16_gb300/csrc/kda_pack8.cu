@@ -9,8 +9,8 @@
 // bf16, two of fp32) and join their maxima with two shuffles; a thread takes kRows rows of the
 // same columns at once to keep enough loads in flight.
 //
-// Measured, 8,192 x 12,288 bf16: packing 59 us (5.1 TB/s, bound by instruction issue: the maximum, the scaling and the
-// conversion of every element), unpacking 47 us (6.4 TB/s).
+// Measured, 8,192 x 12,288 bf16: packing 55 us (5.5 TB/s, the integer pipe 53 % busy: maxima, widening, conversions),
+// unpacking 46 us (6.5 TB/s).  Two rows per thread and six blocks: 59 and 50 us; eight rows: 60 and 56.
 #include "kda_block.cuh"
 
 namespace kda {
@@ -57,7 +57,7 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_pack8(const T* __restrict__ x, int64_t xs, int64_t M, int C,
+__global__ void __launch_bounds__(kThreads, 4) k_pack8(const T* __restrict__ x, int64_t xs, int64_t M, int C,
                                                     uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
     constexpr int W = VEC ? 16 / (int)sizeof(T) : 1;
     const int nb = (C + KDA_PACK8_BLOCK - 1) / KDA_PACK8_BLOCK;
@@ -66,14 +66,19 @@ __global__ void __launch_bounds__(kThreads) k_pack8(const T* __restrict__ x, int
     const int64_t tile = (int64_t)blockDim.y * kRows;
     for (int64_t base = blockIdx.y * tile; base < M; base += gridDim.y * tile) {  // the same for the whole block
         const int64_t r0 = base + threadIdx.y * kRows;
+        const int rows = n == 0 || r0 >= M ? 0 : M - r0 < kRows ? (int)(M - r0) : kRows;  // this thread's
+        const T* src = x + r0 * xs + c0;
+        uint8_t *dst = codes + r0 * C + c0, *sdst = scales + r0 * nb + c0 / KDA_PACK8_BLOCK;
         Raw<T, W> raw[kRows][kElems / W];
 #pragma unroll
-        for (int q = 0; q < kRows; ++q)
+        for (int q = 0; q < kRows; ++q) {
 #pragma unroll
             for (int i = 0; i < kElems / W; ++i)
-                if (r0 + q < M && i * W < n) raw[q][i].load(x + (r0 + q) * xs + c0 + i * W); else raw[q][i].zero();
+                if (q < rows && (W == kElems || i * W < n)) raw[q][i].load(src + i * W); else raw[q][i].zero();
+            src += xs;
+        }
 #pragma unroll
-        for (int q = 0; q < kRows; ++q) {
+        for (int q = 0; q < kRows; ++q, dst += C, sdst += nb) {
             float v[kElems];
 #pragma unroll
             for (int i = 0; i < kElems / W; ++i) {
@@ -93,8 +98,7 @@ __global__ void __launch_bounds__(kThreads) k_pack8(const T* __restrict__ x, int
             }
             amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            const int64_t r = r0 + q;
-            if (r >= M || n == 0) continue;
+            if (q >= rows) continue;  // every lane comes to the shuffles
             const uint32_t byte = scale_byte(amax);
             const f2 inv = f2_dup(__uint_as_float((254u - byte) << 23));  // 2^-e
             uint32_t two[kElems / 2];
@@ -103,7 +107,6 @@ __global__ void __launch_bounds__(kThreads) k_pack8(const T* __restrict__ x, int
                 const f2 s = mul2(f2_of(v[2 * i], v[2 * i + 1]), inv);
                 two[i] = to_e4m3x2(f2_lo(s), f2_hi(s));
             }
-            uint8_t* dst = codes + r * C + c0;
             if constexpr (VEC) {  // C is a multiple of W, so a row's codes start on a W-byte boundary
 #pragma unroll
                 for (int i = 0; i < kElems / 4; ++i) two[i] = two[2 * i] | (two[2 * i + 1] << 16);
@@ -119,13 +122,13 @@ __global__ void __launch_bounds__(kThreads) k_pack8(const T* __restrict__ x, int
                 for (int i = 0; i < kElems; ++i)
                     if (i < n) dst[i] = (uint8_t)(two[i / 2] >> (8 * (i & 1)));
             }
-            if ((threadIdx.x & 3) == 0) scales[r * nb + c0 / KDA_PACK8_BLOCK] = (uint8_t)byte;
+            if ((threadIdx.x & 3) == 0) *sdst = (uint8_t)byte;
         }
     }
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_unpack8(const uint8_t* __restrict__ codes,
+__global__ void __launch_bounds__(kThreads, 4) k_unpack8(const uint8_t* __restrict__ codes,
                                                       const uint8_t* __restrict__ scales, int64_t M, int C,
                                                       T* __restrict__ x, int64_t xs) {
     constexpr int W = VEC ? 16 / (int)sizeof(T) : 1;
@@ -136,25 +139,30 @@ __global__ void __launch_bounds__(kThreads) k_unpack8(const uint8_t* __restrict_
     const int64_t tile = (int64_t)blockDim.y * kRows;
     for (int64_t base = blockIdx.y * tile; base < M; base += gridDim.y * tile) {  // the same for the whole block
         const int64_t r0 = base + threadIdx.y * kRows;
+        const int rows = r0 >= M ? 0 : M - r0 < kRows ? (int)(M - r0) : kRows;  // this thread's
+        const uint8_t *src = codes + r0 * C + c0, *ssrc = scales + r0 * nb + c0 / KDA_PACK8_BLOCK;
+        T* dst = x + r0 * xs + c0;
         Raw<uint8_t, W> raw[kRows][kElems / W];
         uint32_t sc[kRows];
 #pragma unroll
         for (int q = 0; q < kRows; ++q) {
-            const bool in = r0 + q < M;
-            sc[q] = in ? (uint32_t)__ldg(scales + (r0 + q) * nb + c0 / KDA_PACK8_BLOCK) : 127u;
+            sc[q] = q < rows ? (uint32_t)__ldg(ssrc) : 127u;
 #pragma unroll
             for (int i = 0; i < kElems / W; ++i)
-                if (in && i * W < n) raw[q][i].load(codes + (r0 + q) * C + c0 + i * W); else raw[q][i].zero();
+                if (q < rows && (W == kElems || i * W < n)) raw[q][i].load(src + i * W); else raw[q][i].zero();
+            src += C;
+            ssrc += nb;
         }
 #pragma unroll
         for (int q = 0; q < kRows; ++q) {
-            if (r0 + q >= M) continue;
+            if (q >= rows) break;
 #pragma unroll
             for (int i = 0; i < kElems / W; ++i) {
                 float t[W];
                 unraw8(raw[q][i], scale_of_byte(sc[q]), t);
-                if (i * W < n) store_row(x + (r0 + q) * xs + c0 + i * W, t);
+                if (W == kElems || i * W < n) store_row(dst + i * W, t);
             }
+            dst += xs;
         }
     }
 }
