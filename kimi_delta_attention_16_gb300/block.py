@@ -96,7 +96,11 @@ def _rows(t: torch.Tensor, M: int, C: int, dtype, name: str) -> int:
     s0, s1 = t.stride()
     if s1 != 1 and C > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return s0 if M > 1 else C
+    if M <= 1:
+        return C
+    if s0 < C:  # a broadcast row above all: to the library a stride of 0 means C
+        raise ValueError(f"the rows of {name} overlap (stride {s0} below {C})")
+    return s0
 
 
 def _dense(t: Optional[torch.Tensor], shape, dtype, name: str) -> int:
@@ -347,7 +351,11 @@ def _grouped(t: torch.Tensor, rows: int, G: int, N: int, dtype, name: str) -> in
     s0, s1, s2 = t.stride()
     if (N > 1 and s2 != 1) or (G > 1 and s1 != N):
         raise ValueError(f"the (G, N) block of each row of {name} must be contiguous")
-    return s0 if rows > 1 else G * N
+    if rows <= 1:
+        return G * N
+    if s0 < G * N:
+        raise ValueError(f"the rows of {name} overlap (stride {s0} below {G * N})")
+    return s0
 
 
 def _ssm_inputs(u, dt, A, B, C, D, z, dt_bias):

@@ -270,3 +270,23 @@ def test_packed_structs_are_the_declared_ones():
             for part in name.split("."):
                 obj = getattr(obj, part)
             assert obj == v, name
+
+
+def test_broadcast_rows_are_refused():
+    """A stride of 0 means "dense" to the library, so a broadcast row would be read past its end."""
+    row, rows = torch.zeros(1, 64).expand(8, 64), torch.zeros(8, 64)
+    w, cu, A = torch.zeros(64, 4), torch.tensor([0, 8], dtype=torch.int32), torch.zeros(64, 16)
+    BC, one = torch.zeros(8, 1, 16), torch.zeros(1, 1, 16).expand(8, 1, 16)
+    stats = torch.zeros(8, 2)
+    for call in (lambda: kda.kda_layer_norm(row), lambda: kda.kda_layer_norm(rows, y=row),
+                 lambda: kda.kda_layer_norm_backward(row, rows, stats), lambda: kda.kda_layer_norm_backward(rows, row, stats),
+                 lambda: kda.kda_pack8(row), lambda: kda.kda_pack8(torch.zeros(1, 1).expand(4, 1)),
+                 lambda: kda.kda_ssm_conv(row, w, cu), lambda: kda.kda_ssm_conv_step(row, w, torch.zeros(8, 64, 3)),
+                 lambda: kda.kda_ssm_conv_backward(rows, w, cu, row), lambda: kda.kda_ssm_scan(row, rows, A, BC, BC, cu),
+                 lambda: kda.kda_ssm_scan(rows, rows, A, one, BC, cu), lambda: kda.kda_ssm_scan(rows, rows, A, BC, one, cu),
+                 lambda: kda.kda_ssm_scan(rows, rows, A, BC, BC, cu, z=row),
+                 lambda: kda.kda_ssm_step(rows, row, A, BC, BC, torch.zeros(8, 64, 16)),
+                 lambda: kda.kda_ssm_backward(rows, rows, A, BC, BC, cu, row),
+                 lambda: kda.kda_layer_norm(torch.zeros(4, 40).as_strided((8, 16), (8, 1)))):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
