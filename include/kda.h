@@ -630,7 +630,7 @@ kda_status kda_ssm_step(const kda_ssm_args* args, kda_stream_t stream);
  * fwd: the forward call's arguments; its y, final_state and workspace are ignored (the states are
  * recomputed).  du, ddt, dz, dB and dC are io, dense ([T_total][C], [T_total][G][Nst]), rounded
  * once; dA [C][Nst], dD [C], ddt_bias [C] and dinitial_state [N][C][Nst] are fp32.  dz, dD,
- * ddt_bias and dinitial_state may be NULL (not wanted); the others must not.  Sums over channels
+ * ddt_bias and dinitial_state may be NULL (not wanted); the others must not.  G is at most 65535.  Sums over channels
  * and tokens go through the workspace in a fixed order.
  * ------------------------------------------------------------------------ */
 typedef struct {

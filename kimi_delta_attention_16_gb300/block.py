@@ -46,6 +46,7 @@ def _on(stream, *inputs):
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
     if s != torch.cuda.current_stream():
         for t in inputs:
+            t = t[0] if isinstance(t, tuple) else t  # the device half of a cu_seqlens pair
             if isinstance(t, torch.Tensor) and t.is_cuda:
                 t.record_stream(s)
     with torch.cuda.stream(s):
@@ -72,6 +73,14 @@ def _stream_of(index: int) -> int:
 
 def _ptr(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.data_ptr()
+
+
+def _status(t: Optional[torch.Tensor]) -> int:
+    if t is None:
+        return 0
+    if t.dtype != torch.int32 or t.numel() < 1:
+        raise ValueError(f"d_status must be an int32 tensor, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _io(t: torch.Tensor, name: str) -> int:
@@ -132,6 +141,8 @@ def _workspace(name: str, index: int, sizes, fmt, args, tail, workspace, device)
             return 0, 0, None
         workspace = torch.empty(n, dtype=_U8, device=device)
         return workspace.data_ptr(), n, workspace
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
@@ -266,7 +277,7 @@ def kda_ssm_conv(x: torch.Tensor, w: torch.Tensor, cu_seqlens, *, bias: Optional
     conv_state_in [N, C, 3] like x continues earlier tokens.  Returns y, or (y, conv_state_out [N, C, 3]) when
     output_conv_state is set or a conv_state_out is given."""
     if stream is not None:
-        with _on(stream, x, w, bias, conv_state_in, conv_state_out, y, d_status):
+        with _on(stream, x, w, cu_seqlens, bias, conv_state_in, conv_state_out, y, d_status):
             return kda_ssm_conv(x, w, cu_seqlens, bias=bias, silu=silu, conv_state_in=conv_state_in,
                                 conv_state_out=conv_state_out, output_conv_state=output_conv_state, y=y,
                                 d_status=d_status, check_cu_on_host=check_cu_on_host)
@@ -285,7 +296,7 @@ def kda_ssm_conv(x: torch.Tensor, w: torch.Tensor, cu_seqlens, *, bias: Optional
     if y is None:
         y = torch.empty((T, C), dtype=dtype, device=dev)
     a = _CONV.pack(N, C, T, io, bool(silu), cu.data_ptr(), host.ctypes.data if check_cu_on_host else 0, x.data_ptr(), xs,
-                   wp, bp, si, so, y.data_ptr(), ys, _ptr(d_status))
+                   wp, bp, si, so, y.data_ptr(), ys, _status(d_status))
     _check(lib.kda_ssm_conv(a, _stream_of(index)), "kda_ssm_conv")
     return y if conv_state_out is None else (y, conv_state_out)
 
@@ -318,7 +329,7 @@ def kda_ssm_conv_backward(x: torch.Tensor, w: torch.Tensor, cu_seqlens, dy: torc
     """Gradients of sum(dy * y) of one kda_ssm_conv call (same inputs): a dict of dx (x's dtype), dw [C, 4] fp32, dbias
     [C] fp32 when bias is given, dconv_state_in [N, C, 3] fp32 when conv_state_in is given."""
     if stream is not None:
-        with _on(stream, x, w, dy, bias, conv_state_in, workspace, d_status):
+        with _on(stream, x, w, cu_seqlens, dy, bias, conv_state_in, workspace, d_status):
             return kda_ssm_conv_backward(x, w, cu_seqlens, dy, bias=bias, silu=silu, conv_state_in=conv_state_in,
                                          workspace=workspace, d_status=d_status, check_cu_on_host=check_cu_on_host)
     lib = _lib.load()
@@ -336,7 +347,7 @@ def kda_ssm_conv_backward(x: torch.Tensor, w: torch.Tensor, cu_seqlens, dy: torc
     if conv_state_in is not None:
         res["dconv_state_in"] = torch.empty((N, C, 3), dtype=_F32, device=dev)
     args = (N, C, T, io, bool(silu), cu.data_ptr(), host.ctypes.data if check_cu_on_host else 0, x.data_ptr(), xs, wp, bp,
-            si, 0, 0, 0, _ptr(d_status), dy.data_ptr(), dys, res["dx"].data_ptr(), C, res["dw"].data_ptr(),
+            si, 0, 0, 0, _status(d_status), dy.data_ptr(), dys, res["dx"].data_ptr(), C, res["dw"].data_ptr(),
             _ptr(res.get("dbias")), _ptr(res.get("dconv_state_in")))
     p, n, keep = _workspace("kda_ssm_conv_backward_workspace_size", index, (T, C, io), _CONV_BWD, args, (), workspace, dev)
     _check(lib.kda_ssm_conv_backward(_CONV_BWD.pack(*args, p, n), _stream_of(index)), "kda_ssm_conv_backward")
@@ -387,7 +398,7 @@ def kda_ssm_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Te
     softplus: the step size is softplus(dt + dt_bias), else dt + dt_bias.  initial_state / final_state [num_sequences,
     Ch, N] fp32 (not the same buffer)."""
     if stream is not None:
-        with _on(stream, u, dt, A, B, C, D, z, dt_bias, initial_state, final_state, y, workspace, d_status):
+        with _on(stream, u, dt, A, B, C, cu_seqlens, D, z, dt_bias, initial_state, final_state, y, workspace, d_status):
             return kda_ssm_scan(u, dt, A, B, C, cu_seqlens, D=D, z=z, dt_bias=dt_bias, softplus=softplus,
                                 initial_state=initial_state, output_final_state=output_final_state,
                                 final_state=final_state, y=y, workspace=workspace, d_status=d_status,
@@ -407,7 +418,7 @@ def kda_ssm_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Te
         y = torch.empty((T, Ch), dtype=dtype, device=dev)
     args = (n, Ch, N, G, T, io, bool(softplus), cu.data_ptr(), host.ctypes.data if check_cu_on_host else 0, *vals, ip, fp,
             y.data_ptr(), ys)
-    status = _ptr(d_status)
+    status = _status(d_status)
     p, size, keep = _workspace("kda_ssm_scan_workspace_size", index, (T, Ch, N, G, io), _SSM, args, (status,), workspace, dev)
     _check(lib.kda_ssm_scan(_SSM.pack(*args, p, size, status), _stream_of(index)), "kda_ssm_scan")
     return y, final_state
@@ -445,7 +456,7 @@ def kda_ssm_backward(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torc
     ddt_bias [Ch] fp32 and dinitial_state fp32.  The workspace holds the states in front of every fourth token:
     about T * Ch * N bytes."""
     if stream is not None:
-        with _on(stream, u, dt, A, B, C, dy, D, z, dt_bias, initial_state, d_final_state, workspace, d_status):
+        with _on(stream, u, dt, A, B, C, cu_seqlens, dy, D, z, dt_bias, initial_state, d_final_state, workspace, d_status):
             return kda_ssm_backward(u, dt, A, B, C, cu_seqlens, dy, D=D, z=z, dt_bias=dt_bias, softplus=softplus,
                                     initial_state=initial_state, d_final_state=d_final_state, workspace=workspace,
                                     d_status=d_status, check_cu_on_host=check_cu_on_host)
@@ -475,7 +486,7 @@ def kda_ssm_backward(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torc
     if initial_state is not None:
         res["dinitial_state"] = params(n, Ch, N)
     args = (n, Ch, N, G, T, io, bool(softplus), cu.data_ptr(), host.ctypes.data if check_cu_on_host else 0, *vals, ip, 0,
-            0, 0, 0, 0, _ptr(d_status), dy.data_ptr(), dys, dfp,
+            0, 0, 0, 0, _status(d_status), dy.data_ptr(), dys, dfp,
             *(_ptr(res.get(k)) for k in ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dinitial_state")))
     p, size, keep = _workspace("kda_ssm_backward_workspace_size", index, (T, Ch, N, G, io), _SSM_BWD, args, (), workspace, dev)
     _check(lib.kda_ssm_backward(_SSM_BWD.pack(*args, p, size), _stream_of(index)), "kda_ssm_backward")

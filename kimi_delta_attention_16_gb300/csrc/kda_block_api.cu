@@ -111,6 +111,12 @@ kda_status check_ssm_sizes(const kda_ssm_args& a) {
     return KDA_OK;
 }
 
+// The gradients sum dB and dC with one row of blocks per group.
+kda_status check_backward_groups(const kda_ssm_args& a) {
+    if (a.G > 65535) return fail(KDA_ERR_UNSUPPORTED, "G=%d above 65535", a.G);
+    return KDA_OK;
+}
+
 size_t state_bytes(const kda_ssm_args& a) { return (size_t)a.N * a.C * a.Nst * sizeof(float); }
 
 kda_status check_ssm_rows(const kda_ssm_args& a, int64_t rows) {
@@ -417,7 +423,8 @@ kda_status kda_ssm_backward_workspace_size(const kda_ssm_backward_args* b, size_
     *bytes = 0;
     if (!b) return fail(KDA_ERR_INVALID_ARG, "args is NULL");
     const kda_ssm_args& f = b->fwd;
-    if (kda_status st = check_ssm_sizes(f)) return st;
+    kda_status st;
+    if ((st = check_ssm_sizes(f)) || (st = check_backward_groups(f))) return st;
     if (f.T_total < 0 || f.T_total > 0x7fffffffLL || f.C > kMaxChannels) return fail(KDA_ERR_INVALID_ARG, "bad sizes");
     if (f.T_total > 0) *bytes = ssm_backward_plan(f).workspace;
     return ok();
@@ -427,7 +434,8 @@ kda_status kda_ssm_backward(const kda_ssm_backward_args* b, kda_stream_t stream)
     if (!b) return fail(KDA_ERR_INVALID_ARG, "args is NULL");
     const kda_ssm_args& f = b->fwd;
     kda_status st;
-    if ((st = check_packed(f.N, f.C, f.T_total, f.io, f.cu_seqlens, f.cu_seqlens_host)) || (st = check_ssm_sizes(f)))
+    if ((st = check_packed(f.N, f.C, f.T_total, f.io, f.cu_seqlens, f.cu_seqlens_host)) || (st = check_ssm_sizes(f)) ||
+        (st = check_backward_groups(f)))
         return st;
     const size_t es = dsize(f.io), cb = (size_t)f.C * 4, an = cb * f.Nst, sb = state_bytes(f);
     if (!b->dA) return fail(KDA_ERR_INVALID_ARG, "dA is NULL");

@@ -290,3 +290,23 @@ def test_broadcast_rows_are_refused():
                  lambda: kda.kda_layer_norm(torch.zeros(4, 40).as_strided((8, 16), (8, 1)))):
         with pytest.raises(ValueError, match="overlap"):
             call()
+
+
+def test_status_words_and_workspaces_are_checked():
+    from kimi_delta_attention_16_gb300 import block
+    assert block._status(None) == 0
+    for bad in (torch.zeros(1, dtype=torch.int8), torch.zeros(0, dtype=torch.int32), torch.zeros(1)):
+        with pytest.raises(ValueError, match="int32"):
+            block._status(bad)
+    wide = torch.zeros(1, dtype=torch.uint8).expand(1 << 20)  # claims a million bytes and has one
+    with pytest.raises(ValueError, match="contiguous"):
+        block._workspace("", 0, (), None, (), (), wide, None)
+
+
+def test_scan_gradients_refuse_more_groups_than_a_grid_has_rows():
+    n = ctypes.c_size_t(0)
+    for groups, code in ((65536, UNSUPPORTED), (65535, 0)):
+        a = ssm_bwd(fwd__G=groups, fwd__C=groups, fwd__T_total=0)
+        assert _lib.load().kda_ssm_backward_workspace_size(ctypes.byref(a), ctypes.byref(n)) == code
+    a = ssm_bwd(fwd__G=65536, fwd__C=65536)
+    assert call("kda_ssm_backward", a) == UNSUPPORTED

@@ -459,3 +459,27 @@ def test_large_offsets():
     assert torch.equal(c[0], c0[0]) and torch.equal(c[1], c0[1])
     out = torch.as_strided(buf, (T, C), (stride, 1), 256)
     assert torch.equal(kda.kda_unpack8(*c, out=out), kda.kda_unpack8(*c))
+
+
+def test_inputs_of_a_call_on_another_stream_are_marked(monkeypatch):
+    """The allocator is told that the other stream reads the inputs, cu_seqlens among them (a list's device copy
+    is made on that stream itself)."""
+    a = ssm_inputs(5, 32, 16, 16, 1, FP, 1)
+    cu = torch.tensor([0, 32], dtype=torch.int32)
+    pair = (cu.to(DEV), cu.numpy())
+    marked = []
+    mark = torch.Tensor.record_stream
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: (marked.append(t.data_ptr()), mark(t, s))[1])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    w = torch.zeros(16, 4, device=DEV)
+    dev = {k: v.to(DEV) if isinstance(v, torch.Tensor) else v for k, v in a.items()}
+    s.wait_stream(torch.cuda.current_stream())
+    for call in (lambda: kda.kda_ssm_conv(dev["u"], w, pair, stream=s),
+                 lambda: kda.kda_ssm_conv_backward(dev["u"], w, pair, dev["u"], stream=s),
+                 lambda: kda.kda_ssm_scan(dev["u"], dev["dt"], dev["A"], dev["B"], dev["C"], pair, stream=s),
+                 lambda: kda.kda_ssm_backward(dev["u"], dev["dt"], dev["A"], dev["B"], dev["C"], pair, dev["u"], stream=s)):
+        marked.clear()
+        call()
+        assert pair[0].data_ptr() in marked and dev["u"].data_ptr() in marked
+    s.synchronize()
