@@ -579,9 +579,9 @@ SsmBackwardPlan ssm_backward_plan(const kda_ssm_args& f) {
     const int64_t sms = current_device_info(&di) ? di.sm_count : 1;
     const int64_t cg = f.C / f.G, ch = ch_of(f.Nst), blocks = f.G * ((cg + ch - 1) / ch);
     SsmBackwardPlan p{};
-    // Two blocks of the main kernel run on an SM and eight of the passes before it, of which there are twice as many:
-    // two whole rounds of the former are one of the latter (4,096 tokens x 4,096 channels x 16: 0.71 ms for forward
-    // and gradients, 0.74 to 0.77 with one, three, four or six rounds).  Pieces of at least 64 tokens.
+    // Two blocks of the main kernel run on an SM and eight of the passes before it, of which there are up to twice as
+    // many: two whole rounds of the former are one of the latter (4,096 tokens x 4,096 channels x 16: 0.67 ms for forward
+    // and gradients, 0.75, 0.71 and 0.70 with one, three and four rounds).  Pieces of at least 64 tokens.
     int64_t k = 4 * sms / blocks;
     if (k > kMaxPieces) k = kMaxPieces;
     if (k > f.T_total / 64) k = f.T_total / 64;

@@ -22,8 +22,8 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;   // tokens taken together
-constexpr int kWide = 4;   // channels per thread where the layout allows (8 bytes of bf16, 16 of fp32)
+constexpr int kBatch = 4;  // tokens taken together
+constexpr int kWide = 4;  // channels per thread where the layout allows (8 bytes of bf16, 16 of fp32)
 
 // A thread's own rows (W channels, consecutive tokens) through shared memory: up to four batches of kBatch
 // tokens are in flight, the thread reads back what it copied itself, so nothing waits for anybody else.
@@ -141,7 +141,7 @@ template <int W> __device__ __forceinline__ void load_state(const bf16* p, float
 }
 
 template <typename T, int W>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 k_conv(const T* __restrict__ x, int64_t xs, const float* __restrict__ w, const float* __restrict__ bias, int silu,
        const int32_t* cu, int N, int64_t T_total, int C, const T* __restrict__ cs_in, T* __restrict__ cs_out,
        T* __restrict__ y, int64_t ys, int run, unsigned strips) {
