@@ -62,7 +62,7 @@ def _device(first: torch.Tensor, *others) -> int:
             raise ValueError(f"tensors are on {first.device} and on {t.device}; every tensor must be on one CUDA device")
     if index < 0:
         raise ValueError(f"tensors are on {first.device}; every tensor must be on a CUDA device")
-    if index != torch.cuda.current_device():
+    if index != torch._C._cuda_getDevice():  # CUDA is up: a tensor is on it
         raise ValueError(f"tensors are on {first.device} but the current device is cuda:{torch.cuda.current_device()}")
     return index
 
@@ -286,9 +286,8 @@ def kda_ssm_conv(x: torch.Tensor, w: torch.Tensor, cu_seqlens, *, bias: Optional
     io, dtype, dev = _io(x, "x"), x.dtype, x.device
     xs, wp, bp = _rows(x, T, C, dtype, "x"), _dense(_need(w, "w"), (C, 4), _F32, "w"), _dense(bias, (C,), _F32, "bias")
     ys = C if y is None else _rows(y, T, C, dtype, "y")
-    index = _device(x, w, bias, conv_state_in, conv_state_out, y, d_status)
     cu, host, N = _packed_cu(cu_seqlens, dev)
-    _device(x, cu)
+    index = _device(x, w, cu, bias, conv_state_in, conv_state_out, y, d_status)
     if conv_state_out is None and output_conv_state:
         conv_state_out = torch.empty((N, C, 3), dtype=dtype, device=dev)
     si = _dense(conv_state_in, (N, C, 3), dtype, "conv_state_in")
@@ -337,9 +336,8 @@ def kda_ssm_conv_backward(x: torch.Tensor, w: torch.Tensor, cu_seqlens, dy: torc
     io, dtype, dev = _io(x, "x"), x.dtype, x.device
     xs, wp, bp = _rows(x, T, C, dtype, "x"), _dense(_need(w, "w"), (C, 4), _F32, "w"), _dense(bias, (C,), _F32, "bias")
     dys = _rows(dy, T, C, dtype, "dy")
-    index = _device(x, w, dy, bias, conv_state_in, workspace, d_status)
     cu, host, N = _packed_cu(cu_seqlens, dev)
-    _device(x, cu)
+    index = _device(x, w, cu, dy, bias, conv_state_in, workspace, d_status)
     si = _dense(conv_state_in, (N, C, 3), dtype, "conv_state_in")
     res = {"dx": torch.empty((T, C), dtype=dtype, device=dev), "dw": torch.empty((C, 4), dtype=_F32, device=dev)}
     if bias is not None:
@@ -406,10 +404,8 @@ def kda_ssm_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Te
     lib = _lib.load()
     T, Ch, N, G, io, dtype, vals = _ssm_inputs(u, dt, A, B, C, D, z, dt_bias)
     ys, dev = Ch if y is None else _rows(y, T, Ch, dtype, "y"), u.device
-    index = _device(u, dt, A, B, C, D, z, dt_bias, initial_state,
-                    final_state, y, workspace, d_status)
     cu, host, n = _packed_cu(cu_seqlens, dev)
-    _device(u, cu)
+    index = _device(u, dt, A, B, C, cu, D, z, dt_bias, initial_state, final_state, y, workspace, d_status)
     ip = _dense(initial_state, (n, Ch, N), _F32, "initial_state")
     if final_state is None and output_final_state:
         final_state = torch.empty((n, Ch, N), dtype=_F32, device=dev)
@@ -463,10 +459,8 @@ def kda_ssm_backward(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torc
     lib = _lib.load()
     T, Ch, N, G, io, dtype, vals = _ssm_inputs(u, dt, A, B, C, D, z, dt_bias)
     dys, dev = _rows(dy, T, Ch, dtype, "dy"), u.device
-    index = _device(u, dt, A, B, C, dy, D, z, dt_bias, initial_state,
-                    d_final_state, workspace, d_status)
     cu, host, n = _packed_cu(cu_seqlens, dev)
-    _device(u, cu)
+    index = _device(u, dt, A, B, C, cu, dy, D, z, dt_bias, initial_state, d_final_state, workspace, d_status)
     ip = _dense(initial_state, (n, Ch, N), _F32, "initial_state")
     dfp = _dense(d_final_state, (n, Ch, N), _F32, "d_final_state")
 
