@@ -7,21 +7,20 @@
 namespace kda {
 namespace ssm {
 
-// softplus(x) = max(x, 0) + log(1 + e^-|x|), to a few units of the last place for every x: the
-// logarithm as 2 atanh(s), s = e / (2 + e) <= 1/3, by its odd power series up to s^13 (the next
-// term is below 2^-26 of the sum).  log(1 + e) directly would lose the digits of a small e.
-// Both halves of a pair at once.
+// softplus(x) = max(x, 0) + log(1 + e^-|x|), to a few units of the last place (far below 0 the exponent's own
+// rounding, |x| 2^-24, comes on top, where e^x is all that is left): the
+// logarithm as 2 atanh(s) = s P(s^2), s = e / (2 + e) <= 1/3, with a polynomial of degree 4 fitted to the quotient
+// 2 atanh(s) / s over s^2 in [0, 1/9] (relative error 2^-26; its power series would take degree 6).
+// log(1 + e) directly would lose the digits of a small e.  Both halves of a pair at once.
 __device__ __forceinline__ f2 softplus2(f2 x) {
     const f2 t = mul2(f2_of(fabsf(f2_lo(x)), fabsf(f2_hi(x))), f2_dup(-kLog2e));
     const f2 e = f2_of(exp2_hw(f2_lo(t)), exp2_hw(f2_hi(t)));
     const f2 d = add2(e, f2_dup(2.f));
     const f2 s = mul2(e, f2_of(rcp_hw(f2_lo(d)), rcp_hw(f2_hi(d)))), q = mul2(s, s);
-    f2 p = f2_dup(2.f / 13.f);
-    p = fma2(p, q, f2_dup(2.f / 11.f));
-    p = fma2(p, q, f2_dup(2.f / 9.f));
-    p = fma2(p, q, f2_dup(2.f / 7.f));
-    p = fma2(p, q, f2_dup(2.f / 5.f));
-    p = fma2(p, q, f2_dup(2.f / 3.f));
+    f2 p = f2_dup(0.2817833423614502f);
+    p = fma2(p, q, f2_dup(0.27960604429244995f));
+    p = fma2(p, q, f2_dup(0.40024909377098083f));
+    p = fma2(p, q, f2_dup(0.6666631698608398f));
     p = fma2(p, q, f2_dup(2.f));
     return fma2(s, p, f2_of(fmaxf(f2_lo(x), 0.f), fmaxf(f2_hi(x), 0.f)));
 }

@@ -14,7 +14,7 @@
 // pieces.  kPiece runs every piece from a zero state, k_scan_join carries the states through (a piece's
 // effect on what enters it is 2^(A log2 e sum of delta)), kOut runs the pieces again from the right states.
 //
-// Measured, 8,192 x 12,288 x 16 bf16 with the gate: 691 us = 404 (kOut, 2.0 TB/s) + 278 (kPiece) + 9.
+// Measured, 8,192 x 12,288 x 16 bf16 with the gate: 685 us = 401 (kOut, 2.0 TB/s) + 275 (kPiece) + 9.
 // Bound by instruction issue and the register file: taken out one at a time in a copy, the exponentials
 // are worth 35 us, reading B and C 56, softplus 50, the gate 40, the copies 67, the stores 0.
 //
