@@ -13,7 +13,7 @@
 // reads three tokens past its end to finish its own.  dw and dbias: per thread over its run, per block over
 // its runs through shared memory, then over the blocks, in a fixed order.
 //
-// Measured, 8,192 x 8,192 bf16 in 7 sequences: forward 48 us (5.6 TB/s), backward 97 us (4.2 TB/s: two blocks
+// Measured, 8,192 x 8,192 bf16 in 7 sequences: forward 46 us (5.8 TB/s), backward 97 us (4.2 TB/s: two blocks
 // of 128-register threads per SM); one token for 256 sequences of 12,288 channels 12 us.
 #include "kda_block.cuh"
 

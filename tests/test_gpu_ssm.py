@@ -483,3 +483,27 @@ def test_inputs_of_a_call_on_another_stream_are_marked(monkeypatch):
         call()
         assert pair[0].data_ptr() in marked and dev["u"].data_ptr() in marked
     s.synchronize()
+
+
+SHORT = [37, 5, 90, 1, 0, 64, 8, 200, 3, 120, 16, 31, 64, 64, 7, 400, 2, 128, 129, 63, 1]
+
+
+@pytest.mark.parametrize("how", ["dense", "odd"])
+@pytest.mark.parametrize("Ch,N,G,io", [(48, 16, 1, FP), (26, 32, 2, BF), (40, 8, 1, BF), (20, 64, 2, FP)])
+def test_short_sequences_over_pieces(Ch, N, G, io, how):
+    """Pieces that hold several sequences: only the last that starts in one leaves a state to the next, and only the
+    first that ends in one sends a gradient back.  Initial and final states of all of them take part."""
+    T, n = sum(SHORT), len(SHORT)
+    a = ssm_inputs(T + Ch, T, Ch, N, G, io, n, slow=True)
+    y, fin = run_scan(a, SHORT, how)
+    ry, rf = ssm_ref(a["u"], a["dt"], a["A"], a["B"], a["C"], SHORT, a["D"], a["z"], a["dt_bias"], True, a["init"])
+    ey, ef = scan_bounds(a, SHORT)
+    within(y, ry, ey + U[io] * (ry.abs() + ey), "y")
+    within(fin, rf, ef, "final_state")
+    g = gen(T + 1)
+    dy, dfin = randn(g, T, Ch, dtype=io), randn(g, n, Ch, N)
+    got = run_backward(a, SHORT, dy, dfin, how)
+    ref, tol = ref_grads(a, SHORT, dy, dfin), grad_bounds(a, SHORT, dy, dfin)
+    for name, r in ref.items():
+        u = U[io] if name in ("du", "ddt", "dz", "dB", "dC") else 0.0
+        within(got[name], r, tol[name] + u * (r.abs() + tol[name]) + U32 * r.abs(), name)
