@@ -87,13 +87,15 @@ constexpr int kJoinThreads = 128;
 constexpr int kMaxPieces = 1024;  // of a plan
 constexpr int kJoinBits = kMaxPieces;
 
-// Bit k: a sequence starts in piece k (at its first token or inside), so nothing passes through it.
-__device__ __forceinline__ void mark_started(const Params& p, uint32_t (&bits)[kJoinBits / 32]) {
+// Bit k: nothing passes through piece k.  From the left (kDir = 1) because a sequence starts in it, at its first
+// token or inside; from the right (kDir = -1) because one ends in it, inside or at its last token.  The two differ where
+// a sequence's border is a piece's: its end closes the piece before, its start the piece behind.
+template <int kDir> __device__ __forceinline__ void mark_closed(const Params& p, uint32_t (&bits)[kJoinBits / 32]) {
     for (int k = threadIdx.x; k < kJoinBits; k += kJoinThreads) {
         bool s = false;
         if (k < p.pieces) {
-            const int64_t t1 = (k + 1) * p.piece < p.T ? (k + 1) * p.piece : p.T;
-            s = p.cu[seq_of(p.cu, p.N, t1 - 1)] >= k * p.piece;
+            const int64_t t0 = k * p.piece, t1 = t0 + p.piece < p.T ? t0 + p.piece : p.T;
+            s = kDir > 0 ? p.cu[seq_of(p.cu, p.N, t1 - 1)] >= t0 : p.cu[seq_of(p.cu, p.N, t0) + 1] <= t1;
         }
         const uint32_t w = __ballot_sync(0xffffffffu, s);
         if ((threadIdx.x & 31) == 0) bits[k / 32] = w;
@@ -101,11 +103,11 @@ __device__ __forceinline__ void mark_started(const Params& p, uint32_t (&bits)[k
     __syncthreads();
 }
 
-// carry = (carry, unless a sequence started in the piece) 2^(a2 sum of delta) + the piece's own, over
+// carry = (carry, unless the piece is closed to it) 2^(a2 sum of delta) + the piece's own, over
 // `count` pieces from `k` on (kDir: +1 or -1), each result written over the own one.  Eight pieces' values
 // are loaded before the first is used: the chain is one multiply-add per piece, not one latency.
 template <int kDir>
-__device__ __forceinline__ void join(const Params& p, const uint32_t* started, int k, int count, float a2, float carry,
+__device__ __forceinline__ void join(const Params& p, const uint32_t* closed, int k, int count, float a2, float carry,
                                      float* slot, const float* sum, int64_t row) {
     constexpr int U = 8;
     for (int c = 0; c < count; c += U) {
@@ -120,7 +122,7 @@ __device__ __forceinline__ void join(const Params& p, const uint32_t* started, i
         for (int j = 0; j < U; ++j) {
             if (c + j >= count) break;
             const int64_t q = k + (int64_t)kDir * (c + j);
-            carry = started[q / 32] >> (q & 31) & 1 ? o[j] : fmaf(exp2_hw(a2 * f[j]), carry, o[j]);
+            carry = closed[q / 32] >> (q & 31) & 1 ? o[j] : fmaf(exp2_hw(a2 * f[j]), carry, o[j]);
             slot[q * row] = carry;
         }
     }

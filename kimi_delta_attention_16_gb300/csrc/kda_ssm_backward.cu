@@ -195,14 +195,14 @@ __global__ void __launch_bounds__(Lay<NS, 1>::NT, 8) k_rev(BParams b) {
 // Slot k: from what piece k sends to its left by itself to all that it sends (what piece k - 1 starts from).
 template <int NS> __global__ void __launch_bounds__(kJoinThreads) k_rev_join(BParams b) {
     const Params& p = b.f;
-    __shared__ uint32_t started[kJoinBits / 32];
-    mark_started(p, started);
+    __shared__ uint32_t closed[kJoinBits / 32];
+    mark_closed<-1>(p, closed);
     const int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x, row = (int64_t)p.C * NS;
     if (i >= row) return;
     const float a2 = p.A[i] * kLog2e;
     float* slot = b.rev + i;
     const float* sum = b.rsum + i / NS;
-    join<-1>(p, started, p.pieces - 2, p.pieces - 2, a2, slot[(p.pieces - 1) * row], slot, sum, row);
+    join<-1>(p, closed, p.pieces - 2, p.pieces - 2, a2, slot[(p.pieces - 1) * row], slot, sum, row);
 }
 
 // ------------------------------------------------------------------ the main kernel

@@ -297,13 +297,13 @@ __global__ void __launch_bounds__(ScanLay<NS, kMode>::NT, kMode == kOut ? 6 : 8)
 // The state at each piece's start, in the slots where the pieces left their own: slot k + 1 holds what
 // piece k leaves by itself, and then what piece k + 1 starts from.
 template <int NS> __global__ void __launch_bounds__(kJoinThreads) k_scan_join(Params p) {
-    __shared__ uint32_t started[kJoinBits / 32];
-    mark_started(p, started);
+    __shared__ uint32_t closed[kJoinBits / 32];
+    mark_closed<1>(p, closed);
     const int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x, row = (int64_t)p.C * NS;
     if (i >= row) return;
     const float a2 = p.A[i] * kLog2e;
     float* slot = p.ws_state + row + i;  // of piece 0
-    join<1>(p, started, 1, p.pieces - 2, a2, *slot, slot, p.ws_sum + i / NS, row);
+    join<1>(p, closed, 1, p.pieces - 2, a2, *slot, slot, p.ws_sum + i / NS, row);
 }
 
 // One token per sequence: a thread holds 4 states of one channel and takes several sequences in turn,
