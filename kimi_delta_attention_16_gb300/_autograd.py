@@ -1,11 +1,18 @@
 """What the differentiable operations share: the choice of how inputs are kept for the backward pass,
-and the check that a call inside a stream capture can be differentiated there."""
+and the checks that a step inside a stream capture can be differentiated there.
+
+A leaf tensor has one gradient accumulator for all graphs that are alive, and it belongs to the stream on which the
+first of them was built.  A captured backward pass makes that stream wait for the capture.  Another stream of the
+program joins the capture by that; the default stream must not, and the attempt ends the process.  So each call marks its
+leaves' accumulators with its stream, and a capture that meets the default stream's mark raises: an eager graph of that
+leaf, or whatever else holds its accumulator (hooks, a data-parallel wrapper), is still alive."""
 from __future__ import annotations
 
 import torch
 
 SAVED = ("io", "e4m3")  # how a layer keeps its large inputs for its backward pass
 _STREAM = "kda_stream"
+_DEFAULT = 0  # the handle of the default stream
 
 
 def check_saved(saved: str) -> None:
@@ -13,14 +20,16 @@ def check_saved(saved: str) -> None:
         raise ValueError(f"saved must be one of {SAVED}, got {saved!r}")
 
 
-def apply(function, where: str, *args):
-    """function.apply(*args), refusing a capture that could not be differentiated.
+def _raise(where: str) -> None:
+    raise RuntimeError(f"{where} is being captured while a gradient accumulator of one of its leaves, made on the default "
+                       "stream, is alive: before the capture drop the eager graphs of that leaf (their outputs and losses) "
+                       "and what holds accumulators (hooks, wrappers), or build them on another stream")
 
-    A leaf tensor has one gradient accumulator for all graphs that are alive, and it belongs to the stream on
-    which the first of them was built.  A backward pass captured on another stream would wait on that one, which
-    the capture forbids and which ends the process.  So each call marks its leaves' accumulators with its stream,
-    and a call that is being captured raises when it meets another stream's mark: an eager graph of that leaf is
-    still alive."""
+
+def apply(function, where: str, *args, early: bool = True):
+    """function.apply(*args), with its leaves' accumulators marked.  early: inside a capture, refuses what its backward
+    pass could not do in the same capture before anything is recorded (a forward pass that is captured alone runs
+    under torch.no_grad())."""
     leaves = [a for a in args if isinstance(a, torch.Tensor) and a.requires_grad and a.is_leaf and a.is_cuda]
     if not leaves or not torch.is_grad_enabled():
         return function.apply(*args)
@@ -30,8 +39,15 @@ def apply(function, where: str, *args):
     nodes = [torch.autograd.graph.get_gradient_edge(a).node for a in leaves]
     for node in nodes:
         mark = node.metadata.setdefault(_STREAM, stream)
-        if capturing and mark != stream:
-            raise RuntimeError(f"{where} is being captured while a graph of one of its leaves, built on another stream, "
-                               "is alive: drop that graph (its outputs and losses) before the capture, or capture the "
-                               "forward and backward calls that this layer is made of")
+        if early and capturing and mark == _DEFAULT:
+            _raise(where)
     return function.apply(*args)
+
+
+def check_backward(ctx, where: str) -> None:
+    """Inside a function's backward: raises where the pass is being captured and would go on to an accumulator of the
+    default stream."""
+    if torch.cuda.is_current_stream_capturing():
+        for node, _ in ctx.next_functions:
+            if node is not None and node.metadata.get(_STREAM) == _DEFAULT:
+                _raise(where)

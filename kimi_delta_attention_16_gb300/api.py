@@ -455,6 +455,7 @@ class _KDALayer(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dout, dfin):
+        _autograd.check_backward(ctx, "kda_layer")
         *kept, conv_w, g, beta, rms_w, initial_state, conv_state_in = ctx.saved_tensors
         q, k, v, gate = (t if sc is None else _unpack_heads(t, sc, ctx.dtype, g.shape)
                          for t, sc in zip(kept[::2], kept[1::2]))
@@ -499,9 +500,11 @@ def kda_layer(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, conv_w: torch.T
     gradients are those of the exact layer in fp32, cast to each input's dtype.
 
     saved="e4m3" keeps q, k, v and gate in 8 bits for the backward pass (kda_pack8: a little over half of bf16's
-    memory): the gradients are then those at the rounded values.  g, beta and the states stay as they are.  In a
-    captured graph, see kda_ssm_layer's note."""
+    memory): the gradients are then those at the rounded values.  g, beta and the states stay as they are.
+
+    In a captured graph: pass cu_seqlens as a prepared (device, host) pair.  A captured backward pass raises while an
+    eager graph of the same leaves, built on the default stream, is alive."""
     _autograd.check_saved(saved)
     cu_pair = _cu_pair(cu_seqlens, q.device)
     return _autograd.apply(_KDALayer, "kda_layer", q, k, v, conv_w, g, beta, gate, rms_w, initial_state, conv_state_in,
-                           cu_pair, float(eps_l2), float(eps_rms), float(scale), saved)
+                           cu_pair, float(eps_l2), float(eps_rms), float(scale), saved, early=False)

@@ -593,8 +593,9 @@ def kda_ssm_layer(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.T
     dt_bias and initial_state.  saved="e4m3" keeps u and z in 8 bits for the backward pass; dt, B and C stay as they
     are (a step size enters the decays' exponents, and B and C are small).
 
-    In a captured graph: pass cu_seqlens as a prepared (device, host) pair, and let no eager graph of the same leaves
-    live; the call raises if one that it knows of does."""
+    In a captured graph: pass cu_seqlens as a prepared (device, host) pair, and let no eager graph of the same leaves,
+    built on the default stream, live; the call raises if one that it knows of does (a forward pass that is captured
+    alone runs under torch.no_grad())."""
     _autograd.check_saved(saved)
     return _autograd.apply(_SsmLayer, "kda_ssm_layer", u, dt, A, B, C, D, z, dt_bias, initial_state,
                            _cu_pair(cu_seqlens, u.device), bool(softplus), saved)
