@@ -184,9 +184,11 @@ RowShape row_shape(int64_t n) {  // for n accesses per row, at most kRowAccesses
     else if (h.nt == 128) { X(1, 128); }                 \
     else if (h.nt == 256) { X(1, 256); }                 \
     else { X(1, kRowThreads); }
-__device__ __forceinline__ float rstd_of(float v) {  // 1 / sqrt(v): the hardware's value and one Newton step
-    const float r = rsqrtf(v);
-    return r * fmaf(-0.5f * v * r, r, 1.5f);
+// 1 / sqrt(v): the hardware's value r and one Newton step r (1.5 - v r r / 2).  Where v r r is no number (v = 0, or a
+// variance that overflowed: r is infinite or 0) r is the result already, the one that 1 / sqrtf(v) has too.
+__device__ __forceinline__ float rstd_of(float v) {
+    const float r = rsqrtf(v), n = fmaf(-0.5f * (v * r), r, 1.5f);  // v r first: v may be below the normal numbers
+    return n == n ? r * n : r;
 }
 
 template <typename T, int W, int VPT, int R, int NT>
