@@ -477,22 +477,23 @@ k_layer_norm_bwd_rows(const T* __restrict__ dy, uint32_t dys, const void* __rest
     int buf = 0;
     for (int r0 = blockIdx.x; r0 < M; r0 += step) {
         cp_wait<kDepth - 2>();
-        float rs[R], sh[R];  // 1 / deviation and -mean / deviation
+        float rs[R], mean[R];
         uint32_t sc[R][VPT];
         float s[4] = {0.f, 0.f, 0.f, 0.f};
-        // xh and dy of one access, from the ring: read once for the sums and once for dx, since registers for
-        // them would halve the blocks.
-        auto terms = [&](int k, int i, f2 (&xh)[P], f2 (&d)[P]) {
-            unraw2(ring_x[get + (k * VPT + i) * NT], xh);
+        // x - mean and dy of one access, from the ring: read once for the sums and once for dx, since registers for
+        // them would halve the blocks.  The mean is subtracted from x itself (x rstd - mean rstd in one multiply-add
+        // would round at the size of mean / deviation), and rstd comes to the sums and factors where that is free.
+        auto terms = [&](int k, int i, f2 (&xm)[P], f2 (&d)[P]) {
+            unraw2(ring_x[get + (k * VPT + i) * NT], xm);
             unraw2(ring_y[get + (k * VPT + i) * NT], d);
-            const f2 m = f2_dup(X8 ? scale_of_byte(sc[k][i]) * rs[k] : rs[k]), shift = f2_dup(sh[k]);
+            const f2 m = f2_dup(-mean[k]), scale = f2_dup(scale_of_byte(sc[k][i]));
 #pragma unroll
-            for (int j = 0; j < P; ++j) xh[j] = fma2(xh[j], m, shift);
+            for (int j = 0; j < P; ++j) xm[j] = X8 ? fma2(xm[j], scale, m) : add2(xm[j], m);
         };
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             rs[k] = st[k].y;
-            sh[k] = -st[k].x * st[k].y;
+            mean[k] = st[k].x;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) sc[k][i] = sr[k][i];
             if (R > 1 && r0 + k * row_step >= M) continue;  // its slot holds no row
@@ -500,15 +501,16 @@ k_layer_norm_bwd_rows(const T* __restrict__ dy, uint32_t dys, const void* __rest
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 if (!in[i]) continue;
-                f2 xh[P], d[P];
-                terms(k, i, xh, d);
+                f2 xm[P], d[P];
+                terms(k, i, xm, d);
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
-                    dw[i][j] = fma2(d[j], xh[j], dw[i][j]);
+                    const f2 xh = mul2(xm[j], f2_dup(rs[k]));
+                    dw[i][j] = fma2(d[j], xh, dw[i][j]);
                     db[i][j] = add2(db[i][j], d[j]);
                     d[j] = mul2(d[j], wv[i][j]);
                     a = add2(a, d[j]);
-                    b = fma2(d[j], xh[j], b);
+                    b = fma2(d[j], xh, b);
                 }
             }
             s[2 * k] = f2_sum(a);
@@ -528,16 +530,16 @@ k_layer_norm_bwd_rows(const T* __restrict__ dy, uint32_t dys, const void* __rest
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             if (R > 1 && r0 + k * row_step >= M) break;
-            const f2 m0 = f2_dup(-s[2 * k] * inv_c * rs[k]), m1 = f2_dup(-s[2 * k + 1] * inv_c * rs[k]), rr = f2_dup(rs[k]);
+            const f2 m0 = f2_dup(-s[2 * k] * inv_c), m1 = f2_dup(-s[2 * k + 1] * inv_c * rs[k]), rr = f2_dup(rs[k]);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 if (!in[i]) continue;
-                f2 xh[P], d[P];
-                terms(k, i, xh, d);
+                f2 xm[P], d[P];
+                terms(k, i, xm, d);
                 float o[W];
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
-                    const f2 v = fma2(rr, mul2(d[j], wv[i][j]), fma2(xh[j], m1, m0));
+                    const f2 v = mul2(rr, fma2(xm[j], m1, fma2(d[j], wv[i][j], m0)));
                     o[2 * j] = f2_lo(v);
                     o[2 * j + 1] = f2_hi(v);
                 }
