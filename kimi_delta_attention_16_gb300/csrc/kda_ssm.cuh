@@ -7,14 +7,25 @@
 namespace kda {
 namespace ssm {
 
-// softplus(x) = max(x, 0) + log(1 + e^-|x|), to a few units of the last place (far below 0 the exponent's own
-// rounding, |x| 2^-24, comes on top, where e^x is all that is left): the
+// The larger of two values, NaN where one is NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+constexpr float kLn2 = 0.6931471805599453f;
+
+// softplus(x) = max(x, 0) + log(1 + e^-|x|), to a dozen units of 2^-24 (four of them the hardware exponential's).
+// e^-|x| = 2^h (1 + r) with h = -|x| log2 e as rounded and r = -|x| - h ln 2 what that left out (one multiply-add: the
+// product is exact); without r the exponent's rounding would cost |x| units more, 10 where trained step sizes lie.
+// From -104 on e^-|x| is 0 in fp32; the bound keeps h finite.  The
 // logarithm as 2 atanh(s) = s P(s^2), s = e / (2 + e) <= 1/3, with a polynomial of degree 4 fitted to the quotient
 // 2 atanh(s) / s over s^2 in [0, 1/9] (relative error 2^-26; its power series would take degree 6).
 // log(1 + e) directly would lose the digits of a small e.  Both halves of a pair at once.
 __device__ __forceinline__ f2 softplus2(f2 x) {
-    const f2 t = mul2(f2_of(fabsf(f2_lo(x)), fabsf(f2_hi(x))), f2_dup(-kLog2e));
-    const f2 e = f2_of(exp2_hw(f2_lo(t)), exp2_hw(f2_hi(t)));
+    const f2 t = f2_of(max_nan(-fabsf(f2_lo(x)), -104.f), max_nan(-fabsf(f2_hi(x)), -104.f));
+    const f2 h = mul2(t, f2_dup(kLog2e)), r = fma2(h, f2_dup(-kLn2), t);
+    const f2 e0 = f2_of(exp2_hw(f2_lo(h)), exp2_hw(f2_hi(h))), e = fma2(e0, r, e0);
     const f2 d = add2(e, f2_dup(2.f));
     const f2 s = mul2(e, f2_of(rcp_hw(f2_lo(d)), rcp_hw(f2_hi(d)))), q = mul2(s, s);
     f2 p = f2_dup(0.2817833423614502f);

@@ -45,8 +45,6 @@ struct BParams {
     bool wide;  // two channels per access to du, ddt and dz
 };
 
-constexpr float kLn2 = 0.6931471805599453f;
-
 // ------------------------------------------------------------------ what enters a piece from the right
 // Pieces 1 .. pieces - 1, each from zero at its right end (or from d_final_state where a sequence
 // ends; what lies behind the first end is passed over): q in front of its first token, and its sum of delta.  Layout and copies as in the forward scan.
