@@ -261,8 +261,8 @@ cudaError_t launch_ssm_backward(const kda_ssm_backward_args& a, const SsmBackwar
 
 cudaError_t launch_layer_norm(const kda_norm_args& a, cudaStream_t s);
 
-// How many row blocks kda_layer_norm_backward runs for M rows of C channels (each leaves one
-// partial sum of the weight's and the bias's gradient in the workspace), and its threads per block.
+// How many row blocks kda_layer_norm_backward runs for M rows of C channels: each leaves one
+// partial sum of the weight's and the bias's gradient in the workspace.
 struct NormBackwardPlan {
     int blocks;
     size_t workspace;  // bytes

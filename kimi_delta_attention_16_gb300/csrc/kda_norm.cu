@@ -153,7 +153,6 @@ template <int NT> __device__ __forceinline__ void block_sum4(float (&v)[4], floa
 }
 __device__ __forceinline__ float f2_sum(f2 v) { return f2_lo(v) + f2_hi(v); }
 
-// Threads that a block of the row kernels may have: what leaves a thread the registers it needs.
 // Shapes of the row kernels: accesses per thread and threads, fixed so that every offset in the ring is a
 // constant.  448 threads of 72 registers leave two blocks to an SM (7,168 bf16 channels: 2 x 448 accesses); up
 // to 1,792 accesses take four per thread.  Wider rows go through the kernels above, one at a time.
@@ -633,7 +632,7 @@ cudaError_t launch_layer_norm(const kda_norm_args& a, cudaStream_t s) {
         case 2: KDA_LN(T, W, 2); break;                                                                       \
         case 4: KDA_LN(T, W, 4); break;                                                                       \
         case 8: KDA_LN(T, W, 8); break;                                                                       \
-        default: KDA_LN(T, W, (W == 1 ? 32 : 16)); break;                                                     \
+        default: KDA_LN(T, W, (W == 1 ? 32 : W == 4 ? 16 : 8)); break; /* bf16 vectors never need more than 8 */ \
     }
     if (a.io == KDA_BF16) {
         if (vec) { KDA_LN_V(bf16, 8) } else { KDA_LN_V(bf16, 1) }
@@ -726,8 +725,8 @@ cudaError_t launch_layer_norm_backward(const kda_norm_backward_args& a, const No
         case 1: KDA_LNB(T, X8, W, 1); break;                                                                   \
         case 2: KDA_LNB(T, X8, W, 2); break;                                                                   \
         case 4: KDA_LNB(T, X8, W, 4); break;                                                                   \
-        case 8: KDA_LNB(T, X8, W, 8); break;                                                                   \
-        default: KDA_LNB(T, X8, W, (W == 1 ? 32 : 8)); break; /* vectors never need more than 8 */                                                  \
+        case 8: KDA_LNB(T, X8, W, (W == 8 ? 4 : 8)); break;                                                    \
+        default: KDA_LNB(T, X8, W, (W == 1 ? 32 : W == 4 ? 8 : 4)); break; /* vectors: never more than these */ \
     }
 #define KDA_LNB_X(T, W)                                                                                        \
     if (a.x_scales) { KDA_LNB_V(T, true, W) } else { KDA_LNB_V(T, false, W) }

@@ -36,13 +36,6 @@ __device__ __forceinline__ f2 softplus2(f2 x) {
     return fma2(s, p, f2_of(fmaxf(f2_lo(x), 0.f), fmaxf(f2_hi(x), 0.f)));
 }
 __device__ __forceinline__ float softplus(float x) { return f2_lo(softplus2(f2_of(x, 0.f))); }
-template <typename T> __device__ __forceinline__ float ldf(const T* p) {
-    Raw<T, 1> r;
-    r.load(p);
-    float v[1];
-    unraw(r, v);
-    return v[0];
-}
 
 // One call's arguments as the kernels take them (strides in elements, never 0).
 struct Params {
