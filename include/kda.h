@@ -401,7 +401,9 @@ kda_status kda_backward(const kda_backward_args* args, kda_stream_t stream);
 /* ------------------------------------------------------------------------
  * kda_layer_norm -- y = (x - mean) / sqrt(var + eps) * weight + bias over the
  * last axis of x, var the mean of the squared deviations (two passes over the
- * registers, so a row whose mean is large loses nothing).
+ * registers, so a row whose mean is large loses nothing).  fp32 throughout: a
+ * variance beyond its range makes rstd 0 and y the bias.  How a row is summed
+ * depends on M (many rows share a block's work), so its last bits may too.
  *
  *   x, y    [M][row stride] io; y must not overlap x.
  *   weight, bias  [C] fp32, or NULL (ones, zeros).
@@ -428,6 +430,7 @@ kda_status kda_layer_norm(const kda_norm_args* args, kda_stream_t stream);
 /* ------------------------------------------------------------------------
  * kda_layer_norm_backward -- with xh = (x - mean) rstd and p = dy weight:
  *   dx = rstd (p - mean(p) - xh mean(p xh)),  dweight = sum_rows dy xh,  dbias = sum_rows dy.
+ * The mean is subtracted from x first, so that a large one costs no digits here either.
  *
  *   x        the forward's input (io), or its 8-bit form (x_scales non-NULL: x is
  *            then [M][C] codes and x_scales [M][ceil(C/32)], both dense, as
@@ -631,7 +634,9 @@ kda_status kda_ssm_step(const kda_ssm_args* args, kda_stream_t stream);
  * recomputed).  du, ddt, dz, dB and dC are io, dense ([T_total][C], [T_total][G][Nst]), rounded
  * once; dA [C][Nst], dD [C], ddt_bias [C] and dinitial_state [N][C][Nst] are fp32.  dz, dD,
  * ddt_bias and dinitial_state may be NULL (not wanted); the others must not.  G is at most 65535.  Sums over channels
- * and tokens go through the workspace in a fixed order.
+ * and tokens go through the workspace in a fixed order.  The workspace grows with the tokens: it holds the fp32 states
+ * in front of every fourth one, T_total * C * Nst bytes, and the parts of dB and dC (13 GB and more for 65,536 tokens x
+ * 12,288 channels x 16 states), for this call alone.
  * ------------------------------------------------------------------------ */
 typedef struct {
     kda_ssm_args fwd;

@@ -95,8 +95,11 @@ template <int W> __device__ __forceinline__ void load_param(const float* p, floa
 }
 
 // ------------------------------------------------------------------ activations
-// Sigmoid and SiLU from the hardware's exponential and reciprocal (each within two units of the last
-// place, without the range checks of the library forms: e^-x overflows to a sigmoid of 0, as it should).
+// Sigmoid and SiLU from the hardware's exponential and reciprocal, without the range checks of the library
+// forms: e^-x overflows to a sigmoid of 0, as it should.  In units of 2^-24, relative: the exponential 4, the
+// reciprocal 2, and for negative x the rounding of the exponent x log2 e, |x| units (10 at -10, where SiLU has
+// 5e-5 of x left).  The convolution and the gates take it so: bf16 rows round by 2^16 units, fp32 rows carry
+// these, and correcting the exponent would cost a guard against infinities in every token.
 __device__ __forceinline__ float rcp_hw(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

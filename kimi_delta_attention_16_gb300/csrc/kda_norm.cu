@@ -14,8 +14,12 @@
 // partial per block, which k_column_sum adds up in block order (no atomics: the same bits
 // every time).
 //
-// Measured, 8,192 x 7,168 bf16: forward 40 us (5.8 TB/s), backward 69 us (5.1 TB/s; 74 from 8-bit x) and 6 us
-// for the column sums.  The backward is bound by instruction issue (two rows' sums, dw and db per element).
+// Measured, 8,192 x 7,168 bf16: forward 40 us (5.8 TB/s), backward 70 us (5.0 TB/s; 75 from 8-bit x) and 6 us
+// for the column sums.  The backward is bound by latency: 40 % of an SM's warps, one barrier and one chain of
+// shuffles per row with one row in hand; its warps wait for memory and shared memory first, and 54 % of the issue
+// slots are taken.  Rows wider than the ring kernels' (bf16 above 14,336 channels, fp32 above 7,168) keep dw and db of
+// up to 32 channels per thread beside the row in 64 registers and spill, up to 2,000 bytes: 8,192 x 16,384 bf16 256 us
+// (floor 119), fp32 986 (238).
 #include "kda_block.cuh"
 
 namespace kda {

@@ -18,10 +18,10 @@
 // and the rest goes through shared memory.  Sums over the blocks' channels and over the pieces go
 // through the workspace and are added in a fixed order.
 //
-// Measured, 4,096 x 4,096 x 16 bf16 with the gate: 600 us = pieces' own states 54, checkpoints 72,
-// k_rev 65, the main kernel 321, joins and sums 35, launch gaps.  The main kernel issues an instruction in 44 %
-// of the cycles: two blocks of 255-register threads per SM leave two warps per scheduler, whose dependent
-// instructions wait for one another.  Three blocks (168 registers) spill: 640 us; 2 channels x 4 states
+// Measured, 4,096 x 4,096 x 16 bf16 with the gate: 543 us = pieces' own states 55, checkpoints 72,
+// k_rev 69, the main kernel 320, joins and sums 27.  The main kernel issues an instruction in 40 %
+// of the cycles: two blocks of 255-register threads per SM (112 bytes spilled with 16 states, 44 with 8, 16 with 32)
+// leave two warps per scheduler, whose dependent instructions wait for one another.  Three blocks (168 registers) spill: 640 us; 2 channels x 4 states
 // per thread (four blocks of 128 registers) 356, its cross-thread sums cost what the warps gain.
 // In a copy without them: the border path 18 us, dB and dC across threads 42, the elementwise end
 // of a tile 68, the copies 60.

@@ -14,14 +14,20 @@
 // pieces.  kPiece runs every piece from a zero state, k_scan_join carries the states through (a piece's
 // effect on what enters it is 2^(A log2 e sum of delta)), kOut runs the pieces again from the right states.
 //
-// Measured, 8,192 x 12,288 x 16 bf16 with the gate: 685 us = 401 (kOut, 2.0 TB/s) + 275 (kPiece) + 9.
-// Bound by instruction issue and the register file: taken out one at a time in a copy, the exponentials
-// are worth 35 us, reading B and C 56, softplus 50, the gate 40, the copies 67, the stores 0.
+// A decay 2^(delta A log2 e) carries the hardware exponential's 4 units of 2^-24 and 2 |delta A| of its exponent's
+// roundings; correcting the exponent as the step size's (softplus2) would put two more instructions on every pair of
+// states, in a loop that is nothing else.
+//
+// Measured, 8,192 x 12,288 x 16 bf16 with the gate: 695 us = 406 (kOut, 2.0 TB/s) + 280 (kPiece) + 9.
+// Bound by latency at low occupancy: 17 to 20 % of an SM's warps (168 and 128 registers), which issue in 58 to 63 %
+// of the cycles and wait for their own paired instructions (two or three cycles each) first; the exponential unit is
+// 49 to 62 % busy.  Taken out one at a time in a copy of 488 us, the exponentials were worth 35 us, reading B
+// and C 56, softplus 50, the gate 40, the copies 67, the stores 0.
 //
 // Sequences are walked, not mapped: a piece of the packed stream starts in the middle of whatever
 // sequence holds its first token, and at a border the state is stored and the next one's loaded.
 // kPiece begins at the last sequence that starts in its piece: nothing before it leaves the piece (8,192 tokens in
-// sequences of 512: 275 -> 199 us, of 128: 70).
+// sequences of 512: 275 -> 199 us, of 128: 70, when the step was made).
 #include "kda_ssm.cuh"
 
 namespace kda {
@@ -309,7 +315,7 @@ template <int NS> __global__ void __launch_bounds__(kJoinThreads) k_scan_join(Pa
 // One token per sequence: a thread holds 4 states of one channel and takes several sequences in turn,
 // kRows states in flight at once.  Bound by HBM: the state read and written.  kVec: a thread's four
 // elements of B and C come in one access.
-// 256 sequences x 12,288 channels x 16, bf16: 76 us (5.6 TB/s).
+// 256 sequences x 12,288 channels x 16, bf16: 76 us (5.6 TB/s); fp32 95 us (4.8 TB/s, 28 bytes spilled per thread).
 constexpr int kStepThreads = 256;
 constexpr int kRows = 4;
 template <typename T, int NS, bool kVec> __global__ void __launch_bounds__(kStepThreads, 3) k_step(Params p, int rows) {
@@ -467,7 +473,8 @@ ScanPlan scan_plan(const kda_ssm_args& a) {
     const int64_t tt = 8, cb = a.Nst <= 16 ? 128 : 2048 / a.Nst;  // ScanLay<Nst, kOut>'s tile and channels per block
     ScanPlan p{};
     const int64_t blocks = a.G * ((a.C / a.G + cb - 1) / cb);
-    // Two whole rounds of blocks, of which six run on an SM; pieces of at least 8 tiles.  (One piece of 8,192
+    // Two whole rounds of blocks, of which six run on an SM (five in fp32 with 8 or 16 states, whose rings take 39 to
+    // 42 KB: 2.4 rounds there); pieces of at least 8 tiles.  (One piece of 8,192
     // tokens x 12,288 channels leaves most warp slots empty: 1.5 ms, against 0.69 ms in 19 pieces, the pass over
     // their own states included; one round: 0.76 ms, three: 0.71, four: 0.69.)
     int64_t k = 12 * sms / blocks;
