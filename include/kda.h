@@ -659,6 +659,148 @@ typedef struct {
 kda_status kda_ssm_backward_workspace_size(const kda_ssm_backward_args* args, size_t* bytes);
 kda_status kda_ssm_backward(const kda_ssm_backward_args* args, kda_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * A decode step over few tokens -- weights stored in 4 bits, a
+ * mixture-of-experts layer, and the verification of drafted tokens.  Page
+ * "Kimi K3 / Architecture": the weights are kept in 4 bits with a power of two
+ * per 32 of them, and a mixture of experts with a sigmoid top-k router follows
+ * every attention layer; a drafter proposes tokens that kda_prefill's
+ * multi-token decode runs through the layer.
+ *
+ * A weight w[row][k] is stored along k (K, the product's axis):
+ *   KDA_WEIGHT_E2M1  codes of sign, two bits of exponent, one of mantissa (0, 0.5, 1,
+ *                    1.5, 2, 3, 4, 6), 32 under one power of two: scale bytes hold its
+ *                    exponent + 127 as kda_pack8's do, 1 to 254
+ *   KDA_WEIGHT_INT4  w = (code - 8) * scale, group (32, 64 or 128) weights per scale,
+ *                    scales bf16 or fp32
+ *   KDA_WEIGHT_BF16  (kda_moe only) bf16 weights, no scales
+ * Two codes per byte, the even k in the low half: codes [rows][K/2], scales
+ * [rows][K/group], both dense; codes 16-byte aligned; K a multiple of the group.
+ * ------------------------------------------------------------------------ */
+typedef enum { KDA_WEIGHT_BF16 = 0, KDA_WEIGHT_E2M1 = 1, KDA_WEIGHT_INT4 = 2 } kda_weight_format;
+
+/* kda_pack4 -- weights into codes and scales.  e2m1: 2^e is the smallest power of two
+ * (e >= -126) with max|w| <= 6 * 2^e over the group, codes round to nearest, ties to even.
+ * int4: scale = max|w| / 7 rounded to scale_dtype, code = w / scale rounded + 8 (8 for a
+ * group of zeros).  Weights must be finite: others come back as some finite value.
+ * kda_unpack4 -- and back: w is written, codes and scales are read. */
+typedef struct {
+    int64_t rows;
+    int K;
+    void* w;               /* [rows][w_stride]; read by kda_pack4, written by kda_unpack4 */
+    int64_t w_stride;      /* 0 means K */
+    kda_dtype w_dtype;
+    int format;            /* kda_weight_format, not KDA_WEIGHT_BF16 */
+    int group;             /* 32; 32, 64 or 128 for int4 */
+    kda_dtype scale_dtype; /* int4 only */
+    uint8_t* codes;
+    void* scales;
+} kda_pack4_args;
+
+kda_status kda_pack4(const kda_pack4_args* args, kda_stream_t stream);
+kda_status kda_unpack4(const kda_pack4_args* args, kda_stream_t stream);
+
+/* kda_gemm4 -- kda_gemm for weights in 4 bits: C[M][N] = epilogue(A[M][K] . W[N][K]^T), for
+ * the few rows of a decode step (any M is taken; the weights are read once per 64 rows).
+ * A [M][lda] bf16 (any alignment of its elements; 16-byte rows are read faster), C [M][ldc] bf16
+ * or fp32, rounded once; products are exact in fp32 groups, sums fp32, in a fixed order.  M, N >= 0; C must not
+ * overlap an input.  Epilogues as in kda_gemm. */
+typedef struct {
+    int M, N, K;
+    const void* A;
+    int64_t lda;
+    int format;
+    int group;
+    kda_dtype scale_dtype;
+    const uint8_t* codes;
+    const void* scales;
+    void* C;
+    int64_t ldc;
+    kda_dtype c_dtype;
+    int epilogue;
+} kda_gemm4_args;
+
+kda_status kda_gemm4(const kda_gemm4_args* args, kda_stream_t stream);
+
+/* kda_moe -- a mixture-of-experts layer for few tokens.
+ *   logit[t][e] = x_t . router_e, summed to about 48 bits
+ *   score = sigmoid(logit): the `top` experts with the largest score + bias are chosen, weighted by score
+ *   score = softmax(logit): the `top` largest logits are chosen (bias must be NULL)
+ *   weight = scale * score / (sum of the chosen scores); a tie goes to the lower expert, NaN ranks last
+ *   y_t = sum over the chosen, in the order of their rank, of weight * W_out (silu(g) u),
+ *   g, u = the first and second F rows of W_in x_t
+ *   x [M][x_stride] bf16; router [E][D] bf16 or fp32, dense; bias [E] fp32 or NULL
+ *   w_in [E][2F][D], w_out [E][D][F] in one format (scales NULL for bf16); D and F multiples of the group,
+ *   of 8 for bf16
+ *   y [M][y_stride] bf16 or fp32; ids [M][top] int32 and weights [M][top] fp32, best first, or NULL
+ * The values between the two products stay in fp32 (22 bits or more in the second one).  E up to 1024, top up to 32 and
+ * to E, M * top up to 65535. */
+typedef enum { KDA_SCORE_SIGMOID = 0, KDA_SCORE_SOFTMAX = 1 } kda_moe_score;
+
+typedef struct {
+    int M, E, top, D, F;
+    const void* x;
+    int64_t x_stride;      /* 0 means D */
+    const void* router;
+    kda_dtype router_dtype;
+    const float* bias;
+    int score;             /* kda_moe_score */
+    float scale;
+    int format;
+    int group;
+    kda_dtype scale_dtype;
+    const void* w_in;
+    const void* w_in_scales;
+    const void* w_out;
+    const void* w_out_scales;
+    void* y;
+    int64_t y_stride;      /* 0 means D */
+    kda_dtype y_dtype;
+    int* ids;
+    float* weights;
+    void* workspace;       /* kda_moe_workspace_size bytes, 256-byte aligned; for this call alone */
+    size_t workspace_bytes;
+} kda_moe_args;
+
+kda_status kda_moe_workspace_size(const kda_moe_args* args, size_t* bytes);
+kda_status kda_moe(const kda_moe_args* args, kda_stream_t stream);
+
+/* kda_verify -- which drafted tokens stand.  Rows are packed as kda_prefill's multi-token decode ran
+ * them: a sequence of L + 1 rows (its last token and L drafts) has the target's distribution after each.
+ *   target  [T_total][target_stride] bf16 or fp32 probabilities over V tokens (they need not sum to 1;
+ *           values that are not above 0 count as 0)
+ *   draft   [T_total][draft_stride], same dtype: row i is what draft i was drawn from; the last row of a
+ *           sequence is not read.  NULL: a drafter that proposes its best token only (probability 1)
+ *   tokens  [T_total] int32 or int64: row i holds draft i; the last row of a sequence is not read
+ *   u       [T_total] fp32 in [0, 1)
+ * Draft i (token d) is taken while u_i draft_i(d) < target_i(d); a token outside [0, V) is never taken.
+ * After the first one that is not (row a), or after all, one token is drawn with the last row's u: the
+ * lowest index whose running sum exceeds u times the sum, of max(target_a - draft_a, 0) after a refusal
+ * (of target_a where that is 0 everywhere), of the last row's target otherwise; -1 where nothing is above 0.
+ *   out      [T_total] of tokens' type: the accepted drafts, the drawn token, then -1
+ *   accepted [N] int32: drafts taken (0 for a sequence without rows)
+ * Comparisons are exact in fp64 and sums carry about 48 bits.  V up to 4,000,000. */
+typedef struct {
+    int N;
+    int64_t T_total;
+    int V;
+    kda_dtype dtype;
+    const void* target;
+    int64_t target_stride; /* 0 means V */
+    const void* draft;
+    int64_t draft_stride;  /* 0 means V */
+    const void* tokens;
+    int token_bytes;       /* 4 or 8 */
+    const float* u;
+    const int32_t* cu_seqlens;
+    const int32_t* cu_seqlens_host;  /* NULL: checked on the device, findings go to d_status */
+    void* out;
+    int32_t* accepted;
+    int* d_status;
+} kda_verify_args;
+
+kda_status kda_verify(const kda_verify_args* args, kda_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,7 +27,9 @@ KDA_RECURRENT_MAX_LEN = 8
 KDA_MAX_SEGMENTS = 16
 KDA_PACK8_BLOCK = 32
 KDA_EPI_NONE, KDA_EPI_DECAY, KDA_EPI_SIGMOID = 0, 1, 2
-ABI_VERSION = 10500  # layer norm, 8-bit activations and the selective state space scan
+KDA_WEIGHT_BF16, KDA_WEIGHT_E2M1, KDA_WEIGHT_INT4 = 0, 1, 2
+KDA_SCORE_SIGMOID, KDA_SCORE_SOFTMAX = 0, 1
+ABI_VERSION = 10600  # 4-bit weights, the mixture of experts and the verification of drafts
 
 # Every symbol include/kda.h declares.
 EXPORTED = ("kda_status_string", "kda_last_error", "kda_version", "kda_short_conv",
@@ -36,7 +38,8 @@ EXPORTED = ("kda_status_string", "kda_last_error", "kda_version", "kda_short_con
             "kda_layer_norm", "kda_layer_norm_backward_workspace_size", "kda_layer_norm_backward",
             "kda_pack8", "kda_unpack8", "kda_ssm_conv", "kda_ssm_conv_step",
             "kda_ssm_conv_backward_workspace_size", "kda_ssm_conv_backward", "kda_ssm_scan_workspace_size",
-            "kda_ssm_scan", "kda_ssm_step", "kda_ssm_backward_workspace_size", "kda_ssm_backward")
+            "kda_ssm_scan", "kda_ssm_step", "kda_ssm_backward_workspace_size", "kda_ssm_backward",
+            "kda_pack4", "kda_unpack4", "kda_gemm4", "kda_moe_workspace_size", "kda_moe", "kda_verify")
 NOALLOC_SCRATCH_BYTES = 64 << 20  # KDA_NOALLOC_SCRATCH_BYTES in include/kda.h
 
 _vp = ctypes.c_void_p
@@ -154,6 +157,42 @@ class SsmBackwardArgs(ctypes.Structure):
     ]
 
 
+class Pack4Args(ctypes.Structure):
+    """Mirror of kda_pack4_args."""
+    _fields_ = [
+        ("rows", _i64), ("K", _int), ("w", _vp), ("w_stride", _i64), ("w_dtype", _int), ("format", _int), ("group", _int),
+        ("scale_dtype", _int), ("codes", _vp), ("scales", _vp),
+    ]
+
+
+class Gemm4Args(ctypes.Structure):
+    """Mirror of kda_gemm4_args."""
+    _fields_ = [
+        ("M", _int), ("N", _int), ("K", _int), ("A", _vp), ("lda", _i64), ("format", _int), ("group", _int),
+        ("scale_dtype", _int), ("codes", _vp), ("scales", _vp), ("C", _vp), ("ldc", _i64), ("c_dtype", _int), ("epilogue", _int),
+    ]
+
+
+class MoeArgs(ctypes.Structure):
+    """Mirror of kda_moe_args."""
+    _fields_ = [
+        ("M", _int), ("E", _int), ("top", _int), ("D", _int), ("F", _int), ("x", _vp), ("x_stride", _i64), ("router", _vp),
+        ("router_dtype", _int), ("bias", _vp), ("score", _int), ("scale", _f), ("format", _int), ("group", _int),
+        ("scale_dtype", _int), ("w_in", _vp), ("w_in_scales", _vp), ("w_out", _vp), ("w_out_scales", _vp), ("y", _vp),
+        ("y_stride", _i64), ("y_dtype", _int), ("ids", _vp), ("weights", _vp), ("workspace", _vp),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class VerifyArgs(ctypes.Structure):
+    """Mirror of kda_verify_args."""
+    _fields_ = [
+        ("N", _int), ("T_total", _i64), ("V", _int), ("dtype", _int), ("target", _vp), ("target_stride", _i64), ("draft", _vp),
+        ("draft_stride", _i64), ("tokens", _vp), ("token_bytes", _int), ("u", _vp), ("cu_seqlens", _vp),
+        ("cu_seqlens_host", _vp), ("out", _vp), ("accepted", _vp), ("d_status", _vp),
+    ]
+
+
 def lib_path() -> str:
     return _build.SO
 
@@ -212,10 +251,11 @@ def load(auto_build: bool = True) -> ctypes.CDLL:
         lib.kda_backward.argtypes = [ctypes.POINTER(BackwardArgs), _vp]
         # the operators around the layer take their structs as bytes or by reference
         for name in ("kda_layer_norm", "kda_layer_norm_backward", "kda_ssm_conv", "kda_ssm_conv_step",
-                     "kda_ssm_conv_backward", "kda_ssm_scan", "kda_ssm_step", "kda_ssm_backward"):
+                     "kda_ssm_conv_backward", "kda_ssm_scan", "kda_ssm_step", "kda_ssm_backward", "kda_pack4",
+                     "kda_unpack4", "kda_gemm4", "kda_moe", "kda_verify"):
             f = getattr(lib, name)
             f.restype, f.argtypes = _int, [_vp, _vp]
-        for name in ("kda_layer_norm_backward", "kda_ssm_conv_backward", "kda_ssm_scan", "kda_ssm_backward"):
+        for name in ("kda_layer_norm_backward", "kda_ssm_conv_backward", "kda_ssm_scan", "kda_ssm_backward", "kda_moe"):
             f = getattr(lib, name + "_workspace_size")
             f.restype, f.argtypes = _int, [_vp, _vp]
         lib.kda_pack8.restype = _int

@@ -1,0 +1,428 @@
+// kda_moe.cu -- a mixture-of-experts layer for few tokens: router, choice of experts, the experts'
+// products, their weighted sum.
+//
+//   logit[t][e] = x_t . router_e;  score = sigmoid(logit), or the softmax of the chosen logits
+//   choice: the `top` experts with the largest score + bias (logits for the softmax), ties to the lower expert
+//   w_tj = scale * score / (sum of the chosen scores)
+//   y_t = sum_j w_tj W_out[e_j] (silu(g) u),   (g, u) = the halves of W_in[e_j] x_t
+//
+// Bound by the bytes of the experts that some token chose; each is read once for all its tokens.  Five launches:
+// scores, choice with the lists of every expert's tokens, first products with their activation, second
+// products, sum over a token's experts in the order of their rank.
+#include "kda_few.cuh"
+#include "kda_serve.cuh"
+
+namespace kda {
+
+namespace {
+
+using namespace few;
+
+// ------------------------------------------------------------------ scores
+// The sum of a lane's products as two fp32 (value and what its rounding lost): a choice between two experts
+// hangs on the last digits of a sum over thousands of products, and fp64 runs at 1/64 of the fp32 rate here.
+struct Sum2 {
+    float hi, lo;
+    __device__ __forceinline__ void add(float v) {
+        const float s = hi + v, b = s - hi;
+        lo += (hi - (s - b)) + (v - b);
+        hi = s;
+    }
+};
+
+constexpr int kScoreThreads = 256, kScoreWarps = 8;
+
+__device__ __forceinline__ uint64_t ordered(double v) {  // a larger value is a larger integer; NaN is the smallest
+    if (isnan(v)) return 0;
+    const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
+    return b >> 63 ? ~b : b | (1ull << 63);
+}
+
+template <typename T> __device__ __forceinline__ void load8_any(const T* p, bool wide, float (&v)[8]) {
+    if (wide) {
+        load8(p, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = to_f(p[i]);
+    }
+}
+
+// A warp takes one expert and TB tokens, a block eight experts; the scores of a block are computed by one warp
+// at once (fp64 instructions cost by the warp).
+template <typename Tr, int TB>
+__global__ void __launch_bounds__(kScoreThreads) k_moe_scores(const bf16* __restrict__ x, int64_t xs, bool wide, const Tr* __restrict__ router,
+                                                              bool rwide, const float* __restrict__ bias, int M, int E, int D,
+                                                              int sigmoid, double* __restrict__ score, uint64_t* __restrict__ key) {
+    __shared__ double sums[kScoreWarps][TB];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int e0 = blockIdx.x * kScoreWarps, e = min(e0 + warp, E - 1), t0 = blockIdx.y * TB;
+    Sum2 s[TB];
+#pragma unroll
+    for (int j = 0; j < TB; ++j) s[j] = Sum2{0.f, 0.f};
+    const Tr* r = router + (int64_t)e * D;
+#pragma unroll 2
+    for (int k = lane * 8; k < D; k += 256) {
+        float rv[8];
+        load8_any(r + k, rwide, rv);
+#pragma unroll
+        for (int j = 0; j < TB; ++j) {
+            float xv[8];
+            load8_any(x + (int64_t)min(t0 + j, M - 1) * xs + k, wide, xv);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float p = xv[i] * rv[i];  // exact for a bf16 router
+                s[j].add(p);
+                if constexpr (sizeof(Tr) == 4) s[j].lo += fmaf(xv[i], rv[i], -p);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+            const float h = __shfl_xor_sync(0xffffffffu, s[j].hi, d), l = __shfl_xor_sync(0xffffffffu, s[j].lo, d);
+            s[j].add(h);
+            s[j].lo += l;
+        }
+        // a sum that is not finite leaves NaN in its rounding term
+        if (lane == 0) sums[warp][j] = isfinite(s[j].hi) ? (double)s[j].hi + (double)s[j].lo : (double)s[j].hi;
+    }
+    __syncthreads();
+    if (threadIdx.x < kScoreWarps * TB) {
+        const int w = threadIdx.x & (kScoreWarps - 1), j = threadIdx.x / kScoreWarps;
+        if (e0 + w < E && t0 + j < M) {
+            const int64_t at = (int64_t)(t0 + j) * E + e0 + w;
+            const double l = sums[w][j], v = sigmoid ? 1.0 / (1.0 + exp(-l)) : l;
+            score[at] = v;
+            key[at] = ordered(bias ? v + (double)bias[e0 + w] : v);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ choice and lists
+constexpr int kPickThreads = 512, kPickWarps = 16;
+
+// One block.  A warp per token finds its experts one after another: the lanes' best keys are joined by the
+// warp's integer maximum, upper half first.  Then the slots (token, rank) are listed by expert; the order of
+// an expert's slots is free, since every column of a product is computed alike.
+template <int KPL>  // keys per lane
+__global__ void __launch_bounds__(kPickThreads) k_moe_pick(const double* __restrict__ score, const uint64_t* __restrict__ key, int M, int E,
+                                                           int top, int sigmoid, float scale, int* __restrict__ ids, float* __restrict__ weights,
+                                                           int* __restrict__ lists, int* __restrict__ user_ids, float* __restrict__ user_weights) {
+    __shared__ int count[1024], begin[1024];
+    __shared__ uint32_t warp_sum[kPickWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < 1024; i += kPickThreads) count[i] = 0;
+    __syncthreads();
+    for (int t = warp; t < M; t += kPickWarps) {
+        uint64_t k[KPL];
+#pragma unroll
+        for (int i = 0; i < KPL; ++i) k[i] = lane + 32 * i < E ? key[(int64_t)t * E + lane + 32 * i] : 0;
+        uint32_t left = 0;  // keys of this lane that are not taken
+#pragma unroll
+        for (int i = 0; i < KPL; ++i) left |= (lane + 32 * i < E ? 1u : 0u) << i;
+        uint64_t best = 0;
+        int at = 0;
+        auto refresh = [&]() {
+            best = 0;
+            at = left ? __ffs(left) - 1 : 0;
+#pragma unroll
+            for (int i = 0; i < KPL; ++i)
+                if (((left >> i) & 1u) && k[i] > best) best = k[i], at = i;
+        };
+        refresh();
+        int mine = 0;
+        for (int j = 0; j < top; ++j) {
+            const uint32_t hi = __reduce_max_sync(0xffffffffu, left ? (uint32_t)(best >> 32) : 0u);
+            const bool in = left && (uint32_t)(best >> 32) == hi;
+            const uint32_t lo = __reduce_max_sync(0xffffffffu, in ? (uint32_t)best : 0u);
+            const int e = (int)__reduce_min_sync(0xffffffffu, in && (uint32_t)best == lo ? (uint32_t)(lane + 32 * at) : 0x7fffffffu);
+            if (lane == j) mine = e;
+            if ((e & 31) == lane) {
+                left &= ~(1u << (e >> 5));
+                refresh();
+            }
+        }
+        const double l = lane < top ? score[(int64_t)t * E + mine] : 0.0;
+        double v = 0.0;
+        if (sigmoid) {
+            v = l;
+        } else {
+            const double first = __shfl_sync(0xffffffffu, l, 0);  // the largest logit
+            if (lane < top) v = exp(l - first);
+        }
+        double sum = v;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane < top) {
+            const float w = (float)(v / sum * (double)scale);
+            const int slot = t * top + lane;
+            ids[slot] = mine;
+            weights[slot] = w;
+            if (user_ids) user_ids[slot] = mine;
+            if (user_weights) user_weights[slot] = w;
+            atomicAdd(&count[mine], 1);
+        }
+    }
+    __syncthreads();
+    // running sums over the experts: slots in the low half, experts in use in the high half
+    const int c0 = count[2 * threadIdx.x], c1 = count[2 * threadIdx.x + 1];
+    const uint32_t own0 = (uint32_t)c0 | (c0 ? 1u << 20 : 0u), own1 = (uint32_t)c1 | (c1 ? 1u << 20 : 0u);
+    uint32_t run = own0 + own1;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, run, d);
+        if (lane >= d) run += o;
+    }
+    if (lane == 31) warp_sum[warp] = run;
+    __syncthreads();
+    uint32_t before = run - own0 - own1;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    int* which = lists + 1;
+    int* starts = lists + 1 + E;
+    int* slots = lists + 2 + 2 * E;
+    constexpr uint32_t kLow = (1u << 20) - 1;
+    begin[2 * threadIdx.x] = before & kLow;
+    begin[2 * threadIdx.x + 1] = (before & kLow) + c0;
+    if (c0) {
+        which[before >> 20] = 2 * threadIdx.x;
+        starts[before >> 20] = before & kLow;
+    }
+    before += own0;
+    if (c1) {
+        which[before >> 20] = 2 * threadIdx.x + 1;
+        starts[before >> 20] = before & kLow;
+    }
+    before += own1;
+    if (threadIdx.x == kPickThreads - 1) {
+        lists[0] = before >> 20;
+        starts[before >> 20] = before & kLow;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < M * top; i += kPickThreads) slots[atomicAdd(&begin[ids[i]], 1)] = i;
+}
+
+// ------------------------------------------------------------------ the experts' products
+struct Experts {
+    const uint8_t* w;
+    const uint8_t* scales;
+    int64_t w_bytes, s_bytes;  // of one expert
+    int scale_type, group_shift;
+    int rows, K;               // of one expert's matrix
+    const int* lists;
+    int E, top, ranks;
+    __device__ __forceinline__ Matrix matrix(int e) const {
+        return Matrix{w + e * w_bytes, scales + e * s_bytes, scale_type, group_shift};
+    }
+};
+
+// hidden[slot][f] = silu(g) u: the tile's rows are 64 of the gate's and the same 64 of the other half.
+template <int F, int NT>
+__global__ void __launch_bounds__(kThreads, 2) k_moe_in(const Experts p, const Bf16Rows src, float* __restrict__ hidden) {
+    using L = Layout<F, NT>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int of[L::cols], slot[L::cols];
+    if ((int)blockIdx.y >= p.lists[0]) return;  // the whole cluster
+    const int e = p.lists[1 + blockIdx.y], first = p.lists[1 + p.E + blockIdx.y], last = p.lists[2 + p.E + blockIdx.y];
+    const int* slots = p.lists + 2 + 2 * p.E;
+    const int rank = blockIdx.x % p.ranks, row0 = blockIdx.x / p.ranks * (kTileRows / 2), half = p.rows / 2;
+    int k0, k1;
+    slice_of(p.K, rank, p.ranks, k0, k1);
+    const auto row_of = [&](int r) { return (int64_t)(min(row0 + (r & 63), half - 1) + (r >= 64 ? half : 0)); };
+    const Matrix m = p.matrix(e);
+    for (int c0 = first; c0 < last; c0 += L::cols) {
+        const int n = min(L::cols, last - c0);
+        if (threadIdx.x < n) {
+            slot[threadIdx.x] = slots[c0 + threadIdx.x];
+            of[threadIdx.x] = slots[c0 + threadIdx.x] / p.top;
+        }
+        __syncthreads();
+        float acc[NT][4];
+        product<F, NT>(smem, m, p.K, row_of, src, of, n, k0, k1, acc);
+        float* red = gather<F, NT>(smem, acc, p.ranks);
+        const int share = 64 / p.ranks;
+        for (int i = threadIdx.x; i < n * share; i += kThreads) {
+            const int c = i / share, r = rank * share + i % share;
+            if (row0 + r >= half) continue;
+            const float gate = joined<1>(red, p.ranks, c, r), up = joined<1>(red, p.ranks, c, r + 64);
+            hidden[(int64_t)slot[c] * half + row0 + r] = gate / (1.0f + expf(-gate)) * up;
+        }
+        release(p.ranks);
+    }
+}
+
+// parts[slot][d] = w_slot W_out hidden_slot.
+template <int F, int NT>
+__global__ void __launch_bounds__(kThreads, 2) k_moe_out(const Experts p, const float* __restrict__ hidden, const float* __restrict__ weights,
+                                                         float* __restrict__ parts) {
+    using L = Layout<F, NT>;
+    constexpr int kTerms = Format<F>::terms, kRows = L::cols / kTerms;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int of[kRows];
+    if ((int)blockIdx.y >= p.lists[0]) return;
+    const int e = p.lists[1 + blockIdx.y], first = p.lists[1 + p.E + blockIdx.y], last = p.lists[2 + p.E + blockIdx.y];
+    const int* slots = p.lists + 2 + 2 * p.E;
+    const int rank = blockIdx.x % p.ranks, row0 = blockIdx.x / p.ranks * kTileRows;
+    int k0, k1;
+    slice_of(p.K, rank, p.ranks, k0, k1);
+    const auto row_of = [&](int r) { return (int64_t)min(row0 + r, p.rows - 1); };
+    const Matrix m = p.matrix(e);
+    for (int c0 = first; c0 < last; c0 += kRows) {
+        const int n = min(kRows, last - c0);
+        if (threadIdx.x < n) of[threadIdx.x] = slots[c0 + threadIdx.x];
+        __syncthreads();
+        float acc[NT][4];
+        product<F, NT>(smem, m, p.K, row_of, F32Rows{hidden, p.K}, of, n, k0, k1, acc);
+        float* red = gather<F, NT>(smem, acc, p.ranks);
+        const int share = kTileRows / p.ranks;
+        for (int i = threadIdx.x; i < n * share; i += kThreads) {
+            const int c = i / share, r = rank * share + i % share;
+            if (row0 + r < p.rows) parts[(int64_t)of[c] * p.rows + row0 + r] = weights[of[c]] * joined<kTerms>(red, p.ranks, c, r);
+        }
+        release(p.ranks);
+    }
+}
+
+// y[t][d] = the sum of the token's parts, in the order of their rank.
+template <typename T>
+__global__ void __launch_bounds__(256) k_moe_sum(const float* __restrict__ parts, int M, int D, int top, T* __restrict__ y, int64_t ys) {
+    const int t = blockIdx.y;
+    for (int d = (blockIdx.x * 256 + threadIdx.x) * 4; d < D; d += gridDim.x * 1024) {  // D is a multiple of 8
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int j = 0; j < top; ++j) {
+            const float4 p = *reinterpret_cast<const float4*>(parts + (int64_t)(t * top + j) * D + d);
+            v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+        }
+        T* o = y + (int64_t)t * ys + d;
+        o[0] = from_f<T>(v.x), o[1] = from_f<T>(v.y), o[2] = from_f<T>(v.z), o[3] = from_f<T>(v.w);
+    }
+}
+
+// ------------------------------------------------------------------ launches
+template <typename... P, typename... A>
+cudaError_t launch_cluster(void (*kernel)(P...), dim3 grid, int ranks, int smem, cudaStream_t s, A&&... args) {
+    if (const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ranks;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = kThreads;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = ranks > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+template <typename Tr> cudaError_t launch_scores(const kda_moe_args& a, int64_t xs, bool wide, double* score, uint64_t* key, cudaStream_t s) {
+    const bf16* x = static_cast<const bf16*>(a.x);
+    const Tr* r = static_cast<const Tr*>(a.router);
+    const bool rwide = reinterpret_cast<uintptr_t>(r) % 16 == 0;
+    const int blocks = (a.E + kScoreWarps - 1) / kScoreWarps, sg = a.score == KDA_SCORE_SIGMOID;
+    if (a.M == 1)
+        k_moe_scores<Tr, 1><<<dim3(blocks, 1), kScoreThreads, 0, s>>>(x, xs, wide, r, rwide, a.bias, a.M, a.E, a.D, sg, score, key);
+    else
+        k_moe_scores<Tr, 4><<<dim3(blocks, (a.M + 3) / 4), kScoreThreads, 0, s>>>(x, xs, wide, r, rwide, a.bias, a.M, a.E, a.D, sg, score, key);
+    return cudaGetLastError();
+}
+
+template <int F, int NT>
+cudaError_t launch_experts(const kda_moe_args& a, const Experts& in, const Experts& out, const Bf16Rows& src, float* hidden, const float* weights,
+                           float* parts, int most, cudaStream_t s) {
+    using L = Layout<F, NT>;
+    cudaError_t e = launch_cluster(k_moe_in<F, NT>, dim3((a.F + 63) / 64 * in.ranks, most), in.ranks, L::bytes, s, in, src, hidden);
+    if (e) return e;
+    return launch_cluster(k_moe_out<F, NT>, dim3((a.D + kTileRows - 1) / kTileRows * out.ranks, most), out.ranks, L::bytes, s, out,
+                          (const float*)hidden, weights, parts);
+}
+
+template <int F, typename... A> cudaError_t launch_width(int columns, A&&... args) {
+    if (columns <= 8) return launch_experts<F, 1>(std::forward<A>(args)...);
+    if (columns <= 16) return launch_experts<F, 2>(std::forward<A>(args)...);
+    return launch_experts<F, 4>(std::forward<A>(args)...);
+}
+
+size_t weight_bytes(const kda_moe_args& a, int64_t rows, int64_t K) { return a.format == KDA_WEIGHT_BF16 ? rows * K * 2 : rows * K / 2; }
+size_t scale_bytes(const kda_moe_args& a, int64_t rows, int64_t K) {
+    if (a.format == KDA_WEIGHT_BF16) return 0;
+    return rows * (K / a.group) * (a.format == KDA_WEIGHT_E2M1 ? 1 : a.scale_dtype == KDA_BF16 ? 2 : 4);
+}
+
+}  // namespace
+
+MoePlan moe_plan(const kda_moe_args& a) {
+    MoePlan p;
+    size_t at = 0;
+    const size_t slots = (size_t)a.M * a.top;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at = (at + bytes + 255) / 256 * 256;
+        return here;
+    };
+    p.score = take((size_t)a.M * a.E * 8);
+    p.key = take((size_t)a.M * a.E * 8);
+    p.ids = take(slots * 4);
+    p.weights = take(slots * 4);
+    p.lists = take((2 + 2 * (size_t)a.E + slots) * 4);
+    p.hidden = take(slots * a.F * 4);
+    p.parts = take(slots * a.D * 4);
+    p.workspace = at;
+    return p;
+}
+
+cudaError_t launch_moe(const kda_moe_args& a, const MoePlan& p, cudaStream_t s) {
+    char* ws = static_cast<char*>(a.workspace);
+    double* score = reinterpret_cast<double*>(ws + p.score);
+    uint64_t* key = reinterpret_cast<uint64_t*>(ws + p.key);
+    int* ids = reinterpret_cast<int*>(ws + p.ids);
+    float* weights = reinterpret_cast<float*>(ws + p.weights);
+    int* lists = reinterpret_cast<int*>(ws + p.lists);
+    float* hidden = reinterpret_cast<float*>(ws + p.hidden);
+    float* parts = reinterpret_cast<float*>(ws + p.parts);
+    const int64_t xs = a.x_stride ? a.x_stride : a.D, ys = a.y_stride ? a.y_stride : a.D;
+    const bool wide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (xs % 8 == 0 || a.M == 1);
+    cudaError_t e = a.router_dtype == KDA_BF16 ? launch_scores<bf16>(a, xs, wide, score, key, s)
+                                               : launch_scores<float>(a, xs, wide, score, key, s);
+    if (e) return e;
+    const int sg = a.score == KDA_SCORE_SIGMOID;
+    const auto pick = a.E <= 256 ? k_moe_pick<8> : a.E <= 512 ? k_moe_pick<16> : k_moe_pick<32>;
+    pick<<<1, kPickThreads, 0, s>>>(score, key, a.M, a.E, a.top, sg, a.scale, ids, weights, lists, a.ids, a.weights);
+    if ((e = cudaGetLastError())) return e;
+
+    const int slots = a.M * a.top, most = slots < a.E ? slots : a.E;
+    // experts in use if the choices were even: what the clusters are sized for
+    const int64_t likely = most;
+    Experts in = {}, out = {};
+    in.w = static_cast<const uint8_t*>(a.w_in), in.scales = static_cast<const uint8_t*>(a.w_in_scales);
+    in.w_bytes = weight_bytes(a, 2 * a.F, a.D), in.s_bytes = scale_bytes(a, 2 * a.F, a.D);
+    in.scale_type = a.format == KDA_WEIGHT_E2M1 ? 0 : a.scale_dtype == KDA_BF16 ? 1 : 2;
+    in.group_shift = group_shift(a.group);
+    in.rows = 2 * a.F, in.K = a.D, in.lists = lists, in.E = a.E, in.top = a.top;
+    in.ranks = cluster_ranks(likely * ((a.F + 63) / 64), a.D);
+    out = in;
+    out.w = static_cast<const uint8_t*>(a.w_out), out.scales = static_cast<const uint8_t*>(a.w_out_scales);
+    out.w_bytes = weight_bytes(a, a.D, a.F), out.s_bytes = scale_bytes(a, a.D, a.F);
+    out.rows = a.D, out.K = a.F;
+    out.ranks = cluster_ranks(likely * ((a.D + kTileRows - 1) / kTileRows), a.F);
+    // columns for twice an expert's even share of the slots, and no more than there are tokens
+    const int even = 2 * ((slots + a.E - 1) / a.E) + 2, columns = a.M < even ? a.M : even;
+    const Bf16Rows src{static_cast<const bf16*>(a.x), xs, wide};
+    if (a.format == KDA_WEIGHT_E2M1)
+        e = launch_width<KDA_WEIGHT_E2M1>(columns, a, in, out, src, hidden, weights, parts, most, s);
+    else if (a.format == KDA_WEIGHT_INT4)
+        e = launch_width<KDA_WEIGHT_INT4>(columns, a, in, out, src, hidden, weights, parts, most, s);
+    else
+        e = launch_width<KDA_WEIGHT_BF16>(columns, a, in, out, src, hidden, weights, parts, most, s);
+    if (e) return e;
+    const dim3 grid((a.D + 1023) / 1024, a.M);
+    if (a.y_dtype == KDA_BF16)
+        k_moe_sum<bf16><<<grid, 256, 0, s>>>(parts, a.M, a.D, a.top, static_cast<bf16*>(a.y), ys);
+    else
+        k_moe_sum<float><<<grid, 256, 0, s>>>(parts, a.M, a.D, a.top, static_cast<float*>(a.y), ys);
+    return cudaGetLastError();
+}
+
+}  // namespace kda
