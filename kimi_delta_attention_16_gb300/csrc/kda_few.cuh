@@ -172,7 +172,7 @@ __device__ __forceinline__ void stage_columns(uint8_t* smem, const Src& src, con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* xs = reinterpret_cast<float*>(smem + L::xs_at);
     const int chunks = min(L::seg_chunks, (k1 - k0 + kChunk - 1) / kChunk);
-    const int rows = L::cols / kTerms, items = rows * chunks;
+    const int items = n * chunks;
     for (int it0 = warp; it0 < items; it0 += kWarps * kBatch) {
         uint32_t v[kBatch][Src::split ? 8 : 4];
 #pragma unroll
@@ -180,7 +180,7 @@ __device__ __forceinline__ void stage_columns(uint8_t* smem, const Src& src, con
             const int it = it0 + b * kWarps, c = it / chunks, k = k0 + (it - c * chunks) * kChunk + lane * 8;
 #pragma unroll
             for (int i = 0; i < (Src::split ? 8 : 4); ++i) v[b][i] = 0;
-            if (c < n && k < k1) {
+            if (it < items && k < k1) {
                 if constexpr (Src::split) {
                     const float4* p = reinterpret_cast<const float4*>(src.x + (int64_t)of[c] * src.stride + k);
                     const float4 lo = p[0], hi = p[1];
@@ -269,11 +269,17 @@ __device__ __forceinline__ void stage_columns(uint8_t* smem, const Src& src, con
             }
         }
     }
-    if constexpr (kTerms > 1 && L::cols % kTerms != 0) {  // columns behind the last whole row
-        for (int c = rows * kTerms; c < L::cols; ++c)
-            for (int i = threadIdx.x; i < L::x_pitch / 16; i += kThreads)
-                reinterpret_cast<uint4*>(smem + L::x_at + c * L::x_pitch)[i] = make_uint4(0, 0, 0, 0);
-    }
+}
+
+// Zeros for the columns that hold no token: what multiplies them is never read, but must not trap or turn up as NaN in
+// other columns' runs.
+template <int F, int NT> __device__ __forceinline__ void clear_columns(uint8_t* smem, int used) {
+    using L = Layout<F, NT>;
+    float* xs = reinterpret_cast<float*>(smem + L::xs_at);
+    uint4* x = reinterpret_cast<uint4*>(smem + L::x_at + used * L::x_pitch);
+    for (int i = threadIdx.x; i < (L::cols - used) * (L::x_pitch / 16); i += kThreads) x[i] = make_uint4(0, 0, 0, 0);
+    if constexpr (F != KDA_WEIGHT_BF16)
+        for (int i = used * L::seg_chunks + threadIdx.x; i < L::cols * L::seg_chunks; i += kThreads) xs[i] = 0.f;
 }
 
 // Scales of the tile's rows for K in [k0, k0 + seg), one fp32 per row and 32 elements (zeros from k1).
@@ -362,6 +368,7 @@ __device__ __forceinline__ void product(uint8_t* smem, const Matrix& m, int K, c
     const float* sc1 = sc0 + 8 * L::s_pitch;
     const float* xs = reinterpret_cast<const float*>(smem + L::xs_at);
     const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+    clear_columns<F, NT>(smem, n * (Src::split ? Format<F>::terms : 1));
     int c = 0;
     for (int seg = k0; seg < k1; seg += L::seg) {
         if (seg != k0) __syncthreads();  // every warp is done with the last columns
@@ -375,6 +382,13 @@ __device__ __forceinline__ void product(uint8_t* smem, const Matrix& m, int K, c
             issue(c + L::stages - 1);
             const uint32_t wrow = ring + (uint32_t)(c % L::stages) * kWarpStage + g * kRowStage + t * 4;
             if constexpr (kBf16) {
+                // a stage's sum starts from zero and is added in fp32: the matrix instructions drop digits below the
+                // accumulator's last one, which over a long chain takes 5 of its 24 bits
+                float part[NT][4];
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) part[i][j] = 0.f;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t w[4][2];
@@ -389,10 +403,14 @@ __device__ __forceinline__ void product(uint8_t* smem, const Matrix& m, int K, c
                         const uint4 x = lds128(col + i * 8 * L::x_pitch + (run * kStageK + 32 * h) * 2);
                         const uint32_t a0[4] = {w[0][0], w[0][1], w[1][0], w[1][1]};
                         const uint32_t a1[4] = {w[2][0], w[2][1], w[3][0], w[3][1]};
-                        mma<true>(acc[i], a0, x.x, x.y, acc[i]);
-                        mma<true>(acc[i], a1, x.z, x.w, acc[i]);
+                        mma<true>(part[i], a0, x.x, x.y, part[i]);
+                        mma<true>(part[i], a1, x.z, x.w, part[i]);
                     }
                 }
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[i][j] += part[i][j];
             } else {
                 float part[NT][4];
 #pragma unroll

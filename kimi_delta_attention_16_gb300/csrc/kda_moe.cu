@@ -11,6 +11,7 @@
 // products, sum over a token's experts in the order of their rank.
 #include "kda_few.cuh"
 #include "kda_serve.cuh"
+#include "kda_wide.cuh"
 
 namespace kda {
 
@@ -19,27 +20,21 @@ namespace {
 using namespace few;
 
 // ------------------------------------------------------------------ scores
-// The sum of a lane's products as two fp32 (value and what its rounding lost): a choice between two experts
-// hangs on the last digits of a sum over thousands of products, and fp64 runs at 1/64 of the fp32 rate here.
-struct Sum2 {
-    float hi, lo;
-    __device__ __forceinline__ void add(float v) {
-        const float s = hi + v, b = s - hi;
-        lo += (hi - (s - b)) + (v - b);
-        hi = s;
-    }
-};
-
+// A choice between two experts hangs on the last digits of a sum over thousands of products, so logits and scores are
+// pairs of fp32 (kda_wide.cuh).  A block takes one expert and TB tokens, its warps share the row: with few
+// tokens all of the router is on its way at once.
 constexpr int kScoreThreads = 256, kScoreWarps = 8;
 
-__device__ __forceinline__ uint64_t ordered(double v) {  // a larger value is a larger integer; NaN is the smallest
-    if (isnan(v)) return 0;
-    const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
-    return b >> 63 ? ~b : b | (1ull << 63);
+__device__ __forceinline__ uint32_t ordered(float v) {  // a larger value is a larger integer
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    return b >> 31 ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t ordered(Wide v) {  // NaN is the smallest
+    return isnan(v.hi) ? 0 : (uint64_t)ordered(v.hi) << 32 | ordered(v.lo);
 }
 
-template <typename T> __device__ __forceinline__ void load8_any(const T* p, bool wide, float (&v)[8]) {
-    if (wide) {
+template <typename T> __device__ __forceinline__ void load8_any(const T* p, bool aligned, float (&v)[8]) {
+    if (aligned) {
         load8(p, v);
     } else {
 #pragma unroll
@@ -47,32 +42,30 @@ template <typename T> __device__ __forceinline__ void load8_any(const T* p, bool
     }
 }
 
-// A warp takes one expert and TB tokens, a block eight experts; the scores of a block are computed by one warp
-// at once (fp64 instructions cost by the warp).
 template <typename Tr, int TB>
-__global__ void __launch_bounds__(kScoreThreads) k_moe_scores(const bf16* __restrict__ x, int64_t xs, bool wide, const Tr* __restrict__ router,
+__global__ void __launch_bounds__(kScoreThreads) k_moe_scores(const bf16* __restrict__ x, int64_t xs, bool xwide, const Tr* __restrict__ router,
                                                               bool rwide, const float* __restrict__ bias, int M, int E, int D,
-                                                              int sigmoid, double* __restrict__ score, uint64_t* __restrict__ key) {
-    __shared__ double sums[kScoreWarps][TB];
+                                                              int sigmoid, Wide* __restrict__ score, uint64_t* __restrict__ key,
+                                                              int* __restrict__ done) {
+    __shared__ Wide sums[kScoreWarps][TB];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int e0 = blockIdx.x * kScoreWarps, e = min(e0 + warp, E - 1), t0 = blockIdx.y * TB;
+    const int e = blockIdx.x, t0 = blockIdx.y * TB;
+    if (e == 0 && t0 == 0 && threadIdx.x == 0) *done = 0;
     Sum2 s[TB];
-#pragma unroll
-    for (int j = 0; j < TB; ++j) s[j] = Sum2{0.f, 0.f};
     const Tr* r = router + (int64_t)e * D;
 #pragma unroll 2
-    for (int k = lane * 8; k < D; k += 256) {
-        float rv[8];
+    for (int k = threadIdx.x * 8; k < D; k += kScoreThreads * 8) {
+        float rv[8], xv[TB][8];
         load8_any(r + k, rwide, rv);
 #pragma unroll
+        for (int j = 0; j < TB; ++j) load8_any(x + (int64_t)min(t0 + j, M - 1) * xs + k, xwide, xv[j]);
+#pragma unroll
         for (int j = 0; j < TB; ++j) {
-            float xv[8];
-            load8_any(x + (int64_t)min(t0 + j, M - 1) * xs + k, wide, xv);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float p = xv[i] * rv[i];  // exact for a bf16 router
+                const float p = xv[j][i] * rv[i];  // exact for a bf16 router
                 s[j].add(p);
-                if constexpr (sizeof(Tr) == 4) s[j].lo += fmaf(xv[i], rv[i], -p);
+                if constexpr (sizeof(Tr) == 4) s[j].lo += fmaf(xv[j][i], rv[i], -p);
             }
         }
     }
@@ -84,88 +77,123 @@ __global__ void __launch_bounds__(kScoreThreads) k_moe_scores(const bf16* __rest
             s[j].add(h);
             s[j].lo += l;
         }
-        // a sum that is not finite leaves NaN in its rounding term
-        if (lane == 0) sums[warp][j] = isfinite(s[j].hi) ? (double)s[j].hi + (double)s[j].lo : (double)s[j].hi;
+        if (lane == 0) sums[warp][j] = wide(s[j]);
     }
     __syncthreads();
-    if (threadIdx.x < kScoreWarps * TB) {
-        const int w = threadIdx.x & (kScoreWarps - 1), j = threadIdx.x / kScoreWarps;
-        if (e0 + w < E && t0 + j < M) {
-            const int64_t at = (int64_t)(t0 + j) * E + e0 + w;
-            const double l = sums[w][j], v = sigmoid ? 1.0 / (1.0 + exp(-l)) : l;
-            score[at] = v;
-            key[at] = ordered(bias ? v + (double)bias[e0 + w] : v);
-        }
+    const int j = threadIdx.x;
+    if (j < TB && t0 + j < M) {
+        Wide v = sums[0][j];
+#pragma unroll
+        for (int w = 1; w < kScoreWarps; ++w) v = add(v, sums[w][j]);
+        const int64_t at = (int64_t)(t0 + j) * E + e;
+        const Wide logit = v;
+        if (sigmoid) v = sigmoid_wide(v);
+        score[at] = v;
+        // scores next to 1 are equal where fp64 holds them equal; small ones without a bias are ordered by their logits
+        // (negative, so below every other score), which do not underflow
+        key[at] = ordered(!sigmoid ? logit : bias ? to_53_bits(add(v, Wide{bias[e], 0.f})) : logit.hi < 0.f ? logit : to_53_bits(v));
     }
 }
 
 // ------------------------------------------------------------------ choice and lists
 constexpr int kPickThreads = 512, kPickWarps = 16;
 
-// One block.  A warp per token finds its experts one after another: the lanes' best keys are joined by the
-// warp's integer maximum, upper half first.  Then the slots (token, rank) are listed by expert; the order of
-// an expert's slots is free, since every column of a product is computed alike.
-template <int KPL>  // keys per lane
-__global__ void __launch_bounds__(kPickThreads) k_moe_pick(const double* __restrict__ score, const uint64_t* __restrict__ key, int M, int E,
-                                                           int top, int sigmoid, float scale, int* __restrict__ ids, float* __restrict__ weights,
-                                                           int* __restrict__ lists, int* __restrict__ user_ids, float* __restrict__ user_weights) {
+// The largest key of the warp and the lowest index among its holders; a lane without a key has index 0x7fffffff.
+__device__ __forceinline__ int largest(uint64_t key, int index, uint64_t& top) {
+    const bool has = index != 0x7fffffff;
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, has ? (uint32_t)(key >> 32) : 0u);
+    const bool in = has && (uint32_t)(key >> 32) == hi;
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, in ? (uint32_t)key : 0u);
+    top = (uint64_t)hi << 32 | lo;
+    return (int)__reduce_min_sync(0xffffffffu, in && (uint32_t)key == lo ? (uint32_t)index : 0x7fffffffu);
+}
+
+// A block per token: each warp orders the best `top` of its 64 experts, one warp merges the sixteen lists.  The block
+// that finishes last lists the slots (token, rank) by expert; the order of an expert's slots is free, since every
+// column of a product is computed alike.
+__global__ void __launch_bounds__(kPickThreads) k_moe_pick(const Wide* __restrict__ score, const uint64_t* __restrict__ key, int M, int E, int top,
+                                                           int sigmoid, float scale, int* __restrict__ ids, float* __restrict__ weights,
+                                                           int* __restrict__ done, int* __restrict__ lists, int* __restrict__ user_ids,
+                                                           float* __restrict__ user_weights) {
+    __shared__ uint64_t best_key[kPickWarps][33];
+    __shared__ int best_id[kPickWarps][33];
     __shared__ int count[1024], begin[1024];
     __shared__ uint32_t warp_sum[kPickWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < 1024; i += kPickThreads) count[i] = 0;
-    __syncthreads();
-    for (int t = warp; t < M; t += kPickWarps) {
-        uint64_t k[KPL];
+    __shared__ bool last;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.x;
+    {
+        // a warp's experts are 64 in a row, two per lane
+        uint64_t k[2];
+        int id[2];
 #pragma unroll
-        for (int i = 0; i < KPL; ++i) k[i] = lane + 32 * i < E ? key[(int64_t)t * E + lane + 32 * i] : 0;
-        uint32_t left = 0;  // keys of this lane that are not taken
-#pragma unroll
-        for (int i = 0; i < KPL; ++i) left |= (lane + 32 * i < E ? 1u : 0u) << i;
-        uint64_t best = 0;
-        int at = 0;
-        auto refresh = [&]() {
-            best = 0;
-            at = left ? __ffs(left) - 1 : 0;
-#pragma unroll
-            for (int i = 0; i < KPL; ++i)
-                if (((left >> i) & 1u) && k[i] > best) best = k[i], at = i;
-        };
-        refresh();
-        int mine = 0;
+        for (int i = 0; i < 2; ++i) {
+            const int e = warp * 64 + 32 * i + lane;
+            k[i] = e < E ? key[(int64_t)t * E + e] : 0;
+            id[i] = e < E ? e : 0x7fffffff;
+        }
+        if (id[1] != 0x7fffffff && k[1] > k[0]) {  // the better one first; the lower index where they are equal
+            const uint64_t kk = k[0];
+            const int ii = id[0];
+            k[0] = k[1], id[0] = id[1], k[1] = kk, id[1] = ii;
+        }
+        int mine = 0x7fffffff;
+        uint64_t mine_key = 0;
         for (int j = 0; j < top; ++j) {
-            const uint32_t hi = __reduce_max_sync(0xffffffffu, left ? (uint32_t)(best >> 32) : 0u);
-            const bool in = left && (uint32_t)(best >> 32) == hi;
-            const uint32_t lo = __reduce_max_sync(0xffffffffu, in ? (uint32_t)best : 0u);
-            const int e = (int)__reduce_min_sync(0xffffffffu, in && (uint32_t)best == lo ? (uint32_t)(lane + 32 * at) : 0x7fffffffu);
+            uint64_t v;
+            const int e = largest(k[0], id[0], v);
+            if (lane == j) mine = e, mine_key = v;
+            if (id[0] == e) k[0] = k[1], id[0] = id[1], k[1] = 0, id[1] = 0x7fffffff;
+        }
+        best_key[warp][lane] = mine_key;
+        best_id[warp][lane] = mine;
+        if (lane == 0) best_id[warp][32] = 0x7fffffff;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int head = 0, mine = 0;
+        uint64_t k = lane < kPickWarps ? best_key[lane][0] : 0, v;
+        int id = lane < kPickWarps ? best_id[lane][0] : 0x7fffffff;
+        for (int j = 0; j < top; ++j) {
+            const int e = largest(k, id, v);
             if (lane == j) mine = e;
-            if ((e & 31) == lane) {
-                left &= ~(1u << (e >> 5));
-                refresh();
+            if (id == e) {
+                ++head;
+                k = best_key[lane][head];
+                id = best_id[lane][head];
             }
         }
-        const double l = lane < top ? score[(int64_t)t * E + mine] : 0.0;
-        double v = 0.0;
-        if (sigmoid) {
-            v = l;
-        } else {
-            const double first = __shfl_sync(0xffffffffu, l, 0);  // the largest logit
-            if (lane < top) v = exp(l - first);
+        Wide w;
+        if (lane < top) w = score[(int64_t)t * E + mine];
+        if (!sigmoid) {
+            const Wide first = from(0xffffffffu, w, 0);  // the largest logit
+            if (lane < top) w = exp_wide(add(w, minus(first)));
         }
-        double sum = v;
+        Wide sum = w;
 #pragma unroll
-        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        for (int d = 16; d; d >>= 1) sum = add(sum, Wide{__shfl_xor_sync(0xffffffffu, sum.hi, d), __shfl_xor_sync(0xffffffffu, sum.lo, d)});
         if (lane < top) {
-            const float w = (float)(v / sum * (double)scale);
+            const Wide q = times(over(w, sum), Wide{scale, 0.f});
             const int slot = t * top + lane;
             ids[slot] = mine;
-            weights[slot] = w;
+            weights[slot] = q.hi;
             if (user_ids) user_ids[slot] = mine;
-            if (user_weights) user_weights[slot] = w;
-            atomicAdd(&count[mine], 1);
+            if (user_weights) user_weights[slot] = q.hi;
+        }
+        __syncwarp();
+        if (lane == 0) {
+            __threadfence();
+            last = atomicAdd(done, 1) == M - 1;
         }
     }
     __syncthreads();
-    // running sums over the experts: slots in the low half, experts in use in the high half
+    if (!last) return;
+    __threadfence();
+    for (int i = threadIdx.x; i < 1024; i += kPickThreads) count[i] = 0;
+    __syncthreads();
+    const int slots = M * top;
+    for (int i = threadIdx.x; i < slots; i += kPickThreads) atomicAdd(&count[__ldcg(ids + i)], 1);
+    __syncthreads();
+    // running sums over the experts: slots in the low 20 bits, experts in use above them
     const int c0 = count[2 * threadIdx.x], c1 = count[2 * threadIdx.x + 1];
     const uint32_t own0 = (uint32_t)c0 | (c0 ? 1u << 20 : 0u), own1 = (uint32_t)c1 | (c1 ? 1u << 20 : 0u);
     uint32_t run = own0 + own1;
@@ -180,7 +208,7 @@ __global__ void __launch_bounds__(kPickThreads) k_moe_pick(const double* __restr
     for (int w = 0; w < warp; ++w) before += warp_sum[w];
     int* which = lists + 1;
     int* starts = lists + 1 + E;
-    int* slots = lists + 2 + 2 * E;
+    int* listed = lists + 2 + 2 * E;
     constexpr uint32_t kLow = (1u << 20) - 1;
     begin[2 * threadIdx.x] = before & kLow;
     begin[2 * threadIdx.x + 1] = (before & kLow) + c0;
@@ -199,7 +227,7 @@ __global__ void __launch_bounds__(kPickThreads) k_moe_pick(const double* __restr
         starts[before >> 20] = before & kLow;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < M * top; i += kPickThreads) slots[atomicAdd(&begin[ids[i]], 1)] = i;
+    for (int i = threadIdx.x; i < slots; i += kPickThreads) listed[atomicAdd(&begin[__ldcg(ids + i)], 1)] = i;
 }
 
 // ------------------------------------------------------------------ the experts' products
@@ -317,15 +345,15 @@ cudaError_t launch_cluster(void (*kernel)(P...), dim3 grid, int ranks, int smem,
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
-template <typename Tr> cudaError_t launch_scores(const kda_moe_args& a, int64_t xs, bool wide, double* score, uint64_t* key, cudaStream_t s) {
+template <typename Tr> cudaError_t launch_scores(const kda_moe_args& a, int64_t xs, bool xwide, Wide* score, uint64_t* key, int* done, cudaStream_t s) {
     const bf16* x = static_cast<const bf16*>(a.x);
     const Tr* r = static_cast<const Tr*>(a.router);
     const bool rwide = reinterpret_cast<uintptr_t>(r) % 16 == 0;
-    const int blocks = (a.E + kScoreWarps - 1) / kScoreWarps, sg = a.score == KDA_SCORE_SIGMOID;
+    const int sg = a.score == KDA_SCORE_SIGMOID;
     if (a.M == 1)
-        k_moe_scores<Tr, 1><<<dim3(blocks, 1), kScoreThreads, 0, s>>>(x, xs, wide, r, rwide, a.bias, a.M, a.E, a.D, sg, score, key);
+        k_moe_scores<Tr, 1><<<dim3(a.E, 1), kScoreThreads, 0, s>>>(x, xs, xwide, r, rwide, a.bias, a.M, a.E, a.D, sg, score, key, done);
     else
-        k_moe_scores<Tr, 4><<<dim3(blocks, (a.M + 3) / 4), kScoreThreads, 0, s>>>(x, xs, wide, r, rwide, a.bias, a.M, a.E, a.D, sg, score, key);
+        k_moe_scores<Tr, 4><<<dim3(a.E, (a.M + 3) / 4), kScoreThreads, 0, s>>>(x, xs, xwide, r, rwide, a.bias, a.M, a.E, a.D, sg, score, key, done);
     return cudaGetLastError();
 }
 
@@ -364,6 +392,7 @@ MoePlan moe_plan(const kda_moe_args& a) {
     };
     p.score = take((size_t)a.M * a.E * 8);
     p.key = take((size_t)a.M * a.E * 8);
+    p.done = take(4);
     p.ids = take(slots * 4);
     p.weights = take(slots * 4);
     p.lists = take((2 + 2 * (size_t)a.E + slots) * 4);
@@ -375,7 +404,7 @@ MoePlan moe_plan(const kda_moe_args& a) {
 
 cudaError_t launch_moe(const kda_moe_args& a, const MoePlan& p, cudaStream_t s) {
     char* ws = static_cast<char*>(a.workspace);
-    double* score = reinterpret_cast<double*>(ws + p.score);
+    Wide* score = reinterpret_cast<Wide*>(ws + p.score);
     uint64_t* key = reinterpret_cast<uint64_t*>(ws + p.key);
     int* ids = reinterpret_cast<int*>(ws + p.ids);
     float* weights = reinterpret_cast<float*>(ws + p.weights);
@@ -383,13 +412,13 @@ cudaError_t launch_moe(const kda_moe_args& a, const MoePlan& p, cudaStream_t s) 
     float* hidden = reinterpret_cast<float*>(ws + p.hidden);
     float* parts = reinterpret_cast<float*>(ws + p.parts);
     const int64_t xs = a.x_stride ? a.x_stride : a.D, ys = a.y_stride ? a.y_stride : a.D;
-    const bool wide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (xs % 8 == 0 || a.M == 1);
-    cudaError_t e = a.router_dtype == KDA_BF16 ? launch_scores<bf16>(a, xs, wide, score, key, s)
-                                               : launch_scores<float>(a, xs, wide, score, key, s);
+    const bool xwide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (xs % 8 == 0 || a.M == 1);
+    int* done = reinterpret_cast<int*>(ws + p.done);
+    cudaError_t e = a.router_dtype == KDA_BF16 ? launch_scores<bf16>(a, xs, xwide, score, key, done, s)
+                                               : launch_scores<float>(a, xs, xwide, score, key, done, s);
     if (e) return e;
-    const int sg = a.score == KDA_SCORE_SIGMOID;
-    const auto pick = a.E <= 256 ? k_moe_pick<8> : a.E <= 512 ? k_moe_pick<16> : k_moe_pick<32>;
-    pick<<<1, kPickThreads, 0, s>>>(score, key, a.M, a.E, a.top, sg, a.scale, ids, weights, lists, a.ids, a.weights);
+    k_moe_pick<<<a.M, kPickThreads, 0, s>>>(score, key, a.M, a.E, a.top, a.score == KDA_SCORE_SIGMOID, a.scale, ids, weights, done, lists,
+                                            a.ids, a.weights);
     if ((e = cudaGetLastError())) return e;
 
     const int slots = a.M * a.top, most = slots < a.E ? slots : a.E;
@@ -409,7 +438,7 @@ cudaError_t launch_moe(const kda_moe_args& a, const MoePlan& p, cudaStream_t s) 
     out.ranks = cluster_ranks(likely * ((a.D + kTileRows - 1) / kTileRows), a.F);
     // columns for twice an expert's even share of the slots, and no more than there are tokens
     const int even = 2 * ((slots + a.E - 1) / a.E) + 2, columns = a.M < even ? a.M : even;
-    const Bf16Rows src{static_cast<const bf16*>(a.x), xs, wide};
+    const Bf16Rows src{static_cast<const bf16*>(a.x), xs, xwide};
     if (a.format == KDA_WEIGHT_E2M1)
         e = launch_width<KDA_WEIGHT_E2M1>(columns, a, in, out, src, hidden, weights, parts, most, s);
     else if (a.format == KDA_WEIGHT_INT4)

@@ -1,19 +1,19 @@
 // kda_verify.cu -- which drafted tokens stand, and the token that follows them.
 //
-// Rows i of a sequence: draft i is taken while u_i q_i(d_i) < p_i(d_i), as products of fp32 in fp64, which
-// are exact; the first that is not stops the sequence at row a.  The new token is drawn from the residual
+// Rows i of a sequence: draft i is taken while u_i q_i(d_i) < p_i(d_i), compared without rounding the
+// product; the first that is not stops the sequence at row a.  The new token is drawn from the residual
 //   r = max(p_a - q_a, 0)      (q a single 1 at d_a for a drafter that proposes its best token only)
 // or, when every draft stands, from p of the last row, with the last row's u: the first token whose running
 // sum is above u times the sum of all.  Without anything left in r, p_a itself is drawn from.
 //
 // Bound by the one pair of rows per sequence that is read: N V 8 bytes.  The sums decide which token comes out, so
-// they are kept in two fp32 (value and rounding; fp64 at its rate here would take longer than the read), and
-// every 2,048 tokens leave one sum in shared memory: the pass over the row happens once, and only the
-// block of 2,048 that holds the threshold is read again, token by token, in fp64.  The CTAs of a cluster
-// share a row where there are few sequences.
+// they are kept in pairs of fp32 (kda_wide.cuh).  Every 1,024 tokens leave one sum in shared memory: the pass over the
+// row happens once, and only the run of 1,024 that holds the threshold is read again.  The CTAs of a cluster share a
+// row.
 #include <cooperative_groups.h>
 
 #include "kda_serve.cuh"
+#include "kda_wide.cuh"
 
 namespace kda {
 
@@ -21,41 +21,38 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512, kWarps = 16;
-constexpr int kTile = 2048;        // tokens per sum
-constexpr int kMaxTiles = 2048;    // of one CTA
+constexpr int kTile = 1024;        // tokens per sum
+constexpr int kMaxTiles = 4096;    // of one CTA
+constexpr int kEnough = 2;         // CTAs per SM that a row is shared for
+constexpr unsigned kAll = 0xffffffffu;
 
-struct Sum2 {  // fp32 value and what its roundings lost
-    float hi = 0.f, lo = 0.f;
-    __device__ __forceinline__ void add(float v) {
-        const float s = hi + v, b = s - hi;
-        lo += (hi - (s - b)) + (v - b);
-        hi = s;
-    }
-    __device__ __forceinline__ double value() const { return isfinite(hi) ? (double)hi + (double)lo : (double)hi; }
-};
+// s += p - q where that is positive (neither is negative).
+__device__ __forceinline__ void add_rest(Sum2& s, float p, float q) {
+    const float m = fmaxf(p, q), v = m - q;
+    s.lo += (m - v) - q;
+    s.add(v);
+}
 
 template <typename T> struct Pack { static constexpr int width = 16 / sizeof(T); };
 
-// `width` probabilities from element i of a row (i - first element of an aligned 16 bytes when wide), zeros
-// outside the row; NaN and negative values count as 0.
-template <typename T> __device__ __forceinline__ void load_row(const T* row, int64_t i, int V, bool wide, float (&v)[Pack<T>::width]) {
-    constexpr int W = Pack<T>::width;
-    if (wide && i >= 0 && i + W <= V) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + i));
+// 16 bytes as probabilities; NaN and negative values count as 0.
+template <typename T> __device__ __forceinline__ void unpack16(const uint4& r, float (&v)[Pack<T>::width]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
         if constexpr (sizeof(T) == 4) {
-            v[0] = __uint_as_float(q.x), v[1] = __uint_as_float(q.y), v[2] = __uint_as_float(q.z), v[3] = __uint_as_float(q.w);
+            v[j] = fmaxf(__uint_as_float(w[j]), 0.f);
         } else {
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[2 * j] = __uint_as_float(w[j] << 16), v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            v[2 * j] = fmaxf(__uint_as_float(w[j] << 16), 0.f);
+            v[2 * j + 1] = fmaxf(__uint_as_float(w[j] & 0xffff0000u), 0.f);
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < W; ++j) v[j] = i + j >= 0 && i + j < V ? to_f(row[i + j]) : 0.f;
     }
+}
+
+// The same of elements i and on, zeros outside the row.
+template <typename T> __device__ __forceinline__ void load_edge(const T* row, int64_t i, int V, float (&v)[Pack<T>::width]) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) v[j] = v[j] > 0.f ? v[j] : 0.f;
+    for (int j = 0; j < Pack<T>::width; ++j) v[j] = i + j >= 0 && i + j < V ? fmaxf(to_f(row[i + j]), 0.f) : 0.f;
 }
 
 struct Verify {
@@ -78,25 +75,96 @@ template <typename T> struct Rest {
     int kind, hole, V;
     bool wide;
     int shift;  // elements between the row's start and the 16-byte boundary in front of it
-    __device__ __forceinline__ void at(int64_t i, float (&v)[Pack<T>::width], float (&q_)[Pack<T>::width]) const {
-        load_row(p, i, V, wide, v);
-        if (kind == 1) {
-            load_row(q, i, V, wide, q_);
-        } else {
+    // Adds `Steps` accesses of W tokens, `stride` apart, to a sum.  Where all of [from, to) is inside the row the loads
+    // stand in front of the sums, without a branch between them, and are on their way together.
+    template <int Steps, int Unroll> __device__ __forceinline__ void sum(Sum2& s, int64_t i, int stride, int64_t from, int64_t to) const {
+        constexpr int W = Pack<T>::width;
+        if (wide && !(kind == 2 && hole >= from && hole < to) && from >= 0 && to <= V) {
+            for (int k0 = 0; k0 < Steps; k0 += Unroll) {
+                uint4 pr[Unroll], qr[Unroll];
 #pragma unroll
-            for (int j = 0; j < Pack<T>::width; ++j) {
-                q_[j] = 0.f;
-                if (kind == 2 && i + j == hole) v[j] = 0.f;
+                for (int k = 0; k < Unroll; ++k) pr[k] = __ldg(reinterpret_cast<const uint4*>(p + i + (k0 + k) * stride));
+                if (kind == 1) {
+#pragma unroll
+                    for (int k = 0; k < Unroll; ++k) qr[k] = __ldg(reinterpret_cast<const uint4*>(q + i + (k0 + k) * stride));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < Unroll; ++k) qr[k] = make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int k = 0; k < Unroll; ++k) {
+                    float pv[W], qv[W];
+                    unpack16<T>(pr[k], pv);
+                    unpack16<T>(qr[k], qv);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) add_rest(s, pv[j], qv[j]);
+                }
+            }
+        } else {
+#pragma unroll 4
+            for (int k = 0; k < Steps; ++k) {
+                float pv[W], qv[W];
+                const int64_t at = i + k * stride;
+                load_edge(p, at, V, pv);
+                if (kind == 1) {
+                    load_edge(q, at, V, qv);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) {
+                        qv[j] = 0.f;
+                        if (kind == 2 && at + j == hole) pv[j] = 0.f;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < W; ++j) add_rest(s, pv[j], qv[j]);
             }
         }
     }
+    __device__ __forceinline__ Wide one(int64_t i) const {  // of one token
+        if (i < 0 || i >= V || (kind == 2 && i == hole)) return Wide{};
+        Sum2 s;
+        add_rest(s, fmaxf(to_f(p[i]), 0.f), kind == 1 ? fmaxf(to_f(q[i]), 0.f) : 0.f);
+        return kda::wide(s);
+    }
 };
 
-template <typename T, typename Tok> __global__ void __launch_bounds__(kThreads, 2) k_verify(const Verify a) {
-    constexpr int W = Pack<T>::width, kSteps = kTile / (32 * W);
-    __shared__ double tile_sum[kMaxTiles];
-    __shared__ double total_here, before_tile;
-    __shared__ int stop_at, found_tile, found;
+// Running sums of the lanes' values, this lane's own included.
+__device__ __forceinline__ Wide running(Wide v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Wide w{__shfl_up_sync(kAll, v.hi, o), __shfl_up_sync(kAll, v.lo, o)};
+        if (lane >= o) v = add(w, v);
+    }
+    return v;
+}
+
+// The sum in front of a lane.
+__device__ __forceinline__ Wide in_front(Wide end, int lane) {
+    const Wide w{__shfl_up_sync(kAll, end.hi, 1), __shfl_up_sync(kAll, end.lo, 1)};
+    return lane ? w : Wide{};
+}
+
+// The first lane whose part is above 0 and ends above the threshold; rounding may leave none: then the last lane
+// with a part.  -1: no lane has one.
+__device__ __forceinline__ int holder(Wide part, Wide end, Wide threshold) {
+    const unsigned past = __ballot_sync(kAll, part.hi > 0.f && above(end, threshold)), with = __ballot_sync(kAll, part.hi > 0.f);
+    return past ? __ffs(past) - 1 : 31 - __clz(with);
+}
+
+// u q < p without rounding the product (the smallest values scaled up, so that its lower half does not vanish).
+__device__ __forceinline__ bool takes(float u, float q, float p) {
+    if (p < 0x1p-60f) p *= 0x1p64f, q *= 0x1p64f;
+    const float v = u * q;
+    return v < p || (v == p && fmaf(u, q, -v) < 0.f);
+}
+
+// Few sequences: 512 threads and a whole tile on its way per warp, for the shortest chain of latencies.  Many: 256
+// threads, three CTAs per SM, so that one's start and search run beside the others' reads.
+template <typename T, typename Tok, int kThreads> __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 1 : 3) k_verify(const Verify a) {
+    constexpr int W = Pack<T>::width, kSteps = kTile / (32 * W), kWarps = kThreads / 32, kUnroll = kThreads == 512 && kSteps == 8 ? 8 : 4;
+    __shared__ Wide tile_sum[kMaxTiles];
+    __shared__ Wide total_here;
+    __shared__ int stop_at, s_owner, found;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n = blockIdx.x / a.ranks, rank = blockIdx.x % a.ranks;
     const int64_t first = a.cu[n], last = a.cu[n + 1] - 1;
@@ -113,9 +181,8 @@ template <typename T, typename Tok> __global__ void __launch_bounds__(kThreads, 
         const int64_t d = (int64_t)tokens[i];
         bool take = false;
         if (d >= 0 && d < a.V) {  // no other token is ever proposed
-            const double p = (double)to_f(target[i * a.target_stride + d]);
-            const double q = draft ? (double)to_f(draft[i * a.draft_stride + d]) : 1.0;
-            take = (double)a.u[i] * q < p;
+            const float p = to_f(target[i * a.target_stride + d]);
+            take = takes(a.u[i], draft ? to_f(draft[i * a.draft_stride + d]) : 1.f, p);
         }
         if (!take) atomicMin(&stop_at, (int)(i - first));
     }
@@ -133,145 +200,96 @@ template <typename T, typename Tok> __global__ void __launch_bounds__(kThreads, 
     rest.shift = rest.wide ? (int)(mis / sizeof(T)) : 0;
 
     const int tiles = (a.V + rest.shift + kTile - 1) / kTile;
-    const int t0 = (int)((int64_t)tiles * rank / a.ranks), t1 = (int)((int64_t)tiles * (rank + 1) / a.ranks);
+    const int t0 = (int)((int64_t)tiles * rank / a.ranks), t1 = (int)((int64_t)tiles * (rank + 1) / a.ranks), own = t1 - t0;
     cg::cluster_group cluster = cg::this_cluster();
-    double before = 0.0, threshold = 0.0;
-    int owner = -1;
+    const int per = (own + 31) / 32, l0 = min(lane * per, own), l1 = min(l0 + per, own);  // tiles of a lane of warp 0
+    Wide before, threshold, part, end;
     for (;;) {
         for (int t = t0 + warp; t < t1; t += kWarps) {
             Sum2 s;
-#pragma unroll 4
-            for (int k = 0; k < kSteps; ++k) {
-                float p[W], q[W];
-                rest.at((int64_t)t * kTile + (k * 32 + lane) * W - rest.shift, p, q);
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    const float v = p[j] - q[j];
-                    if (v > 0.f) {
-                        s.lo += (p[j] - v) - q[j];
-                        s.add(v);
-                    }
-                }
-            }
+            const int64_t at = (int64_t)t * kTile - rest.shift;
+            rest.template sum<kSteps, kUnroll>(s, at + lane * W, 32 * W, at, at + kTile);
 #pragma unroll
             for (int o = 16; o; o >>= 1) {
-                const float h = __shfl_xor_sync(0xffffffffu, s.hi, o), l = __shfl_xor_sync(0xffffffffu, s.lo, o);
+                const float h = __shfl_xor_sync(kAll, s.hi, o), l = __shfl_xor_sync(kAll, s.lo, o);
                 s.add(h);
                 s.lo += l;
             }
-            if (lane == 0) tile_sum[t - t0] = s.value();
+            if (lane == 0) tile_sum[t - t0] = wide(s);
         }
         __syncthreads();
         if (warp == 0) {
-            double s = 0.0;
-            for (int t = lane; t < t1 - t0; t += 32) s += tile_sum[t];
-#pragma unroll
-            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (lane == 0) total_here = s;
+            part = Wide{};
+            for (int t = l0; t < l1; ++t) part = add(part, tile_sum[t]);
+            end = running(part, lane);
+            if (lane == 31) total_here = end;
         }
         if (a.ranks > 1) cluster.sync(); else __syncthreads();
-        double total = 0.0, sums[8];
-        for (int r = 0; r < a.ranks; ++r) {
-            sums[r] = a.ranks > 1 ? *cluster.map_shared_rank(&total_here, r) : total_here;
-            total += sums[r];
-        }
-        threshold = (double)a.u[last] * total;
-        before = 0.0;
-        owner = -1;
-        int last_with = -1;
-        double run = 0.0;
-        for (int r = 0; r < a.ranks; ++r) {
-            if (sums[r] > 0.0) {
-                last_with = r;
-                if (owner < 0 && run + sums[r] > threshold) owner = r, before = run;
-            }
-            run += sums[r];
-        }
-        if (owner < 0 && last_with >= 0) {  // rounding, or a sum that is not finite: the last part that holds anything
-            owner = last_with;
-            before = threshold;
+        if (warp == 0) {
+            Wide total;
+            if (lane < a.ranks) total = a.ranks > 1 ? *cluster.map_shared_rank(&total_here, lane) : total_here;
+            const Wide upto = running(total, lane);
+            threshold = times(Wide{a.u[last], 0.f}, from(kAll, upto, 31));
+            const int owner = holder(total, upto, threshold);
+            before = from(kAll, in_front(upto, lane), owner < 0 ? 0 : owner);
+            if (lane == 0) s_owner = owner;
         }
         if (a.ranks > 1) cluster.sync(); else __syncthreads();
-        if (owner >= 0 || rest.kind == 0) break;
+        if (s_owner >= 0 || rest.kind == 0) break;
         rest.kind = 0;  // nothing is left of the residual: p itself
     }
-    if (owner < 0 ? rank == 0 : rank == owner) {
-        if (threadIdx.x == 0) {
-            found = -1;
-            found_tile = -1;
-            double run = before;
-            int last_with = -1;
-            for (int t = 0; t < t1 - t0 && owner >= 0; ++t) {
-                if (!(tile_sum[t] > 0.0)) continue;
-                last_with = t;
-                if (run + tile_sum[t] > threshold) {
-                    found_tile = t;
-                    before_tile = run;
-                    break;
+    const int owner = s_owner;
+    if (owner < 0 ? rank != 0 : rank != owner) return;
+    if (warp == 0) {
+        int pick = -1;
+        if (owner >= 0) {
+            // the lane's tiles, then the tile, then the lane's share of it, then the token
+            end = add(before, end);
+            int src = holder(part, end, threshold), tile = 0;
+            Wide at = in_front(end, lane);
+            if (lane == 0) at = before;
+            if (lane == src) {
+                int left = 0;  // the lane's tiles that hold anything
+                for (int t = l0; t < l1; ++t) left += tile_sum[t].hi > 0.f;
+                for (int t = l0; t < l1; ++t) {
+                    if (!(tile_sum[t].hi > 0.f)) continue;
+                    tile = t;
+                    const Wide to = add(at, tile_sum[t]);
+                    if (above(to, threshold) || --left == 0) break;
+                    at = to;
                 }
-                run += tile_sum[t];
             }
-            if (found_tile < 0 && last_with >= 0) {
-                found_tile = last_with;
-                before_tile = run - tile_sum[last_with];
-            }
+            tile = __shfl_sync(kAll, tile, src);
+            at = from(kAll, at, src);
+            constexpr int kShare = kTile / 32;
+            const int64_t base = (int64_t)(t0 + tile) * kTile - rest.shift;
+            Sum2 s;
+            rest.template sum<kShare / W, 4>(s, base + lane * kShare, W, base, base + kTile);
+            part = wide(s);
+            end = add(at, running(part, lane));
+            src = holder(part, end, threshold);
+            const Wide front = in_front(end, lane);
+            at = from(kAll, lane ? front : at, src);
+            const int64_t token = base + src * kShare + lane;  // kShare is 32
+            part = rest.one(token);
+            end = add(at, running(part, lane));
+            src = holder(part, end, threshold);
+            pick = (int)__shfl_sync(kAll, token, src);
         }
-        __syncthreads();
-        if (warp == 0 && found_tile >= 0) {
-            // a lane takes kTile / 32 tokens in a row; the first lane whose running sum passes the threshold holds the token
-            const int64_t base = (int64_t)(t0 + found_tile) * kTile + lane * (kTile / 32) - rest.shift;
-            double s = 0.0;
-            for (int k = 0; k < kTile / 32 / W; ++k) {
-                float p[W], q[W];
-                rest.at(base + k * W, p, q);
-#pragma unroll
-                for (int j = 0; j < W; ++j)
-                    if (p[j] > q[j]) s += (double)p[j] - (double)q[j];
-            }
-            double run = s;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double v = __shfl_up_sync(0xffffffffu, run, o);
-                if (lane >= o) run += v;
-            }
-            const double upto = before_tile + (run - s);
-            const unsigned over = __ballot_sync(0xffffffffu, s > 0.0 && before_tile + run > threshold);
-            const unsigned with = __ballot_sync(0xffffffffu, s > 0.0);
-            const int holder = over ? __ffs(over) - 1 : 31 - __clz(with | 1u);
-            if (lane == holder) {
-                double sum = upto;
-                int pick = -1;
-                bool done = false;
-                for (int k = 0; k < kTile / 32 / W && !done; ++k) {
-                    float p[W], q[W];
-                    rest.at(base + k * W, p, q);
-#pragma unroll
-                    for (int j = 0; j < W; ++j) {
-                        if (done || !(p[j] > q[j])) continue;
-                        sum += (double)p[j] - (double)q[j];
-                        pick = (int)(base + k * W + j);  // the last one with a share, should rounding leave the threshold above all
-                        done = sum > threshold;
-                    }
-                }
-                found = pick;
-            }
-        }
-        __syncthreads();
-        Tok* out = static_cast<Tok*>(a.out);
-        for (int64_t i = first + threadIdx.x; i <= last; i += kThreads) out[i] = i < row ? tokens[i] : i == row ? (Tok)found : (Tok)-1;
-        if (threadIdx.x == 0) a.accepted[n] = stop_at;
+        if (lane == 0) found = pick;
     }
+    __syncthreads();
+    Tok* out = static_cast<Tok*>(a.out);
+    for (int64_t i = first + threadIdx.x; i <= last; i += kThreads) out[i] = i < row ? tokens[i] : i == row ? (Tok)found : (Tok)-1;
+    if (threadIdx.x == 0) a.accepted[n] = stop_at;
 }
 
-template <typename T, typename Tok> cudaError_t launch(const kda_verify_args& a, cudaStream_t s) {
+template <typename T, typename Tok, int kThreads> cudaError_t launch_threads(const kda_verify_args& a, int ranks, cudaStream_t s) {
     Verify p;
     p.target = a.target, p.target_stride = a.target_stride ? a.target_stride : a.V;
     p.draft = a.draft, p.draft_stride = a.draft_stride ? a.draft_stride : a.V;
     p.tokens = a.tokens, p.u = a.u, p.cu = a.cu_seqlens;
     p.N = a.N, p.V = a.V, p.T_total = a.T_total, p.out = a.out, p.accepted = a.accepted;
-    // CTAs for about two per SM, and at least a tile per warp
-    int ranks = 1;
-    while (ranks < 8 && (int64_t)a.N * ranks < 2 * 152 && a.V / kTile >= 2 * ranks * kWarps / 4) ranks *= 2;
     p.ranks = ranks;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -283,7 +301,13 @@ template <typename T, typename Tok> cudaError_t launch(const kda_verify_args& a,
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = ranks > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_verify<T, Tok>, p);
+    return cudaLaunchKernelEx(&cfg, k_verify<T, Tok, kThreads>, p);
+}
+
+template <typename T, typename Tok> cudaError_t launch(const kda_verify_args& a, cudaStream_t s) {
+    int ranks = 1;
+    while (ranks < 8 && (int64_t)a.N * ranks < kEnough * 152 && a.V / kTile >= 2 * ranks) ranks *= 2;
+    return (int64_t)a.N * ranks <= 152 ? launch_threads<T, Tok, 512>(a, ranks, s) : launch_threads<T, Tok, 256>(a, ranks, s);
 }
 
 }  // namespace
