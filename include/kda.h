@@ -718,8 +718,12 @@ typedef struct {
     int64_t ldc;
     kda_dtype c_dtype;
     int epilogue;
+    void* workspace;       /* kda_gemm4_workspace_size bytes, 256-byte aligned; for this call alone */
+    size_t workspace_bytes;
+    int* d_status;         /* optional device int for device-side conditions */
 } kda_gemm4_args;
 
+kda_status kda_gemm4_workspace_size(const kda_gemm4_args* args, size_t* bytes);
 kda_status kda_gemm4(const kda_gemm4_args* args, kda_stream_t stream);
 
 /* kda_moe -- a mixture-of-experts layer for few tokens.
@@ -760,6 +764,7 @@ typedef struct {
     float* weights;
     void* workspace;       /* kda_moe_workspace_size bytes, 256-byte aligned; for this call alone */
     size_t workspace_bytes;
+    int* d_status;         /* optional device int for device-side conditions */
 } kda_moe_args;
 
 kda_status kda_moe_workspace_size(const kda_moe_args* args, size_t* bytes);

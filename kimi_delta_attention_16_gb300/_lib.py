@@ -39,7 +39,7 @@ EXPORTED = ("kda_status_string", "kda_last_error", "kda_version", "kda_short_con
             "kda_pack8", "kda_unpack8", "kda_ssm_conv", "kda_ssm_conv_step",
             "kda_ssm_conv_backward_workspace_size", "kda_ssm_conv_backward", "kda_ssm_scan_workspace_size",
             "kda_ssm_scan", "kda_ssm_step", "kda_ssm_backward_workspace_size", "kda_ssm_backward",
-            "kda_pack4", "kda_unpack4", "kda_gemm4", "kda_moe_workspace_size", "kda_moe", "kda_verify")
+            "kda_pack4", "kda_unpack4", "kda_gemm4_workspace_size", "kda_gemm4", "kda_moe_workspace_size", "kda_moe", "kda_verify")
 NOALLOC_SCRATCH_BYTES = 64 << 20  # KDA_NOALLOC_SCRATCH_BYTES in include/kda.h
 
 _vp = ctypes.c_void_p
@@ -170,6 +170,7 @@ class Gemm4Args(ctypes.Structure):
     _fields_ = [
         ("M", _int), ("N", _int), ("K", _int), ("A", _vp), ("lda", _i64), ("format", _int), ("group", _int),
         ("scale_dtype", _int), ("codes", _vp), ("scales", _vp), ("C", _vp), ("ldc", _i64), ("c_dtype", _int), ("epilogue", _int),
+        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("d_status", _vp),
     ]
 
 
@@ -180,7 +181,7 @@ class MoeArgs(ctypes.Structure):
         ("router_dtype", _int), ("bias", _vp), ("score", _int), ("scale", _f), ("format", _int), ("group", _int),
         ("scale_dtype", _int), ("w_in", _vp), ("w_in_scales", _vp), ("w_out", _vp), ("w_out_scales", _vp), ("y", _vp),
         ("y_stride", _i64), ("y_dtype", _int), ("ids", _vp), ("weights", _vp), ("workspace", _vp),
-        ("workspace_bytes", ctypes.c_size_t),
+        ("workspace_bytes", ctypes.c_size_t), ("d_status", _vp),
     ]
 
 
@@ -255,7 +256,8 @@ def load(auto_build: bool = True) -> ctypes.CDLL:
                      "kda_unpack4", "kda_gemm4", "kda_moe", "kda_verify"):
             f = getattr(lib, name)
             f.restype, f.argtypes = _int, [_vp, _vp]
-        for name in ("kda_layer_norm_backward", "kda_ssm_conv_backward", "kda_ssm_scan", "kda_ssm_backward", "kda_moe"):
+        for name in ("kda_layer_norm_backward", "kda_ssm_conv_backward", "kda_ssm_scan", "kda_ssm_backward", "kda_moe",
+                     "kda_gemm4"):
             f = getattr(lib, name + "_workspace_size")
             f.restype, f.argtypes = _int, [_vp, _vp]
         lib.kda_pack8.restype = _int

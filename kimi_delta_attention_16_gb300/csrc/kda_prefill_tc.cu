@@ -1375,18 +1375,23 @@ cudaError_t tc_launch(const kda_prefill_args& a, const SegPlan& sp, cudaStream_t
 
 }  // namespace
 
-bool encode_tensor_map_2d(CUtensorMap* m, const void* base, bool fp32, uint64_t cols, uint64_t rows,
-                          uint64_t row_bytes, uint32_t box_c, uint32_t box_r, bool swizzle128) {
+bool encode_tensor_map_2d_as(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t cols, uint64_t rows,
+                             uint64_t row_bytes, uint32_t box_c, uint32_t box_r, bool swizzle128) {
     const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t dims[2] = {cols, rows};
     const cuuint64_t strides[1] = {row_bytes};
     const cuuint32_t box[2] = {box_c, box_r};
     const cuuint32_t es[2] = {1, 1};
-    return enc(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
-               dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    return enc(m, type, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_tensor_map_2d(CUtensorMap* m, const void* base, bool fp32, uint64_t cols, uint64_t rows,
+                          uint64_t row_bytes, uint32_t box_c, uint32_t box_r, bool swizzle128) {
+    return encode_tensor_map_2d_as(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, cols,
+                                   rows, row_bytes, box_c, box_r, swizzle128);
 }
 
 bool tc_prefill_applies(const kda_prefill_args& a) {

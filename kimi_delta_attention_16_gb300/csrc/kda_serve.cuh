@@ -8,6 +8,7 @@ namespace kda {
 
 cudaError_t launch_pack4(const kda_pack4_args& a, cudaStream_t s);
 cudaError_t launch_unpack4(const kda_pack4_args& a, cudaStream_t s);
+size_t gemm4_workspace(const kda_gemm4_args& a);
 cudaError_t launch_gemm4(const kda_gemm4_args& a, cudaStream_t s);
 
 // Parts of kda_moe's workspace, as byte offsets.

@@ -91,6 +91,26 @@ kda_status check_pack4(const kda_pack4_args* a) {
     return check_overlaps(all, none);
 }
 
+kda_status check_gemm4(const kda_gemm4_args* a) {
+    if (!a) return fail(KDA_ERR_INVALID_ARG, "args is NULL");
+    if (a->M < 0 || a->N < 0 || a->K < 1) return fail(KDA_ERR_INVALID_ARG, "bad sizes M=%d N=%d K=%d", a->M, a->N, a->K);
+    if (a->M > 4000000 || a->N > 1 << 24 || a->K > 1 << 24)
+        return fail(KDA_ERR_UNSUPPORTED, "M=%d above 4,000,000, or N=%d or K=%d above 2^24", a->M, a->N, a->K);
+    kda_status st;
+    if ((st = check_format(a->format, a->group, a->scale_dtype, a->K, false, "K"))) return st;
+    if (!valid_dtype(a->c_dtype)) return fail(KDA_ERR_INVALID_ARG, "unknown dtype %d", (int)a->c_dtype);
+    if (a->epilogue < KDA_EPI_NONE || a->epilogue > KDA_EPI_SIGMOID) return fail(KDA_ERR_INVALID_ARG, "unknown epilogue %d", a->epilogue);
+    return KDA_OK;
+}
+
+kda_status check_workspace(const void* ws, size_t have, size_t need) {
+    if (need == 0) return KDA_OK;
+    if (!ws) return fail(KDA_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", need);
+    if (have < need) return fail(KDA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", have, need);
+    if (!aligned(ws, 256)) return fail(KDA_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+    return KDA_OK;
+}
+
 kda_status check_moe(const kda_moe_args* a) {
     if (!a) return fail(KDA_ERR_INVALID_ARG, "args is NULL");
     if (a->M < 0 || a->E < 1 || a->D < 1 || a->F < 1)
@@ -126,21 +146,25 @@ kda_status kda_unpack4(const kda_pack4_args* a, kda_stream_t stream) {
     return ok();
 }
 
+kda_status kda_gemm4_workspace_size(const kda_gemm4_args* a, size_t* bytes) {
+    if (!bytes) return fail(KDA_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = 0;
+    if (kda_status st = check_gemm4(a)) return st;
+    *bytes = a->N ? gemm4_workspace(*a) : 0;
+    return ok();
+}
+
 kda_status kda_gemm4(const kda_gemm4_args* a, kda_stream_t stream) {
-    if (!a) return fail(KDA_ERR_INVALID_ARG, "args is NULL");
-    if (a->M < 0 || a->N < 0 || a->K < 1) return fail(KDA_ERR_INVALID_ARG, "bad sizes M=%d N=%d K=%d", a->M, a->N, a->K);
-    if (a->M > 4000000 || a->N > 1 << 24 || a->K > 1 << 24)
-        return fail(KDA_ERR_UNSUPPORTED, "M=%d above 4,000,000, or N=%d or K=%d above 2^24", a->M, a->N, a->K);
     kda_status st;
-    if ((st = check_format(a->format, a->group, a->scale_dtype, a->K, false, "K"))) return st;
-    if (!valid_dtype(a->c_dtype)) return fail(KDA_ERR_INVALID_ARG, "unknown dtype %d", (int)a->c_dtype);
-    if (a->epilogue < KDA_EPI_NONE || a->epilogue > KDA_EPI_SIGMOID) return fail(KDA_ERR_INVALID_ARG, "unknown epilogue %d", a->epilogue);
+    if ((st = check_gemm4(a))) return st;
     if (a->M == 0 || a->N == 0) return ok();
     if ((st = check_rows_of(a->A, a->M, a->lda, a->K, 2, "A")) ||
         (st = check_rows_of(a->C, a->M, a->ldc, a->N, dsize(a->c_dtype), "C")) ||
         (st = check_weight(a->codes, a->scales, a->format, a->scale_dtype, "codes")))
         return st;
-    const Span outs[] = {{a->C, rows_bytes(a->M, a->ldc, a->N, dsize(a->c_dtype)), "C"}};
+    const size_t ws = gemm4_workspace(*a);
+    if ((st = check_workspace(a->workspace, a->workspace_bytes, ws))) return st;
+    const Span outs[] = {{a->C, rows_bytes(a->M, a->ldc, a->N, dsize(a->c_dtype)), "C"}, {a->workspace, ws, "workspace"}};
     const Span ins[] = {{a->A, rows_bytes(a->M, a->lda, a->K, 2), "A"}, {a->codes, weight_size(a->N, a->K, a->format), "codes"},
                         {a->scales, scales_size(a->N, a->K, a->format, a->group, a->scale_dtype), "scales"}};
     if ((st = check_overlaps(outs, ins))) return st;
@@ -170,10 +194,7 @@ kda_status kda_moe(const kda_moe_args* a, kda_stream_t stream) {
     if (!aligned(a->bias, 4) || !aligned(a->ids, 4) || !aligned(a->weights, 4))
         return fail(KDA_ERR_INVALID_ARG, "bias, ids or weights is not aligned to its element");
     const MoePlan p = moe_plan(*a);
-    if (!a->workspace) return fail(KDA_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", p.workspace);
-    if (a->workspace_bytes < p.workspace)
-        return fail(KDA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", a->workspace_bytes, p.workspace);
-    if (!aligned(a->workspace, 256)) return fail(KDA_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+    if ((st = check_workspace(a->workspace, a->workspace_bytes, p.workspace))) return st;
     const size_t slots = (size_t)a->M * a->top * 4;
     const int64_t in = (int64_t)a->E * 2 * a->F, out = (int64_t)a->E * a->D;
     const Span outs[] = {{a->y, rows_bytes(a->M, ys, a->D, dsize(a->y_dtype)), "y"}, {a->ids, slots, "ids"},

@@ -14,6 +14,10 @@ namespace kda {
 bool encode_tensor_map_2d(CUtensorMap* m, const void* base, bool fp32, uint64_t cols, uint64_t rows,
                           uint64_t row_bytes, uint32_t box_c, uint32_t box_r, bool swizzle128);
 
+// The same for elements of any type of tensor map (row_bytes: the pitch in memory).
+bool encode_tensor_map_2d_as(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t cols, uint64_t rows,
+                             uint64_t row_bytes, uint32_t box_c, uint32_t box_r, bool swizzle128);
+
 // True when the tensor-core path takes these arguments (D = 128, chunk = 64,
 // bf16 inputs) and this device supports it.
 bool tc_prefill_applies(const kda_prefill_args& a);

@@ -22,8 +22,8 @@ _SCORE = {"sigmoid": _lib.KDA_SCORE_SIGMOID, "softmax": _lib.KDA_SCORE_SOFTMAX}
 
 # the argument structs of include/kda.h, member by member
 _PACK4 = struct.Struct("@qiPqiiiiPP")
-_GEMM4 = struct.Struct("@iiiPqiiiPPPqii")
-_MOE = struct.Struct("@iiiiiPqPiPifiiiPPPPPqiPPPN")
+_GEMM4 = struct.Struct("@iiiPqiiiPPPqii PNP")
+_MOE = struct.Struct("@iiiiiPqPiPifiiiPPPPPqiPP PNP")
 _VERIFY = struct.Struct("@iqiiPqPqPiPPPPPP")
 
 Weight = Union[torch.Tensor, Tuple[torch.Tensor, torch.Tensor]]
@@ -92,13 +92,15 @@ def kda_unpack4(codes: torch.Tensor, scales: torch.Tensor, *, dtype=torch.bfloat
 
 
 def kda_gemm4(A: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, epilogue: str = "none",
-              out: Optional[torch.Tensor] = None, out_dtype=None, stream=None) -> torch.Tensor:
+              out: Optional[torch.Tensor] = None, out_dtype=None, workspace: Optional[torch.Tensor] = None, d_status=None,
+              stream=None) -> torch.Tensor:
     """C = epilogue(A @ W^T) for the few rows of a decode step: A [M, K] bf16 (rows may be strided), W [N, K] in 4 bits
     (codes [N, K / 2] and scales [N, K / group] as kda_pack4 returns them).  Epilogues and out_dtype as in kda_gemm; out
     [M, N] may have strided rows.  Products are exact and sums fp32, in a fixed order, rounded once."""
     if stream is not None:
-        with _on(stream, A, codes, scales, out):
-            return kda_gemm4(A, codes, scales, epilogue=epilogue, out=out, out_dtype=out_dtype)
+        with _on(stream, A, codes, scales, out, workspace, d_status):
+            return kda_gemm4(A, codes, scales, epilogue=epilogue, out=out, out_dtype=out_dtype, workspace=workspace,
+                             d_status=d_status)
     M, K = _shape2(A, "A")
     if codes.dim() != 2:
         raise ValueError(f"expected codes [N, K / 2], got {tuple(codes.shape)}")
@@ -109,20 +111,23 @@ def kda_gemm4(A: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, epi
     if epi is None:
         raise ValueError(f"epilogue is {epilogue!r}; expected one of {tuple(_EPI)}")
     N, lda = codes.shape[0], _rows(A, M, K, _BF16, "A")
-    index = _device(A, codes, scales, out)
+    index = _device(A, codes, scales, out, workspace, d_status)
+    dev = A.device
     if out is None:
         dt = out_dtype or (_BF16 if epi == _lib.KDA_EPI_NONE else _F32)
         if dt not in _DT:
             raise ValueError(f"out_dtype is {dt}; expected bfloat16 or float32")
-        out, ldc = torch.empty((M, N), dtype=dt, device=A.device), N
+        out, ldc = torch.empty((M, N), dtype=dt, device=dev), N
     else:
         if out_dtype is not None and out.dtype != out_dtype:
             raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
         _io(out, "out")
         ldc = _rows(out, M, N, out.dtype, "out")
-    a = _GEMM4.pack(M, N, K, A.data_ptr(), lda, fmt, group, sdt, codes.data_ptr(), scales.data_ptr(), out.data_ptr(), ldc,
-                    _DT[out.dtype], epi)
-    _check(_lib.load().kda_gemm4(a, _stream_of(index)), "kda_gemm4")
+    args = (M, N, K, A.data_ptr(), lda, fmt, group, sdt, codes.data_ptr(), scales.data_ptr(), out.data_ptr(), ldc,
+            _DT[out.dtype], epi)
+    st = _status(d_status)
+    p, n, keep = _workspace("kda_gemm4_workspace_size", index, (M, N, K, fmt, group), _GEMM4, args, (st,), workspace, dev)
+    _check(_lib.load().kda_gemm4(_GEMM4.pack(*args, p, n, st), _stream_of(index)), "kda_gemm4")
     return out
 
 
@@ -141,7 +146,7 @@ def _experts(w: Weight, rows: int, E: int, K: int, name: str):
 def kda_moe(x: torch.Tensor, router: torch.Tensor, w_in: Weight, w_out: Weight, top: int, *,
             bias: Optional[torch.Tensor] = None, score: str = "sigmoid", scale: float = 1.0,
             y: Optional[torch.Tensor] = None, out_dtype=None, return_routing: bool = False,
-            workspace: Optional[torch.Tensor] = None, stream=None):
+            workspace: Optional[torch.Tensor] = None, d_status=None, stream=None):
     """A mixture-of-experts layer for few tokens: x [M, D] bf16 (rows may be strided), router [E, D] bf16 or fp32.
     Each token takes the `top` experts with the largest score + bias (score "sigmoid" of its logits; bias [E] fp32 or
     None) or the largest logits ("softmax"), ties to the lower expert, weighted by their scores divided by the sum of
@@ -151,9 +156,9 @@ def kda_moe(x: torch.Tensor, router: torch.Tensor, w_in: Weight, w_out: Weight, 
     return_routing.  M * top is at most 65535, E 1024, top 32."""
     if stream is not None:
         pair = lambda w: (w,) if isinstance(w, torch.Tensor) else w  # noqa: E731
-        with _on(stream, x, router, *pair(w_in), *pair(w_out), bias, y, workspace):
+        with _on(stream, x, router, *pair(w_in), *pair(w_out), bias, y, workspace, d_status):
             return kda_moe(x, router, w_in, w_out, top, bias=bias, score=score, scale=scale, y=y, out_dtype=out_dtype,
-                           return_routing=return_routing, workspace=workspace)
+                           return_routing=return_routing, workspace=workspace, d_status=d_status)
     lib = _lib.load()
     M, D = _shape2(x, "x")
     E, _ = _shape2(router, "router")
@@ -172,7 +177,7 @@ def kda_moe(x: torch.Tensor, router: torch.Tensor, w_in: Weight, w_out: Weight, 
     rdt = _io(router, "router")
     r = _dense(router, (E, D), router.dtype, "router")
     b = _dense(bias, (E,), _F32, "bias")
-    index = _device(x, router, wi, si, wo, so, bias, y, workspace)
+    index = _device(x, router, wi, si, wo, so, bias, y, workspace, d_status)
     dev = x.device
     if y is None:
         dt = out_dtype or _BF16
@@ -188,9 +193,10 @@ def kda_moe(x: torch.Tensor, router: torch.Tensor, w_in: Weight, w_out: Weight, 
     weights = torch.empty((M, top), dtype=_F32, device=dev) if return_routing and top > 0 else None
     args = (M, E, top, D, F, x.data_ptr(), xs, r, rdt, b, mode, scale, fmt, group, sdt, wi.data_ptr(), _ptr(si), wo.data_ptr(),
             _ptr(so), y.data_ptr(), ys, _DT[y.dtype], _ptr(ids), _ptr(weights))
+    st = _status(d_status)
     p, n, keep = _workspace("kda_moe_workspace_size", index, (M, E, top, D, F, fmt, group, sdt, rdt, mode, b != 0), _MOE, args,
-                            (), workspace, dev)
-    _check(lib.kda_moe(_MOE.pack(*args, p, n), _stream_of(index)), "kda_moe")
+                            (st,), workspace, dev)
+    _check(lib.kda_moe(_MOE.pack(*args, p, n, st), _stream_of(index)), "kda_moe")
     return (y, ids, weights) if return_routing else y
 
 
