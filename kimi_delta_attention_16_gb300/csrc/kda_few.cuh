@@ -21,6 +21,8 @@
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
+#include <utility>
+
 #include "kda_internal.cuh"
 
 namespace kda {
@@ -130,6 +132,36 @@ __device__ __forceinline__ void run_scale(uint32_t exponent, float& up, float& d
     up = __uint_as_float(b << 23);
     const uint32_t d = 254u - b;
     down = __uint_as_float(d ? d << 23 : 0x00400000u);
+}
+
+// A kernel that was launched beside the one in front of it on the stream waits here until that one has ended, and with it
+// all before; the one in front lets it begin.  Without such a launch both do nothing.
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Launches a kernel in clusters of `ranks` along x, `beside` the kernel in front of it.
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, int threads, int ranks, int smem, bool beside, cudaStream_t s, A&&... args) {
+    if (smem > 48 * 1024)
+        if (const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
+    cudaLaunchAttribute at[2];
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = threads;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    if (beside) {
+        at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (ranks > 1) {
+        at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        at[cfg.numAttrs].val.clusterDim.x = ranks;
+        at[cfg.numAttrs].val.clusterDim.y = 1;
+        at[cfg.numAttrs++].val.clusterDim.z = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
 // Where the columns come from.  Bf16Rows: column c is row of[c] of a bf16 tensor.  F32Rows: columns

@@ -124,8 +124,8 @@ __device__ __forceinline__ int alignment(const uint8_t* p, int64_t pitch) {
 }
 __device__ __forceinline__ void scale_warps_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// Waits until the kernel before has written what this one reads (a launch that may begin beside it).
-__device__ __forceinline__ void wait_for_columns() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// A launch may begin beside the kernel in front of it (launch_beside); it waits for what that one writes, the columns.
+__device__ __forceinline__ void wait_for_columns() { few::wait_for_kernel_before(); }
 
 // Once per CTA, before the first product.
 template <int N> __device__ __forceinline__ void start(Barriers& bar) {
@@ -371,9 +371,33 @@ __device__ __forceinline__ void put_digits(float (&r)[8], uint32_t top, bool in,
     if (in && (k & 31) == 0) scales[(token * K + k) >> 5] = finite ? (uint8_t)byte : (uint8_t)255;
 }
 
+// The same with one value per lane, 32 in a row from element k - lane; `top` is their largest.
+__device__ __forceinline__ void put_digits_of_lanes(float v, uint32_t top, bool in, int64_t token, int k, int K, uint8_t* digits, uint8_t* scales) {
+    const bool finite = top < 0x7f800000u;
+    const int byte = max((int)((top + 0x7fffffu) >> 23) - 2, kLowestByte), lane = threadIdx.x & 31;
+    float r = finite ? v * __uint_as_float((uint32_t)(254 - byte) << 23) : 0.f;
+#pragma unroll
+    for (int t = 0; t < kDigits; ++t) {
+        const float d = rintf(r);
+        r = (r - d) * 8.f;
+        // 0, 1, 2, 3, 4 are the codes 0, 2, 4, 5, 6; bit 3 is the sign
+        const uint32_t code = (0x65420u >> (4 * (int)fabsf(d)) & 15u) | (d < 0.f ? 8u : 0u);
+        // eight lanes' codes in one word
+        uint32_t w = code << (4 * (lane & 7));
+        w |= __shfl_xor_sync(0xffffffffu, w, 1);
+        w |= __shfl_xor_sync(0xffffffffu, w, 2);
+        w |= __shfl_xor_sync(0xffffffffu, w, 4);
+        if (in && (lane & 7) == 0) *reinterpret_cast<uint32_t*>(digits + ((token * kDigits + t) * K + k) / 2) = w;
+    }
+    if (in && lane == 0) scales[(token * K + k) >> 5] = finite ? (uint8_t)byte : (uint8_t)255;
+}
+
 // Digits of bf16 rows: token p is row of[p] / per of x (p itself without `of`).
 cudaError_t launch_digits(const bf16* x, int64_t xs, bool wide, const int* of, int per, int tokens, int K, uint8_t* digits, uint8_t* scales,
                           cudaStream_t s);
+
+// The rows themselves, for bf16 weights.
+cudaError_t launch_rows(const bf16* x, int64_t xs, bool wide, const int* of, int per, int tokens, int K, bf16* rows, cudaStream_t s);
 
 // Bytes of the digits of so many values, and of their scales.
 inline size_t digits_bytes(int64_t tokens, int64_t K) { return (size_t)tokens * kDigits * K / 2; }
@@ -385,6 +409,12 @@ struct Maps {
 inline bool encode_maps(Maps* m, const void* codes, int64_t rows, const uint8_t* digits, int64_t tokens, int K, int box) {
     return encode_tensor_map_2d_as(&m->w, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, K / 2, rows, K / 2, kRowBytes, 64, true) &&
            encode_tensor_map_2d_as(&m->b, CU_TENSOR_MAP_DATA_TYPE_UINT8, digits, K / 2, tokens * kDigits, K / 2, kRowBytes, box, true);
+}
+
+// The same for bf16 weights and columns, in boxes of 64 elements.
+inline bool encode_maps_bf16(Maps* m, const void* w, int64_t rows, const void* columns, int64_t n, int K, int box) {
+    return encode_tensor_map_2d_as(&m->w, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, w, K, rows, 2 * (uint64_t)K, 64, 64, true) &&
+           encode_tensor_map_2d_as(&m->b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, columns, K, n, 2 * (uint64_t)K, 64, box, true);
 }
 
 // One product by itself, for a sum that came out as NaN: a row of x that digits do not hold (values that are not finite,

@@ -51,26 +51,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemm4(const Gemm4 p, Tout* __re
 
 template <int F, int NT, typename Tout> cudaError_t launch(const kda_gemm4_args& a, int ranks, cudaStream_t s) {
     using L = Layout<F, NT>;
-    const auto kernel = k_gemm4<F, NT, Tout>;
-    if (const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes)) return e;
     Gemm4 p;
     p.w = Matrix{a.codes, a.scales, a.format == KDA_WEIGHT_E2M1 ? 0 : a.scale_dtype == KDA_BF16 ? 1 : 2, group_shift(a.group)};
     p.M = a.M, p.N = a.N, p.K = a.K, p.epi = a.epilogue, p.ranks = ranks;
     p.a = static_cast<const bf16*>(a.A), p.lda = a.lda;
     p.wide = reinterpret_cast<uintptr_t>(a.A) % 16 == 0 && (a.lda % 8 == 0 || a.M == 1);
     p.ldc = a.ldc;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = ranks;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.N + kTileRows - 1) / kTileRows * ranks, (a.M + L::cols - 1) / L::cols);
-    cfg.blockDim = kThreads;
-    cfg.dynamicSmemBytes = L::bytes;
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = ranks > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, p, static_cast<Tout*>(a.C));
+    return launch_kernel(k_gemm4<F, NT, Tout>, dim3((a.N + kTileRows - 1) / kTileRows * ranks, (a.M + L::cols - 1) / L::cols), kThreads, ranks,
+                         L::bytes, false, s, p, static_cast<Tout*>(a.C));
 }
 
 template <int F, int NT> cudaError_t launch_out(const kda_gemm4_args& a, int ranks, cudaStream_t s) {
@@ -148,8 +136,6 @@ __global__ void __launch_bounds__(fewtc::kThreads, fewtc::Shape<N>::per_sm) k_ge
 
 template <int N, typename Tout> cudaError_t launch_tc(const kda_gemm4_args& a, cudaStream_t s) {
     using S = fewtc::Shape<N>;
-    const auto kernel = k_gemm4_tc<N, Tout>;
-    if (const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem)) return e;
     uint8_t* digits = static_cast<uint8_t*>(a.workspace);
     uint8_t* scales = digits + fewtc::digits_bytes(a.M, a.K);
     const bool wide = reinterpret_cast<uintptr_t>(a.A) % 16 == 0 && (a.lda % 8 == 0 || a.M == 1);
@@ -162,20 +148,8 @@ template <int N, typename Tout> cudaError_t launch_tc(const kda_gemm4_args& a, c
     p.ranks = fewtc::cluster_ranks(tiles * blocks, a.K, S::per_sm, 8);
     p.w_scales = static_cast<const uint8_t*>(a.scales), p.b_scales = scales, p.codes = a.codes;
     p.a = static_cast<const bf16*>(a.A), p.lda = a.lda, p.ldc = a.ldc, p.d_status = a.d_status;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // begins beside the columns' kernel, and waits for it itself
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = p.ranks;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(tiles * p.ranks, blocks);
-    cfg.blockDim = fewtc::kThreads;
-    cfg.dynamicSmemBytes = S::smem;
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = p.ranks > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, maps, p, static_cast<Tout*>(a.C));
+    return launch_kernel(k_gemm4_tc<N, Tout>, dim3(tiles * p.ranks, blocks), fewtc::kThreads, p.ranks, S::smem, true, s, maps, p,
+                         static_cast<Tout*>(a.C));
 }
 
 template <int N> cudaError_t launch_tc_out(const kda_gemm4_args& a, cudaStream_t s) {

@@ -8,8 +8,10 @@
 //
 // Bound by the bytes of the experts that some token chose; each is read once for all its tokens.  Five launches:
 // scores, choice with the lists of every expert's tokens, first products with their activation, second
-// products, sum over a token's experts in the order of their rank.
+// products, sum over a token's experts in the order of their rank.  e2m1 and bf16 experts go through the tensor cores
+// (kda_moe_tc.cuh), with one launch more for the tokens' columns, integer codes through kda_few.cuh.
 #include "kda_few.cuh"
+#include "kda_moe_tc.cuh"
 #include "kda_serve.cuh"
 #include "kda_wide.cuh"
 
@@ -51,7 +53,9 @@ __global__ void __launch_bounds__(kScoreThreads) k_moe_scores(const bf16* __rest
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int e = blockIdx.x, t0 = blockIdx.y * TB;
     if (e == 0 && t0 == 0 && threadIdx.x == 0) *done = 0;
-    Sum2 s[TB];
+    f2 hi[TB], lo[TB];  // two running sums (kda_wide.cuh) side by side
+#pragma unroll
+    for (int j = 0; j < TB; ++j) hi[j] = lo[j] = f2_dup(0.f);
     const Tr* r = router + (int64_t)e * D;
 #pragma unroll 2
     for (int k = threadIdx.x * 8; k < D; k += kScoreThreads * 8) {
@@ -62,12 +66,22 @@ __global__ void __launch_bounds__(kScoreThreads) k_moe_scores(const bf16* __rest
 #pragma unroll
         for (int j = 0; j < TB; ++j) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float p = xv[j][i] * rv[i];  // exact for a bf16 router
-                s[j].add(p);
-                if constexpr (sizeof(Tr) == 4) s[j].lo += fmaf(xv[j][i], rv[i], -p);
+            for (int i = 0; i < 8; i += 2) {
+                const f2 a = f2_of(xv[j][i], xv[j][i + 1]), b = f2_of(rv[i], rv[i + 1]);
+                const f2 p = mul2(a, b);  // exact for a bf16 router
+                const f2 sum = add2(hi[j], p), back = sub2(sum, hi[j]);
+                f2 lost = add2(sub2(hi[j], sub2(sum, back)), sub2(p, back));
+                if constexpr (sizeof(Tr) == 4) lost = add2(lost, fma2(a, b, sub2(f2_dup(0.f), p)));
+                lo[j] = add2(lo[j], lost);
+                hi[j] = sum;
             }
         }
+    }
+    Sum2 s[TB];
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {
+        s[j].hi = f2_lo(hi[j]), s[j].lo = f2_lo(lo[j]) + f2_hi(lo[j]);
+        s[j].add(f2_hi(hi[j]));
     }
 #pragma unroll
     for (int j = 0; j < TB; ++j) {
@@ -81,6 +95,8 @@ __global__ void __launch_bounds__(kScoreThreads) k_moe_scores(const bf16* __rest
     }
     __syncthreads();
     const int j = threadIdx.x;
+    let_next_kernel_begin();
+    wait_for_kernel_before();  // the digits' kernel, if one runs beside this: what comes next counts on both
     if (j < TB && t0 + j < M) {
         Wide v = sums[0][j];
 #pragma unroll
@@ -121,6 +137,8 @@ __global__ void __launch_bounds__(kPickThreads) k_moe_pick(const Wide* __restric
     __shared__ uint32_t warp_sum[kPickWarps];
     __shared__ bool last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.x;
+    wait_for_kernel_before();
+    let_next_kernel_begin();
     {
         // a warp's experts are 64 in a row, two per lane
         uint64_t k[2];
@@ -250,6 +268,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_moe_in(const Experts p, const B
     using L = Layout<F, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int of[L::cols], slot[L::cols];
+    wait_for_kernel_before();
+    let_next_kernel_begin();
     if ((int)blockIdx.y >= p.lists[0]) return;  // the whole cluster
     const int e = p.lists[1 + blockIdx.y], first = p.lists[1 + p.E + blockIdx.y], last = p.lists[2 + p.E + blockIdx.y];
     const int* slots = p.lists + 2 + 2 * p.E;
@@ -287,6 +307,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_moe_out(const Experts p, const 
     constexpr int kTerms = Format<F>::terms, kRows = L::cols / kTerms;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int of[kRows];
+    wait_for_kernel_before();
+    let_next_kernel_begin();
     if ((int)blockIdx.y >= p.lists[0]) return;
     const int e = p.lists[1 + blockIdx.y], first = p.lists[1 + p.E + blockIdx.y], last = p.lists[2 + p.E + blockIdx.y];
     const int* slots = p.lists + 2 + 2 * p.E;
@@ -311,10 +333,90 @@ __global__ void __launch_bounds__(kThreads, 2) k_moe_out(const Experts p, const 
     }
 }
 
+// ------------------------------------------------------------------ e2m1 and bf16 experts
+// The place of a slot in the lists is its row in the columns of the second product, and of the first one where a token's
+// columns are repeated for each of its experts; where all tokens fit into the columns at once (by_token) every expert
+// takes them all and leaves those it was not chosen for.
+//
+// A kernel may begin beside the one in front of it.  Where that is not the choice itself the lists are complete by then
+// (that one has waited for the choice), so weights and their scales can be on their way before the columns are written.
+struct Direct {  // the operands as they were given, for sums that come out as NaN
+    const uint8_t *codes, *scales;
+    const bf16* x;
+    int64_t xs;
+};
+
+// First products: the hidden values become digits (four bf16 columns, the last of zeros, for bf16 weights) where they
+// arise.  32 rows of a token share a scale: a warp's lanes.
+template <int N, bool Mx>
+__global__ void __launch_bounds__(fewtc::kStayThreads, fewtc::Stay<N, Mx ? 8 : 1, Mx>::per_sm)
+k_moe_in_tc(const __grid_constant__ fewtc::Maps maps, const fewtc::StayArgs p, const Direct given, void* __restrict__ columns,
+            uint8_t* __restrict__ scales, int* d_status) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ fewtc::StayBarriers bar;
+    const uint32_t raw = smem_addr(smem_raw);
+    uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    const int lane = threadIdx.x & 31, F = p.half;
+    const int* slots = p.lists + 2 + 2 * p.E;
+    fewtc::stay<N, Mx ? 8 : 1, Mx>(smem, bar, maps, p, d_status, [&](int e, int row0, int c0, int n, const float* red, int q) {
+        for (int i = q; i < 2 * n; i += 4) {
+            const int c = i >> 1, r = (i & 1) * 32 + lane, f = row0 + r, token = slots[c0 + c] / p.top;
+            const float* sum = red + (p.by_token ? token : c) * kRedPitch + r;
+            float gate = sum[0], up = sum[64];
+            if constexpr (Mx) {
+                if (f < F && (isnan(gate) || isnan(up))) {
+                    const bf16* row = given.x + (int64_t)token * given.xs;
+                    const int64_t g = (int64_t)e * p.rows + f, u = g + F;
+                    gate = fewtc::direct(given.codes + g * (p.K / 2), given.scales + g * (p.K / 32), row, p.K);
+                    up = fewtc::direct(given.codes + u * (p.K / 2), given.scales + u * (p.K / 32), row, p.K);
+                }
+            }
+            float v = f < F ? gate / (1.0f + expf(-gate)) * up : 0.f;
+            if constexpr (Mx) {
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu);
+                fewtc::put_digits_of_lanes(v, top, f < F, c0 + c, f, F, static_cast<uint8_t*>(columns), scales);
+            } else if (f < F) {
+                bf16* to = static_cast<bf16*>(columns) + (int64_t)(c0 + c) * 4 * F + f;
+#pragma unroll
+                for (int t = 0; t < 3; ++t) {
+                    const bf16 h = __float2bfloat16_rn(v);
+                    to[(int64_t)t * F] = h;
+                    v = isfinite(__bfloat162float(h)) ? v - __bfloat162float(h) : 0.f;
+                }
+                to[(int64_t)3 * F] = __float2bfloat16_rn(0.f);
+            }
+        }
+    });
+}
+
+// Second products: parts[slot][d] = w_slot W_out hidden_slot.
+template <int N, bool Mx>
+__global__ void __launch_bounds__(fewtc::kStayThreads, fewtc::Stay<N, Mx ? 8 : 4, Mx>::per_sm)
+k_moe_out_tc(const __grid_constant__ fewtc::Maps maps, const fewtc::StayArgs p, const float* __restrict__ weights, float* __restrict__ parts,
+             int* d_status) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ fewtc::StayBarriers bar;
+    const uint32_t raw = smem_addr(smem_raw);
+    uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    const int* slots = p.lists + 2 + 2 * p.E;
+    fewtc::stay<N, Mx ? 8 : 4, Mx>(smem, bar, maps, p, d_status, [&](int, int row0, int c0, int n, const float* red, int q) {
+        for (int i = q * 32 + (threadIdx.x & 31); i < n * 32; i += 128) {
+            const int c = i >> 5, r = (i & 31) * 4;
+            if (row0 + r >= p.rows) continue;  // rows are a multiple of 8
+            float4 v = *reinterpret_cast<const float4*>(red + c * kRedPitch + r);
+            const int slot = slots[c0 + c];
+            const float w = weights[slot];
+            v.x *= w, v.y *= w, v.z *= w, v.w *= w;
+            *reinterpret_cast<float4*>(parts + (int64_t)slot * p.rows + row0 + r) = v;
+        }
+    });
+}
+
 // y[t][d] = the sum of the token's parts, in the order of their rank.
 template <typename T>
 __global__ void __launch_bounds__(256) k_moe_sum(const float* __restrict__ parts, int M, int D, int top, T* __restrict__ y, int64_t ys) {
     const int t = blockIdx.y;
+    wait_for_kernel_before();
     for (int d = (blockIdx.x * 256 + threadIdx.x) * 4; d < D; d += gridDim.x * 1024) {  // D is a multiple of 8
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -328,43 +430,101 @@ __global__ void __launch_bounds__(256) k_moe_sum(const float* __restrict__ parts
 }
 
 // ------------------------------------------------------------------ launches
-template <typename... P, typename... A>
-cudaError_t launch_cluster(void (*kernel)(P...), dim3 grid, int ranks, int smem, cudaStream_t s, A&&... args) {
-    if (const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = ranks;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = kThreads;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = ranks > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
-}
-
-template <typename Tr> cudaError_t launch_scores(const kda_moe_args& a, int64_t xs, bool xwide, Wide* score, uint64_t* key, int* done, cudaStream_t s) {
+template <typename Tr> cudaError_t launch_scores(const kda_moe_args& a, int64_t xs, bool xwide, Wide* score, uint64_t* key, int* done, bool beside,
+                                               cudaStream_t s) {
     const bf16* x = static_cast<const bf16*>(a.x);
     const Tr* r = static_cast<const Tr*>(a.router);
     const bool rwide = reinterpret_cast<uintptr_t>(r) % 16 == 0;
     const int sg = a.score == KDA_SCORE_SIGMOID;
     if (a.M == 1)
-        k_moe_scores<Tr, 1><<<dim3(a.E, 1), kScoreThreads, 0, s>>>(x, xs, xwide, r, rwide, a.bias, a.M, a.E, a.D, sg, score, key, done);
-    else
-        k_moe_scores<Tr, 4><<<dim3(a.E, (a.M + 3) / 4), kScoreThreads, 0, s>>>(x, xs, xwide, r, rwide, a.bias, a.M, a.E, a.D, sg, score, key, done);
-    return cudaGetLastError();
+        return launch_kernel(k_moe_scores<Tr, 1>, dim3(a.E, 1), kScoreThreads, 1, 0, beside, s, x, xs, xwide, r, rwide, a.bias, a.M, a.E, a.D, sg, score,
+                             key, done);
+    return launch_kernel(k_moe_scores<Tr, 4>, dim3(a.E, (a.M + 3) / 4), kScoreThreads, 1, 0, beside, s, x, xs, xwide, r, rwide, a.bias, a.M, a.E, a.D,
+                         sg, score, key, done);
 }
 
 template <int F, int NT>
 cudaError_t launch_experts(const kda_moe_args& a, const Experts& in, const Experts& out, const Bf16Rows& src, float* hidden, const float* weights,
                            float* parts, int most, cudaStream_t s) {
     using L = Layout<F, NT>;
-    cudaError_t e = launch_cluster(k_moe_in<F, NT>, dim3((a.F + 63) / 64 * in.ranks, most), in.ranks, L::bytes, s, in, src, hidden);
+    cudaError_t e = launch_kernel(k_moe_in<F, NT>, dim3((a.F + 63) / 64 * in.ranks, most), kThreads, in.ranks, L::bytes, true, s, in, src, hidden);
     if (e) return e;
-    return launch_cluster(k_moe_out<F, NT>, dim3((a.D + kTileRows - 1) / kTileRows * out.ranks, most), out.ranks, L::bytes, s, out,
+    return launch_kernel(k_moe_out<F, NT>, dim3((a.D + kTileRows - 1) / kTileRows * out.ranks, most), kThreads, out.ranks, L::bytes, true, s, out,
                           (const float*)hidden, weights, parts);
+}
+
+template <int N, bool Mx>
+cudaError_t launch_in_tc(const fewtc::Maps& maps, const fewtc::StayArgs& p, int most, const Direct& given, void* columns, uint8_t* scales, int* d_status,
+                         cudaStream_t s) {
+    using S = fewtc::Stay<N, Mx ? 8 : 1, Mx>;
+    const int64_t items = (int64_t)most * p.tiles;
+    return launch_kernel(k_moe_in_tc<N, Mx>, dim3(items < 152 * S::per_sm ? items : 152 * S::per_sm), fewtc::kStayThreads, 1, S::smem, true, s, maps, p,
+                         given, columns, scales, d_status);
+}
+template <int N, bool Mx>
+cudaError_t launch_out_tc(const fewtc::Maps& maps, const fewtc::StayArgs& p, int most, const float* weights, float* parts, int* d_status, cudaStream_t s) {
+    using S = fewtc::Stay<N, Mx ? 8 : 4, Mx>;
+    const int64_t items = (int64_t)most * p.tiles;
+    return launch_kernel(k_moe_out_tc<N, Mx>, dim3(items < 152 * S::per_sm ? items : 152 * S::per_sm), fewtc::kStayThreads, 1, S::smem, true, s, maps, p,
+                         weights, parts, d_status);
+}
+
+// Columns that a pass over an expert's tile holds: for `tokens` tokens of T columns each, 16 to 128.
+int box_for(int tokens, int T, int most) {
+    int box = 16;
+    while (box < most && box / T < tokens) box *= 2;
+    return box;
+}
+
+template <bool Mx>
+cudaError_t launch_experts_tc(const kda_moe_args& a, const MoePlan& p, const int* lists, const bf16* x, int64_t xs, bool xwide, const float* weights,
+                              float* parts, int most, int columns, bool by_token, cudaStream_t s) {
+    char* ws = static_cast<char*>(a.workspace);
+    const int slots = a.M * a.top, rows = by_token ? a.M : slots;
+    uint8_t* xc = reinterpret_cast<uint8_t*>(ws + p.x_columns);
+    uint8_t* hc = reinterpret_cast<uint8_t*>(ws + p.hidden);
+    uint8_t *xsc = xc + fewtc::digits_bytes(rows, a.D), *hsc = hc + fewtc::digits_bytes(slots, a.F);
+    const int in_box = box_for(columns, Mx ? 8 : 1, Mx ? 128 : 64), out_box = box_for(columns, Mx ? 8 : 4, Mx ? 128 : 64);
+    const int* of = lists + 2 + 2 * a.E;
+    fewtc::Maps in, out;
+    cudaError_t e = cudaSuccess;
+    if constexpr (Mx) {
+        if (!fewtc::encode_maps(&in, a.w_in, (int64_t)a.E * 2 * a.F, xc, rows, a.D, in_box) ||
+            !fewtc::encode_maps(&out, a.w_out, (int64_t)a.E * a.D, hc, slots, a.F, out_box))
+            return cudaErrorInvalidValue;
+        if (!by_token) e = fewtc::launch_digits(x, xs, xwide, of, a.top, slots, a.D, xc, xsc, s);
+    } else {
+        if (!fewtc::encode_maps_bf16(&in, a.w_in, (int64_t)a.E * 2 * a.F, xc, rows, a.D, in_box) ||
+            !fewtc::encode_maps_bf16(&out, a.w_out, (int64_t)a.E * a.D, hc, 4 * (int64_t)slots, a.F, out_box))
+            return cudaErrorInvalidValue;
+        if (!by_token) e = fewtc::launch_rows(x, xs, xwide, of, a.top, slots, a.D, reinterpret_cast<bf16*>(xc), s);
+    }
+    if (e) return e;
+    fewtc::StayArgs pi = {}, po = {};
+    pi.w_scales = static_cast<const uint8_t*>(a.w_in_scales), pi.b_scales = xsc;
+    pi.rows = 2 * a.F, pi.half = a.F, pi.K = a.D, pi.tile_rows = kTileRows / 2, pi.tiles = (a.F + 63) / 64;
+    pi.lists = lists, pi.E = a.E, pi.top = a.top, pi.tokens = rows, pi.by_token = by_token;
+    po = pi;
+    po.w_scales = static_cast<const uint8_t*>(a.w_out_scales), po.b_scales = hsc;
+    po.rows = a.D, po.half = 64, po.K = a.F, po.tile_rows = kTileRows, po.tiles = (a.D + kTileRows - 1) / kTileRows;
+    po.tokens = slots, po.by_token = false;
+    const Direct given{static_cast<const uint8_t*>(a.w_in), static_cast<const uint8_t*>(a.w_in_scales), x, xs};
+    switch (in_box) {
+        case 16: e = launch_in_tc<16, Mx>(in, pi, most, given, hc, hsc, a.d_status, s); break;
+        case 32: e = launch_in_tc<32, Mx>(in, pi, most, given, hc, hsc, a.d_status, s); break;
+        case 64: e = launch_in_tc<64, Mx>(in, pi, most, given, hc, hsc, a.d_status, s); break;
+        default:
+            if constexpr (Mx) e = launch_in_tc<128, Mx>(in, pi, most, given, hc, hsc, a.d_status, s);
+    }
+    if (e) return e;
+    switch (out_box) {
+        case 16: return launch_out_tc<16, Mx>(out, po, most, weights, parts, a.d_status, s);
+        case 32: return launch_out_tc<32, Mx>(out, po, most, weights, parts, a.d_status, s);
+        case 64: return launch_out_tc<64, Mx>(out, po, most, weights, parts, a.d_status, s);
+        default:
+            if constexpr (Mx) return launch_out_tc<128, Mx>(out, po, most, weights, parts, a.d_status, s);
+            return cudaErrorInvalidValue;  // not reached: bf16 boxes end at 64
+    }
 }
 
 template <int F, typename... A> cudaError_t launch_width(int columns, A&&... args) {
@@ -396,7 +556,9 @@ MoePlan moe_plan(const kda_moe_args& a) {
     p.ids = take(slots * 4);
     p.weights = take(slots * 4);
     p.lists = take((2 + 2 * (size_t)a.E + slots) * 4);
-    p.hidden = take(slots * a.F * 4);
+    const bool mx = a.format == KDA_WEIGHT_E2M1, tc = mx || a.format == KDA_WEIGHT_BF16;
+    p.x_columns = take(mx ? fewtc::digits_bytes(slots, a.D) + fewtc::digit_scales_bytes(slots, a.D) : tc ? slots * a.D * 2 : 0);
+    p.hidden = take(mx ? fewtc::digits_bytes(slots, a.F) + fewtc::digit_scales_bytes(slots, a.F) : tc ? slots * a.F * 8 : slots * a.F * 4);
     p.parts = take(slots * a.D * 4);
     p.workspace = at;
     return p;
@@ -409,49 +571,54 @@ cudaError_t launch_moe(const kda_moe_args& a, const MoePlan& p, cudaStream_t s) 
     int* ids = reinterpret_cast<int*>(ws + p.ids);
     float* weights = reinterpret_cast<float*>(ws + p.weights);
     int* lists = reinterpret_cast<int*>(ws + p.lists);
-    float* hidden = reinterpret_cast<float*>(ws + p.hidden);
     float* parts = reinterpret_cast<float*>(ws + p.parts);
     const int64_t xs = a.x_stride ? a.x_stride : a.D, ys = a.y_stride ? a.y_stride : a.D;
     const bool xwide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (xs % 8 == 0 || a.M == 1);
     int* done = reinterpret_cast<int*>(ws + p.done);
-    cudaError_t e = a.router_dtype == KDA_BF16 ? launch_scores<bf16>(a, xs, xwide, score, key, done, s)
-                                               : launch_scores<float>(a, xs, xwide, score, key, done, s);
-    if (e) return e;
-    k_moe_pick<<<a.M, kPickThreads, 0, s>>>(score, key, a.M, a.E, a.top, a.score == KDA_SCORE_SIGMOID, a.scale, ids, weights, done, lists,
-                                            a.ids, a.weights);
-    if ((e = cudaGetLastError())) return e;
-
-    const int slots = a.M * a.top, most = slots < a.E ? slots : a.E;
-    // experts in use if the choices were even: what the clusters are sized for
-    const int64_t likely = most;
-    Experts in = {}, out = {};
-    in.w = static_cast<const uint8_t*>(a.w_in), in.scales = static_cast<const uint8_t*>(a.w_in_scales);
-    in.w_bytes = weight_bytes(a, 2 * a.F, a.D), in.s_bytes = scale_bytes(a, 2 * a.F, a.D);
-    in.scale_type = a.format == KDA_WEIGHT_E2M1 ? 0 : a.scale_dtype == KDA_BF16 ? 1 : 2;
-    in.group_shift = group_shift(a.group);
-    in.rows = 2 * a.F, in.K = a.D, in.lists = lists, in.E = a.E, in.top = a.top;
-    in.ranks = cluster_ranks(likely * ((a.F + 63) / 64), a.D);
-    out = in;
-    out.w = static_cast<const uint8_t*>(a.w_out), out.scales = static_cast<const uint8_t*>(a.w_out_scales);
-    out.w_bytes = weight_bytes(a, a.D, a.F), out.s_bytes = scale_bytes(a, a.D, a.F);
-    out.rows = a.D, out.K = a.F;
-    out.ranks = cluster_ranks(likely * ((a.D + kTileRows - 1) / kTileRows), a.F);
     // columns for twice an expert's even share of the slots, and no more than there are tokens
+    const int slots = a.M * a.top, most = slots < a.E ? slots : a.E;
     const int even = 2 * ((slots + a.E - 1) / a.E) + 2, columns = a.M < even ? a.M : even;
-    const Bf16Rows src{static_cast<const bf16*>(a.x), xs, xwide};
-    if (a.format == KDA_WEIGHT_E2M1)
-        e = launch_width<KDA_WEIGHT_E2M1>(columns, a, in, out, src, hidden, weights, parts, most, s);
-    else if (a.format == KDA_WEIGHT_INT4)
+    const bf16* x = static_cast<const bf16*>(a.x);
+    const bool mx = a.format == KDA_WEIGHT_E2M1, tc = mx || a.format == KDA_WEIGHT_BF16;
+    const bool by_token = tc && a.M == columns && a.M <= (mx ? 16 : 64);
+    cudaError_t e;
+    if (by_token) {
+        uint8_t* xc = reinterpret_cast<uint8_t*>(ws + p.x_columns);
+        e = mx ? fewtc::launch_digits(x, xs, xwide, nullptr, 1, a.M, a.D, xc, xc + fewtc::digits_bytes(a.M, a.D), s)
+               : fewtc::launch_rows(x, xs, xwide, nullptr, 1, a.M, a.D, reinterpret_cast<bf16*>(xc), s);
+        if (e) return e;
+    }
+    e = a.router_dtype == KDA_BF16 ? launch_scores<bf16>(a, xs, xwide, score, key, done, by_token, s)
+                                   : launch_scores<float>(a, xs, xwide, score, key, done, by_token, s);
+    if (e) return e;
+    if ((e = launch_kernel(k_moe_pick, dim3(a.M), kPickThreads, 1, 0, true, s, score, key, a.M, a.E, a.top, (int)(a.score == KDA_SCORE_SIGMOID),
+                           a.scale, ids, weights, done, lists, a.ids, a.weights)))
+        return e;
+    if (mx) {
+        e = launch_experts_tc<true>(a, p, lists, x, xs, xwide, weights, parts, most, columns, by_token, s);
+    } else if (tc) {
+        e = launch_experts_tc<false>(a, p, lists, x, xs, xwide, weights, parts, most, columns, by_token, s);
+    } else {
+        Experts in = {}, out = {};
+        float* hidden = reinterpret_cast<float*>(ws + p.hidden);
+        in.w = static_cast<const uint8_t*>(a.w_in), in.scales = static_cast<const uint8_t*>(a.w_in_scales);
+        in.w_bytes = weight_bytes(a, 2 * a.F, a.D), in.s_bytes = scale_bytes(a, 2 * a.F, a.D);
+        in.scale_type = a.scale_dtype == KDA_BF16 ? 1 : 2;
+        in.group_shift = group_shift(a.group);
+        in.rows = 2 * a.F, in.K = a.D, in.lists = lists, in.E = a.E, in.top = a.top;
+        in.ranks = cluster_ranks((int64_t)most * ((a.F + 63) / 64), a.D);
+        out = in;
+        out.w = static_cast<const uint8_t*>(a.w_out), out.scales = static_cast<const uint8_t*>(a.w_out_scales);
+        out.w_bytes = weight_bytes(a, a.D, a.F), out.s_bytes = scale_bytes(a, a.D, a.F);
+        out.rows = a.D, out.K = a.F;
+        out.ranks = cluster_ranks((int64_t)most * ((a.D + kTileRows - 1) / kTileRows), a.F);
+        const Bf16Rows src{x, xs, xwide};
         e = launch_width<KDA_WEIGHT_INT4>(columns, a, in, out, src, hidden, weights, parts, most, s);
-    else
-        e = launch_width<KDA_WEIGHT_BF16>(columns, a, in, out, src, hidden, weights, parts, most, s);
+    }
     if (e) return e;
     const dim3 grid((a.D + 1023) / 1024, a.M);
-    if (a.y_dtype == KDA_BF16)
-        k_moe_sum<bf16><<<grid, 256, 0, s>>>(parts, a.M, a.D, a.top, static_cast<bf16*>(a.y), ys);
-    else
-        k_moe_sum<float><<<grid, 256, 0, s>>>(parts, a.M, a.D, a.top, static_cast<float*>(a.y), ys);
-    return cudaGetLastError();
+    if (a.y_dtype == KDA_BF16) return launch_kernel(k_moe_sum<bf16>, grid, 256, 1, 0, true, s, parts, a.M, a.D, a.top, static_cast<bf16*>(a.y), ys);
+    return launch_kernel(k_moe_sum<float>, grid, 256, 1, 0, true, s, parts, a.M, a.D, a.top, static_cast<float*>(a.y), ys);
 }
 
 }  // namespace kda

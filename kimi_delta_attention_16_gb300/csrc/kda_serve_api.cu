@@ -120,6 +120,8 @@ kda_status check_moe(const kda_moe_args* a) {
     if (a->top > 32) return fail(KDA_ERR_UNSUPPORTED, "top=%d above 32", a->top);
     if ((int64_t)a->M * a->top > 65535) return fail(KDA_ERR_UNSUPPORTED, "M * top = %lld above 65535", (long long)a->M * a->top);
     if (a->D > 1 << 20 || a->F > 1 << 20) return fail(KDA_ERR_UNSUPPORTED, "D=%d or F=%d above 2^20", a->D, a->F);
+    if ((int64_t)a->E * 2 * a->F > 1 << 30 || (int64_t)a->E * a->D > 1 << 30)
+        return fail(KDA_ERR_UNSUPPORTED, "the experts have more than 2^30 rows (E=%d D=%d F=%d)", a->E, a->D, a->F);
     if (!valid_dtype(a->router_dtype) || !valid_dtype(a->y_dtype)) return fail(KDA_ERR_INVALID_ARG, "unknown dtype");
     if (a->score != KDA_SCORE_SIGMOID && a->score != KDA_SCORE_SOFTMAX) return fail(KDA_ERR_INVALID_ARG, "unknown score %d", a->score);
     if (a->score == KDA_SCORE_SOFTMAX && a->bias) return fail(KDA_ERR_INVALID_ARG, "softmax scores take no bias");
