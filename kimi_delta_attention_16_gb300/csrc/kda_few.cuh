@@ -1,21 +1,25 @@
-// kda_few.cuh -- products of a weight matrix [rows][K] with a few columns (tokens), for weights in
-// 4 bits or bf16: what the 4-bit projections (kda_gemm4.cu) and the experts (kda_moe.cu) share.
+// kda_few.cuh -- products of a matrix of integer codes in 4 bits with a few columns (tokens): what the 4-bit projections
+// (kda_gemm4.cu) and the experts (kda_moe.cu) share for weights (code - 8) * scale, one scale per 32, 64 or 128 weights.
 //
-// Bound by the weights' bytes: every weight is read once and used for at most 8 NT columns.  A CTA
-// takes 128 rows, a warp 16 of them, on mma.sync (m16n8k16, fp32 accumulation: an instruction whose
-// narrow side is 8 columns fits a few tokens, where a tcgen05 tile of 128 x N would spend its time on
-// feeding codes that registers have to widen first).  K is split over the CTAs of a cluster, which
-// join their parts through distributed shared memory in the order of their ranks.
+// Bound by the codes' bytes and by the instructions that take them apart.  A scale of any value cannot go to the
+// block-scaled tensor cores, so codes become fp16 operands of mma.sync (m16n8k16, fp32 accumulation: its narrow side of 8
+// fits a few tokens) by a mask alone: four bits in a half's mantissa are the subnormal code 2^-24, or 16 code 2^-24 from the
+// next four bits, where the column's element is kept divided by 16.  The 8 to be taken off is not taken off the codes: a
+// group's sum starts from -8 times the sum of the column's elements in it.  (Codes as 1024 + code, 1032 taken off in
+// registers, were 16 instructions more per 512 weights.)  A group's sum is multiplied by the weights' scale in fp32
+// when it is added up: scales are never rounded.
 //
-// 4-bit codes go through cp.async into a ring of stages of each warp's own (16 rows x 128 bytes, no
-// barrier among warps), are widened to fp16 in registers, exactly, and multiply columns held in
-// shared memory as fp16.  Each run of 256 elements of a column is brought to 2^14..2^15 by a power of
-// two first: that is exact for a bf16 element down to 2^-28 of its run's largest and off by at most
-// 2^-40 of the largest below that, less than an fp32 sum would keep.  A group's product (32 weights
-// under one scale) is a sum of two instructions from zero, multiplied by the weights' scale in fp32
-// when it is added up, so scales are never rounded.  bf16 weights multiply bf16 columns.
-// fp32 columns (the experts' hidden values) are split into two fp16 or three bf16 terms of a column
-// each, added up at the end.
+// Columns are prepared by a kernel in front (k_few_halves): each run of 128 elements is brought to 2^14..2^15 by a
+// power of two, which is exact for a bf16 element down to 2^-27 of its run's largest and off by at most 2^-35 of the largest
+// below that, less than an fp32 sum would keep; fp32 values are two columns, value and remainder.  The power's
+// inverse is multiplied in at the end of a run.
+//
+// A CTA has 8 or 12 warps.  A warp takes 32 rows, two tiles of an instruction, so that each operand of the columns is read from
+// shared memory once for both and their chains of instructions overlap (16 warps of 16 rows each: 199 us instead of
+// MEASURED for 160,000 x 7,168 codes and 16 tokens).  Its codes and scales go through cp.async into a ring of its own
+// (32 rows x 256 elements a stage), no barrier among warps.  All columns of a segment of K are in shared memory for all
+// warps, the next segment's on their way meanwhile: one barrier per segment.  `ks` warps share 32 rows along K where there
+// are few rows.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -28,111 +32,8 @@
 namespace kda {
 namespace few {
 
-constexpr int kThreads = 256, kWarps = 8;
-constexpr int kTileRows = 128;               // rows of weights per CTA
-constexpr int kChunk = 256;                  // elements of a column under one power of two
-constexpr int kRowStage = 128;               // bytes of a row per stage
-constexpr int kWarpStage = 16 * kRowStage;   // bytes of a warp's stage
-constexpr int kRedPitch = kTileRows + 4;     // floats between columns of the sums' buffer
-
-template <int F> struct Format;              // elements of K per stage
-template <> struct Format<KDA_WEIGHT_BF16> { static constexpr int stage_k = 64, terms = 3; };
-template <> struct Format<KDA_WEIGHT_E2M1> { static constexpr int stage_k = 256, terms = 2; };
-template <> struct Format<KDA_WEIGHT_INT4> { static constexpr int stage_k = 256, terms = 2; };
-
-// Shared memory of one CTA: ring of stages (reused for the sums), columns, scales of both sides.
-template <int F, int NT> struct Layout {
-    static constexpr int cols = 8 * NT;
-    static constexpr int stages = NT == 1 ? 4 : 3;
-    static constexpr int seg = NT <= 2 ? 1024 : 2048 / NT;       // elements of K whose columns are held at once
-    static constexpr int seg_chunks = seg / kChunk, seg_units = seg / 32;
-    static constexpr int x_pitch = (seg + 32) * 2;               // bytes; 64 past a multiple of 128: no bank conflicts
-    static constexpr int s_pitch = seg_units + 4;                // floats
-    static constexpr int ring = kWarps * stages * kWarpStage;
-    static constexpr int red = cols * kRedPitch * 4;
-    static constexpr int x_at = ring > red ? ring : red;
-    static constexpr int s_at = x_at + cols * x_pitch;
-    static constexpr int xs_at = s_at + (F == KDA_WEIGHT_BF16 ? 0 : kTileRows * s_pitch * 4);
-    static constexpr int bytes = xs_at + cols * seg_chunks * 4;
-};
-
-// One matrix [rows][K] of weights.
-struct Matrix {
-    const uint8_t* w;       // codes [rows][K / 2], or bf16 [rows][K]
-    const void* scales;     // [rows][K >> (5 + group_shift)]
-    int scale_type;         // 0: bytes (exponent + 127), 1: bf16, 2: fp32
-    int group_shift;        // log2(group / 32)
-};
-
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool valid) {
-    const int n = valid ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-    return v;
-}
-
-// d = a b + c on 16 x 8 x 16.
-template <bool Bf16>
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4]) {
-    if constexpr (Bf16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
-            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
-            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
-}
-
-// Eight codes as four pairs of fp16.  e2m1: elements (0,1) (2,3) (4,5) (6,7).  int4: a code of four bits put
-// into the mantissa of 1024 (or, 16 times itself, of the same) and the offset taken off, which leaves
-// elements (0,4) (1,5) (2,6) (3,7); the columns are laid out in that order.
-template <int F> __device__ __forceinline__ void widen(uint32_t w, uint32_t (&p)[4]) {
-    if constexpr (F == KDA_WEIGHT_E2M1) {
-        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-            "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-            "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-            "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-            : "=r"(p[0]), "=r"(p[1]), "=r"(p[2]), "=r"(p[3]) : "r"(w));
-    } else {
-        const uint32_t h = w >> 8;
-        const __half2 one = __half2half2(__ushort_as_half(0x6408));     // 1032
-        const __half2 sixteenth = __half2half2(__ushort_as_half(0x2c00));
-        const __half2 off = __half2half2(__ushort_as_half(0xd480));     // -72
-        auto bits = [](__half2 v) { return *reinterpret_cast<uint32_t*>(&v); };
-        auto half = [](uint32_t v) { return *reinterpret_cast<__half2*>(&v); };
-        p[0] = bits(__hsub2(half((w & 0x000f000fu) | 0x64006400u), one));
-        p[1] = bits(__hfma2(half((w & 0x00f000f0u) | 0x64006400u), sixteenth, off));
-        p[2] = bits(__hsub2(half((h & 0x000f000fu) | 0x64006400u), one));
-        p[3] = bits(__hfma2(half((h & 0x00f000f0u) | 0x64006400u), sixteenth, off));
-    }
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// The power of two that brings a magnitude with these fp32 exponent bits to 2^14..2^15 (as far as fp32 has
-// one), and its inverse.
-__device__ __forceinline__ void run_scale(uint32_t exponent, float& up, float& down) {
-    const uint32_t e = 268u - exponent;             // 127 + 14 + 127 - exponent
-    const uint32_t b = e > 254u ? 254u : e;
-    up = __uint_as_float(b << 23);
-    const uint32_t d = 254u - b;
-    down = __uint_as_float(d ? d << 23 : 0x00400000u);
-}
+constexpr int kTileRows = 128;               // rows of a tile on the tensor cores (kda_few_tc.cuh)
+constexpr int kRedPitch = kTileRows + 4;     // floats between columns of its sums
 
 // A kernel that was launched beside the one in front of it on the stream waits here until that one has ended, and with it
 // all before; the one in front lets it begin.  Without such a launch both do nothing.
@@ -164,385 +65,351 @@ cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, int threads, int rank
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
-// Where the columns come from.  Bf16Rows: column c is row of[c] of a bf16 tensor.  F32Rows: columns
-// c * terms .. c * terms + terms - 1 are the parts of fp32 row of[c].
-struct Bf16Rows {
-    const bf16* x;
-    int64_t stride;
-    bool wide;  // 16-byte accesses
-    static constexpr bool split = false;
+constexpr int kRows = 32;                    // of a warp
+constexpr int kStageK = 256;                 // elements of a row per stage
+constexpr int kRun = 128;                    // elements of a column under one power of two
+constexpr int kWarpStage = kRows * kStageK / 2; // bytes of codes in a warp's stage
+constexpr int kStages = 3;
+
+// A CTA of W warps for 8 NT columns, GS groups in a stage and SB bytes of a scale.
+template <int W_, int NT_, int GS_, int SB_> struct Layout {
+    static constexpr int W = W_, NT = NT_, GS = GS_, SB = SB_, threads = 32 * W;
+    static constexpr int cols = 8 * NT, scale_row = GS * SB;     // bytes of a row's scales in a stage
+    static constexpr int seg = 2048 / NT, seg_stages = seg / kStageK, seg_runs = seg / kRun;
+    static constexpr int most_ks = seg_stages / 2;               // a warp has two stages of a segment at least
+    static constexpr int x_pitch = (seg + 32) * 2;               // bytes; 64 past a multiple of 128: no bank conflicts
+    static constexpr int scales_at = W * kStages * kWarpStage;
+    static constexpr int x_at = scales_at + W * kStages * kRows * scale_row;
+    static constexpr int f_at = x_at + 2 * cols * x_pitch;       // [2][cols][seg_runs]
+    static constexpr int most_groups = seg / 32;                 // of a segment: sums [2][groups][cols]
+    static constexpr int sums_at = f_at + 2 * cols * seg_runs * 4;
+    static constexpr int bytes = sums_at + 2 * most_groups * cols * 4;
+    static_assert(most_ks < 2 || W * kRows * cols * 4 <= cols * x_pitch, "sums of warps that share rows fit over a segment's columns");
+    static_assert(bytes <= 227 * 1024, "shared memory of an SM");
 };
-struct F32Rows {
-    const float* x;
-    int64_t stride;
-    static constexpr bool split = true;
+
+struct Weights {  // of one matrix [rows][K]
+    const uint8_t* codes;
+    const uint8_t* scales;
+};
+struct Columns {  // laid out by k_few_halves
+    const __half* x;      // [.][K]
+    const float* factor;  // [.][runs of 128]: what a sum is to be multiplied by, but for 2^24
+    const float* sums;    // [.][groups]: -8 2^-24 times the sum of a group's elements
 };
 
-// 16 bytes of a column (eight elements from k, a multiple of 8) to their places in shared memory.
-template <int F>
-__device__ __forceinline__ void put8(uint8_t* col, int k, const uint32_t (&v)[4]) {
-    if constexpr (F == KDA_WEIGHT_E2M1) {
-        *reinterpret_cast<uint4*>(col + 2 * k) = make_uint4(v[0], v[1], v[2], v[3]);
-    } else if constexpr (F == KDA_WEIGHT_INT4) {
-        *reinterpret_cast<uint4*>(col + 2 * k) = make_uint4(__byte_perm(v[0], v[2], 0x5410), __byte_perm(v[0], v[2], 0x7632),
-                                                            __byte_perm(v[1], v[3], 0x5410), __byte_perm(v[1], v[3], 0x7632));
-    } else {  // word t of the four accesses of 32 elements next to each other: the order the lanes read them in
-        uint32_t* p = reinterpret_cast<uint32_t*>(col + 2 * (k & ~31)) + ((k >> 3) & 3);
-        p[0] = v[0];
-        p[4] = v[1];
-        p[8] = v[2];
-        p[12] = v[3];
-    }
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int n) {  // zeros behind the first n bytes
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// d = a b + c on 16 x 8 x 16.
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1, const float (&c)[4]) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-// Columns [0, n) of K in [k0, k0 + seg) (zeros from k1 and past the last column) into shared memory.
-template <int F, int NT, typename Src>
-__device__ __forceinline__ void stage_columns(uint8_t* smem, const Src& src, const int* of, int n, int k0, int k1) {
-    using L = Layout<F, NT>;
-    constexpr int kTerms = Src::split ? Format<F>::terms : 1;
-    constexpr int kBatch = Src::split ? 2 : 4;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float* xs = reinterpret_cast<float*>(smem + L::xs_at);
-    const int chunks = min(L::seg_chunks, (k1 - k0 + kChunk - 1) / kChunk);
-    const int items = n * chunks;
-    for (int it0 = warp; it0 < items; it0 += kWarps * kBatch) {
-        uint32_t v[kBatch][Src::split ? 8 : 4];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int it = it0 + b * kWarps, c = it / chunks, k = k0 + (it - c * chunks) * kChunk + lane * 8;
-#pragma unroll
-            for (int i = 0; i < (Src::split ? 8 : 4); ++i) v[b][i] = 0;
-            if (it < items && k < k1) {
-                if constexpr (Src::split) {
-                    const float4* p = reinterpret_cast<const float4*>(src.x + (int64_t)of[c] * src.stride + k);
-                    const float4 lo = p[0], hi = p[1];
-                    v[b][0] = __float_as_uint(lo.x), v[b][1] = __float_as_uint(lo.y), v[b][2] = __float_as_uint(lo.z);
-                    v[b][3] = __float_as_uint(lo.w), v[b][4] = __float_as_uint(hi.x), v[b][5] = __float_as_uint(hi.y);
-                    v[b][6] = __float_as_uint(hi.z), v[b][7] = __float_as_uint(hi.w);
-                } else {
-                    const bf16* p = src.x + (int64_t)of[c] * src.stride + k;
-                    if (src.wide) {
-                        const uint4 q = *reinterpret_cast<const uint4*>(p);
-                        v[b][0] = q.x, v[b][1] = q.y, v[b][2] = q.z, v[b][3] = q.w;
-                    } else {
-                        const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) v[b][i] = h[2 * i] | ((uint32_t)h[2 * i + 1] << 16);
-                    }
-                }
-            }
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int it = it0 + b * kWarps, c = it / chunks, ch = it - c * chunks;
-            if (it >= items) break;
-            const int k = ch * kChunk + lane * 8;
-            uint8_t* col = smem + L::x_at + c * kTerms * L::x_pitch;
-            if constexpr (F == KDA_WEIGHT_BF16) {
-                if constexpr (!Src::split) {
-                    put8<F>(col, k, v[b]);
-                } else {
-                    float r[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) r[i] = __uint_as_float(v[b][i]);
-#pragma unroll
-                    for (int t = 0; t < kTerms; ++t) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const bf16 a = __float2bfloat16_rn(r[2 * i]), c2 = __float2bfloat16_rn(r[2 * i + 1]);
-                            o[i] = (uint32_t)__bfloat16_as_ushort(a) | ((uint32_t)__bfloat16_as_ushort(c2) << 16);
-                            const float fa = __bfloat162float(a), fb = __bfloat162float(c2);
-                            r[2 * i] = isinf(fa) ? 0.f : r[2 * i] - fa;
-                            r[2 * i + 1] = isinf(fb) ? 0.f : r[2 * i + 1] - fb;
-                        }
-                        put8<F>(col + t * L::x_pitch, k, o);
-                    }
-                }
-            } else {
-                uint32_t top = 0;
-                if constexpr (Src::split) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) top = max(top, v[b][i] & 0x7fffffffu);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) top = __vmaxu2(top, v[b][i] & 0x7fff7fffu);
-                    top = max(top << 16, top & 0xffff0000u);
-                }
-                top = __reduce_max_sync(0xffffffffu, top);
-                float up, down;
-                run_scale(top >> 23, up, down);
-                float r[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (Src::split) {
-                        r[2 * i] = __uint_as_float(v[b][2 * i]) * up;
-                        r[2 * i + 1] = __uint_as_float(v[b][2 * i + 1]) * up;
-                    } else {
-                        r[2 * i] = __uint_as_float(v[b][i] << 16) * up;
-                        r[2 * i + 1] = __uint_as_float(v[b][i] & 0xffff0000u) * up;
-                    }
-                }
-#pragma unroll
-                for (int t = 0; t < kTerms; ++t) {
-                    uint32_t o[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        o[i] = pack_half2(r[2 * i], r[2 * i + 1]);
-                        if constexpr (kTerms > 1) {
-                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o[i]));
-                            r[2 * i] = isinf(f.x) ? 0.f : r[2 * i] - f.x;
-                            r[2 * i + 1] = isinf(f.y) ? 0.f : r[2 * i + 1] - f.y;
-                        }
-                    }
-                    put8<F>(col + t * L::x_pitch, k, o);
-                    if (lane == 0) xs[(c * kTerms + t) * L::seg_chunks + ch] = down;
-                }
-            }
-        }
-    }
+// Eight codes as four pairs of fp16: elements (0,4) as code 2^-24, (1,5) as 16 code 2^-24, (2,6) and (3,7) likewise.  The
+// columns are laid out in that order, elements 1, 3, 5 and 7 divided by 16.
+__device__ __forceinline__ void part(uint32_t w, uint32_t (&p)[4]) {
+    const uint32_t h = w >> 8;
+    p[0] = w & 0x000f000fu;
+    p[1] = w & 0x00f000f0u;
+    p[2] = h & 0x000f000fu;
+    p[3] = h & 0x00f000f0u;
 }
 
-// Zeros for the columns that hold no token: what multiplies them is never read, but must not trap or turn up as NaN in
-// other columns' runs.
-template <int F, int NT> __device__ __forceinline__ void clear_columns(uint8_t* smem, int used) {
-    using L = Layout<F, NT>;
-    float* xs = reinterpret_cast<float*>(smem + L::xs_at);
-    uint4* x = reinterpret_cast<uint4*>(smem + L::x_at + used * L::x_pitch);
-    for (int i = threadIdx.x; i < (L::cols - used) * (L::x_pitch / 16); i += kThreads) x[i] = make_uint4(0, 0, 0, 0);
-    if constexpr (F != KDA_WEIGHT_BF16)
-        for (int i = used * L::seg_chunks + threadIdx.x; i < L::cols * L::seg_chunks; i += kThreads) xs[i] = 0.f;
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Scales of the tile's rows for K in [k0, k0 + seg), one fp32 per row and 32 elements (zeros from k1).
-// row_of(r): the tile's row r as a row of the matrix.
-template <int F, int NT, typename RowOf>
-__device__ __forceinline__ void stage_scales(uint8_t* smem, const Matrix& m, int K, const RowOf& row_of, int k0, int k1) {
-    using L = Layout<F, NT>;
-    float* sc = reinterpret_cast<float*>(smem + L::s_at);
-    const int64_t per_row = K >> (5 + m.group_shift);
-    const int u0 = k0 >> 5, units = min(L::seg_units, (k1 - k0) >> 5);
-    // two threads per row, each half of the row's units: four at a time
-    const int r = threadIdx.x >> 1;
-    const int64_t row = row_of(r) * per_row;
-    float* dst = sc + r * L::s_pitch;
-    const bool quads = m.scale_type == 0 && m.group_shift == 0 && (per_row & 3) == 0 &&
-                       (reinterpret_cast<uintptr_t>(m.scales) & 3) == 0 && (units & 3) == 0;
-    if (quads) {
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(m.scales) + row + u0);
-#pragma unroll 4
-        for (int q = threadIdx.x & 1; q < L::seg_units / 4; q += 2) {
-            const uint32_t b = q * 4 < units ? p[q] : 0;
-            *reinterpret_cast<float4*>(dst + 4 * q) =
-                make_float4(__uint_as_float((b & 0xffu) << 23), __uint_as_float((b & 0xff00u) << 15),
-                            __uint_as_float((b & 0xff0000u) << 7), __uint_as_float((b >> 24) << 23));
-        }
-        return;
-    }
-#pragma unroll 4
-    for (int u = threadIdx.x & 1; u < L::seg_units; u += 2) {
-        float v = 0.f;
-        if (u < units) {
-            const int64_t at = row + ((u0 + u) >> m.group_shift);
-            if (m.scale_type == 0)
-                v = __uint_as_float((uint32_t)static_cast<const uint8_t*>(m.scales)[at] << 23);
-            else if (m.scale_type == 1)
-                v = __bfloat162float(static_cast<const bf16*>(m.scales)[at]);
-            else
-                v = static_cast<const float*>(m.scales)[at];
-        }
-        dst[u] = v;
-    }
+// The power of two that brings a magnitude with these fp32 exponent bits to 2^14..2^15 (as far as fp32 has
+// one), and its inverse.
+__device__ __forceinline__ void run_scale(uint32_t exponent, float& up, float& down) {
+    const uint32_t e = 268u - exponent;             // 127 + 14 + 127 - exponent
+    const uint32_t b = e > 254u ? 254u : e;
+    up = __uint_as_float(b << 23);
+    const uint32_t d = 254u - b;
+    down = __uint_as_float(d ? d << 23 : 0x00400000u);
 }
 
-// acc[n][.] += the tile's 128 rows times up to 8 NT columns over K in [k0, k1) (k0 a multiple of 256): a lane
-// of a warp holds rows g and g + 8 of its 16 and columns 8 n + 2 t, + 1.
-template <int F, int NT, typename Src, typename RowOf>
-__device__ __forceinline__ void product(uint8_t* smem, const Matrix& m, int K, const RowOf& row_of, const Src& src,
-                                        const int* of, int n, int k0, int k1, float (&acc)[NT][4]) {
-    using L = Layout<F, NT>;
-    constexpr int kStageK = Format<F>::stage_k;
-    constexpr bool kBf16 = F == KDA_WEIGHT_BF16;
+// Where the columns of `n` rows of K elements lie in a buffer, and what they take.
+inline Columns columns_at(void* buffer, int64_t n, int64_t K) {
+    __half* x = static_cast<__half*>(buffer);
+    float* factor = reinterpret_cast<float*>(x + n * K);
+    return Columns{x, factor, factor + n * ((K + kRun - 1) / kRun)};
+}
+inline size_t columns_bytes(int64_t n, int64_t K, int group) {
+    return (size_t)n * K * 2 + (size_t)n * ((K + kRun - 1) / kRun) * 4 + (size_t)n * (K / group) * 4;
+}
+// The columns of bf16 rows [rows][K] (K a multiple of the group).
+cudaError_t launch_halves(const bf16* x, int64_t xs, bool wide, int rows, int K, int group, const Columns& columns, cudaStream_t s);
+
+constexpr float kSumOf = -8.f * 0x1p-24f;
+
+// One product by itself, for a sum that came out as NaN: what is taken off a row with an infinity is one too.
+static __device__ __noinline__ float direct(const uint8_t* codes, const uint8_t* scales, int scale_bytes, int group, const bf16* x, int K) {
+    float sum = 0.f;
+    for (int g = 0; g < K / group; ++g) {
+        float one = 0.f;
+        for (int i = g * group; i < (g + 1) * group; ++i) one = fmaf((float)((int)(codes[i >> 1] >> (4 * (i & 1)) & 15u) - 8), to_f(x[i]), one);
+        const float s = scale_bytes == 2 ? to_f(reinterpret_cast<const bf16*>(scales)[g]) : reinterpret_cast<const float*>(scales)[g];
+        sum = fmaf(one, s, sum);
+    }
+    return sum;
+}
+
+// The sums of a CTA.  row_of(pass, tile, r): the matrix's row of row r of one of the W / ks tiles of 32 rows that the CTA
+// takes in a pass, or -1 for a tile that does not exist; column c is row of[c] of the columns' tensor, c < n.  After each
+// pass the warps call done(pass, acc) with a lane's sums: acc[u] holds rows 16 u + g and + 8 of the warp's tile (warp / ks),
+// columns 8 i + 2 t, + 1; where ks warps share a tile the first of them holds the sums.
+template <typename L, typename RowOf, typename Done>
+__device__ __forceinline__ void products(uint8_t* smem, const Weights& w, const Columns& x, int K, const int* of, int n, int ks, int passes,
+                                         const RowOf& row_of, const Done& done) {
+    constexpr int NT = L::NT, GS = L::GS, SB = L::SB, kThreads = L::threads, kScaleRow = L::scale_row;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-    if (k1 <= k0) return;  // the whole CTA: more ranks than runs of 256
-
-    const int64_t pitch = kBf16 ? (int64_t)K * 2 : (int64_t)K / 2;
-    const int slice = kBf16 ? (k1 - k0) * 2 : (k1 - k0) / 2;  // bytes of a row
-    const int total = (slice + kRowStage - 1) / kRowStage;
-    const uint32_t ring = smem_addr(smem) + warp * L::stages * kWarpStage;
+    const int tile = warp / ks, slot = warp - tile * ks;
+    const int stages = (K + kStageK - 1) / kStageK, segs = (K + L::seg - 1) / L::seg, own = L::seg_stages / ks, runs = (K + kRun - 1) / kRun;
+    const int row_scales = K / (kStageK / GS);
+    const uint32_t ring = smem_addr(smem) + warp * kStages * kWarpStage;
+    const uint32_t sring = smem_addr(smem) + L::scales_at + warp * kStages * kRows * kScaleRow;
     const int piece = lane & 7, r0 = lane >> 3;
-    const uint8_t* from[4];
-    uint32_t to[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = r0 + 4 * i;
-        from[i] = m.w + row_of(16 * warp + r) * pitch + (kBf16 ? (int64_t)k0 * 2 : (int64_t)k0 / 2) + piece * 16;
-        to[i] = ring + r * kRowStage + ((piece ^ (r & 7)) << 4);
-    }
-    auto issue = [&](int c) {
-        if (c < total) {
-            const bool in = c * kRowStage + piece * 16 < slice;
-            const uint32_t slot = (uint32_t)(c % L::stages) * kWarpStage;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) cp_async16_or_zero(to[i] + slot, in ? from[i] + (int64_t)c * kRowStage : m.w, in);
-        }
-        cp_commit();
-    };
-#pragma unroll
-    for (int c = 0; c < L::stages - 1; ++c) issue(c);
+    constexpr int kStageScales = GS * SB, kUnit = kStageScales < 16 ? kStageScales : 16;  // bytes of a row's scales, and of a copy
+    const bool whole = ((uint64_t)(row_scales * SB) | reinterpret_cast<uint64_t>(w.scales)) % kUnit == 0;
 
-    const uint32_t col = smem_addr(smem) + L::x_at + g * L::x_pitch + t * 16;
-    const float* sc0 = reinterpret_cast<const float*>(smem + L::s_at) + (16 * warp + g) * L::s_pitch;
-    const float* sc1 = sc0 + 8 * L::s_pitch;
-    const float* xs = reinterpret_cast<const float*>(smem + L::xs_at);
-    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-    clear_columns<F, NT>(smem, n * (Src::split ? Format<F>::terms : 1));
-    int c = 0;
-    for (int seg = k0; seg < k1; seg += L::seg) {
-        if (seg != k0) __syncthreads();  // every warp is done with the last columns
-        if constexpr (!kBf16) stage_scales<F, NT>(smem, m, K, row_of, seg, k1);
-        stage_columns<F, NT>(smem, src, of, n, seg, k1);
-        __syncthreads();
-        const int runs = (min(k1 - seg, L::seg) + kStageK - 1) / kStageK;
-        for (int run = 0; run < runs; ++run, ++c) {
-            cp_wait<L::stages - 2>();
-            __syncwarp();
-            issue(c + L::stages - 1);
-            const uint32_t wrow = ring + (uint32_t)(c % L::stages) * kWarpStage + g * kRowStage + t * 4;
-            if constexpr (kBf16) {
-                // a stage's sum starts from zero and is added in fp32: the matrix instructions drop digits below the
-                // accumulator's last one, which over a long chain takes 5 of its 24 bits
-                float part[NT][4];
+    // columns of segment q (counted over the passes) into buffer q & 1, 8 elements at a time
+    constexpr int kPieces = L::seg / 8;
+    const auto load_columns = [&](int q) {
+        const int s = q % segs;
+        const uint32_t to = smem_addr(smem) + L::x_at + (q & 1) * L::cols * L::x_pitch;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < L::cols * kPieces; i += kThreads) {
+            const int c = i / kPieces, k = i % kPieces * 8;
+            const bool in = c < n && s * L::seg + k < K;
+            cp_async16(to + c * L::x_pitch + k * 2, in ? x.x + (int64_t)of[c] * K + s * L::seg + k : x.x, in ? 16 : 0);
+        }
+        if (threadIdx.x < L::cols * L::seg_runs) {
+            float* f = reinterpret_cast<float*>(smem + L::f_at) + (q & 1) * L::cols * L::seg_runs + threadIdx.x;
+            const int c = threadIdx.x / L::seg_runs, r = s * L::seg_runs + threadIdx.x % L::seg_runs;
+            if (c < n && r < runs)
+                cp_async4(smem_addr(f), x.factor + (int64_t)of[c] * runs + r);
+            else
+                *f = 0.f;
+        }
+        constexpr int kGroups = L::seg_stages * GS;  // of a segment
+        for (int i = threadIdx.x; i < kGroups * L::cols; i += kThreads) {
+            const int c = i / kGroups, j = i % kGroups, at = s * kGroups + j;
+            float* f = reinterpret_cast<float*>(smem + L::sums_at) + (q & 1) * L::most_groups * L::cols + j * L::cols + c;
+            if (c < n && at < row_scales)
+                cp_async4(smem_addr(f), x.sums + (int64_t)of[c] * row_scales + at);
+            else
+                *f = 0.f;
+        }
+    };
+
+    // this warp's stages, counted over passes, segments and its share of a segment's stages
+    const uint8_t *row = nullptr, *srow = nullptr;  // of this lane's first piece and of its row's scales, at K = 0
+    bool inside = false;                            // all 32 rows are rows of their own, one after another
+    int ipass = -1;                                 // the pass that these belong to
+    const int64_t every4 = (int64_t)K * 2;          // bytes between rows r and r + 4
+    const uint32_t to_even = ring + r0 * 128 + ((piece ^ r0) << 4), to_odd = ring + (r0 + 4) * 128 + ((piece ^ (r0 + 4)) << 4);
+    const uint32_t to_scales = sring + lane * kScaleRow;
+    const auto issue = [&](int pass, int st, int buffer) {
+        if (pass >= passes || st >= stages) return;
+        if (pass != ipass) {
+            ipass = pass;
+            const int64_t r = row_of(pass, tile, r0), s = row_of(pass, tile, lane);
+            row = r < 0 ? nullptr : w.codes + r * (K / 2) + piece * 16;
+            srow = r < 0 ? nullptr : w.scales + s * row_scales * SB;
+            inside = r >= 0 && row_of(pass, tile, kRows - 1) == row_of(pass, tile, 0) + kRows - 1;
+        }
+        if (!row) return;
+        const uint32_t off = buffer * kWarpStage;
+        const bool full = (st + 1) * kStageK <= K;
+        if (inside && full) {
+            const uint8_t* p = row + st * 128;
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < 8; ++i) {
+                cp_async16((i & 1 ? to_odd : to_even) + off + (i >> 1) * 1024, p);
+                p += every4;
+            }
+        } else {
+            const int left = K / 2 - st * 128 - piece * 16;  // bytes of a row from here
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                const uint8_t* p = w.codes + row_of(pass, tile, r0 + 4 * i) * (K / 2);
+                cp_async16((i & 1 ? to_odd : to_even) + off + (i >> 1) * 1024, left > 0 ? p + st * 128 + piece * 16 : p, left > 0 ? 16 : 0);
+            }
+        }
+        // a row's scales per lane
+        const uint32_t sto = to_scales + buffer * kRows * kScaleRow;
+        const uint8_t* from = srow + st * kStageScales;
+        if (whole && full) {
+            if constexpr (kUnit == 4) cp_async4(sto, from);
+            else if constexpr (kUnit == 8) cp_async8(sto, from);
+            else cp_async16(sto, from);
+            if constexpr (kStageScales == 32) cp_async16(sto + 16, from + 16);
+        } else {
+            const int have = min(GS, row_scales - st * GS) * SB;
+            for (int b = 0; b < kStageScales; b += 2)  // zeros for groups behind K
+                asm volatile("st.shared.b16 [%0], %1;" ::"r"(sto + b), "h"(b < have ? *reinterpret_cast<const unsigned short*>(from + b) : (unsigned short)0) : "memory");
+        }
+    };
+    int l_pass = 0, l_seg = 0, l_i = 0, l_buffer = 0;  // the next stage to issue
+    const auto advance = [&]() {
+        issue(l_pass, l_seg * L::seg_stages + l_i * ks + slot, l_buffer);
+        if (++l_buffer == kStages) l_buffer = 0;
+        if (++l_i == own) {
+            l_i = 0;
+            if (++l_seg == segs) l_seg = 0, ++l_pass;
+        }
+    };
+
+    load_columns(0);
+    advance();
+    cp_commit();
+    advance();
+    cp_commit();
+    int buffer = 0;
+    for (int pass = 0; pass < passes; ++pass) {
+        float acc[2][NT][4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) part[i][j] = 0.f;
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t w[4][2];
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        const uint32_t at = wrow + (((4 * h + p) ^ g) << 4);
-                        w[p][0] = lds32(at);
-                        w[p][1] = lds32(at + 8 * kRowStage);
-                    }
-#pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        const uint4 x = lds128(col + i * 8 * L::x_pitch + (run * kStageK + 32 * h) * 2);
-                        const uint32_t a0[4] = {w[0][0], w[0][1], w[1][0], w[1][1]};
-                        const uint32_t a1[4] = {w[2][0], w[2][1], w[3][0], w[3][1]};
-                        mma<true>(part[i], a0, x.x, x.y, part[i]);
-                        mma<true>(part[i], a1, x.z, x.w, part[i]);
-                    }
+                for (int j = 0; j < 4; ++j) acc[u][i][j] = 0.f;
+        const bool active = row_of(pass, tile, 0) >= 0;
+        for (int s = 0; s < segs; ++s) {
+            const int q = pass * segs + s;
+            for (int i = 0; i < own; ++i) {
+                cp_wait<1>();
+                if (i == 0) {
+                    __syncthreads();  // everyone's columns are there, and nobody reads the other buffer any more
+                    if (q + 1 < passes * segs) load_columns(q + 1);
+                } else {
+                    __syncwarp();
                 }
+                advance();
+                cp_commit();
+                const int at_stage = i * ks + slot;  // in the segment
+                if (active && s * L::seg_stages + at_stage < stages) {
+                    const uint8_t* col = smem + L::x_at + (q & 1) * L::cols * L::x_pitch + g * L::x_pitch + t * 16 + at_stage * kStageK * 2;
+                    const uint32_t wrow = (warp * kStages * kWarpStage + buffer * kWarpStage + g * 128 + t * 4) ^ (g << 4);
+                    const uint8_t* srow_at = smem + L::scales_at + (warp * kStages * kRows + buffer * kRows + g) * kScaleRow;
+                    const float* f = reinterpret_cast<const float*>(smem + L::f_at) + (q & 1) * L::cols * L::seg_runs + 2 * t * L::seg_runs + at_stage * 2;
+                    const float* sum = reinterpret_cast<const float*>(smem + L::sums_at) + (q & 1) * L::most_groups * L::cols + at_stage * GS * L::cols + 2 * t;
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {  // runs of 128; both unrolled are too much code for the instruction cache
+                        constexpr int kHalf = GS / 2, kUnits = 4 / kHalf;  // groups of a run, units of 32 of a group
+                        float run[2][NT][4];
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
+                        for (int j = 0; j < kHalf; ++j) {
+                            float sc[4];  // of rows g, g + 8, g + 16, g + 24
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] += part[i][j];
-            } else {
-                float part[NT][4];
+                            for (int r = 0; r < 4; ++r) {
+                                const uint8_t* p = srow_at + 8 * r * kScaleRow + (h * kHalf + j) * SB;
+                                sc[r] = SB == 2 ? __uint_as_float((uint32_t)*reinterpret_cast<const unsigned short*>(p) << 16) : *reinterpret_cast<const float*>(p);
+                            }
+                            float d[2][NT][4];
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
+                            for (int c = 0; c < NT; ++c) {
+                                const float2 v = *reinterpret_cast<const float2*>(sum + (h * kHalf + j) * L::cols + 8 * c);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) part[i][j] = 0.f;
+                                for (int u = 0; u < 2; ++u) d[u][c][0] = d[u][c][2] = v.x, d[u][c][1] = d[u][c][3] = v.y;
+                            }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float4 s0 = *reinterpret_cast<const float4*>(sc0 + run * 8 + 4 * h);
-                    const float4 s1 = *reinterpret_cast<const float4*>(sc1 + run * 8 + 4 * h);
-                    const float f0[4] = {s0.x, s0.y, s0.z, s0.w}, f1[4] = {s1.x, s1.y, s1.z, s1.w};
+                            for (int k = 0; k < kUnits; ++k) {
+                                const int unit = h * 4 + j * kUnits + k;
+                                const uint8_t* at = smem + (wrow ^ (unit << 4));
+                                uint32_t a[4][4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int j = 4 * h + q;
-                        const uint32_t at = wrow + ((j ^ g) << 4);
-                        uint32_t lo[4], hi[4];
-                        widen<F>(lds32(at), lo);
-                        widen<F>(lds32(at + 8 * kRowStage), hi);
-                        const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+                                for (int r = 0; r < 4; ++r) part(*reinterpret_cast<const uint32_t*>(at + r * 1024), a[r]);
 #pragma unroll
-                        for (int i = 0; i < NT; ++i) {
-                            const uint4 x = lds128(col + i * 8 * L::x_pitch + (run * kChunk + 32 * j) * 2);
-                            float d[4];
-                            mma<false>(d, a0, x.x, x.y, zero);
-                            mma<false>(d, a1, x.z, x.w, d);
-                            part[i][0] = fmaf(f0[q], d[0], part[i][0]);
-                            part[i][1] = fmaf(f0[q], d[1], part[i][1]);
-                            part[i][2] = fmaf(f1[q], d[2], part[i][2]);
-                            part[i][3] = fmaf(f1[q], d[3], part[i][3]);
+                                for (int c = 0; c < NT; ++c) {
+                                    const uint4 b = *reinterpret_cast<const uint4*>(col + c * 8 * L::x_pitch + unit * 64);
+#pragma unroll
+                                    for (int u = 0; u < 2; ++u) mma(d[u][c], a[2 * u][0], a[2 * u + 1][0], a[2 * u][1], a[2 * u + 1][1], b.x, b.y, d[u][c]);
+#pragma unroll
+                                    for (int u = 0; u < 2; ++u) mma(d[u][c], a[2 * u][2], a[2 * u + 1][2], a[2 * u][3], a[2 * u + 1][3], b.z, b.w, d[u][c]);
+                                }
+                            }
+#pragma unroll
+                            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                                for (int c = 0; c < NT; ++c)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const float by = sc[2 * u + (e >> 1)];
+                                        run[u][c][e] = j ? fmaf(by, d[u][c][e], run[u][c][e]) : by * d[u][c][e];
+                                    }
+                        }
+#pragma unroll
+                        for (int c = 0; c < NT; ++c) {
+                            const float by[2] = {f[8 * c * L::seg_runs + h], f[(8 * c + 1) * L::seg_runs + h]};  // of columns 2 t and 2 t + 1
+#pragma unroll
+                            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) acc[u][c][e] = fmaf(by[e & 1], run[u][c][e], acc[u][c][e]);
                         }
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const float x0 = xs[(8 * i + 2 * t) * L::seg_chunks + run], x1 = xs[(8 * i + 2 * t + 1) * L::seg_chunks + run];
-                    acc[i][0] = fmaf(x0, part[i][0], acc[i][0]);
-                    acc[i][1] = fmaf(x1, part[i][1], acc[i][1]);
-                    acc[i][2] = fmaf(x0, part[i][2], acc[i][2]);
-                    acc[i][3] = fmaf(x1, part[i][3], acc[i][3]);
-                }
+                if (++buffer == kStages) buffer = 0;
             }
         }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[u][c][j] *= 0x1p24f;
+        if (ks > 1) {  // the first warp of each tile adds up the others' sums, in their order; they lie over the last columns
+            __syncthreads();
+            float4* red = reinterpret_cast<float4*>(smem + L::x_at + ((pass * segs + segs - 1) & 1) * L::cols * L::x_pitch) + warp * 2 * NT * 32 + lane;
+            if (slot) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int c = 0; c < NT; ++c) red[(u * NT + c) * 32] = make_float4(acc[u][c][0], acc[u][c][1], acc[u][c][2], acc[u][c][3]);
+            }
+            __syncthreads();
+            if (!slot) {
+                for (int o = 1; o < ks; ++o)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int c = 0; c < NT; ++c) {
+                            const float4 v = red[(o * 2 * NT + u * NT + c) * 32];
+                            acc[u][c][0] += v.x, acc[u][c][1] += v.y, acc[u][c][2] += v.z, acc[u][c][3] += v.w;
+                        }
+            }
+        }
+        done(pass, acc);
     }
     cp_wait<0>();
 }
 
-// The tile's sums from the lanes to the buffer [column][128 rows] in shared memory (over the ring), visible to
-// the whole cluster when it returns.
-template <int F, int NT> __device__ __forceinline__ float* gather(uint8_t* smem, const float (&acc)[NT][4], int ranks) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    float* red = reinterpret_cast<float*>(smem);
-    __syncthreads();  // every warp is done with the ring
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        float* p = red + (8 * i + 2 * t) * kRedPitch + 16 * warp + g;
-        p[0] = acc[i][0];
-        p[kRedPitch] = acc[i][1];
-        p[8] = acc[i][2];
-        p[kRedPitch + 8] = acc[i][3];
-    }
-    if (ranks > 1) cooperative_groups::this_cluster().sync(); else __syncthreads();
-    return red;
-}
-
-// One element of the joined tile: column c (or the terms of row c) and tile row r, ranks added in their order.
-template <int Terms> __device__ __forceinline__ float joined(float* red, int ranks, int c, int r) {
-    float v = 0.f;
-    for (int rank = 0; rank < ranks; ++rank) {
-        const float* p = ranks > 1 ? cooperative_groups::this_cluster().map_shared_rank(red, rank) : red;
-        float one = p[c * Terms * kRedPitch + r];
-#pragma unroll
-        for (int t = 1; t < Terms; ++t) one += p[(c * Terms + t) * kRedPitch + r];
-        v = rank ? v + one : one;
-    }
-    return v;
-}
-
-// Before the buffer is written again, or the CTA ends: nobody reads it any more.
-__device__ __forceinline__ void release(int ranks) {
-    if (ranks > 1) cooperative_groups::this_cluster().sync(); else __syncthreads();
-}
-
-// The part of K that this rank takes, in whole runs of 256.
-__device__ __forceinline__ void slice_of(int K, int rank, int ranks, int& k0, int& k1) {
-    const int runs = (K + kChunk - 1) / kChunk;
-    k0 = (int)((int64_t)runs * rank / ranks) * kChunk;
-    k1 = min(K, (int)((int64_t)runs * (rank + 1) / ranks) * kChunk);
-}
-
-// CTAs of a cluster that share a tile's K: the number with the shortest run of rounds of CTAs, where a CTA's time is
-// its runs of 256 and about four more to start and to join.
-inline int cluster_ranks(int64_t tiles, int K) {
-    const int runs = (K + kChunk - 1) / kChunk, at_once = 2 * 152;
+// Warps that share 32 rows along K: as many as leave the busiest CTA the least to do.
+template <typename L> int shared_k(int64_t row_tiles, int ctas, int K) {
+    const int stages = (K + kStageK - 1) / kStageK;
     int best = 1;
-    double least = 1e300;
-    for (int r = 1; r <= 8 && r <= runs; r *= 2) {
-        const int64_t ctas = tiles * r;
-        const double rounds = ctas <= at_once ? 1.0 : (double)ctas / at_once + 0.5;
-        const double t = rounds * ((double)runs / r + 4.0);
-        if (t < least) least = t, best = r;
+    int64_t least = INT64_MAX;
+    for (int ks = 1; ks <= L::most_ks && L::W % ks == 0; ks *= 2) {
+        const int64_t per = L::W / ks, passes = ((row_tiles + per - 1) / per + ctas - 1) / ctas;
+        const int64_t t = passes * ((stages + ks - 1) / ks);
+        if (t < least) least = t, best = ks;
     }
     return best;
 }

@@ -433,6 +433,13 @@ static __device__ __noinline__ float direct(const uint8_t* codes, const uint8_t*
     return sum;
 }
 
+// The part of K that a rank of a cluster takes, in whole runs of 256.
+__device__ __forceinline__ void slice_of(int K, int rank, int ranks, int& k0, int& k1) {
+    const int runs = (K + kStageK - 1) / kStageK;
+    k0 = (int)((int64_t)runs * rank / ranks) * kStageK;
+    k1 = min(K, (int)((int64_t)runs * (rank + 1) / ranks) * kStageK);
+}
+
 // The rows of a tile that a rank joins and writes, in fours.
 __device__ __forceinline__ void rows_of(int rank, int ranks, int& r0, int& r1) {
     r0 = 32 * rank / ranks * 4;

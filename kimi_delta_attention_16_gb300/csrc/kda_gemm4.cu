@@ -2,8 +2,8 @@
 // (e2m1 or offset integers under one scale per group): the projections of a decode step.
 //
 // What a call has to read is N K / 2 bytes of codes and their scales.  e2m1 weights go through the block-scaled tensor
-// cores (kda_few_tc.cuh), integer codes through registers (kda_few.cuh).  A CTA takes 128 of the N outputs for some
-// tokens, a cluster splits K.
+// cores (kda_few_tc.cuh): a CTA takes 128 of the N outputs for some tokens, a cluster splits K.  Integer codes go
+// through registers (kda_few.cuh).
 #include "kda_few.cuh"
 #include "kda_few_tc.cuh"
 #include "kda_serve.cuh"
@@ -14,62 +14,82 @@ namespace {
 
 using namespace few;
 
+// ------------------------------------------------------------------ integer codes
 struct Gemm4 {
-    Matrix w;
-    int M, N, K, epi, ranks;
+    Weights w;
+    Columns x;
+    int M, N, K, epi, ks, group;
+    int64_t ldc;
     const bf16* a;
     int64_t lda;
-    bool wide;
-    int64_t ldc;
 };
 
-template <int F, int NT, typename Tout>
-__global__ void __launch_bounds__(kThreads, 2) k_gemm4(const Gemm4 p, Tout* __restrict__ out) {
-    using L = Layout<F, NT>;
+__device__ __forceinline__ float apply(int epi, float v) {
+    return epi == KDA_EPI_NONE ? v : (epi == KDA_EPI_DECAY ? -5.0f : 1.0f) / (1.0f + expf(-v));
+}
+
+// A CTA takes an equal share of the tiles of 32 rows, 12 / ks at a time (8 / ks where more scales leave room for 8 warps'
+// rings only).
+constexpr int warps_for(int scale_row) { return scale_row <= 8 ? 12 : 8; }
+
+template <int NT, int GS, int SB> __global__ void __launch_bounds__(32 * warps_for(GS * SB), 1) k_gemm4(const Gemm4 p, void* __restrict__ out, bool out32) {
+    using L = Layout<warps_for(GS * SB), NT, GS, SB>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int of[L::cols];
-    const int rank = blockIdx.x % p.ranks, row0 = blockIdx.x / p.ranks * kTileRows;
-    const int c0 = blockIdx.y * L::cols, n = min(L::cols, p.M - c0);
+    const int c0 = blockIdx.y * L::cols, n = min(L::cols, p.M - c0), per = L::W / p.ks;
+    const int tiles = (p.N + kRows - 1) / kRows;
+    const int first = (int)((int64_t)tiles * blockIdx.x / gridDim.x), last = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
     if (threadIdx.x < L::cols) of[threadIdx.x] = c0 + threadIdx.x;
     __syncthreads();
-    int k0, k1;
-    slice_of(p.K, rank, p.ranks, k0, k1);
-    const auto row_of = [&](int r) { return (int64_t)min(row0 + r, p.N - 1); };
-    float acc[NT][4];
-    product<F, NT>(smem, p.w, p.K, row_of, Bf16Rows{p.a, p.lda, p.wide}, of, n, k0, k1, acc);
-    float* red = gather<F, NT>(smem, acc, p.ranks);
-    const int share = kTileRows / p.ranks;
-    for (int i = threadIdx.x; i < n * share; i += kThreads) {
-        const int c = i / share, r = rank * share + i % share;
-        if (row0 + r >= p.N) continue;
-        float v = joined<1>(red, p.ranks, c, r);
-        if (p.epi != KDA_EPI_NONE) v = (p.epi == KDA_EPI_DECAY ? -5.0f : 1.0f) / (1.0f + expf(-v));
-        out[(int64_t)(c0 + c) * p.ldc + row0 + r] = from_f<Tout>(v);
-    }
-    if (p.ranks > 1) release(p.ranks);
+    wait_for_kernel_before();  // the columns
+    const auto row_of = [&](int pass, int tile, int r) -> int64_t {
+        const int at = first + pass * per + tile;
+        return at < last ? min(at * kRows + r, p.N - 1) : -1;
+    };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    products<L>(smem, p.w, p.x, p.K, of, n, p.ks, (last - first + per - 1) / per, row_of, [&](int pass, const float (&acc)[2][NT][4]) {
+        const int at = first + pass * per + warp / p.ks;
+        if (warp % p.ks || at >= last) return;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int col = 8 * c + 2 * t + (j & 1), row = at * kRows + 16 * u + g + 8 * (j >> 1);
+                    if (col >= n || row >= p.N) continue;
+                    float v = acc[u][c][j];
+                    if (isnan(v))
+                        v = direct(p.w.codes + (int64_t)row * (p.K / 2), p.w.scales + (int64_t)row * (p.K / p.group) * SB, SB, p.group,
+                                   p.a + (int64_t)(c0 + col) * p.lda, p.K);
+                    v = apply(p.epi, v);
+                    const int64_t o = (int64_t)(c0 + col) * p.ldc + row;
+                    if (out32) static_cast<float*>(out)[o] = v; else static_cast<bf16*>(out)[o] = from_f<bf16>(v);
+                }
+    });
 }
 
-template <int F, int NT, typename Tout> cudaError_t launch(const kda_gemm4_args& a, int ranks, cudaStream_t s) {
-    using L = Layout<F, NT>;
+template <int NT, int GS, int SB> cudaError_t launch(const kda_gemm4_args& a, cudaStream_t s) {
+    using L = Layout<warps_for(GS * SB), NT, GS, SB>;
+    const Columns columns = columns_at(a.workspace, a.M, a.K);
+    const bool wide = reinterpret_cast<uintptr_t>(a.A) % 16 == 0 && (a.lda % 8 == 0 || a.M == 1);
+    if (const cudaError_t e = launch_halves(static_cast<const bf16*>(a.A), a.lda, wide, a.M, a.K, a.group, columns, s)) return e;
     Gemm4 p;
-    p.w = Matrix{a.codes, a.scales, a.format == KDA_WEIGHT_E2M1 ? 0 : a.scale_dtype == KDA_BF16 ? 1 : 2, group_shift(a.group)};
-    p.M = a.M, p.N = a.N, p.K = a.K, p.epi = a.epilogue, p.ranks = ranks;
+    p.w = Weights{a.codes, static_cast<const uint8_t*>(a.scales)};
+    p.x = columns;
+    p.M = a.M, p.N = a.N, p.K = a.K, p.epi = a.epilogue, p.ldc = a.ldc, p.group = a.group;
     p.a = static_cast<const bf16*>(a.A), p.lda = a.lda;
-    p.wide = reinterpret_cast<uintptr_t>(a.A) % 16 == 0 && (a.lda % 8 == 0 || a.M == 1);
-    p.ldc = a.ldc;
-    return launch_kernel(k_gemm4<F, NT, Tout>, dim3((a.N + kTileRows - 1) / kTileRows * ranks, (a.M + L::cols - 1) / L::cols), kThreads, ranks,
-                         L::bytes, false, s, p, static_cast<Tout*>(a.C));
+    const int tiles = (a.N + kRows - 1) / kRows, blocks = (a.M + L::cols - 1) / L::cols;
+    p.ks = shared_k<L>(tiles, 152, a.K);
+    const int ctas = (tiles * p.ks + L::W - 1) / L::W;
+    return launch_kernel(k_gemm4<NT, GS, SB>, dim3(ctas < 152 ? ctas : 152, blocks), L::threads, 1, L::bytes, true, s, p, a.C, a.c_dtype == KDA_FP32);
 }
 
-template <int F, int NT> cudaError_t launch_out(const kda_gemm4_args& a, int ranks, cudaStream_t s) {
-    return a.c_dtype == KDA_BF16 ? launch<F, NT, bf16>(a, ranks, s) : launch<F, NT, float>(a, ranks, s);
+template <int NT, int SB> cudaError_t launch_group(const kda_gemm4_args& a, cudaStream_t s) {
+    return a.group == 32 ? launch<NT, 8, SB>(a, s) : a.group == 64 ? launch<NT, 4, SB>(a, s) : launch<NT, 2, SB>(a, s);
 }
-
-template <int F> cudaError_t launch_cols(const kda_gemm4_args& a, int ranks, cudaStream_t s) {
-    if (a.M <= 8) return launch_out<F, 1>(a, ranks, s);
-    if (a.M <= 16) return launch_out<F, 2>(a, ranks, s);
-    if (a.M <= 32) return launch_out<F, 4>(a, ranks, s);
-    return launch_out<F, 8>(a, ranks, s);
+template <int NT> cudaError_t launch_scales(const kda_gemm4_args& a, cudaStream_t s) {
+    return a.scale_dtype == KDA_BF16 ? launch_group<NT, 2>(a, s) : launch_group<NT, 4>(a, s);
 }
 
 // ------------------------------------------------------------------ block-scaled tensor cores
@@ -86,7 +106,7 @@ __global__ void __launch_bounds__(fewtc::kThreads, fewtc::Shape<N>::per_sm) k_ge
                                                                                       Tout* __restrict__ out) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ fewtc::Barriers bar;
-    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t raw = tc::smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
     const int rank = blockIdx.x % p.ranks, row0 = blockIdx.x / p.ranks * kTileRows;
     constexpr int kTokens = fewtc::Shape<N>::tokens;
@@ -96,7 +116,7 @@ __global__ void __launch_bounds__(fewtc::kThreads, fewtc::Shape<N>::per_sm) k_ge
     t.w = &maps.w, t.b = &maps.b;
     t.row0 = row0, t.row64 = row0 + 64, t.token0 = c0;
     t.w_scales = p.w_scales, t.b_scales = p.b_scales, t.last_row = p.N - 1, t.last_token = p.M - 1, t.K = p.K;
-    slice_of(p.K, rank, p.ranks, t.k0, t.k1);
+    fewtc::slice_of(p.K, rank, p.ranks, t.k0, t.k1);
     fewtc::Counters count;
     float* red = reinterpret_cast<float*>(smem);
     fewtc::product<N>(smem, bar, t, count, red);
@@ -114,7 +134,7 @@ __global__ void __launch_bounds__(fewtc::kThreads, fewtc::Shape<N>::per_sm) k_ge
             const int64_t row = row0 + r + j;
             if (isnan(v[j]) && j < left)
                 v[j] = fewtc::direct(p.codes + row * (p.K / 2), p.w_scales + row * (p.K / 32), p.a + (int64_t)(c0 + c) * p.lda, p.K);
-            if (p.epi != KDA_EPI_NONE) v[j] = (p.epi == KDA_EPI_DECAY ? -5.0f : 1.0f) / (1.0f + expf(-v[j]));
+            v[j] = apply(p.epi, v[j]);
         }
         Tout* o = out + (int64_t)(c0 + c) * p.ldc + row0 + r;
         if (left >= 4 && reinterpret_cast<uintptr_t>(o) % (4 * sizeof(Tout)) == 0) {
@@ -130,7 +150,7 @@ __global__ void __launch_bounds__(fewtc::kThreads, fewtc::Shape<N>::per_sm) k_ge
                 if (j < left) o[j] = from_f<Tout>(v[j]);
         }
     }
-    release(p.ranks);
+    if (p.ranks > 1) cooperative_groups::this_cluster().sync(); else __syncthreads();
     fewtc::finish<N>(bar, p.d_status);
 }
 
@@ -159,7 +179,7 @@ template <int N> cudaError_t launch_tc_out(const kda_gemm4_args& a, cudaStream_t
 }  // namespace
 
 size_t gemm4_workspace(const kda_gemm4_args& a) {
-    return a.format == KDA_WEIGHT_E2M1 ? fewtc::digits_bytes(a.M, a.K) + fewtc::digit_scales_bytes(a.M, a.K) : 0;
+    return a.format == KDA_WEIGHT_E2M1 ? fewtc::digits_bytes(a.M, a.K) + fewtc::digit_scales_bytes(a.M, a.K) : columns_bytes(a.M, a.K, a.group);
 }
 
 cudaError_t launch_gemm4(const kda_gemm4_args& a, cudaStream_t s) {
@@ -170,9 +190,9 @@ cudaError_t launch_gemm4(const kda_gemm4_args& a, cudaStream_t s) {
         if (a.M <= 16) return launch_tc_out<128>(a, s);
         return launch_tc_out<256>(a, s);
     }
-    const int64_t tiles = (int64_t)((a.N + kTileRows - 1) / kTileRows) * ((a.M + 63) / 64);
-    const int ranks = cluster_ranks(tiles, a.K);
-    return launch_cols<KDA_WEIGHT_INT4>(a, ranks, s);
+    if (a.M <= 8) return launch_scales<1>(a, s);
+    if (a.M <= 16) return launch_scales<2>(a, s);
+    return launch_scales<4>(a, s);
 }
 
 }  // namespace kda

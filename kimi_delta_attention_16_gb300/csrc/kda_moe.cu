@@ -248,88 +248,146 @@ __global__ void __launch_bounds__(kPickThreads) k_moe_pick(const Wide* __restric
     for (int i = threadIdx.x; i < slots; i += kPickThreads) listed[atomicAdd(&begin[__ldcg(ids + i)], 1)] = i;
 }
 
-// ------------------------------------------------------------------ the experts' products
+// ------------------------------------------------------------------ experts in integer codes
+constexpr int kExpertWarps = 8;
+
 struct Experts {
-    const uint8_t* w;
-    const uint8_t* scales;
+    Weights w;                 // of expert 0
     int64_t w_bytes, s_bytes;  // of one expert
-    int scale_type, group_shift;
-    int rows, K;               // of one expert's matrix
+    Columns x;
+    int rows, K, group;        // of one expert's matrix
     const int* lists;
-    int E, top, ranks;
-    __device__ __forceinline__ Matrix matrix(int e) const {
-        return Matrix{w + e * w_bytes, scales + e * s_bytes, scale_type, group_shift};
-    }
+    int E, top;
+    __device__ __forceinline__ Weights matrix(int e) const { return Weights{w.codes + e * w_bytes, w.scales + e * s_bytes}; }
 };
 
-// hidden[slot][f] = silu(g) u: the tile's rows are 64 of the gate's and the same 64 of the other half.
-template <int F, int NT>
-__global__ void __launch_bounds__(kThreads, 2) k_moe_in(const Experts p, const Bf16Rows src, float* __restrict__ hidden) {
-    using L = Layout<F, NT>;
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int of[L::cols], slot[L::cols];
-    wait_for_kernel_before();
-    let_next_kernel_begin();
-    if ((int)blockIdx.y >= p.lists[0]) return;  // the whole cluster
-    const int e = p.lists[1 + blockIdx.y], first = p.lists[1 + p.E + blockIdx.y], last = p.lists[2 + p.E + blockIdx.y];
-    const int* slots = p.lists + 2 + 2 * p.E;
-    const int rank = blockIdx.x % p.ranks, row0 = blockIdx.x / p.ranks * (kTileRows / 2), half = p.rows / 2;
-    int k0, k1;
-    slice_of(p.K, rank, p.ranks, k0, k1);
-    const auto row_of = [&](int r) { return (int64_t)(min(row0 + (r & 63), half - 1) + (r >= 64 ? half : 0)); };
-    const Matrix m = p.matrix(e);
-    for (int c0 = first; c0 < last; c0 += L::cols) {
-        const int n = min(L::cols, last - c0);
-        if (threadIdx.x < n) {
-            slot[threadIdx.x] = slots[c0 + threadIdx.x];
-            of[threadIdx.x] = slots[c0 + threadIdx.x] / p.top;
-        }
-        __syncthreads();
-        float acc[NT][4];
-        product<F, NT>(smem, m, p.K, row_of, src, of, n, k0, k1, acc);
-        float* red = gather<F, NT>(smem, acc, p.ranks);
-        const int share = 64 / p.ranks;
-        for (int i = threadIdx.x; i < n * share; i += kThreads) {
-            const int c = i / share, r = rank * share + i % share;
-            if (row0 + r >= half) continue;
-            const float gate = joined<1>(red, p.ranks, c, r), up = joined<1>(red, p.ranks, c, r + 64);
-            hidden[(int64_t)slot[c] * half + row0 + r] = gate / (1.0f + expf(-gate)) * up;
-        }
-        release(p.ranks);
-    }
-}
+struct Direct {  // the operands as they were given, for sums that come out as NaN
+    const uint8_t *codes, *scales;
+    const bf16* x;
+    int64_t xs;
+};
 
-// parts[slot][d] = w_slot W_out hidden_slot.
-template <int F, int NT>
-__global__ void __launch_bounds__(kThreads, 2) k_moe_out(const Experts p, const float* __restrict__ hidden, const float* __restrict__ weights,
-                                                         float* __restrict__ parts) {
-    using L = Layout<F, NT>;
-    constexpr int kTerms = Format<F>::terms, kRows = L::cols / kTerms;
+
+// First products.  Warps 0 to 3 take 128 rows of the gate's half, 4 to 7 the same of the other; the hidden values become
+// two columns of the second products' (value and remainder) where they arise, 128 rows under one power of two.
+template <int NT, int GS, int SB>
+__global__ void __launch_bounds__(32 * kExpertWarps, 1) k_moe_in(const Experts p, const Direct given, const Columns hidden) {
+    using L = Layout<kExpertWarps, NT, GS, SB>;
+    constexpr int kPitch = 256 + 4;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int of[kRows];
+    __shared__ int of[L::cols];
+    float* sums = reinterpret_cast<float*>(smem + L::bytes);  // [cols][256 rows]
     wait_for_kernel_before();
     let_next_kernel_begin();
     if ((int)blockIdx.y >= p.lists[0]) return;
     const int e = p.lists[1 + blockIdx.y], first = p.lists[1 + p.E + blockIdx.y], last = p.lists[2 + p.E + blockIdx.y];
     const int* slots = p.lists + 2 + 2 * p.E;
-    const int rank = blockIdx.x % p.ranks, row0 = blockIdx.x / p.ranks * kTileRows;
-    int k0, k1;
-    slice_of(p.K, rank, p.ranks, k0, k1);
-    const auto row_of = [&](int r) { return (int64_t)min(row0 + r, p.rows - 1); };
-    const Matrix m = p.matrix(e);
-    for (int c0 = first; c0 < last; c0 += kRows) {
-        const int n = min(kRows, last - c0);
-        if (threadIdx.x < n) of[threadIdx.x] = slots[c0 + threadIdx.x];
+    const int row0 = blockIdx.x * 128, F = p.rows / 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int runs = (F + kRun - 1) / kRun;
+    const auto row_of = [&](int, int tile, int r) -> int64_t { return min(row0 + few::kRows * (tile & 3) + r, F - 1) + (tile >= 4 ? F : 0); };
+    const Weights m = p.matrix(e);
+    for (int c0 = first; c0 < last; c0 += L::cols) {
+        const int n = min(L::cols, last - c0);
         __syncthreads();
-        float acc[NT][4];
-        product<F, NT>(smem, m, p.K, row_of, F32Rows{hidden, p.K}, of, n, k0, k1, acc);
-        float* red = gather<F, NT>(smem, acc, p.ranks);
-        const int share = kTileRows / p.ranks;
-        for (int i = threadIdx.x; i < n * share; i += kThreads) {
-            const int c = i / share, r = rank * share + i % share;
-            if (row0 + r < p.rows) parts[(int64_t)of[c] * p.rows + row0 + r] = weights[of[c]] * joined<kTerms>(red, p.ranks, c, r);
+        if (threadIdx.x < n) of[threadIdx.x] = slots[c0 + threadIdx.x] / p.top;
+        __syncthreads();
+        products<L>(smem, m, p.x, p.K, of, n, 1, 1, row_of, [&](int, const float (&acc)[2][NT][4]) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int c = 0; c < NT; ++c)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sums[(8 * c + 2 * t + (j & 1)) * kPitch + few::kRows * warp + 16 * u + g + 8 * (j >> 1)] = acc[u][c][j];
+        });
+        __syncthreads();
+        __half* columns = const_cast<__half*>(hidden.x);
+        float *factor = const_cast<float*>(hidden.factor), *group_sums = const_cast<float*>(hidden.sums);
+        const int out_groups = F / p.group;
+        // a warp per token: four values a lane, rows 32 i + lane
+        for (int c = warp; c < n; c += kExpertWarps) {
+            float v[4];
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float gate = sums[c * kPitch + 32 * i + lane], up = sums[c * kPitch + 128 + 32 * i + lane];
+                if (row0 + 32 * i + lane < F && (isnan(gate) || isnan(up))) {
+                    const bf16* x = given.x + of[c] * given.xs;
+                    const int64_t rg = row0 + 32 * i + lane, ru = rg + F;
+                    const int row_scales = p.K / p.group * SB;
+                    gate = few::direct(m.codes + rg * (p.K / 2), m.scales + rg * row_scales, SB, p.group, x, p.K);
+                    up = few::direct(m.codes + ru * (p.K / 2), m.scales + ru * row_scales, SB, p.group, x, p.K);
+                }
+                v[i] = row0 + 32 * i + lane < F ? gate / (1.0f + expf(-gate)) * up : 0.f;
+                top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+            }
+            top = __reduce_max_sync(0xffffffffu, top);
+            float up, down;
+            run_scale(top >> 23, up, down);
+            // element k of eight lies at the place where codes come out of a word: (0,4) (1,5) (2,6) (3,7)
+            const int place = (lane & ~7) + 2 * (lane & 3) + (lane >> 2 & 1);
+            const int64_t at = (int64_t)(c0 + c) * 2;
+            const float by = lane & 1 ? 0.0625f : 1.f, back = lane & 1 ? 16.f : 1.f;
+            float sum_hi = 0.f, sum_lo = 0.f;  // of a group, as far as it goes
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (row0 + 32 * i >= F) break;  // F is a multiple of the group
+                const float x = v[i] * up * by;
+                const __half hi = __float2half_rn(x);
+                const float h = __half2float(hi);
+                const __half lo = __float2half_rn(isinf(h) ? 0.f : x - h);
+                columns[at * F + row0 + 32 * i + place] = hi;
+                columns[(at + 1) * F + row0 + 32 * i + place] = lo;
+                sum_hi += h * back, sum_lo += __half2float(lo) * back;
+                if ((i + 1) * 32 % p.group == 0) {
+#pragma unroll
+                    for (int d = 16; d; d >>= 1) {
+                        sum_hi += __shfl_xor_sync(0xffffffffu, sum_hi, d);
+                        sum_lo += __shfl_xor_sync(0xffffffffu, sum_lo, d);
+                    }
+                    const int group = (row0 + 32 * i) / p.group;
+                    if (lane < 2) group_sums[(at + lane) * out_groups + group] = kSumOf * (lane ? sum_lo : sum_hi);
+                    sum_hi = sum_lo = 0.f;
+                }
+            }
+            if (lane < 2) factor[(at + lane) * runs + blockIdx.x] = down;
         }
-        release(p.ranks);
+    }
+}
+
+// Second products: parts[slot][d] = w_slot W_out hidden_slot, from two columns a slot.
+template <int NT, int GS, int SB>
+__global__ void __launch_bounds__(32 * kExpertWarps, 1) k_moe_out(const Experts p, const float* __restrict__ weights, float* __restrict__ parts) {
+    using L = Layout<kExpertWarps, NT, GS, SB>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int of[L::cols];
+    wait_for_kernel_before();
+    let_next_kernel_begin();
+    if ((int)blockIdx.y >= p.lists[0]) return;
+    const int e = p.lists[1 + blockIdx.y], first = p.lists[1 + p.E + blockIdx.y], last = p.lists[2 + p.E + blockIdx.y];
+    const int* slots = p.lists + 2 + 2 * p.E;
+    const int row0 = blockIdx.x * 256, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const auto row_of = [&](int, int tile, int r) -> int64_t { return row0 + few::kRows * tile < p.rows ? min(row0 + few::kRows * tile + r, p.rows - 1) : -1; };
+    const Weights m = p.matrix(e);
+    for (int c0 = first; c0 < last; c0 += L::cols / 2) {
+        const int n = min(L::cols / 2, last - c0);
+        __syncthreads();
+        if (threadIdx.x < 2 * n) of[threadIdx.x] = 2 * c0 + threadIdx.x;
+        __syncthreads();
+        products<L>(smem, m, p.x, p.K, of, 2 * n, 1, 1, row_of, [&](int, const float (&acc)[2][NT][4]) {
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+                const int token = 4 * c + t;  // columns 8 c + 2 t and the next
+                if (token >= n) continue;
+                const int slot = slots[c0 + token];
+                const float w = weights[slot];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int row = row0 + few::kRows * warp + g + 8 * j;
+                    const float(&s)[4] = acc[j >> 1][c];
+                    if (row < p.rows) parts[(int64_t)slot * p.rows + row] = w * (s[2 * (j & 1)] + s[2 * (j & 1) + 1]);
+                }
+            }
+        });
     }
 }
 
@@ -340,12 +398,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_moe_out(const Experts p, const 
 //
 // A kernel may begin beside the one in front of it.  Where that is not the choice itself the lists are complete by then
 // (that one has waited for the choice), so weights and their scales can be on their way before the columns are written.
-struct Direct {  // the operands as they were given, for sums that come out as NaN
-    const uint8_t *codes, *scales;
-    const bf16* x;
-    int64_t xs;
-};
-
 // First products: the hidden values become digits (four bf16 columns, the last of zeros, for bf16 weights) where they
 // arise.  32 rows of a token share a scale: a warp's lanes.
 template <int N, bool Mx>
@@ -354,7 +406,7 @@ k_moe_in_tc(const __grid_constant__ fewtc::Maps maps, const fewtc::StayArgs p, c
             uint8_t* __restrict__ scales, int* d_status) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ fewtc::StayBarriers bar;
-    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t raw = tc::smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
     const int lane = threadIdx.x & 31, F = p.half;
     const int* slots = p.lists + 2 + 2 * p.E;
@@ -396,7 +448,7 @@ k_moe_out_tc(const __grid_constant__ fewtc::Maps maps, const fewtc::StayArgs p, 
              int* d_status) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ fewtc::StayBarriers bar;
-    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t raw = tc::smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
     const int* slots = p.lists + 2 + 2 * p.E;
     fewtc::stay<N, Mx ? 8 : 4, Mx>(smem, bar, maps, p, d_status, [&](int, int row0, int c0, int n, const float* red, int q) {
@@ -443,14 +495,15 @@ template <typename Tr> cudaError_t launch_scores(const kda_moe_args& a, int64_t 
                          sg, score, key, done);
 }
 
-template <int F, int NT>
-cudaError_t launch_experts(const kda_moe_args& a, const Experts& in, const Experts& out, const Bf16Rows& src, float* hidden, const float* weights,
-                           float* parts, int most, cudaStream_t s) {
-    using L = Layout<F, NT>;
-    cudaError_t e = launch_kernel(k_moe_in<F, NT>, dim3((a.F + 63) / 64 * in.ranks, most), kThreads, in.ranks, L::bytes, true, s, in, src, hidden);
+template <int NT, int GS, int SB>
+cudaError_t launch_experts(const kda_moe_args& a, const Experts& in, const Experts& out, const Direct& given, const float* weights, float* parts,
+                           int most, cudaStream_t s) {
+    using L = Layout<kExpertWarps, NT, GS, SB>;
+    constexpr int kSums = L::cols * (256 + 4) * 4;
+    static_assert(L::bytes + kSums <= 227 * 1024, "shared memory of an SM");
+    const cudaError_t e = launch_kernel(k_moe_in<NT, GS, SB>, dim3((a.F + 127) / 128, most), L::threads, 1, L::bytes + kSums, true, s, in, given, out.x);
     if (e) return e;
-    return launch_kernel(k_moe_out<F, NT>, dim3((a.D + kTileRows - 1) / kTileRows * out.ranks, most), kThreads, out.ranks, L::bytes, true, s, out,
-                          (const float*)hidden, weights, parts);
+    return launch_kernel(k_moe_out<NT, GS, SB>, dim3((a.D + 255) / 256, most), L::threads, 1, L::bytes, true, s, out, weights, parts);
 }
 
 template <int N, bool Mx>
@@ -527,16 +580,13 @@ cudaError_t launch_experts_tc(const kda_moe_args& a, const MoePlan& p, const int
     }
 }
 
-template <int F, typename... A> cudaError_t launch_width(int columns, A&&... args) {
-    if (columns <= 8) return launch_experts<F, 1>(std::forward<A>(args)...);
-    if (columns <= 16) return launch_experts<F, 2>(std::forward<A>(args)...);
-    return launch_experts<F, 4>(std::forward<A>(args)...);
+template <int NT, int SB, typename... A> cudaError_t launch_group(int group, A&&... args) {
+    return group == 32   ? launch_experts<NT, 8, SB>(std::forward<A>(args)...)
+           : group == 64 ? launch_experts<NT, 4, SB>(std::forward<A>(args)...)
+                         : launch_experts<NT, 2, SB>(std::forward<A>(args)...);
 }
-
-size_t weight_bytes(const kda_moe_args& a, int64_t rows, int64_t K) { return a.format == KDA_WEIGHT_BF16 ? rows * K * 2 : rows * K / 2; }
-size_t scale_bytes(const kda_moe_args& a, int64_t rows, int64_t K) {
-    if (a.format == KDA_WEIGHT_BF16) return 0;
-    return rows * (K / a.group) * (a.format == KDA_WEIGHT_E2M1 ? 1 : a.scale_dtype == KDA_BF16 ? 2 : 4);
+template <int NT, typename... A> cudaError_t launch_codes(bool bf16_scales, A&&... args) {
+    return bf16_scales ? launch_group<NT, 2>(std::forward<A>(args)...) : launch_group<NT, 4>(std::forward<A>(args)...);
 }
 
 }  // namespace
@@ -557,8 +607,8 @@ MoePlan moe_plan(const kda_moe_args& a) {
     p.weights = take(slots * 4);
     p.lists = take((2 + 2 * (size_t)a.E + slots) * 4);
     const bool mx = a.format == KDA_WEIGHT_E2M1, tc = mx || a.format == KDA_WEIGHT_BF16;
-    p.x_columns = take(mx ? fewtc::digits_bytes(slots, a.D) + fewtc::digit_scales_bytes(slots, a.D) : tc ? slots * a.D * 2 : 0);
-    p.hidden = take(mx ? fewtc::digits_bytes(slots, a.F) + fewtc::digit_scales_bytes(slots, a.F) : tc ? slots * a.F * 8 : slots * a.F * 4);
+    p.x_columns = take(mx ? fewtc::digits_bytes(slots, a.D) + fewtc::digit_scales_bytes(slots, a.D) : tc ? slots * a.D * 2 : few::columns_bytes(a.M, a.D, a.group));
+    p.hidden = take(mx ? fewtc::digits_bytes(slots, a.F) + fewtc::digit_scales_bytes(slots, a.F) : tc ? slots * a.F * 8 : few::columns_bytes(2 * slots, a.F, a.group));
     p.parts = take(slots * a.D * 4);
     p.workspace = at;
     return p;
@@ -582,14 +632,16 @@ cudaError_t launch_moe(const kda_moe_args& a, const MoePlan& p, cudaStream_t s) 
     const bool mx = a.format == KDA_WEIGHT_E2M1, tc = mx || a.format == KDA_WEIGHT_BF16;
     const bool by_token = tc && a.M == columns && a.M <= (mx ? 16 : 64);
     cudaError_t e;
-    if (by_token) {
+    // columns that need no lists come first: the router's scores run beside them
+    if (by_token || !tc) {
         uint8_t* xc = reinterpret_cast<uint8_t*>(ws + p.x_columns);
-        e = mx ? fewtc::launch_digits(x, xs, xwide, nullptr, 1, a.M, a.D, xc, xc + fewtc::digits_bytes(a.M, a.D), s)
-               : fewtc::launch_rows(x, xs, xwide, nullptr, 1, a.M, a.D, reinterpret_cast<bf16*>(xc), s);
+        e = mx   ? fewtc::launch_digits(x, xs, xwide, nullptr, 1, a.M, a.D, xc, xc + fewtc::digits_bytes(a.M, a.D), s)
+            : tc ? fewtc::launch_rows(x, xs, xwide, nullptr, 1, a.M, a.D, reinterpret_cast<bf16*>(xc), s)
+                 : launch_halves(x, xs, xwide, a.M, a.D, a.group, columns_at(xc, a.M, a.D), s);
         if (e) return e;
     }
-    e = a.router_dtype == KDA_BF16 ? launch_scores<bf16>(a, xs, xwide, score, key, done, by_token, s)
-                                   : launch_scores<float>(a, xs, xwide, score, key, done, by_token, s);
+    e = a.router_dtype == KDA_BF16 ? launch_scores<bf16>(a, xs, xwide, score, key, done, by_token || !tc, s)
+                                   : launch_scores<float>(a, xs, xwide, score, key, done, by_token || !tc, s);
     if (e) return e;
     if ((e = launch_kernel(k_moe_pick, dim3(a.M), kPickThreads, 1, 0, true, s, score, key, a.M, a.E, a.top, (int)(a.score == KDA_SCORE_SIGMOID),
                            a.scale, ids, weights, done, lists, a.ids, a.weights)))
@@ -599,21 +651,21 @@ cudaError_t launch_moe(const kda_moe_args& a, const MoePlan& p, cudaStream_t s) 
     } else if (tc) {
         e = launch_experts_tc<false>(a, p, lists, x, xs, xwide, weights, parts, most, columns, by_token, s);
     } else {
+        const int sb = a.scale_dtype == KDA_BF16 ? 2 : 4;
         Experts in = {}, out = {};
-        float* hidden = reinterpret_cast<float*>(ws + p.hidden);
-        in.w = static_cast<const uint8_t*>(a.w_in), in.scales = static_cast<const uint8_t*>(a.w_in_scales);
-        in.w_bytes = weight_bytes(a, 2 * a.F, a.D), in.s_bytes = scale_bytes(a, 2 * a.F, a.D);
-        in.scale_type = a.scale_dtype == KDA_BF16 ? 1 : 2;
-        in.group_shift = group_shift(a.group);
-        in.rows = 2 * a.F, in.K = a.D, in.lists = lists, in.E = a.E, in.top = a.top;
-        in.ranks = cluster_ranks((int64_t)most * ((a.F + 63) / 64), a.D);
+        in.w = Weights{static_cast<const uint8_t*>(a.w_in), static_cast<const uint8_t*>(a.w_in_scales)};
+        in.w_bytes = (int64_t)a.F * a.D, in.s_bytes = (int64_t)2 * a.F * (a.D / a.group) * sb;
+        in.x = columns_at(ws + p.x_columns, a.M, a.D);
+        in.rows = 2 * a.F, in.K = a.D, in.group = a.group, in.lists = lists, in.E = a.E, in.top = a.top;
         out = in;
-        out.w = static_cast<const uint8_t*>(a.w_out), out.scales = static_cast<const uint8_t*>(a.w_out_scales);
-        out.w_bytes = weight_bytes(a, a.D, a.F), out.s_bytes = scale_bytes(a, a.D, a.F);
+        out.w = Weights{static_cast<const uint8_t*>(a.w_out), static_cast<const uint8_t*>(a.w_out_scales)};
+        out.w_bytes = (int64_t)a.D * a.F / 2, out.s_bytes = (int64_t)a.D * (a.F / a.group) * sb;
+        out.x = columns_at(ws + p.hidden, 2 * (int64_t)slots, a.F);
         out.rows = a.D, out.K = a.F;
-        out.ranks = cluster_ranks((int64_t)most * ((a.D + kTileRows - 1) / kTileRows), a.F);
-        const Bf16Rows src{x, xs, xwide};
-        e = launch_width<KDA_WEIGHT_INT4>(columns, a, in, out, src, hidden, weights, parts, most, s);
+        const Direct given{nullptr, nullptr, x, xs};
+        // 16 columns where an expert may have more than four tokens
+        e = columns <= 4 ? launch_codes<1>(sb == 2, a.group, a, in, out, given, weights, parts, most, s)
+                         : launch_codes<2>(sb == 2, a.group, a, in, out, given, weights, parts, most, s);
     }
     if (e) return e;
     const dim3 grid((a.D + 1023) / 1024, a.M);

@@ -19,8 +19,8 @@ struct MoePlan {
     size_t ids;      // [M * top] int: experts by token and rank
     size_t weights;  // [M * top] fp32
     size_t lists;    // int: [1] experts in use, [E] which, [E + 1] where their slots begin, [M * top] slots
-    size_t x_columns; // e2m1 experts: digits of the tokens' values and their scales; bf16 experts: the tokens' rows
-    size_t hidden;   // [M * top][F] fp32; digits and scales (e2m1 experts); four bf16 columns (bf16 experts)
+    size_t x_columns; // the tokens' columns: digits and scales (e2m1 experts), bf16 rows, or fp16 and factors (integer codes)
+    size_t hidden;    // the same of the hidden values: eight digits, four bf16 or two fp16 columns each
     size_t parts;    // [M * top][D] fp32
     size_t workspace;
 };
