@@ -23,8 +23,8 @@ using namespace few;
 
 // ------------------------------------------------------------------ scores
 // A choice between two experts hangs on the last digits of a sum over thousands of products, so logits and scores are
-// pairs of fp32 (kda_wide.cuh).  A block takes one expert and TB tokens, its warps share the row: with few
-// tokens all of the router is on its way at once.
+// pairs of fp32 (kda_wide.cuh).  A block takes EB experts and TB tokens, its warps share the rows: with one token all of the
+// router is on its way at once; with many, four by four keep what is read from L2 below what the sums take.
 constexpr int kScoreThreads = 256, kScoreWarps = 8;
 
 __device__ __forceinline__ uint32_t ordered(float v) {  // a larger value is a larger integer
@@ -44,63 +44,55 @@ template <typename T> __device__ __forceinline__ void load8_any(const T* p, bool
     }
 }
 
-template <typename Tr, int TB>
+template <typename Tr, int EB, int TB>
 __global__ void __launch_bounds__(kScoreThreads) k_moe_scores(const bf16* __restrict__ x, int64_t xs, bool xwide, const Tr* __restrict__ router,
                                                               bool rwide, const float* __restrict__ bias, int M, int E, int D,
                                                               int sigmoid, Wide* __restrict__ score, uint64_t* __restrict__ key,
                                                               int* __restrict__ done) {
-    __shared__ Wide sums[kScoreWarps][TB];
+    __shared__ Wide sums[kScoreWarps][EB * TB];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int e = blockIdx.x, t0 = blockIdx.y * TB;
-    if (e == 0 && t0 == 0 && threadIdx.x == 0) *done = 0;
-    f2 hi[TB], lo[TB];  // two running sums (kda_wide.cuh) side by side
-#pragma unroll
-    for (int j = 0; j < TB; ++j) hi[j] = lo[j] = f2_dup(0.f);
-    const Tr* r = router + (int64_t)e * D;
-#pragma unroll 2
+    const int e0 = blockIdx.x * EB, t0 = blockIdx.y * TB;
+    if (e0 == 0 && t0 == 0 && threadIdx.x == 0) *done = 0;
+    Sum2 s[EB][TB];
+#pragma unroll EB * TB == 1 ? 2 : 1
     for (int k = threadIdx.x * 8; k < D; k += kScoreThreads * 8) {
-        float rv[8], xv[TB][8];
-        load8_any(r + k, rwide, rv);
+        float rv[EB][8], xv[TB][8];
+#pragma unroll
+        for (int i = 0; i < EB; ++i) load8_any(router + (int64_t)min(e0 + i, E - 1) * D + k, rwide, rv[i]);
 #pragma unroll
         for (int j = 0; j < TB; ++j) load8_any(x + (int64_t)min(t0 + j, M - 1) * xs + k, xwide, xv[j]);
 #pragma unroll
+        for (int i = 0; i < EB; ++i)
+#pragma unroll
+            for (int j = 0; j < TB; ++j)
+#pragma unroll
+                for (int v = 0; v < 8; ++v) {
+                    const float p = xv[j][v] * rv[i][v];  // exact for a bf16 router
+                    s[i][j].add(p);
+                    if constexpr (sizeof(Tr) == 4) s[i][j].lo += fmaf(xv[j][v], rv[i][v], -p);
+                }
+    }
+#pragma unroll
+    for (int i = 0; i < EB; ++i)
+#pragma unroll
         for (int j = 0; j < TB; ++j) {
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const f2 a = f2_of(xv[j][i], xv[j][i + 1]), b = f2_of(rv[i], rv[i + 1]);
-                const f2 p = mul2(a, b);  // exact for a bf16 router
-                const f2 sum = add2(hi[j], p), back = sub2(sum, hi[j]);
-                f2 lost = add2(sub2(hi[j], sub2(sum, back)), sub2(p, back));
-                if constexpr (sizeof(Tr) == 4) lost = add2(lost, fma2(a, b, sub2(f2_dup(0.f), p)));
-                lo[j] = add2(lo[j], lost);
-                hi[j] = sum;
+            for (int d = 16; d; d >>= 1) {
+                const float h = __shfl_xor_sync(0xffffffffu, s[i][j].hi, d), l = __shfl_xor_sync(0xffffffffu, s[i][j].lo, d);
+                s[i][j].add(h);
+                s[i][j].lo += l;
             }
+            if (lane == 0) sums[warp][i * TB + j] = wide(s[i][j]);
         }
-    }
-    Sum2 s[TB];
-#pragma unroll
-    for (int j = 0; j < TB; ++j) {
-        s[j].hi = f2_lo(hi[j]), s[j].lo = f2_lo(lo[j]) + f2_hi(lo[j]);
-        s[j].add(f2_hi(hi[j]));
-    }
-#pragma unroll
-    for (int j = 0; j < TB; ++j) {
-#pragma unroll
-        for (int d = 16; d; d >>= 1) {
-            const float h = __shfl_xor_sync(0xffffffffu, s[j].hi, d), l = __shfl_xor_sync(0xffffffffu, s[j].lo, d);
-            s[j].add(h);
-            s[j].lo += l;
-        }
-        if (lane == 0) sums[warp][j] = wide(s[j]);
-    }
     __syncthreads();
-    const int j = threadIdx.x;
+    const int i = threadIdx.x / TB, j = threadIdx.x % TB;
     let_next_kernel_begin();
-    wait_for_kernel_before();  // the digits' kernel, if one runs beside this: what comes next counts on both
-    if (j < TB && t0 + j < M) {
-        Wide v = sums[0][j];
+    wait_for_kernel_before();  // the columns' kernel, if one runs beside this: what comes next counts on both
+    if (i < EB && e0 + i < E && t0 + j < M) {
+        const int e = e0 + i;
+        Wide v = sums[0][threadIdx.x];
 #pragma unroll
-        for (int w = 1; w < kScoreWarps; ++w) v = add(v, sums[w][j]);
+        for (int w = 1; w < kScoreWarps; ++w) v = add(v, sums[w][threadIdx.x]);
         const int64_t at = (int64_t)(t0 + j) * E + e;
         const Wide logit = v;
         if (sigmoid) v = sigmoid_wide(v);
@@ -488,11 +480,13 @@ template <typename Tr> cudaError_t launch_scores(const kda_moe_args& a, int64_t 
     const Tr* r = static_cast<const Tr*>(a.router);
     const bool rwide = reinterpret_cast<uintptr_t>(r) % 16 == 0;
     const int sg = a.score == KDA_SCORE_SIGMOID;
-    if (a.M == 1)
-        return launch_kernel(k_moe_scores<Tr, 1>, dim3(a.E, 1), kScoreThreads, 1, 0, beside, s, x, xs, xwide, r, rwide, a.bias, a.M, a.E, a.D, sg, score,
-                             key, done);
-    return launch_kernel(k_moe_scores<Tr, 4>, dim3(a.E, (a.M + 3) / 4), kScoreThreads, 1, 0, beside, s, x, xs, xwide, r, rwide, a.bias, a.M, a.E, a.D,
-                         sg, score, key, done);
+    const auto go = [&](auto kernel, int eb, int tb) {
+        return launch_kernel(kernel, dim3((a.E + eb - 1) / eb, (a.M + tb - 1) / tb), kScoreThreads, 1, 0, beside, s, x, xs, xwide, r, rwide, a.bias, a.M,
+                             a.E, a.D, sg, score, key, done);
+    };
+    if (a.M == 1) return go(k_moe_scores<Tr, 1, 1>, 1, 1);
+    if (a.M <= 4) return go(k_moe_scores<Tr, 1, 4>, 1, 4);
+    return go(k_moe_scores<Tr, 4, 4>, 4, 4);
 }
 
 template <int NT, int GS, int SB>

@@ -29,21 +29,23 @@ _VERIFY = struct.Struct("@iqiiPqPqPiPPPPPP")
 Weight = Union[torch.Tensor, Tuple[torch.Tensor, torch.Tensor]]
 
 
+# format and type of scales by the scales' dtype
+_SCALES = {_U8: (_lib.KDA_WEIGHT_E2M1, 0), **{d: (_lib.KDA_WEIGHT_INT4, v) for d, v in _DT.items()}}
+
+
 def _weight4(codes: torch.Tensor, scales: torch.Tensor, name: str):
     """(format, group, scale dtype, K) of 4-bit weights [..., K / 2] with scales [..., K / group]."""
-    if codes.dtype != _U8 or codes.dim() < 2 or not codes.is_contiguous():
-        raise ValueError(f"the codes of {name} must be a contiguous uint8 tensor [..., rows, K / 2], got {codes.dtype} {tuple(codes.shape)}")
-    if scales.dim() != codes.dim() or scales.shape[:-1] != codes.shape[:-1] or not scales.is_contiguous():
-        raise ValueError(f"the scales of {name} must be contiguous, one row of them per row of codes {tuple(codes.shape)}, "
-                         f"got {tuple(scales.shape)}")
-    K, groups = 2 * codes.shape[-1], scales.shape[-1]
+    kind, cs, ss = _SCALES.get(scales.dtype), codes.shape, scales.shape
+    if kind is None:
+        raise ValueError(f"the scales of {name} are {scales.dtype}; expected uint8 (e2m1), bfloat16 or float32 (int4)")
+    if codes.dtype is not _U8 or len(cs) < 2 or not codes.is_contiguous():
+        raise ValueError(f"the codes of {name} must be a contiguous uint8 tensor [..., rows, K / 2], got {codes.dtype} {tuple(cs)}")
+    if ss[:-1] != cs[:-1] or not scales.is_contiguous():
+        raise ValueError(f"the scales of {name} must be contiguous, one row of them per row of codes {tuple(cs)}, got {tuple(ss)}")
+    K, groups = 2 * cs[-1], ss[-1]
     if groups < 1 or K % groups:
         raise ValueError(f"{groups} scales do not divide the {K} weights of a row of {name}")
-    if scales.dtype == _U8:
-        return _lib.KDA_WEIGHT_E2M1, K // groups, 0, K
-    if scales.dtype not in _DT:
-        raise ValueError(f"the scales of {name} are {scales.dtype}; expected uint8 (e2m1), bfloat16 or float32 (int4)")
-    return _lib.KDA_WEIGHT_INT4, K // groups, _DT[scales.dtype], K
+    return kind[0], K // groups, kind[1], K
 
 
 def kda_pack4(w: torch.Tensor, *, format: str = "e2m1", group: int = 32, scale_dtype=torch.bfloat16, stream=None):
@@ -125,7 +127,7 @@ def kda_gemm4(A: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, epi
         ldc = _rows(out, M, N, out.dtype, "out")
     args = (M, N, K, A.data_ptr(), lda, fmt, group, sdt, codes.data_ptr(), scales.data_ptr(), out.data_ptr(), ldc,
             _DT[out.dtype], epi)
-    st = _status(d_status)
+    st = 0 if d_status is None else _status(d_status)
     p, n, keep = _workspace("kda_gemm4_workspace_size", index, (M, N, K, fmt, group), _GEMM4, args, (st,), workspace, dev)
     _check(_lib.load().kda_gemm4(_GEMM4.pack(*args, p, n, st), _stream_of(index)), "kda_gemm4")
     return out
@@ -138,7 +140,7 @@ def _experts(w: Weight, rows: int, E: int, K: int, name: str):
         return _lib.KDA_WEIGHT_BF16, 0, 0, w, None
     codes, scales = w
     fmt, group, sdt, Kw = _weight4(codes, scales, name)
-    if codes.shape[:-1] != (E, rows) or Kw != K:
+    if codes.shape != (E, rows, K // 2) or Kw != K:
         raise ValueError(f"{name} must be {(E, rows, K)}, got {(*codes.shape[:-1], Kw)}")
     return fmt, group, sdt, codes, scales
 
@@ -189,13 +191,16 @@ def kda_moe(x: torch.Tensor, router: torch.Tensor, w_in: Weight, w_out: Weight, 
             raise ValueError(f"y is {y.dtype}, out_dtype {out_dtype}")
         _io(y, "y")
         ys = _rows(y, M, D, y.dtype, "y")
-    ids = torch.empty((M, top), dtype=torch.int32, device=dev) if return_routing and top > 0 else None
-    weights = torch.empty((M, top), dtype=_F32, device=dev) if return_routing and top > 0 else None
+    ids = weights = None
+    ip = wp = 0
+    if return_routing and top > 0:
+        ids, weights = torch.empty((M, top), dtype=torch.int32, device=dev), torch.empty((M, top), dtype=_F32, device=dev)
+        ip, wp = ids.data_ptr(), weights.data_ptr()
     args = (M, E, top, D, F, x.data_ptr(), xs, r, rdt, b, mode, scale, fmt, group, sdt, wi.data_ptr(), _ptr(si), wo.data_ptr(),
-            _ptr(so), y.data_ptr(), ys, _DT[y.dtype], _ptr(ids), _ptr(weights))
-    st = _status(d_status)
-    p, n, keep = _workspace("kda_moe_workspace_size", index, (M, E, top, D, F, fmt, group, sdt, rdt, mode, b != 0), _MOE, args,
-                            (st,), workspace, dev)
+            _ptr(so), y.data_ptr(), ys, _DT[y.dtype], ip, wp)
+    st = 0 if d_status is None else _status(d_status)
+    p, n, keep = _workspace("kda_moe_workspace_size", index, (M, E, top, D, F, fmt, group, b != 0), _MOE, args, (st,),
+                            workspace, dev)
     _check(lib.kda_moe(_MOE.pack(*args, p, n, st), _stream_of(index)), "kda_moe")
     return (y, ids, weights) if return_routing else y
 

@@ -31,9 +31,14 @@ def fill(a, kw):
 
 
 def test_structs_match_the_binding():
+    """The packed formats lay every member of the C structs where their mirrors have it."""
     for fmt, cls in ((serve._PACK4, _lib.Pack4Args), (serve._GEMM4, _lib.Gemm4Args), (serve._MOE, _lib.MoeArgs),
                      (serve._VERIFY, _lib.VerifyArgs)):
+        values = [0.5 if t is ctypes.c_float else 1000 + i for i, (_, t) in enumerate(cls._fields_)]
+        got = cls.from_buffer_copy(fmt.pack(*values))
         assert fmt.size == ctypes.sizeof(cls)
+        for (name, _), v in zip(cls._fields_, values):
+            assert getattr(got, name) == v, name
 
 
 def pack4(**kw):
@@ -62,6 +67,7 @@ def gemm4(**kw):
     a = _lib.Gemm4Args()
     a.M, a.N, a.K, a.A, a.lda, a.format, a.group = 4, 100, 256, at(0), 256, _lib.KDA_WEIGHT_E2M1, 32
     a.codes, a.scales, a.C, a.ldc, a.c_dtype = at(1), at(2), at(3), 100, _lib.KDA_BF16
+    a.workspace, a.workspace_bytes = at(4), 1 << 24
     return fill(a, kw)
 
 
@@ -72,7 +78,9 @@ def gemm4(**kw):
     (dict(c_dtype=7), INVALID), (dict(epilogue=3), INVALID), (dict(epilogue=-1), INVALID), (dict(A=None), INVALID),
     (dict(A=at(0, 1)), INVALID), (dict(lda=255), INVALID), (dict(ldc=99), INVALID), (dict(C=None), INVALID),
     (dict(C=at(0)), INVALID), (dict(C=at(1, 128)), INVALID), (dict(C=at(2, 2)), INVALID), (dict(codes=at(1, 4)), INVALID),
-    (dict(codes=None), INVALID), (dict(scales=None), INVALID), (dict(lda=1 << 58), UNSUPPORTED)])
+    (dict(codes=None), INVALID), (dict(scales=None), INVALID), (dict(lda=1 << 58), UNSUPPORTED), (dict(workspace=None), WORKSPACE),
+    (dict(workspace_bytes=4096), WORKSPACE), (dict(workspace=at(4, 16)), WORKSPACE), (dict(workspace=at(1)), INVALID),
+    (dict(workspace=at(3)), INVALID)])
 def test_gemm4_refusals(kw, code):
     assert call("kda_gemm4", gemm4(**kw)) == code
 
@@ -106,6 +114,15 @@ def test_moe_workspace_size():
     assert n.value >= 4 * 16 * 16 + 8 * (128 + 256) * 4 and n.value % 256 == 0
     assert _lib.load().kda_moe_workspace_size(ctypes.byref(moe(M=0)), ctypes.byref(n)) == 0 and n.value == 0
     assert _lib.load().kda_moe_workspace_size(ctypes.byref(moe(top=0)), ctypes.byref(n)) == INVALID
+
+
+def test_gemm4_workspace_size():
+    n = ctypes.c_size_t(1)
+    size = _lib.load().kda_gemm4_workspace_size
+    assert size(ctypes.byref(gemm4()), ctypes.byref(n)) == 0 and n.value >= 4 * 256 * 4
+    assert size(ctypes.byref(gemm4(**INT4)), ctypes.byref(n)) == 0 and n.value >= 4 * 256 * 2
+    assert size(ctypes.byref(gemm4(N=0)), ctypes.byref(n)) == 0 and n.value == 0
+    assert size(ctypes.byref(gemm4(K=7)), ctypes.byref(n)) == UNSUPPORTED
 
 
 def verify(**kw):
