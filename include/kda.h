@@ -701,10 +701,13 @@ kda_status kda_pack4(const kda_pack4_args* args, kda_stream_t stream);
 kda_status kda_unpack4(const kda_pack4_args* args, kda_stream_t stream);
 
 /* kda_gemm4 -- kda_gemm for weights in 4 bits: C[M][N] = epilogue(A[M][K] . W[N][K]^T), for
- * the few rows of a decode step (any M is taken; the weights are read once per 64 rows).
+ * the few rows of a decode step (M up to 65,535; the weights are read once per 32 rows).
  * A [M][lda] bf16 (any alignment of its elements; 16-byte rows are read faster), C [M][ldc] bf16
- * or fp32, rounded once; products are exact in fp32 groups, sums fp32, in a fixed order.  M, N >= 0; C must not
- * overlap an input.  Epilogues as in kda_gemm. */
+ * or fp32, rounded once; epilogues as in kda_gemm; M, N >= 0; C must not overlap an input.
+ * Values of A enter the products exactly but for what lies below 2^-22 of the largest of their 32 (e2m1) or 2^-35 of
+ * the largest of their 128 (int4); sums are fp32, in a fixed order.  A row of A with values that are not finite gives what
+ * the formula gives, slowly.  Needs an sm_103 device.  A wait that times out on the device is reported through
+ * d_status (KDA_ERR_TIMEOUT). */
 typedef struct {
     int M, N, K;
     const void* A;
@@ -737,8 +740,11 @@ kda_status kda_gemm4(const kda_gemm4_args* args, kda_stream_t stream);
  *   w_in [E][2F][D], w_out [E][D][F] in one format (scales NULL for bf16); D and F multiples of the group,
  *   of 8 for bf16
  *   y [M][y_stride] bf16 or fp32; ids [M][top] int32 and weights [M][top] fp32, best first, or NULL
- * The values between the two products stay in fp32 (22 bits or more in the second one).  E up to 1024, top up to 32 and
- * to E, M * top up to 65535. */
+ * The values between the two products keep 22 bits or more of the largest of their 32 (e2m1), 128 (int4) or of their
+ * own (bf16); sums are fp32.  One that is not finite (or, int4, beyond 2^117) makes its token's y
+ * NaN, of the others nothing changes.  E up to 1024, top up
+ * to 32 and to E, M * top up to 65535, E * 2F and E * D up to 2^30.  Needs an sm_103 device; a wait that times out on the
+ * device is reported through d_status (KDA_ERR_TIMEOUT). */
 typedef enum { KDA_SCORE_SIGMOID = 0, KDA_SCORE_SOFTMAX = 1 } kda_moe_score;
 
 typedef struct {
@@ -784,7 +790,7 @@ kda_status kda_moe(const kda_moe_args* args, kda_stream_t stream);
  * (of target_a where that is 0 everywhere), of the last row's target otherwise; -1 where nothing is above 0.
  *   out      [T_total] of tokens' type: the accepted drafts, the drawn token, then -1
  *   accepted [N] int32: drafts taken (0 for a sequence without rows)
- * Comparisons are exact in fp64 and sums carry about 48 bits.  V up to 4,000,000. */
+ * Comparisons of drafts are exact, sums carry about 48 bits.  V up to 4,000,000. */
 typedef struct {
     int N;
     int64_t T_total;

@@ -16,7 +16,7 @@
 //
 // A CTA has 8 or 12 warps.  A warp takes 32 rows, two tiles of an instruction, so that each operand of the columns is read from
 // shared memory once for both and their chains of instructions overlap (16 warps of 16 rows each: 199 us instead of
-// MEASURED for 160,000 x 7,168 codes and 16 tokens).  Its codes and scales go through cp.async into a ring of its own
+// 178 for 160,000 x 7,168 codes and 16 tokens).  Its codes and scales go through cp.async into a ring of its own
 // (32 rows x 256 elements a stage), no barrier among warps.  All columns of a segment of K are in shared memory for all
 // warps, the next segment's on their way meanwhile: one barrier per segment.  `ks` warps share 32 rows along K where there
 // are few rows.
@@ -94,7 +94,7 @@ struct Weights {  // of one matrix [rows][K]
 };
 struct Columns {  // laid out by k_few_halves
     const __half* x;      // [.][K]
-    const float* factor;  // [.][runs of 128]: what a sum is to be multiplied by, but for 2^24
+    const float* factor;  // [.][runs of 128]: what a sum is to be multiplied by
     const float* sums;    // [.][groups]: -8 2^-24 times the sum of a group's elements
 };
 
@@ -136,13 +136,14 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 }
 
 // The power of two that brings a magnitude with these fp32 exponent bits to 2^14..2^15 (as far as fp32 has
-// one), and its inverse.
+// one), and what sums of subnormal codes are to be multiplied by: its inverse times 2^24.  Magnitudes from 2^117 on, for which
+// fp32 has none, get NaN.
 __device__ __forceinline__ void run_scale(uint32_t exponent, float& up, float& down) {
     const uint32_t e = 268u - exponent;             // 127 + 14 + 127 - exponent
     const uint32_t b = e > 254u ? 254u : e;
     up = __uint_as_float(b << 23);
-    const uint32_t d = 254u - b;
-    down = __uint_as_float(d ? d << 23 : 0x00400000u);
+    const uint32_t d = 254u - b + 24u;
+    down = d < 255u ? __uint_as_float(d << 23) : NAN;
 }
 
 // Where the columns of `n` rows of K elements lie in a buffer, and what they take.
@@ -159,7 +160,7 @@ cudaError_t launch_halves(const bf16* x, int64_t xs, bool wide, int rows, int K,
 
 constexpr float kSumOf = -8.f * 0x1p-24f;
 
-// One product by itself, for a sum that came out as NaN: what is taken off a row with an infinity is one too.
+// One product by itself, for a sum that came out as NaN: a row of x with an infinity or values that no factor is for.
 static __device__ __noinline__ float direct(const uint8_t* codes, const uint8_t* scales, int scale_bytes, int group, const bf16* x, int K) {
     float sum = 0.f;
     for (int g = 0; g < K / group; ++g) {
@@ -369,12 +370,6 @@ __device__ __forceinline__ void products(uint8_t* smem, const Weights& w, const 
                 if (++buffer == kStages) buffer = 0;
             }
         }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int c = 0; c < NT; ++c)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[u][c][j] *= 0x1p24f;
         if (ks > 1) {  // the first warp of each tile adds up the others' sums, in their order; they lie over the last columns
             __syncthreads();
             float4* red = reinterpret_cast<float4*>(smem + L::x_at + ((pass * segs + segs - 1) & 1) * L::cols * L::x_pitch) + warp * 2 * NT * 32 + lane;

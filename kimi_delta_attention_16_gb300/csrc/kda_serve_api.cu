@@ -94,8 +94,8 @@ kda_status check_pack4(const kda_pack4_args* a) {
 kda_status check_gemm4(const kda_gemm4_args* a) {
     if (!a) return fail(KDA_ERR_INVALID_ARG, "args is NULL");
     if (a->M < 0 || a->N < 0 || a->K < 1) return fail(KDA_ERR_INVALID_ARG, "bad sizes M=%d N=%d K=%d", a->M, a->N, a->K);
-    if (a->M > 4000000 || a->N > 1 << 24 || a->K > 1 << 24)
-        return fail(KDA_ERR_UNSUPPORTED, "M=%d above 4,000,000, or N=%d or K=%d above 2^24", a->M, a->N, a->K);
+    if (a->M > 65535 || a->N > 1 << 24 || a->K > 1 << 24)
+        return fail(KDA_ERR_UNSUPPORTED, "M=%d above 65535, or N=%d or K=%d above 2^24", a->M, a->N, a->K);
     kda_status st;
     if ((st = check_format(a->format, a->group, a->scale_dtype, a->K, false, "K"))) return st;
     if (!valid_dtype(a->c_dtype)) return fail(KDA_ERR_INVALID_ARG, "unknown dtype %d", (int)a->c_dtype);
@@ -170,6 +170,7 @@ kda_status kda_gemm4(const kda_gemm4_args* a, kda_stream_t stream) {
     const Span ins[] = {{a->A, rows_bytes(a->M, a->lda, a->K, 2), "A"}, {a->codes, weight_size(a->N, a->K, a->format), "codes"},
                         {a->scales, scales_size(a->N, a->K, a->format, a->group, a->scale_dtype), "scales"}};
     if ((st = check_overlaps(outs, ins))) return st;
+    if (!gemm_supported_device()) return fail(KDA_ERR_UNSUPPORTED, "kda_gemm4 needs an sm_103 device");
     if (const cudaError_t e = launch_gemm4(*a, cu_stream(stream))) return cuda_fail(e, "gemm4");
     return ok();
 }
@@ -207,6 +208,7 @@ kda_status kda_moe(const kda_moe_args* a, kda_stream_t stream) {
                         {a->w_out, weight_size(out, a->F, a->format), "w_out"},
                         {a->w_out_scales, scales_size(out, a->F, a->format, a->group, a->scale_dtype), "w_out_scales"}};
     if ((st = check_overlaps(outs, ins))) return st;
+    if (!gemm_supported_device()) return fail(KDA_ERR_UNSUPPORTED, "kda_moe needs an sm_103 device");
     if (const cudaError_t e = launch_moe(*a, p, cu_stream(stream))) return cuda_fail(e, "moe");
     return ok();
 }

@@ -98,7 +98,7 @@ def kda_gemm4(A: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, epi
               stream=None) -> torch.Tensor:
     """C = epilogue(A @ W^T) for the few rows of a decode step: A [M, K] bf16 (rows may be strided), W [N, K] in 4 bits
     (codes [N, K / 2] and scales [N, K / group] as kda_pack4 returns them).  Epilogues and out_dtype as in kda_gemm; out
-    [M, N] may have strided rows.  Products are exact and sums fp32, in a fixed order, rounded once."""
+    [M, N] may have strided rows.  Sums are fp32, in a fixed order, rounded once.  M is at most 65535."""
     if stream is not None:
         with _on(stream, A, codes, scales, out, workspace, d_status):
             return kda_gemm4(A, codes, scales, epilogue=epilogue, out=out, out_dtype=out_dtype, workspace=workspace,

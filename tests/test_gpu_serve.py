@@ -87,20 +87,22 @@ def test_gemm4_many_tiles():
     check_gemm4(70, 9000, 256, "int4", 128, BF16)
 
 
+@pytest.mark.parametrize("fmt,group,sdt", FORMATS)
 @pytest.mark.parametrize("exponent", [-120, -60, 0, 60, 100])
-def test_gemm4_magnitudes(exponent):
+def test_gemm4_magnitudes(exponent, fmt, group, sdt):
     """Columns of any magnitude, and elements far below the largest of their run."""
     g = gen(exponent + 200)
     x = randn(g, 6, 1024) * torch.exp2(torch.randint(-25, 1, (6, 1024), generator=g).float()) * 2.0 ** exponent
-    check_gemm4(6, 50, 1024, "e2m1", 32, None, out_dtype=F32, x=x.to(BF16))
+    check_gemm4(6, 50, 1024, fmt, group, sdt, out_dtype=F32, x=x.to(BF16))
 
 
-def test_gemm4_not_finite_stays_in_its_row():
+@pytest.mark.parametrize("fmt,group,sdt", FORMATS)
+def test_gemm4_not_finite_stays_in_its_row(fmt, group, sdt):
     g = gen(3)
     x = randn(g, 4, 512, dtype=BF16)
     x[1, 300] = float("inf")
     x[2, 5] = float("nan")
-    codes, scales = lib.random_weight(g, 60, 512, fmt="e2m1", group=32)
+    codes, scales = lib.random_weight(g, 60, 512, fmt=fmt, group=group, scale_dtype=sdt)
     got = kda.kda_gemm4(x.cuda(), codes.cuda(), scales.cuda(), out_dtype=F32).cpu()
     w = lib.unpack_ref(codes, scales)
     ref, err = lib.gemm4_ref(x[[0, 3]], w, "none")
@@ -110,10 +112,22 @@ def test_gemm4_not_finite_stays_in_its_row():
     assert bool(torch.isnan(got[2]).all())
 
 
-def test_gemm4_strides_and_alignment():
+def test_gemm4_rows_of_zeros_and_tiny_values():
+    """Padding beside rows in use, rows whose values all lie below what digits hold, and such values beside others."""
+    g = gen(14)
+    x = randn(g, 5, 640)
+    x[1] = 0
+    x[2] *= 2.0 ** -115
+    x[3, 32:64] *= 2.0 ** -110
+    for fmt, group, sdt in FORMATS:
+        check_gemm4(5, 60, 640, fmt, group, sdt, out_dtype=F32, x=x.to(BF16))
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "int4"])
+def test_gemm4_strides_and_alignment(fmt):
     g = gen(11)
     x = randn(g, 7, 300, dtype=BF16)
-    codes, scales = lib.random_weight(g, 90, 288, fmt="int4", group=32, scale_dtype=BF16)
+    codes, scales = lib.random_weight(g, 90, 288, fmt=fmt, group=32, scale_dtype=BF16)
     ref, err = lib.gemm4_ref(x[:, 5:293], lib.unpack_ref(codes, scales), "none")
     big = torch.full((7, 101), 7.0, device="cuda")
     out = kda.kda_gemm4(x.cuda()[:, 5:293], codes.cuda(), scales.cuda(), out=big[:, 3:93])
@@ -122,29 +136,35 @@ def test_gemm4_strides_and_alignment():
     assert bool((big[:, :3] == 7).all()) and bool((big[:, 93:] == 7).all())
 
 
-def test_gemm4_empty_and_same_bits():
+@pytest.mark.parametrize("fmt,group,sdt", FORMATS)
+def test_gemm4_empty_and_same_bits(fmt, group, sdt):
     g = gen(12)
     x = randn(g, 30, 2304, dtype=BF16).cuda()
-    codes, scales = (t.cuda() for t in lib.random_weight(g, 500, 2304, fmt="e2m1", group=32))
+    codes, scales = (t.cuda() for t in lib.random_weight(g, 500, 2304, fmt=fmt, group=group, scale_dtype=sdt))
     one = kda.kda_gemm4(x, codes, scales, out_dtype=F32)
     assert torch.equal(one, kda.kda_gemm4(x, codes, scales, out_dtype=F32))
     assert kda.kda_gemm4(x[:0], codes, scales).shape == (0, 500)
     assert kda.kda_gemm4(x, codes[:0], scales[:0]).shape == (30, 0)
 
 
-def test_gemm4_offsets_past_32_bits():
+@pytest.mark.parametrize("fmt,sdt", [("e2m1", torch.uint8), ("int4", F32)])
+def test_gemm4_offsets_past_32_bits(fmt, sdt):
     """Codes of 4.6 GB: the last rows are at offsets that 32 bits do not hold."""
     N, K = 600000, 15360
     if torch.cuda.mem_get_info()[0] < 12 << 30:
         pytest.skip("needs 12 GB of free memory")
-    codes = torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda")
-    scales = torch.full((N, K // 32), 127, dtype=torch.uint8, device="cuda")
+    codes = torch.full((N, K // 2), 0 if fmt == "e2m1" else 0x88, dtype=torch.uint8, device="cuda")  # weights of 0
+    scales = torch.full((N, K // 32), 127 if fmt == "e2m1" else 1.0, dtype=sdt, device="cuda")
     g = gen(13)
-    tail, st = lib.random_weight(g, 200, K, fmt="e2m1", group=32)
+    tail, st = lib.random_weight(g, 200, K, fmt=fmt, group=32, scale_dtype=sdt)
     codes[-200:], scales[-200:] = tail.cuda(), st.cuda()
     x = randn(g, 2, K, dtype=BF16)
     got = kda.kda_gemm4(x.cuda(), codes, scales, out_dtype=F32)
-    assert bool((got[:, :-200] == 0).all())
+    # Integer codes enter as they are, and 8 times a group's sum of x is taken off: of a group of zeros (codes 8, scale 1)
+    # remain the roundings of that sum (32 additions) and of the two matrix instructions that build it up again, each at
+    # most 2^-23 of 8 sum |x|; groups add up, each addition within 2^-24 of what is left so far.
+    zeros = 0.0 if fmt == "e2m1" else float(36 * 2.0 ** -23 * 8 * f64(x).abs().sum(1).max())
+    assert bool((got[:, :-200].abs() <= zeros).all())
     ref, err = lib.gemm4_ref(x, lib.unpack_ref(tail, st), "none")
     within(got[:, -200:], ref, err + U[F32] * ref.abs())
 
@@ -221,18 +241,33 @@ def test_moe_close_logits_are_told_apart():
     check_moe(3, E, 3, D, 32, x=x, router=router, router_dtype=F32, with_bias=False)
 
 
-def test_moe_all_tokens_to_one_expert():
+@pytest.mark.parametrize("fmt", ["e2m1", "int4", "bf16"])
+def test_moe_all_tokens_to_one_expert(fmt):
     """More tokens of an expert than one pass holds columns for."""
     g = gen(6)
     x = randn(g, 70, 256).abs().to(BF16)
     router = randn(g, 64, 256, std=0.01, dtype=BF16)
     router[17] = 0.5
-    check_moe(70, 64, 2, 256, 96, x=x, router=router, with_bias=False)
+    check_moe(70, 64, 2, 256, 96, fmt, 32, BF16, x=x, router=router, with_bias=False)
 
 
-def test_moe_not_finite_token():
-    x, router, bias, wi, wo, wi64, wo64 = make_moe(4, 20, 128, 64, "e2m1", 32, None, 1)
-    pair = lambda w: tuple(t.cuda() for t in w)  # noqa: E731
+@pytest.mark.parametrize("fmt", ["e2m1", "int4", "bf16"])
+@pytest.mark.parametrize("M,E,top", [(2, 3, 2), (6, 2, 2), (13, 2, 1), (17, 2, 2), (40, 3, 3), (100, 3, 1)])
+def test_moe_many_tokens_per_expert(M, E, top, fmt):
+    """Every width of the columns, tokens that fit at once and tokens that do not, several tiles of rows."""
+    check_moe(M, E, top, 320, 160, fmt, 32, BF16)
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "int4", "bf16"])
+def test_moe_long_rows(fmt):
+    """More of K than a ring of stages or a segment of columns holds."""
+    check_moe(3, 5, 2, 2656, 1312, fmt, 32, F32)
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "int4", "bf16"])
+def test_moe_not_finite_token(fmt):
+    x, router, bias, wi, wo, wi64, wo64 = make_moe(4, 20, 128, 64, fmt, 32, BF16, 1)
+    pair = lambda w: w.cuda() if isinstance(w, torch.Tensor) else tuple(t.cuda() for t in w)  # noqa: E731
     call = lambda x: kda.kda_moe(x.cuda(), router.cuda(), pair(wi), pair(wo), 3, bias=bias.cuda(), out_dtype=F32,  # noqa: E731
                                  return_routing=True)
     clean = call(x)
@@ -244,9 +279,10 @@ def test_moe_not_finite_token():
     assert torch.equal(y[keep], clean[0][keep]) and torch.equal(ids[keep], clean[1][keep])
 
 
-def test_moe_strides_workspace_and_same_bits():
-    x, router, bias, wi, wo, _, _ = make_moe(6, 20, 128, 64, "int4", 64, F32, 2)
-    pair = lambda w: tuple(t.cuda() for t in w)  # noqa: E731
+@pytest.mark.parametrize("fmt,group", [("e2m1", 32), ("int4", 64), ("bf16", 0)])
+def test_moe_strides_workspace_and_same_bits(fmt, group):
+    x, router, bias, wi, wo, _, _ = make_moe(6, 20, 128, 64, fmt, group, F32, 2)
+    pair = lambda w: w.cuda() if isinstance(w, torch.Tensor) else tuple(t.cuda() for t in w)  # noqa: E731
     big = torch.zeros(6, 135, dtype=BF16, device="cuda")
     big[:, 3:131] = x.cuda()
     a = kda.kda_moe(x.cuda(), router.cuda(), pair(wi), pair(wo), 4, bias=bias.cuda())
@@ -339,6 +375,20 @@ def test_verify_strides_tails_and_device_cu():
     assert np.array_equal(out.cpu().numpy(), ro) and np.array_equal(acc.cpu().numpy(), ra) and int(status) == 0
 
 
+def test_verify_offsets_past_32_bits():
+    """Rows of both distributions that lie more than 2^32 bytes apart."""
+    V, far = 1003, 1200000001
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GB of free memory")
+    p, q, tokens, u, cu = make_verify([3, 1], V, BF16, 4)
+    held = [torch.empty(3 * far + V, dtype=BF16, device="cuda") for _ in range(2)]
+    wide = [h.as_strided((4, V), (far, 1)) for h in held]
+    wide[0].copy_(p), wide[1].copy_(q)
+    out, acc = kda.kda_verify(wide[0], tokens.cuda(), u.cuda(), cu, draft=wide[1])
+    ro, ra = lib.verify_ref(p, q, tokens, u, cu)
+    assert np.array_equal(out.cpu().numpy(), ro) and np.array_equal(acc.cpu().numpy(), ra)
+
+
 def test_verify_expected_share():
     """Over evenly spread u the accepted drafts and the drawn tokens have the target's distribution."""
     V, n = 6, 20000
@@ -387,11 +437,13 @@ def test_one_speculative_step():
     assert np.array_equal(out.cpu().numpy(), ro) and np.array_equal(acc.cpu().numpy(), ra)
 
 
-def test_streams_and_captures():
+@pytest.mark.parametrize("fmt", ["e2m1", "int4", "bf16"])
+def test_streams_and_captures(fmt):
     """The same bits on another stream and from a replayed graph with new inputs."""
-    x, router, bias, wi, wo, _, _ = make_moe(5, 24, 256, 128, "e2m1", 32, None, 7)
+    x, router, bias, wi, wo, _, _ = make_moe(5, 24, 256, 128, fmt, 32, BF16, 7)
     x, router, bias = dev(x, router, bias)
-    wi, wo = tuple(t.cuda() for t in wi), tuple(t.cuda() for t in wo)
+    wi, wo = (w.cuda() if isinstance(w, torch.Tensor) else tuple(t.cuda() for t in w) for w in (wi, wo))
+    e2m1 = tuple(t.cuda() for t in lib.random_weight(gen(2), 300, 256, fmt="e2m1", group=32))
     codes, scales = (t.cuda() for t in lib.random_weight(gen(1), 300, 256, fmt="int4", group=64, scale_dtype=F32))
     p, q, tokens, u, cu = make_verify([4, 3, 5], 5000, F32, 2)
     p, q, tokens, u = dev(p, q, tokens, u)
@@ -399,7 +451,7 @@ def test_streams_and_captures():
 
     def run(stream=None):
         y, ids, w = kda.kda_moe(x, router, wi, wo, 4, bias=bias, return_routing=True, stream=stream)
-        return [y, ids, w, kda.kda_gemm4(x, codes, scales, stream=stream),
+        return [y, ids, w, kda.kda_gemm4(x, codes, scales, stream=stream), kda.kda_gemm4(x, *e2m1, stream=stream),
                 *kda.kda_verify(p, tokens, u, pair, draft=q, stream=stream), *kda.kda_pack4(x, stream=stream)]
 
     want = run()
@@ -417,3 +469,66 @@ def test_streams_and_captures():
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(run(), held))
+
+
+def test_calls_side_by_side():
+    """Calls on several streams at once, each with its own workspace, give the bits of calls one after another."""
+    sets = []
+    for i, fmt in enumerate(("e2m1", "int4", "bf16", "e2m1")):
+        x, router, bias, wi, wo, _, _ = make_moe(9, 40, 512, 256, fmt, 32, BF16, 30 + i)
+        w = [v.cuda() if isinstance(v, torch.Tensor) else tuple(t.cuda() for t in v) for v in (wi, wo)]
+        sets.append((*dev(x, router, bias), *w, tuple(t.cuda() for t in lib.random_weight(gen(i), 700, 512, fmt="e2m1", group=32))))
+
+    def call(x, router, bias, wi, wo, w4, stream=None):
+        return [kda.kda_moe(x, router, wi, wo, 5, bias=bias, stream=stream), kda.kda_gemm4(x, *w4, stream=stream)]
+
+    want = [call(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = [call(*s, stream=st) for s, st in zip(sets, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_after_the_multi_token_decode():
+    """A step as it is run: the layer decodes each sequence's last token and its drafts from kept states, projections in 4 bits
+    on both sides, the drafts are verified, and the layer runs again over what was accepted."""
+    H, D, N, V = 2, 128, 3, 600
+    width = H * D
+    g = gen(40)
+    lens = [4, 2, 5]
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    T = int(cu[-1])
+    x = randn(g, T, width, dtype=BF16).cuda()
+    proj = [kda.kda_pack4(randn(g, width, width, std=width ** -0.5).cuda()) for _ in range(3)]
+    gates = kda.kda_pack4(randn(g, width, width, std=width ** -0.5).cuda(), format="int4", group=64, scale_dtype=F32)
+    head = kda.kda_pack4(randn(g, V, width, std=3 * width ** -0.5).cuda())
+    conv_w = randn(g, 3, width, 4, std=0.5).cuda()
+    beta = torch.rand(T, H, generator=g).cuda()
+    state, conv = torch.randn(N, H, D, D, generator=g).cuda() * 0.02, randn(g, N, 3 * width, 3, dtype=BF16).cuda()
+    router, wi, wo = (randn(g, *s, std=0.06, dtype=BF16).cuda() for s in ((8, width), (8, 256, width), (8, width, 128)))
+
+    def layer(rows, cu):
+        t = rows.shape[0]
+        q, k, v = (kda.kda_gemm4(rows, *w).view(t, H, D) for w in proj)
+        decay = kda.kda_gemm4(rows, *gates, epilogue="decay").view(t, H, D)
+        b = beta[:t].contiguous()
+        out, fin = kda.kda_prefill(q, k, v, conv_w, decay, b, cu, initial_state=state, conv_state_in=conv,
+                                   conv_state_out=torch.empty_like(conv))
+        y = kda.kda_moe(out.reshape(t, width), router, wi, wo, 2, score="softmax")
+        return torch.softmax(kda.kda_gemm4(y, *head, out_dtype=F32), 1), fin
+
+    probs, _ = layer(x, cu)
+    drafts = probs.argmax(1)
+    drafts[2] = (drafts[2] + 1) % V  # not the target's best
+    u = torch.full((T,), 0.3).cuda()
+    tokens, accepted = kda.kda_verify(probs, drafts, u, cu)
+    ro, ra = lib.verify_ref(probs.cpu(), None, drafts.cpu(), u.cpu(), cu)
+    assert np.array_equal(tokens.cpu().numpy(), ro) and np.array_equal(accepted.cpu().numpy(), ra)
+    # the states of what stands: the sequences again, as far as they were accepted
+    keep = accepted.cpu().numpy() + 1
+    rows = torch.cat([x[cu[i]:cu[i] + keep[i]] for i in range(N)])
+    again, fin = layer(rows, np.concatenate([[0], np.cumsum(keep)]).astype(np.int32))
+    assert fin.shape == state.shape and bool(torch.isfinite(fin).all()) and again.shape == (int(keep.sum()), V)

@@ -73,7 +73,7 @@ def gemm4(**kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(M=-1), INVALID), (dict(N=-1), INVALID), (dict(K=0), INVALID), (dict(K=40), UNSUPPORTED),
-    (dict(M=4000001), UNSUPPORTED), (dict(N=(1 << 24) + 1), UNSUPPORTED), (dict(K=(1 << 24) + 32, lda=1 << 25), UNSUPPORTED),
+    (dict(M=65536), UNSUPPORTED), (dict(N=(1 << 24) + 1), UNSUPPORTED), (dict(K=(1 << 24) + 32, lda=1 << 25), UNSUPPORTED),
     (dict(format=_lib.KDA_WEIGHT_BF16), INVALID), (dict(group=128), UNSUPPORTED), (dict(INT4, scale_dtype=2), INVALID),
     (dict(c_dtype=7), INVALID), (dict(epilogue=3), INVALID), (dict(epilogue=-1), INVALID), (dict(A=None), INVALID),
     (dict(A=at(0, 1)), INVALID), (dict(lda=255), INVALID), (dict(ldc=99), INVALID), (dict(C=None), INVALID),
@@ -97,7 +97,7 @@ def moe(**kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(M=-1), INVALID), (dict(E=0), INVALID), (dict(D=0), INVALID), (dict(F=0), INVALID), (dict(top=0), INVALID),
     (dict(top=17), INVALID), (dict(E=1025), UNSUPPORTED), (dict(E=64, top=33), UNSUPPORTED), (dict(M=40000), UNSUPPORTED),
-    (dict(D=(1 << 20) + 32), UNSUPPORTED), (dict(D=250), UNSUPPORTED), (dict(F=100), UNSUPPORTED), (dict(format=0, F=100), UNSUPPORTED),
+    (dict(D=(1 << 20) + 32), UNSUPPORTED), (dict(E=1024, F=1 << 20), UNSUPPORTED), (dict(D=250), UNSUPPORTED), (dict(F=100), UNSUPPORTED), (dict(format=0, F=100), UNSUPPORTED),
     (dict(router_dtype=3), INVALID), (dict(y_dtype=3), INVALID), (dict(score=2), INVALID), (dict(score=1), INVALID),
     (dict(x=None), INVALID), (dict(y=None), INVALID), (dict(router=None), INVALID), (dict(w_in=None), INVALID),
     (dict(w_out=at(5, 8)), INVALID), (dict(w_in_scales=None), INVALID), (dict(x_stride=100), INVALID), (dict(y=at(0)), INVALID),
