@@ -396,17 +396,24 @@ __device__ __forceinline__ void products(uint8_t* smem, const Weights& w, const 
     cp_wait<0>();
 }
 
-// Warps that share 32 rows along K: as many as leave the busiest CTA the least to do.
-template <typename L> int shared_k(int64_t row_tiles, int ctas, int K) {
-    const int stages = (K + kStageK - 1) / kStageK;
-    int best = 1;
+// CTAs along the rows, for `blocks` blocks of columns: all SMs, as far as there are tiles of 32 rows, and warps that share
+// a tile along K: the number that leaves a CTA the least to do.
+struct Split {
+    int ctas, ks;
+};
+template <typename L> Split split_rows(int tiles, int blocks, int K) {
+    const int stages = (K + kStageK - 1) / kStageK, least_ctas = (tiles + L::W - 1) / L::W;
+    Split s;
+    s.ctas = 152 / blocks > least_ctas ? 152 / blocks : least_ctas < 152 ? least_ctas : 152;
+    if (s.ctas > tiles) s.ctas = tiles;
+    const int each = (tiles + s.ctas - 1) / s.ctas;
+    s.ks = 1;
     int64_t least = INT64_MAX;
     for (int ks = 1; ks <= L::most_ks && L::W % ks == 0; ks *= 2) {
-        const int64_t per = L::W / ks, passes = ((row_tiles + per - 1) / per + ctas - 1) / ctas;
-        const int64_t t = passes * ((stages + ks - 1) / ks);
-        if (t < least) least = t, best = ks;
+        const int64_t per = L::W / ks, t = ((each + per - 1) / per) * ((stages + ks - 1) / ks);
+        if (t < least) least = t, s.ks = ks;
     }
-    return best;
+    return s;
 }
 
 }  // namespace few

@@ -80,9 +80,9 @@ template <int NT, int GS, int SB> cudaError_t launch(const kda_gemm4_args& a, cu
     p.M = a.M, p.N = a.N, p.K = a.K, p.epi = a.epilogue, p.ldc = a.ldc, p.group = a.group;
     p.a = static_cast<const bf16*>(a.A), p.lda = a.lda;
     const int tiles = (a.N + kRows - 1) / kRows, blocks = (a.M + L::cols - 1) / L::cols;
-    p.ks = shared_k<L>(tiles, 152, a.K);
-    const int ctas = (tiles * p.ks + L::W - 1) / L::W;
-    return launch_kernel(k_gemm4<NT, GS, SB>, dim3(ctas < 152 ? ctas : 152, blocks), L::threads, 1, L::bytes, true, s, p, a.C, a.c_dtype == KDA_FP32);
+    const Split split = split_rows<L>(tiles, blocks, a.K);
+    p.ks = split.ks;
+    return launch_kernel(k_gemm4<NT, GS, SB>, dim3(split.ctas, blocks), L::threads, 1, L::bytes, true, s, p, a.C, a.c_dtype == KDA_FP32);
 }
 
 template <int NT, int SB> cudaError_t launch_group(const kda_gemm4_args& a, cudaStream_t s) {

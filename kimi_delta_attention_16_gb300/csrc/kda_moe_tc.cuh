@@ -2,11 +2,15 @@
 // stay and walk over tiles of 128 rows of the experts in use.
 //
 // As in kda_few_tc.cuh warp 0 feeds a ring of stages by TMA, warp 1 issues the products, warps 4 to 7 bring scales (e2m1
-// only).  Warps 8 to 11 carry sums out of one of two accumulators in tensor memory while the next tile fills the other, so
+// only).  Warps 8 to 11 carry sums out of one accumulator in tensor memory while the next tile fills another, so
 // copies never pause between tiles.  A stage is 128 bytes of every row: 256 elements of e2m1, 64 of bf16.
 //
 // bf16 weights take bf16 columns on tcgen05.mma kind::f16; an fp32 hidden value is the sum of three bf16 terms, columns of
-// their own (and one of zeros), added up at the end.
+// their own (and one of zeros), added up at the end.  That instruction cuts its sums off where the accumulator ends: over
+// 2,048 elements (128 instructions) the result is off by 5.7e-6.  So a bf16 tile is carried out every two stages (8
+// instructions) and added up in fp32: 4.0e-7, and 83.7 us for four tokens of 6 of 64 experts (2,048 x 1,408) against 82.1
+// for whole tiles (every four stages: 7.2e-7, 82.8).  The 4-bit instruction rounds (4e-8 over 7,168 elements), its tiles
+// stay whole.
 #pragma once
 
 #include "kda_few_tc.cuh"
@@ -21,12 +25,14 @@ constexpr int kMaxExperts = 1024;
 template <int N, int T, bool Mx> struct Stay {
     static constexpr int tokens = N / T;
     static constexpr int stage_k = Mx ? 256 : 64;
+    static constexpr int chunk = Mx ? 1 << 30 : 2;               // stages that an accumulator takes
     static constexpr uint32_t stage = kTileA + N * 128;
     static constexpr int stages = N == 128 ? 6 : T == 1 ? (N == 16 ? 5 : N == 32 ? 4 : 3) : N <= 32 ? 5 : 4;
     static constexpr int per_sm = N <= 64 ? 2 : 1;
     static constexpr int nb = N < 32 ? 1 : N / 32, set = nb < 4 ? 4 : nb, group = 16 + 4 * set;
-    static constexpr int acc = N < 32 ? 32 : N;                  // columns from one accumulator to the other
-    static constexpr int scales_at = 2 * acc;
+    static constexpr int acc = N < 32 ? 32 : N;                  // columns from one accumulator to the next
+    static constexpr int accs = Mx ? 2 : 4;                      // accumulators: bf16 chunks go on while a tile is put away
+    static constexpr int scales_at = accs * acc;
     static constexpr int need = scales_at + (Mx ? kSlots * group : 0);
     static constexpr int tmem = need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
     static_assert(tmem * per_sm <= 512, "tensor memory of an SM");
@@ -40,7 +46,7 @@ template <int N, int T, bool Mx> struct Stay {
 };
 
 struct StayBarriers {
-    uint64_t full[6], empty[6], scales_full[kSlots], scales_empty[kSlots], sums[2], free[2];
+    uint64_t full[6], empty[6], scales_full[kSlots], scales_empty[kSlots], sums[4], free[4];
     uint32_t tmem;
     int failed;
 };
@@ -54,11 +60,6 @@ struct StayArgs {
     int E, top, tokens;   // tokens: rows of the columns' tensor / T
     bool by_token;        // the columns are the tokens themselves, every expert takes them all
 };
-
-template <int N>
-__device__ __forceinline__ uint32_t idesc_bf16_few() {
-    return idesc_bf16(128, N, false, false);
-}
 
 // The epilogue is called by warps 8 to 11 with a tile's sums in red[token][128 rows]: put(expert, first row of the tile, first
 // place, places, red, warp of four).
@@ -91,7 +92,7 @@ __device__ __forceinline__ void stay(uint8_t* smem, StayBarriers& bar, const Map
             mbar_init(&bar.scales_full[s], 4);
             mbar_init(&bar.scales_empty[s], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < S::accs; ++i) {
             mbar_init(&bar.sums[i], 1);
             mbar_init(&bar.free[i], 4);
         }
@@ -105,6 +106,7 @@ __device__ __forceinline__ void stay(uint8_t* smem, StayBarriers& bar, const Map
 
     const uint32_t base = smem_u32(ring), tm = bar.tmem;
     const int blocks = (a.K + S::stage_k - 1) / S::stage_k, groups = (a.K + kGroupK - 1) / kGroupK;
+    const int chunks = Mx ? 1 : (blocks + S::chunk - 1) / S::chunk;
     // what every role walks over: tiles of the experts in use, and an expert's tokens by as many as there are columns for
     const auto walk = [&](auto&& step) {
         uint32_t p = 0;
@@ -152,12 +154,16 @@ __device__ __forceinline__ void stay(uint8_t* smem, StayBarriers& bar, const Map
         });
     } else if (warp == 1 && lane == 0) {
         walk([&](uint32_t p, int, int, int, int) {
-            const uint32_t d = tm + (p & 1) * S::acc;
-            bool ok = mbar_wait(&bar.free[p & 1], ((p >> 1) & 1u) ^ 1u);
-            fence_after_sync();
+            bool ok = true;
+            uint32_t d = 0, turn = p * chunks;
             for (int kb = 0; kb < blocks && ok; ++kb) {
                 const uint32_t i = p * blocks + kb, s = i % S::stages, at = base + s * S::stage;
-                ok = mbar_wait(&bar.full[s], (i / S::stages) & 1u);
+                const int in_chunk = Mx ? kb : kb % S::chunk;
+                if (in_chunk == 0) {
+                    ok = mbar_wait(&bar.free[turn % S::accs], ((turn / S::accs) & 1u) ^ 1u);
+                    d = tm + turn % S::accs * S::acc;
+                }
+                ok = ok && mbar_wait(&bar.full[s], (i / S::stages) & 1u);
                 if constexpr (Mx) {
                     const uint32_t gi = p * groups + kb / 2, slot = gi % kSlots, sf = tm + S::scales_at + slot * S::group;
                     if (ok && (kb & 1) == 0) ok = mbar_wait(&bar.scales_full[slot], (gi / kSlots) & 1u);
@@ -176,12 +182,12 @@ __device__ __forceinline__ void stay(uint8_t* smem, StayBarriers& bar, const Map
                     fence_after_sync();
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_ss(d, desc_sw128(at + kk * 32, 16, 1024), desc_sw128(at + kTileA + kk * 32, 16, 1024), idesc_bf16_few<N>(), (kb | kk) != 0);
+                        mma_ss(d, desc_sw128(at + kk * 32, 16, 1024), desc_sw128(at + kTileA + kk * 32, 16, 1024), idesc_bf16(128, N, false, false), (in_chunk | kk) != 0);
                     mma_commit(&bar.empty[s]);
                 }
+                if (in_chunk == S::chunk - 1 || kb == blocks - 1) mma_commit(&bar.sums[turn++ % S::accs]);
             }
             if (!ok) bar.failed = 1;
-            mma_commit(&bar.sums[p & 1]);
             return ok;
         });
     } else if (Mx && warp >= 4 && warp < 8) {
@@ -295,25 +301,29 @@ __device__ __forceinline__ void stay(uint8_t* smem, StayBarriers& bar, const Map
         few::wait_for_kernel_before();  // before anything is written that an earlier kernel may still read
         bool ok = true;                 // once a wait ran out none follows, as above
         walk([&](uint32_t p, int e, int row0, int c0, int n) {
-            if (lane == 0 && ok) ok = mbar_wait(&bar.sums[p & 1], (p >> 1) & 1u);
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
-            fence_after_sync();
+            for (int k = 0; k < chunks; ++k) {
+                const uint32_t turn = p * chunks + k;
+                if (lane == 0 && ok) ok = mbar_wait(&bar.sums[turn % S::accs], (turn / S::accs) & 1u);
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
+                fence_after_sync();
 #pragma unroll 1
-            for (int c = 0; c < N && ok; c += 16) {
-                uint32_t v[16];
-                tmem_ld16(tm + quadrant + (p & 1) * S::acc + c, v);
-                tmem_ld_wait();
+                for (int c = 0; c < N && ok; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(tm + quadrant + turn % S::accs * S::acc + c, v);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; i += T) {
-                    float sum = __uint_as_float(v[i + T - 1]);
+                    for (int i = 0; i < 16; i += T) {
+                        float sum = __uint_as_float(v[i + T - 1]);
 #pragma unroll
-                    for (int j = T - 2; j >= 0; --j) sum += __uint_as_float(v[i + j]);
-                    red[(c + i) / T * few::kRedPitch + 32 * q + lane] = sum;
+                        for (int j = T - 2; j >= 0; --j) sum += __uint_as_float(v[i + j]);
+                        float& to = red[(c + i) / T * few::kRedPitch + 32 * q + lane];
+                        to = k ? to + sum : sum;
+                    }
                 }
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) arrive(&bar.free[turn % S::accs]);
             }
-            fence_before_sync();
-            __syncwarp();
-            if (lane == 0) arrive(&bar.free[p & 1]);
             asm volatile("bar.sync 2, 128;" ::: "memory");
             if (ok) put(e, row0, c0, n, red, q);
             asm volatile("bar.sync 2, 128;" ::: "memory");
