@@ -38,10 +38,9 @@ __global__ void __launch_bounds__(256) k_few_halves(const bf16* __restrict__ x, 
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float by = i & 1 ? 0.0625f : 1.f;
-        o[i] = pack_half2(r[i] * by, r[i + 4] * by);
+        o[i] = pack_half2(r[i], r[i + 4]);
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o[i]));
-        sum += (f.x + f.y) * (i & 1 ? 16.f : 1.f);
+        sum += f.x + f.y;
     }
     for (int d = 1; d < group / 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     if (in) {

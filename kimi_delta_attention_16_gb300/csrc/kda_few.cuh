@@ -3,20 +3,25 @@
 //
 // Bound by the codes' bytes and by the instructions that take them apart.  A scale of any value cannot go to the
 // block-scaled tensor cores, so codes become fp16 operands of mma.sync (m16n8k16, fp32 accumulation: its narrow side of 8
-// fits a few tokens) by a mask alone: four bits in a half's mantissa are the subnormal code 2^-24, or 16 code 2^-24 from the
-// next four bits, where the column's element is kept divided by 16.  The 8 to be taken off is not taken off the codes: a
-// group's sum starts from -8 times the sum of the column's elements in it.  (Codes as 1024 + code, 1032 taken off in
-// registers, were 16 instructions more per 512 weights.)  A group's sum is multiplied by the weights' scale in fp32
-// when it is added up: scales are never rounded.
+// fits a few tokens) by a shift and a mask: four bits in a half's mantissa are the subnormal code 2^-20.  The 8 to be taken
+// off is not taken off the codes: a group's sum starts from -8 times the sum of the column's elements in it.  (Codes as
+// 1024 + code, 1032 taken off in registers, were 16 instructions more per 512 weights.)  A group's sum is multiplied by
+// the weights' scale in fp32 when it is added up: scales are never rounded.
+//
+// The instruction lines products up by their operands' exponents, which for a subnormal is that of 2^-14 whatever its
+// leading zeros, and drops what lies too far below the largest.  Codes lie in mantissa bits 4 to 7, which leaves 1.2e-7 of
+// a product over 2,048 elements.  In bits 0 to 3 for every other element (no shift for three of four) it was
+// 5e-7, and 4e-6 to 7e-6 for experts, whose hidden values spread over more exponents; 160,000 x 7,168 codes and 16 tokens
+// took 178 us against 185.
 //
 // Columns are prepared by a kernel in front (k_few_halves): each run of 128 elements is brought to 2^14..2^15 by a
-// power of two, which is exact for a bf16 element down to 2^-27 of its run's largest and off by at most 2^-35 of the largest
+// power of two, which is exact for a bf16 element down to 2^-31 of its run's largest and off by at most 2^-39 of the largest
 // below that, less than an fp32 sum would keep; fp32 values are two columns, value and remainder.  The power's
 // inverse is multiplied in at the end of a run.
 //
 // A CTA has 8 or 12 warps.  A warp takes 32 rows, two tiles of an instruction, so that each operand of the columns is read from
-// shared memory once for both and their chains of instructions overlap (16 warps of 16 rows each: 199 us instead of
-// 178 for 160,000 x 7,168 codes and 16 tokens).  Its codes and scales go through cp.async into a ring of its own
+// shared memory once for both and their chains of instructions overlap (16 warps of 16 rows each: 12 % longer for 160,000
+// x 7,168 codes and 16 tokens).  Its codes and scales go through cp.async into a ring of its own
 // (32 rows x 256 elements a stage), no barrier among warps.  All columns of a segment of K are in shared memory for all
 // warps, the next segment's on their way meanwhile: one barrier per segment.  `ks` warps share 32 rows along K where there
 // are few rows.
@@ -95,7 +100,7 @@ struct Weights {  // of one matrix [rows][K]
 struct Columns {  // laid out by k_few_halves
     const __half* x;      // [.][K]
     const float* factor;  // [.][runs of 128]: what a sum is to be multiplied by
-    const float* sums;    // [.][groups]: -8 2^-24 times the sum of a group's elements
+    const float* sums;    // [.][groups]: -8 2^-20 times the sum of a group's elements
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -120,14 +125,12 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-// Eight codes as four pairs of fp16: elements (0,4) as code 2^-24, (1,5) as 16 code 2^-24, (2,6) and (3,7) likewise.  The
-// columns are laid out in that order, elements 1, 3, 5 and 7 divided by 16.
+// Eight codes as four pairs of fp16, code 2^-20: elements (0,4), (1,5), (2,6), (3,7).  The columns are laid out in that order.
 __device__ __forceinline__ void part(uint32_t w, uint32_t (&p)[4]) {
-    const uint32_t h = w >> 8;
-    p[0] = w & 0x000f000fu;
+    p[0] = w << 4 & 0x00f000f0u;
     p[1] = w & 0x00f000f0u;
-    p[2] = h & 0x000f000fu;
-    p[3] = h & 0x00f000f0u;
+    p[2] = w >> 4 & 0x00f000f0u;
+    p[3] = w >> 8 & 0x00f000f0u;
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -136,13 +139,13 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 }
 
 // The power of two that brings a magnitude with these fp32 exponent bits to 2^14..2^15 (as far as fp32 has
-// one), and what sums of subnormal codes are to be multiplied by: its inverse times 2^24.  Magnitudes from 2^117 on, for which
+// one), and what sums of subnormal codes are to be multiplied by: its inverse times 2^20.  Magnitudes from 2^121 on, for which
 // fp32 has none, get NaN.
 __device__ __forceinline__ void run_scale(uint32_t exponent, float& up, float& down) {
     const uint32_t e = 268u - exponent;             // 127 + 14 + 127 - exponent
     const uint32_t b = e > 254u ? 254u : e;
     up = __uint_as_float(b << 23);
-    const uint32_t d = 254u - b + 24u;
+    const uint32_t d = 254u - b + 20u;
     down = d < 255u ? __uint_as_float(d << 23) : NAN;
 }
 
@@ -158,7 +161,7 @@ inline size_t columns_bytes(int64_t n, int64_t K, int group) {
 // The columns of bf16 rows [rows][K] (K a multiple of the group).
 cudaError_t launch_halves(const bf16* x, int64_t xs, bool wide, int rows, int K, int group, const Columns& columns, cudaStream_t s);
 
-constexpr float kSumOf = -8.f * 0x1p-24f;
+constexpr float kSumOf = -8.f * 0x1p-20f;
 
 // One product by itself, for a sum that came out as NaN: a row of x with an infinity or values that no factor is for.
 static __device__ __noinline__ float direct(const uint8_t* codes, const uint8_t* scales, int scale_bytes, int group, const bf16* x, int K) {

@@ -259,7 +259,6 @@ struct Direct {  // the operands as they were given, for sums that come out as N
     int64_t xs;
 };
 
-
 // First products.  Warps 0 to 3 take 128 rows of the gate's half, 4 to 7 the same of the other; the hidden values become
 // two columns of the second products' (value and remainder) where they arise, 128 rows under one power of two.
 template <int NT, int GS, int SB>
@@ -318,18 +317,17 @@ __global__ void __launch_bounds__(32 * kExpertWarps, 1) k_moe_in(const Experts p
             // element k of eight lies at the place where codes come out of a word: (0,4) (1,5) (2,6) (3,7)
             const int place = (lane & ~7) + 2 * (lane & 3) + (lane >> 2 & 1);
             const int64_t at = (int64_t)(c0 + c) * 2;
-            const float by = lane & 1 ? 0.0625f : 1.f, back = lane & 1 ? 16.f : 1.f;
             float sum_hi = 0.f, sum_lo = 0.f;  // of a group, as far as it goes
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (row0 + 32 * i >= F) break;  // F is a multiple of the group
-                const float x = v[i] * up * by;
+                const float x = v[i] * up;
                 const __half hi = __float2half_rn(x);
                 const float h = __half2float(hi);
                 const __half lo = __float2half_rn(isinf(h) ? 0.f : x - h);
                 columns[at * F + row0 + 32 * i + place] = hi;
                 columns[(at + 1) * F + row0 + 32 * i + place] = lo;
-                sum_hi += h * back, sum_lo += __half2float(lo) * back;
+                sum_hi += h, sum_lo += __half2float(lo);
                 if ((i + 1) * 32 % p.group == 0) {
 #pragma unroll
                     for (int d = 16; d; d >>= 1) {

@@ -169,6 +169,28 @@ def test_gemm4_offsets_past_32_bits(fmt, sdt):
     within(got[:, -200:], ref, err + U[F32] * ref.abs())
 
 
+def close_in_norm(got, ref, units):
+    """The error of all outputs together, in units of 2^-24 of theirs: roundings are independent, so those of one kind come to
+    one unit at most however many outputs there are, while a systematic loss of bits stands out."""
+    err = float((f64(got) - ref).norm() / ref.norm()) * 2.0 ** 24
+    assert err <= units, f"{err:.1f} units of 2^-24, {units} allowed"
+
+
+# A product: roundings of the column (1), of partial sums (each 32 elements' sum and each of the K / 32 additions rounds at
+# about the size of the final sum or below, which in norm is sqrt(K / 32) units at most).
+@pytest.mark.parametrize("fmt,group,sdt", FORMATS)
+@pytest.mark.parametrize("M", [1, 8, 40])
+@pytest.mark.parametrize("spread", [False, True])
+def test_gemm4_keeps_fp32(M, fmt, group, sdt, spread):
+    K = 2048
+    g = gen(M + K)
+    x = randn(g, M, K, dtype=F32)
+    x = (x * randn(g, M, K, dtype=F32) if spread else x).to(BF16)  # products of normal values spread over more exponents
+    codes, scales = lib.random_weight(g, 256, K, fmt=fmt, group=group, scale_dtype=sdt)
+    got = kda.kda_gemm4(x.cuda(), codes.cuda(), scales.cuda(), out_dtype=F32)
+    close_in_norm(got, lib.gemm4_ref(x, lib.unpack_ref(codes, scales), "none")[0], 1 + (K / 32) ** 0.5)
+
+
 # ------------------------------------------------------------------ mixture of experts
 def make_moe(M, E, D, F, fmt, group, sdt, seed, router_dtype=BF16):
     g = gen(seed + M + E + D + F)
@@ -203,6 +225,19 @@ def check_moe(M, E, top, D, F, fmt="e2m1", group=32, sdt=None, score="sigmoid", 
                                          (20, 4, 4, 256, 128), (33, 300, 5, 128, 128)])
 def test_moe_sizes(M, E, top, D, F, fmt, group, sdt):
     check_moe(M, E, top, D, F, fmt, group, sdt)
+
+
+# Two products in a row, the silu and the product of its two sides (its derivative is at most 1.1: the first products' errors
+# pass on about once for the gate and once for the other side, sqrt(2) times), the hidden value's rounding and the weight's,
+# the sum over the experts: sqrt(2) (1 + sqrt(D / 32)) + (1 + sqrt(F / 32)) + 4 units.
+@pytest.mark.parametrize("fmt,group,sdt", FORMATS + [("bf16", 0, None)])
+@pytest.mark.parametrize("M,E,top,D,F", [(1, 6, 3, 1536, 512), (6, 4, 2, 1024, 768), (12, 2, 2, 512, 384)])
+def test_moe_keeps_fp32(M, E, top, D, F, fmt, group, sdt):
+    x, router, bias, wi, wo, wi64, wo64 = make_moe(M, E, D, F, fmt, group, sdt, 5)
+    pair = lambda w: w.cuda() if isinstance(w, torch.Tensor) else tuple(t.cuda() for t in w)  # noqa: E731
+    y = kda.kda_moe(x.cuda(), router.cuda(), pair(wi), pair(wo), top, bias=bias.cuda(), out_dtype=F32)
+    ref = lib.moe_ref(x, router, wi64, wo64, top, bias, "sigmoid", 1.0)[0]
+    close_in_norm(y, ref, 2 ** 0.5 * (1 + (D / 32) ** 0.5) + (1 + (F / 32) ** 0.5) + 4)
 
 
 @pytest.mark.parametrize("M,E,top,D,F,fmt", [(7, 33, 3, 1056, 352, "int4"), (2, 10, 2, 96, 32, "e2m1"), (5, 6, 2, 72, 40, "bf16"),
