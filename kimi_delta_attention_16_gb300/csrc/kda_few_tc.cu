@@ -40,15 +40,15 @@ cudaError_t launch_digits(const bf16* x, int64_t xs, bool wide, const int* of, i
     return few::launch_kernel(k_few_digits, dim3((K + 2047) / 2048, tokens), 256, 1, 0, of != nullptr, s, x, xs, wide, of, per, K, digits, scales);
 }
 
-// bf16 rows as they are, dense: token p is row of[p] / per of x (p itself without `of`).
+// bf16 rows as they are, dense: token p is row of[p] / per of x.
 __global__ void __launch_bounds__(256) k_few_rows(const bf16* __restrict__ x, int64_t xs, bool wide, const int* __restrict__ of, int per, int K,
                                                   bf16* __restrict__ rows) {
-    if (of) few::wait_for_kernel_before();  // the lists
+    few::wait_for_kernel_before();  // the lists
     few::let_next_kernel_begin();
     const int64_t p = blockIdx.y;
     const int k = (blockIdx.x * 256 + threadIdx.x) * 8;  // K is a multiple of 8
     if (k >= K) return;
-    const bf16* row = x + (int64_t)(of ? of[p] / per : (int)p) * xs + k;
+    const bf16* row = x + (int64_t)(of[p] / per) * xs + k;
     bf16* to = rows + p * K + k;
     if (wide) {
         *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(row);
@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(256) k_few_rows(const bf16* __restrict__ x, in
 }
 
 cudaError_t launch_rows(const bf16* x, int64_t xs, bool wide, const int* of, int per, int tokens, int K, bf16* rows, cudaStream_t s) {
-    return few::launch_kernel(k_few_rows, dim3((K + 2047) / 2048, tokens), 256, 1, 0, of != nullptr, s, x, xs, wide, of, per, K, rows);
+    return few::launch_kernel(k_few_rows, dim3((K + 2047) / 2048, tokens), 256, 1, 0, true, s, x, xs, wide, of, per, K, rows);
 }
 
 }  // namespace fewtc

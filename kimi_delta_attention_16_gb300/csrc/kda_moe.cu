@@ -23,8 +23,10 @@ using namespace few;
 
 // ------------------------------------------------------------------ scores
 // A choice between two experts hangs on the last digits of a sum over thousands of products, so logits and scores are
-// pairs of fp32 (kda_wide.cuh).  A block takes EB experts and TB tokens, its warps share the rows: with one token all of the
-// router is on its way at once; with many, four by four keep what is read from L2 below what the sums take.
+// pairs of fp32 (kda_wide.cuh).  A block takes one expert and TB tokens, its warps share the rows.  One token: all of the
+// router is on its way at once; a block that stands for four takes 6 us longer (896 experts, 3,584 channels).  More: four
+// tokens share what is read of the router, 99 us instead of 118 for a small layer behind the same router and 32
+// tokens; four experts by four tokens: 97.
 constexpr int kScoreThreads = 256, kScoreWarps = 8;
 
 __device__ __forceinline__ uint32_t ordered(float v) {  // a larger value is a larger integer
@@ -44,55 +46,49 @@ template <typename T> __device__ __forceinline__ void load8_any(const T* p, bool
     }
 }
 
-template <typename Tr, int EB, int TB>
+template <typename Tr, int TB>
 __global__ void __launch_bounds__(kScoreThreads) k_moe_scores(const bf16* __restrict__ x, int64_t xs, bool xwide, const Tr* __restrict__ router,
                                                               bool rwide, const float* __restrict__ bias, int M, int E, int D,
                                                               int sigmoid, Wide* __restrict__ score, uint64_t* __restrict__ key,
                                                               int* __restrict__ done) {
-    __shared__ Wide sums[kScoreWarps][EB * TB];
+    __shared__ Wide sums[kScoreWarps][TB];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int e0 = blockIdx.x * EB, t0 = blockIdx.y * TB;
-    if (e0 == 0 && t0 == 0 && threadIdx.x == 0) *done = 0;
-    Sum2 s[EB][TB];
-#pragma unroll EB * TB == 1 ? 2 : 1
+    const int e = blockIdx.x, t0 = blockIdx.y * TB;
+    if (e == 0 && t0 == 0 && threadIdx.x == 0) *done = 0;
+    Sum2 s[TB];
+#pragma unroll TB == 1 ? 2 : 1
     for (int k = threadIdx.x * 8; k < D; k += kScoreThreads * 8) {
-        float rv[EB][8], xv[TB][8];
-#pragma unroll
-        for (int i = 0; i < EB; ++i) load8_any(router + (int64_t)min(e0 + i, E - 1) * D + k, rwide, rv[i]);
+        float rv[8], xv[TB][8];
+        load8_any(router + (int64_t)e * D + k, rwide, rv);
 #pragma unroll
         for (int j = 0; j < TB; ++j) load8_any(x + (int64_t)min(t0 + j, M - 1) * xs + k, xwide, xv[j]);
 #pragma unroll
-        for (int i = 0; i < EB; ++i)
+        for (int j = 0; j < TB; ++j)
 #pragma unroll
-            for (int j = 0; j < TB; ++j)
-#pragma unroll
-                for (int v = 0; v < 8; ++v) {
-                    const float p = xv[j][v] * rv[i][v];  // exact for a bf16 router
-                    s[i][j].add(p);
-                    if constexpr (sizeof(Tr) == 4) s[i][j].lo += fmaf(xv[j][v], rv[i][v], -p);
-                }
+            for (int v = 0; v < 8; ++v) {
+                const float p = xv[j][v] * rv[v];  // exact for a bf16 router
+                s[j].add(p);
+                if constexpr (sizeof(Tr) == 4) s[j].lo += fmaf(xv[j][v], rv[v], -p);
+            }
     }
 #pragma unroll
-    for (int i = 0; i < EB; ++i)
+    for (int j = 0; j < TB; ++j) {
 #pragma unroll
-        for (int j = 0; j < TB; ++j) {
-#pragma unroll
-            for (int d = 16; d; d >>= 1) {
-                const float h = __shfl_xor_sync(0xffffffffu, s[i][j].hi, d), l = __shfl_xor_sync(0xffffffffu, s[i][j].lo, d);
-                s[i][j].add(h);
-                s[i][j].lo += l;
-            }
-            if (lane == 0) sums[warp][i * TB + j] = wide(s[i][j]);
+        for (int d = 16; d; d >>= 1) {
+            const float h = __shfl_xor_sync(0xffffffffu, s[j].hi, d), l = __shfl_xor_sync(0xffffffffu, s[j].lo, d);
+            s[j].add(h);
+            s[j].lo += l;
         }
+        if (lane == 0) sums[warp][j] = wide(s[j]);
+    }
     __syncthreads();
-    const int i = threadIdx.x / TB, j = threadIdx.x % TB;
+    const int j = threadIdx.x;
     let_next_kernel_begin();
     wait_for_kernel_before();  // the columns' kernel, if one runs beside this: what comes next counts on both
-    if (i < EB && e0 + i < E && t0 + j < M) {
-        const int e = e0 + i;
-        Wide v = sums[0][threadIdx.x];
+    if (j < TB && t0 + j < M) {
+        Wide v = sums[0][j];
 #pragma unroll
-        for (int w = 1; w < kScoreWarps; ++w) v = add(v, sums[w][threadIdx.x]);
+        for (int w = 1; w < kScoreWarps; ++w) v = add(v, sums[w][j]);
         const int64_t at = (int64_t)(t0 + j) * E + e;
         const Wide logit = v;
         if (sigmoid) v = sigmoid_wide(v);
@@ -382,12 +378,12 @@ __global__ void __launch_bounds__(32 * kExpertWarps, 1) k_moe_out(const Experts 
 }
 
 // ------------------------------------------------------------------ e2m1 and bf16 experts
-// The place of a slot in the lists is its row in the columns of the second product, and of the first one where a token's
-// columns are repeated for each of its experts; where all tokens fit into the columns at once (by_token) every expert
-// takes them all and leaves those it was not chosen for.
+// The place of a slot in the lists is its row in the columns of both products: a token's columns are repeated for each of
+// its experts.  (Tokens' own columns for all experts at once, where they fit: the same time for 1 to 16 tokens.)
 //
-// A kernel may begin beside the one in front of it.  Where that is not the choice itself the lists are complete by then
-// (that one has waited for the choice), so weights and their scales can be on their way before the columns are written.
+// A kernel may begin beside the one in front of it.  That one, the columns' or the first products', has waited for the
+// choice before it let this one begin, so the lists are complete, and weights and their scales can be on their way
+// before the columns are written.
 // First products: the hidden values become digits (four bf16 columns, the last of zeros, for bf16 weights) where they
 // arise.  32 rows of a token share a scale: a warp's lanes.
 template <int N, bool Mx>
@@ -403,7 +399,7 @@ k_moe_in_tc(const __grid_constant__ fewtc::Maps maps, const fewtc::StayArgs p, c
     fewtc::stay<N, Mx ? 8 : 1, Mx>(smem, bar, maps, p, d_status, [&](int e, int row0, int c0, int n, const float* red, int q) {
         for (int i = q; i < 2 * n; i += 4) {
             const int c = i >> 1, r = (i & 1) * 32 + lane, f = row0 + r, token = slots[c0 + c] / p.top;
-            const float* sum = red + (p.by_token ? token : c) * kRedPitch + r;
+            const float* sum = red + c * kRedPitch + r;
             float gate = sum[0], up = sum[64];
             if constexpr (Mx) {
                 if (f < F && (isnan(gate) || isnan(up))) {
@@ -478,13 +474,11 @@ template <typename Tr> cudaError_t launch_scores(const kda_moe_args& a, int64_t 
     const Tr* r = static_cast<const Tr*>(a.router);
     const bool rwide = reinterpret_cast<uintptr_t>(r) % 16 == 0;
     const int sg = a.score == KDA_SCORE_SIGMOID;
-    const auto go = [&](auto kernel, int eb, int tb) {
-        return launch_kernel(kernel, dim3((a.E + eb - 1) / eb, (a.M + tb - 1) / tb), kScoreThreads, 1, 0, beside, s, x, xs, xwide, r, rwide, a.bias, a.M,
+    const auto go = [&](auto kernel, int tb) {
+        return launch_kernel(kernel, dim3(a.E, (a.M + tb - 1) / tb), kScoreThreads, 1, 0, beside, s, x, xs, xwide, r, rwide, a.bias, a.M,
                              a.E, a.D, sg, score, key, done);
     };
-    if (a.M == 1) return go(k_moe_scores<Tr, 1, 1>, 1, 1);
-    if (a.M <= 4) return go(k_moe_scores<Tr, 1, 4>, 1, 4);
-    return go(k_moe_scores<Tr, 4, 4>, 4, 4);
+    return a.M == 1 ? go(k_moe_scores<Tr, 1>, 1) : go(k_moe_scores<Tr, 4>, 4);
 }
 
 template <int NT, int GS, int SB>
@@ -523,36 +517,35 @@ int box_for(int tokens, int T, int most) {
 
 template <bool Mx>
 cudaError_t launch_experts_tc(const kda_moe_args& a, const MoePlan& p, const int* lists, const bf16* x, int64_t xs, bool xwide, const float* weights,
-                              float* parts, int most, int columns, bool by_token, cudaStream_t s) {
+                              float* parts, int most, int columns, cudaStream_t s) {
     char* ws = static_cast<char*>(a.workspace);
-    const int slots = a.M * a.top, rows = by_token ? a.M : slots;
+    const int slots = a.M * a.top;
     uint8_t* xc = reinterpret_cast<uint8_t*>(ws + p.x_columns);
     uint8_t* hc = reinterpret_cast<uint8_t*>(ws + p.hidden);
-    uint8_t *xsc = xc + fewtc::digits_bytes(rows, a.D), *hsc = hc + fewtc::digits_bytes(slots, a.F);
+    uint8_t *xsc = xc + fewtc::digits_bytes(slots, a.D), *hsc = hc + fewtc::digits_bytes(slots, a.F);
     const int in_box = box_for(columns, Mx ? 8 : 1, Mx ? 128 : 64), out_box = box_for(columns, Mx ? 8 : 4, Mx ? 128 : 64);
     const int* of = lists + 2 + 2 * a.E;
     fewtc::Maps in, out;
     cudaError_t e = cudaSuccess;
     if constexpr (Mx) {
-        if (!fewtc::encode_maps(&in, a.w_in, (int64_t)a.E * 2 * a.F, xc, rows, a.D, in_box) ||
+        if (!fewtc::encode_maps(&in, a.w_in, (int64_t)a.E * 2 * a.F, xc, slots, a.D, in_box) ||
             !fewtc::encode_maps(&out, a.w_out, (int64_t)a.E * a.D, hc, slots, a.F, out_box))
             return cudaErrorInvalidValue;
-        if (!by_token) e = fewtc::launch_digits(x, xs, xwide, of, a.top, slots, a.D, xc, xsc, s);
+        e = fewtc::launch_digits(x, xs, xwide, of, a.top, slots, a.D, xc, xsc, s);
     } else {
-        if (!fewtc::encode_maps_bf16(&in, a.w_in, (int64_t)a.E * 2 * a.F, xc, rows, a.D, in_box) ||
+        if (!fewtc::encode_maps_bf16(&in, a.w_in, (int64_t)a.E * 2 * a.F, xc, slots, a.D, in_box) ||
             !fewtc::encode_maps_bf16(&out, a.w_out, (int64_t)a.E * a.D, hc, 4 * (int64_t)slots, a.F, out_box))
             return cudaErrorInvalidValue;
-        if (!by_token) e = fewtc::launch_rows(x, xs, xwide, of, a.top, slots, a.D, reinterpret_cast<bf16*>(xc), s);
+        e = fewtc::launch_rows(x, xs, xwide, of, a.top, slots, a.D, reinterpret_cast<bf16*>(xc), s);
     }
     if (e) return e;
     fewtc::StayArgs pi = {}, po = {};
     pi.w_scales = static_cast<const uint8_t*>(a.w_in_scales), pi.b_scales = xsc;
     pi.rows = 2 * a.F, pi.half = a.F, pi.K = a.D, pi.tile_rows = kTileRows / 2, pi.tiles = (a.F + 63) / 64;
-    pi.lists = lists, pi.E = a.E, pi.top = a.top, pi.tokens = rows, pi.by_token = by_token;
+    pi.lists = lists, pi.E = a.E, pi.top = a.top, pi.tokens = slots;
     po = pi;
     po.w_scales = static_cast<const uint8_t*>(a.w_out_scales), po.b_scales = hsc;
     po.rows = a.D, po.half = 64, po.K = a.F, po.tile_rows = kTileRows, po.tiles = (a.D + kTileRows - 1) / kTileRows;
-    po.tokens = slots, po.by_token = false;
     const Direct given{static_cast<const uint8_t*>(a.w_in), static_cast<const uint8_t*>(a.w_in_scales), x, xs};
     switch (in_box) {
         case 16: e = launch_in_tc<16, Mx>(in, pi, most, given, hc, hsc, a.d_status, s); break;
@@ -622,26 +615,22 @@ cudaError_t launch_moe(const kda_moe_args& a, const MoePlan& p, cudaStream_t s) 
     const int even = 2 * ((slots + a.E - 1) / a.E) + 2, columns = a.M < even ? a.M : even;
     const bf16* x = static_cast<const bf16*>(a.x);
     const bool mx = a.format == KDA_WEIGHT_E2M1, tc = mx || a.format == KDA_WEIGHT_BF16;
-    const bool by_token = tc && a.M == columns && a.M <= (mx ? 16 : 64);
     cudaError_t e;
-    // columns that need no lists come first: the router's scores run beside them
-    if (by_token || !tc) {
-        uint8_t* xc = reinterpret_cast<uint8_t*>(ws + p.x_columns);
-        e = mx   ? fewtc::launch_digits(x, xs, xwide, nullptr, 1, a.M, a.D, xc, xc + fewtc::digits_bytes(a.M, a.D), s)
-            : tc ? fewtc::launch_rows(x, xs, xwide, nullptr, 1, a.M, a.D, reinterpret_cast<bf16*>(xc), s)
-                 : launch_halves(x, xs, xwide, a.M, a.D, a.group, columns_at(xc, a.M, a.D), s);
+    // integer codes: columns that need no lists come first, the router's scores run beside them
+    if (!tc) {
+        e = launch_halves(x, xs, xwide, a.M, a.D, a.group, columns_at(ws + p.x_columns, a.M, a.D), s);
         if (e) return e;
     }
-    e = a.router_dtype == KDA_BF16 ? launch_scores<bf16>(a, xs, xwide, score, key, done, by_token || !tc, s)
-                                   : launch_scores<float>(a, xs, xwide, score, key, done, by_token || !tc, s);
+    e = a.router_dtype == KDA_BF16 ? launch_scores<bf16>(a, xs, xwide, score, key, done, !tc, s)
+                                   : launch_scores<float>(a, xs, xwide, score, key, done, !tc, s);
     if (e) return e;
     if ((e = launch_kernel(k_moe_pick, dim3(a.M), kPickThreads, 1, 0, true, s, score, key, a.M, a.E, a.top, (int)(a.score == KDA_SCORE_SIGMOID),
                            a.scale, ids, weights, done, lists, a.ids, a.weights)))
         return e;
     if (mx) {
-        e = launch_experts_tc<true>(a, p, lists, x, xs, xwide, weights, parts, most, columns, by_token, s);
+        e = launch_experts_tc<true>(a, p, lists, x, xs, xwide, weights, parts, most, columns, s);
     } else if (tc) {
-        e = launch_experts_tc<false>(a, p, lists, x, xs, xwide, weights, parts, most, columns, by_token, s);
+        e = launch_experts_tc<false>(a, p, lists, x, xs, xwide, weights, parts, most, columns, s);
     } else {
         const int sb = a.scale_dtype == KDA_BF16 ? 2 : 4;
         Experts in = {}, out = {};

@@ -58,7 +58,6 @@ struct StayArgs {
     int tiles;            // per expert
     const int* lists;     // experts in use; which; where their places begin; the places' slots
     int E, top, tokens;   // tokens: rows of the columns' tensor / T
-    bool by_token;        // the columns are the tokens themselves, every expert takes them all
 };
 
 // The epilogue is called by warps 8 to 11 with a tile's sums in red[token][128 rows]: put(expert, first row of the tile, first
@@ -71,7 +70,6 @@ __device__ __forceinline__ void stay(uint8_t* smem, StayBarriers& bar, const Map
     float* red = reinterpret_cast<float*>(smem + S::ring + S::scales);
     uint16_t* which = reinterpret_cast<uint16_t*>(smem + S::ring + S::scales + S::red);
     uint16_t* begin = which + kMaxExperts;
-    if (a.by_token) few::wait_for_kernel_before();  // the kernel in front is the choice itself; else the lists are complete
     const int experts = a.lists[0];
     const int items = experts * a.tiles;
     if ((int)blockIdx.x >= items) return;
@@ -127,7 +125,7 @@ __device__ __forceinline__ void stay(uint8_t* smem, StayBarriers& bar, const Map
                 tma_2d(base + s * S::stage + kTileA / 2, &maps.w, x, e * a.rows + row0 + a.half, &bar.full[s]);
             };
             const auto columns = [&](int kb, uint32_t s) {
-                tma_2d(base + s * S::stage + kTileA, &maps.b, Mx ? kb * 128 : kb * S::stage_k, a.by_token ? 0 : c0 * T, &bar.full[s]);
+                tma_2d(base + s * S::stage + kTileA, &maps.b, Mx ? kb * 128 : kb * S::stage_k, c0 * T, &bar.full[s]);
             };
             int kb = 0;
             if (!waited) {  // the first round's weights, then - once they are written - its columns
@@ -208,7 +206,7 @@ __device__ __forceinline__ void stay(uint8_t* smem, StayBarriers& bar, const Map
             const int at = c.it / a.tiles, e = which[at];
             const int r = (c.it - at * a.tiles) * a.tile_rows + (q < 2 ? 0 : a.half - 64) + 32 * q + lane;
             c.ra = a.w_scales + ((int64_t)e * a.rows + min(r, a.rows - 1)) * pitch;
-            c.rb = a.b_scales + (int64_t)min((a.by_token ? 0 : c.c0) + token, a.tokens - 1) * pitch;
+            c.rb = a.b_scales + (int64_t)min(c.c0 + token, a.tokens - 1) * pitch;
         };
         const auto next = [&](Cursor& c) {
             if (++c.g < groups) return;
