@@ -704,7 +704,7 @@ kda_status kda_unpack4(const kda_pack4_args* args, kda_stream_t stream);
  * the few rows of a decode step (M up to 65,535; the weights are read once per 32 rows).
  * A [M][lda] bf16 (any alignment of its elements; 16-byte rows are read faster), C [M][ldc] bf16
  * or fp32, rounded once; epilogues as in kda_gemm; M, N >= 0; C must not overlap an input.
- * Values of A enter the products exactly but for what lies below 2^-22 of the largest of their 32 (e2m1) or 2^-35 of
+ * Values of A enter the products exactly but for what lies below 2^-22 of the largest of their 32 (e2m1) or 2^-39 of
  * the largest of their 128 (int4); sums are fp32, in a fixed order.  A row of A with values that are not finite gives what
  * the formula gives, slowly.  Needs an sm_103 device.  A wait that times out on the device is reported through
  * d_status (KDA_ERR_TIMEOUT). */
@@ -741,7 +741,7 @@ kda_status kda_gemm4(const kda_gemm4_args* args, kda_stream_t stream);
  *   of 8 for bf16
  *   y [M][y_stride] bf16 or fp32; ids [M][top] int32 and weights [M][top] fp32, best first, or NULL
  * The values between the two products keep 22 bits or more of the largest of their 32 (e2m1), 128 (int4) or of their
- * own (bf16); sums are fp32.  One that is not finite (or, int4, beyond 2^117) makes its token's y
+ * own (bf16); sums are fp32.  One that is not finite (or, int4, beyond 2^121) makes its token's y
  * NaN, of the others nothing changes.  E up to 1024, top up
  * to 32 and to E, M * top up to 65535, E * 2F and E * D up to 2^30.  Needs an sm_103 device; a wait that times out on the
  * device is reported through d_status (KDA_ERR_TIMEOUT). */

@@ -400,7 +400,7 @@ __device__ __forceinline__ void products(uint8_t* smem, const Weights& w, const 
 }
 
 // CTAs along the rows, for `blocks` blocks of columns: all SMs, as far as there are tiles of 32 rows, and warps that share
-// a tile along K: the number that leaves a CTA the least to do.
+// a tile along K: the number that leaves a CTA the least to do (1,024 x 7,168 for one row: 15 us, 30 with a warp per tile).
 struct Split {
     int ctas, ks;
 };

@@ -4,6 +4,12 @@
 // What a call has to read is N K / 2 bytes of codes and their scales.  e2m1 weights go through the block-scaled tensor
 // cores (kda_few_tc.cuh): a CTA takes 128 of the N outputs for some tokens, a cluster splits K.  Integer codes go
 // through registers (kda_few.cuh).
+//
+// On the GPU, columns included: e2m1, 12,288 x 7,168: 1 row 11 us (4.2 TB/s), 32 rows 17 us; 7,168 x 12,288, 256 rows 75 us.
+// One row is bound by the chain of two launches, first bytes and join; many by the bytes in flight towards the
+// SMs: a CTA of 32 tokens has 256 columns of digits, 48 KB a stage, four stages fill shared memory, and a stage
+// takes 0.40 us where its products take 0.29.  Integer codes, 160,000 x 7,168, 16 rows 183 us (3.2 TB/s): latency
+// of three warps per scheduler (issue 45 %, tensor pipe 32 %, HBM 37 %).
 #include "kda_few.cuh"
 #include "kda_few_tc.cuh"
 #include "kda_serve.cuh"
@@ -29,7 +35,7 @@ __device__ __forceinline__ float apply(int epi, float v) {
 }
 
 // A CTA takes an equal share of the tiles of 32 rows, 12 / ks at a time (8 / ks where more scales leave room for 8 warps'
-// rings only).
+// rings only; 12 warps 178 us where 8 took 185).
 constexpr int warps_for(int scale_row) { return scale_row <= 8 ? 12 : 8; }
 
 template <int NT, int GS, int SB> __global__ void __launch_bounds__(32 * warps_for(GS * SB), 1) k_gemm4(const Gemm4 p, void* __restrict__ out, bool out32) {
@@ -184,12 +190,15 @@ size_t gemm4_workspace(const kda_gemm4_args& a) {
 
 cudaError_t launch_gemm4(const kda_gemm4_args& a, cudaStream_t s) {
     if (a.format == KDA_WEIGHT_E2M1) {
+        // as few columns as hold all rows, and at most 32 rows' (256 rows: 82 us, 91 with 16 rows per CTA, 146 with 8)
         if (a.M <= 2) return launch_tc_out<16>(a, s);
         if (a.M <= 4) return launch_tc_out<32>(a, s);
         if (a.M <= 8) return launch_tc_out<64>(a, s);
         if (a.M <= 16) return launch_tc_out<128>(a, s);
         return launch_tc_out<256>(a, s);
     }
+    // 8 columns an instruction: one, two or four of them (160,000 x 7,168 for 16 rows: 302, 193 and 283 us; 1,001 x 1,056 for
+    // 5: 13, 15 and 23)
     if (a.M <= 8) return launch_scales<1>(a, s);
     if (a.M <= 16) return launch_scales<2>(a, s);
     return launch_scales<4>(a, s);
