@@ -89,6 +89,17 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// The warp that issues products runs as a whole, one lane of it issues: what an instruction takes is then known to be the same in all
+// lanes and stays where the instruction takes it from.  Under a branch for one lane each product takes some 90 cycles
+// to issue, more than most take to run.
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0); }
+__device__ __forceinline__ bool elected() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)); }
+
 // What one product reads.  The tile's rows are two runs of 64.
 struct Tile {
     const CUtensorMap *w, *b; // codes of the weights in boxes of 64 rows, digits of the columns in boxes of N
@@ -166,7 +177,7 @@ struct Counters {  // of stages, places of scales and products so far: the barri
 // barrier of the CTA.  After a wait that ran out bar.failed is set and red holds nothing of use.
 template <int N> __device__ __forceinline__ void product(uint8_t* ring, Barriers& bar, const Tile& t, Counters& c, float* red) {
     using S = Shape<N>;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int blocks = (t.k1 - t.k0 + kStageK - 1) / kStageK, groups = (blocks + 1) / 2;
     const uint32_t base = smem_u32(ring), tm = bar.tmem;
     if (warp == 0 && lane == 0) {
@@ -208,26 +219,31 @@ template <int N> __device__ __forceinline__ void product(uint8_t* ring, Barriers
             for (int kb = issued > S::stages ? issued - S::stages : 0; kb < issued; ++kb)
                 mbar_wait(&bar.full[(c.stage + kb) % S::stages], ((c.stage + kb) / S::stages) & 1u);
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
+        const uint64_t rows = desc_sw128(base, 16, 1024), columns = desc_sw128(base + kTileA, 16, 1024);
         for (int kb = 0; kb < blocks; ++kb) {
             const uint32_t i = c.stage + kb, s = i % S::stages, gi = c.slot + kb / 2, slot = gi % kSlots;
-            if (!mbar_wait(&bar.full[s], (i / S::stages) & 1u) ||
-                ((kb & 1) == 0 && !mbar_wait(&bar.scales_full[slot], (gi / kSlots) & 1u))) {
+            if (!warp_wait(&bar.full[s], (i / S::stages) & 1u) ||
+                ((kb & 1) == 0 && !warp_wait(&bar.scales_full[slot], (gi / kSlots) & 1u))) {
                 bar.failed = 1;
                 break;
             }
             fence_after_sync();
-            const uint32_t at = base + s * S::stage, sf = tm + S::scales_at + slot * S::group;
+            if (elected()) {
+                const uint32_t at = s * (S::stage >> 4), sf = tm + S::scales_at + slot * S::group;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                const int set = 2 * (kb & 1) + (kk >> 1);  // of 128 elements
-                mma_mxf4(tm, desc_sw128(at + kk * 32, 16, 1024), desc_sw128(at + kTileA + kk * 32, 16, 1024), idesc_mxf4(N, 2 * (kk & 1)),
-                         sf + 4 * set, sf + 16 + S::set * set, (kb | kk) != 0);
+                for (int kk = 0; kk < 4; ++kk) {
+                    const int set = 2 * (kb & 1) + (kk >> 1);  // of 128 elements
+                    mma_mxf4(tm, rows + at + 2 * kk, columns + at + 2 * kk, idesc_mxf4(N, 2 * (kk & 1)), sf + 4 * set, sf + 16 + S::set * set,
+                             (kb | kk) != 0);
+                }
+                mma_commit(&bar.empty[s]);
+                if ((kb & 1) || kb == blocks - 1) mma_commit(&bar.scales_empty[slot]);
             }
-            mma_commit(&bar.empty[s]);
-            if ((kb & 1) || kb == blocks - 1) mma_commit(&bar.scales_empty[slot]);
+            __syncwarp();
         }
-        mma_commit(&bar.sums);
+        if (elected()) mma_commit(&bar.sums);
+        __syncwarp();
     } else if (warp >= 4) {
         // This warp's 32 rows, and the tokens whose scales it brings: eight lanes stand for one token.
         const int q = warp & 3;

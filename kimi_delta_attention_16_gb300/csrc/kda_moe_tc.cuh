@@ -65,7 +65,7 @@ struct StayArgs {
 template <int N, int T, bool Mx, typename Put>
 __device__ __forceinline__ void stay(uint8_t* smem, StayBarriers& bar, const Maps& maps, const StayArgs& a, int* d_status, Put put) {
     using S = Stay<N, T, Mx>;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     uint8_t* ring = smem;
     float* red = reinterpret_cast<float*>(smem + S::ring + S::scales);
     uint16_t* which = reinterpret_cast<uint16_t*>(smem + S::ring + S::scales + S::red);
@@ -150,40 +150,41 @@ __device__ __forceinline__ void stay(uint8_t* smem, StayBarriers& bar, const Map
             }
             return true;
         });
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
+        const uint64_t rows = desc_sw128(base, 16, 1024), columns = desc_sw128(base + kTileA, 16, 1024);
         walk([&](uint32_t p, int, int, int, int) {
             bool ok = true;
             uint32_t d = 0, turn = p * chunks;
             for (int kb = 0; kb < blocks && ok; ++kb) {
-                const uint32_t i = p * blocks + kb, s = i % S::stages, at = base + s * S::stage;
+                const uint32_t i = p * blocks + kb, s = i % S::stages, at = s * (S::stage >> 4);
                 const int in_chunk = Mx ? kb : kb % S::chunk;
                 if (in_chunk == 0) {
-                    ok = mbar_wait(&bar.free[turn % S::accs], ((turn / S::accs) & 1u) ^ 1u);
+                    ok = warp_wait(&bar.free[turn % S::accs], ((turn / S::accs) & 1u) ^ 1u);
                     d = tm + turn % S::accs * S::acc;
                 }
-                ok = ok && mbar_wait(&bar.full[s], (i / S::stages) & 1u);
-                if constexpr (Mx) {
-                    const uint32_t gi = p * groups + kb / 2, slot = gi % kSlots, sf = tm + S::scales_at + slot * S::group;
-                    if (ok && (kb & 1) == 0) ok = mbar_wait(&bar.scales_full[slot], (gi / kSlots) & 1u);
-                    if (!ok) break;
-                    fence_after_sync();
+                ok = ok && warp_wait(&bar.full[s], (i / S::stages) & 1u);
+                const uint32_t gi = p * groups + kb / 2, slot = gi % kSlots, sf = tm + S::scales_at + slot * S::group;
+                if (Mx && ok && (kb & 1) == 0) ok = warp_wait(&bar.scales_full[slot], (gi / kSlots) & 1u);
+                if (ok) fence_after_sync();
+                if (elected()) {
+                    if (ok) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const int set = 2 * (kb & 1) + (kk >> 1);
-                        mma_mxf4(d, desc_sw128(at + kk * 32, 16, 1024), desc_sw128(at + kTileA + kk * 32, 16, 1024), idesc_mxf4(N, 2 * (kk & 1)),
-                                 sf + 4 * set, sf + 16 + S::set * set, (kb | kk) != 0);
+                        for (int kk = 0; kk < 4; ++kk) {
+                            if constexpr (Mx) {
+                                const int set = 2 * (kb & 1) + (kk >> 1);  // of 128 elements
+                                mma_mxf4(d, rows + at + 2 * kk, columns + at + 2 * kk, idesc_mxf4(N, 2 * (kk & 1)), sf + 4 * set,
+                                         sf + 16 + S::set * set, (kb | kk) != 0);
+                            } else {
+                                mma_ss(d, rows + at + 2 * kk, columns + at + 2 * kk, idesc_bf16(128, N, false, false), (in_chunk | kk) != 0);
+                            }
+                        }
+                        mma_commit(&bar.empty[s]);
+                        if (Mx && ((kb & 1) || kb == blocks - 1)) mma_commit(&bar.scales_empty[slot]);
                     }
-                    mma_commit(&bar.empty[s]);
-                    if ((kb & 1) || kb == blocks - 1) mma_commit(&bar.scales_empty[slot]);
-                } else {
-                    if (!ok) break;
-                    fence_after_sync();
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ss(d, desc_sw128(at + kk * 32, 16, 1024), desc_sw128(at + kTileA + kk * 32, 16, 1024), idesc_bf16(128, N, false, false), (in_chunk | kk) != 0);
-                    mma_commit(&bar.empty[s]);
+                    if (in_chunk == S::chunk - 1 || kb == blocks - 1) mma_commit(&bar.sums[turn % S::accs]);
                 }
-                if (in_chunk == S::chunk - 1 || kb == blocks - 1) mma_commit(&bar.sums[turn++ % S::accs]);
+                __syncwarp();
+                if (in_chunk == S::chunk - 1 || kb == blocks - 1) ++turn;
             }
             if (!ok) bar.failed = 1;
             return ok;
