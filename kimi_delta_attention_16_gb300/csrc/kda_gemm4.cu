@@ -5,14 +5,13 @@
 // cores (kda_few_tc.cuh): a CTA takes 128 of the N outputs for some tokens, a cluster splits K.  Integer codes go
 // through registers (kda_few.cuh).
 //
-// On the GPU, columns included: e2m1, 12,288 x 7,168: 1 row 11 us (4.2 TB/s), 32 rows 17 us; 7,168 x 12,288, 256 rows 75 us.
-// One row is bound by the chain of two launches, first bytes and join; many by the bytes in flight towards the
-// SMs: a CTA of 32 tokens has 256 columns of digits, 48 KB a stage, four stages fill shared memory, and a stage
-// takes 0.40 us where its products take 0.29.  Integer codes, 160,000 x 7,168, 16 rows 183 us (3.2 TB/s): latency
+// On the GPU, columns included: e2m1, 12,288 x 7,168: 1 row 11 us (4.2 TB/s), 32 rows 17 us; 256 rows (kda_widen_tc.cuh) 53 us.
+// One row is bound by the chain of two launches, first bytes and join.  Integer codes, 160,000 x 7,168, 16 rows 183 us (3.2 TB/s): latency
 // of three warps per scheduler (issue 45 %, tensor pipe 32 %, HBM 37 %).
 #include "kda_few.cuh"
 #include "kda_few_tc.cuh"
 #include "kda_serve.cuh"
+#include "kda_widen_tc.cuh"
 
 namespace kda {
 
@@ -107,6 +106,41 @@ struct Gemm4Tc {
     int* d_status;
 };
 
+// The part of a tile's joined sums that this rank writes: tokens [c0, c0 + n).  What came out as NaN (Inf: or infinite) is
+// computed again from the operands as they were given.
+template <int Threads, bool Inf, typename Tout>
+__device__ __forceinline__ void put_tile(const Gemm4Tc& p, const float* red, int rank, int row0, int c0, int n, Tout* __restrict__ out) {
+    int r0, r1;
+    fewtc::rows_of(rank, p.ranks, r0, r1);
+    const int share = (r1 - r0) / 4;
+    for (int i = threadIdx.x; i < n * share; i += Threads) {
+        const int c = i / share, r = r0 + i % share * 4, left = p.N - row0 - r;
+        if (left <= 0) continue;
+        const float4 q = fewtc::joined4(red, p.ranks, c, r);
+        float v[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t row = row0 + r + j;
+            if ((Inf ? !isfinite(v[j]) : isnan(v[j])) && j < left)
+                v[j] = fewtc::direct(p.codes + row * (p.K / 2), p.w_scales + row * (p.K / 32), p.a + (int64_t)(c0 + c) * p.lda, p.K);
+            v[j] = apply(p.epi, v[j]);
+        }
+        Tout* o = out + (int64_t)(c0 + c) * p.ldc + row0 + r;
+        if (left >= 4 && reinterpret_cast<uintptr_t>(o) % (4 * sizeof(Tout)) == 0) {
+            if constexpr (sizeof(Tout) == 4) {
+                *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+            } else {
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+                *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < left) o[j] = from_f<Tout>(v[j]);
+        }
+    }
+}
+
 template <int N, typename Tout>
 __global__ void __launch_bounds__(fewtc::kThreads, fewtc::Shape<N>::per_sm) k_gemm4_tc(const __grid_constant__ fewtc::Maps maps, const Gemm4Tc p,
                                                                                       Tout* __restrict__ out) {
@@ -127,35 +161,7 @@ __global__ void __launch_bounds__(fewtc::kThreads, fewtc::Shape<N>::per_sm) k_ge
     float* red = reinterpret_cast<float*>(smem);
     fewtc::product<N>(smem, bar, t, count, red);
     if (p.ranks > 1) cooperative_groups::this_cluster().sync();
-    int r0, r1;
-    fewtc::rows_of(rank, p.ranks, r0, r1);
-    const int share = (r1 - r0) / 4;
-    for (int i = threadIdx.x; i < n * share; i += fewtc::kThreads) {
-        const int c = i / share, r = r0 + i % share * 4, left = p.N - row0 - r;
-        if (left <= 0) continue;
-        const float4 q = fewtc::joined4(red, p.ranks, c, r);
-        float v[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t row = row0 + r + j;
-            if (isnan(v[j]) && j < left)
-                v[j] = fewtc::direct(p.codes + row * (p.K / 2), p.w_scales + row * (p.K / 32), p.a + (int64_t)(c0 + c) * p.lda, p.K);
-            v[j] = apply(p.epi, v[j]);
-        }
-        Tout* o = out + (int64_t)(c0 + c) * p.ldc + row0 + r;
-        if (left >= 4 && reinterpret_cast<uintptr_t>(o) % (4 * sizeof(Tout)) == 0) {
-            if constexpr (sizeof(Tout) == 4) {
-                *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
-            } else {
-                const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
-                *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j < left) o[j] = from_f<Tout>(v[j]);
-        }
-    }
+    put_tile<fewtc::kThreads, false>(p, red, rank, row0, c0, n, out);
     if (p.ranks > 1) cooperative_groups::this_cluster().sync(); else __syncthreads();
     fewtc::finish<N>(bar, p.d_status);
 }
@@ -178,6 +184,69 @@ template <int N, typename Tout> cudaError_t launch_tc(const kda_gemm4_args& a, c
                          static_cast<Tout*>(a.C));
 }
 
+// ------------------------------------------------------------------ many rows
+// 12,288 x 7,168: 256 rows 53 us, of which 7 the start and end of a CTA; 7,168 x 12,288 49.  A stage of 64 elements takes some 650
+// cycles whatever the columns up to 128, 256 columns' products alone 512: the issuing warp shares its scheduler with four
+// that widen, and waits for two barriers, issues and commits once per stage.
+template <int N>
+__global__ void __launch_bounds__(widetc::kThreads, 1) k_gemm4_widen(const __grid_constant__ fewtc::Maps maps, const Gemm4Tc p, bf16* __restrict__ out) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ widetc::Barriers bar;
+    const uint32_t raw = tc::smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    const int rank = blockIdx.x % p.ranks, row0 = blockIdx.x / p.ranks * kTileRows, c0 = blockIdx.y * N;
+    widetc::start<N>(bar);
+    widetc::Tile t;
+    t.w = &maps.w, t.x = &maps.b;
+    t.row0 = row0, t.c0 = c0, t.scales = p.w_scales, t.last_row = p.N - 1, t.K = p.K;
+    fewtc::slice_of(p.K, rank, p.ranks, t.k0, t.k1);
+    float* red = reinterpret_cast<float*>(smem);
+    widetc::product<N>(smem, bar, t, red);
+    if (p.ranks > 1) cooperative_groups::this_cluster().sync();
+    put_tile<widetc::kThreads, true>(p, red, rank, row0, c0, min(N, p.M - c0), out);
+    if (p.ranks > 1) cooperative_groups::this_cluster().sync(); else __syncthreads();
+    widetc::finish<N>(bar, p.d_status);
+}
+
+// The rows of A packed, eight elements in the order in which codes come out of a word.
+__global__ void __launch_bounds__(256) k_widen_rows(const bf16* __restrict__ x, int64_t xs, bool wide, int K, uint4* __restrict__ rows) {
+    let_next_kernel_begin();
+    const int k = (blockIdx.x * 256 + threadIdx.x) * 8;  // K is a multiple of 32
+    if (k >= K) return;
+    const bf16* row = x + (int64_t)blockIdx.y * xs + k;
+    uint32_t v[4];
+    if (wide) {
+        const uint4 q = *reinterpret_cast<const uint4*>(row);
+        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+    } else {
+        const unsigned short* h = reinterpret_cast<const unsigned short*>(row);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
+    }
+    rows[((int64_t)blockIdx.y * K + k) / 8] = make_uint4(__byte_perm(v[0], v[2], 0x5410), __byte_perm(v[0], v[2], 0x7632),
+                                                         __byte_perm(v[1], v[3], 0x5410), __byte_perm(v[1], v[3], 0x7632));
+}
+
+template <int N> cudaError_t launch_widen(const kda_gemm4_args& a, cudaStream_t s) {
+    using S = widetc::Shape<N>;
+    const bf16* x = static_cast<const bf16*>(a.A);
+    const bool wide = reinterpret_cast<uintptr_t>(x) % 16 == 0 && a.lda % 8 == 0;
+    if (const cudaError_t e = launch_kernel(k_widen_rows, dim3((a.K + 2047) / 2048, a.M), 256, 1, 0, false, s, x, a.lda, wide, a.K,
+                                            static_cast<uint4*>(a.workspace)))
+        return e;
+    fewtc::Maps maps;
+    if (!encode_tensor_map_2d_as(&maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, a.K / 2, a.N, a.K / 2, widetc::kCodesK / 2, kTileRows, true) ||
+        !encode_tensor_map_2d_as(&maps.b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.workspace, a.K, a.M, 2 * (uint64_t)a.K, widetc::kSubK, N, true))
+        return cudaErrorInvalidValue;
+    Gemm4Tc p;
+    const int tiles = (a.N + kTileRows - 1) / kTileRows, blocks = (a.M + N - 1) / N;
+    p.M = a.M, p.N = a.N, p.K = a.K, p.epi = a.epilogue;
+    p.ranks = fewtc::cluster_ranks((int64_t)tiles * blocks, a.K, 1, 10);
+    p.w_scales = static_cast<const uint8_t*>(a.scales), p.b_scales = nullptr, p.codes = a.codes;
+    p.a = static_cast<const bf16*>(a.A), p.lda = a.lda, p.ldc = a.ldc, p.d_status = a.d_status;
+    return launch_kernel(k_gemm4_widen<N>, dim3(tiles * p.ranks, blocks), widetc::kThreads, p.ranks, S::smem, true, s, maps, p, static_cast<bf16*>(a.C));
+}
+
 template <int N> cudaError_t launch_tc_out(const kda_gemm4_args& a, cudaStream_t s) {
     return a.c_dtype == KDA_BF16 ? launch_tc<N, bf16>(a, s) : launch_tc<N, float>(a, s);
 }
@@ -190,6 +259,9 @@ size_t gemm4_workspace(const kda_gemm4_args& a) {
 
 cudaError_t launch_gemm4(const kda_gemm4_args& a, cudaStream_t s) {
     if (a.format == KDA_WEIGHT_E2M1) {
+        // From 97 rows on widened weights, where C is bf16.  12,288 x 7,168, digits against widened: 64 rows 35 and 43 us, 128 rows
+        // 48 and 46, 256 rows 92 and 53, 512 rows 174 and 96; 7,168 x 12,288: 27 and 39, 50 and 42, 72 and 49, 148 and 83.
+        if (a.c_dtype == KDA_BF16 && a.M > 96) return a.M <= 128 ? launch_widen<128>(a, s) : launch_widen<256>(a, s);
         // as few columns as hold all rows, and at most 32 rows' (256 rows: 82 us, 91 with 16 rows per CTA, 146 with 8)
         if (a.M <= 2) return launch_tc_out<16>(a, s);
         if (a.M <= 4) return launch_tc_out<32>(a, s);

@@ -169,6 +169,76 @@ def test_gemm4_offsets_past_32_bits(fmt, sdt):
     within(got[:, -200:], ref, err + U[F32] * ref.abs())
 
 
+# More than 96 rows of e2m1 with a bf16 result go another way (weights widened to bf16).
+@pytest.mark.parametrize("M,N,K", [(96, 70, 288), (97, 1, 32), (97, 128, 64), (100, 129, 96), (113, 300, 256), (127, 64, 288), (128, 257, 1056),
+                                   (128, 130, 512), (130, 96, 2080), (129, 200, 4128), (256, 40, 1280), (300, 384, 992), (513, 64, 160)])
+@pytest.mark.parametrize("epilogue", ["none", "sigmoid"])
+def test_gemm4_many_rows(M, N, K, epilogue):
+    check_gemm4(M, N, K, "e2m1", 32, None, epilogue, out_dtype=BF16)
+
+
+def test_gemm4_many_rows_exact():
+    """Whole numbers whose products and sums fp32 holds, and a bf16 result too: every code, scale by scale, in its place."""
+    M, N, K = 140, 200, 320
+    g = gen(3)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8)
+    scales = torch.randint(120, 136, (N, K // 32), generator=g, dtype=torch.uint8)
+    x = torch.zeros(M, K)
+    at = torch.randint(0, K, (M,), generator=g)
+    x[torch.arange(M), at] = 2.0 ** torch.randint(-3, 4, (M,), generator=g)
+    got = kda.kda_gemm4(x.to(BF16).cuda(), codes.cuda(), scales.cuda())
+    assert torch.equal(f64(got), x.double() @ lib.unpack_ref(codes, scales).T)
+
+
+@pytest.mark.parametrize("byte", [1, 2, 64, 128, 129, 200, 250, 253])
+def test_gemm4_many_rows_scales(byte):
+    """Scales from one end to the other, rows of x that bring the results back to where bf16 has them."""
+    M, N, K = 99, 65, 256
+    g = gen(byte)
+    codes, _ = lib.random_weight(g, N, K, fmt="e2m1", group=32)
+    scales = torch.full((N, K // 32), byte, dtype=torch.uint8)
+    scales[::3] = max(byte - 1, 1)
+    x = (randn(g, M, K, dtype=F32) * 2.0 ** min(max(127 - byte, -100), 100)).to(BF16)
+    got = kda.kda_gemm4(x.cuda(), codes.cuda(), scales.cuda())
+    ref, err = lib.gemm4_ref(x, lib.unpack_ref(codes, scales), "none")
+    # what lies below 2^-126 in a product or a sum may be dropped
+    within(got, ref, err + U[BF16] * (ref.abs() + err) + K * 2.0 ** -126, f"byte {byte}")
+
+
+def test_gemm4_many_rows_strides_and_values():
+    M, N, K = 130, 140, 416
+    g = gen(9)
+    x = randn(g, M, K, dtype=BF16)
+    codes, scales = lib.random_weight(g, N, K, fmt="e2m1", group=32)
+    c, s = codes.cuda(), scales.cuda()
+    plain = kda.kda_gemm4(x.cuda(), c, s)
+    for offset, pitch in ((0, K + 8), (8, K + 24), (1, K + 8), (0, K + 1), (3, K + 5)):
+        big = torch.full((M, pitch + offset), float("nan"), dtype=BF16, device="cuda")
+        view = big[:, offset:offset + K]
+        view.copy_(x)
+        out = torch.full((M + 1, N + 3), 7.0, dtype=BF16, device="cuda")
+        kda.kda_gemm4(view, c, s, out=out[:M, 1:N + 1])
+        assert torch.equal(out[:M, 1:N + 1], plain)
+        assert bool((out[M] == 7).all() and (out[:, 0] == 7).all() and (out[:, N + 1:] == 7).all())
+    # a row that is not finite gives what the formula gives and leaves the others alone
+    y = x.clone()
+    y[5, 17], y[9, 2], y[9, 40], y[66, 0] = float("inf"), float("inf"), float("-inf"), float("nan")
+    got = kda.kda_gemm4(y.cuda(), c, s)
+    w = lib.unpack_ref(codes, scales)
+    keep = [i for i in range(M) if i not in (5, 9, 66)]
+    assert torch.equal(got[keep], plain[keep])
+    ref = f64(y[[5, 9, 66]]) @ w.T
+    have = f64(got[[5, 9, 66]])
+    assert torch.equal(torch.isnan(have), torch.isnan(ref)) and torch.equal(torch.isinf(have), torch.isinf(ref))
+    assert torch.equal(have[torch.isinf(ref)], ref[torch.isinf(ref)])
+    assert torch.equal(kda.kda_gemm4(x.cuda(), c, s), plain)
+
+
+@pytest.mark.parametrize("M,N,K", [(100, 128, 7168), (128, 256, 7168), (256, 7168, 512), (1000, 140, 2048)])
+def test_gemm4_many_rows_split_and_wide(M, N, K):
+    check_gemm4(M, N, K, "e2m1", 32, None, out_dtype=BF16)
+
+
 def close_in_norm(got, ref, units):
     """The error of all outputs together, in units of 2^-24 of theirs: roundings are independent, so those of one kind come to
     one unit at most however many outputs there are, while a systematic loss of bits stands out."""
