@@ -701,12 +701,13 @@ kda_status kda_pack4(const kda_pack4_args* args, kda_stream_t stream);
 kda_status kda_unpack4(const kda_pack4_args* args, kda_stream_t stream);
 
 /* kda_gemm4 -- kda_gemm for weights in 4 bits: C[M][N] = epilogue(A[M][K] . W[N][K]^T), for
- * the few rows of a decode step (M up to 65,535; the weights are read once per 32 rows).
+ * the few rows of a decode step (M up to 65,535; the weights are read once per 32 rows, 256 of e2m1 with a bf16 C).
  * A [M][lda] bf16 (any alignment of its elements; 16-byte rows are read faster), C [M][ldc] bf16
  * or fp32, rounded once; epilogues as in kda_gemm; M, N >= 0; C must not overlap an input.
  * Values of A enter the products exactly but for what lies below 2^-22 of the largest of their 32 (e2m1) or 2^-39 of
- * the largest of their 128 (int4); sums are fp32, in a fixed order.  A row of A with values that are not finite gives what
- * the formula gives, slowly.  Needs an sm_103 device.  A wait that times out on the device is reported through
+ * the largest of their 128 (int4); sums are fp32, in a fixed order that depends on M, N and K (e2m1, more than 96 rows and a
+ * bf16 C: values exact, sums cut off instead of rounded, 6e-6 over 2,048 elements).  A row of A with values that are
+ * not finite gives what the formula gives, slowly.  Needs an sm_103 device.  A wait that times out on the device is reported through
  * d_status (KDA_ERR_TIMEOUT). */
 typedef struct {
     int M, N, K;
