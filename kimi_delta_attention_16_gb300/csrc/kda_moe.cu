@@ -54,7 +54,7 @@ template <typename T> __device__ __forceinline__ void load8_any(const T* p, bool
 template <typename Tr, int TB>
 __global__ void __launch_bounds__(kScoreThreads) k_moe_scores(const bf16* __restrict__ x, int64_t xs, bool xwide, const Tr* __restrict__ router,
                                                               bool rwide, const float* __restrict__ bias, int M, int E, int D,
-                                                              int sigmoid, Wide* __restrict__ score, uint64_t* __restrict__ key,
+                                                              int sigmoid, Wide* __restrict__ logits, uint64_t* __restrict__ key,
                                                               int* __restrict__ done) {
     __shared__ Wide sums[kScoreWarps][TB];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kScoreThreads) k_moe_scores(const bf16* __rest
         const int64_t at = (int64_t)(t0 + j) * E + e;
         const Wide logit = v;
         if (sigmoid) v = sigmoid_wide(v);
-        score[at] = v;
+        logits[at] = logit;
         // scores next to 1 are equal where fp64 holds them equal; small ones without a bias are ordered by their logits
         // (negative, so below every other score), which do not underflow
         key[at] = ordered(!sigmoid ? logit : bias ? to_53_bits(add(v, Wide{bias[e], 0.f})) : logit.hi < 0.f ? logit : to_53_bits(v));
@@ -120,7 +120,7 @@ __device__ __forceinline__ int largest(uint64_t key, int index, uint64_t& top) {
 // A block per token: each warp orders the best `top` of its 64 experts, one warp merges the sixteen lists.  The block
 // that finishes last lists the slots (token, rank) by expert; the order of an expert's slots is free, since every
 // column of a product is computed alike.
-__global__ void __launch_bounds__(kPickThreads) k_moe_pick(const Wide* __restrict__ score, const uint64_t* __restrict__ key, int M, int E, int top,
+__global__ void __launch_bounds__(kPickThreads) k_moe_pick(const Wide* __restrict__ logits, const uint64_t* __restrict__ key, int M, int E, int top,
                                                            int sigmoid, float scale, int* __restrict__ ids, float* __restrict__ weights,
                                                            int* __restrict__ done, int* __restrict__ lists, int* __restrict__ user_ids,
                                                            float* __restrict__ user_weights) {
@@ -173,11 +173,21 @@ __global__ void __launch_bounds__(kPickThreads) k_moe_pick(const Wide* __restric
                 id = best_id[lane][head];
             }
         }
+        // Weights are quotients: every score times e^-m is as good, and does not underflow with m the largest logit, or 0
+        // for sigmoids where that is positive.
         Wide w;
-        if (lane < top) w = score[(int64_t)t * E + mine];
-        if (!sigmoid) {
-            const Wide first = from(0xffffffffu, w, 0);  // the largest logit
-            if (lane < top) w = exp_wide(add(w, minus(first)));
+        if (lane < top) w = logits[(int64_t)t * E + mine];
+        float m = lane < top ? w.hi : -INFINITY;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));  // leaves NaN out
+        const Wide first = from(0xffffffffu, w, 0);  // the largest logit itself, for the softmax
+        if (lane < top) {
+            if (!sigmoid)
+                w = exp_wide(add(w, minus(first)));
+            else if (w.hi > 0.f)
+                w = sigmoid_wide(w);
+            else if (!isnan(w.hi))
+                w = over(exp_wide(add(w, Wide{-fminf(m, 0.f), 0.f})), add(Wide{1.f, 0.f}, exp_wide(w)));
         }
         Wide sum = w;
 #pragma unroll
@@ -473,7 +483,7 @@ __global__ void __launch_bounds__(256) k_moe_sum(const float* __restrict__ parts
 }
 
 // ------------------------------------------------------------------ launches
-template <typename Tr> cudaError_t launch_scores(const kda_moe_args& a, int64_t xs, bool xwide, Wide* score, uint64_t* key, int* done, bool beside,
+template <typename Tr> cudaError_t launch_scores(const kda_moe_args& a, int64_t xs, bool xwide, Wide* logits, uint64_t* key, int* done, bool beside,
                                                cudaStream_t s) {
     const bf16* x = static_cast<const bf16*>(a.x);
     const Tr* r = static_cast<const Tr*>(a.router);
@@ -481,7 +491,7 @@ template <typename Tr> cudaError_t launch_scores(const kda_moe_args& a, int64_t 
     const int sg = a.score == KDA_SCORE_SIGMOID;
     const auto go = [&](auto kernel, int tb) {
         return launch_kernel(kernel, dim3(a.E, (a.M + tb - 1) / tb), kScoreThreads, 1, 0, beside, s, x, xs, xwide, r, rwide, a.bias, a.M,
-                             a.E, a.D, sg, score, key, done);
+                             a.E, a.D, sg, logits, key, done);
     };
     return a.M == 1 ? go(k_moe_scores<Tr, 1>, 1) : go(k_moe_scores<Tr, 4>, 4);
 }
@@ -590,7 +600,7 @@ MoePlan moe_plan(const kda_moe_args& a) {
         at = (at + bytes + 255) / 256 * 256;
         return here;
     };
-    p.score = take((size_t)a.M * a.E * 8);
+    p.logits = take((size_t)a.M * a.E * 8);
     p.key = take((size_t)a.M * a.E * 8);
     p.done = take(4);
     p.ids = take(slots * 4);
@@ -606,7 +616,7 @@ MoePlan moe_plan(const kda_moe_args& a) {
 
 cudaError_t launch_moe(const kda_moe_args& a, const MoePlan& p, cudaStream_t s) {
     char* ws = static_cast<char*>(a.workspace);
-    Wide* score = reinterpret_cast<Wide*>(ws + p.score);
+    Wide* logits = reinterpret_cast<Wide*>(ws + p.logits);
     uint64_t* key = reinterpret_cast<uint64_t*>(ws + p.key);
     int* ids = reinterpret_cast<int*>(ws + p.ids);
     float* weights = reinterpret_cast<float*>(ws + p.weights);
@@ -626,10 +636,10 @@ cudaError_t launch_moe(const kda_moe_args& a, const MoePlan& p, cudaStream_t s) 
         e = launch_halves(x, xs, xwide, a.M, a.D, a.group, columns_at(ws + p.x_columns, a.M, a.D), s);
         if (e) return e;
     }
-    e = a.router_dtype == KDA_BF16 ? launch_scores<bf16>(a, xs, xwide, score, key, done, !tc, s)
-                                   : launch_scores<float>(a, xs, xwide, score, key, done, !tc, s);
+    e = a.router_dtype == KDA_BF16 ? launch_scores<bf16>(a, xs, xwide, logits, key, done, !tc, s)
+                                   : launch_scores<float>(a, xs, xwide, logits, key, done, !tc, s);
     if (e) return e;
-    if ((e = launch_kernel(k_moe_pick, dim3(a.M), kPickThreads, 1, 0, true, s, score, key, a.M, a.E, a.top, (int)(a.score == KDA_SCORE_SIGMOID),
+    if ((e = launch_kernel(k_moe_pick, dim3(a.M), kPickThreads, 1, 0, true, s, logits, key, a.M, a.E, a.top, (int)(a.score == KDA_SCORE_SIGMOID),
                            a.scale, ids, weights, done, lists, a.ids, a.weights)))
         return e;
     if (mx) {

@@ -13,7 +13,7 @@ cudaError_t launch_gemm4(const kda_gemm4_args& a, cudaStream_t s);
 
 // Parts of kda_moe's workspace, as byte offsets.
 struct MoePlan {
-    size_t score;    // [M][E] pairs of fp32
+    size_t logits;    // [M][E] pairs of fp32
     size_t key;      // [M][E] uint64: what the choice is made by, ordered as integers
     size_t done;     // int: tokens whose choice is made
     size_t ids;      // [M * top] int: experts by token and rank

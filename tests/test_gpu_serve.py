@@ -346,6 +346,19 @@ def test_moe_close_logits_are_told_apart():
     check_moe(3, E, 3, D, 32, x=x, router=router, router_dtype=F32, with_bias=False)
 
 
+@pytest.mark.parametrize("with_bias", [True, False])
+@pytest.mark.parametrize("low", [-30.0, -85.0, -110.0, -600.0, 90.0])
+def test_moe_logits_far_from_zero(low, with_bias):
+    """Scores that vanish, or all but reach 1: the weights are their quotients all the same."""
+    M, E, D = 3, 9, 64
+    x = torch.ones(M, D, dtype=BF16)
+    x[1, 0] = 3.0
+    router = torch.zeros(E, D)
+    router[:, 1] = low - torch.arange(E) * 0.75
+    router[:, 0] = torch.linspace(-0.5, 0.5, E)
+    check_moe(M, E, 4, D, 32, x=x, router=router, router_dtype=F32, with_bias=with_bias)
+
+
 @pytest.mark.parametrize("fmt", ["e2m1", "int4", "bf16"])
 def test_moe_all_tokens_to_one_expert(fmt):
     """More tokens of an expert than one pass holds columns for."""
