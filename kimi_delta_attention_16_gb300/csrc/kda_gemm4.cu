@@ -5,7 +5,7 @@
 // cores (kda_few_tc.cuh): a CTA takes 128 of the N outputs for some tokens, a cluster splits K.  Integer codes go
 // through registers (kda_few.cuh).
 //
-// On the GPU, columns included: e2m1, 12,288 x 7,168: 1 row 11 us (4.2 TB/s), 32 rows 17 us; 256 rows (kda_widen_tc.cuh) 53 us.
+// On the GPU, columns included: e2m1, 12,288 x 7,168: 1 row 11 us (4.2 TB/s), 32 rows 17 us; 256 rows (kda_widen_tc.cuh) 48 us.
 // One row is bound by the chain of two launches, first bytes and join.  Integer codes, 160,000 x 7,168, 16 rows 183 us (3.2 TB/s): latency
 // of three warps per scheduler (issue 45 %, tensor pipe 32 %, HBM 37 %).
 #include "kda_few.cuh"
@@ -185,9 +185,9 @@ template <int N, typename Tout> cudaError_t launch_tc(const kda_gemm4_args& a, c
 }
 
 // ------------------------------------------------------------------ many rows
-// 12,288 x 7,168: 256 rows 53 us (0.86 PFLOP/s), of which 7 the start and the end of a CTA; 7,168 x 12,288 49.  64 elements
-// take some 680 cycles with 128 columns and 780 with 256, whose products alone take 512: the warp that issues them shares its
-// scheduler with four that widen, and waits for two barriers, issues and commits once per 64 elements.
+// 12,288 x 7,168: 256 rows 48 us (0.93 PFLOP/s), of which 7 the start and the end of a CTA; 7,168 x 12,288 48.  128 elements
+// take some 1,270 cycles with 128 columns and 1,430 with 256, whose products alone take 1,024: the warp that issues
+// them shares its scheduler with four that widen.  (Barriers and commits every 64 elements: 53 us, 46 with 128 rows.)
 template <int N>
 __global__ void __launch_bounds__(widetc::kThreads, 1) k_gemm4_widen(const __grid_constant__ fewtc::Maps maps, const Gemm4Tc p, bf16* __restrict__ out) {
     extern __shared__ uint8_t smem_raw[];
@@ -260,7 +260,7 @@ size_t gemm4_workspace(const kda_gemm4_args& a) {
 cudaError_t launch_gemm4(const kda_gemm4_args& a, cudaStream_t s) {
     if (a.format == KDA_WEIGHT_E2M1) {
         // From 97 rows on widened weights, where C is bf16.  12,288 x 7,168, digits against widened: 64 rows 35 and 43 us, 128 rows
-        // 48 and 46, 256 rows 92 and 53, 512 rows 174 and 96; 7,168 x 12,288: 27 and 39, 50 and 42, 72 and 49, 148 and 83.
+        // 48 and 44, 256 rows 92 and 49, 512 rows 174 and 89; 7,168 x 12,288: 25 and 39, 50 and 42, 72 and 48, 148 and 79.
         if (a.c_dtype == KDA_BF16 && a.M > 96) return a.M <= 128 ? launch_widen<128>(a, s) : launch_widen<256>(a, s);
         // as few columns as hold all rows, and at most 32 rows' (256 rows: 82 us, 91 with 16 rows per CTA, 146 with 8)
         if (a.M <= 2) return launch_tc_out<16>(a, s);

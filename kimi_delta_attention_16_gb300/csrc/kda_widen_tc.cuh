@@ -5,9 +5,9 @@
 // every CTA moves into shared memory and reads from there again, 2 here.  Weights are the operand in tensor
 // memory, so that shared memory holds and passes on their codes only, half a byte each.
 //
-// Warps of a CTA: 0 and 3 feed two rings by TMA, 64 elements of N columns and codes of 256 elements of 128 rows (a swizzled tile
+// Warps of a CTA: 0 and 3 feed two rings by TMA, 128 elements of N columns and codes of 256 elements of 128 rows (a swizzled tile
 // of 128-byte rows each); 1 issues the products; 4 to 19 widen codes, four warps 64 of every 256 elements, a thread a row (its
-// lane of tensor memory), into a ring of eight places of 64 elements, and carry the sums out at the end.
+// lane of tensor memory), into a ring of four places of 128 elements, and carry the sums out at the end.
 //
 // Widening: three bits of a code, put at bits 6 to 8 of a bf16, are its value times 2^-126 (e2m1's subnormals are bf16's
 // there), so one product with 2^(byte - 1) ends it; bytes above 128 need a second.
@@ -27,18 +27,18 @@ using fewtc::arrive;
 using fewtc::tma_2d;
 
 constexpr int kThreads = 640;
-constexpr int kSubK = 64, kCodesK = 256, kPlaces = 8;
+constexpr int kSubK = 64, kRoundK = 128, kCodesK = 256, kPlaces = 4;
 constexpr uint32_t kCodes = few::kTileRows * (kCodesK / 2);
 
 template <int N> struct Shape {
-    static constexpr uint32_t sub = N * kSubK * 2;               // bytes of 64 elements of the columns
-    static constexpr int codes = N == 256 ? 3 : 5, subs = N == 256 ? 5 : 8;
+    static constexpr uint32_t sub = N * kSubK * 2, round = 2 * sub;  // bytes of 64 and 128 elements of the columns
+    static constexpr int codes = N == 256 ? 2 : 4, rounds = N == 256 ? 3 : 5;
     static constexpr int places_at = N, tmem = 512;
-    static constexpr uint32_t ring = codes * kCodes + subs * sub;
+    static constexpr uint32_t ring = codes * kCodes + rounds * round;
     static constexpr uint32_t red = N * few::kRedPitch * 4;      // the sums lie over the rings
-    static_assert(codes <= 8 && subs <= kPlaces, "barriers; a product frees its place and its columns at once");
+    static_assert(codes <= 8 && rounds <= 8, "barriers");
     static_assert(red <= ring, "the sums fit over the rings");
-    static_assert(places_at + kPlaces * kSubK / 2 <= tmem, "accumulator and widened weights");
+    static_assert(places_at + kPlaces * kRoundK / 2 <= tmem, "accumulator and widened weights");
     static constexpr uint32_t smem = ring + 1024;
     // CTAs of a cluster wait for one another and for tensor memory.  They hold all of it here, so none that waits in the
     // same way (kda_few_tc.cuh: 90 KB at least) may fit beside them on an SM.
@@ -46,7 +46,7 @@ template <int N> struct Shape {
 };
 
 struct Barriers {
-    uint64_t codes_full[8], codes_empty[8], full[8], place_full[kPlaces], place_empty[kPlaces], sums;
+    uint64_t codes_full[8], codes_empty[8], full[8], empty[8], place_full[kPlaces], place_empty[kPlaces], sums;
     uint32_t tmem;
     int failed;
 };
@@ -62,7 +62,10 @@ template <int N> __device__ __forceinline__ void start(Barriers& bar) {
             mbar_init(&bar.codes_full[s], 1);
             mbar_init(&bar.codes_empty[s], 16);
             mbar_init(&bar.full[s], 1);
-            mbar_init(&bar.place_full[s], 4);
+            mbar_init(&bar.empty[s], 1);
+        }
+        for (int s = 0; s < kPlaces; ++s) {
+            mbar_init(&bar.place_full[s], 8);
             mbar_init(&bar.place_empty[s], 1);
         }
         mbar_init(&bar.sums, 1);
@@ -120,33 +123,37 @@ struct Tile {
 template <int N> __device__ __forceinline__ void product(uint8_t* ring, Barriers& bar, const Tile& t, float* red) {
     using S = Shape<N>;
     const int warp = fewtc::warp_index(), lane = threadIdx.x & 31;
-    const int subs = (t.k1 - t.k0 + kSubK - 1) / kSubK, blocks = (subs + 3) / 4;
+    const int subs = (t.k1 - t.k0 + kSubK - 1) / kSubK, rounds = (subs + 1) / 2, blocks = (subs + 3) / 4;
     const uint32_t base = smem_u32(ring), cols = base + S::codes * kCodes, tm = bar.tmem;
     if ((warp == 0 || warp == 3) && lane == 0) {
         // columns and codes, each as far ahead as its own ring goes; codes need not wait for the kernel that writes the columns
         const bool codes = warp == 3;
         if (!codes) few::wait_for_kernel_before();
-        uint64_t* full = codes ? bar.codes_full : bar.full;
-        const int stages = codes ? S::codes : S::subs, last = codes ? blocks : subs;
+        uint64_t *full = codes ? bar.codes_full : bar.full, *empty = codes ? bar.codes_empty : bar.empty;
+        const int stages = codes ? S::codes : S::rounds, last = codes ? blocks : rounds;
         for (int i = 0; i < last; ++i) {
-            const int s = i % stages, j = i - stages;  // j: what was there before
-            if (j >= 0 && !mbar_wait(codes ? &bar.codes_empty[s] : &bar.place_empty[j % kPlaces], (codes ? j / stages : j / kPlaces) & 1u)) {
+            const int s = i % stages;
+            if (!mbar_wait(&empty[s], ((i / stages) & 1u) ^ 1u)) {
                 bar.failed = 1;
                 // copies still in flight: wait for them before the shared memory is used for anything else
                 for (int j = max(i - stages, 0); j < i; ++j) mbar_wait(&full[j % stages], (j / stages) & 1u);
                 break;
             }
-            mbar_expect_tx(&full[s], codes ? kCodes : S::sub);
-            if (codes)
+            if (codes) {
+                mbar_expect_tx(&full[s], kCodes);
                 tma_2d(base + s * kCodes, t.w, (t.k0 + i * kCodesK) / 2, t.row0, &full[s]);
-            else
-                tma_2d(cols + s * S::sub, t.x, t.k0 + i * kSubK, t.c0, &full[s]);
+            } else {
+                const bool both = 2 * i + 1 < subs;
+                mbar_expect_tx(&full[s], both ? S::round : S::sub);
+                tma_2d(cols + s * S::round, t.x, t.k0 + i * kRoundK, t.c0, &full[s]);
+                if (both) tma_2d(cols + s * S::round + S::sub, t.x, t.k0 + i * kRoundK + kSubK, t.c0, &full[s]);
+            }
         }
     } else if (warp == 1) {
         const uint64_t first = desc_sw128(cols, 16, 1024);
         int s = 0;
         uint32_t phase = 0;
-        for (int i = 0; i < subs; ++i) {
+        for (int i = 0; i < rounds; ++i) {
             const int place = i % kPlaces;
             if (!fewtc::warp_wait(&bar.full[s], phase) || !fewtc::warp_wait(&bar.place_full[place], (i / kPlaces) & 1u)) {
                 bar.failed = 1;
@@ -154,15 +161,18 @@ template <int N> __device__ __forceinline__ void product(uint8_t* ring, Barriers
             }
             fence_after_sync();
             if (fewtc::elected()) {
-                const uint64_t b = first + s * (S::sub >> 4);
-                const uint32_t a = tm + S::places_at + place * (kSubK / 2);
+                const uint64_t b = first + s * (S::round >> 4);
+                const uint32_t a = tm + S::places_at + place * (kRoundK / 2);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) mma_ts(tm, a + 8 * kk, b + 2 * kk, idesc_bf16(128, N, false, false), (i | kk) != 0);
-                mma_commit(&bar.place_empty[place]);  // and the columns' place in their ring
-                if (i == subs - 1) mma_commit(&bar.sums);
+                for (int kk = 0; kk < 8; ++kk)
+                    if (kk < 4 || 2 * i + 1 < subs)
+                        mma_ts(tm, a + 8 * kk, b + (kk >> 2) * (S::sub >> 4) + 2 * (kk & 3), idesc_bf16(128, N, false, false), (i | kk) != 0);
+                mma_commit(&bar.empty[s]);
+                mma_commit(&bar.place_empty[place]);
+                if (i == rounds - 1) mma_commit(&bar.sums);
             }
             __syncwarp();
-            if (++s == S::subs) s = 0, phase ^= 1u;
+            if (++s == S::rounds) s = 0, phase ^= 1u;
         }
     } else if (warp >= 4) {
         const int q = warp & 3, set = (warp - 4) >> 2, r = 32 * q + lane;
@@ -180,7 +190,7 @@ template <int N> __device__ __forceinline__ void product(uint8_t* ring, Barriers
             const uint32_t two = ahead[0];
             ahead[0] = ahead[1];
             ahead[1] = load_scales(g + 2);
-            const int s = g % S::codes, i = 4 * g + set, place = i % kPlaces;
+            const int s = g % S::codes, i = 4 * g + set, round = i >> 1, place = round % kPlaces;
             if (lane == 0) ok = mbar_wait(&bar.codes_full[s], (g / S::codes) & 1u);
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
             if (!ok) break;
@@ -194,16 +204,18 @@ template <int N> __device__ __forceinline__ void product(uint8_t* ring, Barriers
             widen(b, eb, large, vb);
             __syncwarp();
             if (lane == 0) arrive(&bar.codes_empty[s]);
-            if (i >= subs) continue;
-            if (lane == 0) ok = mbar_wait(&bar.place_empty[place], ((i / kPlaces) & 1u) ^ 1u);
+            if (round >= rounds) continue;
+            if (lane == 0) ok = mbar_wait(&bar.place_empty[place], ((round / kPlaces) & 1u) ^ 1u);
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
             if (!ok) break;
-            fence_after_sync();
-            const uint32_t at = tm + quadrant + S::places_at + place * (kSubK / 2);
-            tmem_st16(at, va);
-            tmem_st16(at + 16, vb);
-            tmem_st_wait();
-            fence_before_sync();
+            if (i < subs) {
+                fence_after_sync();
+                const uint32_t at = tm + quadrant + S::places_at + place * (kRoundK / 2) + (set & 1) * (kSubK / 2);
+                tmem_st16(at, va);
+                tmem_st16(at + 16, vb);
+                tmem_st_wait();
+                fence_before_sync();
+            }
             __syncwarp();
             if (lane == 0) arrive(&bar.place_full[place]);
         }
