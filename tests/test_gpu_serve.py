@@ -610,6 +610,39 @@ def test_calls_side_by_side():
             assert all(torch.equal(p, q) for p, q in zip(a, b))
 
 
+@pytest.mark.parametrize("M", [130, 300])
+def test_many_rows_in_a_chain(M):
+    """Products whose rows another product wrote just before, beside other calls on other streams, and replayed."""
+    K, N = 1024, 640
+    g = gen(M)
+    x = randn(g, M, K, dtype=BF16).cuda()
+    w1 = tuple(t.cuda() for t in lib.random_weight(g, N, K, fmt="e2m1", group=32))
+    w2 = tuple(t.cuda() for t in lib.random_weight(g, K, N, fmt="e2m1", group=32))
+
+    def chain(x, stream=None):
+        for _ in range(4):
+            x = kda.kda_gemm4(kda.kda_gemm4(x, *w1, stream=stream), *w2, stream=stream)
+        return x
+
+    want, few = chain(x), chain(x[:20])
+    torch.cuda.synchronize()
+    assert torch.isfinite(want).all()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    for _ in range(5):
+        got = [chain(x if i % 2 else x[:20], s) for i, s in enumerate(streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, want if i % 2 else few) for i, y in enumerate(got))
+    held_in = x.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = chain(held_in)
+    held_in.copy_(x.flip(0))
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(held, chain(x.flip(0))) and torch.equal(held, want.flip(0))
+
+
 def test_after_the_multi_token_decode():
     """A step as it is run: the layer decodes each sequence's last token and its drafts from kept states, projections in 4 bits
     on both sides, the drafts are verified, and the layer runs again over what was accepted."""
