@@ -221,6 +221,7 @@ template <int N> __device__ __forceinline__ void product(uint8_t* ring, Barriers
         }
     } else if (warp == 1) {
         const uint64_t rows = desc_sw128(base, 16, 1024), columns = desc_sw128(base + kTileA, 16, 1024);
+        wait_for_columns();  // the time of the kernel in front does not count against a wait's deadline
         for (int kb = 0; kb < blocks; ++kb) {
             const uint32_t i = c.stage + kb, s = i % S::stages, gi = c.slot + kb / 2, slot = gi % kSlots;
             if (!warp_wait(&bar.full[s], (i / S::stages) & 1u) ||

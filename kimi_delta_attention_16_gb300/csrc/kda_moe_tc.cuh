@@ -152,6 +152,7 @@ __device__ __forceinline__ void stay(uint8_t* smem, StayBarriers& bar, const Map
         });
     } else if (warp == 1) {
         const uint64_t rows = desc_sw128(base, 16, 1024), columns = desc_sw128(base + kTileA, 16, 1024);
+        few::wait_for_kernel_before();  // its time does not count against a wait's deadline
         walk([&](uint32_t p, int, int, int, int) {
             bool ok = true;
             uint32_t d = 0, turn = p * chunks;

@@ -151,6 +151,7 @@ template <int N> __device__ __forceinline__ void product(uint8_t* ring, Barriers
         }
     } else if (warp == 1) {
         const uint64_t first = desc_sw128(cols, 16, 1024);
+        few::wait_for_kernel_before();  // its time does not count against a wait's deadline
         int s = 0;
         uint32_t phase = 0;
         for (int i = 0; i < rounds; ++i) {
@@ -205,6 +206,7 @@ template <int N> __device__ __forceinline__ void product(uint8_t* ring, Barriers
             __syncwarp();
             if (lane == 0) arrive(&bar.codes_empty[s]);
             if (round >= rounds) continue;
+            if (2 * g == kPlaces) few::wait_for_kernel_before();  // from here on places come back as products end
             if (lane == 0) ok = mbar_wait(&bar.place_empty[place], ((round / kPlaces) & 1u) ^ 1u);
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
             if (!ok) break;
@@ -219,6 +221,7 @@ template <int N> __device__ __forceinline__ void product(uint8_t* ring, Barriers
             __syncwarp();
             if (lane == 0) arrive(&bar.place_full[place]);
         }
+        few::wait_for_kernel_before();
         if (lane == 0 && ok) ok = mbar_wait(&bar.sums, 0u);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
         if (ok) {

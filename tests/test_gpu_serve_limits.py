@@ -1,0 +1,50 @@
+"""4-bit weights, the mixture of experts and the verification of drafts at the limits of what they accept: largest batches,
+magnitudes at either end, values that are not finite, kernels that take seconds."""
+import numpy as np
+import pytest
+import torch
+
+import kimi_delta_attention_16_gb300 as kda
+import serve_testlib as lib
+from serve_testlib import U, f64, gen, randn, within
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def cuda(w):
+    return w.cuda() if isinstance(w, torch.Tensor) else tuple(t.cuda() for t in w)
+
+
+def experts(g, E, D, F, fmt, group=32, sdt=BF16):
+    """Router, w_in, w_out on the GPU and the weights' values."""
+    router = randn(g, E, D, std=D ** -0.5, dtype=BF16)
+    if fmt == "bf16":
+        wi, wo = randn(g, E, 2 * F, D, std=D ** -0.5, dtype=BF16), randn(g, E, D, F, std=F ** -0.5, dtype=BF16)
+        return router, cuda(wi), cuda(wo), f64(wi), f64(wo)
+    wi = lib.random_weight(g, E, 2 * F, D, fmt=fmt, group=group, scale_dtype=sdt)
+    wo = lib.random_weight(g, E, D, F, fmt=fmt, group=group, scale_dtype=sdt)
+    return router, cuda(wi), cuda(wo), lib.unpack_ref(*wi), lib.unpack_ref(*wo)
+
+
+# ------------------------------------------------------------------ waits and their deadlines
+def test_moe_first_products_longer_than_a_deadline():
+    """The second products start beside the first ones and wait for them for as long as they take: 61,440 tokens that digits
+    do not hold are multiplied one by one by a single CTA, for longer than a wait inside a kernel may last."""
+    M, D, F = 65535, 2048, 32
+    g = gen(50)
+    router, wi, wo, wi64, wo64 = experts(g, 1, D, F, "e2m1")
+    x = torch.full((M, D), 2.0 ** -110, dtype=BF16, device="cuda")
+    some = torch.arange(0, M, 16)
+    rows = randn(g, len(some), D, dtype=BF16)
+    x[some.cuda()] = rows.cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = kda.kda_moe(x, router.cuda(), wi, wo, 1, out_dtype=F32, d_status=status)
+    assert int(status) == 0
+    few = torch.arange(0, len(some), 400)
+    ry, _, _, bound = lib.moe_ref(rows[few], router, wi64, wo64, 1, None, "sigmoid", 1.0)
+    within(y[some[few].cuda()], ry, bound + U[F32] * (ry.abs() + bound))
+    # what such a token's hidden values (|x|^2 and less) give lies below fp32's smallest
+    rest = torch.ones(M, dtype=torch.bool)
+    rest[some] = False
+    assert bool((y[rest.cuda()] == 0).all())
