@@ -163,16 +163,18 @@ cudaError_t launch_halves(const bf16* x, int64_t xs, bool wide, int rows, int K,
 
 constexpr float kSumOf = -8.f * 0x1p-20f;
 
-// One product by itself, for a sum that came out as NaN: a row of x with an infinity or values that no factor is for.
+// One product by itself, for a sum that came out as NaN: a row of x with an infinity or values that no factor is for.  An eighth
+// of the weight times x, so that neither a scale nor an x next to the end of fp32 overflows where the product does not.
 static __device__ __noinline__ float direct(const uint8_t* codes, const uint8_t* scales, int scale_bytes, int group, const bf16* x, int K) {
     float sum = 0.f;
     for (int g = 0; g < K / group; ++g) {
-        float one = 0.f;
-        for (int i = g * group; i < (g + 1) * group; ++i) one = fmaf((float)((int)(codes[i >> 1] >> (4 * (i & 1)) & 15u) - 8), to_f(x[i]), one);
         const float s = scale_bytes == 2 ? to_f(reinterpret_cast<const bf16*>(scales)[g]) : reinterpret_cast<const float*>(scales)[g];
-        sum = fmaf(one, s, sum);
+        for (int i = g * group; i < (g + 1) * group; ++i) {
+            const float eighth = 0.125f * ((int)(codes[i >> 1] >> (4 * (i & 1)) & 15u) - 8);
+            sum = fmaf(eighth * s, to_f(x[i]), sum);
+        }
     }
-    return sum;
+    return 8.f * sum;
 }
 
 // The sums of a CTA.  row_of(pass, tile, r): the matrix's row of row r of one of the W / ks tiles of 32 rows that the CTA

@@ -83,3 +83,23 @@ def test_moe_many_tokens_of_nan(fmt):
     for a, b in zip(clean, (y, ids, w)):
         assert torch.equal(a[1::2], b[1::2])
     assert milliseconds(call) < 10 * before
+
+
+# ------------------------------------------------------------------ magnitudes
+@pytest.mark.parametrize("group,sdt", [(32, F32), (64, BF16), (128, F32)])
+@pytest.mark.parametrize("exponent", [121, 122, 124, 126, 127])
+def test_gemm4_integer_codes_largest_rows(group, sdt, exponent):
+    """Rows that no power of two brings to where fp16 holds them are multiplied one by one; the result fits fp32, a code times x
+    does not.  Each product is rounded twice (the eighth of a weight, the sum), which is less than what gemm4_ref allows."""
+    M, N, K = 5, 60, 512
+    g = gen(exponent + group)
+    codes, scales = lib.random_weight(g, N, K, fmt="int4", group=group, scale_dtype=sdt, std=2.0 ** -30)
+    x = torch.where(torch.rand(M, K, generator=g) < 0.5, -1.0, 1.0) * 2.0 ** exponent * (1 + 0.75 * torch.rand(M, K, generator=g)).clamp(max=1.75)
+    x[3] = randn(g, K)  # beside an ordinary one
+    x = x.to(BF16)
+    got = kda.kda_gemm4(x.cuda(), codes.cuda(), scales.cuda(), out_dtype=F32)
+    ref, err = lib.gemm4_ref(x, lib.unpack_ref(codes, scales), "none")
+    assert float(ref.abs().max()) < 3e38
+    # K products and as many additions, each within 2^-24 of the sum of magnitudes so far
+    mass = f64(x).abs() @ lib.unpack_ref(codes, scales).abs().T
+    within(got, ref, torch.maximum(err, (K + 2) * 2.0 ** -24 * mass) + U[F32] * ref.abs())
