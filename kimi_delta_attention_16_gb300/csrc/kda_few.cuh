@@ -163,7 +163,8 @@ cudaError_t launch_halves(const bf16* x, int64_t xs, bool wide, int rows, int K,
 
 constexpr float kSumOf = -8.f * 0x1p-20f;
 
-// One product by itself, for a sum that came out as NaN: a row of x with an infinity or values that no factor is for.  An eighth
+// One product by itself, for a sum that came out as NaN or infinite: a row of x with an infinity or values that no factor is for, or
+// scales from 2^123 on (a run's sum, before its factor, is up to 2^5 of them).  An eighth
 // of the weight times x, so that neither a scale nor an x next to the end of fp32 overflows where the product does not.
 static __device__ __noinline__ float direct(const uint8_t* codes, const uint8_t* scales, int scale_bytes, int group, const bf16* x, int K) {
     float sum = 0.f;
@@ -173,6 +174,22 @@ static __device__ __noinline__ float direct(const uint8_t* codes, const uint8_t*
             const float eighth = 0.125f * ((int)(codes[i >> 1] >> (4 * (i & 1)) & 15u) - 8);
             sum = fmaf(eighth * s, to_f(x[i]), sum);
         }
+    }
+    return 8.f * sum;
+}
+
+// The same with a hidden value's two columns (value and remainder, laid out by k_moe_in): NaN where a run has no factor.
+static __device__ __noinline__ float direct_columns(const uint8_t* codes, const uint8_t* scales, int scale_bytes, int group, const __half* hi,
+                                                    const __half* lo, const float* factor, int K) {
+    float sum = 0.f;
+    for (int r = 0; r * kRun < K; ++r)
+        if (isnan(factor[r])) return NAN;
+    for (int k = 0; k < K; ++k) {
+        const float s = scale_bytes == 2 ? to_f(reinterpret_cast<const bf16*>(scales)[k / group]) : reinterpret_cast<const float*>(scales)[k / group];
+        const float eighth = 0.125f * ((int)(codes[k >> 1] >> (4 * (k & 1)) & 15u) - 8);
+        const int at = (k & ~7) + 2 * (k & 3) + (k >> 2 & 1);
+        const float x = (__half2float(hi[at]) + __half2float(lo[at])) * (factor[k / kRun] * 0x1p-20f);
+        sum = fmaf(eighth * s, x, sum);
     }
     return 8.f * sum;
 }

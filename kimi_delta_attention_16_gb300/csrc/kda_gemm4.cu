@@ -64,7 +64,7 @@ template <int NT, int GS, int SB> __global__ void __launch_bounds__(32 * warps_f
                     const int col = 8 * c + 2 * t + (j & 1), row = at * kRows + 16 * u + g + 8 * (j >> 1);
                     if (col >= n || row >= p.N) continue;
                     float v = acc[u][c][j];
-                    if (isnan(v))
+                    if (!isfinite(v))
                         v = direct(p.w.codes + (int64_t)row * (p.K / 2), p.w.scales + (int64_t)row * (p.K / p.group) * SB, SB, p.group,
                                    p.a + (int64_t)(c0 + col) * p.lda, p.K);
                     v = apply(p.epi, v);

@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(32 * kExpertWarps, 1) k_moe_in(const Experts p
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float gate = sums[c * kPitch + 32 * i + lane], up = sums[c * kPitch + 128 + 32 * i + lane];
-                if (row0 + 32 * i + lane < F && (isnan(gate) || isnan(up)) && given.wanted(slots[c0 + c])) {
+                if (row0 + 32 * i + lane < F && !(isfinite(gate) && isfinite(up)) && given.wanted(slots[c0 + c])) {
                     const bf16* x = given.x + of[c] * given.xs;
                     const int64_t rg = row0 + 32 * i + lane, ru = rg + F;
                     const int row_scales = p.K / p.group * SB;
@@ -390,7 +390,14 @@ __global__ void __launch_bounds__(32 * kExpertWarps, 1) k_moe_out(const Experts 
                 for (int j = 0; j < 4; ++j) {
                     const int row = row0 + few::kRows * warp + g + 8 * j;
                     const float(&s)[4] = acc[j >> 1][c];
-                    if (row < p.rows) parts[(int64_t)slot * p.rows + row] = w * (s[2 * (j & 1)] + s[2 * (j & 1) + 1]);
+                    if (row >= p.rows) continue;
+                    float v = s[2 * (j & 1)] + s[2 * (j & 1) + 1];
+                    if (!isfinite(v) && !isnan(w)) {
+                        const int64_t at = 2 * (int64_t)(c0 + token);
+                        v = few::direct_columns(m.codes + (int64_t)row * (p.K / 2), m.scales + (int64_t)row * (p.K / p.group) * SB, SB, p.group,
+                                                p.x.x + at * p.K, p.x.x + (at + 1) * p.K, p.x.factor + at * ((p.K + kRun - 1) / kRun), p.K);
+                    }
+                    parts[(int64_t)slot * p.rows + row] = w * v;
                 }
             }
         });

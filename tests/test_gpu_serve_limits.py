@@ -103,3 +103,49 @@ def test_gemm4_integer_codes_largest_rows(group, sdt, exponent):
     # K products and as many additions, each within 2^-24 of the sum of magnitudes so far
     mass = f64(x).abs() @ lib.unpack_ref(codes, scales).abs().T
     within(got, ref, torch.maximum(err, (K + 2) * 2.0 ** -24 * mass) + U[F32] * ref.abs())
+
+
+@pytest.mark.parametrize("sdt", [F32, BF16])
+@pytest.mark.parametrize("M", [1, 20])
+def test_gemm4_integer_codes_largest_scales(M, sdt):
+    """Scales next to the end of fp32 (as kda_pack4 makes them of weights of 3e38) and small rows: a run's sum times its scale
+    passes fp32 before the row's power of two is taken off, the result does not."""
+    N, K = 40, 512
+    g = gen(M)
+    codes = torch.full((N, K // 2), 0xff, dtype=torch.uint8)
+    codes[::4] = 0
+    codes[1::4] = torch.randint(0, 256, codes[1::4].shape, generator=g, dtype=torch.uint8)
+    scales = torch.full((N, K // 128), 4.5e37).to(sdt)
+    x = (1e-10 * (1 + torch.rand(M, K, generator=g))).to(BF16)
+    got = kda.kda_gemm4(x.cuda(), codes.cuda(), scales.cuda(), out_dtype=F32)
+    w = lib.unpack_ref(codes, scales)
+    ref, err = lib.gemm4_ref(x, w, "none")
+    # or K products of an eighth of the weight, each with two roundings, added up one by one
+    within(got, ref, torch.maximum(err, (K + 2) * 2.0 ** -24 * (f64(x).abs() @ w.abs().T)) + U[F32] * ref.abs())
+
+
+@pytest.mark.parametrize("which", ["in", "out"])
+def test_moe_integer_codes_largest_scales(which):
+    """The same in either of the experts' products: x and, in the second, the weights of the first bring the values back."""
+    M, E, top, D, F = 5, 3, 2, 256, 384
+    g = gen(60)
+    router, wi, wo, _, _ = experts(g, E, D, F, "int4", 128, F32)
+    # the first products' weights are not negative, so that hidden values are of one sign
+    wi[0].bitwise_or_(0x88)
+    if which == "in":
+        wi[0].fill_(0xff)
+        wi[1].fill_(4.5e37)
+        wo[1].mul_(1e-20)
+    else:
+        wo[0].fill_(0xff)
+        wo[1].fill_(4.8e37)
+    # gates and their counterparts of 1e8 and weights of 1e-22 behind them, or hidden values of 1e-26 and weights of 3e38
+    x = (1 + torch.rand(M, D, generator=g)) * (1e-33 if which == "in" else 1e-13)
+    x = x.to(BF16)
+    y = kda.kda_moe(x.cuda(), router.cuda(), wi, wo, top, out_dtype=F32, score="softmax")
+    wi64, wo64 = lib.unpack_ref(*wi), lib.unpack_ref(*wo)
+    ry, _, _, bound = lib.moe_ref(x, router, wi64, wo64, top, None, "softmax", 1.0)
+    assert 1e-6 < float(ry.abs().max()) < 1e30
+    # products added up one by one instead of by groups: F + 2 roundings each of 2^-24 of the sum of magnitudes, where
+    # moe_ref counts F / 32 + 16 of 2^-23 (for all of them at once: (F + 2) / 2 / (F / 32 + 16) = 6.9 times, D alike)
+    within(y, ry, 8 * bound + U[F32] * ry.abs())
