@@ -434,20 +434,20 @@ inline bool encode_maps_bf16(Maps* m, const void* w, int64_t rows, const void* c
            encode_tensor_map_2d_as(&m->b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, columns, K, n, 2 * (uint64_t)K, 64, box, true);
 }
 
-// One product by itself, for a sum that came out as NaN: a row of x that digits do not hold (values that are not finite,
-// or all tiny) is multiplied here as it stands.
+// One product by itself, for a sum that came out as NaN or infinite: a row of x that digits do not hold (values that are not
+// finite, or all tiny), or sums next to the end of fp32, where the digits in front, rounded up, pass it.  An eighth of the
+// weight times x, so that only a product that overflows does.
 static __device__ __noinline__ float direct(const uint8_t* codes, const uint8_t* scales, const bf16* x, int K) {
     float sum = 0.f;
     for (int g = 0; g < K / 32; ++g) {
-        float part = 0.f;
+        const float s = __uint_as_float((uint32_t)scales[g] << 23);
         for (int i = 0; i < 32; ++i) {
             const uint32_t c = codes[(g * 32 + i) >> 1] >> (4 * (i & 1)) & 15u;
-            const float m = (c & 6u) ? __uint_as_float(((126u + ((c >> 1) & 3u)) << 23) | ((c & 1u) << 22)) : 0.5f * (c & 1u);
-            part = fmaf((c & 8u) ? -m : m, to_f(x[g * 32 + i]), part);
+            const float eighth = (c & 6u) ? __uint_as_float(((123u + ((c >> 1) & 3u)) << 23) | ((c & 1u) << 22)) : 0.0625f * (c & 1u);
+            sum = fmaf(((c & 8u) ? -eighth : eighth) * s, to_f(x[g * 32 + i]), sum);
         }
-        sum = fmaf(part, __uint_as_float((uint32_t)scales[g] << 23), sum);
     }
-    return sum;
+    return 8.f * sum;
 }
 
 // The part of K that a rank of a cluster takes, in whole runs of 256.

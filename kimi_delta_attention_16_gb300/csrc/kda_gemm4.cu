@@ -106,9 +106,9 @@ struct Gemm4Tc {
     int* d_status;
 };
 
-// The part of a tile's joined sums that this rank writes: tokens [c0, c0 + n).  What came out as NaN (Inf: or infinite) is
+// The part of a tile's joined sums that this rank writes: tokens [c0, c0 + n).  What came out as NaN or infinite is
 // computed again from the operands as they were given.
-template <int Threads, bool Inf, typename Tout>
+template <int Threads, typename Tout>
 __device__ __forceinline__ void put_tile(const Gemm4Tc& p, const float* red, int rank, int row0, int c0, int n, Tout* __restrict__ out) {
     int r0, r1;
     fewtc::rows_of(rank, p.ranks, r0, r1);
@@ -121,7 +121,7 @@ __device__ __forceinline__ void put_tile(const Gemm4Tc& p, const float* red, int
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int64_t row = row0 + r + j;
-            if ((Inf ? !isfinite(v[j]) : isnan(v[j])) && j < left)
+            if (!isfinite(v[j]) && j < left)
                 v[j] = fewtc::direct(p.codes + row * (p.K / 2), p.w_scales + row * (p.K / 32), p.a + (int64_t)(c0 + c) * p.lda, p.K);
             v[j] = apply(p.epi, v[j]);
         }
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(fewtc::kThreads, fewtc::Shape<N>::per_sm) k_ge
     float* red = reinterpret_cast<float*>(smem);
     fewtc::product<N>(smem, bar, t, count, red);
     if (p.ranks > 1) cooperative_groups::this_cluster().sync();
-    put_tile<fewtc::kThreads, false>(p, red, rank, row0, c0, n, out);
+    put_tile<fewtc::kThreads>(p, red, rank, row0, c0, n, out);
     if (p.ranks > 1) cooperative_groups::this_cluster().sync(); else __syncthreads();
     fewtc::finish<N>(bar, p.d_status);
 }
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(widetc::kThreads, 1) k_gemm4_widen(const __gri
     float* red = reinterpret_cast<float*>(smem);
     widetc::product<N>(smem, bar, t, red);
     if (p.ranks > 1) cooperative_groups::this_cluster().sync();
-    put_tile<widetc::kThreads, true>(p, red, rank, row0, c0, min(N, p.M - c0), out);
+    put_tile<widetc::kThreads>(p, red, rank, row0, c0, min(N, p.M - c0), out);
     if (p.ranks > 1) cooperative_groups::this_cluster().sync(); else __syncthreads();
     widetc::finish<N>(bar, p.d_status);
 }

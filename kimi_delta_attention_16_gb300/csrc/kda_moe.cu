@@ -264,7 +264,7 @@ struct Experts {
     __device__ __forceinline__ Weights matrix(int e) const { return Weights{w.codes + e * w_bytes, w.scales + e * s_bytes}; }
 };
 
-struct Direct {  // the operands as they were given, for sums that come out as NaN
+struct Direct {  // the operands as they were given, for sums that come out as NaN or infinite
     const uint8_t *codes, *scales;
     const bf16* x;
     int64_t xs;
@@ -429,7 +429,7 @@ k_moe_in_tc(const __grid_constant__ fewtc::Maps maps, const fewtc::StayArgs p, c
             const float* sum = red + c * kRedPitch + r;
             float gate = sum[0], up = sum[64];
             if constexpr (Mx) {
-                if (f < F && (isnan(gate) || isnan(up)) && given.wanted(slots[c0 + c])) {
+                if (f < F && !(isfinite(gate) && isfinite(up)) && given.wanted(slots[c0 + c])) {
                     const bf16* row = given.x + (int64_t)token * given.xs;
                     const int64_t g = (int64_t)e * p.rows + f, u = g + F;
                     gate = fewtc::direct(given.codes + g * (p.K / 2), given.scales + g * (p.K / 32), row, p.K);

@@ -149,3 +149,49 @@ def test_moe_integer_codes_largest_scales(which):
     # products added up one by one instead of by groups: F + 2 roundings each of 2^-24 of the sum of magnitudes, where
     # moe_ref counts F / 32 + 16 of 2^-23 (for all of them at once: (F + 2) / 2 / (F / 32 + 16) = 6.9 times, D alike)
     within(y, ry, 8 * bound + U[F32] * ry.abs())
+
+
+@pytest.mark.parametrize("M,dtype", [(1, F32), (7, BF16), (40, F32), (130, BF16)])
+def test_gemm4_e2m1_results_next_to_the_end_of_fp32(M, dtype):
+    """1.75 times 2^127 is 2.98e38; its digit in front, 2 times 2^127, is not a number of fp32.  Rows that hold it alone, exact, and
+    beside others that do overflow."""
+    N, K = 30, 64
+    codes = torch.zeros(N, K // 2, dtype=torch.uint8)
+    codes[:, 5] = 2  # 1.0 at element 10
+    codes[1::2, 5] = 10  # -1.0
+    codes[2, 5] = 6  # 4.0
+    codes[:, 20] = 2  # and 1.0 at element 40
+    scales = torch.full((N, K // 32), 254, dtype=torch.uint8)
+    scales[:, 1] = 127
+    x = torch.zeros(M, K)
+    x[:, 10] = 1.75
+    x[:, 40] = 2.0 ** 110  # lies below a bf16's last digit of the first, above an fp32's
+    got = kda.kda_gemm4(x.to(BF16).cuda(), codes.cuda(), scales.cuda(), out_dtype=dtype)
+    want = (x.double() @ lib.unpack_ref(codes, scales).T).float()
+    assert bool(torch.isinf(want[:, 2]).all()) and int(torch.isinf(want).sum()) == M
+    assert torch.equal(got.cpu(), want.to(dtype))
+
+
+def test_moe_e2m1_gates_next_to_the_end_of_fp32():
+    """The same in the experts' first products: a gate of -2.98e38 gives a hidden value of 0, one that overflows as well; a gate of
+    2.98e38 under a counterpart of 1e-38 an ordinary one."""
+    E, D, F = 2, 64, 32
+    ci, si = torch.zeros(E, 2 * F, D // 2, dtype=torch.uint8), torch.full((E, 2 * F, D // 32), 127, dtype=torch.uint8)
+    ci[:, :F, 0] = 2   # gates: x[0] 2^127
+    ci[:, :F // 2, 0] = 10
+    si[:, :F, 0] = 254
+    ci[:, F:, 16] = 2  # the other side: x[32] 2^-126
+    si[:, F:, 1] = 1
+    g = gen(70)
+    wo = lib.random_weight(g, E, D, F, fmt="e2m1", group=32)
+    x = torch.zeros(3, D)
+    x[:, 0], x[:, 32] = 1.75, 1.0
+    router = randn(g, E, D, dtype=BF16)
+    y = kda.kda_moe(x.to(BF16).cuda(), router.cuda(), (ci.cuda(), si.cuda()), cuda(wo), 2, out_dtype=F32, score="softmax")
+    h = torch.zeros(F, dtype=torch.float64)
+    h[F // 2:] = 1.75 * 2.0  # silu(1.75 2^127) 2^-126
+    w = torch.softmax(x.double() @ f64(router).T, 1)
+    parts = torch.stack([lib.unpack_ref(wo[0][e], wo[1][e]) @ h for e in range(E)])
+    # a hidden value and a weight, each rounded once, products exact, F additions
+    mass = torch.stack([lib.unpack_ref(wo[0][e], wo[1][e]).abs() @ h for e in range(E)])
+    within(y, w @ parts, (F + 8) * 2.0 ** -24 * (w @ mass))
