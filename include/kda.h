@@ -706,7 +706,8 @@ kda_status kda_unpack4(const kda_pack4_args* args, kda_stream_t stream);
  * or fp32, rounded once; epilogues as in kda_gemm; M, N >= 0; C must not overlap an input.
  * Values of A enter the products exactly but for what lies below 2^-22 of the largest of their 32 (e2m1) or 2^-39 of
  * the largest of their 128 (int4); sums are fp32, in a fixed order that depends on M, N and K (e2m1, more than 96 rows and a
- * bf16 C: values exact, sums cut off instead of rounded, 6e-6 over 2,048 elements).  A row of A with values that are
+ * bf16 C, K up to 262,144: values exact, sums cut off instead of rounded, by 2^-12 of the sum of |products| at most, an eighth
+ * of what rounding C costs; 4e-5 measured for products of one sign, 5e-6 for random ones).  A row of A with values that are
  * not finite gives what the formula gives, slowly.  Needs an sm_103 device.  A wait that times out on the device is reported through
  * d_status (KDA_ERR_TIMEOUT). */
 typedef struct {

@@ -480,11 +480,11 @@ __device__ __forceinline__ float4 joined4(const float* red, int ranks, int token
 // CTAs of a cluster that share a tile's K: the number that leaves the busiest SM the least to do, in runs of 256 elements,
 // where the CTAs that run side by side take about `overhead` runs' time to start and to join.  One row: 12,288 x 7,168 in
 // 19.6 us by one CTA per tile, 14.4 by three (the rule), 24.7 by eight; 1,024 x 7,168 in 18.5, 14.4 and 12.4 (the rule).
-inline int cluster_ranks(int64_t tiles, int K, int per_sm, int overhead) {
+inline int cluster_ranks(int64_t tiles, int K, int per_sm, int overhead, int at_least = 1) {
     const int runs = (K + 255) / 256;
-    int best = 1;
+    int best = at_least;
     int64_t least = INT64_MAX;
-    for (int r = 1; r <= 8 && r <= runs; ++r) {
+    for (int r = at_least; r <= 8 && r <= runs; ++r) {
         const int64_t on_one = (tiles * r + 151) / 152;
         const int64_t t = on_one * ((runs + r - 1) / r) + (on_one + per_sm - 1) / per_sm * overhead;
         if (t < least) least = t, best = r;

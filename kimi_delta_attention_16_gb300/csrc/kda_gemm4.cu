@@ -241,7 +241,7 @@ template <int N> cudaError_t launch_widen(const kda_gemm4_args& a, cudaStream_t 
     Gemm4Tc p;
     const int tiles = (a.N + kTileRows - 1) / kTileRows, blocks = (a.M + N - 1) / N;
     p.M = a.M, p.N = a.N, p.K = a.K, p.epi = a.epilogue;
-    p.ranks = fewtc::cluster_ranks((int64_t)tiles * blocks, a.K, 1, 10);
+    p.ranks = fewtc::cluster_ranks((int64_t)tiles * blocks, a.K, 1, 10, widetc::least_ranks(a.K));
     p.w_scales = static_cast<const uint8_t*>(a.scales), p.b_scales = nullptr, p.codes = a.codes;
     p.a = static_cast<const bf16*>(a.A), p.lda = a.lda, p.ldc = a.ldc, p.d_status = a.d_status;
     return launch_kernel(k_gemm4_widen<N>, dim3(tiles * p.ranks, blocks), widetc::kThreads, p.ranks, S::smem, true, s, maps, p, static_cast<bf16*>(a.C));
@@ -261,7 +261,7 @@ cudaError_t launch_gemm4(const kda_gemm4_args& a, cudaStream_t s) {
     if (a.format == KDA_WEIGHT_E2M1) {
         // From 97 rows on widened weights, where C is bf16.  12,288 x 7,168, digits against widened: 64 rows 35 and 43 us, 128 rows
         // 48 and 44, 256 rows 92 and 49, 512 rows 174 and 89; 7,168 x 12,288: 25 and 39, 50 and 42, 72 and 48, 148 and 79.
-        if (a.c_dtype == KDA_BF16 && a.M > 96) return a.M <= 128 ? launch_widen<128>(a, s) : launch_widen<256>(a, s);
+        if (a.c_dtype == KDA_BF16 && a.M > 96 && widetc::least_ranks(a.K) <= widetc::kMostRanks) return a.M <= 128 ? launch_widen<128>(a, s) : launch_widen<256>(a, s);
         // as few columns as hold all rows, and at most 32 rows' (256 rows: 82 us, 91 with 16 rows per CTA, 146 with 8)
         if (a.M <= 2) return launch_tc_out<16>(a, s);
         if (a.M <= 4) return launch_tc_out<32>(a, s);

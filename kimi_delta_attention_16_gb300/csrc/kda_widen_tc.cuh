@@ -12,9 +12,13 @@
 // Widening: three bits of a code, put at bits 6 to 8 of a bf16, are its value times 2^-126 (e2m1's subnormals are bf16's
 // there), so one product with 2^(byte - 1) ends it; bytes above 128 need a second.
 //
-// Sums stay in one accumulator.  The instruction cuts them off where the accumulator ends: 5.7e-6 over 2,048 elements
-// (measured with fp32 results in kda_moe_tc.cuh), in proportion more over longer rows, against 1.7e-3 for rounding the result to
-// bf16 - and so C is bf16 here; fp32 takes digits.
+// Sums stay in one accumulator, which every instruction (16 elements) cuts off instead of rounding: 2^-23 of the sum of
+// magnitudes at most, and all in one direction where products have one sign.  So a CTA takes kMostK elements at most: 2^-12 of
+// the sum of magnitudes, an eighth of what rounding the result to bf16 costs - and so C is bf16 here, fp32 takes digits.
+// Parts of longer rows are added up in fp32 by the cluster; rows longer than a cluster takes go to the digits.  Measured, 19,456 x K,
+// 130 rows, products of one sign, all results together: 5e-6 too small at K = 7,168, 1.5e-5 at 16,384, and with one accumulator
+// whatever the length 8.3e-5 at 65,536, 2.1e-4 at 131,072, 3.9e-3 at 2^20; random signs a twentieth of that.
+// (kMostK = 16,384: 20,000 elements in 121 us instead of 111, 65,536 in 445 instead of 338.)
 #pragma once
 
 #include "kda_few_tc.cuh"
@@ -28,6 +32,10 @@ using fewtc::tma_2d;
 
 constexpr int kThreads = 640;
 constexpr int kSubK = 64, kRoundK = 128, kCodesK = 256, kPlaces = 4;
+constexpr int kMostK = 32768;  // of one accumulator
+constexpr int kMostRanks = 8;
+static_assert(kMostK % fewtc::kStageK == 0, "slices are whole runs");
+inline int least_ranks(int K) { return (K + kMostK - 1) / kMostK; }
 constexpr uint32_t kCodes = few::kTileRows * (kCodesK / 2);
 
 template <int N> struct Shape {

@@ -195,3 +195,44 @@ def test_moe_e2m1_gates_next_to_the_end_of_fp32():
     # a hidden value and a weight, each rounded once, products exact, F additions
     mass = torch.stack([lib.unpack_ref(wo[0][e], wo[1][e]).abs() @ h for e in range(E)])
     within(y, w @ parts, (F + 8) * 2.0 ** -24 * (w @ mass))
+
+
+@pytest.mark.parametrize("M", [100, 130])
+@pytest.mark.parametrize("K", [12288, 32768, 40000, 131072, 262144, 294912])
+def test_gemm4_many_rows_do_not_shrink(M, K):
+    """Long sums of products of one sign, more than 96 rows and a bf16 result, on as many tiles as there are SMs (so that no
+    cluster shares K of its own accord): an accumulator takes 32,768 elements, 2,048 instructions that cut off 2^-23 of what
+    has come together so far, half of the sum on average: 2^-13 for all results together at most, whatever the length.
+    Rounding to bf16 leaves nothing of the kind: the results spread evenly over a power of two, each is off by 2^-8 / sqrt(12) of
+    itself on average, so all 1.9 million of them by 6 * 2^-8 / sqrt(12 * 1.9e6) = 5e-6 together (six standard deviations)."""
+    N = 128 * 152
+    g = torch.Generator(device="cuda")
+    g.manual_seed(K + M)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8) & 0x77  # 0 to 6
+    # the first part of a row's scales a power of two lower, so that rows differ by up to 2
+    scales = torch.full((N, K // 32), 120, device="cuda", dtype=torch.uint8)
+    share = torch.rand(N, 1, generator=g, device="cuda")
+    scales -= (torch.arange(K // 32, device="cuda").unsqueeze(0) < share * (K // 32)).to(torch.uint8)
+    x = (torch.rand(M, K, generator=g, device="cuda") * (1 + torch.rand(M, 1, generator=g, device="cuda"))).to(BF16)
+    y = kda.kda_gemm4(x, codes, scales).double()
+    ref = kda.kda_gemm4(x, codes, scales, out_dtype=F32).double()  # rounded sums, 1e-7 off
+    assert abs(float((y / ref - 1).mean())) < 2.0 ** -13 + 5e-6
+    assert float((y / ref - 1).abs().max()) < 2.0 ** -12 + 2.0 ** -8
+
+
+def test_gemm4_many_rows_tiny_values():
+    """Rows of any magnitude beside one another, from 97 rows on as below: products and sums that fp32 holds as subnormal numbers only
+    are kept."""
+    N, K = 70, 640
+    g = gen(80)
+    codes, scales = lib.random_weight(g, N, K, fmt="e2m1", group=32)
+    for M in (96, 97, 140, 260):
+        x = randn(g, M, K)
+        x[1] = 0
+        x *= 2.0 ** torch.arange(0, -M, -1).clamp(min=-122).float().unsqueeze(1)
+        x[5, 32:64] *= 2.0 ** -100
+        x = x.to(BF16)
+        got = kda.kda_gemm4(x.cuda(), codes.cuda(), scales.cuda())
+        ref, err = lib.gemm4_ref(x, lib.unpack_ref(codes, scales), "none")
+        # the result's last digit is 2^-133 at least, an fp32 sum's 2^-149
+        within(got, ref, torch.maximum(err, torch.tensor(K * 2.0 ** -149)) + torch.maximum(U[BF16] * (ref.abs() + err), torch.tensor(2.0 ** -134)))
