@@ -781,8 +781,8 @@ kda_status kda_moe(const kda_moe_args* args, kda_stream_t stream);
 
 /* kda_verify -- which drafted tokens stand.  Rows are packed as kda_prefill's multi-token decode ran
  * them: a sequence of L + 1 rows (its last token and L drafts) has the target's distribution after each.
- *   target  [T_total][target_stride] bf16 or fp32 probabilities over V tokens (they need not sum to 1;
- *           values that are not above 0 count as 0)
+ *   target  [T_total][target_stride] bf16 or fp32 probabilities over V tokens (they need not sum to 1; of target and draft
+ *           alike, values that are not above 0 count as 0, NaN among them)
  *   draft   [T_total][draft_stride], same dtype: row i is what draft i was drawn from; the last row of a
  *           sequence is not read.  NULL: a drafter that proposes its best token only (probability 1)
  *   tokens  [T_total] int32 or int64: row i holds draft i; the last row of a sequence is not read

@@ -151,8 +151,10 @@ __device__ __forceinline__ int holder(Wide part, Wide end, Wide threshold) {
     return past ? __ffs(past) - 1 : 31 - __clz(with);
 }
 
-// u q < p without rounding the product (the smallest values scaled up, so that its lower half does not vanish).
+// u q < p without rounding the product (the smallest values scaled up, so that its lower half does not vanish).  What is not above 0
+// counts as 0 here as in the sums, NaN too.
 __device__ __forceinline__ bool takes(float u, float q, float p) {
+    q = fmaxf(q, 0.f), p = fmaxf(p, 0.f);
     if (p < 0x1p-60f) p *= 0x1p64f, q *= 0x1p64f;
     const float v = u * q;
     return v < p || (v == p && fmaf(u, q, -v) < 0.f);

@@ -236,3 +236,31 @@ def test_gemm4_many_rows_tiny_values():
         ref, err = lib.gemm4_ref(x, lib.unpack_ref(codes, scales), "none")
         # the result's last digit is 2^-133 at least, an fp32 sum's 2^-149
         within(got, ref, torch.maximum(err, torch.tensor(K * 2.0 ** -149)) + torch.maximum(U[BF16] * (ref.abs() + err), torch.tensor(2.0 ** -134)))
+
+
+# ------------------------------------------------------------------ verification
+def one_draft(p, q, u):
+    """Whether the draft of token 0 stands, for every triple: sequences of two rows over two tokens."""
+    n = len(u)
+    target, draft = torch.ones(2 * n, 2), torch.ones(2 * n, 2)
+    target[::2, 0], draft[::2, 0] = p, q
+    us = torch.full((2 * n,), 0.25)
+    us[::2] = u
+    cu = np.arange(0, 2 * n + 1, 2, dtype=np.int32)
+    out, accepted = kda.kda_verify(target.cuda(), torch.zeros(2 * n, dtype=torch.int32).cuda(), us.cuda(), cu, draft=draft.cuda())
+    assert bool(((out.cpu()[::2] == 0) | (accepted.cpu() == 0)).all())
+    return accepted.cpu().bool()
+
+
+def positive(v):
+    return torch.where(v > 0, v, torch.zeros_like(v)).double()
+
+
+def test_verify_drafts_of_any_value():
+    """Values that are not above 0 count as 0 on both sides; products of the smallest and of neighbours are not rounded."""
+    nan = float("nan")
+    vs = [nan, -1.0, -0.5, -1e-40, -0.0, 0.0, 1e-45, 3e-39, 2.0 ** -61, 2.0 ** -60, 0.1, 0.5, 1.0 - 2.0 ** -24, 1.0]
+    us = [0.0, 1e-45, 2.0 ** -64, 2.0 ** -24, 0.1, 0.5, 1.0 - 2.0 ** -24]
+    p, q, u = (t.reshape(-1).float() for t in torch.meshgrid(torch.tensor(vs), torch.tensor(vs), torch.tensor(us), indexing="ij"))
+    want = u.double() * positive(q) < positive(p)  # exact: 48 bits
+    assert torch.equal(one_draft(p, q, u), want)
