@@ -155,7 +155,7 @@ __device__ __forceinline__ int holder(Wide part, Wide end, Wide threshold) {
 // counts as 0 here as in the sums, NaN too.
 __device__ __forceinline__ bool takes(float u, float q, float p) {
     q = fmaxf(q, 0.f), p = fmaxf(p, 0.f);
-    if (p < 0x1p-60f) p *= 0x1p64f, q *= 0x1p64f;
+    if (p < 0x1p-60f) p *= 0x1p64f, u *= 0x1p64f;  // u, not q, which may be anything where values need not sum to 1
     const float v = u * q;
     return v < p || (v == p && fmaf(u, q, -v) < 0.f);
 }

@@ -264,3 +264,11 @@ def test_verify_drafts_of_any_value():
     p, q, u = (t.reshape(-1).float() for t in torch.meshgrid(torch.tensor(vs), torch.tensor(vs), torch.tensor(us), indexing="ij"))
     want = u.double() * positive(q) < positive(p)  # exact: 48 bits
     assert torch.equal(one_draft(p, q, u), want)
+
+
+def test_verify_large_values_beside_small_ones():
+    """Values need not sum to 1: a draft's value from 2^64 on beside a target's below 2^-60, u of 0 among them."""
+    vs = [1e-45, 1e-39, 1e-20, 2.0 ** -61, 2.0 ** -60, 1.0, 2.0 ** 63, 2.0 ** 64, 1e30, 3e38]
+    us = [0.0, 1e-45, 1e-38, 2.0 ** -64, 0.5]
+    p, q, u = (t.reshape(-1).float() for t in torch.meshgrid(torch.tensor(vs), torch.tensor(vs), torch.tensor(us), indexing="ij"))
+    assert torch.equal(one_draft(p, q, u), u.double() * q.double() < p.double())
