@@ -790,7 +790,8 @@ kda_status kda_moe(const kda_moe_args* args, kda_stream_t stream);
  * Draft i (token d) is taken while u_i draft_i(d) < target_i(d); a token outside [0, V) is never taken.
  * After the first one that is not (row a), or after all, one token is drawn with the last row's u: the
  * lowest index whose running sum exceeds u times the sum, of max(target_a - draft_a, 0) after a refusal
- * (of target_a where that is 0 everywhere), of the last row's target otherwise; -1 where nothing is above 0.
+ * (of target_a where that is 0 everywhere), of the last row's target otherwise; -1 where nothing is above 0, or
+ * where what is drawn from has an infinity in it or a sum beyond fp32.
  *   out      [T_total] of tokens' type: the accepted drafts, the drawn token, then -1
  *   accepted [N] int32: drafts taken (0 for a sequence without rows)
  * Comparisons of drafts are exact, sums carry about 48 bits.  V up to 4,000,000. */

@@ -24,6 +24,7 @@ namespace cg = cooperative_groups;
 constexpr int kTile = 1024;        // tokens per sum
 constexpr int kMaxTiles = 4096;    // of one CTA
 constexpr int kEnough = 2;         // CTAs per SM that a row is shared for
+constexpr int kNotFinite = -2;     // in place of the rank that holds the token, -1 where there is none
 constexpr unsigned kAll = 0xffffffffu;
 
 // s += p - q where that is positive (neither is negative).
@@ -233,12 +234,13 @@ template <typename T, typename Tok, int kThreads> __global__ void __launch_bound
             if (lane < a.ranks) total = a.ranks > 1 ? *cluster.map_shared_rank(&total_here, lane) : total_here;
             const Wide upto = running(total, lane);
             threshold = times(Wide{a.u[last], 0.f}, from(kAll, upto, 31));
-            const int owner = holder(total, upto, threshold);
+            // kNotFinite: an infinity, or a sum beyond fp32, has no share of anything
+            const int owner = __shfl_sync(kAll, upto.hi, 31) < INFINITY ? holder(total, upto, threshold) : kNotFinite;
             before = from(kAll, in_front(upto, lane), owner < 0 ? 0 : owner);
             if (lane == 0) s_owner = owner;
         }
         if (a.ranks > 1) cluster.sync(); else __syncthreads();
-        if (s_owner >= 0 || rest.kind == 0) break;
+        if (s_owner != -1 || rest.kind == 0) break;
         rest.kind = 0;  // nothing is left of the residual: p itself
     }
     const int owner = s_owner;

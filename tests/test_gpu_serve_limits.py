@@ -272,3 +272,38 @@ def test_verify_large_values_beside_small_ones():
     us = [0.0, 1e-45, 1e-38, 2.0 ** -64, 0.5]
     p, q, u = (t.reshape(-1).float() for t in torch.meshgrid(torch.tensor(vs), torch.tensor(vs), torch.tensor(us), indexing="ij"))
     assert torch.equal(one_draft(p, q, u), u.double() * q.double() < p.double())
+
+
+@pytest.mark.parametrize("V", [50, 5000, 40001])
+@pytest.mark.parametrize("N", [1, 200])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_verify_infinities_draw_nothing(N, V, dtype):
+    """What is drawn from with an infinity in it, or a sum beyond fp32, gives -1 wherever it stands and whatever u is; the other sequences
+    are as they were."""
+    g = gen(V + N)
+    inf = float("inf")
+    p = torch.rand(2 * N, V, generator=g).to(dtype)
+    q = torch.rand(2 * N, V, generator=g).to(dtype)
+    p[::2, 0], q[::2, 0] = 0.25, 0.5  # token 0 is proposed: taken where u is below a half
+    u = torch.rand(2 * N, generator=g)
+    tokens, cu = torch.zeros(2 * N, dtype=torch.int32), np.arange(0, 2 * N + 1, 2, dtype=np.int32)
+    run = lambda p, q: [t.cpu() for t in kda.kda_verify(p.cuda(), tokens.cuda(), u.cuda(), cu, draft=None if q is None else q.cuda())]  # noqa: E731
+    for at in (1, V // 2, V - 1):
+        for where, value in ((p, inf), (q, inf), (p, 3.0e38)):
+            a, b = p.clone(), q.clone()
+            bad = a if where is p else b
+            bad[::6, at] = value       # the first of two rows: what is drawn from after a refusal
+            bad[1::6, at] = value      # the second: after an acceptance
+            if value < inf:
+                bad[::6, 2], bad[1::6, 2] = 3.0e38, 3.0e38  # two of them: their sum, or the rest of it, passes fp32
+                if at == 2:
+                    continue
+            for draft in (b, None):
+                plain, (out, accepted) = run(p, None if draft is None else q), run(a, draft)
+                assert torch.equal(accepted, plain[1])
+                for n in range(N):
+                    row = 2 * n + int(accepted[n])
+                    if n % 3 == 0 and not (where is q and (draft is None or accepted[n])):
+                        assert int(out[row]) == -1
+                        out[row] = plain[0][row]
+                assert torch.equal(out, plain[0])
