@@ -70,12 +70,13 @@ __device__ __forceinline__ void stay(uint8_t* smem, StayBarriers& bar, const Map
     float* red = reinterpret_cast<float*>(smem + S::ring + S::scales);
     uint16_t* which = reinterpret_cast<uint16_t*>(smem + S::ring + S::scales + S::red);
     uint16_t* begin = which + kMaxExperts;
-    const int experts = a.lists[0];
+    // The lists come from two kernels back, which has ended; what this CTA has not waited for itself it reads from L2.
+    const int experts = __ldcg(a.lists);
     const int items = experts * a.tiles;
     if ((int)blockIdx.x >= items) return;
     for (int i = threadIdx.x; i <= experts; i += kStayThreads) {
-        if (i < experts) which[i] = (uint16_t)a.lists[1 + i];
-        begin[i] = (uint16_t)a.lists[1 + a.E + i];
+        if (i < experts) which[i] = (uint16_t)__ldcg(a.lists + 1 + i);
+        begin[i] = (uint16_t)__ldcg(a.lists + 1 + a.E + i);
     }
     if (warp == 2) {
         tmem_alloc(&bar.tmem, S::tmem);

@@ -307,3 +307,32 @@ def test_verify_infinities_draw_nothing(N, V, dtype):
                         assert int(out[row]) == -1
                         out[row] = plain[0][row]
                 assert torch.equal(out, plain[0])
+
+
+# ------------------------------------------------------------------ one workspace, call after call
+@pytest.mark.parametrize("fmt", ["e2m1", "bf16", "int4"])
+def test_moe_one_workspace_other_experts_every_call(fmt):
+    """Calls in a row in one workspace, eager and replayed: each reads the lists of its own tokens, not what the call in front left
+    in the same place."""
+    M, E, top, D, F, n = 6, 60, 3, 256, 128, 8
+    g = gen(90)
+    router, wi, wo, _, _ = experts(g, E, D, F, fmt)
+    router = (4 * router.float()).to(BF16).cuda()
+    xs = [randn(g, M, D, dtype=BF16).cuda() for _ in range(n)]
+    call = lambda x, **kw: kda.kda_moe(x, router, wi, wo, top, return_routing=True, **kw)  # noqa: E731
+    want = [call(x) for x in xs]
+    assert len({tuple(w[1].flatten().tolist()) for w in want}) == n
+    ws = torch.zeros(1 << 22, dtype=torch.uint8, device="cuda")
+    held = [x.clone() for x in xs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [call(x, workspace=ws) for x in held]
+    for turn in range(12):
+        order = [(i * (1 + 2 * (turn % 4)) + turn) % n for i in range(n)]
+        for h, i in zip(held, order):
+            h.copy_(xs[i])
+        graph.replay()
+        eager = [call(xs[i], workspace=ws) for i in order]
+        for outs in (got, eager):
+            for o, i in zip(outs, order):
+                assert all(torch.equal(a, b) for a, b in zip(o, want[i]))
