@@ -354,7 +354,8 @@ __device__ __forceinline__ uint32_t largest_of_32(const float (&r)[8]) {
 }
 
 // The scale of the digits in front goes down to 2^-105, so that the eighth digit's is one too: values below 2^-103 lose
-// digits, what is left of them is off by 2^-127 at most.
+// digits, what is left of them is off by 2^-127 at most.  Rows of x that are as small throughout go to direct(); hidden values
+// of an expert have no such way (their rows come together from many CTAs) and are off by that much.
 constexpr int kLowestByte = 22;
 constexpr uint32_t kLowestTop = (uint32_t)(kLowestByte + 2) << 23;
 

@@ -336,3 +336,33 @@ def test_moe_one_workspace_other_experts_every_call(fmt):
         for outs in (got, eager):
             for o, i in zip(outs, order):
                 assert all(torch.equal(a, b) for a, b in zip(o, want[i]))
+
+
+@pytest.mark.parametrize("fmt,floor", [("e2m1", 2.0 ** -127), ("int4", 0.0), ("bf16", 2.0 ** -134)])
+@pytest.mark.parametrize("exponent", [-120, -90, -75, -60, -57, -54, -50, -40, -20, 0, 20, 40, 55])
+def test_moe_magnitudes(exponent, fmt, floor):
+    """Tokens of any magnitude: hidden values of about its square, of which what lies below `floor` may be dropped."""
+    M, E, top, D, F = 4, 6, 2, 128, 96
+    g = gen(100)
+    router, wi, wo, wi64, wo64 = experts(g, E, D, F, fmt)
+    x = (randn(g, M, D) * 2.0 ** exponent).to(BF16)
+    logits = f64(x) @ f64(router).T
+    for score in ("softmax", "sigmoid"):
+        y, ids, w = kda.kda_moe(x.cuda(), router.cuda(), wi, wo, top, out_dtype=F32, score=score, return_routing=True)
+        ids = ids.cpu().long()
+        # no expert that was left out has a score that is larger by more than 2^-50 (a logit by 2^-48 where it is small)
+        out = logits.clone().scatter_(1, ids, -torch.inf)
+        best, worst = (torch.sigmoid(v) if score == "sigmoid" else v for v in (out.amax(1), logits.gather(1, ids).amin(1)))
+        assert bool((best <= worst + (2.0 ** -50 if score == "sigmoid" else 0.0)).all())
+        # the reference for this choice: a bias that makes it
+        for t in range(M):
+            choice = torch.full((E,), -9.0 if score == "sigmoid" else -torch.inf).index_fill_(0, ids[t], 0.0)
+            if score == "sigmoid":
+                ry, rids, rw, bound = lib.moe_ref(x[t:t + 1], router, wi64, wo64, top, choice, score, 1.0)
+            else:
+                ry, rids, rw, bound = lib.moe_ref(x[t:t + 1], router, wi64, wo64, top, None, score, 1.0)
+            assert sorted(rids[0].tolist()) == sorted(ids[t].tolist())
+            # the floor and, of gates, hidden values, products and sums, the last digit of fp32's subnormal numbers
+            hidden = floor + 4 * 2.0 ** -149
+            small = sum(rw[0, j] * (wo64[rids[0, j]].abs().sum(1) * hidden + (F + 4) * 2.0 ** -149) for j in range(top))
+            within(y[t:t + 1], ry, bound + U[F32] * (ry.abs() + bound) + small, score)
