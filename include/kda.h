@@ -735,8 +735,8 @@ kda_status kda_gemm4(const kda_gemm4_args* args, kda_stream_t stream);
  *   logit[t][e] = x_t . router_e, summed to about 48 bits
  *   score = sigmoid(logit): the `top` experts with the largest score + bias are chosen, weighted by score
  *   score = softmax(logit): the `top` largest logits are chosen (bias must be NULL)
- *   weight = scale * score / (sum of the chosen scores), also where scores underflow; a tie goes to the lower
- *   expert; a logit or a score + bias that is not finite counts as NaN, which ranks last
+ *   weight = scale * score / (sum of the chosen scores), also where scores underflow; a tie (of logits, or of
+ *   scores to about 50 bits, 53 next to 1/2 and 1) goes to the lower expert; a logit or a score + bias that is not finite counts as NaN, which ranks last
  *   y_t = sum over the chosen, in the order of their rank, of weight * W_out (silu(g) u),
  *   g, u = the first and second F rows of W_in x_t
  *   x [M][x_stride] bf16; router [E][D] bf16 or fp32, dense; bias [E] fp32 or NULL

@@ -96,11 +96,13 @@ __global__ void __launch_bounds__(kScoreThreads) k_moe_scores(const bf16* __rest
         for (int w = 1; w < kScoreWarps; ++w) v = add(v, sums[w][j]);
         const int64_t at = (int64_t)(t0 + j) * E + e;
         const Wide logit = v;
-        if (sigmoid) v = sigmoid_wide(v);
+        // next to 1/2 the score is 1/2 + logit / 4 (what follows is below 2^-59), which loses no digits of the logit's
+        constexpr float kSmall = 0x1p-18f;
+        if (sigmoid) v = fabsf(logit.hi) < kSmall ? add(Wide{0.5f, 0.f}, Wide{0.25f * logit.hi, 0.25f * logit.lo}) : sigmoid_wide(v);
         logits[at] = logit;
-        // scores next to 1 are equal where fp64 holds them equal; small ones without a bias are ordered by their logits
-        // (negative, so below every other score), which do not underflow
-        key[at] = ordered(!sigmoid ? logit : bias ? to_53_bits(add(v, Wide{bias[e], 0.f})) : logit.hi < 0.f ? logit : to_53_bits(v));
+        // scores next to 1 and to 1/2 are equal where fp64 holds them equal; those well below 1/2 without a bias are ordered by their
+        // logits (negative, so below every other score), which do not underflow
+        key[at] = ordered(!sigmoid ? logit : bias ? to_53_bits(add(v, Wide{bias[e], 0.f})) : logit.hi <= -kSmall ? logit : to_53_bits(v));
     }
 }
 

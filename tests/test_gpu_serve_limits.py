@@ -366,3 +366,19 @@ def test_moe_magnitudes(exponent, fmt, floor):
             hidden = floor + 4 * 2.0 ** -149
             small = sum(rw[0, j] * (wo64[rids[0, j]].abs().sum(1) * hidden + (F + 4) * 2.0 ** -149) for j in range(top))
             within(y[t:t + 1], ry, bound + U[F32] * (ry.abs() + bound) + small, score)
+
+
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_moe_scores_around_a_half(with_bias):
+    """Scores that 53 bits do not tell apart are equal, whichever sign their logits have, and go to the lower expert; small logits
+    that they do tell apart are chosen by."""
+    M, E, top, D, F = 8, 40, 5, 64, 32
+    g = gen(110)
+    router, wi, wo, _, _ = experts(g, E, D, F, "e2m1")
+    bias = torch.zeros(E).cuda() if with_bias else None
+    for exponent in (-120, -100, -70, -60, -40, -30, -25, -20, -15, -10):
+        x = (randn(g, M, D) * 2.0 ** exponent).to(BF16)
+        _, ids, _ = kda.kda_moe(x.cuda(), router.cuda(), wi, wo, top, bias=bias, return_routing=True)
+        key = f64(x) @ f64(router).T if exponent >= -40 else torch.zeros(M, E, dtype=torch.float64)
+        want = torch.sort(key, dim=1, descending=True, stable=True).indices[:, :top]
+        assert torch.equal(ids.cpu().long(), want), exponent
