@@ -212,7 +212,7 @@ __device__ __forceinline__ void stay(uint8_t* smem, StayBarriers& bar, const Map
             c.rb = a.b_scales + (int64_t)min(c.c0 + token, a.tokens - 1) * pitch;
         };
         const auto next = [&](Cursor& c) {
-            if (++c.g < groups) return;
+            if (c.it >= items || ++c.g < groups) return;  // behind the end there is nothing to look up
             c.g = 0;
             c.c0 += S::tokens;
             if (c.c0 >= begin[c.it / a.tiles + 1]) {

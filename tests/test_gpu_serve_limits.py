@@ -382,3 +382,47 @@ def test_moe_scores_around_a_half(with_bias):
         key = f64(x) @ f64(router).T if exponent >= -40 else torch.zeros(M, E, dtype=torch.float64)
         want = torch.sort(key, dim=1, descending=True, stable=True).indices[:, :top]
         assert torch.equal(ids.cpu().long(), want), exponent
+
+
+# ------------------------------------------------------------------ the largest batches
+def moe_ref_by_expert(x, router, w_in, w_out, ids, w):
+    """serve_testlib.moe_ref's y and bound for a given choice and its weights, an expert's tokens at a time on the GPU."""
+    x, w_in, w_out, ids = f64(x).cuda(), w_in.cuda(), w_out.cuda(), ids.long().cuda()
+    w = w.double().cuda()
+    D, F = w_out.shape[1], w_out.shape[2]
+    y, bound = torch.zeros_like(x), torch.zeros_like(x)
+    for e in range(w_in.shape[0]):
+        t, j = torch.nonzero(ids == e, as_tuple=True)
+        if not len(t):
+            continue
+        gu, dgu = x[t] @ w_in[e].T, (D / 32 + 16) * 2.0 ** -23 * (x[t].abs() @ w_in[e].abs().T)
+        gate, u, dg, du = gu[:, :F], gu[:, F:], dgu[:, :F], dgu[:, F:]
+        s = gate * torch.sigmoid(gate)
+        h = s * u
+        dh = 1.1 * dg * (u.abs() + du) + s.abs() * du + 12 * 2.0 ** -24 * h.abs() + 2.0 ** -21 * h.abs() + 2.0 ** -36 * h.abs().amax(1, keepdim=True)
+        p = h @ w_out[e].T
+        dp = dh @ w_out[e].abs().T + (F / 32 + 16) * 2.0 ** -23 * ((h.abs() + dh) @ w_out[e].abs().T)
+        k = w[t, j].unsqueeze(1)
+        y.index_add_(0, t, k * p)  # a token has an expert once
+        bound.index_add_(0, t, k * (dp + 8 * 2.0 ** -24 * p.abs()))
+    return y, bound + ids.shape[1] * 2.0 ** -23 * y.abs()
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "int4", "bf16"])
+@pytest.mark.parametrize("M,E,top", [(65535, 5, 1), (2047, 1024, 32), (8191, 64, 8), (300, 200, 6)])
+def test_moe_largest_batches(M, E, top, fmt):
+    """Up to 65,535 places of tokens with experts: slots, lists and their 16-bit starts, many passes over an expert's tokens."""
+    D, F = 128, 96
+    g = gen(M)
+    router, wi, wo, wi64, wo64 = experts(g, E, D, F, fmt)
+    x = randn(g, M, D, dtype=BF16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y, ids, w = kda.kda_moe(x.cuda(), router.cuda(), wi, wo, top, score="softmax", scale=1.5, out_dtype=F32, return_routing=True, d_status=status)
+    assert int(status) == 0
+    logits = f64(x) @ f64(router).T
+    want = torch.sort(logits, dim=1, descending=True, stable=True)
+    assert torch.equal(ids.cpu().long(), want.indices[:, :top])
+    rw = 1.5 * torch.softmax(want.values[:, :top], 1)
+    within(w, rw, 2.0 ** -23 * rw)
+    ry, bound = moe_ref_by_expert(x, router, wi64, wo64, ids, rw)
+    within(y, ry.cpu(), (bound + U[F32] * (ry.abs() + bound)).cpu())
