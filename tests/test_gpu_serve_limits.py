@@ -385,6 +385,19 @@ def test_moe_scores_around_a_half(with_bias):
 
 
 # ------------------------------------------------------------------ the largest batches
+@pytest.mark.parametrize("fmt,group,sdt", lib.FORMATS)
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("M", [1001, 5000, 65535])
+def test_gemm4_largest_batches(M, fmt, group, sdt, out_dtype):
+    N, K = 70, 384
+    g = gen(M)
+    x = randn(g, M, K, dtype=BF16)
+    codes, scales = lib.random_weight(g, N, K, fmt=fmt, group=group, scale_dtype=sdt)
+    got = kda.kda_gemm4(x.cuda(), codes.cuda(), scales.cuda(), out_dtype=out_dtype)
+    ref, err = lib.gemm4_ref(x, lib.unpack_ref(codes, scales), "none")
+    within(got, ref, err + U[out_dtype] * (ref.abs() + err))
+
+
 def moe_ref_by_expert(x, router, w_in, w_out, ids, w):
     """serve_testlib.moe_ref's y and bound for a given choice and its weights, an expert's tokens at a time on the GPU."""
     x, w_in, w_out, ids = f64(x).cuda(), w_in.cuda(), w_out.cuda(), ids.long().cuda()
@@ -426,3 +439,25 @@ def test_moe_largest_batches(M, E, top, fmt):
     within(w, rw, 2.0 ** -23 * rw)
     ry, bound = moe_ref_by_expert(x, router, wi64, wo64, ids, rw)
     within(y, ry.cpu(), (bound + U[F32] * (ry.abs() + bound)).cpu())
+
+
+# ------------------------------------------------------------------ one large value beside small ones
+@pytest.mark.parametrize("M", [5, 130])
+def test_gemm4_e2m1_large_value_beside_small_ones(M):
+    """A value holds what lies above 2^-22 of the largest of its 32, however small that one's weight is: the largest of a group has a
+    weight of 0, the others are 1 to 2 and 2^6 to 2^24 times smaller.  From 97 rows on with a bf16 result nothing is lost."""
+    N, K = 60, 256
+    g = gen(120)
+    codes, scales = lib.random_weight(g, N, K, fmt="e2m1", group=32)
+    codes[:, ::16] &= 0xf0  # element 0 of each group
+    w = lib.unpack_ref(codes, scales)
+    for exponent in (6, 14, 18, 22, 24):
+        x = 1 + torch.rand(M, K, generator=g)
+        x[:, ::32] = 2.0 ** exponent
+        x = x.to(BF16)
+        for dtype in (BF16, F32):
+            got = kda.kda_gemm4(x.cuda(), codes.cuda(), scales.cuda(), out_dtype=dtype)
+            ref, err = lib.gemm4_ref(x, w, "none")
+            # bf16 values of 1 to 2 end at 2^-7: exact where that is above 2^-22 of the largest
+            lost = 0.0 if exponent <= 14 or (M > 96 and dtype is BF16) else 2.0 ** (exponent - 22)
+            within(got, ref, err + lost * w.abs().sum(1) + U[dtype] * (ref.abs() + err), f"{exponent} {dtype}")
