@@ -461,3 +461,92 @@ def test_gemm4_e2m1_large_value_beside_small_ones(M):
             # bf16 values of 1 to 2 end at 2^-7: exact where that is above 2^-22 of the largest
             lost = 0.0 if exponent <= 14 or (M > 96 and dtype is BF16) else 2.0 ** (exponent - 22)
             within(got, ref, err + lost * w.abs().sum(1) + U[dtype] * (ref.abs() + err), f"{exponent} {dtype}")
+
+
+# ------------------------------------------------------------------ the largest sizes
+@pytest.mark.parametrize("fmt,group,sdt", lib.FORMATS)
+@pytest.mark.parametrize("M", [2, 100])
+def test_gemm4_longest_rows(M, fmt, group, sdt):
+    """Rows of 2^24 weights, of which few meet an x that is not 0: the others, and the groups' sums that they leave, add nothing."""
+    N, K = 3, 1 << 24
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scales = torch.full((N, K // group), 118, device="cuda", dtype=torch.uint8) if fmt == "e2m1" else torch.full((N, K // group), 0.25, device="cuda", dtype=sdt)
+    at = torch.cat([torch.randint(0, K, (60,), generator=g, device="cuda"), torch.tensor([0, K - 1], device="cuda")]).unique()
+    x = torch.zeros(M, K, dtype=BF16, device="cuda")
+    x[:, at] = torch.randn(M, len(at), generator=g, device="cuda").to(BF16)
+    got = kda.kda_gemm4(x, codes, scales, out_dtype=F32)
+    c = (codes[:, at // 2].int() >> (4 * (at % 2)).int()) & 15
+    w = torch.cat([lib.E2M1, -lib.E2M1]).cuda()[c.long()] * 2.0 ** -9 if fmt == "e2m1" else (c - 8).double() * 0.25
+    ref, mass = x[:, at].double() @ w.T, x[:, at].double().abs() @ w.abs().T
+    # a term's own rounding, and (integer codes) those of the 8 that is taken off its group's sum: 80 roundings of a group's
+    # 8 |x| at most
+    extra = 0.0 if fmt == "e2m1" else 80 * 2.0 ** -23 * 0.25 * 8 * x[:, at].double().abs().sum(1, keepdim=True)
+    within(got, ref.cpu(), (80 * 2.0 ** -23 * mass + extra).cpu())
+
+
+@pytest.mark.parametrize("fmt,sdt", [("e2m1", torch.uint8), ("int4", F32)])
+def test_gemm4_most_outputs(fmt, sdt):
+    N, K, M = 1 << 24, 32, 3
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scales = torch.randint(118, 126, (N, 1), generator=g, device="cuda").to(torch.uint8) if fmt == "e2m1" else torch.rand(N, 1, generator=g, device="cuda") + 0.1
+    x = torch.randn(M, K, generator=g, device="cuda").to(BF16)
+    got = kda.kda_gemm4(x, codes, scales, out_dtype=F32)
+    assert bool(torch.isfinite(got).all())
+    some = torch.cat([torch.arange(1000), torch.randint(0, N, (4000,), generator=gen(2)), torch.arange(N - 1000, N)])
+    ref, err = lib.gemm4_ref(x, lib.unpack_ref(codes[some.cuda()], scales[some.cuda()]), "none")
+    within(got[:, some.cuda()], ref, err + U[F32] * ref.abs())
+
+
+@pytest.mark.parametrize("N", [1, 40, 304])
+def test_verify_largest_vocabulary(N):
+    """4,000,000 tokens, by one CTA of a row or by eight."""
+    V = 4000000
+    p = torch.rand(N, V, device="cuda").to(BF16)
+    u = torch.rand(N, generator=gen(N))
+    out, _ = kda.kda_verify(p, torch.zeros(N, dtype=torch.int64).cuda(), u.cuda(), np.arange(N + 1, dtype=np.int32))
+    for n in {0, N // 2, N - 1}:
+        ro, _ = lib.verify_ref(p[n:n + 1].cpu(), None, torch.zeros(1, dtype=torch.int64), u[n:n + 1], np.array([0, 1], np.int32))
+        assert int(out[n]) == int(ro[0])
+
+
+def test_verify_long_and_many_sequences():
+    """A hundred thousand drafts of a sequence, all taken or none; two hundred thousand sequences."""
+    V, lens = 9, [100000, 1, 0, 50000, 70001]
+    T = sum(lens)
+    g = gen(3)
+    p, u = torch.rand(T, V, generator=g) + 0.1, torch.rand(T, generator=g) * 0.5
+    tokens = torch.randint(0, V, (T,), generator=g).int()
+    q = p.clone()
+    first = 150001  # of the last sequence, which stops at 60,000
+    q[first + 60000, tokens[first + 60000]] = 50.0
+    u[first + 60000] = 0.9
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    out, accepted = kda.kda_verify(p.cuda(), tokens.cuda(), u.cuda(), cu, draft=q.cuda())
+    assert accepted.tolist() == [99999, 0, 0, 49999, 60000]
+    out = out.cpu()
+    for n, a in enumerate(accepted.tolist()):
+        b = int(cu[n])
+        assert torch.equal(out[b:b + a], tokens[b:b + a]) and bool((out[b + a + 1:int(cu[n + 1])] == -1).all())
+    n = 200000
+    p, u = torch.rand(n, V, generator=g), torch.rand(n, generator=g)
+    out, accepted = kda.kda_verify(p.cuda(), torch.zeros(n, dtype=torch.int32).cuda(), u.cuda(), np.arange(n + 1, dtype=np.int32))
+    cum = p.double().cumsum(1)
+    assert torch.equal(out.cpu().long(), (cum > u.double().unsqueeze(1) * cum[:, -1:]).int().argmax(1)) and not bool(accepted.any())
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "int4", "bf16"])
+def test_moe_smallest_and_widest(fmt):
+    """Experts of the least sizes, and rows of 2^17 and more on either side."""
+    unit = 8 if fmt == "bf16" else 32
+    for M, E, top, D, F in ((3, 4, 2, unit, unit), (1, 1, 1, unit, 96), (2, 2, 1, (1 << 17) + 96, 32), (2, 2, 2, 64, (1 << 17) + 32)):
+        g = gen(D + F)
+        router, wi, wo, wi64, wo64 = experts(g, E, D, F, fmt)
+        x = randn(g, M, D, dtype=BF16)
+        y, ids, w = kda.kda_moe(x.cuda(), router.cuda(), wi, wo, top, out_dtype=F32, score="softmax", return_routing=True)
+        ry, rids, rw, bound = lib.moe_ref(x, router, wi64, wo64, top, None, "softmax", 1.0)
+        assert torch.equal(ids.cpu().long(), rids)
+        within(y, ry, bound + U[F32] * (ry.abs() + bound), f"{D} x {F}")
