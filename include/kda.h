@@ -701,11 +701,12 @@ kda_status kda_pack4(const kda_pack4_args* args, kda_stream_t stream);
 kda_status kda_unpack4(const kda_pack4_args* args, kda_stream_t stream);
 
 /* kda_gemm4 -- kda_gemm for weights in 4 bits: C[M][N] = epilogue(A[M][K] . W[N][K]^T), for
- * the few rows of a decode step (M up to 65,535; the weights are read once per 32 rows, 256 of e2m1 with a bf16 C).
+ * the few rows of a decode step (M up to 65,535; the weights are read once per 32 rows, 256 of e2m1 with a bf16 C: from some 32
+ * rows on kda_gemm on bf16 weights is faster than integer codes, by three to four times at 256 rows).
  * A [M][lda] bf16 (any alignment of its elements; 16-byte rows are read faster), C [M][ldc] bf16
  * or fp32, rounded once; epilogues as in kda_gemm; M, N >= 0; C must not overlap an input.
- * Values of A enter the products exactly but for what lies below 2^-22 of the largest of their 32 (e2m1) or 2^-39 of
- * the largest of their 128 (int4); sums are fp32, in a fixed order that depends on M, N and K (e2m1, more than 96 rows and a
+ * Values of A enter the products exactly but for what lies below 2^-22 of the largest of their 32 (e2m1), whatever that one's
+ * weight, or 2^-39 of the largest of their 128 (int4); sums are fp32, in a fixed order that depends on M, N and K (e2m1, more than 96 rows and a
  * bf16 C, K up to 262,144: values exact, sums cut off instead of rounded, by 2^-12 of the sum of |products| at most, an eighth
  * of what rounding C costs; 4e-5 measured for products of one sign, 5e-6 for random ones).  A row of A with values that are
  * not finite gives what the formula gives, slowly.  Needs an sm_103 device.  A wait that times out on the device is reported through
@@ -736,7 +737,8 @@ kda_status kda_gemm4(const kda_gemm4_args* args, kda_stream_t stream);
  *   score = sigmoid(logit): the `top` experts with the largest score + bias are chosen, weighted by score
  *   score = softmax(logit): the `top` largest logits are chosen (bias must be NULL)
  *   weight = scale * score / (sum of the chosen scores), also where scores underflow; a tie (of logits, or of
- *   scores to about 50 bits, 53 next to 1/2 and 1) goes to the lower expert; a logit or a score + bias that is not finite counts as NaN, which ranks last
+ *   scores to about 50 bits, 53 next to 1/2 and 1) goes to the lower expert; a logit or a score + bias that is not
+ *   finite counts as NaN, which ranks last
  *   y_t = sum over the chosen, in the order of their rank, of weight * W_out (silu(g) u),
  *   g, u = the first and second F rows of W_in x_t
  *   x [M][x_stride] bf16; router [E][D] bf16 or fp32, dense; bias [E] fp32 or NULL
@@ -746,7 +748,9 @@ kda_status kda_gemm4(const kda_gemm4_args* args, kda_stream_t stream);
  * The values between the two products keep 22 bits or more of the largest of their 32 (e2m1), 128 (int4) or of their
  * own (bf16), as far as these lie above 2^-127 (e2m1) or 2^-134 (bf16): what is left below is dropped.  Sums are fp32 (bf16: eight
  * instructions' sums cut off at a time).  A value that is not finite (or, int4, beyond 2^122) makes its token's y infinite or
- * NaN, of the others nothing changes.  E up to 1024, top up
+ * NaN, of the others nothing changes; e2m1 sums of the second products may overflow from 2^127.8 on.  An expert's weights pass
+ * once per 4 to 64 of its tokens: for a prompt's tokens this is slow (8 of 256 e2m1 experts: 0.7 ms for 256 tokens, 2.0 for 1,024,
+ * 7.9 for 4,096 where the weights alone take 0.44).  E up to 1024, top up
  * to 32 and to E, M * top up to 65535, E * 2F and E * D up to 2^30.  Needs an sm_103 device; a wait that times out on the
  * device is reported through d_status (KDA_ERR_TIMEOUT). */
 typedef enum { KDA_SCORE_SIGMOID = 0, KDA_SCORE_SOFTMAX = 1 } kda_moe_score;

@@ -135,7 +135,7 @@ __device__ __forceinline__ int alignment(const uint8_t* p, int64_t pitch) {
 }
 __device__ __forceinline__ void scale_warps_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// A launch may begin beside the kernel in front of it (launch_beside); it waits for what that one writes, the columns.
+// A launch may begin beside the kernel in front of it (launch_kernel); it waits for what that one writes, the columns.
 __device__ __forceinline__ void wait_for_columns() { few::wait_for_kernel_before(); }
 
 // Once per CTA, before the first product.
@@ -479,8 +479,9 @@ __device__ __forceinline__ float4 joined4(const float* red, int ranks, int token
 }
 
 // CTAs of a cluster that share a tile's K: the number that leaves the busiest SM the least to do, in runs of 256 elements,
-// where the CTAs that run side by side take about `overhead` runs' time to start and to join.  One row: 12,288 x 7,168 in
-// 19.6 us by one CTA per tile, 14.4 by three (the rule), 24.7 by eight; 1,024 x 7,168 in 18.5, 14.4 and 12.4 (the rule).
+// where the CTAs that run side by side take about `overhead` runs' time to start and to join; `at_least` of them.  In a captured
+// graph, one row: 12,288 x 7,168 in 14.0 us by one CTA per tile, 12.7 by three (the rule), 21.0 by eight; 1,024 x 7,168 in 12.7, 8.5
+// and 6.9 (the rule).  Whole ranks per tile only: 32 rows of 12,288 x 7,168 keep one CTA per tile, 96 on 152 SMs (18.6 us; two 24.6).
 inline int cluster_ranks(int64_t tiles, int K, int per_sm, int overhead, int at_least = 1) {
     const int runs = (K + 255) / 256;
     int best = at_least;

@@ -5,9 +5,10 @@
 // cores (kda_few_tc.cuh): a CTA takes 128 of the N outputs for some tokens, a cluster splits K.  Integer codes go
 // through registers (kda_few.cuh).
 //
-// On the GPU, columns included: e2m1, 12,288 x 7,168: 1 row 11 us (4.2 TB/s), 32 rows 17 us; 256 rows (kda_widen_tc.cuh) 48 us.
-// One row is bound by the chain of two launches, first bytes and join.  Integer codes, 160,000 x 7,168, 16 rows 183 us (3.2 TB/s): latency
-// of three warps per scheduler (issue 45 %, tensor pipe 32 %, HBM 37 %).
+// Figures here are per call in a captured graph of calls in a row, weights from HBM, columns included.  e2m1, 12,288 x 7,168: 1 row 13 us
+// (3.7 TB/s), 32 rows 19 us; 256 rows (kda_widen_tc.cuh) 47 us.  One row is bound by the chain of two launches, first bytes and
+// join; 32 rows have 96 CTAs for 152 SMs.  Integer codes, 160,000 x 7,168, 16 rows 185 us (3.2 TB/s): latency of three warps per
+// scheduler (issue 45 %, tensor pipe 32 %, HBM 37 %); every 32 rows more read and take apart the codes again (256 x 12,288 x 7,168: 185 us).
 #include "kda_few.cuh"
 #include "kda_few_tc.cuh"
 #include "kda_serve.cuh"
@@ -34,7 +35,7 @@ __device__ __forceinline__ float apply(int epi, float v) {
 }
 
 // A CTA takes an equal share of the tiles of 32 rows, 12 / ks at a time (8 / ks where more scales leave room for 8 warps'
-// rings only; 12 warps 178 us where 8 took 185).
+// rings only; 160,000 x 7,168, 16 rows: 185 us, 209 with 8).
 constexpr int warps_for(int scale_row) { return scale_row <= 8 ? 12 : 8; }
 
 template <int NT, int GS, int SB> __global__ void __launch_bounds__(32 * warps_for(GS * SB), 1) k_gemm4(const Gemm4 p, void* __restrict__ out, bool out32) {
@@ -185,9 +186,11 @@ template <int N, typename Tout> cudaError_t launch_tc(const kda_gemm4_args& a, c
 }
 
 // ------------------------------------------------------------------ many rows
-// 12,288 x 7,168: 256 rows 48 us (0.93 PFLOP/s), of which 7 the start and the end of a CTA; 7,168 x 12,288 48.  128 elements
-// take some 1,270 cycles with 128 columns and 1,430 with 256, whose products alone take 1,024: the warp that issues
-// them, by clock stamps where the time went, shares its scheduler with four that widen.  (Barriers and commits every 64 elements: 53 us, 46 with 128 rows.)
+// 12,288 x 7,168: 256 rows 47 us (0.96 PFLOP/s), of which 7 the start and the end of a CTA; 7,168 x 12,288 45.  Two causes of about
+// the same weight: 96 and 112 CTAs leave a third and a quarter of the SMs without work (an SM is active for 66 % of the
+// kernel's time), and 128 elements take some 1,270 cycles with 128 columns and 1,430 with 256, whose products alone take 1,024:
+// the warp that issues them, by clock stamps where the time went, shares its scheduler with four that widen.  (Barriers and
+// commits every 64 elements: 53 us, 46 with 128 rows.)
 template <int N>
 __global__ void __launch_bounds__(widetc::kThreads, 1) k_gemm4_widen(const __grid_constant__ fewtc::Maps maps, const Gemm4Tc p, bf16* __restrict__ out) {
     extern __shared__ uint8_t smem_raw[];
@@ -259,18 +262,21 @@ size_t gemm4_workspace(const kda_gemm4_args& a) {
 
 cudaError_t launch_gemm4(const kda_gemm4_args& a, cudaStream_t s) {
     if (a.format == KDA_WEIGHT_E2M1) {
-        // From 97 rows on widened weights, where C is bf16.  12,288 x 7,168, digits against widened: 64 rows 35 and 43 us, 128 rows
-        // 48 and 44, 256 rows 92 and 49, 512 rows 174 and 89; 7,168 x 12,288: 25 and 39, 50 and 42, 72 and 48, 148 and 79.
+        // From 97 rows on widened weights, where C is bf16 and a cluster's accumulators take K.  Digits against widened, us: 12,288 x
+        // 7,168 64 rows 36 and 36, 96 rows 34 and 37, 128 rows 48 and 38, 256 rows 91 and 47, 512 rows 166 and 87; 7,168 x 12,288 64 rows 25
+        // and 36, 96 46 and 36, 128 49 and 37, 256 71 and 45, 512 141 and 74; 7,168 x 7,168 100 rows 35 and 24, 256 rows 49 and 31; 4,000 x
+        // 2,048 100 rows 10 and 12, 256 rows 18 and 16.  Small matrices, whose digits' CTAs run all at once, would keep the digits:
+        // 1,000 x 1,024 100 rows 7 and 9, 256 rows 9 and 13; 1,024 x 4,096 256 rows 12 and 18.
         if (a.c_dtype == KDA_BF16 && a.M > 96 && widetc::least_ranks(a.K) <= widetc::kMostRanks) return a.M <= 128 ? launch_widen<128>(a, s) : launch_widen<256>(a, s);
-        // as few columns as hold all rows, and at most 32 rows' (256 rows: 82 us, 91 with 16 rows per CTA, 146 with 8)
+        // as few columns as hold all rows, and at most 32 rows' (256 rows of 7,168 x 12,288: 71 us, 82 with 16 rows per CTA, 129 with 8)
         if (a.M <= 2) return launch_tc_out<16>(a, s);
         if (a.M <= 4) return launch_tc_out<32>(a, s);
         if (a.M <= 8) return launch_tc_out<64>(a, s);
         if (a.M <= 16) return launch_tc_out<128>(a, s);
         return launch_tc_out<256>(a, s);
     }
-    // 8 columns an instruction: one, two or four of them (160,000 x 7,168 for 16 rows: 302, 193 and 283 us; 1,001 x 1,056 for
-    // 5: 13, 15 and 23)
+    // 8 columns an instruction: one, two or four of them (160,000 x 7,168 for 16 rows: 301, 185 and 276 us; 1,001 x 1,056 for
+    // 5: 6.5, 9.1 and 15.2)
     if (a.M <= 8) return launch_scales<1>(a, s);
     if (a.M <= 16) return launch_scales<2>(a, s);
     return launch_scales<4>(a, s);

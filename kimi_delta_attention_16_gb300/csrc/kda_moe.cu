@@ -12,9 +12,10 @@
 // columns first).  e2m1 and bf16 experts
 // go through the tensor cores (kda_moe_tc.cuh), integer codes through kda_few.cuh.
 //
-// e2m1, 32 tokens, 8 of 256 experts, 7,168 x 2,048: 609 us (6.3 TB/s of what has to be read; scores 25, choice
-// and columns 11, products 575); one token, 16 of 896, 3,584 x 2,048: 57 us, half of it the chain of launches; bf16, 4 tokens, 6
-// of 64, 2,048 x 1,408: 80 us (4.5 TB/s).
+// e2m1, 32 tokens, 8 of 256 experts, 7,168 x 2,048: 597 to 635 us (6.0 to 6.4 TB/s of what has to be read; scores 25, choice
+// and columns 12, products 575); one token, 16 of 896, 3,584 x 2,048: 56 us, half of it the chain of launches; bf16, 4 tokens, 6
+// of 64, 2,048 x 1,408: 74 to 81 us (4.5 to 4.9 TB/s).  Meant for few tokens: an expert's weights pass once per 16 of its tokens (e2m1, 8 of
+// 256, 3,584 x 2,048: 1,024 tokens 2.0 ms, 4,096 tokens 7.9 ms).
 #include "kda_few.cuh"
 #include "kda_moe_tc.cuh"
 #include "kda_serve.cuh"
@@ -272,7 +273,7 @@ struct Direct {  // the operands as they were given, for sums that come out as N
     int64_t xs;
     // Slots with this weight need no such sum: a token whose logits are NaN has a y of NaN whatever its hidden values.  Its experts
     // are the lowest ones, for all such tokens (1,000 of 2,000 tokens, 4 of 16 experts of 1,024 x 256: 41 ms, integer codes 150,
-    // with the sums, 0.6 and 0.7 without).
+    // with the sums, 1.1 and 1.6 without, 0.6 and 0.7 for ordinary tokens).
     const float* weights;
     __device__ __forceinline__ bool wanted(int slot) const { return !isnan(weights[slot]); }
 };
@@ -673,7 +674,7 @@ cudaError_t launch_moe(const kda_moe_args& a, const MoePlan& p, cudaStream_t s) 
         out.x = columns_at(ws + p.hidden, 2 * (int64_t)slots, a.F);
         out.rows = a.D, out.K = a.F;
         const Direct given{nullptr, nullptr, x, xs, weights};
-        // 16 columns where an expert may have more than four tokens (7 tokens of 3 of 33 experts: 39 us with 8, 42 with 16)
+        // 16 columns where an expert may have more than four tokens (7 tokens of 3 of 33 experts, called one after another: 39 us with 8, 42 with 16)
         e = columns <= 4 ? launch_codes<1>(sb == 2, a.group, a, in, out, given, weights, parts, most, s)
                          : launch_codes<2>(sb == 2, a.group, a, in, out, given, weights, parts, most, s);
     }

@@ -9,7 +9,7 @@
 // Bound by the one pair of rows per sequence that is read: N V 8 bytes.  The sums decide which token comes out, so
 // they are kept in pairs of fp32 (kda_wide.cuh).  Every 1,024 tokens leave one sum in shared memory: the pass over the
 // row happens once, and only the run of 1,024 that holds the threshold is read again.  The CTAs of a cluster share a
-// row.  256 sequences, 160,000 fp32 tokens: 50 us (6.5 TB/s); one sequence: 10 us, latency.
+// row.  256 sequences, 160,000 fp32 tokens: 50 to 52 us (6.3 to 6.5 TB/s); one sequence: 10 us, latency.
 #include <cooperative_groups.h>
 
 #include "kda_serve.cuh"
@@ -162,8 +162,8 @@ __device__ __forceinline__ bool takes(float u, float q, float p) {
 }
 
 // Few sequences: 512 threads and a whole tile on its way per warp, for the shortest chain of latencies (one sequence of
-// 160,000 tokens: 17 us, 19 with 256).  Many: 256 threads, three CTAs per SM, so that one's start and search run
-// beside the others' reads (256 sequences: 66 us, 89 with 512; caches cold).
+// 160,000 tokens: 10.4 us, 10.7 with 256).  Many: 256 threads, three CTAs per SM, so that one's start and search run
+// beside the others' reads (256 sequences: 51 us, 77 with 512).
 template <typename T, typename Tok, int kThreads> __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 1 : 3) k_verify(const Verify a) {
     constexpr int W = Pack<T>::width, kSteps = kTile / (32 * W), kWarps = kThreads / 32, kUnroll = kThreads == 512 && kSteps == 8 ? 8 : 4;
     __shared__ Wide tile_sum[kMaxTiles];

@@ -98,7 +98,10 @@ def kda_gemm4(A: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, epi
               stream=None) -> torch.Tensor:
     """C = epilogue(A @ W^T) for the few rows of a decode step: A [M, K] bf16 (rows may be strided), W [N, K] in 4 bits
     (codes [N, K / 2] and scales [N, K / group] as kda_pack4 returns them).  Epilogues and out_dtype as in kda_gemm; out
-    [M, N] may have strided rows.  Sums are fp32, in a fixed order, rounded once.  M is at most 65535."""
+    [M, N] may have strided rows.  Sums are fp32, in a fixed order, rounded once (e2m1, more than 96 rows, bf16 result: cut off, by
+    an eighth of that rounding at most).  e2m1 up to 96 rows, or with an fp32 result: what lies below 2^-22 of the largest of 32
+    values of A is dropped.  Integer codes are for few rows: from some 32 on kda_gemm on bf16 weights is faster.  M is at
+    most 65535."""
     if stream is not None:
         with _on(stream, A, codes, scales, out, workspace, d_status):
             return kda_gemm4(A, codes, scales, epilogue=epilogue, out=out, out_dtype=out_dtype, workspace=workspace,
@@ -155,7 +158,8 @@ def kda_moe(x: torch.Tensor, router: torch.Tensor, w_in: Weight, w_out: Weight, 
     the chosen ones, times `scale`; an expert computes W_out (silu(g) u) with g and u the halves of W_in x.  w_in
     [E, 2 F, D] and w_out [E, D, F] are bf16 tensors or (codes, scales) in one 4-bit format (kda_pack4).  Returns y
     [M, D] in out_dtype (default bf16), or (y, ids [M, top] int32, weights [M, top] fp32), best first, with
-    return_routing.  M * top is at most 65535, E 1024, top 32."""
+    return_routing.  A token whose logits are not finite gets NaN.  M * top is at most 65535, E 1024, top 32; made for the tokens of
+    a decode step, slow for a prompt's (an expert's weights pass again for every few of its tokens)."""
     if stream is not None:
         pair = lambda w: (w,) if isinstance(w, torch.Tensor) else w  # noqa: E731
         with _on(stream, x, router, *pair(w_in), *pair(w_out), bias, y, workspace, d_status):
@@ -212,7 +216,8 @@ def kda_verify(target: torch.Tensor, tokens: torch.Tensor, u: torch.Tensor, cu_s
     the drafts were drawn from, None for a drafter that proposes its best token; tokens [T] int32 or int64: row i holds
     the draft after it; u [T] fp32 in [0, 1).  The last row of a sequence has no draft.  A draft d is taken while
     u draft(d) < target(d); after the first refusal, or after all, one token is drawn by the last row's u from
-    max(target - draft, 0), or from the last row's target.  Returns (tokens [T]: the accepted drafts, the drawn token,
+    max(target - draft, 0), or from the last row's target.  Values not above 0, NaN among them, count as 0; an infinity in what
+    is drawn from, or a sum beyond fp32, draws -1, as a row of zeros does.  Returns (tokens [T]: the accepted drafts, the drawn token,
     then -1; accepted [N] int32)."""
     if stream is not None:
         with _on(stream, target, tokens, u, cu_seqlens, draft, d_status):
