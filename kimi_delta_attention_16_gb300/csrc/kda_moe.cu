@@ -12,7 +12,7 @@
 // columns first).  e2m1 and bf16 experts
 // go through the tensor cores (kda_moe_tc.cuh), integer codes through kda_few.cuh.
 //
-// e2m1, 32 tokens, 8 of 256 experts, 7,168 x 2,048: 597 to 635 us (6.0 to 6.4 TB/s of what has to be read; scores 25, choice
+// e2m1, 32 tokens, 8 of 256 experts, 7,168 x 2,048: 597 to 640 us (6.0 to 6.4 TB/s of what has to be read; scores 25, choice
 // and columns 12, products 575); one token, 16 of 896, 3,584 x 2,048: 56 us, half of it the chain of launches; bf16, 4 tokens, 6
 // of 64, 2,048 x 1,408: 74 to 81 us (4.5 to 4.9 TB/s).  Meant for few tokens: an expert's weights pass once per 16 of its tokens (e2m1, 8 of
 // 256, 3,584 x 2,048: 1,024 tokens 2.0 ms, 4,096 tokens 7.9 ms).
